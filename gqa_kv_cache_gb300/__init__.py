@@ -20,9 +20,21 @@ A cache of E4M3 (FP8) bytes (``torch.uint8`` or ``torch.float8_e4m3fn``
 tensors) takes ``k_scale`` / ``v_scale`` float32 (Hkv,) tensors: K =
 k_scale[kvh] * K8; the decode step then takes bfloat16 q, k_new and v_new and
 quantises the appended token.
+
+A cache of 4-bit E2M1 values holds D / 2 bytes a vector (``torch.uint8`` or
+``torch.float4_e2m1fn_x2``) and takes ``k_group_scale`` / ``v_group_scale``
+besides: E4M3 bytes of the cache's shape with D // 16 last, one scale per 16
+dims (the format is the C header's GQA_DTYPE_E2M1).
+
+``append`` and ``append_paged`` write packed tokens into any of these caches
+without attending (and keep the key bounds of its blocks), ``read`` and
+``read_paged`` give slots back as vectors. ``select_blocks`` and
+``select_blocks_paged`` choose the blocks of slots whose key bounds promise
+the highest scores, and ``attend_selected`` attends those alone.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -30,7 +42,8 @@ import torch
 from . import _lib
 
 __all__ = ["decode_step", "decode_step_paged", "attend", "attend_paged", "decode_multi",
-           "decode_multi_paged", "workspace_bytes", "validate", "validate_attend", "validate_multi",
+           "decode_multi_paged", "append", "append_paged", "read", "read_paged", "select_blocks",
+           "select_blocks_paged", "attend_selected", "Selection", "workspace_bytes", "validate", "validate_attend", "validate_multi",
            "GqaError", "trace_enable", "trace_collect", "KERNELS", "library_path"]
 
 OK, INVALID_ARGUMENT, UNSUPPORTED, CUDA_ERROR, WORKSPACE = 0, 1, 2, 3, 4
@@ -38,7 +51,9 @@ KERNELS = {"auto": 0, "simt": 1, "tc": 2, "unit": 3, "tc5": 4}
 STATUS_BITS = {1: "bad length", 2: "bad slot id", 4: "bad block", 8: "timeout", 16: "bad kept prefix",
                32: "bad token offsets"}
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
-E4M3 = 2
+E4M3, E2M1 = 2, 3
+_GROUP = 16   # dims that share an E4M3 scale in an E2M1 cache
+_NIBBLE_DTYPES = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
 _BYTE_DTYPES = (torch.uint8,) + ((torch.float8_e4m3fn,) if hasattr(torch, "float8_e4m3fn") else ())
 
 
@@ -70,7 +85,8 @@ def _ptr(t):
 
 
 def _opts(kernel, grid_ctas, sched_pad=None, sink=None, window=0, kept_prefix=0, device=None, B=None,
-          Hq=None, k_scale=None, v_scale=None, Hkv=None, wait_limit_cycles=0, test_stall=False):
+          Hq=None, k_scale=None, v_scale=None, Hkv=None, wait_limit_cycles=0, test_stall=False,
+          k_group_scale=None, v_group_scale=None):
     """The gqa_options struct. Softmax modifiers: ``sink`` a float32 (Hq,)
     device tensor, ``window`` an int >= 0, ``kept_prefix`` an int >= 0 or an
     int32 (B,) device tensor. ``wait_limit_cycles`` > 0 shortens the
@@ -102,36 +118,71 @@ def _opts(kernel, grid_ctas, sched_pad=None, sink=None, window=0, kept_prefix=0,
         if t.dtype != torch.float32 or t.shape != (Hkv,) or not t.is_contiguous() or t.device != device:
             raise TypeError(f"{name} must be a contiguous float32 (Hkv,) tensor on q's device")
         setattr(o, name, t.data_ptr())
+    if k_group_scale is not None:
+        o.k_group_scale = k_group_scale.data_ptr()
+        o.v_group_scale = v_group_scale.data_ptr()
     return o
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
 
 
 _ws_cache: dict = {}
 
 
-def _workspace(device, nbytes):
-    """A per-device workspace, zero-filled when allocated; the library leaves
-    it zero-filled after every call, whatever the sizes."""
-    buf = _ws_cache.get(device)
+def _workspace(device, nbytes, stream=None):
+    """A workspace of the device and stream, zero-filled when allocated; the
+    library leaves it zero-filled after every call, whatever the sizes. Calls
+    on one stream run one after the other; each stream has its own, and so has
+    every call that is captured into a graph (the graph fills it with zeros
+    and may then be replayed beside any other work)."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(max(nbytes, 1), dtype=torch.uint8, device=device)
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    key = (device, s.cuda_stream) if s.cuda_stream else device
+    buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _ws_cache[device] = buf
+        with torch.cuda.stream(s):   # zero-filled before the stream's next kernel
+            buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        _ws_cache[key] = buf
     return buf
 
 
+def _on(device):
+    """The device as the current one, where it is not."""
+    if device.index == torch.cuda.current_device():
+        return _HERE
+    return torch.cuda.device(device)
+
+
+_HERE = contextlib.nullcontext()
+
+
 def workspace_bytes(B, Hq, Hkv, D, dtype=torch.bfloat16, kernel="auto", grid_ctas=0) -> int:
-    """Workspace bytes the library needs for one step of these sizes."""
+    """Workspace bytes the library needs for one step of these sizes.
+    ``dtype`` is the cache's; "e2m1" for a 4-bit cache."""
     o = _opts(kernel, grid_ctas)
-    code = E4M3 if dtype in _BYTE_DTYPES else _DTYPES[dtype]
+    code = E2M1 if dtype == "e2m1" else E4M3 if dtype in _BYTE_DTYPES else _DTYPES[dtype]
     return int(_lib.load().gqa_workspace_bytes(B, Hq, Hkv, D, code, ctypes.byref(o)))
 
 
-def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False):
+def _group_scales(caches, k_group_scale, v_group_scale, D):
+    """Checks of an E2M1 cache's tensors (the shapes against D dims a vector)."""
+    for (name, c), (gname, t) in zip(caches, (("k_group_scale", k_group_scale), ("v_group_scale", v_group_scale))):
+        if c.dtype not in _NIBBLE_DTYPES:
+            raise TypeError(f"{name} with group scales must hold E2M1 pairs (uint8 or float4_e2m1fn_x2)")
+        if t is None or t.dtype not in _BYTE_DTYPES:
+            raise TypeError("k_group_scale and v_group_scale must both be E4M3 bytes (uint8 or float8_e4m3fn)")
+        if D % _GROUP or c.shape[-1] * 2 != D or t.shape != (*c.shape[:-1], D // _GROUP):
+            raise ValueError(f"{name} must hold D // 2 bytes and {gname} D // {_GROUP} scales a vector, D = {D}")
+        if t.device != c.device or not t.is_contiguous():
+            raise ValueError(f"{gname} must be contiguous and on the cache's device")
+
+
+def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False, groups=None):
     """Checks shared by the entry points; returns (cache gqa_dtype, out). The
     query and the new keys / values share the cache dtype, except over an E4M3
     cache (bfloat16 then; the attend's query is free)."""
@@ -139,10 +190,14 @@ def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False):
         raise ValueError("tensors must be on a CUDA device")
     if q.dtype not in _DTYPES:
         raise TypeError("q must be float32 or bfloat16")
-    code = _cache_code(caches[0][1])
-    if code == E4M3:
+    if groups is not None and (groups[0] is not None or groups[1] is not None):
+        _group_scales(caches, *groups, q.shape[-1])
+        code = E2M1
+    else:
+        code = _cache_code(caches[0][1])
+    if code >= E4M3:
         if not q_any_dtype and q.dtype != torch.bfloat16:
-            raise TypeError("over an E4M3 cache q, k_new and v_new are bfloat16")
+            raise TypeError("over an E4M3 or E2M1 cache q, k_new and v_new are bfloat16")
         new_dt = torch.bfloat16
     else:
         dt = caches[0][1].dtype if q_any_dtype else q.dtype
@@ -176,25 +231,26 @@ def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False):
 def decode_step(q, k_new, v_new, k_cache, v_cache, lengths, slot_ids=None, *, out=None,
                 status=None, kernel="auto", grid_ctas=0, workspace=None, stream=None, sched_pad=None,
                 sink=None, window=0, kept_prefix=0, k_scale=None, v_scale=None,
-                wait_limit_cycles=0, test_stall=False):
+                wait_limit_cycles=0, test_stall=False, k_group_scale=None,
+                v_group_scale=None):
     """One decode step on a dense (R, Hkv, Smax, D) cache (continuous batch
     when ``slot_ids`` is given). Appends in place; returns ``out``. A
     ``workspace`` passed in must be zero-filled before its first use (the
     library leaves it zero-filled after every call). ``sink``, ``window`` and
     ``kept_prefix`` are the softmax modifiers of the C header's gqa_options."""
     dt, out = _common_checks(q, k_new, v_new, (("k_cache", k_cache), ("v_cache", v_cache)),
-                             lengths, out)
+                             lengths, out, groups=(k_group_scale, v_group_scale))
     B, Hq, D = q.shape
     R, Hkv, Smax, D2 = k_cache.shape
-    if D2 != D or v_cache.shape != k_cache.shape or k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D):
+    if (D2 * 2 if dt == E2M1 else D2) != D or v_cache.shape != k_cache.shape or k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D):
         raise ValueError("shape mismatch between q, k_new, v_new and the caches")
     if slot_ids is not None and (slot_ids.dtype != torch.int32 or slot_ids.shape != (B,)):
         raise TypeError("slot_ids must be int32 of shape (B,)")
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
-              wait_limit_cycles, test_stall)
+              wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
     need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
-    ws = _workspace(q.device, need) if workspace is None else workspace
+    ws = _workspace(q.device, need, stream) if workspace is None else workspace
     code = lib.gqa_decode_step_ex(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
                                   _ptr(lengths), _ptr(slot_ids), _ptr(out), B, Hq, Hkv, D, R, Smax,
                                   dt, _ptr(ws), ws.numel() * ws.element_size(),
@@ -206,24 +262,25 @@ def decode_step(q, k_new, v_new, k_cache, v_cache, lengths, slot_ids=None, *, ou
 def decode_step_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths, *, out=None,
                       status=None, kernel="auto", grid_ctas=0, workspace=None, stream=None,
                       sched_pad=None, sink=None, window=0, kept_prefix=0, k_scale=None, v_scale=None,
-                      wait_limit_cycles=0, test_stall=False):
+                      wait_limit_cycles=0, test_stall=False, k_group_scale=None,
+                      v_group_scale=None):
     """One decode step on a paged cache (num_blocks, Hkv, block_size, D) with
     a (B, max_blocks) int32 block table (-1 = unused). Appends in place."""
     dt, out = _common_checks(q, k_new, v_new, (("k_blocks", k_blocks), ("v_blocks", v_blocks)),
-                             lengths, out)
+                             lengths, out, groups=(k_group_scale, v_group_scale))
     B, Hq, D = q.shape
     NB, Hkv, BS, D2 = k_blocks.shape
-    if D2 != D or v_blocks.shape != k_blocks.shape or k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D):
+    if (D2 * 2 if dt == E2M1 else D2) != D or v_blocks.shape != k_blocks.shape or k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D):
         raise ValueError("shape mismatch between q, k_new, v_new and the blocks")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
             or not block_table.is_contiguous():
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor")
     MB = block_table.shape[1]
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
-              wait_limit_cycles, test_stall)
+              wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
     need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
-    ws = _workspace(q.device, need) if workspace is None else workspace
+    ws = _workspace(q.device, need, stream) if workspace is None else workspace
     code = lib.gqa_decode_step_paged_ex(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_blocks),
                                         _ptr(v_blocks), _ptr(block_table), _ptr(lengths), _ptr(out),
                                         B, Hq, Hkv, D, NB, BS, MB, dt, _ptr(ws),
@@ -235,23 +292,25 @@ def decode_step_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths,
 
 def attend(q, k_cache, v_cache, lengths, slot_ids=None, *, out=None, status=None, kernel="auto",
            grid_ctas=0, workspace=None, stream=None, sched_pad=None, sink=None, window=0,
-           kept_prefix=0, k_scale=None, v_scale=None, wait_limit_cycles=0, test_stall=False):
+           kept_prefix=0, k_scale=None, v_scale=None, wait_limit_cycles=0, test_stall=False, k_group_scale=None,
+           v_group_scale=None):
     """Read-only attend on a dense (R, Hkv, Smax, D) cache: slots
     ``0..lengths[b]-1`` (1 <= lengths[b] <= Smax), nothing written but ``out``.
     ``q`` (B, Hq, D) is float32 or bfloat16 whatever the cache dtype."""
     dt, out = _common_checks(q, None, None, (("k_cache", k_cache), ("v_cache", v_cache)),
-                             lengths, out, q_any_dtype=True)
+                             lengths, out, q_any_dtype=True,
+                             groups=(k_group_scale, v_group_scale))
     B, Hq, D = q.shape
     R, Hkv, Smax, D2 = k_cache.shape
-    if D2 != D or v_cache.shape != k_cache.shape or Hq % Hkv:
+    if (D2 * 2 if dt == E2M1 else D2) != D or v_cache.shape != k_cache.shape or Hq % Hkv:
         raise ValueError("shape mismatch between q and the caches")
     if slot_ids is not None and (slot_ids.dtype != torch.int32 or slot_ids.shape != (B,)):
         raise TypeError("slot_ids must be int32 of shape (B,)")
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
-              wait_limit_cycles, test_stall)
+              wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
     need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
-    ws = _workspace(q.device, need) if workspace is None else workspace
+    ws = _workspace(q.device, need, stream) if workspace is None else workspace
     code = lib.gqa_attend(_ptr(q), _DTYPES[q.dtype], _ptr(k_cache), _ptr(v_cache), _ptr(lengths),
                           _ptr(slot_ids), _ptr(out), B, Hq, Hkv, D, R, Smax, dt, _ptr(ws),
                           ws.numel() * ws.element_size(), _ptr(status), _stream(stream),
@@ -263,22 +322,24 @@ def attend(q, k_cache, v_cache, lengths, slot_ids=None, *, out=None, status=None
 def attend_paged(q, k_blocks, v_blocks, block_table, lengths, *, out=None, status=None,
                  kernel="auto", grid_ctas=0, workspace=None, stream=None, sched_pad=None,
                  sink=None, window=0, kept_prefix=0, k_scale=None, v_scale=None,
-                wait_limit_cycles=0, test_stall=False):
+                wait_limit_cycles=0, test_stall=False, k_group_scale=None,
+                 v_group_scale=None):
     """Read-only attend on a paged cache (num_blocks, Hkv, block_size, D)."""
     dt, out = _common_checks(q, None, None, (("k_blocks", k_blocks), ("v_blocks", v_blocks)),
-                             lengths, out, q_any_dtype=True)
+                             lengths, out, q_any_dtype=True,
+                             groups=(k_group_scale, v_group_scale))
     B, Hq, D = q.shape
     NB, Hkv, BS, D2 = k_blocks.shape
-    if D2 != D or v_blocks.shape != k_blocks.shape or Hq % Hkv:
+    if (D2 * 2 if dt == E2M1 else D2) != D or v_blocks.shape != k_blocks.shape or Hq % Hkv:
         raise ValueError("shape mismatch between q and the blocks")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
             or not block_table.is_contiguous():
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor")
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
-              wait_limit_cycles, test_stall)
+              wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
     need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
-    ws = _workspace(q.device, need) if workspace is None else workspace
+    ws = _workspace(q.device, need, stream) if workspace is None else workspace
     code = lib.gqa_attend_paged(_ptr(q), _DTYPES[q.dtype], _ptr(k_blocks), _ptr(v_blocks),
                                 _ptr(block_table), _ptr(lengths), _ptr(out), B, Hq, Hkv, D, NB, BS,
                                 block_table.shape[1], dt, _ptr(ws),
@@ -319,7 +380,7 @@ def decode_multi(q, k_new, v_new, k_cache, v_cache, lengths, cu_q, slot_ids=None
               wait_limit_cycles, test_stall)
     lib = _lib.load()
     need = lib.gqa_workspace_bytes_multi(B, Hq, Hkv, D, dt, int(max_q_len), ctypes.byref(o))
-    ws = _workspace(q.device, need) if workspace is None else workspace
+    ws = _workspace(q.device, need, stream) if workspace is None else workspace
     code = lib.gqa_decode_multi(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
                                 _ptr(lengths), _ptr(cu_q), _ptr(slot_ids), _ptr(out), B, T, int(max_q_len),
                                 Hq, Hkv, D, R, Smax, dt, _ptr(ws), ws.numel() * ws.element_size(),
@@ -347,13 +408,306 @@ def decode_multi_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths
               wait_limit_cycles, test_stall)
     lib = _lib.load()
     need = lib.gqa_workspace_bytes_multi(B, Hq, Hkv, D, dt, int(max_q_len), ctypes.byref(o))
-    ws = _workspace(q.device, need) if workspace is None else workspace
+    ws = _workspace(q.device, need, stream) if workspace is None else workspace
     code = lib.gqa_decode_multi_paged(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_blocks), _ptr(v_blocks),
                                       _ptr(block_table), _ptr(lengths), _ptr(cu_q), _ptr(out), B, T,
                                       int(max_q_len), Hq, Hkv, D, NB, BS, block_table.shape[1], dt,
                                       _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
                                       _stream(stream), ctypes.byref(o))
     _check(code, "gqa_decode_multi_paged")
+    return out
+
+
+# ---- writing and reading a cache, block selection ----
+
+def _rows_checks(caches, lengths, cu_q, slot_ids, block_table, groups, D):
+    """Checks shared by append and read; returns the cache's gqa_dtype."""
+    (_, k), (_, v) = caches
+    if not k.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device or k.dim() != 4:
+        raise ValueError("the two caches must be 4-dimensional and alike")
+    if not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("the caches must be contiguous")
+    if groups[0] is not None or groups[1] is not None:
+        _group_scales(caches, *groups, D)
+        code = E2M1
+    else:
+        code = _cache_code(k)
+        if k.shape[-1] != D:
+            raise ValueError("shape mismatch between the vectors and the caches")
+    B = lengths.shape[0]
+    for name, t, shape in (("lengths", lengths, (B,)), ("cu_q", cu_q, (B + 1,)), ("slot_ids", slot_ids, (B,))):
+        if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()
+                              or t.device != k.device):
+            raise TypeError(f"{name} must be a contiguous int32 {shape} tensor on the caches' device")
+    if block_table is not None and (block_table.dtype != torch.int32 or block_table.dim() != 2
+                                    or block_table.shape[0] != B or not block_table.is_contiguous()
+                                    or block_table.device != k.device):
+        raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor on the caches' device")
+    return code
+
+
+def _rows_opts(code, Hkv, device, k_scale, v_scale, groups):
+    """The options that carry a quantised cache's scales (None for the others)."""
+    if code < E4M3:
+        return None
+    return ctypes.byref(_opts("auto", 0, device=device, k_scale=k_scale, v_scale=v_scale, Hkv=Hkv,
+                              k_group_scale=groups[0], v_group_scale=groups[1]))
+
+
+def _status_checks(status, device):
+    if status is not None and (status.dtype != torch.int32 or status.device != device):
+        raise TypeError("status must be an int32 tensor on the caches' device")
+
+
+def _append(k_new, v_new, k, v, block_table, lengths, cu_q, slot_ids, scales, groups, k_bounds, status, stream,
+            names):
+    if k_new.dim() != 3 or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must both be (T, Hkv, D)")
+    T, Hkv, D = k_new.shape
+    code = _rows_checks(((names[0], k), (names[1], v)), lengths, cu_q, slot_ids, block_table, groups, D)
+    if k_new.dtype not in _DTYPES or v_new.dtype != k_new.dtype:
+        raise TypeError("k_new and v_new must both be float32 or bfloat16")
+    for t in (k_new, v_new):
+        if t.device != k.device or not t.is_contiguous():
+            raise ValueError("k_new and v_new must be contiguous and on the caches' device")
+    if k.shape[1] != Hkv:
+        raise ValueError("shape mismatch between k_new and the caches")
+    _status_checks(status, k.device)
+    n0, _, n2, _ = k.shape
+    block = 0
+    if k_bounds is not None:
+        if block_table is not None:
+            shape = (n0, Hkv, 2, D)
+        else:
+            if k_bounds.dim() != 5 or k_bounds.shape[2] < 1 or n2 % k_bounds.shape[2]:
+                raise ValueError("k_bounds must be (R, Hkv, NB, 2, D) with NB a divisor of Smax")
+            block = n2 // k_bounds.shape[2]
+            shape = (n0, Hkv, k_bounds.shape[2], 2, D)
+        if k_bounds.dtype != torch.bfloat16 or k_bounds.shape != shape or not k_bounds.is_contiguous() \
+                or k_bounds.device != k.device:
+            raise TypeError(f"k_bounds must be a contiguous bfloat16 {shape} tensor on the caches' device")
+    o = _rows_opts(code, Hkv, k.device, *scales, groups)
+    lib = _lib.load()
+    B = lengths.shape[0]
+    with _on(k.device):
+        if block_table is not None:
+            what = "gqa_append_paged"
+            rc = lib.gqa_append_paged(_ptr(k_new), _ptr(v_new), _DTYPES[k_new.dtype], _ptr(k), _ptr(v),
+                                      _ptr(block_table), _ptr(lengths), _ptr(cu_q), _ptr(k_bounds), B, T, Hkv, D, n0,
+                                      n2, block_table.shape[1], code, _ptr(status), _stream(stream, k.device), o)
+        else:
+            what = "gqa_append"
+            rc = lib.gqa_append(_ptr(k_new), _ptr(v_new), _DTYPES[k_new.dtype], _ptr(k), _ptr(v), _ptr(lengths),
+                                _ptr(cu_q), _ptr(slot_ids), _ptr(k_bounds), block, B, T, Hkv, D, n0, n2, code,
+                                _ptr(status), _stream(stream, k.device), o)
+    _check(rc, what)
+
+
+def append(k_new, v_new, k_cache, v_cache, lengths, cu_q, slot_ids=None, *, k_bounds=None, k_scale=None,
+           v_scale=None, k_group_scale=None, v_group_scale=None, status=None, stream=None):
+    """Writes the packed tokens cu_q[b] .. cu_q[b+1]-1 (``k_new``, ``v_new``
+    (T, Hkv, D), float32 or bfloat16) into slots lengths[b] .. of row b of a
+    dense (R, Hkv, Smax, D) cache, in place, rounded to its type. Tokens behind
+    the last row are ignored. ``k_bounds``, a bfloat16 (R, Hkv, NB, 2, D)
+    tensor, follows the smallest and largest key of every block of Smax // NB
+    slots for :func:`select_blocks`."""
+    _append(k_new, v_new, k_cache, v_cache, None, lengths, cu_q, slot_ids, (k_scale, v_scale),
+            (k_group_scale, v_group_scale), k_bounds, status, stream, ("k_cache", "v_cache"))
+
+
+def append_paged(k_new, v_new, k_blocks, v_blocks, block_table, lengths, cu_q, *, k_bounds=None, k_scale=None,
+                 v_scale=None, k_group_scale=None, v_group_scale=None, status=None, stream=None):
+    """:func:`append` into a paged cache (num_blocks, Hkv, block_size, D);
+    ``k_bounds`` is (num_blocks, Hkv, 2, D)."""
+    _append(k_new, v_new, k_blocks, v_blocks, block_table, lengths, cu_q, None, (k_scale, v_scale),
+            (k_group_scale, v_group_scale), k_bounds, status, stream, ("k_blocks", "v_blocks"))
+
+
+def _read(k, v, block_table, lengths, cu_q, T, slot_ids, dtype, k_out, v_out, scales, groups, status, stream, names):
+    if dtype not in _DTYPES:
+        raise TypeError("dtype must be torch.float32 or torch.bfloat16")
+    D = k.shape[-1] * (2 if groups[0] is not None or groups[1] is not None else 1)
+    code = _rows_checks(((names[0], k), (names[1], v)), lengths, cu_q, slot_ids, block_table, groups, D)
+    _status_checks(status, k.device)
+    n0, Hkv, n2, _ = k.shape
+    T, shape = int(T), (int(T), Hkv, D)
+    with torch.cuda.stream(stream) if stream is not None else _HERE:
+        k_out = torch.empty(shape, dtype=dtype, device=k.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dtype, device=k.device) if v_out is None else v_out
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t.shape != shape or t.dtype != dtype or t.device != k.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor on the caches' device")
+    o = _rows_opts(code, Hkv, k.device, *scales, groups)
+    lib = _lib.load()
+    B = lengths.shape[0]
+    with _on(k.device):
+        if block_table is not None:
+            what = "gqa_read_paged"
+            rc = lib.gqa_read_paged(_ptr(k), _ptr(v), _ptr(block_table), _ptr(lengths), _ptr(cu_q), _ptr(k_out),
+                                    _ptr(v_out), _DTYPES[dtype], B, T, Hkv, D, n0, n2, block_table.shape[1], code,
+                                    _ptr(status), _stream(stream, k.device), o)
+        else:
+            what = "gqa_read"
+            rc = lib.gqa_read(_ptr(k), _ptr(v), _ptr(lengths), _ptr(cu_q), _ptr(slot_ids), _ptr(k_out), _ptr(v_out),
+                              _DTYPES[dtype], B, T, Hkv, D, n0, n2, code, _ptr(status), _stream(stream, k.device), o)
+    _check(rc, what)
+    return k_out, v_out
+
+
+def read(k_cache, v_cache, lengths, cu_q, T, slot_ids=None, *, dtype=torch.bfloat16, k_out=None, v_out=None,
+         k_scale=None, v_scale=None, k_group_scale=None, v_group_scale=None, status=None, stream=None):
+    """Slots lengths[b] .. lengths[b] + cu_q[b+1] - cu_q[b] - 1 of row b of a
+    dense cache as vectors: two (T, Hkv, D) tensors of ``dtype``, packed by
+    ``cu_q`` (what :func:`append` with the same arguments wrote, rounded to the
+    cache's type). Packed rows of no batch row are left as they were."""
+    return _read(k_cache, v_cache, None, lengths, cu_q, T, slot_ids, dtype, k_out, v_out, (k_scale, v_scale),
+                 (k_group_scale, v_group_scale), status, stream, ("k_cache", "v_cache"))
+
+
+def read_paged(k_blocks, v_blocks, block_table, lengths, cu_q, T, *, dtype=torch.bfloat16, k_out=None, v_out=None,
+               k_scale=None, v_scale=None, k_group_scale=None, v_group_scale=None, status=None, stream=None):
+    """:func:`read` from a paged cache (num_blocks, Hkv, block_size, D)."""
+    return _read(k_blocks, v_blocks, block_table, lengths, cu_q, T, None, dtype, k_out, v_out, (k_scale, v_scale),
+                 (k_group_scale, v_group_scale), status, stream, ("k_blocks", "v_blocks"))
+
+
+class Selection:
+    """The blocks that :func:`select_blocks` kept: ``ids`` (B, Hkv, n_select)
+    int32, ascending, then -1; ``table`` (B * Hkv, n_select), the same blocks in
+    the cache seen as a pool of one-head blocks; ``lengths`` (B * Hkv,), the
+    slots they hold."""
+
+    def __init__(self, B, Hkv, n_select, block_size, device):
+        self.B, self.Hkv, self.n_select, self.block_size = B, Hkv, n_select, block_size
+        self._n = B * Hkv * n_select
+        self._buf = torch.empty(2 * self._n + B * Hkv, dtype=torch.int32, device=device)
+
+    @property
+    def ids(self):
+        return self._buf[:self._n].view(self.B, self.Hkv, self.n_select)
+
+    @property
+    def table(self):
+        return self._buf[self._n:2 * self._n].view(self.B * self.Hkv, self.n_select)
+
+    @property
+    def lengths(self):
+        return self._buf[2 * self._n:]
+
+    def _ptrs(self):
+        at = self._buf.data_ptr()
+        return ctypes.c_void_p(at), ctypes.c_void_p(at + 4 * self._n), ctypes.c_void_p(at + 8 * self._n)
+
+
+def _select(q, k_bounds, block_table, lengths, n_select, slot_ids, block_size, n_first, n_last, selection, status,
+            stream):
+    if not q.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if q.dtype not in _DTYPES or q.dim() != 3:
+        raise TypeError("q must be a float32 or bfloat16 (B, Hq, D) tensor")
+    B, Hq, D = q.shape
+    want = 5 if block_table is None else 4
+    if k_bounds.dtype != torch.bfloat16 or k_bounds.dim() != want or k_bounds.shape[-2] != 2 \
+            or k_bounds.shape[-1] != D:
+        raise TypeError("k_bounds must be bfloat16, (R, Hkv, NB, 2, D) for a dense cache and (num_blocks, Hkv, 2, D) "
+                        "for a paged one")
+    Hkv = k_bounds.shape[1]
+    if Hq % Hkv:
+        raise ValueError("Hq must be a multiple of Hkv")
+    for name, t in (("q", q), ("k_bounds", k_bounds)):
+        if t.device != q.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous and on q's device")
+    for name, t, shape in (("lengths", lengths, (B,)), ("slot_ids", slot_ids, (B,))):
+        if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()
+                              or t.device != q.device):
+            raise TypeError(f"{name} must be a contiguous int32 {shape} tensor on q's device")
+    if block_table is not None and (block_table.dtype != torch.int32 or block_table.dim() != 2
+                                    or block_table.shape[0] != B or not block_table.is_contiguous()
+                                    or block_table.device != q.device):
+        raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor on q's device")
+    _status_checks(status, q.device)
+    n_select = int(n_select)
+    if selection is None:
+        if n_select < 1:
+            raise ValueError("n_select must be positive")
+        with torch.cuda.stream(stream) if stream is not None else _HERE:
+            selection = Selection(B, Hkv, n_select, int(block_size), q.device)
+    elif (selection.B, selection.Hkv, selection.n_select, selection.block_size) != (B, Hkv, n_select, int(block_size)) \
+            or selection._buf.device != q.device:
+        raise ValueError("selection was made for other sizes")
+    ids, table, slots = selection._ptrs()
+    lib = _lib.load()
+    with _on(q.device):
+        if block_table is None:
+            what = "gqa_select_blocks"
+            rc = lib.gqa_select_blocks(_ptr(q), _DTYPES[q.dtype], _ptr(k_bounds), _ptr(lengths), _ptr(slot_ids), ids,
+                                       table, slots, B, Hq, Hkv, D, k_bounds.shape[0], k_bounds.shape[2],
+                                       selection.block_size, n_select, int(n_first), int(n_last), _ptr(status),
+                                       _stream(stream, q.device))
+        else:
+            what = "gqa_select_blocks_paged"
+            rc = lib.gqa_select_blocks_paged(_ptr(q), _DTYPES[q.dtype], _ptr(k_bounds), _ptr(block_table),
+                                             _ptr(lengths), ids, table, slots, B, Hq, Hkv, D, k_bounds.shape[0],
+                                             selection.block_size, block_table.shape[1], n_select, int(n_first),
+                                             int(n_last), _ptr(status), _stream(stream, q.device))
+    _check(rc, what)
+    return selection
+
+
+def select_blocks(q, k_bounds, lengths, n_select, slot_ids=None, *, block_size, n_first=1, n_last=1, selection=None,
+                  status=None, stream=None):
+    """Chooses, for every (row, cache head) of a dense cache, at most
+    ``n_select`` blocks of ``block_size`` slots: the first ``n_first`` and the
+    last ``n_last`` of the row's ceil(lengths[b] / block_size) blocks, and those
+    whose key bounds (``k_bounds`` (R, Hkv, NB, 2, D), see :func:`append`) allow
+    the largest score summed over the cache head's queries. ``lengths`` counts
+    the valid slots, as in :func:`attend`. Returns a :class:`Selection`
+    (``selection``, one of the same sizes, is filled instead when given)."""
+    return _select(q, k_bounds, None, lengths, n_select, slot_ids, block_size, n_first, n_last, selection, status,
+                   stream)
+
+
+def select_blocks_paged(q, k_bounds, block_table, lengths, n_select, *, block_size, n_first=1, n_last=1,
+                        selection=None, status=None, stream=None):
+    """:func:`select_blocks` over a paged cache: a block is a page of
+    ``block_size`` slots, ``k_bounds`` is (num_blocks, Hkv, 2, D)."""
+    return _select(q, k_bounds, block_table, lengths, n_select, None, block_size, n_first, n_last, selection, status,
+                   stream)
+
+
+def attend_selected(q, k_cache, v_cache, selection, *, out=None, status=None, kernel="auto", grid_ctas=0,
+                    workspace=None, stream=None, sched_pad=None, k_scale=None, v_scale=None, k_group_scale=None,
+                    v_group_scale=None):
+    """Read-only attend over the kept blocks of a dense (R, Hkv, Smax, D) or
+    paged (num_blocks, Hkv, block_size, D) float32, bfloat16 or E2M1 cache:
+    every query head attends the slots of its cache head's blocks in
+    ``selection``, and nothing is written but ``out`` (B, Hq, D) float32."""
+    if stream is not None and out is None:
+        with torch.cuda.stream(stream):
+            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    sel = selection
+    dt, out = _common_checks(q, None, None, (("k_cache", k_cache), ("v_cache", v_cache)), sel._buf, out,
+                             q_any_dtype=True, groups=(k_group_scale, v_group_scale))
+    B, Hq, D = q.shape
+    n0, Hkv, n2, D2 = k_cache.shape
+    if (D2 * 2 if dt == E2M1 else D2) != D or v_cache.shape != k_cache.shape or (B, Hkv) != (sel.B, sel.Hkv) \
+            or Hq % Hkv or n2 % sel.block_size:
+        raise ValueError("shape mismatch between q, the caches and the selection")
+    _status_checks(status, q.device)
+    o = ctypes.byref(_opts(kernel, grid_ctas, sched_pad, device=q.device, k_scale=k_scale, v_scale=v_scale, Hkv=Hkv,
+                           k_group_scale=k_group_scale, v_group_scale=v_group_scale))
+    lib = _lib.load()
+    _, table, slots = sel._ptrs()
+    with _on(q.device):
+        need = lib.gqa_workspace_bytes(B * Hkv, Hq // Hkv, 1, D, dt, o)
+        ws = _workspace(q.device, need, stream) if workspace is None else workspace
+        rc = lib.gqa_attend_selected(_ptr(q), _DTYPES[q.dtype], _ptr(k_cache), _ptr(v_cache), table, slots, _ptr(out),
+                                     B, Hq, Hkv, D, n0 * Hkv * (n2 // sel.block_size), sel.block_size, sel.n_select,
+                                     dt, _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
+                                     _stream(stream, q.device), o)
+    _check(rc, "gqa_attend_selected")
     return out
 
 

@@ -28,6 +28,13 @@ SIGNATURES = {
                                    P]),
     "gqa_validate_multi": (I, [P, P, P, P, I, I, I, I, I, I, I, P, P]),
     "gqa_attend_paged": (I, [P, I, P, P, P, P, P, I, I, I, I, I, I, I, I, P, Z, P, P, P]),
+    "gqa_append": (I, [P, P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P]),
+    "gqa_append_paged": (I, [P, P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P]),
+    "gqa_read": (I, [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P]),
+    "gqa_read_paged": (I, [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P, P]),
+    "gqa_select_blocks": (I, [P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P]),
+    "gqa_select_blocks_paged": (I, [P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P]),
+    "gqa_attend_selected": (I, [P, I, P, P, P, P, P, I, I, I, I, I, I, I, I, P, Z, P, P, P]),
     "gqa_trace_enable": (I, [I]),
     "gqa_trace_collect": (I, [I, P, P]),
     "gqa_kernel_name": (ctypes.c_char_p, [I]),
@@ -43,7 +50,8 @@ class GqaOptions(ctypes.Structure):
                 ("kept_prefix", ctypes.c_int), ("wait_limit_cycles", ctypes.c_int),
                 ("test_stall", ctypes.c_int), ("reserved", ctypes.c_int * 1),
                 ("head_sink", ctypes.c_void_p), ("kept_prefix_rows", ctypes.c_void_p),
-                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_group_scale", ctypes.c_void_p), ("v_group_scale", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()

@@ -1,6 +1,7 @@
 // The C ABI (include/gqa_decode.h): host-side argument checks, kernel
 // choice, workspace sizing, TMA descriptor encoding, launches and tracing.
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -47,6 +48,10 @@ bool unit_ok(gqa_dtype dt, int D, int G, long long cap_rows, bool multi)
 int pick_kernel(const gqa_options *opt, gqa_dtype dt, int D, int G, bool paged, int block_size,
                 long long cap_rows = -1, bool multi = false, long long units = 0)
 {
+    if (dt == GQA_DTYPE_E2M1)   // one kernel, on the tensor cores
+        return (!opt || opt->kernel == GQA_KERNEL_AUTO || opt->kernel == GQA_KERNEL_TC) && !multi && q4_supports(D, G)
+                   ? GQA_KERNEL_TC
+                   : -1;
     // GQA_KERNEL_TC5 is the tensor-core kernel with one of its unit forms on
     // tcgen05 (chosen at the launch)
     const int want = opt ? (opt->kernel == GQA_KERNEL_TC5 ? GQA_KERNEL_TC : opt->kernel) : GQA_KERNEL_AUTO;
@@ -86,6 +91,14 @@ int grid_for(int kernel, const gqa_options *opt, gqa_dtype dt, int D, int G)
     if (cudaGetDevice(&dev) != cudaSuccess)
         return 0;
     const int sms = sm_count(dev);
+    if (dt == GQA_DTYPE_E2M1) {
+        static std::atomic<int> per_sm[2];   // by D
+        std::atomic<int> &c = per_sm[D == 128];
+        int n = c.load(std::memory_order_relaxed);
+        if (!n)
+            c.store(n = q4_ctas_per_sm(D), std::memory_order_relaxed);
+        return sms * n;
+    }
     if (kernel == GQA_KERNEL_TC)
         return sms * tc_ctas_per_sm(dt == GQA_DTYPE_E4M3, G);   // G: query rows of a unit
     static std::mutex mu;
@@ -209,6 +222,7 @@ struct Shape {
     gqa_dtype q_dt = GQA_DTYPE_F32;
     bool multi = false;           // multi-token step: T packed tokens, q_len <= max_q
     int T = 0, max_q = 1;
+    int scale_heads = 0;          // attend over selected blocks: cache heads a batch row (see DecodeParams)
 };
 
 // How a multi-token step is cut into virtual rows: tokens per chunk (so that
@@ -236,7 +250,7 @@ gqa_status check_shape(const Shape &s)
 {
     if (s.B < 0 || s.Hq < 1 || s.Hkv < 1 || s.D < 1 || s.Hq % s.Hkv != 0)
         return GQA_ERR_INVALID_ARGUMENT;
-    if ((!valid_dtype(s.dt) && s.dt != GQA_DTYPE_E4M3) || !valid_dtype(s.q_dt))
+    if ((!valid_dtype(s.dt) && s.dt != GQA_DTYPE_E4M3 && s.dt != GQA_DTYPE_E2M1) || !valid_dtype(s.q_dt))
         return GQA_ERR_INVALID_ARGUMENT;
     if (s.paged) {
         if (s.num_blocks < 1 || s.block_size < 1 || s.max_blocks < 1)
@@ -263,9 +277,12 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
         return st;
     if (s.multi && (s.T < 0 || s.max_q < 0 || !cu_q))
         return GQA_ERR_INVALID_ARGUMENT;
-    const bool kv8 = s.dt == GQA_DTYPE_E4M3;
-    if (kv8 && (!opt || !opt->k_scale || !opt->v_scale || (reinterpret_cast<uintptr_t>(opt->k_scale) & 3u) ||
+    const bool kv8 = s.dt == GQA_DTYPE_E4M3, kv4 = s.dt == GQA_DTYPE_E2M1;
+    if ((kv8 || kv4) && (!opt || !opt->k_scale || !opt->v_scale || (reinterpret_cast<uintptr_t>(opt->k_scale) & 3u) ||
                 (reinterpret_cast<uintptr_t>(opt->v_scale) & 3u)))
+        return GQA_ERR_INVALID_ARGUMENT;
+    if (kv4 && (!opt->k_group_scale || !opt->v_group_scale || !aligned16(opt->k_group_scale) ||
+                !aligned16(opt->v_group_scale)))
         return GQA_ERR_INVALID_ARGUMENT;
     if (s.B == 0 || (s.multi && (s.T == 0 || s.max_q == 0)))
         return GQA_OK;
@@ -306,10 +323,15 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
     std::memset(&p, 0, sizeof p);
     p.q = q;
     p.kv8 = kv8 ? 1 : 0;
-    if (kv8) {
+    if (kv8 || kv4) {
         p.k_scale = opt->k_scale;
         p.v_scale = opt->v_scale;
     }
+    if (kv4) {
+        p.k_group = opt->k_group_scale;
+        p.v_group = opt->v_group_scale;
+    }
+    p.scale_heads = s.scale_heads;
     p.attend = s.attend ? 1 : 0;
     p.q_bf16 = s.q_dt == GQA_DTYPE_BF16 ? 1 : 0;
     p.k_new = s.attend ? nullptr : k_new;
@@ -344,7 +366,7 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
         p.kept_prefix = opt->kept_prefix;
         p.kept_prefix_rows = opt->kept_prefix_rows;
     }
-    p.tile = kernel == GQA_KERNEL_TC ? tc_tile() : simt_tile();
+    p.tile = kv4 ? q4_tile() : kernel == GQA_KERNEL_TC ? tc_tile() : simt_tile();
     // about the time a CTA spends finishing a sequence, in tiles of streaming
     p.pad_tiles = (opt && opt->sched_pad > 0) ? opt->sched_pad - 1 : kDefaultSchedPad;
     p.grid = grid;
@@ -360,7 +382,10 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
 
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (kernel == GQA_KERNEL_TC) {
+    if (kv4) {
+        TraceScope ts(1, cs);
+        e = q4_launch(p, cs);
+    } else if (kernel == GQA_KERNEL_TC) {
         TcMaps maps;
         const int T = p.tile;
         bool ok;
@@ -428,7 +453,7 @@ size_t gqa_workspace_bytes(int B, int Hq, int Hkv, int D, gqa_dtype dt, const gq
         return 0;
     int grid = grid_for(kernel, opt, dt, D, G);
     // AUTO may pick either kernel depending on the block size: size for the larger grid
-    if ((!opt || opt->kernel == GQA_KERNEL_AUTO) && simt_supports(D, G)) {
+    if (dt != GQA_DTYPE_E2M1 && (!opt || opt->kernel == GQA_KERNEL_AUTO) && simt_supports(D, G)) {
         const int g2 = grid_for(GQA_KERNEL_SIMT, opt, dt, D, G);
         grid = grid > g2 ? grid : g2;
     }
@@ -443,8 +468,8 @@ gqa_status gqa_decode_step_ex(const void *q, const void *k_new, const void *v_ne
                               gqa_dtype dt, void *workspace, size_t workspace_bytes,
                               int32_t *d_status, void *stream, const gqa_options *opt)
 {
-    // over an E4M3 cache the query and the new key / value are bfloat16
-    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 ? GQA_DTYPE_BF16 : dt;
+    // over an E4M3 or E2M1 cache the query and the new key / value are bfloat16
+    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 || dt == GQA_DTYPE_E2M1 ? GQA_DTYPE_BF16 : dt;
     Shape s = {B, Hq, Hkv, D, dt, false, R, Smax, 0, 0, 0, false, qdt};
     return run_step(s, q, k_new, v_new, k_cache, v_cache, lengths, slot_ids, nullptr, out,
                     workspace, workspace_bytes, d_status, stream, opt);
@@ -468,7 +493,7 @@ gqa_status gqa_decode_step_paged_ex(const void *q, const void *k_new, const void
                                     gqa_dtype dt, void *workspace, size_t workspace_bytes,
                                     int32_t *d_status, void *stream, const gqa_options *opt)
 {
-    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 ? GQA_DTYPE_BF16 : dt;
+    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 || dt == GQA_DTYPE_E2M1 ? GQA_DTYPE_BF16 : dt;
     Shape s = {B, Hq, Hkv, D, dt, true, 0, 0, num_blocks, block_size, max_blocks, false, qdt};
     return run_step(s, q, k_new, v_new, k_blocks, v_blocks, lengths, nullptr, block_table, out,
                     workspace, workspace_bytes, d_status, stream, opt);
@@ -553,7 +578,7 @@ gqa_status gqa_validate_multi(const int32_t *lengths, const int32_t *cu_q, const
 size_t gqa_workspace_bytes_multi(int B, int Hq, int Hkv, int D, gqa_dtype dt, int max_q_len,
                                  const gqa_options *opt)
 {
-    if (B < 0 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv || max_q_len < 0 || Hq / Hkv > 8)
+    if (B < 0 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv || max_q_len < 0 || Hq / Hkv > 8 || dt == GQA_DTYPE_E2M1)
         return 0;
     const int Gh = Hq / Hkv;
     // enough for whichever kernel the call will pick (AUTO may depend on the
@@ -631,6 +656,25 @@ gqa_status gqa_attend_paged(const void *q, gqa_dtype q_dtype, const void *k_bloc
                     opt);
 }
 
+gqa_status gqa_attend_selected(const void *q, gqa_dtype q_dtype, const void *k_cache, const void *v_cache,
+                               const int32_t *table, const int32_t *sel_lengths, float *out, int B, int Hq, int Hkv,
+                               int D, int pool_blocks, int block_size, int n_select, gqa_dtype kv_dtype,
+                               void *workspace, size_t workspace_bytes, int32_t *d_status, void *stream,
+                               const gqa_options *opt)
+{
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (long long)B * Hkv > INT_MAX)
+        return GQA_ERR_INVALID_ARGUMENT;
+    if (opt && (opt->window || opt->kept_prefix || opt->kept_prefix_rows || opt->head_sink))
+        return GQA_ERR_INVALID_ARGUMENT;
+    if (kv_dtype == GQA_DTYPE_E4M3)
+        return GQA_ERR_UNSUPPORTED;      // its kernels take one scale per head of a row's cache
+    // every (row, cache head) is a row of its own over the pool of one-head blocks
+    Shape s = {B * Hkv, Hq / Hkv, 1, D, kv_dtype, true, 0, 0, pool_blocks, block_size, n_select, true, q_dtype};
+    s.scale_heads = Hkv;
+    return run_step(s, q, nullptr, nullptr, const_cast<void *>(k_cache), const_cast<void *>(v_cache), sel_lengths,
+                    nullptr, table, out, workspace, workspace_bytes, d_status, stream, opt);
+}
+
 int gqa_trace_enable(int on)
 {
     std::lock_guard<std::mutex> g(trace().mu);
@@ -686,6 +730,6 @@ gqa_status gqa_workspace_reset(void *workspace, size_t workspace_bytes, void *st
                : GQA_ERR_CUDA;
 }
 
-int gqa_version(void) { return 100; }
+int gqa_version(void) { return 101; }
 
 }  // extern "C"

@@ -98,6 +98,10 @@ struct DecodeParams {
     int32_t *status;   // sticky content-error bits, may be null
     long long wait_cycles;  // consumer warps: SM clock cycles before a wait for a tile gives up
     int test_stall;         // 1: the consumers' first wait also waits on a barrier nothing completes
+    // E2M1 cache (k_cache / v_cache hold D / 2 bytes a vector)
+    void *k_group, *v_group;   // E4M3 scales, D / 16 a vector
+    int scale_heads;           // > 0: row b's scales are those of head b % scale_heads (rows that are
+                               // (batch row, cache head) pairs); 0: of head kvh
 };
 
 // Workspace layout (bytes from the workspace base), shared by host and device.

@@ -72,7 +72,7 @@ typedef enum gqa_status {
 typedef enum gqa_dtype {
     GQA_DTYPE_F32 = 0,  /* float32  (decode step: q, k_new, v_new and the cache) */
     GQA_DTYPE_BF16 = 1, /* bfloat16 (decode step: q, k_new, v_new and the cache) */
-    GQA_DTYPE_E4M3 = 2  /* a cache of OCP FP8 E4M3 bytes with per-cache-head float32
+    GQA_DTYPE_E4M3 = 2, /* a cache of OCP FP8 E4M3 bytes with per-cache-head float32
                            scales (gqa_options.k_scale / v_scale): K = k_scale[kvh] *
                            K8, V = v_scale[kvh] * V8 ("groupQueryAttention": kScale,
                            vScale). The decode step then takes bfloat16 q, k_new and
@@ -81,6 +81,20 @@ typedef enum gqa_dtype {
                            read-only attend takes a float32 or bfloat16 query. Only
                            the tensor-core kernel takes it (D = 128, G <= 8; paged
                            block sizes a power of two >= 8); single-token steps. */
+    GQA_DTYPE_E2M1 = 3  /* a cache of 4-bit E2M1 values: a vector is D / 2 bytes (dim
+                           2 i in the low half of byte i) and D / 16 bytes of E4M3
+                           scales (gqa_options.k_group_scale / v_group_scale, shaped
+                           like the cache with D / 16 for D), one per 16 dims, under
+                           a float32 scale g > 0 per cache head (k_scale / v_scale).
+                           A group x is stored as s = E4M3(min(max|x| / (6 g), 448)),
+                           t = float32(s g) and codes E2M1(x / t) (0 where t is 0),
+                           float32 arithmetic, rounded to nearest even; it stands for
+                           E2M1 * t. A group holding a NaN reads back as NaN. The
+                           decode step takes bfloat16 q, k_new and v_new, the
+                           read-only attend a float32 or bfloat16 query; D = 64 or
+                           128, G <= 8, any paged block size; GQA_KERNEL_AUTO or
+                           GQA_KERNEL_TC. No multi-token step (write prompts with
+                           gqa_append).                                            */
 } gqa_dtype;
 
 /* Bits OR-ed into *d_status by the kernels. */
@@ -158,6 +172,11 @@ typedef struct gqa_options {
     const float *k_scale;            /* (device) (Hkv,) float32: required with an
                                         E4M3 cache (GQA_DTYPE_E4M3), else ignored       */
     const float *v_scale;            /* (device) (Hkv,) float32, likewise               */
+    void *k_group_scale;             /* (device) E4M3 bytes, the key cache's shape with
+                                        D / 16 for D: required with an E2M1 cache
+                                        (then also k_scale / v_scale; 16-byte aligned),
+                                        written by the calls that append, else ignored  */
+    void *v_group_scale;             /* (device) the value cache's, likewise            */
 } gqa_options;
 
 /* Human-readable name of a status code (static storage). */
@@ -416,6 +435,114 @@ gqa_status gqa_decode_step_noalloc(const void *q, const void *k_new, const void 
                                    const int32_t *slot_ids, float *out,
                                    int B, int Hq, int Hkv, int D, int R, int Smax, gqa_dtype dt,
                                    int32_t *d_status, void *stream);
+
+/*
+ * Writing tokens without attending (a prompt, or the tokens of a step whose
+ * attention runs over selected blocks): packed tokens cu_q[b] .. cu_q[b+1]-1
+ * go to slots lengths[b] .. of row b, as in gqa_decode_multi, into a float32,
+ * bfloat16, E4M3 or E2M1 cache (opt carries the scales of the last two; opt
+ * may be NULL for the others). The vectors are float32 or bfloat16 and are
+ * rounded to the cache's type. Tokens of the packed batch that belong to no
+ * row (t >= cu_q[B]) are ignored. Of a row with a bad length, slot id or
+ * offsets nothing is written, of a token whose block is bad neither; the
+ * status bits are those of gqa_decode_multi.
+ *
+ *  k_new, v_new (device) (T, Hkv, D) of new_dtype; D a multiple of 16
+ *  k_bounds     (device) bfloat16 key bounds, or NULL. Dense: (R, Hkv,
+ *               Smax / bounds_block, 2, D), paged: (num_blocks, Hkv, 2, D) (a
+ *               block each). [..., 0, :] is the element-wise smallest key of
+ *               the block's slots, [..., 1, :] the largest, of the keys as
+ *               given (a float32 key rounded outwards; NaN if any is). A
+ *               token at a block's first slot starts the block's bounds
+ *               afresh, others widen them: bounds stay valid, if wider than
+ *               need be, when a row is cut back and written again.
+ *  bounds_block (dense, with k_bounds) slots a block: divides Smax, <= 1024
+ *               (paged: block_size, <= 1024 with k_bounds)
+ */
+gqa_status gqa_append(const void *k_new, const void *v_new, gqa_dtype new_dtype, void *k_cache, void *v_cache,
+                      const int32_t *lengths, const int32_t *cu_q, const int32_t *slot_ids, void *k_bounds,
+                      int bounds_block, int B, int T, int Hkv, int D, int R, int Smax, gqa_dtype kv_dtype,
+                      int32_t *d_status, void *stream, const gqa_options *opt);
+
+gqa_status gqa_append_paged(const void *k_new, const void *v_new, gqa_dtype new_dtype, void *k_blocks,
+                            void *v_blocks, const int32_t *block_table, const int32_t *lengths,
+                            const int32_t *cu_q, void *k_bounds, int B, int T, int Hkv, int D, int num_blocks,
+                            int block_size, int max_blocks, gqa_dtype kv_dtype, int32_t *d_status, void *stream,
+                            const gqa_options *opt);
+
+/*
+ * Reading slots back: k_out and v_out (T, Hkv, D) of out_dtype (float32 or
+ * bfloat16) receive slots lengths[b] .. lengths[b] + cu_q[b+1] - cu_q[b] - 1
+ * of row b at packed rows cu_q[b] .. (the slots that gqa_append with the same
+ * lengths and cu_q writes), as the values the cache stands for, rounded once
+ * to out_dtype. Packed rows of no batch row are left as they were; those of a
+ * bad row or block become NaN. The cache is only read.
+ */
+gqa_status gqa_read(const void *k_cache, const void *v_cache, const int32_t *lengths, const int32_t *cu_q,
+                    const int32_t *slot_ids, void *k_out, void *v_out, gqa_dtype out_dtype, int B, int T, int Hkv,
+                    int D, int R, int Smax, gqa_dtype kv_dtype, int32_t *d_status, void *stream,
+                    const gqa_options *opt);
+
+gqa_status gqa_read_paged(const void *k_blocks, const void *v_blocks, const int32_t *block_table,
+                          const int32_t *lengths, const int32_t *cu_q, void *k_out, void *v_out, gqa_dtype out_dtype,
+                          int B, int T, int Hkv, int D, int num_blocks, int block_size, int max_blocks,
+                          gqa_dtype kv_dtype, int32_t *d_status, void *stream, const gqa_options *opt);
+
+/*
+ * Block-sparse attention, in two calls. gqa_select_blocks chooses, for every
+ * (row, cache head), at most n_select of the row's blocks of slots by a bound
+ * on their scores; gqa_attend_selected attends the slots of those blocks.
+ *
+ * Selection. Row b holds slots 0 .. lengths[b] - 1 (1 <= lengths[b], as in
+ * gqa_attend) in n = ceil(lengths[b] / block_size) blocks. From the key bounds
+ * lo_j, hi_j of block j (k_bounds, kept by gqa_append) and the G = Hq / Hkv
+ * queries q_g of the cache head,
+ *   score_j = sum_d hi_jd sum_g max(q_gd, 0) + lo_jd sum_g min(q_gd, 0),
+ * the largest sum over the group of q_g . k for a key k within the bounds.
+ * The first n_first and the last n_last blocks are kept, then those of the
+ * highest scores; equal scores (of the exact sums) go to the lowest index and
+ * NaN counts as highest. With n <= n_select every block is kept.
+ *
+ *  q        (device) (B, Hq, D) float32 or bfloat16; D = 64, 128 or 256
+ *  k_bounds (device) bfloat16, as in gqa_append: dense (R, Hkv, NB, 2, D),
+ *           paged (num_blocks, Hkv, 2, D)
+ *  n_select >= n_first + n_last, n_first >= 0, n_last >= 1; at most 16384
+ *           blocks a row, and fewer than 2^31 (block, head) pairs in all
+ *  ids      (device) (B, Hkv, n_select) int32: the kept blocks of the row in
+ *           ascending order, then -1
+ *  table    (device) (B * Hkv, n_select) int32: the same blocks in the cache
+ *           seen as (blocks of one head): dense ((row * Hkv + head) * NB + j),
+ *           paged (block * Hkv + head); then -1
+ *  sel_lengths (device) (B * Hkv) int32: slots of the kept blocks
+ * A row with a bad length, slot id or block sets its status bit and selects
+ * nothing (ids and table -1, sel_lengths 0; the attend then gives NaN and
+ * GQA_STATUS_BAD_LENGTH).
+ */
+gqa_status gqa_select_blocks(const void *q, gqa_dtype q_dtype, const void *k_bounds, const int32_t *lengths,
+                             const int32_t *slot_ids, int32_t *ids, int32_t *table, int32_t *sel_lengths, int B,
+                             int Hq, int Hkv, int D, int R, int NB, int block_size, int n_select, int n_first,
+                             int n_last, int32_t *d_status, void *stream);
+
+gqa_status gqa_select_blocks_paged(const void *q, gqa_dtype q_dtype, const void *k_bounds,
+                                   const int32_t *block_table, const int32_t *lengths, int32_t *ids,
+                                   int32_t *table, int32_t *sel_lengths, int B, int Hq, int Hkv, int D,
+                                   int num_blocks, int block_size, int max_blocks, int n_select, int n_first,
+                                   int n_last, int32_t *d_status, void *stream);
+
+/*
+ * The read-only attend of every query head over the slots of its cache head's
+ * kept blocks. The cache, dense (Smax a multiple of block_size) or paged, is
+ * taken as a pool of pool_blocks = R * Hkv * (Smax / block_size) or num_blocks
+ * * Hkv blocks of one head each; `table` and `sel_lengths` are those of the
+ * selection. Softmax modifiers are refused, and so is an E4M3 cache. The
+ * workspace is gqa_workspace_bytes(B * Hkv, Hq / Hkv, 1, D, kv_dtype, opt).
+ * Other arguments, kernels and errors as in gqa_attend_paged.
+ */
+gqa_status gqa_attend_selected(const void *q, gqa_dtype q_dtype, const void *k_cache, const void *v_cache,
+                               const int32_t *table, const int32_t *sel_lengths, float *out, int B, int Hq, int Hkv,
+                               int D, int pool_blocks, int block_size, int n_select, gqa_dtype kv_dtype,
+                               void *workspace, size_t workspace_bytes, int32_t *d_status, void *stream,
+                               const gqa_options *opt);
 
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH. */
 int gqa_version(void);
