@@ -83,7 +83,7 @@ int pick_kernel(const gqa_options *opt, gqa_dtype dt, int D, int G, bool paged, 
 
 // Persistent grid: every SM holds as many CTAs as fit at once (cached per
 // device and kernel instantiation).
-int grid_for(int kernel, const gqa_options *opt, gqa_dtype dt, int D, int G)
+int grid_for(int kernel, const gqa_options *opt, gqa_dtype dt, int D, int G, gqa_dtype q_dt = GQA_DTYPE_BF16)
 {
     if (opt && opt->grid_ctas > 0)
         return opt->grid_ctas;
@@ -92,11 +92,12 @@ int grid_for(int kernel, const gqa_options *opt, gqa_dtype dt, int D, int G)
         return 0;
     const int sms = sm_count(dev);
     if (dt == GQA_DTYPE_E2M1) {
-        static std::atomic<int> per_sm[2];   // by D
-        std::atomic<int> &c = per_sm[D == 128];
+        // (a bfloat16 query's grid is the larger one: it sizes the workspace)
+        static std::atomic<int> per_sm[2][2];   // by D, query type
+        std::atomic<int> &c = per_sm[D == 128][q_dt == GQA_DTYPE_BF16];
         int n = c.load(std::memory_order_relaxed);
         if (!n)
-            c.store(n = q4_ctas_per_sm(D), std::memory_order_relaxed);
+            c.store(n = q4_ctas_per_sm(D, q_dt == GQA_DTYPE_BF16), std::memory_order_relaxed);
         return sms * n;
     }
     if (kernel == GQA_KERNEL_TC)
@@ -312,7 +313,7 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
     const int G = Gh * cut.tpc;             // query rows of a unit
     const int Bv = s.B * cut.chunks;        // (virtual) rows of the schedule
     const bool unit = kernel == GQA_KERNEL_UNIT;   // no schedule, no workspace
-    const int grid = unit ? s.B * s.Hkv : grid_for(kernel, opt, s.dt, s.D, G);
+    const int grid = unit ? s.B * s.Hkv : grid_for(kernel, opt, s.dt, s.D, G, s.q_dt);
     if (grid <= 0)
         return GQA_ERR_CUDA;
     const WorkspaceLayout lay = workspace_layout(Bv, s.Hkv, G, s.D, grid);

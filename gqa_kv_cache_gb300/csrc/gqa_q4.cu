@@ -48,6 +48,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kSub = 2;                       // 16-slot parts of a warp's share of a tile
 constexpr int kTile4 = kWarps * 16 * kSub;    // slots a tile
 constexpr int kRows = 8;                      // query rows (G <= 8)
+constexpr int kFlush = 8;                     // tiles between additions to the state in shared memory
 constexpr float kLift = 7.f;                  // a reference is set this far below the maximum ...
 constexpr float kRoom = 15.f;                 // ... and holds until a score is this far above it
 
@@ -79,93 +80,132 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = u32(__floats2half2_rn(x - f.x, y - f.y));
 }
 
-// Loads that see this SM's own earlier stores (the append).
-__device__ __forceinline__ uint4 ld16(const void *p) { return __ldcg(static_cast<const uint4 *>(p)); }
-__device__ __forceinline__ uint2 ld8(const void *p) { return __ldcg(static_cast<const uint2 *>(p)); }
-__device__ __forceinline__ uint32_t ld4(const void *p) { return __ldcg(static_cast<const uint32_t *>(p)); }
-__device__ __forceinline__ uint32_t ld2(const void *p) { return __ldcg(static_cast<const unsigned short *>(p)); }
-__device__ __forceinline__ uint32_t ld1(const void *p) { return __ldcg(static_cast<const uint8_t *>(p)); }
-
 // A warp's 16 slots of a tile, as loaded.
 template <int D>
 struct Frag {
     uint32_t k[2][D / 32];   // slots g, g + 8: the lane's D / 4 dims
     uint32_t v[4][D / 64];   // slots 2t, 2t + 1, 2t + 8, 2t + 9: the lane's D / 8 dims
-    uint32_t ks;             // K scales: slot g's in the low half (D = 128: two bytes, 64: one)
-    uint32_t vs;             // V scales: one byte a slot
+    uint32_t ks, vs;         // four scale bytes of K, of V: the 16 slots' D scales in memory order,
+                             // lane by lane (D = 64: lanes 16 .. 31 repeat lanes 0 .. 15)
+};
+
+// The lane's places in a cached vector, at vector 0 of the cache.
+struct Bases {
+    const uint8_t *k, *v, *ks, *vs;
 };
 
 template <int D>
-__device__ __forceinline__ void load_k(const DecodeParams &p, long long off, int t, uint32_t (&k)[D / 32], uint32_t &s)
-{
-    const uint8_t *c = static_cast<const uint8_t *>(p.k_cache) + (off >> 1) + (D / 8) * t;
-    const uint8_t *gs = static_cast<const uint8_t *>(p.k_group) + (off >> 4) + (D / 64) * t;
-    if constexpr (D == 128) {
-        const uint4 w = ld16(c);
-        k[0] = w.x; k[1] = w.y; k[2] = w.z; k[3] = w.w;
-        s = ld2(gs);
-    } else {
-        const uint2 w = ld8(c);
-        k[0] = w.x; k[1] = w.y;
-        s = ld1(gs);
-    }
-}
-
-template <int D>
-__device__ __forceinline__ void load_v(const DecodeParams &p, long long off, int g, uint32_t (&v)[D / 64], uint32_t &s)
-{
-    const uint8_t *c = static_cast<const uint8_t *>(p.v_cache) + (off >> 1) + (D / 16) * g;
-    s = ld1(static_cast<const uint8_t *>(p.v_group) + (off >> 4) + (D == 128 ? g : g >> 1));
-    if constexpr (D == 128) {
-        const uint2 w = ld8(c);
-        v[0] = w.x; v[1] = w.y;
-    } else {
-        v[0] = ld4(c);
-    }
-}
-
-// The slots s0 .. s0 + 15 of the cursor's unit. Slots outside the softmax
-// read as zeros. `bad` is set where the block table holds no usable block.
-template <int D>
-__device__ __forceinline__ void load_frag(const DecodeParams &p, const TileCursor &c, bool good, int s0, int lane,
-                                          Frag<D> &f, int &bad)
+__device__ __forceinline__ Bases bases(const DecodeParams &p, int lane)
 {
     const int g = lane >> 2, t = lane & 3;
-    f.ks = f.vs = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int s = s0 + g + 8 * i;
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w)
-            f.k[i][w] = 0;
-        if (good && attended(c.L, c.lo, c.P, s)) {
-            const long long off = slot_offset(p, c.b, c.kvh, s);
-            if (off < 0) {
-                bad = 1;
-            } else {
-                uint32_t sc;
-                load_k<D>(p, off, t, f.k[i], sc);
-                f.ks |= sc << (16 * i);
-            }
-        }
+    Bases r;
+    r.k = static_cast<const uint8_t *>(p.k_cache) + (D / 2) * g + (D / 8) * t;
+    r.v = static_cast<const uint8_t *>(p.v_cache) + (D / 2) * 2 * t + (D / 16) * g;
+    r.ks = static_cast<const uint8_t *>(p.k_group) + 4 * (lane % (D / 4));
+    r.vs = static_cast<const uint8_t *>(p.v_group) + 4 * (lane % (D / 4));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t ld4(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
+
+template <int D>
+__device__ __forceinline__ void ld_k(const uint8_t *p, uint32_t (&k)[D / 32])
+{
+    if constexpr (D == 128) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(p);
+        k[0] = w.x; k[1] = w.y; k[2] = w.z; k[3] = w.w;
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        k[0] = w.x; k[1] = w.y;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int s = s0 + 2 * t + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w)
-            f.v[i][w] = 0;
-        if (good && attended(c.L, c.lo, c.P, s)) {
-            const long long off = slot_offset(p, c.b, c.kvh, s);
-            if (off < 0) {
-                bad = 1;
-            } else {
-                uint32_t sc;
-                load_v<D>(p, off, g, f.v[i], sc);
-                f.vs |= sc << (8 * i);
-            }
-        }
+}
+
+template <int D>
+__device__ __forceinline__ void ld_v(const uint8_t *p, uint32_t (&v)[D / 64])
+{
+    if constexpr (D == 128) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        v[0] = w.x; v[1] = w.y;
+    } else {
+        v[0] = ld4(p);
     }
+}
+
+// Sixteen slots that are vectors `row` .. row + 15 of the cache.
+template <int D>
+__device__ __forceinline__ void load_k(const Bases &r, uint32_t row, Frag<D> &f)
+{
+    const uint8_t *c = r.k + (uint64_t)row * (D / 2);
+    ld_k<D>(c, f.k[0]);
+    ld_k<D>(c + 8 * (D / 2), f.k[1]);
+    f.ks = ld4(r.ks + (uint64_t)row * (D / 16));
+}
+
+template <int D>
+__device__ __forceinline__ void load_v(const Bases &r, uint32_t row, Frag<D> &f)
+{
+    const uint8_t *c = r.v + (uint64_t)row * (D / 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        ld_v<D>(c + (D / 2) * ((i & 1) + 8 * (i >> 1)), f.v[i]);
+    f.vs = ld4(r.vs + (uint64_t)row * (D / 16));
+}
+
+// The segment of a unit that tiles are being loaded from.
+struct Source {
+    int b, kvh, L, lo, P;
+    int t_last;        // its last tile here
+    int tp, gap;       // tile t sits at position t (t < tp) or t + gap
+    uint32_t line;     // dense: vector of slot 0
+    bool good;         // the row's content is in order
+};
+
+// Vector index of slot s of the source's unit in a paged cache, or -1.
+__device__ __noinline__ int paged_row(const int32_t *table, int block_size, int num_blocks, int Hkv, int kvh, int s)
+{
+    const int blk = __ldg(table + s / block_size);
+    if (blk < 0 || blk >= num_blocks)
+        return -1;
+    return (int)(((uint32_t)blk * Hkv + kvh) * (uint32_t)block_size + (uint32_t)(s % block_size));
+}
+
+// Sixteen slots from s0, each vector looked up by itself: any block size, and
+// a slot outside the softmax reads slot L instead (it gets weight 0, which
+// only a finite value survives). `bad` is set where the block table holds no
+// usable block (its output is NaN, whatever is read).
+template <int D, bool V, bool PAGED>
+__device__ __forceinline__ void load_masked(const DecodeParams &p, const Source &c, const Bases &r, int s0, int lane,
+                                            Frag<D> &f, int &bad)
+{
+    const int g = lane >> 2, t = lane & 3;
+    auto row = [&](int j) {
+        const int s = attended(c.L, c.lo, c.P, s0 + j) ? s0 + j : c.L;
+        if constexpr (PAGED) {
+            const int x = paged_row(p.block_table + (long long)c.b * p.max_blocks, p.block_size, p.num_blocks, p.Hkv,
+                                    c.kvh, s);
+            bad |= x == -1;
+            return x == -1 ? 0u : (uint32_t)x;
+        } else {
+            return c.line + (uint32_t)s;
+        }
+    };
+    // the lane's vectors, from the lane's place in vector 0; then its scales
+    if constexpr (V) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            ld_v<D>(r.v - (D / 2) * 2 * t + (uint64_t)row(2 * t + (i & 1) + 8 * (i >> 1)) * (D / 2), f.v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            ld_k<D>(r.k - (D / 2) * g + (uint64_t)row(g + 8 * i) * (D / 2), f.k[i]);
+    }
+    constexpr int W = D / 64;              // words of a vector's scales
+    const int w = lane % (D / 4);
+    const uint32_t at = row(w / W);
+    if constexpr (V)
+        f.vs = ld4(r.vs - 4 * w + 4 * (w % W) + (uint64_t)at * (D / 16));
+    else
+        f.ks = ld4(r.ks - 4 * w + 4 * (w % W) + (uint64_t)at * (D / 16));
 }
 
 // The new token's vector x (bfloat16, D of them) quantised into the cache at
@@ -201,37 +241,39 @@ __device__ __forceinline__ void append_vec(const __nv_bfloat16 *x, void *cache, 
         static_cast<uint8_t *>(groups)[(off >> 4) + lane / LG] = (uint8_t)s;
 }
 
-__device__ __forceinline__ int scale_head(const DecodeParams &p, const TileCursor &c)
+__device__ __forceinline__ int scale_head(const DecodeParams &p, int b, int kvh)
 {
-    return p.scale_heads ? c.b % p.scale_heads : c.kvh;
+    return p.scale_heads ? b % p.scale_heads : kvh;
 }
 
-// A warp's share of the cursor's tile: the append, then the loads.
+// The new token of the source's row into slot L.
 template <int D>
-__device__ __forceinline__ void load_part(const DecodeParams &p, const TileCursor &c, bool good, int warp, int u,
-                                          int lane, Frag<D> &f, int &bad)
+__device__ __noinline__ void append_token(const DecodeParams &p, int b, int kvh, int L, int lane)
 {
-    const int s0 = tile_slot0(c, kTile4) + warp * 16 * kSub + u * 16;
-    if (!p.attend && good && c.L >= s0 && c.L < s0 + 16) {
-        const long long off = slot_offset(p, c.b, c.kvh, c.L);
-        if (off >= 0) {
-            const int h = scale_head(p, c);
-            const long long src = ((long long)c.b * p.Hkv + c.kvh) * D;
-            append_vec<D>(static_cast<const __nv_bfloat16 *>(p.k_new) + src, p.k_cache, p.k_group, off,
-                          __ldg(p.k_scale + h), lane);
-            append_vec<D>(static_cast<const __nv_bfloat16 *>(p.v_new) + src, p.v_cache, p.v_group, off,
-                          __ldg(p.v_scale + h), lane);
-            __syncwarp();              // the loads below see the whole vector
-        }
+    const long long off = slot_offset(p, b, kvh, L);
+    if (off >= 0) {
+        const int h = scale_head(p, b, kvh);
+        const long long src = ((long long)b * p.Hkv + kvh) * D;
+        append_vec<D>(static_cast<const __nv_bfloat16 *>(p.k_new) + src, p.k_cache, p.k_group, off,
+                      __ldg(p.k_scale + h), lane);
+        append_vec<D>(static_cast<const __nv_bfloat16 *>(p.v_new) + src, p.v_cache, p.v_group, off,
+                      __ldg(p.v_scale + h), lane);
+        __syncwarp();              // the warp's loads see the whole vector
     }
-    load_frag<D>(p, c, good, s0, lane, f, bad);
 }
+
+// Where a warp's share of a tile lies.
+struct Place {
+    int s;                 // first slot
+    bool full;             // every slot is in the softmax and the vectors lie as loaded by load_k / load_v
+    uint32_t row[kSub];    // full: the parts' first vectors
+};
 
 // The unit's query fragments: lane (g, t) holds row g's D / 4 dims from
 // D / 4 * t, scaled by a power of two into f16's range; `mul` is the factor
 // that takes a product to a base-2 score for row g.
 template <int D, bool QF32>
-__device__ __forceinline__ void load_query(const DecodeParams &p, const TileCursor &c, int lane,
+__device__ __forceinline__ void load_query(const DecodeParams &p, int b, int kvh, int lane,
                                            uint32_t (&qh)[D / 16][2], uint32_t (&ql)[QF32 ? D / 16 : 1][2], float &mul)
 {
     constexpr int N = D / 4;
@@ -241,7 +283,7 @@ __device__ __forceinline__ void load_query(const DecodeParams &p, const TileCurs
     for (int i = 0; i < N; ++i)
         x[i] = 0.f;
     if (g < p.G) {
-        const long long at = ((long long)c.b * p.Hq + (long long)c.kvh * p.G + g) * D + N * t;
+        const long long at = ((long long)b * p.Hq + (long long)kvh * p.G + g) * D + N * t;
         if constexpr (QF32) {
             const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at);
 #pragma unroll
@@ -285,25 +327,32 @@ __device__ __forceinline__ void load_query(const DecodeParams &p, const TileCurs
         }
 }
 
-// Scores of a part's 16 slots: s[0], s[1] slot g and query rows 2t, 2t + 1;
-// s[2], s[3] slot g + 8.
+// Scores of a part's 16 slots before their scale: s[0], s[1] slot g and query
+// rows 2t, 2t + 1; s[2], s[3] slot g + 8.
 template <int D, bool QF32>
-__device__ __forceinline__ void scores(const Frag<D> &f, const uint32_t (&qh)[D / 16][2],
+__device__ __forceinline__ void scores(const Frag<D> &f, int lane, const uint32_t (&qh)[D / 16][2],
                                        const uint32_t (&ql)[QF32 ? D / 16 : 1][2], float (&s)[4])
 {
+    const int g = lane >> 2, t = lane & 3;
     float s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         s[i] = 0.f;
-    const __half2 sa = h2(e4m3x2_f16(f.ks & 0xffffu)), sb = h2(e4m3x2_f16(f.ks >> 16));
+    // the scales of slots g and g + 8: two groups a lane (D = 64: one)
+    constexpr int W = D / 64;              // words of a vector's scales
+    const int at = D == 128 ? 2 * g + (t >> 1) : g;
+    const int sh = D == 128 ? 16 * (t & 1) : 8 * t;
+    const uint32_t ka = __shfl_sync(0xffffffffu, f.ks, at) >> sh;
+    const uint32_t kb = __shfl_sync(0xffffffffu, f.ks, at + 8 * W) >> sh;
+    const __half2 sa = h2(e4m3x2_f16(ka)), sb = h2(e4m3x2_f16(kb));
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
         uint32_t a[4], b[4];           // four pairs of slot g, of slot g + 8
         e2m1x8_f16(f.k[0][w], a);
         e2m1x8_f16(f.k[1][w], b);
         // D = 128: the lane's first two words are one group, the others the next
-        const __half2 ma = (D == 128 && w >= 2) ? __high2half2(sa) : __low2half2(sa);
-        const __half2 mb = (D == 128 && w >= 2) ? __high2half2(sb) : __low2half2(sb);
+        const __half2 ma = w >= 2 ? __high2half2(sa) : __low2half2(sa);
+        const __half2 mb = w >= 2 ? __high2half2(sb) : __low2half2(sb);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             a[j] = u32(__hmul2(h2(a[j]), ma));
@@ -324,8 +373,9 @@ __device__ __forceinline__ void scores(const Frag<D> &f, const uint32_t (&qh)[D 
 // O^T += V^T P^T for a part's 16 slots; w[0..3] are the weights in the
 // positions of the scores.
 template <int D>
-__device__ __forceinline__ void weigh(const Frag<D> &f, const float (&w)[4], float (&o)[D / 16][4])
+__device__ __forceinline__ void weigh(const Frag<D> &f, int lane, const float (&w)[4], float (&o)[D / 16][4])
 {
+    const int g = lane >> 2, t = lane & 3;
     uint32_t h0, l0, h1, l1;
     split2(w[0], w[1], h0, l0);
     split2(w[2], w[3], h1, l1);
@@ -333,7 +383,13 @@ __device__ __forceinline__ void weigh(const Frag<D> &f, const float (&w)[4], flo
     h1 = movmatrix_t(h1);
     l0 = movmatrix_t(l0);
     l1 = movmatrix_t(l1);
-    const __half2 s01 = h2(e4m3x2_f16(f.vs & 0xffffu)), s23 = h2(e4m3x2_f16(f.vs >> 16));
+    constexpr int W = D / 64;
+    const int at = 2 * t * W + (D == 128 ? g >> 2 : 0);
+    const int by = D == 128 ? g & 3 : g >> 1;
+    const uint32_t w0 = __shfl_sync(0xffffffffu, f.vs, at), w1 = __shfl_sync(0xffffffffu, f.vs, at + W);
+    const uint32_t w2 = __shfl_sync(0xffffffffu, f.vs, at + 8 * W), w3 = __shfl_sync(0xffffffffu, f.vs, at + 9 * W);
+    const uint32_t sel = by | ((4 + by) << 4);
+    const __half2 s01 = h2(e4m3x2_f16(__byte_perm(w0, w1, sel))), s23 = h2(e4m3x2_f16(__byte_perm(w2, w3, sel)));
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
         uint32_t x[4][4];
@@ -342,62 +398,194 @@ __device__ __forceinline__ void weigh(const Frag<D> &f, const float (&w)[4], flo
             e2m1x8_f16(f.v[j][i], x[j]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const __half2 a0 = __hmul2(__lows2half2(h2(x[0][q]), h2(x[1][q])), s01);
-            const __half2 a1 = __hmul2(__highs2half2(h2(x[0][q]), h2(x[1][q])), s01);
-            const __half2 a2 = __hmul2(__lows2half2(h2(x[2][q]), h2(x[3][q])), s23);
-            const __half2 a3 = __hmul2(__highs2half2(h2(x[2][q]), h2(x[3][q])), s23);
-            mma_f16(o[4 * i + q], u32(a0), u32(a1), u32(a2), u32(a3), h0, h1);
-            mma_f16(o[4 * i + q], u32(a0), u32(a1), u32(a2), u32(a3), l0, l1);
+            const uint32_t a0 = u32(__hmul2(__lows2half2(h2(x[0][q]), h2(x[1][q])), s01));
+            const uint32_t a1 = u32(__hmul2(__highs2half2(h2(x[0][q]), h2(x[1][q])), s01));
+            const uint32_t a2 = u32(__hmul2(__lows2half2(h2(x[2][q]), h2(x[3][q])), s23));
+            const uint32_t a3 = u32(__hmul2(__highs2half2(h2(x[2][q]), h2(x[3][q])), s23));
+            mma_f16(o[4 * i + q], a0, a1, a2, a3, l0, l1);
+            mma_f16(o[4 * i + q], a0, a1, a2, a3, h0, h1);
         }
     }
 }
 
-template <int D, bool QF32>
-__global__ void __launch_bounds__(kThreads) q4_decode_kernel(const DecodeParams p)
+// The lane's part of the output state in shared memory: rows 2t, 2t + 1, dims
+// D / 8 * g ..
+template <int D>
+__device__ __forceinline__ float4 *out_at(float (&so)[kRows][D + 4], int lane, int row, int i)
+{
+    return reinterpret_cast<float4 *>(&so[2 * (lane & 3) + row][D / 8 * (lane >> 2) + 2 * i]);
+}
+
+// Adds the accumulators to the state in shared memory (ADD: there is one) and
+// clears them; the state is first scaled by r0, r1.
+template <int D, bool SCALE>
+__device__ __forceinline__ void flush(float (&so)[kRows][D + 4], int lane, float (&o)[D / 16][4], bool add, float r0,
+                                      float r1)
+{
+#pragma unroll
+    for (int i = 0; i < D / 16; i += 2) {
+        float4 *a = out_at<D>(so, lane, 0, i), *b = out_at<D>(so, lane, 1, i);
+        float4 x = make_float4(o[i][0], o[i][2], o[i + 1][0], o[i + 1][2]);
+        float4 y = make_float4(o[i][1], o[i][3], o[i + 1][1], o[i + 1][3]);
+        if (add) {
+            const float4 u = *a, v = *b;
+            x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+            y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+        }
+        if constexpr (SCALE) {
+            x = make_float4(x.x * r0, x.y * r0, x.z * r0, x.w * r0);
+            y = make_float4(y.x * r1, y.y * r1, y.z * r1, y.w * r1);
+        }
+        *a = x;
+        *b = y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            o[i][j] = o[i + 1][j] = 0.f;
+    }
+}
+
+template <int D, bool QF32, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 3) q4_decode_kernel(const DecodeParams p)
 {
     __shared__ long long sched[kThreads / 32 + 8];
     __shared__ TileWalk walk;
+    __shared__ TileCursor sm_cur[kWarps][2];   // the segments being computed and loaded, by parity
     __shared__ int sm_flag;
     __shared__ MergeBuf sm_merge;
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
     __shared__ __align__(16) float sm_o[kWarps][kRows][D + 4];
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2, t4 = lane & 3;
 
     // programmatic dependent of the previous kernel: read no input before it is done
     asm volatile("griddepcontrol.wait;" ::: "memory");
     schedule_walk(p, sched, &walk);
-    TileCursor cur;
     bool in_b = false;
-    bool more = walk_first(p, cur, walk, in_b);
-    if (!more)
-        return;
+    int par = 0;
+    {
+        TileCursor c;
+        if (!walk_first(p, c, walk, in_b))
+            return;
+        if (lane == 0)
+            sm_cur[warp][0] = c;
+        __syncwarp();
+    }
 
-    Frag<D> f[kSub];
-    int bad = 0, bad_next = 0;                  // of the current segment, of the tile loaded ahead
-    bool good = row_ok(p, cur.b, cur.L);
+    const Bases base = bases<D>(p, lane);
+    // whole pages of 16 slots: one vector index a part; else slot by slot
+    const int shift = PAGED ? __ffs(p.block_size) - 1 : 0;
+    const bool pages = !PAGED || (p.block_size >= 16 && (p.block_size & (p.block_size - 1)) == 0);
+    Frag<D> f[kSub] = {};
+    Source src = {};
+    Place at = {};
+    unsigned valid = 0;                        // bits 2 u, 2 u + 1: slots g, g + 8 of part u are in the softmax
+    int bad = 0;                               // of the tile loaded
+    int t = 0;
+    // PAGED: the block of part lane & 1 of the tile (t & ~15) + lane / 2, and of 16 tiles on
+    int page = 0, page_next = 0;
+
+    auto load_pages = [&](int tile) {
+        const int x = tile + (lane >> 1);
+        const int s = (x < src.tp ? x : x + src.gap) * kTile4 + warp * 16 * kSub + 16 * (lane & 1);
+        return x <= src.t_last && s <= src.L ? __ldg(p.block_table + (long long)src.b * p.max_blocks + (s >> shift))
+                                             : 0;
+    };
+    // the segment of cursor nxt becomes the source
+    auto enter = [&](const TileCursor &nxt) {
+        src.b = nxt.b;
+        src.kvh = nxt.kvh;
+        src.L = nxt.L;
+        src.lo = nxt.lo;
+        src.P = nxt.P;
+        src.tp = nxt.tp;
+        src.gap = nxt.gap;
+        src.good = row_ok(p, nxt.b, nxt.L);
+        t = nxt.t;
+        src.t_last = (int)min((long long)nxt.nr - 1, nxt.t + (nxt.end - nxt.g) - 1);
+        if constexpr (PAGED) {
+            if (src.good && pages) {
+                page = load_pages(t & ~15);
+                page_next = load_pages((t & ~15) + 16);
+            }
+        } else if (src.good) {
+            const int r = p.slot_ids ? __ldg(p.slot_ids + src.b) : src.b;
+            src.line = ((uint32_t)r * p.Hkv + src.kvh) * (uint32_t)p.Smax;
+        }
+    };
+    // finds tile t of the source, appends the new token if it is there
+    auto place = [&] {
+        at.s = (t < src.tp ? t : t + src.gap) * kTile4 + warp * 16 * kSub;
+        const int e = at.s + 16 * kSub - 1;
+        at.full = src.good && pages && e <= src.L && (at.s >= src.lo || e < src.P);
+        if (!p.attend && src.good && (unsigned)(src.L - at.s) < 16u * kSub)
+            append_token<D>(p, src.b, src.kvh, src.L, lane);
+        valid = ~0u;
+        bad = 0;
+        if (at.full) {
 #pragma unroll
-    for (int u = 0; u < kSub; ++u)
-        load_part<D>(p, cur, good, warp, u, lane, f[u], bad);
+            for (int u = 0; u < kSub; ++u) {
+                if constexpr (PAGED) {
+                    int blk = __shfl_sync(0xffffffffu, page, 2 * (t & 15) + u);
+                    if (blk < 0 || blk >= p.num_blocks) {
+                        bad = 1;
+                        blk = 0;           // read something: the unit's output is NaN
+                    }
+                    at.row[u] = (((uint32_t)blk * p.Hkv + src.kvh) << shift) +
+                                ((uint32_t)(at.s + 16 * u) & ((1u << shift) - 1u));
+                } else {
+                    at.row[u] = src.line + (uint32_t)(at.s + 16 * u);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (!(src.good && attended(src.L, src.lo, src.P, at.s + 16 * u + 8 * i + g)))
+                        valid &= ~(1u << (2 * u + i));
+        }
+    };
+    auto load_keys = [&](int u) {
+        if (at.full)
+            load_k<D>(base, at.row[u], f[u]);
+        else if (src.good)
+            load_masked<D, false, PAGED>(p, src, base, at.s + 16 * u, lane, f[u], bad);
+    };
+    auto load_values = [&](int u) {
+        if (at.full)
+            load_v<D>(base, at.row[u], f[u]);
+        else if (src.good)
+            load_masked<D, true, PAGED>(p, src, base, at.s + 16 * u, lane, f[u], bad);
+    };
+
+    enter(sm_cur[warp][0]);
+    place();
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+        load_keys(u);
+        load_values(u);
+    }
 
     uint32_t qh[D / 16][2], ql[QF32 ? D / 16 : 1][2];
-    float mul0 = 0.f, mul1 = 0.f;               // product to base-2 score, rows 2t and 2t + 1
+    float mul0 = 0.f, mul1 = 0.f;              // product to base-2 score, rows 2t4 and 2t4 + 1
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float o[D / 16][4];
+    int seg_bad = 0;
     bool start = true;
-    int seg_first_t = 0;
+    int flushed = 0, since = 0;                // the state in shared memory, tiles since it was added to
+    int first_t = 0;
 
-    while (more) {
+    for (;;) {
         if (start) {
-            seg_first_t = cur.t;
-            if (!good && tid == 0 && cur.t == 0 && cur.kvh == 0)
-                report(p, row_error_bits(p, cur.b, cur.L));
+            first_t = t;
+            if (!src.good && tid == 0 && t == 0 && src.kvh == 0)
+                report(p, row_error_bits(p, src.b, src.L));
             float mul;
-            load_query<D, QF32>(p, cur, lane, qh, ql, mul);
-            const float ks = __ldg(p.k_scale + scale_head(p, cur));
-            mul0 = __shfl_sync(0xffffffffu, mul, 8 * t) * ks;
-            mul1 = __shfl_sync(0xffffffffu, mul, 8 * t + 4) * ks;
+            load_query<D, QF32>(p, src.b, src.kvh, lane, qh, ql, mul);
+            const float ks = __ldg(p.k_scale + scale_head(p, src.b, src.kvh));
+            mul0 = __shfl_sync(0xffffffffu, mul, 8 * t4) * ks;
+            mul1 = __shfl_sync(0xffffffffu, mul, 8 * t4 + 4) * ks;
             m0 = m1 = -INFINITY;
             l0 = l1 = 0.f;
 #pragma unroll
@@ -405,107 +593,149 @@ __global__ void __launch_bounds__(kThreads) q4_decode_kernel(const DecodeParams 
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     o[i][j] = 0.f;
+            seg_bad = 0;
+            flushed = since = 0;
             start = false;
         }
-        TileCursor nxt = cur;
-        bool nxt_in_b = in_b;
-        const bool more_n = walk_next(p, nxt, walk, nxt_in_b);
-        const bool good_n = more_n && (nxt.b == cur.b ? good : row_ok(p, nxt.b, nxt.L));
-        const int s0 = tile_slot0(cur, kTile4) + warp * 16 * kSub;
+        float s[kSub][4];
 #pragma unroll
-        for (int u = 0; u < kSub; ++u) {
-            float s[4];
-            scores<D, QF32>(f[u], qh, ql, s);
-            const int j0 = s0 + 16 * u + g;
-            const bool v0 = good && attended(cur.L, cur.lo, cur.P, j0);
-            const bool v1 = good && attended(cur.L, cur.lo, cur.P, j0 + 8);
-            s[0] = v0 ? s[0] * mul0 : -INFINITY;
-            s[1] = v0 ? s[1] * mul1 : -INFINITY;
-            s[2] = v1 ? s[2] * mul0 : -INFINITY;
-            s[3] = v1 ? s[3] * mul1 : -INFINITY;
-            float c0 = fmaxf(s[0], s[2]), c1 = fmaxf(s[1], s[3]);
-            if (__any_sync(0xffffffffu, c0 > m0 + kRoom || c1 > m1 + kRoom)) {
-#pragma unroll
-                for (int q = 4; q < 32; q <<= 1) {
-                    c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, q));
-                    c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, q));
-                }
-                // raised only where a score passed the room left
-                const float n0 = c0 > m0 + kRoom ? c0 - kLift : m0, n1 = c1 > m1 + kRoom ? c1 - kLift : m1;
-                const float r0 = m0 == -INFINITY ? 0.f : fast_ex2(m0 - n0);
-                const float r1 = m1 == -INFINITY ? 0.f : fast_ex2(m1 - n1);
-                m0 = n0;
-                m1 = n1;
-                l0 *= r0;
-                l1 *= r1;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    o[i][0] *= r0;
-                    o[i][1] *= r1;
-                    o[i][2] *= r0;
-                    o[i][3] *= r1;
+        for (int u = 0; u < kSub; ++u)
+            scores<D, QF32>(f[u], lane, qh, ql, s[u]);
+        seg_bad |= bad;
+        const unsigned ok = valid;
+        // the next tile: its keys replace these now, its values below
+        const bool last = t == src.t_last;
+        bool more = true, good = src.good;
+        if (!last) {
+            ++t;
+            if constexpr (PAGED) {
+                if ((t & 15) == 0) {
+                    page = page_next;
+                    page_next = load_pages(t + 16);
                 }
             }
-            s[0] = v0 ? fast_ex2(s[0] - m0) : 0.f;
-            s[1] = v0 ? fast_ex2(s[1] - m1) : 0.f;
-            s[2] = v1 ? fast_ex2(s[2] - m0) : 0.f;
-            s[3] = v1 ? fast_ex2(s[3] - m1) : 0.f;
-            l0 += s[0] + s[2];
-            l1 += s[1] + s[3];
-            weigh<D>(f[u], s, o);
-            if (more_n)
-                load_part<D>(p, nxt, good_n, warp, u, lane, f[u], bad_next);
+        } else {
+            TileCursor c = sm_cur[warp][par];
+            c.g += t - c.t;
+            c.t = t;
+            TileCursor n = c;
+            more = walk_next(p, n, walk, in_b);
+            __syncwarp();
+            if (lane == 0) {
+                sm_cur[warp][par] = c;
+                sm_cur[warp][par ^ 1] = n;
+            }
+            __syncwarp();
+            if (more)
+                enter(n);
+        }
+        if (more) {
+            place();
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+                load_keys(u);
         }
 
-        const bool unit_done = (cur.t == cur.nr - 1);
-        const bool cta_done = (cur.g + 1 == cur.end);
-        if (unit_done || cta_done) {
+        // weights: x = base-2 score - reference
+        float x[kSub][4];
+        float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[u][i] = fmaf(s[u][i], i & 1 ? mul1 : mul0, i & 1 ? -m1 : -m0);
+                x[u][i] = (ok >> (2 * u + (i >> 1))) & 1u ? x[u][i] : -INFINITY;
+            }
+            top0 = fmaxf(top0, fmaxf(x[u][0], x[u][2]));
+            top1 = fmaxf(top1, fmaxf(x[u][1], x[u][3]));
+        }
+        if (__any_sync(0xffffffffu, top0 > kRoom || top1 > kRoom)) {
+            float c0 = -INFINITY, c1 = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if ((ok >> (2 * u + i)) & 1u) {
+                        c0 = fmaxf(c0, s[u][2 * i] * mul0);
+                        c1 = fmaxf(c1, s[u][2 * i + 1] * mul1);
+                    }
 #pragma unroll
             for (int q = 4; q < 32; q <<= 1) {
-                l0 += __shfl_xor_sync(0xffffffffu, l0, q);
-                l1 += __shfl_xor_sync(0xffffffffu, l1, q);
+                c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, q));
+                c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, q));
             }
-            // a NaN score raises no reference: keep the NaN sum in the merge
-            m0 = (l0 != l0 && m0 == -INFINITY) ? 0.f : m0;
-            m1 = (l1 != l1 && m1 == -INFINITY) ? 0.f : m1;
-            if (g == 0) {
-                sm_m[warp][2 * t] = m0;
-                sm_m[warp][2 * t + 1] = m1;
-                sm_l[warp][2 * t] = l0;
-                sm_l[warp][2 * t + 1] = l1;
-            }
-            const float vs = __ldg(p.v_scale + scale_head(p, cur));
+            const float n0 = c0 - m0 > kRoom ? c0 - kLift : m0, n1 = c1 - m1 > kRoom ? c1 - kLift : m1;
+            const float r0 = m0 == -INFINITY ? 0.f : fast_ex2(m0 - n0);
+            const float r1 = m1 == -INFINITY ? 0.f : fast_ex2(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            l0 *= r0;
+            l1 *= r1;
+            flush<D, true>(sm_o[warp], lane, o, flushed, r0, r1);
+            flushed = 1;
+            since = 0;
 #pragma unroll
-            for (int i = 0; i < D / 16; i += 2) {
-                // rows 2t, 2t + 1: dims D / 8 * g + 2i .. + 3
-                *reinterpret_cast<float4 *>(&sm_o[warp][2 * t][D / 8 * g + 2 * i]) =
-                    make_float4(o[i][0] * vs, o[i][2] * vs, o[i + 1][0] * vs, o[i + 1][2] * vs);
-                *reinterpret_cast<float4 *>(&sm_o[warp][2 * t + 1][D / 8 * g + 2 * i]) =
-                    make_float4(o[i][1] * vs, o[i][3] * vs, o[i + 1][1] * vs, o[i + 1][3] * vs);
-            }
-            const bool seg_bad = __syncthreads_or(bad) != 0;
-            bad = 0;
-            if (seg_bad && good && tid == 0)
-                report(p, kBadBlock);
-            finish_segment<kWarps, kRows, D, D + 4, false>(p, cur, walk, seg_first_t, !good || seg_bad, sm_m, sm_l,
-                                                          sm_o, &sm_flag, sm_merge, tid, kThreads,
-                                                          [] { __syncthreads(); });
-            start = true;
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[u][i] = fmaf(s[u][i], i & 1 ? mul1 : mul0, i & 1 ? -m1 : -m0);
+                    x[u][i] = (ok >> (2 * u + (i >> 1))) & 1u ? x[u][i] : -INFINITY;
+                }
         }
-        bad |= bad_next;
-        bad_next = 0;
-        cur = nxt;
-        in_b = nxt_in_b;
-        good = good_n;
-        more = more_n;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[u][i] = fast_ex2(x[u][i]);
+            l0 += x[u][0] + x[u][2];
+            l1 += x[u][1] + x[u][3];
+            weigh<D>(f[u], lane, x[u], o);
+            if (more)
+                load_values(u);
+        }
+        if (++since == kFlush) {
+            flush<D, false>(sm_o[warp], lane, o, flushed, 1.f, 1.f);
+            flushed = 1;
+            since = 0;
+        }
+        if (!last)
+            continue;
+
+        // the end of the segment
+#pragma unroll
+        for (int q = 4; q < 32; q <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, q);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, q);
+        }
+        // a NaN score raises no reference: keep the NaN sum in the merge
+        m0 = (l0 != l0 && m0 == -INFINITY) ? 0.f : m0;
+        m1 = (l1 != l1 && m1 == -INFINITY) ? 0.f : m1;
+        if (g == 0) {
+            sm_m[warp][2 * t4] = m0;
+            sm_m[warp][2 * t4 + 1] = m1;
+            sm_l[warp][2 * t4] = l0;
+            sm_l[warp][2 * t4 + 1] = l1;
+        }
+        const TileCursor cur = sm_cur[warp][par];
+        par ^= 1;
+        const float vs = __ldg(p.v_scale + scale_head(p, cur.b, cur.kvh));
+        flush<D, true>(sm_o[warp], lane, o, flushed, vs, vs);
+        const bool any_bad = __syncthreads_or(seg_bad) != 0;
+        if (any_bad && good && tid == 0)
+            report(p, kBadBlock);
+        finish_segment<kWarps, kRows, D, D + 4, false>(p, cur, walk, first_t, !good || any_bad, sm_m, sm_l, sm_o,
+                                                      &sm_flag, sm_merge, tid, kThreads, [] { __syncthreads(); });
+        if (!more)
+            break;
+        start = true;
     }
 }
 
-template <int D, bool QF32>
+template <int D, bool QF32, bool PAGED>
 cudaError_t launch_one(const DecodeParams *p, cudaStream_t st, int *per_sm)
 {
     if (!p)
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, q4_decode_kernel<D, QF32>, kThreads, 0);
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, q4_decode_kernel<D, QF32, PAGED>, kThreads, 0);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p->grid);
     cfg.blockDim = dim3(kThreads);
@@ -515,7 +745,20 @@ cudaError_t launch_one(const DecodeParams *p, cudaStream_t st, int *per_sm)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, q4_decode_kernel<D, QF32>, *p);
+    return cudaLaunchKernelEx(&cfg, q4_decode_kernel<D, QF32, PAGED>, *p);
+}
+
+template <int D>
+cudaError_t launch_d(bool q_bf16, bool paged, const DecodeParams *p, cudaStream_t st, int *per_sm)
+{
+    if (q_bf16)
+        return paged ? launch_one<D, false, true>(p, st, per_sm) : launch_one<D, false, false>(p, st, per_sm);
+    return paged ? launch_one<D, true, true>(p, st, per_sm) : launch_one<D, true, false>(p, st, per_sm);
+}
+
+cudaError_t launch(int D, bool q_bf16, bool paged, const DecodeParams *p, cudaStream_t st, int *per_sm)
+{
+    return D == 128 ? launch_d<128>(q_bf16, paged, p, st, per_sm) : launch_d<64>(q_bf16, paged, p, st, per_sm);
 }
 
 }  // namespace
@@ -524,22 +767,16 @@ bool q4_supports(int D, int G) { return (D == 64 || D == 128) && G >= 1 && G <= 
 
 int q4_tile() { return kTile4; }
 
-// The smaller of the two query types' CTAs on an SM: one grid (and one
-// workspace size) for both.
-int q4_ctas_per_sm(int D)
+int q4_ctas_per_sm(int D, bool q_bf16)
 {
     int a = 0, b = 0;
-    const cudaError_t e = D == 128 ? launch_one<128, false>(nullptr, nullptr, &a) : launch_one<64, false>(nullptr, nullptr, &a);
-    const cudaError_t h = D == 128 ? launch_one<128, true>(nullptr, nullptr, &b) : launch_one<64, true>(nullptr, nullptr, &b);
+    if (launch(D, q_bf16, false, nullptr, nullptr, &a) != cudaSuccess ||
+        launch(D, q_bf16, true, nullptr, nullptr, &b) != cudaSuccess)
+        return 1;
     const int n = a < b ? a : b;
-    return (e == cudaSuccess && h == cudaSuccess && n > 0) ? n : 1;
+    return n > 0 ? n : 1;
 }
 
-cudaError_t q4_launch(const DecodeParams &p, cudaStream_t st)
-{
-    if (p.D == 128)
-        return p.q_bf16 ? launch_one<128, false>(&p, st, nullptr) : launch_one<128, true>(&p, st, nullptr);
-    return p.q_bf16 ? launch_one<64, false>(&p, st, nullptr) : launch_one<64, true>(&p, st, nullptr);
-}
+cudaError_t q4_launch(const DecodeParams &p, cudaStream_t st) { return launch(p.D, p.q_bf16, p.paged, &p, st, nullptr); }
 
 }  // namespace gqa
