@@ -305,6 +305,9 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
     if (s.multi && Gh > 8)
         return GQA_ERR_UNSUPPORTED;
     const long long cap_rows = s.paged ? (long long)s.max_blocks * s.block_size : (long long)s.Smax;
+    // the E2M1 kernel numbers the cache's vectors in 32 bits
+    if (kv4 && (s.paged ? (double)s.num_blocks * s.Hkv * s.block_size : (double)s.R * s.Hkv * s.Smax) >= 4294967296.0)
+        return GQA_ERR_UNSUPPORTED;
     const int kernel = pick_kernel(opt, s.dt, s.D, Gh, s.paged, s.block_size, cap_rows, s.multi,
                                    (long long)s.B * s.Hkv);
     if (kernel < 0)

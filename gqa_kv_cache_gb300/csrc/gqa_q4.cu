@@ -36,6 +36,8 @@
 #define GQA_MULTI_TOKEN 0   // single-token steps only
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "gqa_common.cuh"
 #include "gqa_fp4.cuh"
 #include "gqa_launch.h"
@@ -46,9 +48,18 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSub = 2;                       // 16-slot parts of a warp's share of a tile
-constexpr int kTile4 = kWarps * 16 * kSub;    // slots a tile
+constexpr int kShare = 16 * kSub;              // a warp's slots of a tile
+constexpr int kTile4 = kWarps * kShare;       // slots a tile
+#ifndef Q4_STAGES
+#define Q4_STAGES 3
+#endif
+#ifndef Q4_CTAS
+#define Q4_CTAS 3
+#endif
+constexpr int kStages = Q4_STAGES;            // tiles of a warp's ring
+constexpr int kCtas = Q4_CTAS;                // resident CTAs per SM
+constexpr int kSegs = 4;                      // segments a warp's copies and products are in at once (< kStages + 1)
 constexpr int kRows = 8;                      // query rows (G <= 8)
-constexpr int kFlush = 8;                     // tiles between additions to the state in shared memory
 constexpr float kLift = 7.f;                  // a reference is set this far below the maximum ...
 constexpr float kRoom = 15.f;                 // ... and holds until a score is this far above it
 
@@ -80,132 +91,57 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = u32(__floats2half2_rn(x - f.x, y - f.y));
 }
 
-// A warp's 16 slots of a tile, as loaded.
+// One tile's share of a warp in shared memory: its slots' codes of K and V
+// and their scales, vectors in slot order. With D = 128 a vector's four
+// 16-byte pieces and the two vectors of a 128-byte line are permuted so that
+// the operand loads below have no bank conflicts.
 template <int D>
-struct Frag {
-    uint32_t k[2][D / 32];   // slots g, g + 8: the lane's D / 4 dims
-    uint32_t v[4][D / 64];   // slots 2t, 2t + 1, 2t + 8, 2t + 9: the lane's D / 8 dims
-    uint32_t ks, vs;         // four scale bytes of K, of V: the 16 slots' D scales in memory order,
-                             // lane by lane (D = 64: lanes 16 .. 31 repeat lanes 0 .. 15)
+struct Stage {
+    uint8_t k[kShare * D / 2], v[kShare * D / 2];
+    uint8_t ks[kShare * D / 16], vs[kShare * D / 16];
 };
 
-// The lane's places in a cached vector, at vector 0 of the cache.
-struct Bases {
-    const uint8_t *k, *v, *ks, *vs;
-};
-
+// Offset of 16-byte piece c of the share's vector r.
 template <int D>
-__device__ __forceinline__ Bases bases(const DecodeParams &p, int lane)
+__device__ __forceinline__ int piece(int r, int c)
 {
-    const int g = lane >> 2, t = lane & 3;
-    Bases r;
-    r.k = static_cast<const uint8_t *>(p.k_cache) + (D / 2) * g + (D / 8) * t;
-    r.v = static_cast<const uint8_t *>(p.v_cache) + (D / 2) * 2 * t + (D / 16) * g;
-    r.ks = static_cast<const uint8_t *>(p.k_group) + 4 * (lane % (D / 4));
-    r.vs = static_cast<const uint8_t *>(p.v_group) + 4 * (lane % (D / 4));
-    return r;
+    if constexpr (D == 128)
+        return (r >> 1) * 128 + (((r ^ (r >> 2)) & 1) << 6) + ((c ^ (r & 2)) << 4);
+    else
+        return r * 32 + c * 16;
 }
 
-__device__ __forceinline__ uint32_t ld4(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
-
-template <int D>
-__device__ __forceinline__ void ld_k(const uint8_t *p, uint32_t (&k)[D / 32])
+__device__ __forceinline__ uint32_t smem_at(const void *p)
 {
-    if constexpr (D == 128) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        k[0] = w.x; k[1] = w.y; k[2] = w.z; k[3] = w.w;
-    } else {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p);
-        k[0] = w.x; k[1] = w.y;
-    }
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-template <int D>
-__device__ __forceinline__ void ld_v(const uint8_t *p, uint32_t (&v)[D / 64])
+// Asynchronous copies to shared memory; `n` of the bytes come from src (all or
+// none of them), the others are zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n)
 {
-    if constexpr (D == 128) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p);
-        v[0] = w.x; v[1] = w.y;
-    } else {
-        v[0] = ld4(p);
-    }
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void *src, int n)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Sixteen slots that are vectors `row` .. row + 15 of the cache.
-template <int D>
-__device__ __forceinline__ void load_k(const Bases &r, uint32_t row, Frag<D> &f)
-{
-    const uint8_t *c = r.k + (uint64_t)row * (D / 2);
-    ld_k<D>(c, f.k[0]);
-    ld_k<D>(c + 8 * (D / 2), f.k[1]);
-    f.ks = ld4(r.ks + (uint64_t)row * (D / 16));
-}
-
-template <int D>
-__device__ __forceinline__ void load_v(const Bases &r, uint32_t row, Frag<D> &f)
-{
-    const uint8_t *c = r.v + (uint64_t)row * (D / 2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        ld_v<D>(c + (D / 2) * ((i & 1) + 8 * (i >> 1)), f.v[i]);
-    f.vs = ld4(r.vs + (uint64_t)row * (D / 16));
-}
-
-// The segment of a unit that tiles are being loaded from.
-struct Source {
-    int b, kvh, L, lo, P;
-    int t_last;        // its last tile here
-    int tp, gap;       // tile t sits at position t (t < tp) or t + gap
-    uint32_t line;     // dense: vector of slot 0
-    bool good;         // the row's content is in order
-};
-
-// Vector index of slot s of the source's unit in a paged cache, or -1.
-__device__ __noinline__ int paged_row(const int32_t *table, int block_size, int num_blocks, int Hkv, int kvh, int s)
+// Vector index of slot s of a unit of a paged cache, or -1.
+__device__ __noinline__ long long paged_row(const int32_t *table, int block_size, int num_blocks, int Hkv, int kvh,
+                                            int s)
 {
     const int blk = __ldg(table + s / block_size);
     if (blk < 0 || blk >= num_blocks)
         return -1;
-    return (int)(((uint32_t)blk * Hkv + kvh) * (uint32_t)block_size + (uint32_t)(s % block_size));
-}
-
-// Sixteen slots from s0, each vector looked up by itself: any block size, and
-// a slot outside the softmax reads slot L instead (it gets weight 0, which
-// only a finite value survives). `bad` is set where the block table holds no
-// usable block (its output is NaN, whatever is read).
-template <int D, bool V, bool PAGED>
-__device__ __forceinline__ void load_masked(const DecodeParams &p, const Source &c, const Bases &r, int s0, int lane,
-                                            Frag<D> &f, int &bad)
-{
-    const int g = lane >> 2, t = lane & 3;
-    auto row = [&](int j) {
-        const int s = attended(c.L, c.lo, c.P, s0 + j) ? s0 + j : c.L;
-        if constexpr (PAGED) {
-            const int x = paged_row(p.block_table + (long long)c.b * p.max_blocks, p.block_size, p.num_blocks, p.Hkv,
-                                    c.kvh, s);
-            bad |= x == -1;
-            return x == -1 ? 0u : (uint32_t)x;
-        } else {
-            return c.line + (uint32_t)s;
-        }
-    };
-    // the lane's vectors, from the lane's place in vector 0; then its scales
-    if constexpr (V) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            ld_v<D>(r.v - (D / 2) * 2 * t + (uint64_t)row(2 * t + (i & 1) + 8 * (i >> 1)) * (D / 2), f.v[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            ld_k<D>(r.k - (D / 2) * g + (uint64_t)row(g + 8 * i) * (D / 2), f.k[i]);
-    }
-    constexpr int W = D / 64;              // words of a vector's scales
-    const int w = lane % (D / 4);
-    const uint32_t at = row(w / W);
-    if constexpr (V)
-        f.vs = ld4(r.vs - 4 * w + 4 * (w % W) + (uint64_t)at * (D / 16));
-    else
-        f.ks = ld4(r.ks - 4 * w + 4 * (w % W) + (uint64_t)at * (D / 16));
+    return ((long long)blk * Hkv + kvh) * block_size + s % block_size;
 }
 
 // The new token's vector x (bfloat16, D of them) quantised into the cache at
@@ -261,13 +197,6 @@ __device__ __noinline__ void append_token(const DecodeParams &p, int b, int kvh,
         __syncwarp();              // the warp's loads see the whole vector
     }
 }
-
-// Where a warp's share of a tile lies.
-struct Place {
-    int s;                 // first slot
-    bool full;             // every slot is in the softmax and the vectors lie as loaded by load_k / load_v
-    uint32_t row[kSub];    // full: the parts' first vectors
-};
 
 // The unit's query fragments: lane (g, t) holds row g's D / 4 dims from
 // D / 4 * t, scaled by a power of two into f16's range; `mul` is the factor
@@ -327,10 +256,156 @@ __device__ __forceinline__ void load_query(const DecodeParams &p, int b, int kvh
         }
 }
 
-// Scores of a part's 16 slots before their scale: s[0], s[1] slot g and query
-// rows 2t, 2t + 1; s[2], s[3] slot g + 8.
+// A segment of a unit: consecutive tiles that this CTA computes. Kept in
+// shared memory, one small ring a warp: the copies run ahead of the products.
+struct Segment {
+    TileCursor c;      // at its first tile
+    int t_last;        // its last tile
+    int good;          // the row's content is in order
+    int bad;           // a block that it needs is not usable
+};
+
+// What a warp's copies are taken from.
+template <int D, bool PAGED>
+struct Fetch {
+    int t, t_last, L, lo, P, tp, gap, b, kvh;
+    bool good;
+    uint32_t line;     // dense: vector of slot 0
+    int page, page_next;   // paged: the block of part lane & 1 of tile (t & ~15) + lane / 2; of 16 tiles on
+};
+
+__device__ __forceinline__ int share_slot(int t, int tp, int gap, int warp)
+{
+    return (t < tp ? t : t + gap) * kTile4 + warp * kShare;
+}
+
+template <int D, bool PAGED>
+__device__ __forceinline__ int load_page(const DecodeParams &p, const Fetch<D, PAGED> &f, int shift, int tile, int warp,
+                                         int lane)
+{
+    const int x = tile + (lane >> 1);
+    const int s = share_slot(x, f.tp, f.gap, warp) + 16 * (lane & 1);
+    return x <= f.t_last && s <= f.L ? __ldg(p.block_table + (long long)f.b * p.max_blocks + (s >> shift)) : 0;
+}
+
+// The copies' segment becomes that of cursor c.
+template <int D, bool PAGED>
+__device__ __forceinline__ void enter(const DecodeParams &p, const TileCursor &c, Fetch<D, PAGED> &f, Segment *seg,
+                                      int shift, bool pages, int warp, int lane)
+{
+    f.b = c.b;
+    f.kvh = c.kvh;
+    f.L = c.L;
+    f.lo = c.lo;
+    f.P = c.P;
+    f.tp = c.tp;
+    f.gap = c.gap;
+    f.t = c.t;
+    f.t_last = (int)min((long long)c.nr - 1, c.t + (c.end - c.g) - 1);
+    f.good = row_ok(p, c.b, c.L);
+    if constexpr (PAGED) {
+        if (f.good && pages) {
+            f.page = load_page(p, f, shift, f.t & ~15, warp, lane);
+            f.page_next = load_page(p, f, shift, (f.t & ~15) + 16, warp, lane);
+        }
+    } else if (f.good) {
+        const int r = p.slot_ids ? __ldg(p.slot_ids + f.b) : f.b;
+        f.line = ((uint32_t)r * p.Hkv + f.kvh) * (uint32_t)p.Smax;
+    }
+    if (lane == 0) {
+        seg->c = c;
+        seg->t_last = f.t_last;
+        seg->good = f.good;
+        seg->bad = 0;
+    }
+}
+
+// Starts the copies of the warp's share of tile f.t.
+template <int D, bool PAGED>
+__device__ __forceinline__ void fetch_tile(const DecodeParams &p, Fetch<D, PAGED> &f, Stage<D> &st, Segment *seg,
+                                           int shift, bool pages, int warp, int lane)
+{
+    if (!f.good)
+        return;                            // its output is NaN, whatever is in the stage
+    const int s = share_slot(f.t, f.tp, f.gap, warp);
+    if (!p.attend && (unsigned)(f.L - s) < (unsigned)kShare)
+        append_token<D>(p, f.b, f.kvh, f.L, lane);
+    constexpr int LV = D / 32;             // lanes (16-byte pieces) a vector
+    constexpr int VI = 32 / LV;            // vectors an instruction
+    constexpr int SB = D / 16;             // scale bytes a vector
+    const uint32_t dk = smem_at(st.k), dv = smem_at(st.v), dks = smem_at(st.ks), dvs = smem_at(st.vs);
+    const uint8_t *kc = static_cast<const uint8_t *>(p.k_cache), *vc = static_cast<const uint8_t *>(p.v_cache);
+    const uint8_t *kg = static_cast<const uint8_t *>(p.k_group), *vg = static_cast<const uint8_t *>(p.v_group);
+    const int e = s + kShare - 1;
+    if (pages && e <= f.L && (s >= f.lo || e < f.P)) {
+        // every slot is in the softmax, 16 vectors in a row at least
+        uint32_t row[kSub];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            if constexpr (PAGED) {
+                int blk = __shfl_sync(0xffffffffu, f.page, 2 * (f.t & 15) + u);
+                if (blk < 0 || blk >= p.num_blocks) {
+                    if (lane == 0)
+                        seg->bad = 1;
+                    blk = 0;               // read something: the unit's output is NaN
+                }
+                row[u] = (((uint32_t)blk * p.Hkv + f.kvh) << shift) + ((uint32_t)(s + 16 * u) & ((1u << shift) - 1u));
+            } else {
+                row[u] = f.line + (uint32_t)(s + 16 * u);
+            }
+        }
+        const int r0 = lane / LV, c0 = lane % LV;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            const uint64_t at = (uint64_t)row[u] * (D / 2) + r0 * (D / 2) + c0 * 16;
+#pragma unroll
+            for (int j = 0; j < 16 / VI; ++j) {
+                copy16(dk + piece<D>(16 * u + VI * j + r0, c0), kc + at + j * VI * (D / 2), 16);
+                copy16(dv + piece<D>(16 * u + VI * j + r0, c0), vc + at + j * VI * (D / 2), 16);
+            }
+        }
+        const uint64_t at = (uint64_t)((lane < 16 ? row[0] : row[kSub - 1]) + (lane & 15)) * SB;
+        copy_small<SB>(dks + lane * SB, kg + at, SB);
+        copy_small<SB>(dvs + lane * SB, vg + at, SB);
+        return;
+    }
+    // slot by slot: any block size; a slot outside the softmax becomes zeros
+    auto vector = [&](int j) -> long long {
+        if (!attended(f.L, f.lo, f.P, s + j))
+            return -1;
+        if constexpr (PAGED) {
+            const long long r = paged_row(p.block_table + (long long)f.b * p.max_blocks, p.block_size, p.num_blocks,
+                                          p.Hkv, f.kvh, s + j);
+            if (r < 0)
+                seg->bad = 1;
+            return r;
+        } else {
+            return (long long)f.line + s + j;
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < kShare / VI; ++j) {
+        const int r = VI * j + lane / LV, c = lane % LV;
+        const long long x = vector(r);
+        const uint64_t at = x < 0 ? 0 : (uint64_t)x * (D / 2) + c * 16;
+        copy16(dk + piece<D>(r, c), kc + at, x < 0 ? 0 : 16);
+        copy16(dv + piece<D>(r, c), vc + at, x < 0 ? 0 : 16);
+    }
+    const long long x = vector(lane);
+    const uint64_t at = x < 0 ? 0 : (uint64_t)x * SB;
+    copy_small<SB>(dks + lane * SB, kg + at, x < 0 ? 0 : SB);
+    copy_small<SB>(dvs + lane * SB, vg + at, x < 0 ? 0 : SB);
+}
+
+// The slot (of a part's 16) at row i of the products' slot side, i = 0 .. 7
+// (row i + 8: eight more). With it the value loads' four vectors at a time
+// are neighbours.
+__device__ __forceinline__ int slot_of(int i) { return (i >> 1) + 4 * (i & 1); }
+
+// Scores of part u before their scale: s[0], s[1] slot slot_of(g) and query
+// rows 2t, 2t + 1; s[2], s[3] eight slots on.
 template <int D, bool QF32>
-__device__ __forceinline__ void scores(const Frag<D> &f, int lane, const uint32_t (&qh)[D / 16][2],
+__device__ __forceinline__ void scores(const Stage<D> &st, int u, int lane, const uint32_t (&qh)[D / 16][2],
                                        const uint32_t (&ql)[QF32 ? D / 16 : 1][2], float (&s)[4])
 {
     const int g = lane >> 2, t = lane & 3;
@@ -338,21 +413,30 @@ __device__ __forceinline__ void scores(const Frag<D> &f, int lane, const uint32_
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         s[i] = 0.f;
-    // the scales of slots g and g + 8: two groups a lane (D = 64: one)
-    constexpr int W = D / 64;              // words of a vector's scales
-    const int at = D == 128 ? 2 * g + (t >> 1) : g;
-    const int sh = D == 128 ? 16 * (t & 1) : 8 * t;
-    const uint32_t ka = __shfl_sync(0xffffffffu, f.ks, at) >> sh;
-    const uint32_t kb = __shfl_sync(0xffffffffu, f.ks, at + 8 * W) >> sh;
-    const __half2 sa = h2(e4m3x2_f16(ka)), sb = h2(e4m3x2_f16(kb));
+    const int r = slot_of(g);
+    uint32_t k[2][D / 32];
+    __half2 sc[2];                         // the lane's group scales: two a vector (D = 64: one)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int v = 16 * u + r + 8 * i;
+        if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(st.k + piece<D>(v, t));
+            k[i][0] = w.x; k[i][1] = w.y; k[i][2] = w.z; k[i][3] = w.w;
+            sc[i] = h2(e4m3x2_f16(*reinterpret_cast<const uint16_t *>(st.ks + v * 8 + 2 * t)));
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2 *>(st.k + piece<D>(v, t >> 1) + 8 * (t & 1));
+            k[i][0] = w.x; k[i][1] = w.y;
+            sc[i] = h2(e4m3x2_f16(st.ks[v * 4 + t]));
+        }
+    }
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
-        uint32_t a[4], b[4];           // four pairs of slot g, of slot g + 8
-        e2m1x8_f16(f.k[0][w], a);
-        e2m1x8_f16(f.k[1][w], b);
+        uint32_t a[4], b[4];
+        e2m1x8_f16(k[0][w], a);
+        e2m1x8_f16(k[1][w], b);
         // D = 128: the lane's first two words are one group, the others the next
-        const __half2 ma = w >= 2 ? __high2half2(sa) : __low2half2(sa);
-        const __half2 mb = w >= 2 ? __high2half2(sb) : __low2half2(sb);
+        const __half2 ma = w >= 2 ? __high2half2(sc[0]) : __low2half2(sc[0]);
+        const __half2 mb = w >= 2 ? __high2half2(sc[1]) : __low2half2(sc[1]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             a[j] = u32(__hmul2(h2(a[j]), ma));
@@ -370,90 +454,83 @@ __device__ __forceinline__ void scores(const Frag<D> &f, int lane, const uint32_
         s[i] += s2[i];
 }
 
-// O^T += V^T P^T for a part's 16 slots; w[0..3] are the weights in the
-// positions of the scores.
+// O^T += V^T P^T over the warp's share; w[u][0..3] are the weights in the
+// positions of the scores. The products of a share are summed from zero and
+// then added to o: the matrix unit truncates its sums, which over a long
+// cache would add up to a relative 1e-5.
 template <int D>
-__device__ __forceinline__ void weigh(const Frag<D> &f, int lane, const float (&w)[4], float (&o)[D / 16][4])
+__device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float (&w)[kSub][4], float (&o)[D / 16][4])
 {
     const int g = lane >> 2, t = lane & 3;
-    uint32_t h0, l0, h1, l1;
-    split2(w[0], w[1], h0, l0);
-    split2(w[2], w[3], h1, l1);
-    h0 = movmatrix_t(h0);
-    h1 = movmatrix_t(h1);
-    l0 = movmatrix_t(l0);
-    l1 = movmatrix_t(l1);
-    constexpr int W = D / 64;
-    const int at = 2 * t * W + (D == 128 ? g >> 2 : 0);
-    const int by = D == 128 ? g & 3 : g >> 1;
-    const uint32_t w0 = __shfl_sync(0xffffffffu, f.vs, at), w1 = __shfl_sync(0xffffffffu, f.vs, at + W);
-    const uint32_t w2 = __shfl_sync(0xffffffffu, f.vs, at + 8 * W), w3 = __shfl_sync(0xffffffffu, f.vs, at + 9 * W);
-    const uint32_t sel = by | ((4 + by) << 4);
-    const __half2 s01 = h2(e4m3x2_f16(__byte_perm(w0, w1, sel))), s23 = h2(e4m3x2_f16(__byte_perm(w2, w3, sel)));
+    uint32_t h[kSub][2], l[kSub][2];
+    __half2 sc[kSub][2];
+    uint32_t v[kSub][4][D / 64];
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+        split2(w[u][0], w[u][1], h[u][0], l[u][0]);
+        split2(w[u][2], w[u][3], h[u][1], l[u][1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            h[u][i] = movmatrix_t(h[u][i]);
+            l[u][i] = movmatrix_t(l[u][i]);
+        }
+        uint32_t b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // rows 2t, 2t + 1, 2t + 8, 2t + 9 of the slot side
+            const int x = 16 * u + t + 4 * j;
+            if constexpr (D == 128) {
+                const uint2 y = *reinterpret_cast<const uint2 *>(st.v + piece<D>(x, g >> 1) + 8 * (g & 1));
+                v[u][j][0] = y.x;
+                v[u][j][1] = y.y;
+                b[j] = st.vs[x * 8 + g];
+            } else {
+                v[u][j][0] = *reinterpret_cast<const uint32_t *>(st.v + piece<D>(x, g >> 2) + 4 * (g & 3));
+                b[j] = st.vs[x * 4 + (g >> 1)];
+            }
+        }
+        sc[u][0] = h2(e4m3x2_f16(b[0] | (b[1] << 8)));
+        sc[u][1] = h2(e4m3x2_f16(b[2] | (b[3] << 8)));
+    }
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-        uint32_t x[4][4];
+        uint32_t x[kSub][4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            e2m1x8_f16(f.v[j][i], x[j]);
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                e2m1x8_f16(v[u][j][i], x[u][j]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const uint32_t a0 = u32(__hmul2(__lows2half2(h2(x[0][q]), h2(x[1][q])), s01));
-            const uint32_t a1 = u32(__hmul2(__highs2half2(h2(x[0][q]), h2(x[1][q])), s01));
-            const uint32_t a2 = u32(__hmul2(__lows2half2(h2(x[2][q]), h2(x[3][q])), s23));
-            const uint32_t a3 = u32(__hmul2(__highs2half2(h2(x[2][q]), h2(x[3][q])), s23));
-            mma_f16(o[4 * i + q], a0, a1, a2, a3, l0, l1);
-            mma_f16(o[4 * i + q], a0, a1, a2, a3, h0, h1);
-        }
-    }
-}
-
-// The lane's part of the output state in shared memory: rows 2t, 2t + 1, dims
-// D / 8 * g ..
-template <int D>
-__device__ __forceinline__ float4 *out_at(float (&so)[kRows][D + 4], int lane, int row, int i)
-{
-    return reinterpret_cast<float4 *>(&so[2 * (lane & 3) + row][D / 8 * (lane >> 2) + 2 * i]);
-}
-
-// Adds the accumulators to the state in shared memory (ADD: there is one) and
-// clears them; the state is first scaled by r0, r1.
-template <int D, bool SCALE>
-__device__ __forceinline__ void flush(float (&so)[kRows][D + 4], int lane, float (&o)[D / 16][4], bool add, float r0,
-                                      float r1)
-{
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < D / 16; i += 2) {
-        float4 *a = out_at<D>(so, lane, 0, i), *b = out_at<D>(so, lane, 1, i);
-        float4 x = make_float4(o[i][0], o[i][2], o[i + 1][0], o[i + 1][2]);
-        float4 y = make_float4(o[i][1], o[i][3], o[i + 1][1], o[i + 1][3]);
-        if (add) {
-            const float4 u = *a, v = *b;
-            x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
-            y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
-        }
-        if constexpr (SCALE) {
-            x = make_float4(x.x * r0, x.y * r0, x.z * r0, x.w * r0);
-            y = make_float4(y.x * r1, y.y * r1, y.z * r1, y.w * r1);
-        }
-        *a = x;
-        *b = y;
+            for (int u = 0; u < kSub; ++u) {
+                const uint32_t a0 = u32(__hmul2(__lows2half2(h2(x[u][0][q]), h2(x[u][1][q])), sc[u][0]));
+                const uint32_t a1 = u32(__hmul2(__highs2half2(h2(x[u][0][q]), h2(x[u][1][q])), sc[u][0]));
+                const uint32_t a2 = u32(__hmul2(__lows2half2(h2(x[u][2][q]), h2(x[u][3][q])), sc[u][1]));
+                const uint32_t a3 = u32(__hmul2(__highs2half2(h2(x[u][2][q]), h2(x[u][3][q])), sc[u][1]));
+                mma_f16(d, a0, a1, a2, a3, l[u][0], l[u][1]);
+                mma_f16(d, a0, a1, a2, a3, h[u][0], h[u][1]);
+            }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            o[i][j] = o[i + 1][j] = 0.f;
+            for (int j = 0; j < 4; ++j)
+                o[4 * i + q][j] += d[j];
+        }
     }
 }
 
 template <int D, bool QF32, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 3) q4_decode_kernel(const DecodeParams p)
+__global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const DecodeParams p)
 {
+    extern __shared__ __align__(128) unsigned char dyn[];
+    Stage<D>(*ring)[kStages] = reinterpret_cast<Stage<D>(*)[kStages]>(dyn);    // [kWarps]
     __shared__ long long sched[kThreads / 32 + 8];
     __shared__ TileWalk walk;
-    __shared__ TileCursor sm_cur[kWarps][2];   // the segments being computed and loaded, by parity
+    __shared__ Segment segs[kWarps][kSegs];
     __shared__ int sm_flag;
     __shared__ MergeBuf sm_merge;
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
-    __shared__ __align__(16) float sm_o[kWarps][kRows][D + 4];
+    __shared__ __align__(16) float sm_o[kWarps][kRows][D];
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane >> 2, t4 = lane & 3;
@@ -461,245 +538,155 @@ __global__ void __launch_bounds__(kThreads, 3) q4_decode_kernel(const DecodePara
     // programmatic dependent of the previous kernel: read no input before it is done
     asm volatile("griddepcontrol.wait;" ::: "memory");
     schedule_walk(p, sched, &walk);
-    bool in_b = false;
-    int par = 0;
-    {
-        TileCursor c;
-        if (!walk_first(p, c, walk, in_b))
-            return;
-        if (lane == 0)
-            sm_cur[warp][0] = c;
-        __syncwarp();
-    }
-
-    const Bases base = bases<D>(p, lane);
     // whole pages of 16 slots: one vector index a part; else slot by slot
     const int shift = PAGED ? __ffs(p.block_size) - 1 : 0;
     const bool pages = !PAGED || (p.block_size >= 16 && (p.block_size & (p.block_size - 1)) == 0);
-    Frag<D> f[kSub] = {};
-    Source src = {};
-    Place at = {};
-    unsigned valid = 0;                        // bits 2 u, 2 u + 1: slots g, g + 8 of part u are in the softmax
-    int bad = 0;                               // of the tile loaded
-    int t = 0;
-    // PAGED: the block of part lane & 1 of the tile (t & ~15) + lane / 2, and of 16 tiles on
-    int page = 0, page_next = 0;
 
-    auto load_pages = [&](int tile) {
-        const int x = tile + (lane >> 1);
-        const int s = (x < src.tp ? x : x + src.gap) * kTile4 + warp * 16 * kSub + 16 * (lane & 1);
-        return x <= src.t_last && s <= src.L ? __ldg(p.block_table + (long long)src.b * p.max_blocks + (s >> shift))
-                                             : 0;
-    };
-    // the segment of cursor nxt becomes the source
-    auto enter = [&](const TileCursor &nxt) {
-        src.b = nxt.b;
-        src.kvh = nxt.kvh;
-        src.L = nxt.L;
-        src.lo = nxt.lo;
-        src.P = nxt.P;
-        src.tp = nxt.tp;
-        src.gap = nxt.gap;
-        src.good = row_ok(p, nxt.b, nxt.L);
-        t = nxt.t;
-        src.t_last = (int)min((long long)nxt.nr - 1, nxt.t + (nxt.end - nxt.g) - 1);
-        if constexpr (PAGED) {
-            if (src.good && pages) {
-                page = load_pages(t & ~15);
-                page_next = load_pages((t & ~15) + 16);
-            }
-        } else if (src.good) {
-            const int r = p.slot_ids ? __ldg(p.slot_ids + src.b) : src.b;
-            src.line = ((uint32_t)r * p.Hkv + src.kvh) * (uint32_t)p.Smax;
-        }
-    };
-    // finds tile t of the source, appends the new token if it is there
-    auto place = [&] {
-        at.s = (t < src.tp ? t : t + src.gap) * kTile4 + warp * 16 * kSub;
-        const int e = at.s + 16 * kSub - 1;
-        at.full = src.good && pages && e <= src.L && (at.s >= src.lo || e < src.P);
-        if (!p.attend && src.good && (unsigned)(src.L - at.s) < 16u * kSub)
-            append_token<D>(p, src.b, src.kvh, src.L, lane);
-        valid = ~0u;
-        bad = 0;
-        if (at.full) {
-#pragma unroll
-            for (int u = 0; u < kSub; ++u) {
+    // the copies: tile f.t of segment sf is the next to fetch
+    Fetch<D, PAGED> f = {};
+    int sf = 0;
+    bool in_b = false, left;
+    {
+        TileCursor c;
+        left = walk_first(p, c, walk, in_b);
+        if (!left)
+            return;
+        enter(p, c, f, &segs[warp][0], shift, pages, warp, lane);
+        __syncwarp();
+    }
+    auto fetch = [&](int slot) {
+        if (left) {
+            fetch_tile(p, f, ring[warp][slot], &segs[warp][sf], shift, pages, warp, lane);
+            if (f.t < f.t_last) {
+                ++f.t;
                 if constexpr (PAGED) {
-                    int blk = __shfl_sync(0xffffffffu, page, 2 * (t & 15) + u);
-                    if (blk < 0 || blk >= p.num_blocks) {
-                        bad = 1;
-                        blk = 0;           // read something: the unit's output is NaN
+                    if ((f.t & 15) == 0 && f.good && pages) {
+                        f.page = f.page_next;
+                        f.page_next = load_page(p, f, shift, f.t + 16, warp, lane);
                     }
-                    at.row[u] = (((uint32_t)blk * p.Hkv + src.kvh) << shift) +
-                                ((uint32_t)(at.s + 16 * u) & ((1u << shift) - 1u));
-                } else {
-                    at.row[u] = src.line + (uint32_t)(at.s + 16 * u);
+                }
+            } else {
+                TileCursor c = segs[warp][sf].c;
+                c.g += f.t - c.t;
+                c.t = f.t;
+                left = walk_next(p, c, walk, in_b);
+                if (left) {
+                    sf = (sf + 1) % kSegs;
+                    enter(p, c, f, &segs[warp][sf], shift, pages, warp, lane);
+                    __syncwarp();
                 }
             }
-        } else {
-#pragma unroll
-            for (int u = 0; u < kSub; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (!(src.good && attended(src.L, src.lo, src.P, at.s + 16 * u + 8 * i + g)))
-                        valid &= ~(1u << (2 * u + i));
         }
+        copy_commit();                     // an empty group behind the last tile
     };
-    auto load_keys = [&](int u) {
-        if (at.full)
-            load_k<D>(base, at.row[u], f[u]);
-        else if (src.good)
-            load_masked<D, false, PAGED>(p, src, base, at.s + 16 * u, lane, f[u], bad);
-    };
-    auto load_values = [&](int u) {
-        if (at.full)
-            load_v<D>(base, at.row[u], f[u]);
-        else if (src.good)
-            load_masked<D, true, PAGED>(p, src, base, at.s + 16 * u, lane, f[u], bad);
-    };
-
-    enter(sm_cur[warp][0]);
-    place();
+    int slot = 0;                          // ring slot of the tile to compute
 #pragma unroll
-    for (int u = 0; u < kSub; ++u) {
-        load_keys(u);
-        load_values(u);
-    }
+    for (int i = 0; i < kStages - 1; ++i)
+        fetch(i);
 
     uint32_t qh[D / 16][2], ql[QF32 ? D / 16 : 1][2];
-    float mul0 = 0.f, mul1 = 0.f;              // product to base-2 score, rows 2t4 and 2t4 + 1
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float mul0, mul1;                      // product to base-2 score, rows 2t4 and 2t4 + 1
+    float m0, m1, l0, l1;
     float o[D / 16][4];
-    int seg_bad = 0;
-    bool start = true;
-    int flushed = 0, since = 0;                // the state in shared memory, tiles since it was added to
-    int first_t = 0;
+    for (int sc = 0;; sc = (sc + 1) % kSegs) {
+        // the next segment
+        const Segment *seg = &segs[warp][sc];
+        const int b = seg->c.b, kvh = seg->c.kvh, L = seg->c.L, lo = seg->c.lo, P = seg->c.P;
+        const int tp = seg->c.tp, gap = seg->c.gap, first_t = seg->c.t, t_last = seg->t_last;
+        const bool good = seg->good;
+        if (!good && tid == 0 && first_t == 0 && kvh == 0)
+            report(p, row_error_bits(p, b, L));
+        float mul;
+        load_query<D, QF32>(p, b, kvh, lane, qh, ql, mul);
+        const float ks = __ldg(p.k_scale + scale_head(p, b, kvh));
+        mul0 = __shfl_sync(0xffffffffu, mul, 8 * t4) * ks;
+        mul1 = __shfl_sync(0xffffffffu, mul, 8 * t4 + 4) * ks;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[i][j] = 0.f;
 
-    for (;;) {
-        if (start) {
-            first_t = t;
-            if (!src.good && tid == 0 && t == 0 && src.kvh == 0)
-                report(p, row_error_bits(p, src.b, src.L));
-            float mul;
-            load_query<D, QF32>(p, src.b, src.kvh, lane, qh, ql, mul);
-            const float ks = __ldg(p.k_scale + scale_head(p, src.b, src.kvh));
-            mul0 = __shfl_sync(0xffffffffu, mul, 8 * t4) * ks;
-            mul1 = __shfl_sync(0xffffffffu, mul, 8 * t4 + 4) * ks;
-            m0 = m1 = -INFINITY;
-            l0 = l1 = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    o[i][j] = 0.f;
-            seg_bad = 0;
-            flushed = since = 0;
-            start = false;
-        }
-        float s[kSub][4];
-#pragma unroll
-        for (int u = 0; u < kSub; ++u)
-            scores<D, QF32>(f[u], lane, qh, ql, s[u]);
-        seg_bad |= bad;
-        const unsigned ok = valid;
-        // the next tile: its keys replace these now, its values below
-        const bool last = t == src.t_last;
-        bool more = true, good = src.good;
-        if (!last) {
-            ++t;
-            if constexpr (PAGED) {
-                if ((t & 15) == 0) {
-                    page = page_next;
-                    page_next = load_pages(t + 16);
-                }
-            }
-        } else {
-            TileCursor c = sm_cur[warp][par];
-            c.g += t - c.t;
-            c.t = t;
-            TileCursor n = c;
-            more = walk_next(p, n, walk, in_b);
+        for (int t = first_t; t <= t_last; ++t) {
+            copy_wait<kStages - 2>();      // this lane's copies of the tile, then the other lanes'
             __syncwarp();
-            if (lane == 0) {
-                sm_cur[warp][par] = c;
-                sm_cur[warp][par ^ 1] = n;
-            }
-            __syncwarp();
-            if (more)
-                enter(n);
-        }
-        if (more) {
-            place();
+            fetch(slot == 0 ? kStages - 1 : slot - 1);
+            const Stage<D> &st = ring[warp][slot];
+            slot = slot + 1 == kStages ? 0 : slot + 1;
+            float s[kSub][4];
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
-                load_keys(u);
-        }
-
-        // weights: x = base-2 score - reference
-        float x[kSub][4];
-        float top0 = -INFINITY, top1 = -INFINITY;
+                scores<D, QF32>(st, u, lane, qh, ql, s[u]);
+            // bits 2 u + i: slot 16 u + slot_of(g) + 8 i is in the softmax
+            unsigned ok = good ? ~0u : 0u;
+            const int s0 = share_slot(t, tp, gap, warp);
+            if (s0 + kShare - 1 > L || (s0 < lo && s0 + kShare - 1 >= P)) {
 #pragma unroll
-        for (int u = 0; u < kSub; ++u) {
+                for (int u = 0; u < kSub; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[u][i] = fmaf(s[u][i], i & 1 ? mul1 : mul0, i & 1 ? -m1 : -m0);
-                x[u][i] = (ok >> (2 * u + (i >> 1))) & 1u ? x[u][i] : -INFINITY;
+                    for (int i = 0; i < 2; ++i)
+                        if (!attended(L, lo, P, s0 + 16 * u + slot_of(g) + 8 * i))
+                            ok &= ~(1u << (2 * u + i));
             }
-            top0 = fmaxf(top0, fmaxf(x[u][0], x[u][2]));
-            top1 = fmaxf(top1, fmaxf(x[u][1], x[u][3]));
-        }
-        if (__any_sync(0xffffffffu, top0 > kRoom || top1 > kRoom)) {
-            float c0 = -INFINITY, c1 = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < kSub; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if ((ok >> (2 * u + i)) & 1u) {
-                        c0 = fmaxf(c0, s[u][2 * i] * mul0);
-                        c1 = fmaxf(c1, s[u][2 * i + 1] * mul1);
-                    }
-#pragma unroll
-            for (int q = 4; q < 32; q <<= 1) {
-                c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, q));
-                c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, q));
-            }
-            const float n0 = c0 - m0 > kRoom ? c0 - kLift : m0, n1 = c1 - m1 > kRoom ? c1 - kLift : m1;
-            const float r0 = m0 == -INFINITY ? 0.f : fast_ex2(m0 - n0);
-            const float r1 = m1 == -INFINITY ? 0.f : fast_ex2(m1 - n1);
-            m0 = n0;
-            m1 = n1;
-            l0 *= r0;
-            l1 *= r1;
-            flush<D, true>(sm_o[warp], lane, o, flushed, r0, r1);
-            flushed = 1;
-            since = 0;
+            // x = base-2 score - reference
+            float x[kSub][4], top = -INFINITY;
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     x[u][i] = fmaf(s[u][i], i & 1 ? mul1 : mul0, i & 1 ? -m1 : -m0);
                     x[u][i] = (ok >> (2 * u + (i >> 1))) & 1u ? x[u][i] : -INFINITY;
+                    top = fmaxf(top, x[u][i]);
                 }
-        }
+            if (__any_sync(0xffffffffu, top > kRoom)) {
+                float c0 = -INFINITY, c1 = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kSub; ++u) {
+                for (int u = 0; u < kSub; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[u][i] = fast_ex2(x[u][i]);
-            l0 += x[u][0] + x[u][2];
-            l1 += x[u][1] + x[u][3];
-            weigh<D>(f[u], lane, x[u], o);
-            if (more)
-                load_values(u);
+                    for (int i = 0; i < 2; ++i)
+                        if ((ok >> (2 * u + i)) & 1u) {
+                            c0 = fmaxf(c0, s[u][2 * i] * mul0);
+                            c1 = fmaxf(c1, s[u][2 * i + 1] * mul1);
+                        }
+#pragma unroll
+                for (int q = 4; q < 32; q <<= 1) {
+                    c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, q));
+                    c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, q));
+                }
+                const float n0 = c0 - m0 > kRoom ? c0 - kLift : m0, n1 = c1 - m1 > kRoom ? c1 - kLift : m1;
+                const float r0 = m0 == -INFINITY ? 0.f : fast_ex2(m0 - n0);
+                const float r1 = m1 == -INFINITY ? 0.f : fast_ex2(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                l0 *= r0;
+                l1 *= r1;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    o[i][0] *= r0;
+                    o[i][1] *= r1;
+                    o[i][2] *= r0;
+                    o[i][3] *= r1;
+                }
+#pragma unroll
+                for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[u][i] = fmaf(s[u][i], i & 1 ? mul1 : mul0, i & 1 ? -m1 : -m0);
+                        x[u][i] = (ok >> (2 * u + (i >> 1))) & 1u ? x[u][i] : -INFINITY;
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[u][i] = fast_ex2(x[u][i]);
+                l0 += x[u][0] + x[u][2];
+                l1 += x[u][1] + x[u][3];
+            }
+            weigh<D>(st, lane, x, o);
         }
-        if (++since == kFlush) {
-            flush<D, false>(sm_o[warp], lane, o, flushed, 1.f, 1.f);
-            flushed = 1;
-            since = 0;
-        }
-        if (!last)
-            continue;
 
         // the end of the segment
 #pragma unroll
@@ -716,29 +703,60 @@ __global__ void __launch_bounds__(kThreads, 3) q4_decode_kernel(const DecodePara
             sm_l[warp][2 * t4] = l0;
             sm_l[warp][2 * t4 + 1] = l1;
         }
-        const TileCursor cur = sm_cur[warp][par];
-        par ^= 1;
-        const float vs = __ldg(p.v_scale + scale_head(p, cur.b, cur.kvh));
-        flush<D, true>(sm_o[warp], lane, o, flushed, vs, vs);
-        const bool any_bad = __syncthreads_or(seg_bad) != 0;
+        const float vs = __ldg(p.v_scale + scale_head(p, b, kvh));
+#pragma unroll
+        for (int i = 0; i < D / 16; i += 2) {
+            // rows 2t4, 2t4 + 1: dims D / 8 * g + 2 i .. + 3
+            *reinterpret_cast<float4 *>(&sm_o[warp][2 * t4][D / 8 * g + 2 * i]) =
+                make_float4(o[i][0] * vs, o[i][2] * vs, o[i + 1][0] * vs, o[i + 1][2] * vs);
+            *reinterpret_cast<float4 *>(&sm_o[warp][2 * t4 + 1][D / 8 * g + 2 * i]) =
+                make_float4(o[i][1] * vs, o[i][3] * vs, o[i + 1][1] * vs, o[i + 1][3] * vs);
+        }
+        __syncwarp();
+        TileCursor cur = seg->c;
+        cur.g += t_last - cur.t;
+        cur.t = t_last;
+        const bool any_bad = __syncthreads_or(seg->bad) != 0;
         if (any_bad && good && tid == 0)
             report(p, kBadBlock);
-        finish_segment<kWarps, kRows, D, D + 4, false>(p, cur, walk, first_t, !good || any_bad, sm_m, sm_l, sm_o,
-                                                      &sm_flag, sm_merge, tid, kThreads, [] { __syncthreads(); });
-        if (!more)
+        const bool end = !left && sc == sf;
+        finish_segment<kWarps, kRows, D, D, false>(p, cur, walk, first_t, !good || any_bad, sm_m, sm_l, sm_o,
+                                                  &sm_flag, sm_merge, tid, kThreads, [] { __syncthreads(); });
+        if (end)
             break;
-        start = true;
     }
+}
+
+template <int D>
+constexpr int dyn_bytes()
+{
+    return kWarps * kStages * (int)sizeof(Stage<D>);
 }
 
 template <int D, bool QF32, bool PAGED>
 cudaError_t launch_one(const DecodeParams *p, cudaStream_t st, int *per_sm)
 {
+    // the ring's size is set once a device
+    static std::atomic<uint64_t> ready;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(q4_decode_kernel<D, QF32, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 dyn_bytes<D>());
+        if (e != cudaSuccess)
+            return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     if (!p)
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, q4_decode_kernel<D, QF32, PAGED>, kThreads, 0);
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, q4_decode_kernel<D, QF32, PAGED>, kThreads,
+                                                             dyn_bytes<D>());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p->grid);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = dyn_bytes<D>();
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
