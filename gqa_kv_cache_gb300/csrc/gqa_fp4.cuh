@@ -56,6 +56,22 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&r)[4])
         : "r"(w));
 }
 
+// The pair of E2M1 codes in byte B of w as an f16 pair; exact.
+template <int B>
+__device__ __forceinline__ uint32_t e2m1x2_f16(uint32_t w)
+{
+    uint32_t r;
+    if constexpr (B == 0)
+        asm("{.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;}" : "=r"(r) : "r"(w));
+    else if constexpr (B == 1)
+        asm("{.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b1;}" : "=r"(r) : "r"(w));
+    else if constexpr (B == 2)
+        asm("{.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b2;}" : "=r"(r) : "r"(w));
+    else
+        asm("{.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b3;}" : "=r"(r) : "r"(w));
+    return r;
+}
+
 // Two float32 as a byte of E2M1 codes (lo in the low half; round to nearest
 // even, saturating to +-6).
 __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi)

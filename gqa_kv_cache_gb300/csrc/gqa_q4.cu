@@ -47,7 +47,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kSub = 2;                       // 16-slot parts of a warp's share of a tile
+constexpr int kSub = 2;                       // 16-slot parts of a warp's share of a tile (the code has two)
 constexpr int kShare = 16 * kSub;              // a warp's slots of a tile
 constexpr int kTile4 = kWarps * kShare;       // slots a tile
 #ifndef Q4_STAGES
@@ -66,7 +66,7 @@ constexpr float kRoom = 15.f;                 // ... and holds until a score is 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
                  "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -116,11 +116,22 @@ __device__ __forceinline__ uint32_t smem_at(const void *p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// Asynchronous copies to shared memory; `n` of the bytes come from src (all or
-// none of them), the others are zeros.
+// Asynchronous copies to shared memory (DO, SO: byte offsets), and those of
+// which `n` bytes come from src (all or none of them) and the others are zeros.
+template <int DO, int SO>
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DO), "n"(SO)
+                 : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void *src, int n)
@@ -256,19 +267,18 @@ __device__ __forceinline__ void load_query(const DecodeParams &p, int b, int kvh
         }
 }
 
-// A segment of a unit: consecutive tiles that this CTA computes. Kept in
-// shared memory, one small ring a warp: the copies run ahead of the products.
+// A segment of a unit: consecutive tiles that this CTA computes. Kept in a
+// small ring in shared memory: the copies run ahead of the products.
 struct Segment {
     TileCursor c;      // at its first tile
     int t_last;        // its last tile
     int good;          // the row's content is in order
-    int bad;           // a block that it needs is not usable
 };
 
 // What a warp's copies are taken from.
 template <int D, bool PAGED>
 struct Fetch {
-    int t, t_last, L, lo, P, tp, gap, b, kvh;
+    int t, t_last;     // (the rest of its segment is read from shared memory)
     bool good;
     uint32_t line;     // dense: vector of slot 0
     int page, page_next;   // paged: the block of part lane & 1 of tile (t & ~15) + lane / 2; of 16 tiles on
@@ -280,56 +290,49 @@ __device__ __forceinline__ int share_slot(int t, int tp, int gap, int warp)
 }
 
 template <int D, bool PAGED>
-__device__ __forceinline__ int load_page(const DecodeParams &p, const Fetch<D, PAGED> &f, int shift, int tile, int warp,
-                                         int lane)
+__device__ __forceinline__ int load_page(const DecodeParams &p, const Fetch<D, PAGED> &f, const TileCursor &c, int shift,
+                                         int tile, int warp, int lane)
 {
     const int x = tile + (lane >> 1);
-    const int s = share_slot(x, f.tp, f.gap, warp) + 16 * (lane & 1);
-    return x <= f.t_last && s <= f.L ? __ldg(p.block_table + (long long)f.b * p.max_blocks + (s >> shift)) : 0;
+    const int s = share_slot(x, c.tp, c.gap, warp) + 16 * (lane & 1);
+    return x <= f.t_last && s <= c.L ? __ldg(p.block_table + (long long)c.b * p.max_blocks + (s >> shift)) : 0;
 }
 
 // The copies' segment becomes that of cursor c.
 template <int D, bool PAGED>
-__device__ __forceinline__ void enter(const DecodeParams &p, const TileCursor &c, Fetch<D, PAGED> &f, Segment *seg,
+__device__ __forceinline__ void enter(const DecodeParams &p, const TileCursor &c, Fetch<D, PAGED> &f, Segment *seg, int *bad,
                                       int shift, bool pages, int warp, int lane)
 {
-    f.b = c.b;
-    f.kvh = c.kvh;
-    f.L = c.L;
-    f.lo = c.lo;
-    f.P = c.P;
-    f.tp = c.tp;
-    f.gap = c.gap;
     f.t = c.t;
     f.t_last = (int)min((long long)c.nr - 1, c.t + (c.end - c.g) - 1);
     f.good = row_ok(p, c.b, c.L);
     if constexpr (PAGED) {
         if (f.good && pages) {
-            f.page = load_page(p, f, shift, f.t & ~15, warp, lane);
-            f.page_next = load_page(p, f, shift, (f.t & ~15) + 16, warp, lane);
+            f.page = load_page(p, f, c, shift, f.t & ~15, warp, lane);
+            f.page_next = load_page(p, f, c, shift, (f.t & ~15) + 16, warp, lane);
         }
     } else if (f.good) {
-        const int r = p.slot_ids ? __ldg(p.slot_ids + f.b) : f.b;
-        f.line = ((uint32_t)r * p.Hkv + f.kvh) * (uint32_t)p.Smax;
+        const int r = p.slot_ids ? __ldg(p.slot_ids + c.b) : c.b;
+        f.line = ((uint32_t)r * p.Hkv + c.kvh) * (uint32_t)p.Smax;
     }
     if (lane == 0) {
         seg->c = c;
         seg->t_last = f.t_last;
         seg->good = f.good;
-        seg->bad = 0;
+        *bad = 0;
     }
 }
 
 // Starts the copies of the warp's share of tile f.t.
 template <int D, bool PAGED>
-__device__ __forceinline__ void fetch_tile(const DecodeParams &p, Fetch<D, PAGED> &f, Stage<D> &st, Segment *seg,
+__device__ __forceinline__ void fetch_tile(const DecodeParams &p, Fetch<D, PAGED> &f, const TileCursor &c, Stage<D> &st, int *bad,
                                            int shift, bool pages, int warp, int lane)
 {
     if (!f.good)
         return;                            // its output is NaN, whatever is in the stage
-    const int s = share_slot(f.t, f.tp, f.gap, warp);
-    if (!p.attend && (unsigned)(f.L - s) < (unsigned)kShare)
-        append_token<D>(p, f.b, f.kvh, f.L, lane);
+    const int s = share_slot(f.t, c.tp, c.gap, warp);
+    if (!p.attend && (unsigned)(c.L - s) < (unsigned)kShare)
+        append_token<D>(p, c.b, c.kvh, c.L, lane);
     constexpr int LV = D / 32;             // lanes (16-byte pieces) a vector
     constexpr int VI = 32 / LV;            // vectors an instruction
     constexpr int SB = D / 16;             // scale bytes a vector
@@ -337,7 +340,7 @@ __device__ __forceinline__ void fetch_tile(const DecodeParams &p, Fetch<D, PAGED
     const uint8_t *kc = static_cast<const uint8_t *>(p.k_cache), *vc = static_cast<const uint8_t *>(p.v_cache);
     const uint8_t *kg = static_cast<const uint8_t *>(p.k_group), *vg = static_cast<const uint8_t *>(p.v_group);
     const int e = s + kShare - 1;
-    if (pages && e <= f.L && (s >= f.lo || e < f.P)) {
+    if (pages && e <= c.L && (s >= c.lo || e < c.P)) {
         // every slot is in the softmax, 16 vectors in a row at least
         uint32_t row[kSub];
 #pragma unroll
@@ -345,39 +348,46 @@ __device__ __forceinline__ void fetch_tile(const DecodeParams &p, Fetch<D, PAGED
             if constexpr (PAGED) {
                 int blk = __shfl_sync(0xffffffffu, f.page, 2 * (f.t & 15) + u);
                 if (blk < 0 || blk >= p.num_blocks) {
-                    if (lane == 0)
-                        seg->bad = 1;
+                    *bad = 1;
                     blk = 0;               // read something: the unit's output is NaN
                 }
-                row[u] = (((uint32_t)blk * p.Hkv + f.kvh) << shift) + ((uint32_t)(s + 16 * u) & ((1u << shift) - 1u));
+                row[u] = (((uint32_t)blk * p.Hkv + c.kvh) << shift) + ((uint32_t)(s + 16 * u) & ((1u << shift) - 1u));
             } else {
                 row[u] = f.line + (uint32_t)(s + 16 * u);
             }
         }
+        // part u, instruction j: vectors 16 u + VI j + lane / LV. piece() of
+        // those is a constant past that of vector lane / LV
         const int r0 = lane / LV, c0 = lane % LV;
-#pragma unroll
-        for (int u = 0; u < kSub; ++u) {
-            const uint64_t at = (uint64_t)row[u] * (D / 2) + r0 * (D / 2) + c0 * 16;
-#pragma unroll
-            for (int j = 0; j < 16 / VI; ++j) {
-                copy16(dk + piece<D>(16 * u + VI * j + r0, c0), kc + at + j * VI * (D / 2), 16);
-                copy16(dv + piece<D>(16 * u + VI * j + r0, c0), vc + at + j * VI * (D / 2), 16);
-            }
+        const uint32_t to = (uint32_t)piece<D>(r0, c0);
+        const uint64_t in = (uint64_t)(r0 * (D / 2) + c0 * 16);
+        const uint8_t *k0 = kc + ((uint64_t)row[0] * (D / 2) + in), *v0 = vc + ((uint64_t)row[0] * (D / 2) + in);
+        const uint8_t *k1 = kc + ((uint64_t)row[1] * (D / 2) + in), *v1 = vc + ((uint64_t)row[1] * (D / 2) + in);
+        constexpr int S = VI * (D / 2);    // bytes between an instruction's vectors and the next one's
+        copy16<0, 0>(dk + to, k0);
+        copy16<0, 0>(dv + to, v0);
+        if constexpr (VI == 8) {
+            copy16<S, S>(dk + to, k0);
+            copy16<S, S>(dv + to, v0);
+            copy16<3 * S, S>(dk + to, k1);
+            copy16<3 * S, S>(dv + to, v1);
         }
-        const uint64_t at = (uint64_t)((lane < 16 ? row[0] : row[kSub - 1]) + (lane & 15)) * SB;
-        copy_small<SB>(dks + lane * SB, kg + at, SB);
-        copy_small<SB>(dvs + lane * SB, vg + at, SB);
+        copy16<16 * (D / 2), 0>(dk + to, k1);
+        copy16<16 * (D / 2), 0>(dv + to, v1);
+        const uint64_t at = (uint64_t)((lane < 16 ? row[0] : row[1]) + (lane & 15)) * SB;
+        copy_small<SB>(dks + lane * SB, kg + at);
+        copy_small<SB>(dvs + lane * SB, vg + at);
         return;
     }
     // slot by slot: any block size; a slot outside the softmax becomes zeros
     auto vector = [&](int j) -> long long {
-        if (!attended(f.L, f.lo, f.P, s + j))
+        if (!attended(c.L, c.lo, c.P, s + j))
             return -1;
         if constexpr (PAGED) {
-            const long long r = paged_row(p.block_table + (long long)f.b * p.max_blocks, p.block_size, p.num_blocks,
-                                          p.Hkv, f.kvh, s + j);
+            const long long r = paged_row(p.block_table + (long long)c.b * p.max_blocks, p.block_size, p.num_blocks,
+                                          p.Hkv, c.kvh, s + j);
             if (r < 0)
-                seg->bad = 1;
+                *bad = 1;
             return r;
         } else {
             return (long long)f.line + s + j;
@@ -385,11 +395,11 @@ __device__ __forceinline__ void fetch_tile(const DecodeParams &p, Fetch<D, PAGED
     };
 #pragma unroll
     for (int j = 0; j < kShare / VI; ++j) {
-        const int r = VI * j + lane / LV, c = lane % LV;
+        const int r = VI * j + lane / LV, q = lane % LV;
         const long long x = vector(r);
-        const uint64_t at = x < 0 ? 0 : (uint64_t)x * (D / 2) + c * 16;
-        copy16(dk + piece<D>(r, c), kc + at, x < 0 ? 0 : 16);
-        copy16(dv + piece<D>(r, c), vc + at, x < 0 ? 0 : 16);
+        const uint64_t at = x < 0 ? 0 : (uint64_t)x * (D / 2) + q * 16;
+        copy16(dk + piece<D>(r, q), kc + at, x < 0 ? 0 : 16);
+        copy16(dv + piece<D>(r, q), vc + at, x < 0 ? 0 : 16);
     }
     const long long x = vector(lane);
     const uint64_t at = x < 0 ? 0 : (uint64_t)x * SB;
@@ -431,27 +441,36 @@ __device__ __forceinline__ void scores(const Stage<D> &st, int u, int lane, cons
     }
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
-        uint32_t a[4], b[4];
-        e2m1x8_f16(k[0][w], a);
-        e2m1x8_f16(k[1][w], b);
         // D = 128: the lane's first two words are one group, the others the next
         const __half2 ma = w >= 2 ? __high2half2(sc[0]) : __low2half2(sc[0]);
         const __half2 mb = w >= 2 ? __high2half2(sc[1]) : __low2half2(sc[1]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            a[j] = u32(__hmul2(h2(a[j]), ma));
-            b[j] = u32(__hmul2(h2(b[j]), mb));
-        }
-        mma_f16(s, a[0], b[0], a[1], b[1], qh[2 * w][0], qh[2 * w][1]);
-        mma_f16(s2, a[2], b[2], a[3], b[3], qh[2 * w + 1][0], qh[2 * w + 1][1]);
+        const uint32_t a0 = u32(__hmul2(h2(e2m1x2_f16<0>(k[0][w])), ma)), b0 = u32(__hmul2(h2(e2m1x2_f16<0>(k[1][w])), mb));
+        const uint32_t a1 = u32(__hmul2(h2(e2m1x2_f16<1>(k[0][w])), ma)), b1 = u32(__hmul2(h2(e2m1x2_f16<1>(k[1][w])), mb));
+        const uint32_t a2 = u32(__hmul2(h2(e2m1x2_f16<2>(k[0][w])), ma)), b2 = u32(__hmul2(h2(e2m1x2_f16<2>(k[1][w])), mb));
+        const uint32_t a3 = u32(__hmul2(h2(e2m1x2_f16<3>(k[0][w])), ma)), b3 = u32(__hmul2(h2(e2m1x2_f16<3>(k[1][w])), mb));
+        mma_f16(s, a0, b0, a1, b1, qh[2 * w][0], qh[2 * w][1]);
+        mma_f16(s2, a2, b2, a3, b3, qh[2 * w + 1][0], qh[2 * w + 1][1]);
         if constexpr (QF32) {
-            mma_f16(s, a[0], b[0], a[1], b[1], ql[2 * w][0], ql[2 * w][1]);
-            mma_f16(s2, a[2], b[2], a[3], b[3], ql[2 * w + 1][0], ql[2 * w + 1][1]);
+            mma_f16(s, a0, b0, a1, b1, ql[2 * w][0], ql[2 * w][1]);
+            mma_f16(s2, a2, b2, a3, b3, ql[2 * w + 1][0], ql[2 * w + 1][1]);
         }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         s[i] += s2[i];
+}
+
+// One product of the sum below: the pair of dims in byte Q of the words x, y
+// of two slots, their scales in the halves of sc, and the weights b0, b1 of
+// the two slots as (f16, remainder) pairs. The contraction runs over (slot,
+// part of the weight), so a value enters twice in a row -- the halves of a
+// register -- and is never paired with another slot's.
+template <int Q>
+__device__ __forceinline__ void weigh_pair(uint32_t x, uint32_t y, __half2 sc, uint32_t b0, uint32_t b1, float (&d)[4])
+{
+    const __half2 p = h2(e2m1x2_f16<Q>(x)), q = h2(e2m1x2_f16<Q>(y));
+    mma_f16(d, u32(__hmul2(__low2half2(p), __low2half2(sc))), u32(__hmul2(__high2half2(p), __low2half2(sc))),
+            u32(__hmul2(__low2half2(q), __high2half2(sc))), u32(__hmul2(__high2half2(q), __high2half2(sc))), b0, b1);
 }
 
 // O^T += V^T P^T over the warp's share; w[u][0..3] are the weights in the
@@ -462,75 +481,74 @@ template <int D>
 __device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float (&w)[kSub][4], float (&o)[D / 16][4])
 {
     const int g = lane >> 2, t = lane & 3;
-    uint32_t h[kSub][2], l[kSub][2];
-    __half2 sc[kSub][2];
+    uint32_t b[kSub][4];                   // rows 2t, 2t + 1, 2t + 8, 2t + 9 of the slot side: (f16, remainder)
+    __half2 sc[kSub][2];                   // their scales
     uint32_t v[kSub][4][D / 64];
 #pragma unroll
     for (int u = 0; u < kSub; ++u) {
-        split2(w[u][0], w[u][1], h[u][0], l[u][0]);
-        split2(w[u][2], w[u][3], h[u][1], l[u][1]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            h[u][i] = movmatrix_t(h[u][i]);
-            l[u][i] = movmatrix_t(l[u][i]);
+            uint32_t h, l;
+            split2(w[u][2 * i], w[u][2 * i + 1], h, l);
+            h = movmatrix_t(h);
+            l = movmatrix_t(l);
+            b[u][2 * i] = __byte_perm(h, l, 0x5410);
+            b[u][2 * i + 1] = __byte_perm(h, l, 0x7632);
         }
-        uint32_t b[4];
+        uint32_t e[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            // rows 2t, 2t + 1, 2t + 8, 2t + 9 of the slot side
             const int x = 16 * u + t + 4 * j;
             if constexpr (D == 128) {
                 const uint2 y = *reinterpret_cast<const uint2 *>(st.v + piece<D>(x, g >> 1) + 8 * (g & 1));
                 v[u][j][0] = y.x;
                 v[u][j][1] = y.y;
-                b[j] = st.vs[x * 8 + g];
+                e[j] = st.vs[x * 8 + g];
             } else {
                 v[u][j][0] = *reinterpret_cast<const uint32_t *>(st.v + piece<D>(x, g >> 2) + 4 * (g & 3));
-                b[j] = st.vs[x * 4 + (g >> 1)];
+                e[j] = st.vs[x * 4 + (g >> 1)];
             }
         }
-        sc[u][0] = h2(e4m3x2_f16(b[0] | (b[1] << 8)));
-        sc[u][1] = h2(e4m3x2_f16(b[2] | (b[3] << 8)));
+        sc[u][0] = h2(e4m3x2_f16(e[0] | (e[1] << 8)));
+        sc[u][1] = h2(e4m3x2_f16(e[2] | (e[3] << 8)));
     }
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-        uint32_t x[kSub][4][4];
+        float d[4][4] = {};
 #pragma unroll
         for (int u = 0; u < kSub; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                e2m1x8_f16(v[u][j][i], x[u][j]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-                const uint32_t a0 = u32(__hmul2(__lows2half2(h2(x[u][0][q]), h2(x[u][1][q])), sc[u][0]));
-                const uint32_t a1 = u32(__hmul2(__highs2half2(h2(x[u][0][q]), h2(x[u][1][q])), sc[u][0]));
-                const uint32_t a2 = u32(__hmul2(__lows2half2(h2(x[u][2][q]), h2(x[u][3][q])), sc[u][1]));
-                const uint32_t a3 = u32(__hmul2(__highs2half2(h2(x[u][2][q]), h2(x[u][3][q])), sc[u][1]));
-                mma_f16(d, a0, a1, a2, a3, l[u][0], l[u][1]);
-                mma_f16(d, a0, a1, a2, a3, h[u][0], h[u][1]);
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t x = v[u][2 * j][i], y = v[u][2 * j + 1][i];
+                weigh_pair<0>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[0]);
+                weigh_pair<1>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[1]);
+                weigh_pair<2>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[2]);
+                weigh_pair<3>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[3]);
             }
 #pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
             for (int j = 0; j < 4; ++j)
-                o[4 * i + q][j] += d[j];
-        }
+                o[4 * i + q][j] += d[q][j];
     }
 }
+
+// Scratch of the merge (segment_out, unit_ticket_merge): as many partials at a
+// time as the spare slot has room for.
+template <int D>
+using Merge = MergeBufT<kRows, D == 128 ? 28 : 12>;
 
 template <int D, bool QF32, bool PAGED>
 __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const DecodeParams p)
 {
     extern __shared__ __align__(128) unsigned char dyn[];
-    Stage<D>(*ring)[kStages] = reinterpret_cast<Stage<D>(*)[kStages]>(dyn);    // [kWarps]
+    Stage<D>(*ring)[kWarps] = reinterpret_cast<Stage<D>(*)[kWarps]>(dyn);      // [kStages]
     __shared__ long long sched[kThreads / 32 + 8];
     __shared__ TileWalk walk;
-    __shared__ Segment segs[kWarps][kSegs];
+    __shared__ Segment segs[kSegs];            // every warp writes the same
+    __shared__ int sm_bad[kWarps][kSegs];      // a block that the segment needs is not usable
     __shared__ int sm_flag;
-    __shared__ MergeBuf sm_merge;
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
-    __shared__ __align__(16) float sm_o[kWarps][kRows][D];
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane >> 2, t4 = lane & 3;
@@ -551,28 +569,28 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
         left = walk_first(p, c, walk, in_b);
         if (!left)
             return;
-        enter(p, c, f, &segs[warp][0], shift, pages, warp, lane);
+        enter(p, c, f, &segs[0], &sm_bad[warp][0], shift, pages, warp, lane);
         __syncwarp();
     }
     auto fetch = [&](int slot) {
         if (left) {
-            fetch_tile(p, f, ring[warp][slot], &segs[warp][sf], shift, pages, warp, lane);
+            fetch_tile(p, f, segs[sf].c, ring[slot][warp], &sm_bad[warp][sf], shift, pages, warp, lane);
             if (f.t < f.t_last) {
                 ++f.t;
                 if constexpr (PAGED) {
                     if ((f.t & 15) == 0 && f.good && pages) {
                         f.page = f.page_next;
-                        f.page_next = load_page(p, f, shift, f.t + 16, warp, lane);
+                        f.page_next = load_page(p, f, segs[sf].c, shift, f.t + 16, warp, lane);
                     }
                 }
             } else {
-                TileCursor c = segs[warp][sf].c;
+                TileCursor c = segs[sf].c;
                 c.g += f.t - c.t;
                 c.t = f.t;
                 left = walk_next(p, c, walk, in_b);
                 if (left) {
                     sf = (sf + 1) % kSegs;
-                    enter(p, c, f, &segs[warp][sf], shift, pages, warp, lane);
+                    enter(p, c, f, &segs[sf], &sm_bad[warp][sf], shift, pages, warp, lane);
                     __syncwarp();
                 }
             }
@@ -590,15 +608,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
     float o[D / 16][4];
     for (int sc = 0;; sc = (sc + 1) % kSegs) {
         // the next segment
-        const Segment *seg = &segs[warp][sc];
-        const int b = seg->c.b, kvh = seg->c.kvh, L = seg->c.L, lo = seg->c.lo, P = seg->c.P;
-        const int tp = seg->c.tp, gap = seg->c.gap, first_t = seg->c.t, t_last = seg->t_last;
+        const Segment *seg = &segs[sc];
         const bool good = seg->good;
-        if (!good && tid == 0 && first_t == 0 && kvh == 0)
-            report(p, row_error_bits(p, b, L));
+        if (!good && tid == 0 && seg->c.t == 0 && seg->c.kvh == 0)
+            report(p, row_error_bits(p, seg->c.b, seg->c.L));
         float mul;
-        load_query<D, QF32>(p, b, kvh, lane, qh, ql, mul);
-        const float ks = __ldg(p.k_scale + scale_head(p, b, kvh));
+        load_query<D, QF32>(p, seg->c.b, seg->c.kvh, lane, qh, ql, mul);
+        const float ks = __ldg(p.k_scale + scale_head(p, seg->c.b, seg->c.kvh));
         mul0 = __shfl_sync(0xffffffffu, mul, 8 * t4) * ks;
         mul1 = __shfl_sync(0xffffffffu, mul, 8 * t4 + 4) * ks;
         m0 = m1 = -INFINITY;
@@ -609,11 +625,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
             for (int j = 0; j < 4; ++j)
                 o[i][j] = 0.f;
 
-        for (int t = first_t; t <= t_last; ++t) {
+        for (int t = seg->c.t; t <= seg->t_last; ++t) {
             copy_wait<kStages - 2>();      // this lane's copies of the tile, then the other lanes'
             __syncwarp();
             fetch(slot == 0 ? kStages - 1 : slot - 1);
-            const Stage<D> &st = ring[warp][slot];
+            const Stage<D> &st = ring[slot][warp];
             slot = slot + 1 == kStages ? 0 : slot + 1;
             float s[kSub][4];
 #pragma unroll
@@ -621,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
                 scores<D, QF32>(st, u, lane, qh, ql, s[u]);
             // bits 2 u + i: slot 16 u + slot_of(g) + 8 i is in the softmax
             unsigned ok = good ? ~0u : 0u;
-            const int s0 = share_slot(t, tp, gap, warp);
+            const int s0 = share_slot(t, seg->c.tp, seg->c.gap, warp), L = seg->c.L, lo = seg->c.lo, P = seg->c.P;
             if (s0 + kShare - 1 > L || (s0 < lo && s0 + kShare - 1 >= P)) {
 #pragma unroll
                 for (int u = 0; u < kSub; ++u)
@@ -703,7 +719,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
             sm_l[warp][2 * t4] = l0;
             sm_l[warp][2 * t4 + 1] = l1;
         }
-        const float vs = __ldg(p.v_scale + scale_head(p, b, kvh));
+        // the ring's slot of the last tile is free until the next segment's
+        // first fetch: the warps' outputs and the merge's scratch go there
+        Stage<D> *spare = ring[slot == 0 ? kStages - 1 : slot - 1];
+        auto &sm_o = *reinterpret_cast<float(*)[kWarps][kRows][D]>(spare);
+        auto &sm_merge = *reinterpret_cast<Merge<D> *>(reinterpret_cast<unsigned char *>(spare) + sizeof sm_o);
+        static_assert(sizeof sm_o + sizeof(Merge<D>) <= kWarps * sizeof(Stage<D>), "the slot holds both");
+        __syncthreads();                   // every warp has read its part of the slot
+        const float vs = __ldg(p.v_scale + scale_head(p, seg->c.b, seg->c.kvh));
 #pragma unroll
         for (int i = 0; i < D / 16; i += 2) {
             // rows 2t4, 2t4 + 1: dims D / 8 * g + 2 i .. + 3
@@ -714,9 +737,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
         }
         __syncwarp();
         TileCursor cur = seg->c;
-        cur.g += t_last - cur.t;
-        cur.t = t_last;
-        const bool any_bad = __syncthreads_or(seg->bad) != 0;
+        const int first_t = cur.t;
+        cur.g += seg->t_last - cur.t;
+        cur.t = seg->t_last;
+        const bool any_bad = __syncthreads_or(sm_bad[warp][sc]) != 0;
         if (any_bad && good && tid == 0)
             report(p, kBadBlock);
         const bool end = !left && sc == sf;
