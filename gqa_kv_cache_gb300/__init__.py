@@ -81,7 +81,7 @@ def _check(code: int, what: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _opts(kernel, grid_ctas, sched_pad=None, sink=None, window=0, kept_prefix=0, device=None, B=None,
@@ -93,13 +93,19 @@ def _opts(kernel, grid_ctas, sched_pad=None, sink=None, window=0, kept_prefix=0,
     tensor-core consumers' wait for a tile to that many SM clock cycles and
     ``test_stall`` makes each consumer's first wait one that runs out (both
     for tests of the timeout path)."""
-    o = _lib.GqaOptions()
-    o.wait_limit_cycles = int(wait_limit_cycles or 0)
-    o.test_stall = 1 if test_stall else 0
-    o.kernel = KERNELS[kernel] if isinstance(kernel, str) else int(kernel)
-    o.grid_ctas = int(grid_ctas)
-    o.sched_pad = 0 if sched_pad is None else int(sched_pad) + 1   # 0 = library default
-    o.window = int(window or 0)
+    o = _lib.GqaOptions()   # zeros: the defaults (a field is set only where it differs: setting costs time)
+    if wait_limit_cycles:
+        o.wait_limit_cycles = int(wait_limit_cycles)
+    if test_stall:
+        o.test_stall = 1
+    if kernel != "auto":
+        o.kernel = KERNELS[kernel] if isinstance(kernel, str) else int(kernel)
+    if grid_ctas:
+        o.grid_ctas = int(grid_ctas)
+    if sched_pad is not None:
+        o.sched_pad = int(sched_pad) + 1   # 0 = library default
+    if window:
+        o.window = int(window)
     if sink is not None:
         if sink.dtype != torch.float32 or sink.shape != (Hq,) or not sink.is_contiguous() \
                 or sink.device != device:
@@ -110,8 +116,8 @@ def _opts(kernel, grid_ctas, sched_pad=None, sink=None, window=0, kept_prefix=0,
                 or not kept_prefix.is_contiguous() or kept_prefix.device != device:
             raise TypeError("kept_prefix must be an int or a contiguous int32 (B,) tensor on q's device")
         o.kept_prefix_rows = kept_prefix.data_ptr()
-    else:
-        o.kept_prefix = int(kept_prefix or 0)
+    elif kept_prefix:
+        o.kept_prefix = int(kept_prefix)
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
         if t is None:
             continue
@@ -124,10 +130,15 @@ def _opts(kernel, grid_ctas, sched_pad=None, sink=None, window=0, kept_prefix=0,
     return o
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # current_stream without its Python object
+
+
 def _stream(stream, device=None):
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device() if device is None else device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 _ws_cache: dict = {}
@@ -139,14 +150,16 @@ def _workspace(device, nbytes, stream=None):
     on one stream run one after the other; each stream has its own, and so has
     every call that is captured into a graph (the graph fills it with zeros
     and may then be replayed beside any other work)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):   # zero-filled before the stream's next kernel
+            return _workspace(device, nbytes)
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(max(nbytes, 1), dtype=torch.uint8, device=device)
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    key = (device, s.cuda_stream) if s.cuda_stream else device
+    handle = _stream(None, device)
+    key = (device, handle) if handle else device
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
-        with torch.cuda.stream(s):   # zero-filled before the stream's next kernel
-            buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
         _ws_cache[key] = buf
     return buf
 
@@ -176,19 +189,31 @@ def _group_scales(caches, k_group_scale, v_group_scale, D):
             raise TypeError(f"{name} with group scales must hold E2M1 pairs (uint8 or float4_e2m1fn_x2)")
         if t is None or t.dtype not in _BYTE_DTYPES:
             raise TypeError("k_group_scale and v_group_scale must both be E4M3 bytes (uint8 or float8_e4m3fn)")
-        if D % _GROUP or c.shape[-1] * 2 != D or t.shape != (*c.shape[:-1], D // _GROUP):
+        a, b, n, d = c.shape
+        if D % _GROUP or d * 2 != D or t.shape != (a, b, n, D // _GROUP):
             raise ValueError(f"{name} must hold D // 2 bytes and {gname} D // {_GROUP} scales a vector, D = {D}")
-        if t.device != c.device or not t.is_contiguous():
+        if t.get_device() != c.get_device() or not t.is_contiguous():
             raise ValueError(f"{gname} must be contiguous and on the cache's device")
+
+
+def _row_checks(lengths, slot_ids, block_table, B, dev):
+    """Checks of the per-row tensors of a call over an E2M1 cache."""
+    if lengths.shape != (B,):
+        raise ValueError("lengths must be of shape (B,)")
+    for name, t in (("slot_ids", slot_ids), ("block_table", block_table)):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous and on q's device")
 
 
 def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False, groups=None):
     """Checks shared by the entry points; returns (cache gqa_dtype, out). The
     query and the new keys / values share the cache dtype, except over an E4M3
     cache (bfloat16 then; the attend's query is free)."""
-    if not q.is_cuda:
+    dev = q.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if q.dtype not in _DTYPES:
+    qt = q.dtype
+    if qt not in _DTYPES:
         raise TypeError("q must be float32 or bfloat16")
     if groups is not None and (groups[0] is not None or groups[1] is not None):
         _group_scales(caches, *groups, q.shape[-1])
@@ -196,11 +221,11 @@ def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False, gro
     else:
         code = _cache_code(caches[0][1])
     if code >= E4M3:
-        if not q_any_dtype and q.dtype != torch.bfloat16:
+        if not q_any_dtype and qt != torch.bfloat16:
             raise TypeError("over an E4M3 or E2M1 cache q, k_new and v_new are bfloat16")
         new_dt = torch.bfloat16
     else:
-        dt = caches[0][1].dtype if q_any_dtype else q.dtype
+        dt = caches[0][1].dtype if q_any_dtype else qt
         if dt not in _DTYPES:
             raise TypeError("the cache must be float32 or bfloat16")
         new_dt = dt
@@ -212,18 +237,18 @@ def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False, gro
         if t.dtype != caches[0][1].dtype:
             raise TypeError(f"{name} must have dtype {caches[0][1].dtype}")
     for name, t in (*news, *caches):
-        if t.device != q.device:
+        if t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, q on {q.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
-    if lengths.dtype != torch.int32 or not lengths.is_contiguous() or lengths.device != q.device:
+    if lengths.dtype != torch.int32 or not lengths.is_contiguous() or lengths.get_device() != dev:
         raise TypeError("lengths must be a contiguous int32 tensor on q's device")
-    B, Hq, D = q.shape
+    shape = q.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
-    elif out.shape != (B, Hq, D) or out.dtype != torch.float32 or not out.is_contiguous():
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+    elif out.shape != shape or out.dtype != torch.float32 or not out.is_contiguous():
         raise ValueError("out must be a contiguous float32 (B, Hq, D) tensor")
     return code, out
 
@@ -242,10 +267,13 @@ def decode_step(q, k_new, v_new, k_cache, v_cache, lengths, slot_ids=None, *, ou
                              lengths, out, groups=(k_group_scale, v_group_scale))
     B, Hq, D = q.shape
     R, Hkv, Smax, D2 = k_cache.shape
-    if (D2 * 2 if dt == E2M1 else D2) != D or v_cache.shape != k_cache.shape or k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D):
+    if (D2 * 2 if dt == E2M1 else D2) != D or v_cache.shape != k_cache.shape or k_new.shape != (B, Hkv, D) \
+            or v_new.shape != (B, Hkv, D):
         raise ValueError("shape mismatch between q, k_new, v_new and the caches")
     if slot_ids is not None and (slot_ids.dtype != torch.int32 or slot_ids.shape != (B,)):
         raise TypeError("slot_ids must be int32 of shape (B,)")
+    if dt == E2M1:
+        _row_checks(lengths, slot_ids, None, B, q.get_device())
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
@@ -270,12 +298,15 @@ def decode_step_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths,
                              lengths, out, groups=(k_group_scale, v_group_scale))
     B, Hq, D = q.shape
     NB, Hkv, BS, D2 = k_blocks.shape
-    if (D2 * 2 if dt == E2M1 else D2) != D or v_blocks.shape != k_blocks.shape or k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D):
+    if (D2 * 2 if dt == E2M1 else D2) != D or v_blocks.shape != k_blocks.shape or k_new.shape != (B, Hkv, D) \
+            or v_new.shape != (B, Hkv, D):
         raise ValueError("shape mismatch between q, k_new, v_new and the blocks")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
             or not block_table.is_contiguous():
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor")
     MB = block_table.shape[1]
+    if dt == E2M1:
+        _row_checks(lengths, None, block_table, B, q.get_device())
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
@@ -306,6 +337,8 @@ def attend(q, k_cache, v_cache, lengths, slot_ids=None, *, out=None, status=None
         raise ValueError("shape mismatch between q and the caches")
     if slot_ids is not None and (slot_ids.dtype != torch.int32 or slot_ids.shape != (B,)):
         raise TypeError("slot_ids must be int32 of shape (B,)")
+    if dt == E2M1:
+        _row_checks(lengths, slot_ids, None, B, q.get_device())
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
@@ -335,6 +368,8 @@ def attend_paged(q, k_blocks, v_blocks, block_table, lengths, *, out=None, statu
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
             or not block_table.is_contiguous():
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor")
+    if dt == E2M1:
+        _row_checks(lengths, None, block_table, B, q.get_device())
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
@@ -423,9 +458,10 @@ def decode_multi_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths
 def _rows_checks(caches, lengths, cu_q, slot_ids, block_table, groups, D):
     """Checks shared by append and read; returns the cache's gqa_dtype."""
     (_, k), (_, v) = caches
-    if not k.is_cuda:
+    dev = k.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device or k.dim() != 4:
+    if v.shape != k.shape or v.dtype != k.dtype or v.get_device() != dev or k.dim() != 4:
         raise ValueError("the two caches must be 4-dimensional and alike")
     if not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("the caches must be contiguous")
@@ -439,11 +475,11 @@ def _rows_checks(caches, lengths, cu_q, slot_ids, block_table, groups, D):
     B = lengths.shape[0]
     for name, t, shape in (("lengths", lengths, (B,)), ("cu_q", cu_q, (B + 1,)), ("slot_ids", slot_ids, (B,))):
         if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()
-                              or t.device != k.device):
+                              or t.get_device() != dev):
             raise TypeError(f"{name} must be a contiguous int32 {shape} tensor on the caches' device")
     if block_table is not None and (block_table.dtype != torch.int32 or block_table.dim() != 2
                                     or block_table.shape[0] != B or not block_table.is_contiguous()
-                                    or block_table.device != k.device):
+                                    or block_table.get_device() != dev):
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor on the caches' device")
     return code
 
@@ -467,10 +503,11 @@ def _append(k_new, v_new, k, v, block_table, lengths, cu_q, slot_ids, scales, gr
         raise ValueError("k_new and v_new must both be (T, Hkv, D)")
     T, Hkv, D = k_new.shape
     code = _rows_checks(((names[0], k), (names[1], v)), lengths, cu_q, slot_ids, block_table, groups, D)
+    dev = k.get_device()
     if k_new.dtype not in _DTYPES or v_new.dtype != k_new.dtype:
         raise TypeError("k_new and v_new must both be float32 or bfloat16")
     for t in (k_new, v_new):
-        if t.device != k.device or not t.is_contiguous():
+        if t.get_device() != dev or not t.is_contiguous():
             raise ValueError("k_new and v_new must be contiguous and on the caches' device")
     if k.shape[1] != Hkv:
         raise ValueError("shape mismatch between k_new and the caches")
@@ -486,7 +523,7 @@ def _append(k_new, v_new, k, v, block_table, lengths, cu_q, slot_ids, scales, gr
             block = n2 // k_bounds.shape[2]
             shape = (n0, Hkv, k_bounds.shape[2], 2, D)
         if k_bounds.dtype != torch.bfloat16 or k_bounds.shape != shape or not k_bounds.is_contiguous() \
-                or k_bounds.device != k.device:
+                or k_bounds.get_device() != dev:
             raise TypeError(f"k_bounds must be a contiguous bfloat16 {shape} tensor on the caches' device")
     o = _rows_opts(code, Hkv, k.device, *scales, groups)
     lib = _lib.load()
@@ -531,13 +568,14 @@ def _read(k, v, block_table, lengths, cu_q, T, slot_ids, dtype, k_out, v_out, sc
     D = k.shape[-1] * (2 if groups[0] is not None or groups[1] is not None else 1)
     code = _rows_checks(((names[0], k), (names[1], v)), lengths, cu_q, slot_ids, block_table, groups, D)
     _status_checks(status, k.device)
+    dev = k.get_device()
     n0, Hkv, n2, _ = k.shape
     T, shape = int(T), (int(T), Hkv, D)
     with torch.cuda.stream(stream) if stream is not None else _HERE:
         k_out = torch.empty(shape, dtype=dtype, device=k.device) if k_out is None else k_out
         v_out = torch.empty(shape, dtype=dtype, device=k.device) if v_out is None else v_out
     for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t.shape != shape or t.dtype != dtype or t.device != k.device or not t.is_contiguous():
+        if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor on the caches' device")
     o = _rows_opts(code, Hkv, k.device, *scales, groups)
     lib = _lib.load()
@@ -598,12 +636,13 @@ class Selection:
 
     def _ptrs(self):
         at = self._buf.data_ptr()
-        return ctypes.c_void_p(at), ctypes.c_void_p(at + 4 * self._n), ctypes.c_void_p(at + 8 * self._n)
+        return at, at + 4 * self._n, at + 8 * self._n
 
 
 def _select(q, k_bounds, block_table, lengths, n_select, slot_ids, block_size, n_first, n_last, selection, status,
             stream):
-    if not q.is_cuda:
+    dev = q.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
     if q.dtype not in _DTYPES or q.dim() != 3:
         raise TypeError("q must be a float32 or bfloat16 (B, Hq, D) tensor")
@@ -617,21 +656,21 @@ def _select(q, k_bounds, block_table, lengths, n_select, slot_ids, block_size, n
     if Hq % Hkv:
         raise ValueError("Hq must be a multiple of Hkv")
     for name, t in (("q", q), ("k_bounds", k_bounds)):
-        if t.device != q.device or not t.is_contiguous():
+        if t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous and on q's device")
     for name, t, shape in (("lengths", lengths, (B,)), ("slot_ids", slot_ids, (B,))):
         if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()
-                              or t.device != q.device):
+                              or t.get_device() != dev):
             raise TypeError(f"{name} must be a contiguous int32 {shape} tensor on q's device")
     if block_table is not None and (block_table.dtype != torch.int32 or block_table.dim() != 2
                                     or block_table.shape[0] != B or not block_table.is_contiguous()
-                                    or block_table.device != q.device):
+                                    or block_table.get_device() != dev):
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor on q's device")
     _status_checks(status, q.device)
     n_select = int(n_select)
     if selection is None:
-        if n_select < 1:
-            raise ValueError("n_select must be positive")
+        if n_select < 1 or block_size < 1:
+            raise ValueError("n_select and block_size must be positive")
         with torch.cuda.stream(stream) if stream is not None else _HERE:
             selection = Selection(B, Hkv, n_select, int(block_size), q.device)
     elif (selection.B, selection.Hkv, selection.n_select, selection.block_size) != (B, Hkv, n_select, int(block_size)) \

@@ -62,6 +62,8 @@ def load() -> ctypes.CDLL:
     """The loaded library. Raises if it has not been built: there is no
     fallback implementation."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

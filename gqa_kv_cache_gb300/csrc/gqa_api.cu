@@ -282,11 +282,11 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
     if ((kv8 || kv4) && (!opt || !opt->k_scale || !opt->v_scale || (reinterpret_cast<uintptr_t>(opt->k_scale) & 3u) ||
                 (reinterpret_cast<uintptr_t>(opt->v_scale) & 3u)))
         return GQA_ERR_INVALID_ARGUMENT;
+    if (s.B == 0 || (s.multi && (s.T == 0 || s.max_q == 0)))
+        return GQA_OK;
     if (kv4 && (!opt->k_group_scale || !opt->v_group_scale || !aligned16(opt->k_group_scale) ||
                 !aligned16(opt->v_group_scale)))
         return GQA_ERR_INVALID_ARGUMENT;
-    if (s.B == 0 || (s.multi && (s.T == 0 || s.max_q == 0)))
-        return GQA_OK;
     if (!q || !kc || !vc || !lengths || !out || (s.paged && !block_table))
         return GQA_ERR_INVALID_ARGUMENT;
     if (!s.attend && (!k_new || !v_new))
@@ -614,7 +614,7 @@ gqa_status gqa_decode_multi(const void *q, const void *k_new, const void *v_new,
                             size_t workspace_bytes, int32_t *d_status, void *stream,
                             const gqa_options *opt)
 {
-    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 ? GQA_DTYPE_BF16 : dt;   // query and new tokens
+    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 || dt == GQA_DTYPE_E2M1 ? GQA_DTYPE_BF16 : dt;   // query and new tokens
     Shape s = {B, Hq, Hkv, D, dt, false, R, Smax, 0, 0, 0, false, qdt, true, T, max_q_len};
     return run_step(s, q, k_new, v_new, k_cache, v_cache, lengths, slot_ids, nullptr, out, workspace,
                     workspace_bytes, d_status, stream, opt, cu_q);
@@ -628,7 +628,7 @@ gqa_status gqa_decode_multi_paged(const void *q, const void *k_new, const void *
                                   size_t workspace_bytes, int32_t *d_status, void *stream,
                                   const gqa_options *opt)
 {
-    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 ? GQA_DTYPE_BF16 : dt;
+    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 || dt == GQA_DTYPE_E2M1 ? GQA_DTYPE_BF16 : dt;
     Shape s = {B, Hq, Hkv, D, dt, true, 0, 0, num_blocks, block_size, max_blocks, false, qdt, true, T,
                max_q_len};
     return run_step(s, q, k_new, v_new, k_blocks, v_blocks, lengths, nullptr, block_table, out,

@@ -57,6 +57,8 @@ gqa_status run_rows(RowsParams p, gqa_dtype vec, gqa_dtype kv, bool write, void 
         p.k_scale = opt->k_scale;
         p.v_scale = opt->v_scale;
     }
+    if (p.B == 0 || p.T == 0)
+        return GQA_OK;
     if (kv == GQA_DTYPE_E2M1) {
         if (!opt->k_group_scale || !opt->v_group_scale || !aligned(opt->k_group_scale, 16) ||
             !aligned(opt->v_group_scale, 16))
@@ -64,8 +66,6 @@ gqa_status run_rows(RowsParams p, gqa_dtype vec, gqa_dtype kv, bool write, void 
         p.k_group = opt->k_group_scale;
         p.v_group = opt->v_group_scale;
     }
-    if (p.B == 0 || p.T == 0)
-        return GQA_OK;
     const void *a = write ? p.k_new : p.k_out, *b = write ? p.v_new : p.v_out;
     if (!a || !b || !p.k_cache || !p.v_cache || !p.lengths || !p.cu_q || (p.paged && !p.block_table) ||
         (!p.paged && !p.slot_ids && p.R < p.B))
