@@ -96,4 +96,33 @@ __device__ __forceinline__ uint32_t group_scale(float amax, float g, float &t)
 // x / t in float32, 0 where t is 0 or NaN.
 __device__ __forceinline__ float over_t(float x, float t) { return t > 0.f ? __fdiv_rn(x, t) : 0.f; }
 
+// The codes of a group x with scale byte s and t, eight a word. The quotients
+// x / t come from one correctly rounded reciprocal r: a product, its exact
+// remainder and one correction (P. Markstein, IBM J. Res. Dev. 34, 1990),
+// which rounds as the division does where nothing leaves float32's range. A t
+// near its ends is first brought towards 1 with its x, by a power of two, and
+// x that the largest scale cannot reach is clamped; both are rare. x is changed.
+__device__ __forceinline__ uint2 e2m1_codes16(float (&x)[16], uint32_t s, float t)
+{
+    if (s == 0x7eu || !(t > 0x1p-90f && t < 0x1p90f)) {
+        const bool none = !(t > 0.f);      // a zero or NaN scale: codes 0
+        const float f = t <= 0x1p-90f ? 0x1p100f : t >= 0x1p90f ? 0x1p-60f : 1.f;
+        t = none ? 1.f : t * f;
+        const float top = 8.f * t;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            x[i] = none ? 0.f : fminf(fmaxf(x[i] * f, -top), top);
+    }
+    const float r = __frcp_rn(t);
+    uint32_t u[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float p = __fmul_rn(x[2 * i], r), q = __fmul_rn(x[2 * i + 1], r);
+        u[i >> 2] |= to_e2m1x2(__fmaf_rn(__fmaf_rn(-p, t, x[2 * i]), r, p),
+                               __fmaf_rn(__fmaf_rn(-q, t, x[2 * i + 1]), r, q))
+                     << (8 * (i & 3));
+    }
+    return make_uint2(u[0], u[1]);
+}
+
 }  // namespace gqa

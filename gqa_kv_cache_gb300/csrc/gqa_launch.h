@@ -61,6 +61,7 @@ struct RowsParams {
     int B, T, Hkv, D, R, Smax, paged, num_blocks, block_size, max_blocks;
     int bounds_block;                // slots a block of the bounds (paged: block_size)
     int chunk;                       // tokens a CTA (set by rows_launch)
+    int wide;                        // vectors and caches lie on 32-byte boundaries (likewise)
 };
 __device__ __forceinline__ void rows_report(const RowsParams &p, int bits)
 {

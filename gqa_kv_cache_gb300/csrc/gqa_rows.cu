@@ -81,52 +81,103 @@ __device__ inline Token find_token(const RowsParams &p, int t)
     return k;
 }
 
-// Sixteen elements at src (element type T) widened to float32.
+// Sixteen elements of type T as loaded. 32 bytes at a time where the vectors
+// lie on 32-byte boundaries (WIDE; half as many requests, and a store fills
+// whole sectors: reading back 131071 tokens of 8 x 128 to bfloat16 took 133 us
+// with 16-byte stores), else 16.
 template <typename T>
-__device__ __forceinline__ void load16(const T *src, float (&x)[16])
+struct Raw {
+    uint32_t u[4 * sizeof(T)];
+};
+
+__device__ __forceinline__ void ld32(const void *src, uint32_t *u)
 {
-    constexpr int V = sizeof(T) == 4 ? 4 : 2;   // 16-byte loads
-    uint4 w[V];
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+        : "l"(src));
+}
+__device__ __forceinline__ void st32(void *dst, const uint32_t *u)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                 "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T *src, bool wide)
+{
+    Raw<T> w;
+    constexpr int N = 4 * sizeof(T);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        w[i] = __ldg(reinterpret_cast<const uint4 *>(src) + i);
-    const uint32_t *u = reinterpret_cast<const uint32_t *>(w);
+    for (int i = 0; i < N; i += 8) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(src) + i / 4;
+        if (wide) {
+            ld32(p, w.u + i);
+        } else {
+            const uint4 a = __ldg(p), b = __ldg(p + 1);
+            w.u[i] = a.x; w.u[i + 1] = a.y; w.u[i + 2] = a.z; w.u[i + 3] = a.w;
+            w.u[i + 4] = b.x; w.u[i + 5] = b.y; w.u[i + 6] = b.z; w.u[i + 7] = b.w;
+        }
+    }
+    return w;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_raw(T *dst, const Raw<T> &w, bool wide)
+{
+    constexpr int N = 4 * sizeof(T);
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        uint4 *p = reinterpret_cast<uint4 *>(dst) + i / 4;
+        if (wide) {
+            st32(p, w.u + i);
+        } else {
+            p[0] = make_uint4(w.u[i], w.u[i + 1], w.u[i + 2], w.u[i + 3]);
+            p[1] = make_uint4(w.u[i + 4], w.u[i + 5], w.u[i + 6], w.u[i + 7]);
+        }
+    }
+}
+
+// Widened to float32, and rounded from it.
+template <typename T>
+__device__ __forceinline__ void widen16(const Raw<T> &w, float (&x)[16])
+{
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         if constexpr (sizeof(T) == 4)
-            x[i] = __uint_as_float(u[i]);
+            x[i] = __uint_as_float(w.u[i]);
         else
-            x[i] = (i & 1) ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
+            x[i] = (i & 1) ? bf16_hi(w.u[i / 2]) : bf16_lo(w.u[i / 2]);
     }
 }
-
 template <typename T>
-__device__ __forceinline__ void store16(T *dst, const float (&x)[16])
+__device__ __forceinline__ Raw<T> round16(const float (&x)[16])
 {
+    Raw<T> w;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            reinterpret_cast<float4 *>(dst)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        for (int i = 0; i < 16; ++i)
+            w.u[i] = __float_as_uint(x[i]);
     } else {
-        uint32_t u[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t *>(&v);
+            w.u[i] = *reinterpret_cast<const uint32_t *>(&v);
         }
-        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
     }
+    return w;
 }
 
 // One group of 16 elements into the cache at element offset `off`.
-template <int KIND>
-__device__ __forceinline__ void put16(void *cache, void *groups, long long off, float g, const float (&x)[16])
+template <int KIND, typename T>
+__device__ __forceinline__ void put16(void *cache, void *groups, long long off, float g, const Raw<T> &w, bool wide)
 {
+    float x[16];
+    widen16(w, x);
     if constexpr (KIND == GQA_DTYPE_F32) {
-        store16(static_cast<float *>(cache) + off, x);
+        store_raw(static_cast<float *>(cache) + off, round16<float>(x), wide);
     } else if constexpr (KIND == GQA_DTYPE_BF16) {
-        store16(static_cast<__nv_bfloat16 *>(cache) + off, x);
+        store_raw(static_cast<__nv_bfloat16 *>(cache) + off, round16<__nv_bfloat16>(x), wide);
     } else if constexpr (KIND == GQA_DTYPE_E4M3) {
         uint32_t u[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -145,23 +196,20 @@ __device__ __forceinline__ void put16(void *cache, void *groups, long long off, 
             amax = max_nan(amax, fabsf(x[i]));
         float t;
         const uint32_t s = group_scale(amax, g, t);
-        uint32_t u[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            u[i >> 2] |= to_e2m1x2(over_t(x[2 * i], t), over_t(x[2 * i + 1], t)) << (8 * (i & 3));
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + (off >> 1)) = make_uint2(u[0], u[1]);
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + (off >> 1)) = e2m1_codes16(x, s, t);
         static_cast<uint8_t *>(groups)[off >> 4] = (uint8_t)s;
     }
 }
 
 // The group at element offset `off` of the cache.
 template <int KIND>
-__device__ __forceinline__ void get16(const void *cache, const void *groups, long long off, float g, float (&x)[16])
+__device__ __forceinline__ void get16(const void *cache, const void *groups, long long off, float g, float (&x)[16],
+                                      bool wide)
 {
     if constexpr (KIND == GQA_DTYPE_F32) {
-        load16(static_cast<const float *>(cache) + off, x);
+        widen16(load_raw(static_cast<const float *>(cache) + off, wide), x);
     } else if constexpr (KIND == GQA_DTYPE_BF16) {
-        load16(static_cast<const __nv_bfloat16 *>(cache) + off, x);
+        widen16(load_raw(static_cast<const __nv_bfloat16 *>(cache) + off, wide), x);
     } else if constexpr (KIND == GQA_DTYPE_E4M3) {
         const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(cache) + off));
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -190,7 +238,7 @@ __device__ __forceinline__ void get16(const void *cache, const void *groups, lon
     }
 }
 
-// min (lo) or max of bfloat16 pairs; NaN where either is.
+// min or max of bfloat16 pairs; NaN where either is.
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b)
 {
     uint32_t r;
@@ -204,133 +252,164 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
-// Eight keys at src as bfloat16 pairs: a float32 key's lower bound is rounded
-// down and its upper bound up, so that the bounds hold (bfloat16 keys: exact).
+// Bounds of sixteen keys' elements as bfloat16 pairs.
+struct Bounds {
+    uint32_t lo[8], hi[8];
+};
+
+// Widens the bounds of the run by one key (its first: replaces them). A
+// float32 key's lower bound is rounded down and its upper bound up, so that the
+// bounds hold (bfloat16 keys: exact).
 template <typename T>
-__device__ __forceinline__ void load_bounds8(const T *src, uint32_t (&lo)[4], uint32_t (&hi)[4])
+__device__ __forceinline__ void take(Bounds &r, const Raw<T> &w, bool first)
 {
-    if constexpr (sizeof(T) == 2) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src));
-        lo[0] = hi[0] = w.x;
-        lo[1] = hi[1] = w.y;
-        lo[2] = hi[2] = w.z;
-        lo[3] = hi[3] = w.w;
-    } else {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(src));
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(src) + 1);
-        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat16 l0 = __float2bfloat16_rd(x[2 * i]), l1 = __float2bfloat16_rd(x[2 * i + 1]);
-            const __nv_bfloat16 h0 = __float2bfloat16_ru(x[2 * i]), h1 = __float2bfloat16_ru(x[2 * i + 1]);
-            lo[i] = (uint32_t)__bfloat16_as_ushort(l0) | ((uint32_t)__bfloat16_as_ushort(l1) << 16);
-            hi[i] = (uint32_t)__bfloat16_as_ushort(h0) | ((uint32_t)__bfloat16_as_ushort(h1) << 16);
+    for (int i = 0; i < 8; ++i) {
+        uint32_t lo, hi;
+        if constexpr (sizeof(T) == 2) {
+            lo = hi = w.u[i];
+        } else {
+            const float x = __uint_as_float(w.u[2 * i]), y = __uint_as_float(w.u[2 * i + 1]);
+            lo = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rd(x)) |
+                 ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rd(y)) << 16);
+            hi = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_ru(x)) |
+                 ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_ru(y)) << 16);
         }
+        r.lo[i] = first ? lo : min_bf16x2(r.lo[i], lo);
+        r.hi[i] = first ? hi : max_bf16x2(r.hi[i], hi);
     }
 }
 
-// One CTA: `chunk` tokens and, with bounds, the rest of the last run that
-// begins among them. Shared memory: the tokens' slots.
-template <typename T, int KIND>
-__global__ void __launch_bounds__(kThreads) append_kernel(const RowsParams p)
+__device__ __forceinline__ void widen(Bounds &a, const Bounds &b)
 {
-    extern __shared__ Token tok[];     // [chunk + run - 1]
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        a.lo[i] = min_bf16x2(a.lo[i], b.lo[i]);
+        a.hi[i] = max_bf16x2(a.hi[i], b.hi[i]);
+    }
+}
+
+// The threads of a CTA over (group, token): group c of the Hkv * D / 16 groups
+// of a token's vectors, every `lanes`-th token. A token's groups are
+// neighbouring threads (and addresses).
+struct Share {
+    int per;       // groups of a token
+    int lanes;     // tokens at once
+    int c, lane;   // this thread's first group and token (lane >= lanes: none)
+    __device__ __forceinline__ Share(const RowsParams &p)
+    {
+        per = p.Hkv * (p.D / kGroup);
+        lanes = per >= kThreads ? 1 : kThreads / per;
+        c = per >= kThreads ? threadIdx.x : threadIdx.x % per;
+        lane = per >= kThreads ? 0 : threadIdx.x / per;
+    }
+};
+
+// One CTA: `chunk` tokens and, with bounds, the rest of the last run that
+// begins among them. Shared memory: the tokens' slots, then (bounds) one
+// Bounds a thread.
+template <typename T, int KIND, bool BOUNDS>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_kernel(const RowsParams p)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int run = BOUNDS ? p.bounds_block : 1;
+    Token *tok = reinterpret_cast<Token *>(smem);      // [chunk + run - 1]
+    Bounds *part = reinterpret_cast<Bounds *>(smem + sizeof(Token) * (p.chunk + run - 1));
     __shared__ int first, last;        // the CTA's tokens: tok[first .. last - 1]
     const int tid = threadIdx.x;
-    const int run = p.bounds ? p.bounds_block : 1;
     const int t0 = blockIdx.x * p.chunk;
     const int n = min(p.chunk + run - 1, p.T - t0);   // tokens looked at
+    // the next kernel may be set up meanwhile (it waits for this one's end)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0) {
-        first = n;
+        first = BOUNDS ? n : 0;
         last = n;
     }
     __syncthreads();
     for (int i = tid; i < n; i += kThreads) {
         const Token k = find_token(p, t0 + i);
         tok[i] = k;
-        // the token begins a run: its block's first slot, or its row's first
-        // token (a skipped token is a run of its own)
-        const bool begins = run == 1 || k.off == kSkip || k.slot % run == 0 || t0 + i == __ldg(p.cu_q + k.b);
-        if (begins) {
-            if (i < p.chunk)
-                atomicMin(&first, i);
-            else
-                atomicMin(&last, i);
+        if constexpr (BOUNDS) {
+            // the token begins a run: its block's first slot, or its row's
+            // first token (a skipped token is a run of its own)
+            if (k.off == kSkip || k.slot % run == 0 || t0 + i == __ldg(p.cu_q + k.b))
+                atomicMin(i < p.chunk ? &first : &last, i);
         }
     }
     __syncthreads();
     const int a = first, e = max(a, last);
-    const int per = p.Hkv * (p.D / kGroup);            // groups of a token
+    const Share s(p);
     const long long head = (long long)(p.paged ? p.block_size : p.Smax) * p.D;   // elements between heads
     const T *kn = static_cast<const T *>(p.k_new), *vn = static_cast<const T *>(p.v_new);
-    const int work = (e - a) * per;
-    for (int w = tid; w < work; w += kThreads) {
-        const int i = a + w / per, c = w % per;
-        const Token k = tok[i];
-        if (k.off == kSkip)
-            continue;
+    constexpr bool kScaled = KIND == GQA_DTYPE_E4M3 || KIND == GQA_DTYPE_E2M1;
+    for (int c0 = 0; c0 < s.per; c0 += kThreads) {     // once, but for very wide tokens
+        const int c = c0 + s.c;
+        const bool mine = c < s.per && s.lane < s.lanes;
         const int h = c / (p.D / kGroup), d = (c % (p.D / kGroup)) * kGroup;
-        const long long src = ((long long)(t0 + i) * p.Hkv + h) * p.D + d;
-        const long long dst = k.off + h * head + d;
-        float x[16], y[16];
-        load16(kn + src, x);
-        load16(vn + src, y);
-        const bool scaled = KIND == GQA_DTYPE_E4M3 || KIND == GQA_DTYPE_E2M1;
-        put16<KIND>(p.k_cache, p.k_group, dst, scaled ? __ldg(p.k_scale + h) : 1.f, x);
-        put16<KIND>(p.v_cache, p.v_group, dst, scaled ? __ldg(p.v_scale + h) : 1.f, y);
-    }
-    if (!p.bounds)
-        return;
-    // eight dims of one head a thread, the CTA's runs one after the other (the
-    // keys were read above and come from a cache now)
-    const int lanes = p.Hkv * (p.D / 8);
-    for (int w = tid; w < lanes; w += kThreads) {
-        const int h = w / (p.D / 8), d = (w % (p.D / 8)) * 8;
+        const float ks = kScaled && mine ? __ldg(p.k_scale + h) : 1.f, vs = kScaled && mine ? __ldg(p.v_scale + h) : 1.f;
+        const long long to = h * head + d;
+        const long long row = (long long)p.Hkv * p.D, from = (long long)t0 * row + (long long)c * kGroup;
         int i = a;
         while (i < e) {
-            const Token k = tok[i];
-            if (k.off == kSkip) {
-                ++i;
-                continue;
-            }
-            const int block = k.slot / run;
-            int j = i + 1;             // one past the run
-            while (j < e && tok[j].off != kSkip && tok[j].b == k.b && tok[j].slot / run == block)
-                ++j;
-            uint32_t lo[4], hi[4];
-            load_bounds8(kn + ((long long)(t0 + i) * p.Hkv + h) * p.D + d, lo, hi);
-#pragma unroll 4
-            for (int m = i + 1; m < j; ++m) {
-                uint32_t l[4], u[4];
-                load_bounds8(kn + ((long long)(t0 + m) * p.Hkv + h) * p.D + d, l, u);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    lo[q] = min_bf16x2(lo[q], l[q]);
-                    hi[q] = max_bf16x2(hi[q], u[q]);
+            int j = e;                                 // one past the run (without bounds: all tokens)
+            if constexpr (BOUNDS) {
+                j = i + 1;
+                if (tok[i].off != kSkip) {
+                    // a run's tokens follow each other and share their block
+                    const int left = run - tok[i].slot % run;
+                    j = min(min(e, i + left), __ldg(p.cu_q + tok[i].b + 1) - t0);
                 }
             }
-            // bounds of (block of the row or of the pool, head)
-            long long at;
-            if (p.paged) {
-                at = k.off / ((long long)p.D * p.block_size) + h;   // off is in head 0 of its block
-            } else {
-                const long long r = p.slot_ids ? __ldg(p.slot_ids + k.b) : k.b;
-                at = (r * p.Hkv + h) * (p.Smax / run) + block;
+            Bounds box;
+            bool any = false;
+            for (int m = i + s.lane; mine && m < j; m += s.lanes) {
+                const long long off = tok[m].off;
+                if (off == kSkip)
+                    continue;
+                const Raw<T> x = load_raw(kn + from + m * row, p.wide), y = load_raw(vn + from + m * row, p.wide);
+                if constexpr (BOUNDS) {
+                    take(box, x, !any);
+                    any = true;
+                }
+                put16<KIND>(p.k_cache, p.k_group, off + to, ks, x, p.wide);
+                put16<KIND>(p.v_cache, p.v_group, off + to, vs, y, p.wide);
             }
-            uint4 *bl = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.bounds) + at * 2 * p.D + d);
-            uint4 *bh = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.bounds) + (at * 2 + 1) * p.D + d);
-            if (k.slot % run) {
-                const uint4 l = *bl, u = *bh;
-                const uint32_t lv[4] = {l.x, l.y, l.z, l.w}, uv[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    lo[q] = min_bf16x2(lo[q], lv[q]);
-                    hi[q] = max_bf16x2(hi[q], uv[q]);
+            if constexpr (BOUNDS) {
+                // the lanes' bounds, and what the block had before
+                const int held = min(s.lanes, j - i);  // lanes with a token
+                if (held > 1) {
+                    if (any)
+                        part[tid] = box;
+                    __syncthreads();
+                    if (any && s.lane == 0)
+                        for (int l = 1; l < held; ++l)
+                            widen(box, part[tid + l * s.per]);
+                    __syncthreads();
+                }
+                if (any && s.lane == 0) {
+                    const Token k = tok[i];
+                    long long at;                      // (block of the row or of the pool, head)
+                    if (p.paged) {
+                        at = k.off / ((long long)p.D * p.block_size) + h;   // off is in head 0 of its block
+                    } else {
+                        const long long r = p.slot_ids ? __ldg(p.slot_ids + k.b) : k.b;
+                        at = (r * p.Hkv + h) * (p.Smax / run) + k.slot / run;
+                    }
+                    uint4 *bl = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.bounds) + at * 2 * p.D + d);
+                    uint4 *bh = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.bounds) + (at * 2 + 1) * p.D + d);
+                    if (k.slot % run) {
+                        const uint4 l0 = bl[0], l1 = bl[1], h0 = bh[0], h1 = bh[1];
+                        const Bounds old = {{l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w},
+                                            {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w}};
+                        widen(box, old);
+                    }
+                    bl[0] = make_uint4(box.lo[0], box.lo[1], box.lo[2], box.lo[3]);
+                    bl[1] = make_uint4(box.lo[4], box.lo[5], box.lo[6], box.lo[7]);
+                    bh[0] = make_uint4(box.hi[0], box.hi[1], box.hi[2], box.hi[3]);
+                    bh[1] = make_uint4(box.hi[4], box.hi[5], box.hi[6], box.hi[7]);
                 }
             }
-            *bl = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            *bh = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             i = j;
         }
     }
@@ -340,46 +419,54 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const RowsParams p)
 template <typename T, int KIND>
 __global__ void __launch_bounds__(kThreads) read_kernel(const RowsParams p)
 {
-    extern __shared__ Token tok[];     // [chunk]
+    extern __shared__ __align__(16) unsigned char smem[];
+    Token *tok = reinterpret_cast<Token *>(smem);      // [chunk]
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * p.chunk;
     const int n = min(p.chunk, p.T - t0);
+    // the next kernel may be set up meanwhile (it waits for this one's end)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int i = tid; i < n; i += kThreads)
         tok[i] = find_token(p, t0 + i);
     __syncthreads();
-    const int per = p.Hkv * (p.D / kGroup);
+    const Share s(p);
     const long long head = (long long)(p.paged ? p.block_size : p.Smax) * p.D;
-    for (int w = tid; w < n * per; w += kThreads) {
-        const int i = w / per, c = w % per;
-        const Token k = tok[i];
-        if (k.b < 0)
-            continue;                  // of no row: left as it was
+    constexpr bool kScaled = KIND == GQA_DTYPE_E4M3 || KIND == GQA_DTYPE_E2M1;
+    for (int c0 = 0; c0 < s.per; c0 += kThreads) {
+        const int c = c0 + s.c;
+        if (c >= s.per || s.lane >= s.lanes)
+            break;
         const int h = c / (p.D / kGroup), d = (c % (p.D / kGroup)) * kGroup;
-        const long long dst = ((long long)(t0 + i) * p.Hkv + h) * p.D + d;
-        float x[16], y[16];
-        if (k.off == kSkip) {
+        const float ks = kScaled ? __ldg(p.k_scale + h) : 1.f, vs = kScaled ? __ldg(p.v_scale + h) : 1.f;
+        const long long row = (long long)p.Hkv * p.D, to = (long long)t0 * row + (long long)c * kGroup;
+        for (int m = s.lane; m < n; m += s.lanes) {
+            const Token k = tok[m];
+            if (k.b < 0)
+                continue;                  // of no row: left as it was
+            float x[16], y[16];
+            if (k.off == kSkip) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-                x[q] = y[q] = __int_as_float(0x7fc00000);
-        } else {
-            const long long src = k.off + h * head + d;
-            const bool scaled = KIND == GQA_DTYPE_E4M3 || KIND == GQA_DTYPE_E2M1;
-            get16<KIND>(p.k_cache, p.k_group, src, scaled ? __ldg(p.k_scale + h) : 1.f, x);
-            get16<KIND>(p.v_cache, p.v_group, src, scaled ? __ldg(p.v_scale + h) : 1.f, y);
+                for (int q = 0; q < 16; ++q)
+                    x[q] = y[q] = __int_as_float(0x7fc00000);
+            } else {
+                const long long src = k.off + h * head + d;
+                get16<KIND>(p.k_cache, p.k_group, src, ks, x, p.wide);
+                get16<KIND>(p.v_cache, p.v_group, src, vs, y, p.wide);
+            }
+            store_raw(static_cast<T *>(p.k_out) + to + m * row, round16<T>(x), p.wide);
+            store_raw(static_cast<T *>(p.v_out) + to + m * row, round16<T>(y), p.wide);
         }
-        store16(static_cast<T *>(p.k_out) + dst, x);
-        store16(static_cast<T *>(p.v_out) + dst, y);
     }
 }
 
 template <typename K>
-cudaError_t launch(K kernel, const RowsParams &p, int smem_tokens, cudaStream_t st)
+cudaError_t launch(K kernel, const RowsParams &p, size_t smem, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((p.T + p.chunk - 1) / p.chunk);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(Token) * (size_t)smem_tokens;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -389,27 +476,36 @@ cudaError_t launch(K kernel, const RowsParams &p, int smem_tokens, cudaStream_t 
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <typename T, int KIND>
+cudaError_t launch_append(const RowsParams &p, cudaStream_t st)
+{
+    if (p.bounds)
+        return launch(append_kernel<T, KIND, true>, p,
+                      sizeof(Token) * (size_t)(p.chunk + p.bounds_block - 1) + sizeof(Bounds) * kThreads, st);
+    return launch(append_kernel<T, KIND, false>, p, sizeof(Token) * (size_t)p.chunk, st);
+}
+
 template <int KIND>
 cudaError_t launch_kind(const RowsParams &p, bool write, cudaStream_t st)
 {
-    if (write) {
-        const int tokens = p.chunk + (p.bounds ? p.bounds_block - 1 : 0);
-        return p.vec_bf16 ? launch(append_kernel<__nv_bfloat16, KIND>, p, tokens, st)
-                          : launch(append_kernel<float, KIND>, p, tokens, st);
-    }
-    return p.vec_bf16 ? launch(read_kernel<__nv_bfloat16, KIND>, p, p.chunk, st)
-                      : launch(read_kernel<float, KIND>, p, p.chunk, st);
+    if (write)
+        return p.vec_bf16 ? launch_append<__nv_bfloat16, KIND>(p, st) : launch_append<float, KIND>(p, st);
+    const size_t smem = sizeof(Token) * (size_t)p.chunk;
+    return p.vec_bf16 ? launch(read_kernel<__nv_bfloat16, KIND>, p, smem, st) : launch(read_kernel<float, KIND>, p, smem, st);
 }
 
 }  // namespace
 
 cudaError_t rows_launch(RowsParams p, int kv_dtype, bool write, int sms, cudaStream_t st)
 {
-    // tokens a CTA: as many as give every SM a few CTAs, at most 32 (a run of
-    // 64 in the bounds form costs that CTA two shares)
+    // tokens a CTA: as many as give every SM eight CTAs, at most 32
     const int ctas = sms * 8;
     p.chunk = (p.T + ctas - 1) / ctas;
     p.chunk = p.chunk < 1 ? 1 : p.chunk > 32 ? 32 : p.chunk;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p.k_new) | reinterpret_cast<uintptr_t>(p.v_new) |
+                         reinterpret_cast<uintptr_t>(p.k_out) | reinterpret_cast<uintptr_t>(p.v_out) |
+                         reinterpret_cast<uintptr_t>(p.k_cache) | reinterpret_cast<uintptr_t>(p.v_cache);
+    p.wide = (at & 31u) == 0;
     switch (kv_dtype) {
     case GQA_DTYPE_F32: return launch_kind<GQA_DTYPE_F32>(p, write, st);
     case GQA_DTYPE_BF16: return launch_kind<GQA_DTYPE_BF16>(p, write, st);
