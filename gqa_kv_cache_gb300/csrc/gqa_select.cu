@@ -33,9 +33,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kFew = 64;            // candidates ordered by comparing each with each
+constexpr int kBins = 256;          // bins of the first cut of the scores
 constexpr int kMaxCluster = 8;
 constexpr int kMaxBlocks = 16384;   // blocks a row: the leader's shared memory (12 bytes each)
 constexpr uint32_t kForced = 0xffffffffu;
@@ -62,32 +61,40 @@ __device__ __forceinline__ float unkey32(uint32_t k)
     return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
-// Sums over the block, one after the other: each takes a counter of its own
-// (zero before), so a sum costs one barrier.
+// Sums over a block of NT threads, one after the other, each with one barrier
+// (two sets of cells in turn: the next sum's writes meet no reader of the last).
+// Two counts below 2^16 can share a sum.
+template <int NT>
 struct Sums {
-    int *cell;
+    int (*cell)[NT / 32];
+    int turn;
     __device__ __forceinline__ int operator()(int v)
     {
         v = __reduce_add_sync(0xffffffffu, v);
+        turn ^= 1;
         if ((threadIdx.x & 31) == 0)
-            atomicAdd(cell, v);
+            cell[turn][threadIdx.x >> 5] = v;
         __syncthreads();
-        return *cell++;
+        int s = 0;
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i)
+            s += cell[turn][i];
+        return s;
     }
 };
-constexpr int kSums = 32 + 64 + 8;
 
 // The n-th largest (n >= 1) of the keys key[0 .. m - 1] (in shared memory) is
 // the smallest key that reaches the value returned: the value is found bit by
 // bit from the top, and its low bits are left at zero once exactly n keys
-// reach it. `at`, with all bits from `bit` up decided, is where to start.
-template <typename K>
-__device__ K nth_largest(const K *key, int m, int n, K at, int bit, Sums &sum)
+// reach it.
+template <int NT, typename K>
+__device__ __noinline__ K nth_largest(const K *key, int m, int n, Sums<NT> &sum)
 {
-    for (; bit >= 0; --bit) {
+    K at = 0;
+    for (int bit = 8 * (int)sizeof(K) - 1; bit >= 0; --bit) {
         const K cand = at | ((K)1 << bit);
         int c = 0;
-        for (int j = threadIdx.x; j < m; j += kThreads)
+        for (int j = threadIdx.x; j < m; j += NT)
             c += key[j] >= cand;
         c = sum(c);
         if (c >= n)
@@ -108,9 +115,19 @@ __device__ __forceinline__ int pool_block(const SelectParams &p, int b, int h, i
     return blk < 0 || blk >= p.num_blocks ? -1 : blk * p.Hkv + h;
 }
 
-__device__ __forceinline__ uint4 load8(const void *bounds, long long off)
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
 {
-    return __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(bounds) + off));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The larger magnitude of each of two bfloat16 (signs xored; NaN ignored).
+__device__ __forceinline__ void raise(uint32_t &top, uint32_t x)
+{
+    asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(x));
 }
 
 // Element d of query head g of the unit.
@@ -121,26 +138,31 @@ __device__ __forceinline__ float query(const SelectParams &p, long long head0, i
                     : static_cast<const float *>(p.q)[at];
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams p)
+// NT threads a CTA: 256 where a unit has few CTAs, 128 where the units fill
+// the GPU (more of them at once, so that one's selection runs beside others'
+// loads).
+template <int D, int NT>
+__global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const SelectParams p)
 {
+    constexpr int NW = NT / 32;
     constexpr int E = 2 * D;               // elements of a block's bounds: lo, then hi
-    constexpr int LPB = E / 8 > 32 ? 32 : E / 8;   // lanes that share a block
-    constexpr int V = E / 8 / LPB;         // 16-byte loads a lane
-    constexpr int BPW = 32 / LPB;          // blocks a warp takes at once
-    constexpr int U = 8 / V;               // and this many times before it sums
-    constexpr int STEP = BPW * U;          // blocks of a warp's step: 8 (D = 64: 16, D = 256: 4)
+    constexpr int LOADS = E / 32;          // 16-byte loads a lane and block
+    constexpr int H = LOADS < 8 ? LOADS : 8;   // those in flight at once
     extern __shared__ __align__(16) unsigned char smem[];
     unsigned long long *key64 = reinterpret_cast<unsigned long long *>(smem);   // [NB]: keys of the 64-bit scores
     uint32_t *key = reinterpret_cast<uint32_t *>(key64 + p.NB);                 // [NB] (leader)
-    __shared__ __align__(16) float wt[E];  // N_d, then P_d
-    __shared__ int cells[kSums];
-    __shared__ float warp_top[kWarps];
-    __shared__ uint32_t warp_key[2][kWarps];
+    __shared__ __align__(16) uint16_t wt[3][E];    // the weights N_d, then P_d, as sums of three bfloat16
+    __shared__ double wt64[E];             // and in 64 bits, where they are needed
+    __shared__ float warp_w[NW];           // sums of |weight|
+    __shared__ int cells[2][NW];
+    __shared__ float warp_top[NW];
+    __shared__ uint32_t warp_key[2][NW];
     __shared__ float err[kMaxCluster];
     __shared__ int any_bad[kMaxCluster];
-    __shared__ int scan[kWarps];
-    __shared__ int few[kFew], n_few;
+    __shared__ float range[kMaxCluster][2];   // lowest and highest score that is not forced
+    __shared__ int scan[NW];
+    __shared__ int bins[kBins];
+    __shared__ int few[kFew], n_few, found[2];
 
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
@@ -162,125 +184,142 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
         bits = kBadSlotId;
     const int n = bits ? 0 : (len + p.block_size - 1) / p.block_size;   // valid blocks
     const bool all = n <= p.n_select;
-    if (rank == 0) {
-        for (int i = tid; i < kSums; i += kThreads)
-            cells[i] = 0;
-        if (tid == 0)
-            n_few = 0;
-    }
+    for (int i = tid; i < kBins; i += NT)
+        bins[i] = 0;
+    if (tid == 0)
+        n_few = 0;
     // the leader's shared memory is written to below: every CTA must have started
     if (ranks > 1)
         cl.sync();
 
     if (!all) {
-        for (int d = tid; d < D; d += kThreads) {
-            float up = 0.f, dn = 0.f;
-#pragma unroll 8
-            for (int g = 0; g < G; ++g) {
-                const float x = query(p, head0, g, D, d);
-                up += x != x ? x : fmaxf(x, 0.f);
-                dn += x != x ? x : fminf(x, 0.f);
-            }
-            wt[d] = dn;
-            wt[D + d] = up;
-        }
-        __syncthreads();
-        const int li = lane % LPB, lb = lane / LPB;
-        float w[V][8];
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                w[v][i] = wt[(v * LPB + li) * 8 + i];
-        uint32_t top[V][4];                // largest |x| of the lane's elements, bfloat16 pairs
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                top[v][i] = 0u;
+        // Scores of 16 blocks at a time on the tensor cores: the blocks are
+        // the M side, the weights' three parts columns 0 .. 2 of the N side.
+        // Lane (g, t) holds blocks g and g + 8, eight elements a load from
+        // 32 i + 8 t; a load makes two product steps, whose weights are taken
+        // in the same order. Four sums of each run side by side. The loads
+        // of a warp's next blocks are issued as soon as these are used; the
+        // blocks' places (one lane each) are known one step ahead of that.
+        const int g = lane >> 2, t = lane & 3;
         uint32_t *out = cl.map_shared_rank(key, 0);
         const int j0 = (int)((long long)n * rank / ranks), j1 = (int)((long long)n * (rank + 1) / ranks);
         bool bad = false;
-        // a warp takes 32 blocks at a time: their places first (one lane
-        // each, those of the next 32 while these are scored)
-        int at_next = j0 + 32 * warp + lane < j1 ? pool_block(p, b, h, r, j0 + 32 * warp + lane) : 0;
-        for (int base = j0 + 32 * warp; base < j1; base += 32 * kWarps) {
-            const int at = at_next;
-            bad |= at < 0;
-            const int jn = base + 32 * kWarps + lane;
-            at_next = jn < j1 ? pool_block(p, b, h, r, jn) : 0;
-#pragma unroll 1
-            for (int sub = 0; sub < 32 && base + sub < j1; sub += STEP) {
-                uint4 x[U][V];
+        auto place = [&](int base) {
+            return lane < 16 && base + lane < j1 ? pool_block(p, b, h, r, base + lane) : 0;
+        };
+        uint4 xa[H], xb[H];
+        // a block behind the last (or a bad one) reads the first of the pool: its score is not used
+        auto load = [&](int at, int i0) {
+            const int a = max(0, __shfl_sync(0xffffffffu, at, g)), c = max(0, __shfl_sync(0xffffffffu, at, g + 8));
+            const uint4 *x0 = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.bounds) + (long long)a * E);
+            const uint4 *x1 = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.bounds) + (long long)c * E);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    // block lb * U + u of the step
-                    const int a = __shfl_sync(0xffffffffu, at, sub + lb * U + u);
-                    const bool in = a >= 0 && base + sub + lb * U + u < j1;
+            for (int i = 0; i < H; ++i) {
+                xa[i] = __ldg(x0 + t + 4 * (i0 + i));
+                xb[i] = __ldg(x1 + t + 4 * (i0 + i));
+            }
+        };
+        constexpr int STEP = 16 * NW;
+        int at = place(j0 + 16 * warp), at_next = place(j0 + 16 * warp + STEP);
+        bad |= at < 0;
+        load(at, 0);
+
+        float mag = 0.f;
+        for (int d = tid; d < D; d += NT) {
+            float dn = 0.f, up = 0.f;      // N_d, P_d
+#pragma unroll 8
+            for (int q = 0; q < G; ++q) {
+                const float v = query(p, head0, q, D, d);
+                dn += v != v ? v : fminf(v, 0.f);
+                up += v != v ? v : fmaxf(v, 0.f);
+            }
+            mag += fabsf(dn) + fabsf(up);
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        x[u][v] = in ? load8(p.bounds, (long long)a * E + (v * LPB + li) * 8) : make_uint4(0u, 0u, 0u, 0u);
-                }
-                float s[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    s[u] = 0.f;
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const uint32_t q[4] = {x[u][v].x, x[u][v].y, x[u][v].z, x[u][v].w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            s[u] = fmaf(w[v][2 * i], bf16_lo(q[i]), s[u]);
-                            s[u] = fmaf(w[v][2 * i + 1], bf16_hi(q[i]), s[u]);
-                            asm("max.bf16x2 %0, %1, %2;" : "=r"(top[v][i]) : "r"(top[v][i]), "r"(q[i] & 0x7fff7fffu));
-                        }
-                    }
-                }
-                // sums over the block's lanes: while there are several
-                // blocks, half of the lanes go on with half of them
-                int o = LPB / 2, mine = 0;
-#pragma unroll
-                for (int m = U; m > 1; m /= 2) {
-                    const bool up = lane & o;
-#pragma unroll
-                    for (int u = 0; u < m / 2; ++u) {
-                        const float keep = up ? s[u + m / 2] : s[u], send = up ? s[u] : s[u + m / 2];
-                        s[u] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                    }
-                    mine = 2 * mine + (up ? 1 : 0);
-                    o /= 2;
-                }
-                const bool writes = (lane & (2 * o - 1)) == 0;
-#pragma unroll
-                for (int q = LPB / 2 / U; q > 0; q /= 2)
-                    s[0] += __shfl_xor_sync(0xffffffffu, s[0], q);
-                const int jj = base + sub + lb * U + mine;
-                if (writes && jj < j1)
-                    out[jj] = (jj < p.n_first || jj >= n - p.n_last) ? kForced : key32(s[0]);
+            for (int i = 0; i < 3; ++i) {
+                const __nv_bfloat16 x = __float2bfloat16_rn(dn), y = __float2bfloat16_rn(up);
+                wt[i][d] = __bfloat16_as_ushort(x);
+                wt[i][D + d] = __bfloat16_as_ushort(y);
+                dn -= __bfloat162float(x);
+                up -= __bfloat162float(y);
             }
         }
-        // sum_d |w_d| max |x_d| over this CTA's blocks: no block's sum of
-        // magnitudes is larger
-        float a = 0.f;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                a += fabsf(w[v][2 * i]) * bf16_lo(top[v][i]) + fabsf(w[v][2 * i + 1]) * bf16_hi(top[v][i]);
-#pragma unroll
-        for (int o = LPB / 2; o > 0; o >>= 1)
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-#pragma unroll
-        for (int o = LPB; o < 32; o <<= 1)
-            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        for (int o = 16; o > 0; o >>= 1)
+            mag += __shfl_xor_sync(0xffffffffu, mag, o);
         if (lane == 0)
+            warp_w[warp] = mag;
+        __syncthreads();
+
+        uint32_t top[4] = {0u, 0u, 0u, 0u};   // largest magnitudes, bfloat16 pairs (signs mixed up)
+        float low = INFINITY, high = -INFINITY;   // of the scores that are not forced
+        for (int base = j0 + 16 * warp; base < j1; base += STEP) {
+            float d[4][4] = {};
+#pragma unroll
+            for (int i0 = 0; i0 < LOADS; i0 += H) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (g < 3)
+                        w = *reinterpret_cast<const uint4 *>(&wt[g][32 * (i0 + i) + 8 * t]);
+                    const uint4 a = xa[i], c = xb[i];
+                    mma_bf16(d[(2 * i) & 3], a.x, c.x, a.y, c.y, w.x, w.y);
+                    mma_bf16(d[(2 * i + 1) & 3], a.z, c.z, a.w, c.w, w.z, w.w);
+                    raise(top[0], a.x); raise(top[1], a.y); raise(top[2], a.z); raise(top[3], a.w);
+                    raise(top[0], c.x); raise(top[1], c.y); raise(top[2], c.z); raise(top[3], c.w);
+                }
+                if (i0 + H < LOADS) {
+                    load(at, i0 + H);
+                } else if (base + STEP < j1) {
+                    at = at_next;
+                    bad |= at < 0;
+                    at_next = place(base + 2 * STEP);
+                    load(at, 0);
+                }
+            }
+            // columns 0, 1 are in lanes t = 0, column 2 in lanes t = 1
+            float s[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                s[i] = (d[0][2 * i] + d[1][2 * i]) + (d[2][2 * i] + d[3][2 * i]);
+                const float m = (d[0][2 * i + 1] + d[1][2 * i + 1]) + (d[2][2 * i + 1] + d[3][2 * i + 1]);
+                s[i] += m + __shfl_down_sync(0xffffffffu, s[i], 1);
+                const int j = base + g + 8 * i;
+                if (t == 0 && j < j1) {
+                    const bool f = j < p.n_first || j >= n - p.n_last;
+                    out[j] = f ? kForced : key32(s[i]);
+                    if (!f) {
+                        low = fminf(low, s[i]);
+                        high = fmaxf(high, s[i]);
+                    }
+                }
+            }
+        }
+        raise(top[0], top[1]);
+        raise(top[2], top[3]);
+        raise(top[0], top[2]);
+        float a = fmaxf(fabsf(bf16_lo(top[0])), fabsf(bf16_hi(top[0])));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+            high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+        }
+        if (lane == 0) {
             warp_top[warp] = a;
+            warp_key[0][warp] = __float_as_uint(low);
+            warp_key[1][warp] = __float_as_uint(high);
+        }
         const int bad_any = __syncthreads_or(bad);
         if (tid == 0) {
-            for (int i = 1; i < kWarps; ++i)
+            for (int i = 1; i < NW; ++i) {
                 a = fmaxf(a, warp_top[i]);
+                low = fminf(low, __uint_as_float(warp_key[0][i]));
+                high = fmaxf(high, __uint_as_float(warp_key[1][i]));
+            }
             *cl.map_shared_rank(&err[rank], 0) = a;
             *cl.map_shared_rank(&any_bad[rank], 0) = bad_any;
+            *cl.map_shared_rank(&range[rank][0], 0) = low;
+            *cl.map_shared_rank(&range[rank][1], 0) = high;
         }
     }
     // the scores are in the leader's shared memory
@@ -291,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
     if (rank != 0)
         return;
 
-    Sums sum = {cells};
+    Sums<NT> sum = {cells, 0};
     float lo = -INFINITY, hi = INFINITY;
     int mode = 0;                          // 0: all; 1: score >= lo; 2: and those between by their 64-bit keys
     unsigned long long thr64 = 0;
@@ -299,36 +338,18 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
     if (all) {
         // every valid block; a bad block is found here
         bool bad = false;
-        for (int j = tid; j < n; j += kThreads)
+        for (int j = tid; j < n; j += NT)
             bad |= pool_block(p, b, h, r, j) < 0;
         if (__syncthreads_or(bad))
             bits |= kBadBlock;
     } else {
-        float amax = err[0];
-        for (int i = 0; i < ranks; ++i) {
+        float amax = err[0], low = range[0][0], high = range[0][1];
+        bits |= any_bad[0] ? kBadBlock : 0;
+        for (int i = 1; i < ranks; ++i) {
             amax = fmaxf(amax, err[i]);
-            if (any_bad[i])
-                bits |= kBadBlock;
-        }
-        // the bits in which the keys (but the forced ones) differ
-        uint32_t low = kForced, high = 0;
-        for (int j = tid; j < n; j += kThreads) {
-            const uint32_t k = key[j];
-            if (k != kForced) {
-                low = min(low, k);
-                high = max(high, k);
-            }
-        }
-        low = __reduce_min_sync(0xffffffffu, low);
-        high = __reduce_max_sync(0xffffffffu, high);
-        if (lane == 0) {
-            warp_key[0][warp] = low;
-            warp_key[1][warp] = high;
-        }
-        __syncthreads();
-        for (int i = 0; i < kWarps; ++i) {
-            low = min(low, warp_key[0][i]);
-            high = max(high, warp_key[1][i]);
+            low = fminf(low, range[i][0]);
+            high = fmaxf(high, range[i][1]);
+            bits |= any_bad[i] ? kBadBlock : 0;
         }
         const int need = p.n_select;       // more than the forced blocks?
         const int forced = min(n, p.n_first) + p.n_last;
@@ -336,104 +357,189 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
         if (need <= forced) {
             lo = hi = INFINITY;            // only those
         } else {
-            // all of them share the bits above the first that low and high differ in
-            const int bit = low == high ? -1 : 31 - __clz(low ^ high);
-            const uint32_t start = bit < 0 ? low : bit == 31 ? 0u : low & ~((2u << bit) - 1u);
-            const uint32_t thr = nth_largest(key, n, need, start, bit, sum);
-            uint32_t least = kForced;      // the smallest key that reaches it
-            for (int j = tid; j < n; j += kThreads)
-                if (key[j] >= thr)
-                    least = min(least, key[j]);
-            least = __reduce_min_sync(0xffffffffu, least);
-            __syncthreads();
-            if (lane == 0)
-                warp_key[0][warp] = least;
-            __syncthreads();
-            for (int i = 0; i < kWarps; ++i)
-                least = min(least, warp_key[0][i]);
-            // adds in a row: a lane's products, the lanes of a block, the
-            // group's queries; 1.1 covers the higher orders and amax's rounding
-            const float e = 1.1f * (float)(8 * V + 8 + G) * 5.9604645e-8f * amax;
-            const float T = unkey32(least);
+            // The need-th largest score T: a cut into bins, equal steps of
+            // the scores' range (any map that keeps their order does), finds
+            // the bin that T is in; its few members are ranked. A bin with
+            // many of them, or scores that are not finite: bit by bit.
+            const float step = (float)kBins / (high - low);
+            auto bin = [&](float s) { return min(kBins - 1, (int)((s - low) * step)); };
+            const bool finite = high - low < INFINITY && step < INFINITY;
+            int odd = 0;                   // NaN scores (low and high do not show them)
+            if (finite)
+                for (int j = tid; j < n; j += NT) {
+                    const uint32_t k = key[j];
+                    if (k == kForced - 1)
+                        odd = 1;
+                    else if (k != kForced)
+                        atomicAdd(&bins[bin(unkey32(k))], 1);
+                }
+            odd = __syncthreads_or(odd);
+            float T = 0.f;
+            bool have = false;
+            if (finite && !odd) {
+                // scores in the bins above this thread's (from the top: 0, 1, ..)
+                constexpr int PER = kBins / NT;
+                int mine[PER], own = 0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    own += mine[i] = bins[kBins - 1 - (tid * PER + i)];
+                int incl = own;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o)
+                        incl += x;
+                }
+                if (lane == 31)
+                    scan[warp] = incl;
+                __syncthreads();
+                int before = forced + incl - own;
+                for (int i = 0; i < warp; ++i)
+                    before += scan[i];
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    if (before < need && before + mine[i] >= need) {
+                        found[0] = kBins - 1 - (tid * PER + i);
+                        found[1] = before;
+                    }
+                    before += mine[i];
+                }
+                __syncthreads();
+                const int at_bin = found[0], rest = need - found[1];   // T is the rest-th of its bin
+                const int members = bins[at_bin];
+                if (members <= kFew) {
+                    for (int j = tid; j < n; j += NT) {
+                        const uint32_t k = key[j];
+                        if (k != kForced && bin(unkey32(k)) == at_bin)
+                            few[atomicAdd(&n_few, 1)] = j;
+                    }
+                    __syncthreads();
+                    for (int i = tid; i < members; i += NT) {
+                        const uint32_t k = key[few[i]];
+                        int above = 0, same = 0;
+                        for (int q = 0; q < members; ++q) {
+                            const uint32_t x = key[few[q]];
+                            above += x > k;
+                            same += x == k;
+                        }
+                        if (above < rest && above + same >= rest)
+                            warp_key[0][0] = k;    // (equal keys write the same)
+                    }
+                    __syncthreads();
+                    T = unkey32(warp_key[0][0]);
+                    have = true;
+                    if (tid == 0)
+                        n_few = 0;
+                }
+            }
+            if (!have) {
+                const uint32_t thr = nth_largest(key, n, need, sum);
+                uint32_t least = kForced;  // the smallest key that reaches it
+                for (int j = tid; j < n; j += NT)
+                    if (key[j] >= thr)
+                        least = min(least, key[j]);
+                least = __reduce_min_sync(0xffffffffu, least);
+                if (lane == 0)
+                    warp_key[1][warp] = least;
+                __syncthreads();
+                for (int i = 0; i < NW; ++i)
+                    least = min(least, warp_key[1][i]);
+                T = unkey32(least);
+            }
+            // sum_d |w_d| |x_d| of any block is at most the sum of |w| times the
+            // largest |x|. In units of 2^-24 of it: a matrix step truncates
+            // its sum (4), E / 64 steps in a row; joining the sums, the
+            // weights' third parts and the group's queries 8 + G. 1.1 covers
+            // higher orders; a weight near float32's smallest loses its low parts
+            float wsum = 0.f;
+            for (int i = 0; i < NW; ++i)
+                wsum += warp_w[i];
+            const float e = 1.1f * (float)(E / 16 + 8 + G) * 5.9604645e-8f * wsum * amax + 2e-37f * amax;
             lo = T - 2.f * e;
             hi = T + 2.f * e;
             // one rounding of each border outwards
             lo -= fabsf(lo) * 1.2e-7f;
             hi += fabsf(hi) * 1.2e-7f;
             int above = 0, between = 0;
-            for (int j = tid; j < n; j += kThreads) {
+            for (int j = tid; j < n; j += NT) {
                 const uint32_t k = key[j];
                 const float s = unkey32(k);
                 const bool f = k == kForced;
                 above += f || s > hi;
                 between += !f && !(s > hi) && !(s < lo);
             }
-            above = sum(above);
-            between = sum(between);
+            const int both = sum(above | (between << 16));
+            above = both & 0xffff;
+            between = (int)((unsigned)both >> 16);
             if (above + between != need) {
                 mode = 2;
                 take = need - above;
-                // 64-bit sums of the blocks in between, a warp each
-                for (int j0 = warp * 32; j0 < n; j0 += kThreads) {
-                    const int j = j0 + lane;
+                // the weights in 64 bits, then the sums of the blocks in
+                // between, a warp each
+                for (int d = tid; d < D; d += NT) {
+                    double dn = 0.0, up = 0.0;
+#pragma unroll 8
+                    for (int q = 0; q < G; ++q) {
+                        const float v = query(p, head0, q, D, d);
+                        dn += v != v ? (double)v : (double)fminf(v, 0.f);
+                        up += v != v ? (double)v : (double)fmaxf(v, 0.f);
+                    }
+                    wt64[d] = dn;
+                    wt64[D + d] = up;
+                }
+                __syncthreads();
+                for (int base = warp * 32; base < n; base += NT) {
+                    const int j = base + lane;
                     const float s = j < n ? unkey32(key[j]) : 0.f;
                     const bool is = j < n && key[j] != kForced && !(s > hi) && !(s < lo);
                     if (j < n)
                         key64[j] = 0;      // not in between (no score has this key)
                     __syncwarp();
                     for (unsigned left = __ballot_sync(0xffffffffu, is); left; left &= left - 1) {
-                        const int jj = j0 + __ffs(left) - 1;
-                        const int at = pool_block(p, b, h, r, jj);
+                        const int jj = base + __ffs(left) - 1;
+                        const int at = max(0, pool_block(p, b, h, r, jj));
+                        const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.bounds) + (long long)at * E;
                         double acc = 0.0;
-                        if (at >= 0) {
-                            const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.bounds) + (long long)at * E;
-                            for (int d = lane; d < D; d += 32) {
-                                double up = 0.0, dn = 0.0;
-                                for (int g = 0; g < G; ++g) {
-                                    const float v = query(p, head0, g, D, d);
-                                    up += v != v ? (double)v : (double)fmaxf(v, 0.f);
-                                    dn += v != v ? (double)v : (double)fminf(v, 0.f);
-                                }
-                                acc += dn * (double)__bfloat162float(x[d]) + up * (double)__bfloat162float(x[D + d]);
-                            }
-                        }
+#pragma unroll
+                        for (int d = 0; d < E; d += 32)
+                            acc += wt64[d + lane] * (double)__bfloat162float(x[d + lane]);
 #pragma unroll
                         for (int o = 16; o > 0; o >>= 1)
                             acc += __shfl_xor_sync(0xffffffffu, acc, o);
                         if (lane == 0) {
                             key64[jj] = key64_of(acc + 0.0);
-                            const int at_few = atomicAdd(&n_few, 1);
-                            if (at_few < kFew)
-                                few[at_few] = jj;
+                            const int i = atomicAdd(&n_few, 1);
+                            if (i < kFew)
+                                few[i] = jj;
                         }
                     }
                 }
                 __syncthreads();
                 if (between <= kFew) {
-                    // few: each one's rank by comparing it with the others
-                    // (the list's order does not matter). The last one kept
-                    // sets the threshold
-                    for (int i = tid; i < between; i += kThreads) {
+                    // each one's rank by comparing it with the others (the
+                    // list's order does not matter); the last one kept sets
+                    // the threshold
+                    for (int i = tid; i < between; i += NT) {
                         const int j = few[i];
+                        const unsigned long long y = key64[j];
                         int before = 0, equal = 0;
-                        for (int k = 0; k < between; ++k) {
-                            const unsigned long long x = key64[few[k]], y = key64[j];
-                            before += x > y || (x == y && few[k] < j);
-                            equal += x == y && few[k] <= j;
+                        for (int q = 0; q < between; ++q) {
+                            const unsigned long long x = key64[few[q]];
+                            before += x > y || (x == y && few[q] < j);
+                            equal += x == y && few[q] <= j;
                         }
                         if (before == take - 1) {
-                            scan[0] = j;
-                            scan[1] = equal;
+                            found[0] = j;
+                            found[1] = equal;
                         }
                     }
                     __syncthreads();
-                    thr64 = key64[scan[0]];
-                    take = scan[1];
-                    __syncthreads();
+                    thr64 = key64[found[0]];
+                    take = found[1];
                 } else {
-                    thr64 = nth_largest(key64, n, take, 0ull, 63, sum);
+                    thr64 = nth_largest(key64, n, take, sum);
                     int over = 0;
-                    for (int j = tid; j < n; j += kThreads)
+                    for (int j = tid; j < n; j += NT)
                         over += key64[j] > thr64;
                     take -= sum(over);
                 }
@@ -447,69 +553,63 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
                 atomicOr(p.status, bits);
             p.sel_lengths[unit] = 0;
         }
-        for (int i = tid; i < p.n_select; i += kThreads)
+        for (int i = tid; i < p.n_select; i += NT)
             p.ids[row + i] = p.table[row + i] = -1;
         return;
     }
-    // the kept blocks in ascending order, kThreads blocks at a time
-    int kept = 0, ties = 0;                // of the blocks before
-    for (int j0 = 0; j0 < n; j0 += kThreads) {
-        const int j = j0 + tid;
-        bool over = false, tie = false;
-        if (j < n) {
-            if (mode == 0) {
-                over = true;
-            } else if (key[j] == kForced) {
-                over = true;
-            } else {
-                const float s = unkey32(key[j]);
-                if (mode == 1) {
-                    over = !(s < lo) && lo < INFINITY;
-                } else {
-                    over = s > hi || key64[j] > thr64;
-                    tie = !over && key64[j] == thr64;
-                }
-            }
-        }
-        // places among the kept: those over, and the first `take` ties
-        const unsigned mo = __ballot_sync(0xffffffffu, over), mt = __ballot_sync(0xffffffffu, tie);
-        __syncthreads();
-        if (lane == 0)
-            scan[warp] = __popc(mo) | (__popc(mt) << 16);
-        __syncthreads();
-        int before = 0, total = 0;
+    // the kept blocks in ascending order: each thread a stretch of the blocks
+    const int per = (n + NT - 1) / NT;
+    const int c0 = min(n, tid * per), c1 = min(n, c0 + per);
+    // 2: kept, 1: kept if among the first `take` of its equals, 0: not
+    auto state = [&](int j) {
+        if (mode == 0 || key[j] == kForced)
+            return 2;
+        const float s = unkey32(key[j]);
+        if (mode == 1)
+            return !(s < lo) && lo < INFINITY ? 2 : 0;
+        return s > hi || key64[j] > thr64 ? 2 : key64[j] == thr64 ? 1 : 0;
+    };
+    int mine = 0;                          // kept | ties << 16
+    for (int j = c0; j < c1; ++j) {
+        const int k = state(j);
+        mine += k == 2 ? 1 : k << 16;
+    }
+    int incl = mine;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            const int c = scan[i];
-            before += i < warp ? c : 0;
-            total += c;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += x;
+    }
+    __syncthreads();
+    if (lane == 31)
+        scan[warp] = incl;
+    __syncthreads();
+    int before = incl - mine;
+    for (int i = 0; i < warp; ++i)
+        before += scan[i];
+    int ties = (int)((unsigned)before >> 16), at = (before & 0xffff) + min(ties, take);
+    for (int j = c0; j < c1; ++j) {
+        const int k = state(j);
+        if (k == 2 || (k == 1 && ties < take)) {
+            if (at < p.n_select) {
+                p.ids[row + at] = j;
+                p.table[row + at] = pool_block(p, b, h, r, j);
+            }
+            ++at;
         }
-        const unsigned below = (1u << lane) - 1u;
-        const int nt = ties + (before >> 16) + __popc(mt & below);    // ties before this block
-        const int at = kept + (before & 0xffff) + __popc(mo & below) + min(max(0, take - ties), nt - ties);
-        if ((over || (tie && nt < take)) && at < p.n_select) {
-            p.ids[row + at] = j;
-            p.table[row + at] = pool_block(p, b, h, r, j);
-        }
-        kept += (total & 0xffff) + min(max(0, take - ties), total >> 16);
-        ties += total >> 16;
+        ties += k == 1;
     }
     const int total = min(n, p.n_select);
-    for (int i = total + tid; i < p.n_select; i += kThreads)
+    for (int i = total + tid; i < p.n_select; i += NT)
         p.ids[row + i] = p.table[row + i] = -1;
     if (tid == 0)
         p.sel_lengths[unit] = (total - 1) * p.block_size + (len - (n - 1) * p.block_size);
 }
 
-template <int D>
-cudaError_t launch_d(const SelectParams &p, int sms, cudaStream_t st)
+template <int D, int NT>
+cudaError_t launch_one(const SelectParams &p, int c, cudaStream_t st)
 {
-    const int units = p.B * p.Hkv;
-    // CTAs a unit: enough to give every SM two, each with work for its warps
-    int c = 1;
-    while (c < kMaxCluster && (long long)units * c * 2 <= 2LL * sms && p.NB >= 64 * c)
-        c *= 2;
-    const size_t smem = 12 * (size_t)p.NB;
     static std::atomic<uint64_t> ready;    // devices whose attribute is set, a bit each
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -517,15 +617,15 @@ cudaError_t launch_d(const SelectParams &p, int sms, cudaStream_t st)
         return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * kMaxBlocks);
+        e = cudaFuncSetAttribute(select_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * kMaxBlocks);
         if (e != cudaSuccess)
             return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(units * c);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3(p.B * p.Hkv * c);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = 12 * (size_t)p.NB;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -536,7 +636,20 @@ cudaError_t launch_d(const SelectParams &p, int sms, cudaStream_t st)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, select_kernel<D>, p);
+    return cudaLaunchKernelEx(&cfg, select_kernel<D, NT>, p);
+}
+
+template <int D>
+cudaError_t launch_d(const SelectParams &p, int sms, cudaStream_t st)
+{
+    const int units = p.B * p.Hkv;
+    if (units > 2 * sms)
+        return launch_one<D, 128>(p, 1, st);
+    // CTAs a unit: enough to give every SM two, each with 16 blocks for its warps
+    int c = 1;
+    while (c < kMaxCluster && (long long)units * c * 2 <= 2LL * sms && p.NB >= 2 * 16 * 8 * c)
+        c *= 2;
+    return launch_one<D, 256>(p, c, st);
 }
 
 }  // namespace
