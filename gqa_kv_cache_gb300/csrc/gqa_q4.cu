@@ -155,6 +155,11 @@ __device__ __noinline__ long long paged_row(const int32_t *table, int block_size
     return ((long long)blk * Hkv + kvh) * block_size + s % block_size;
 }
 
+__device__ __forceinline__ int scale_head(const DecodeParams &p, int b, int kvh)
+{
+    return p.scale_heads ? b % p.scale_heads : kvh;
+}
+
 // The new token's vector x (bfloat16, D of them) quantised into the cache at
 // element offset off, by one warp: D / 32 dims a lane.
 template <int D>
@@ -188,11 +193,6 @@ __device__ __forceinline__ void append_vec(const __nv_bfloat16 *x, void *cache, 
         static_cast<uint8_t *>(groups)[(off >> 4) + lane / LG] = (uint8_t)s;
 }
 
-__device__ __forceinline__ int scale_head(const DecodeParams &p, int b, int kvh)
-{
-    return p.scale_heads ? b % p.scale_heads : kvh;
-}
-
 // The new token of the source's row into slot L.
 template <int D>
 __device__ __noinline__ void append_token(const DecodeParams &p, int b, int kvh, int L, int lane)
@@ -211,37 +211,31 @@ __device__ __noinline__ void append_token(const DecodeParams &p, int b, int kvh,
 
 // The unit's query fragments: lane (g, t) holds row g's D / 4 dims from
 // D / 4 * t, scaled by a power of two into f16's range; `mul` is the factor
-// that takes a product to a base-2 score for row g.
+// that takes a product to a base-2 score for row g. q: the rows in shared memory.
 template <int D, bool QF32>
-__device__ __forceinline__ void load_query(const DecodeParams &p, int b, int kvh, int lane,
+__device__ __forceinline__ void load_query(const DecodeParams &p, const void *q, int lane,
                                            uint32_t (&qh)[D / 16][2], uint32_t (&ql)[QF32 ? D / 16 : 1][2], float &mul)
 {
     constexpr int N = D / 4;
     const int g = lane >> 2, t = lane & 3;
     float x[N];
+    if constexpr (QF32) {
+        const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(q) + g * D + N * t);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        x[i] = 0.f;
-    if (g < p.G) {
-        const long long at = ((long long)b * p.Hq + (long long)kvh * p.G + g) * D + N * t;
-        if constexpr (QF32) {
-            const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at);
+        for (int i = 0; i < N / 4; ++i) {
+            const float4 v = s[i];
+            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+        }
+    } else {
+        const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(q) + g * D + N * t);
 #pragma unroll
-            for (int i = 0; i < N / 4; ++i) {
-                const float4 v = __ldg(s + i);
-                x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-            }
-        } else {
-            const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + at);
+        for (int i = 0; i < N / 8; ++i) {
+            const uint4 v = s[i];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < N / 8; ++i) {
-                const uint4 v = __ldg(s + i);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[8 * i + 2 * j] = bf16_lo(w[j]);
-                    x[8 * i + 2 * j + 1] = bf16_hi(w[j]);
-                }
+            for (int j = 0; j < 4; ++j) {
+                x[8 * i + 2 * j] = bf16_lo(w[j]);
+                x[8 * i + 2 * j + 1] = bf16_hi(w[j]);
             }
         }
     }
@@ -273,7 +267,14 @@ struct Segment {
     TileCursor c;      // at its first tile
     int t_last;        // its last tile
     int good;          // the row's content is in order
+    float ks, vs;      // its head's scales
 };
+
+template <int D, bool QF32>
+constexpr int query_bytes()
+{
+    return kRows * D * (QF32 ? 4 : 2);
+}
 
 // What a warp's copies are taken from.
 template <int D, bool PAGED>
@@ -298,11 +299,26 @@ __device__ __forceinline__ int load_page(const DecodeParams &p, const Fetch<D, P
     return x <= f.t_last && s <= c.L ? __ldg(p.block_table + (long long)c.b * p.max_blocks + (s >> shift)) : 0;
 }
 
-// The copies' segment becomes that of cursor c.
-template <int D, bool PAGED>
+// The copies' segment becomes that of cursor c. The segment's query rows (rows
+// behind the G are zeros) and scales are copied too, a part by each warp, in
+// the group of the copies that comes next.
+template <int D, bool QF32, bool PAGED>
 __device__ __forceinline__ void enter(const DecodeParams &p, const TileCursor &c, Fetch<D, PAGED> &f, Segment *seg, int *bad,
-                                      int shift, bool pages, int warp, int lane)
+                                      void *q, int shift, bool pages, int warp, int lane)
 {
+    constexpr int B = QF32 ? 4 : 2;                // bytes an element
+    constexpr int C = D * B / 16;                  // 16-byte pieces a row
+    const char *src = static_cast<const char *>(p.q) + ((long long)c.b * p.Hq + (long long)c.kvh * p.G) * D * B;
+#pragma unroll
+    for (int i = 0; i < (kRows * C + kThreads - 1) / kThreads; ++i) {
+        const int x = i * kThreads + warp * 32 + lane;
+        if (kRows * C % kThreads == 0 || x < kRows * C)
+            copy16(smem_at(q) + x * 16, x / C < p.G ? src + x * 16 : src, x / C < p.G ? 16 : 0);
+    }
+    if (lane < 2) {
+        const float *sc = (lane ? p.v_scale : p.k_scale) + scale_head(p, c.b, c.kvh);
+        copy_small<4>(smem_at(lane ? &seg->vs : &seg->ks), sc);
+    }
     f.t = c.t;
     f.t_last = (int)min((long long)c.nr - 1, c.t + (c.end - c.g) - 1);
     f.good = row_ok(p, c.b, c.L);
@@ -543,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
 {
     extern __shared__ __align__(128) unsigned char dyn[];
     Stage<D>(*ring)[kWarps] = reinterpret_cast<Stage<D>(*)[kWarps]>(dyn);      // [kStages]
+    auto sm_q = reinterpret_cast<uint8_t(*)[query_bytes<D, QF32>()]>(dyn + kStages * kWarps * sizeof(Stage<D>));   // [kSegs]
     __shared__ long long sched[kThreads / 32 + 8];
     __shared__ TileWalk walk;
     __shared__ Segment segs[kSegs];            // every warp writes the same
@@ -569,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
         left = walk_first(p, c, walk, in_b);
         if (!left)
             return;
-        enter(p, c, f, &segs[0], &sm_bad[warp][0], shift, pages, warp, lane);
+        enter<D, QF32>(p, c, f, &segs[0], &sm_bad[warp][0], sm_q[0], shift, pages, warp, lane);
         __syncwarp();
     }
     auto fetch = [&](int slot) {
@@ -590,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
                 left = walk_next(p, c, walk, in_b);
                 if (left) {
                     sf = (sf + 1) % kSegs;
-                    enter(p, c, f, &segs[sf], &sm_bad[warp][sf], shift, pages, warp, lane);
+                    enter<D, QF32>(p, c, f, &segs[sf], &sm_bad[warp][sf], sm_q[sf], shift, pages, warp, lane);
                     __syncwarp();
                 }
             }
@@ -602,6 +619,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
     for (int i = 0; i < kStages - 1; ++i)
         fetch(i);
 
+    // the first segment's query rows and scales, every warp's part (those of
+    // a later one came with the last tile of the segment before it, whose end
+    // the warps meet at)
+    copy_wait<kStages - 2>();
+    __syncthreads();
     uint32_t qh[D / 16][2], ql[QF32 ? D / 16 : 1][2];
     float mul0, mul1;                      // product to base-2 score, rows 2t4 and 2t4 + 1
     float m0, m1, l0, l1;
@@ -613,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
         if (!good && tid == 0 && seg->c.t == 0 && seg->c.kvh == 0)
             report(p, row_error_bits(p, seg->c.b, seg->c.L));
         float mul;
-        load_query<D, QF32>(p, seg->c.b, seg->c.kvh, lane, qh, ql, mul);
-        const float ks = __ldg(p.k_scale + scale_head(p, seg->c.b, seg->c.kvh));
+        load_query<D, QF32>(p, sm_q[sc], lane, qh, ql, mul);
+        const float ks = seg->ks;
         mul0 = __shfl_sync(0xffffffffu, mul, 8 * t4) * ks;
         mul1 = __shfl_sync(0xffffffffu, mul, 8 * t4 + 4) * ks;
         m0 = m1 = -INFINITY;
@@ -625,7 +647,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
             for (int j = 0; j < 4; ++j)
                 o[i][j] = 0.f;
 
+        int arrived = -1;                  // thread 0: the unit's arrival count before the last tile
         for (int t = seg->c.t; t <= seg->t_last; ++t) {
+            if (t == seg->t_last && tid == 0 && (seg->c.t != 0 || t != seg->c.nr - 1))
+                asm volatile("ld.acquire.gpu.global.s32 %0, [%1];"
+                             : "=r"(arrived)
+                             : "l"(p.ws_cnt + seg->c.b * p.Hkv + seg->c.kvh)
+                             : "memory");
             copy_wait<kStages - 2>();      // this lane's copies of the tile, then the other lanes'
             __syncwarp();
             fetch(slot == 0 ? kStages - 1 : slot - 1);
@@ -726,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
         auto &sm_merge = *reinterpret_cast<Merge<D> *>(reinterpret_cast<unsigned char *>(spare) + sizeof sm_o);
         static_assert(sizeof sm_o + sizeof(Merge<D>) <= kWarps * sizeof(Stage<D>), "the slot holds both");
         __syncthreads();                   // every warp has read its part of the slot
-        const float vs = __ldg(p.v_scale + scale_head(p, seg->c.b, seg->c.kvh));
+        const float vs = seg->vs;
 #pragma unroll
         for (int i = 0; i < D / 16; i += 2) {
             // rows 2t4, 2t4 + 1: dims D / 8 * g + 2 i .. + 3
@@ -744,17 +772,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
         if (any_bad && good && tid == 0)
             report(p, kBadBlock);
         const bool end = !left && sc == sf;
-        finish_segment<kWarps, kRows, D, D, false>(p, cur, walk, first_t, !good || any_bad, sm_m, sm_l, sm_o,
-                                                  &sm_flag, sm_merge, tid, kThreads, [] { __syncthreads(); });
+        finish_segment<kWarps, kRows, D, D, false, true>(p, cur, walk, first_t, !good || any_bad, sm_m, sm_l, sm_o,
+                                                         &sm_flag, sm_merge, tid, kThreads,
+                                                         [] { __syncthreads(); }, arrived);
         if (end)
             break;
     }
 }
 
-template <int D>
+template <int D, bool QF32>
 constexpr int dyn_bytes()
 {
-    return kWarps * kStages * (int)sizeof(Stage<D>);
+    return kWarps * kStages * (int)sizeof(Stage<D>) + kSegs * query_bytes<D, QF32>();
 }
 
 template <int D, bool QF32, bool PAGED>
@@ -769,18 +798,18 @@ cudaError_t launch_one(const DecodeParams *p, cudaStream_t st, int *per_sm)
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
         e = cudaFuncSetAttribute(q4_decode_kernel<D, QF32, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 dyn_bytes<D>());
+                                 dyn_bytes<D, QF32>());
         if (e != cudaSuccess)
             return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     if (!p)
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, q4_decode_kernel<D, QF32, PAGED>, kThreads,
-                                                             dyn_bytes<D>());
+                                                             dyn_bytes<D, QF32>());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p->grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = dyn_bytes<D>();
+    cfg.dynamicSmemBytes = dyn_bytes<D, QF32>();
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
