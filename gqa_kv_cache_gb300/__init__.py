@@ -248,8 +248,8 @@ def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False, gro
     shape = q.shape
     if out is None:
         out = torch.empty(shape, dtype=torch.float32, device=q.device)
-    elif out.shape != shape or out.dtype != torch.float32 or not out.is_contiguous():
-        raise ValueError("out must be a contiguous float32 (B, Hq, D) tensor")
+    elif out.shape != shape or out.dtype != torch.float32 or not out.is_contiguous() or out.get_device() != dev:
+        raise ValueError("out must be a contiguous float32 (B, Hq, D) tensor on q's device")
     return code, out
 
 
@@ -277,12 +277,13 @@ def decode_step(q, k_new, v_new, k_cache, v_cache, lengths, slot_ids=None, *, ou
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
-    need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
-    ws = _workspace(q.device, need, stream) if workspace is None else workspace
-    code = lib.gqa_decode_step_ex(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
-                                  _ptr(lengths), _ptr(slot_ids), _ptr(out), B, Hq, Hkv, D, R, Smax,
-                                  dt, _ptr(ws), ws.numel() * ws.element_size(),
-                                  _ptr(status), _stream(stream), ctypes.byref(o))
+    with _on(q.device):
+        need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
+        ws = _workspace(q.device, need, stream) if workspace is None else workspace
+        code = lib.gqa_decode_step_ex(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                                      _ptr(lengths), _ptr(slot_ids), _ptr(out), B, Hq, Hkv, D, R, Smax,
+                                      dt, _ptr(ws), ws.numel() * ws.element_size(),
+                                      _ptr(status), _stream(stream), ctypes.byref(o))
     _check(code, "gqa_decode_step")
     return out
 
@@ -310,13 +311,14 @@ def decode_step_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths,
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
-    need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
-    ws = _workspace(q.device, need, stream) if workspace is None else workspace
-    code = lib.gqa_decode_step_paged_ex(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_blocks),
-                                        _ptr(v_blocks), _ptr(block_table), _ptr(lengths), _ptr(out),
-                                        B, Hq, Hkv, D, NB, BS, MB, dt, _ptr(ws),
-                                        ws.numel() * ws.element_size(), _ptr(status),
-                                        _stream(stream), ctypes.byref(o))
+    with _on(q.device):
+        need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
+        ws = _workspace(q.device, need, stream) if workspace is None else workspace
+        code = lib.gqa_decode_step_paged_ex(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_blocks),
+                                            _ptr(v_blocks), _ptr(block_table), _ptr(lengths), _ptr(out),
+                                            B, Hq, Hkv, D, NB, BS, MB, dt, _ptr(ws),
+                                            ws.numel() * ws.element_size(), _ptr(status),
+                                            _stream(stream), ctypes.byref(o))
     _check(code, "gqa_decode_step_paged")
     return out
 
@@ -342,12 +344,13 @@ def attend(q, k_cache, v_cache, lengths, slot_ids=None, *, out=None, status=None
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
-    need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
-    ws = _workspace(q.device, need, stream) if workspace is None else workspace
-    code = lib.gqa_attend(_ptr(q), _DTYPES[q.dtype], _ptr(k_cache), _ptr(v_cache), _ptr(lengths),
-                          _ptr(slot_ids), _ptr(out), B, Hq, Hkv, D, R, Smax, dt, _ptr(ws),
-                          ws.numel() * ws.element_size(), _ptr(status), _stream(stream),
-                          ctypes.byref(o))
+    with _on(q.device):
+        need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
+        ws = _workspace(q.device, need, stream) if workspace is None else workspace
+        code = lib.gqa_attend(_ptr(q), _DTYPES[q.dtype], _ptr(k_cache), _ptr(v_cache), _ptr(lengths),
+                              _ptr(slot_ids), _ptr(out), B, Hq, Hkv, D, R, Smax, dt, _ptr(ws),
+                              ws.numel() * ws.element_size(), _ptr(status), _stream(stream),
+                              ctypes.byref(o))
     _check(code, "gqa_attend")
     return out
 
@@ -373,13 +376,14 @@ def attend_paged(q, k_blocks, v_blocks, block_table, lengths, *, out=None, statu
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
-    need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
-    ws = _workspace(q.device, need, stream) if workspace is None else workspace
-    code = lib.gqa_attend_paged(_ptr(q), _DTYPES[q.dtype], _ptr(k_blocks), _ptr(v_blocks),
-                                _ptr(block_table), _ptr(lengths), _ptr(out), B, Hq, Hkv, D, NB, BS,
-                                block_table.shape[1], dt, _ptr(ws),
-                                ws.numel() * ws.element_size(), _ptr(status), _stream(stream),
-                                ctypes.byref(o))
+    with _on(q.device):
+        need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
+        ws = _workspace(q.device, need, stream) if workspace is None else workspace
+        code = lib.gqa_attend_paged(_ptr(q), _DTYPES[q.dtype], _ptr(k_blocks), _ptr(v_blocks),
+                                    _ptr(block_table), _ptr(lengths), _ptr(out), B, Hq, Hkv, D, NB, BS,
+                                    block_table.shape[1], dt, _ptr(ws),
+                                    ws.numel() * ws.element_size(), _ptr(status), _stream(stream),
+                                    ctypes.byref(o))
     _check(code, "gqa_attend_paged")
     return out
 
@@ -414,12 +418,13 @@ def decode_multi(q, k_new, v_new, k_cache, v_cache, lengths, cu_q, slot_ids=None
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
               wait_limit_cycles, test_stall)
     lib = _lib.load()
-    need = lib.gqa_workspace_bytes_multi(B, Hq, Hkv, D, dt, int(max_q_len), ctypes.byref(o))
-    ws = _workspace(q.device, need, stream) if workspace is None else workspace
-    code = lib.gqa_decode_multi(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
-                                _ptr(lengths), _ptr(cu_q), _ptr(slot_ids), _ptr(out), B, T, int(max_q_len),
-                                Hq, Hkv, D, R, Smax, dt, _ptr(ws), ws.numel() * ws.element_size(),
-                                _ptr(status), _stream(stream), ctypes.byref(o))
+    with _on(q.device):
+        need = lib.gqa_workspace_bytes_multi(B, Hq, Hkv, D, dt, int(max_q_len), ctypes.byref(o))
+        ws = _workspace(q.device, need, stream) if workspace is None else workspace
+        code = lib.gqa_decode_multi(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                                    _ptr(lengths), _ptr(cu_q), _ptr(slot_ids), _ptr(out), B, T, int(max_q_len),
+                                    Hq, Hkv, D, R, Smax, dt, _ptr(ws), ws.numel() * ws.element_size(),
+                                    _ptr(status), _stream(stream), ctypes.byref(o))
     _check(code, "gqa_decode_multi")
     return out
 
@@ -442,13 +447,14 @@ def decode_multi_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
               wait_limit_cycles, test_stall)
     lib = _lib.load()
-    need = lib.gqa_workspace_bytes_multi(B, Hq, Hkv, D, dt, int(max_q_len), ctypes.byref(o))
-    ws = _workspace(q.device, need, stream) if workspace is None else workspace
-    code = lib.gqa_decode_multi_paged(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_blocks), _ptr(v_blocks),
-                                      _ptr(block_table), _ptr(lengths), _ptr(cu_q), _ptr(out), B, T,
-                                      int(max_q_len), Hq, Hkv, D, NB, BS, block_table.shape[1], dt,
-                                      _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
-                                      _stream(stream), ctypes.byref(o))
+    with _on(q.device):
+        need = lib.gqa_workspace_bytes_multi(B, Hq, Hkv, D, dt, int(max_q_len), ctypes.byref(o))
+        ws = _workspace(q.device, need, stream) if workspace is None else workspace
+        code = lib.gqa_decode_multi_paged(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_blocks), _ptr(v_blocks),
+                                          _ptr(block_table), _ptr(lengths), _ptr(cu_q), _ptr(out), B, T,
+                                          int(max_q_len), Hq, Hkv, D, NB, BS, block_table.shape[1], dt,
+                                          _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
+                                          _stream(stream), ctypes.byref(o))
     _check(code, "gqa_decode_multi_paged")
     return out
 

@@ -570,7 +570,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane >> 2, t4 = lane & 3;
 
+    // the next kernel may be set up meanwhile (it waits for this one's end);
     // programmatic dependent of the previous kernel: read no input before it is done
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     schedule_walk(p, sched, &walk);
     // whole pages of 16 slots: one vector index a part; else slot by slot

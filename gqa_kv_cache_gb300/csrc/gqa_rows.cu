@@ -191,9 +191,18 @@ __device__ __forceinline__ void put16(void *cache, void *groups, long long off, 
         *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(cache) + off) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
         float amax = 0.f;
+        if constexpr (sizeof(T) == 2) {
+            // two at a time as they came (the signs get mixed up)
+            uint32_t m = w.u[0];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            amax = max_nan(amax, fabsf(x[i]));
+            for (int i = 1; i < 8; ++i)
+                asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w.u[i]));
+            amax = max_nan(fabsf(bf16_lo(m)), fabsf(bf16_hi(m)));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                amax = max_nan(amax, fabsf(x[i]));
+        }
         float t;
         const uint32_t s = group_scale(amax, g, t);
         *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + (off >> 1)) = e2m1_codes16(x, s, t);

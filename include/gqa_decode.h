@@ -401,10 +401,11 @@ gqa_status gqa_validate_multi(const int32_t *lengths, const int32_t *cu_q, const
  * Kernel timing trace. When enabled, every decode call records CUDA events
  * around the kernel it launches; gqa_trace_collect waits for them and
  * returns, per kernel kind, the launches and total milliseconds since the
- * previous collect. Kinds: 0 = SIMT decode, 1 = tensor-core decode, 2 = the
- * small-cache decode, 3 = the tcgen05 form of 17- to 32-row multi-token
+ * previous collect. Kinds: 0 = SIMT decode, 1 = tensor-core decode (over an
+ * E2M1 cache q4_decode_kernel), 2 = the small-cache decode, 3 = the tcgen05 form of 17- to 32-row multi-token
  * units (each decode step is exactly one kernel launch); gqa_kernel_name
- * gives each kind's kernel name. Meant for benchmarks.
+ * gives each kind's kernel name. append, read and block selection are not
+ * traced. Meant for benchmarks.
  */
 int gqa_trace_enable(int on);
 gqa_status gqa_trace_collect(int n_kinds, int64_t *launches, double *ms);

@@ -228,6 +228,43 @@ def test_bounds(layout, bs, dtype):
         assert torch.equal(l, lo) and torch.equal(h, hi), (b, j)
 
 
+@pytest.mark.parametrize("kind", ["e2m1", "bf16"])
+def test_wide_tokens_and_16_byte_alignment(kind):
+    """More scale groups a token than a CTA has threads; vectors and caches that
+    begin 16 bytes past a 32-byte boundary."""
+    c = Case(kind, "dense", [3, 0], [20, 5], 40, 128, 32, bs=16, seed=5, bounds=True)
+    c.append()
+    _check_bytes(c)
+    _check_bounds(c, {})
+    _check_read(c, torch.bfloat16, c.read())
+    c = Case(kind, "paged", [3, 0], [20, 40], 2, 64, 64, bs=16, seed=6, bounds=True)
+
+    def shifted(x):
+        n = 16 // x.element_size()
+        y = torch.empty(x.numel() + n, dtype=x.dtype, device="cuda")[n:].view(x.shape)
+        assert y.data_ptr() % 32 == 16
+        return y.copy_(x)
+    c.kv = [shifted(x) for x in c.kv]
+    x = [shifted(y) for y in c.x]
+    c.x = x
+    c.append()
+    c.x = [y.cpu() for y in x]
+    _check_bytes(c)
+    _check_bounds(c, {})
+    out = [shifted(torch.zeros(60, 2, 64, dtype=torch.bfloat16)) for _ in range(2)]
+    _check_read(c, torch.bfloat16, c.read(k_out=out[0], v_out=out[1]))
+
+
+def test_single_tokens_of_many_rows():
+    """One token a row, more rows than CTAs: every run its own block."""
+    B = 3000
+    c = Case("e2m1", "paged", [i % 48 for i in range(B)], [1] * B, 2, 64, 48, bs=16, seed=7, bounds=True)
+    c.append()
+    _check_bytes(c)
+    _check_bounds(c, {})
+    _check_read(c, torch.bfloat16, c.read())
+
+
 def test_special_values():
     """Zero groups, values that overflow the scale, infinities and NaN."""
     c = Case("e2m1", "dense", [0], [6], 1, 32, 8, dtype=torch.float32)

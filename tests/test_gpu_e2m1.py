@@ -251,6 +251,25 @@ def test_same_bits_twice_and_empty_batch():
     assert e.shape == (0, 8, 128)
 
 
+def test_typed_caches():
+    """The cache under torch's own 4-bit and 8-bit types gives the same bits."""
+    p = Problem("e2m1", "dense", [100, 33], 4, 2, 64, 128, seed=40)
+    t = _gpu(p)
+    want = _attend(p, t)
+    u = {**t, "kg": t["kg"].view(torch.float8_e4m3fn), "vg": t["vg"].view(torch.float8_e4m3fn)}
+    if hasattr(torch, "float4_e2m1fn_x2"):
+        u.update(k=t["k"].view(torch.float4_e2m1fn_x2), v=t["v"].view(torch.float4_e2m1fn_x2))
+    assert torch.equal(_attend(p, u), want)
+
+
+def test_many_short_rows():
+    """More units than CTAs, most of one tile; a few units a CTA in the copies at once."""
+    lens = [1 + (37 * i) % 150 for i in range(700)]
+    for D, q in ((128, torch.bfloat16), (64, torch.float32)):
+        p = Problem("e2m1", "slots", lens, 4, 2, D, 151, seed=41, q_dtype=q)
+        _check(p, _attend(p, _gpu(p)), rows=range(0, 700, 7))
+
+
 def test_refusals():
     import gqa_kv_cache_gb300 as gqa
     p = Problem("e2m1", "dense", [5], 8, 2, 128, 16, seed=31)
