@@ -247,7 +247,7 @@ def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False, gro
         raise TypeError("lengths must be a contiguous int32 tensor on q's device")
     shape = q.shape
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        out = torch.empty_like(q, dtype=torch.float32)
     elif out.shape != shape or out.dtype != torch.float32 or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be a contiguous float32 (B, Hq, D) tensor on q's device")
     return code, out

@@ -374,6 +374,11 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
     // about the time a CTA spends finishing a sequence, in tiles of streaming
     p.pad_tiles = (opt && opt->sched_pad > 0) ? opt->sched_pad - 1 : kDefaultSchedPad;
     p.grid = grid;
+    if (kv4 && opt->grid_ctas <= 0 && (long long)p.B * p.Hkv < INT_MAX &&
+        q4_whole_units(cap_rows, (long long)p.B * p.Hkv, grid)) {
+        p.whole_units = 1;
+        p.grid = p.B * p.Hkv;
+    }
     if (!unit) {
         char *w = static_cast<char *>(ws);
         p.ws_cnt = reinterpret_cast<int *>(w + lay.off_cnt);

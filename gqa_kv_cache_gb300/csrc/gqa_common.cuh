@@ -102,6 +102,7 @@ struct DecodeParams {
     void *k_group, *v_group;   // E4M3 scales, D / 16 a vector
     int scale_heads;           // > 0: row b's scales are those of head b % scale_heads (rows that are
                                // (batch row, cache head) pairs); 0: of head kvh
+    int whole_units;           // 1: CTA u computes unit u, whole (short caches; grid = B * Hkv)
 };
 
 // Workspace layout (bytes from the workspace base), shared by host and device.

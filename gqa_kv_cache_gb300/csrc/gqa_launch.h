@@ -44,6 +44,7 @@ cudaError_t unit_launch(const DecodeParams &p, bool bf16, long long cap_rows, in
 // Decode step and attend over an E2M1 cache (gqa_q4.cu): D = 64 or 128.
 bool q4_supports(int D, int G);
 int q4_tile();
+bool q4_whole_units(long long capacity, long long units, int grid);   // one CTA a unit
 int q4_ctas_per_sm(int D, bool q_bf16);   // resident CTAs per SM
 cudaError_t q4_launch(const DecodeParams &p, cudaStream_t st);
 

@@ -574,7 +574,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
     // programmatic dependent of the previous kernel: read no input before it is done
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    schedule_walk(p, sched, &walk);
+    if (!p.whole_units)
+        schedule_walk(p, sched, &walk);
     // whole pages of 16 slots: one vector index a part; else slot by slot
     const int shift = PAGED ? __ffs(p.block_size) - 1 : 0;
     const bool pages = !PAGED || (p.block_size >= 16 && (p.block_size & (p.block_size - 1)) == 0);
@@ -585,9 +586,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
     bool in_b = false, left;
     {
         TileCursor c;
-        left = walk_first(p, c, walk, in_b);
-        if (!left)
-            return;
+        if (p.whole_units) {
+            // this CTA's tiles are those of its unit, one segment
+            c = cursor_at(p, blockIdx.x / p.Hkv, 0, 0, 0);
+            c.kvh = blockIdx.x % p.Hkv;
+            c.end = c.nr;
+            left = true;
+        } else {
+            left = walk_first(p, c, walk, in_b);
+            if (!left)
+                return;
+        }
         enter<D, QF32>(p, c, f, &segs[0], &sm_bad[warp][0], sm_q[0], shift, pages, warp, lane);
         __syncwarp();
     }
@@ -606,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
                 TileCursor c = segs[sf].c;
                 c.g += f.t - c.t;
                 c.t = f.t;
-                left = walk_next(p, c, walk, in_b);
+                left = !p.whole_units && walk_next(p, c, walk, in_b);
                 if (left) {
                     sf = (sf + 1) % kSegs;
                     enter<D, QF32>(p, c, f, &segs[sf], &sm_bad[warp][sf], sm_q[sf], shift, pages, warp, lane);
@@ -839,6 +848,18 @@ cudaError_t launch(int D, bool q_bf16, bool paged, const DecodeParams *p, cudaSt
 bool q4_supports(int D, int G) { return (D == 64 || D == 128) && G >= 1 && G <= kRows; }
 
 int q4_tile() { return kTile4; }
+
+// One CTA a unit, whole, where units are short: no schedule to assemble, no
+// partial states to merge. Measured back to back (G = 4, D = 128, bfloat16
+// query; one CTA a unit / the schedule, us): capacity 256: 8 units 5.7 / 9.6,
+// 512 units 13.7 / 16.6, 2048 units 34.6 / 36.2; 512: 7.5 / 10.6, 19.3 / 20.6,
+// 52.8 / 53.4; 1024: 10.9 / 11.5, 26.9 / 28.4, 80.2 / 84.3, but 512 units with
+// cold caches 43 / 39; 2048: 17.6 / 12.9, 46.9 / 45.2. So: up to four tiles, or
+// eight where all units run at once.
+bool q4_whole_units(long long capacity, long long units, int grid)
+{
+    return capacity <= 4 * kTile4 || (capacity <= 8 * kTile4 && units <= grid);
+}
 
 int q4_ctas_per_sm(int D, bool q_bf16)
 {

@@ -57,7 +57,8 @@ def test_attend(layout, D, Hq, Hkv, q_dtype):
     t = _gpu(p)
     keep = {n: x.clone() for n, x in t.items()}
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
-    _check(p, _attend(p, t, status=st))
+    _check(p, _attend(p, t, status=st))               # one CTA a unit
+    _check(p, _attend(p, t, status=st, grid_ctas=11))  # units cut by CTAs
     assert int(st) == 0
     for n in keep:
         assert torch.equal(keep[n], t[n]), f"{n} written by a read-only attend"
@@ -77,12 +78,15 @@ def test_cut_units(grid):
 @pytest.mark.parametrize("bs", [1, 5, 8, 16, 24, 32, 128, 256])
 def test_page_sizes(bs):
     p = Problem("e2m1", "paged", [1, 7, 8, 200, 255, 256], 6, 2, 128, 512, bs=bs, seed=bs)
-    _check(p, _attend(p, _gpu(p)))
+    t = _gpu(p)
+    _check(p, _attend(p, t))
+    _check(p, _attend(p, t, grid_ctas=5))
 
 
+@pytest.mark.parametrize("grid", [0, 6])
 @pytest.mark.parametrize("layout", ["dense", "slots", "paged"])
 @pytest.mark.parametrize("D", [64, 128])
-def test_decode_step_appends(layout, D):
+def test_decode_step_appends(layout, D, grid):
     """The appended token's bytes are the format's, and it is attended as stored."""
     lens = [0, 1, 15, 16, 127, 128, 300]
     p = Problem("e2m1", layout, lens, 8, 2, D, 320, seed=9, extra=1)
@@ -90,7 +94,7 @@ def test_decode_step_appends(layout, D):
     kn, vn = (torch.randn(p.B, 2, D, generator=gen).bfloat16() for _ in range(2))
     t = _gpu(p)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
-    got = _decode(p, t, kn.cuda(), vn.cuda(), status=st).double().cpu()
+    got = _decode(p, t, kn.cuda(), vn.cuda(), status=st, grid_ctas=grid).double().cpu()
     assert int(st) == 0
     for i, x in enumerate((kn, vn)):
         c, s, _, _ = quantise_e2m1(x, p.g[i].view(-1, 1))
@@ -110,7 +114,8 @@ def test_window_prefix_and_sink():
     sink = torch.randn(8, generator=torch.Generator().manual_seed(2))
     for window, prefix in ((1, 0), (60, 0), (130, 37), (40, 300), (2000, 4)):
         slots = [[[j for j in range(n) if j > n - 1 - window or j < prefix]] * 2 for n in p.lens]
-        _check(p, _attend(p, t, window=window, kept_prefix=prefix, sink=sink.cuda()), slots, sink)
+        for grid in (0, 13):
+            _check(p, _attend(p, t, window=window, kept_prefix=prefix, sink=sink.cuda(), grid_ctas=grid), slots, sink)
     pp = Problem("e2m1", "paged", [5, 100, 400, 900], 8, 2, 64, 912, seed=12)
     tt = _gpu(pp)
     slots = [[[j for j in range(n) if j > n - 1 - 100 or j < 20]] * 2 for n in pp.lens]
@@ -267,7 +272,9 @@ def test_many_short_rows():
     lens = [1 + (37 * i) % 150 for i in range(700)]
     for D, q in ((128, torch.bfloat16), (64, torch.float32)):
         p = Problem("e2m1", "slots", lens, 4, 2, D, 151, seed=41, q_dtype=q)
-        _check(p, _attend(p, _gpu(p)), rows=range(0, 700, 7))
+        t = _gpu(p)
+        _check(p, _attend(p, t), rows=range(0, 700, 7))
+        _check(p, _attend(p, t, grid_ctas=300), rows=range(0, 700, 7))
 
 
 def test_refusals():
