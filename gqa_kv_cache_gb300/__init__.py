@@ -84,6 +84,12 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _head_scale(name, t, Hkv, device):
+    if t.dtype != torch.float32 or t.shape != (Hkv,) or not t.is_contiguous() or t.get_device() != device.index:
+        raise TypeError(f"{name} must be a contiguous float32 (Hkv,) tensor on q's device")
+    return t.data_ptr()
+
+
 def _opts(kernel, grid_ctas, sched_pad=None, sink=None, window=0, kept_prefix=0, device=None, B=None,
           Hq=None, k_scale=None, v_scale=None, Hkv=None, wait_limit_cycles=0, test_stall=False,
           k_group_scale=None, v_group_scale=None):
@@ -118,12 +124,10 @@ def _opts(kernel, grid_ctas, sched_pad=None, sink=None, window=0, kept_prefix=0,
         o.kept_prefix_rows = kept_prefix.data_ptr()
     elif kept_prefix:
         o.kept_prefix = int(kept_prefix)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is None:
-            continue
-        if t.dtype != torch.float32 or t.shape != (Hkv,) or not t.is_contiguous() or t.device != device:
-            raise TypeError(f"{name} must be a contiguous float32 (Hkv,) tensor on q's device")
-        setattr(o, name, t.data_ptr())
+    if k_scale is not None:
+        o.k_scale = _head_scale("k_scale", k_scale, Hkv, device)
+    if v_scale is not None:
+        o.v_scale = _head_scale("v_scale", v_scale, Hkv, device)
     if k_group_scale is not None:
         o.k_group_scale = k_group_scale.data_ptr()
         o.v_group_scale = v_group_scale.data_ptr()
@@ -164,6 +168,18 @@ def _workspace(device, nbytes, stream=None):
     return buf
 
 
+_need_cache: dict = {}
+
+
+def _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, device):
+    """gqa_workspace_bytes of these sizes on this device (asked once)."""
+    key = (B, Hq, Hkv, D, dt, kernel, grid_ctas, device.index)
+    n = _need_cache.get(key)
+    if n is None:
+        n = _need_cache[key] = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
+    return n
+
+
 def _on(device):
     """The device as the current one, where it is not."""
     if device.index == torch.cuda.current_device():
@@ -184,16 +200,21 @@ def workspace_bytes(B, Hq, Hkv, D, dtype=torch.bfloat16, kernel="auto", grid_cta
 
 def _group_scales(caches, k_group_scale, v_group_scale, D):
     """Checks of an E2M1 cache's tensors (the shapes against D dims a vector)."""
-    for (name, c), (gname, t) in zip(caches, (("k_group_scale", k_group_scale), ("v_group_scale", v_group_scale))):
-        if c.dtype not in _NIBBLE_DTYPES:
-            raise TypeError(f"{name} with group scales must hold E2M1 pairs (uint8 or float4_e2m1fn_x2)")
-        if t is None or t.dtype not in _BYTE_DTYPES:
-            raise TypeError("k_group_scale and v_group_scale must both be E4M3 bytes (uint8 or float8_e4m3fn)")
-        a, b, n, d = c.shape
-        if D % _GROUP or d * 2 != D or t.shape != (a, b, n, D // _GROUP):
-            raise ValueError(f"{name} must hold D // 2 bytes and {gname} D // {_GROUP} scales a vector, D = {D}")
-        if t.get_device() != c.get_device() or not t.is_contiguous():
-            raise ValueError(f"{gname} must be contiguous and on the cache's device")
+    (kname, k), (vname, v) = caches
+    if k.dtype not in _NIBBLE_DTYPES or v.dtype not in _NIBBLE_DTYPES:
+        raise TypeError(f"{kname} and {vname} with group scales must hold E2M1 pairs (uint8 or float4_e2m1fn_x2)")
+    if k_group_scale is None or v_group_scale is None or k_group_scale.dtype not in _BYTE_DTYPES \
+            or v_group_scale.dtype not in _BYTE_DTYPES:
+        raise TypeError("k_group_scale and v_group_scale must both be E4M3 bytes (uint8 or float8_e4m3fn)")
+    shape = k.shape
+    groups = (*shape[:-1], D // _GROUP)
+    if D % _GROUP or shape[-1] * 2 != D or v.shape != shape or k_group_scale.shape != groups \
+            or v_group_scale.shape != groups:
+        raise ValueError(f"{kname} and {vname} must hold D // 2 bytes a vector and the group scales D // {_GROUP}, D = {D}")
+    dev = k.get_device()
+    if k_group_scale.get_device() != dev or v_group_scale.get_device() != dev \
+            or not k_group_scale.is_contiguous() or not v_group_scale.is_contiguous():
+        raise ValueError("the group scales must be contiguous and on the caches' device")
 
 
 def _row_checks(lengths, slot_ids, block_table, B, dev):
@@ -278,7 +299,7 @@ def decode_step(q, k_new, v_new, k_cache, v_cache, lengths, slot_ids=None, *, ou
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
     with _on(q.device):
-        need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
+        need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, q.device)
         ws = _workspace(q.device, need, stream) if workspace is None else workspace
         code = lib.gqa_decode_step_ex(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
                                       _ptr(lengths), _ptr(slot_ids), _ptr(out), B, Hq, Hkv, D, R, Smax,
@@ -312,7 +333,7 @@ def decode_step_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths,
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
     with _on(q.device):
-        need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
+        need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, q.device)
         ws = _workspace(q.device, need, stream) if workspace is None else workspace
         code = lib.gqa_decode_step_paged_ex(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_blocks),
                                             _ptr(v_blocks), _ptr(block_table), _ptr(lengths), _ptr(out),
@@ -345,7 +366,7 @@ def attend(q, k_cache, v_cache, lengths, slot_ids=None, *, out=None, status=None
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
     with _on(q.device):
-        need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
+        need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, q.device)
         ws = _workspace(q.device, need, stream) if workspace is None else workspace
         code = lib.gqa_attend(_ptr(q), _DTYPES[q.dtype], _ptr(k_cache), _ptr(v_cache), _ptr(lengths),
                               _ptr(slot_ids), _ptr(out), B, Hq, Hkv, D, R, Smax, dt, _ptr(ws),
@@ -377,7 +398,7 @@ def attend_paged(q, k_blocks, v_blocks, block_table, lengths, *, out=None, statu
               wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
     lib = _lib.load()
     with _on(q.device):
-        need = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
+        need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, q.device)
         ws = _workspace(q.device, need, stream) if workspace is None else workspace
         code = lib.gqa_attend_paged(_ptr(q), _DTYPES[q.dtype], _ptr(k_blocks), _ptr(v_blocks),
                                     _ptr(block_table), _ptr(lengths), _ptr(out), B, Hq, Hkv, D, NB, BS,
@@ -461,6 +482,11 @@ def decode_multi_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths
 
 # ---- writing and reading a cache, block selection ----
 
+def _int32(name, t, n, dev):
+    if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != dev:
+        raise TypeError(f"{name} must be a contiguous int32 ({n},) tensor on the other tensors' device")
+
+
 def _rows_checks(caches, lengths, cu_q, slot_ids, block_table, groups, D):
     """Checks shared by append and read; returns the cache's gqa_dtype."""
     (_, k), (_, v) = caches
@@ -479,10 +505,10 @@ def _rows_checks(caches, lengths, cu_q, slot_ids, block_table, groups, D):
         if k.shape[-1] != D:
             raise ValueError("shape mismatch between the vectors and the caches")
     B = lengths.shape[0]
-    for name, t, shape in (("lengths", lengths, (B,)), ("cu_q", cu_q, (B + 1,)), ("slot_ids", slot_ids, (B,))):
-        if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()
-                              or t.get_device() != dev):
-            raise TypeError(f"{name} must be a contiguous int32 {shape} tensor on the caches' device")
+    _int32("lengths", lengths, B, dev)
+    _int32("cu_q", cu_q, B + 1, dev)
+    if slot_ids is not None:
+        _int32("slot_ids", slot_ids, B, dev)
     if block_table is not None and (block_table.dtype != torch.int32 or block_table.dim() != 2
                                     or block_table.shape[0] != B or not block_table.is_contiguous()
                                     or block_table.get_device() != dev):
@@ -577,12 +603,13 @@ def _read(k, v, block_table, lengths, cu_q, T, slot_ids, dtype, k_out, v_out, sc
     dev = k.get_device()
     n0, Hkv, n2, _ = k.shape
     T, shape = int(T), (int(T), Hkv, D)
-    with torch.cuda.stream(stream) if stream is not None else _HERE:
-        k_out = torch.empty(shape, dtype=dtype, device=k.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=dtype, device=k.device) if v_out is None else v_out
     for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor on the caches' device")
+    if k_out is None or v_out is None:
+        with torch.cuda.stream(stream) if stream is not None else _HERE:
+            k_out = torch.empty(shape, dtype=dtype, device=k.device) if k_out is None else k_out
+            v_out = torch.empty(shape, dtype=dtype, device=k.device) if v_out is None else v_out
     o = _rows_opts(code, Hkv, k.device, *scales, groups)
     lib = _lib.load()
     B = lengths.shape[0]
@@ -664,10 +691,9 @@ def _select(q, k_bounds, block_table, lengths, n_select, slot_ids, block_size, n
     for name, t in (("q", q), ("k_bounds", k_bounds)):
         if t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous and on q's device")
-    for name, t, shape in (("lengths", lengths, (B,)), ("slot_ids", slot_ids, (B,))):
-        if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()
-                              or t.get_device() != dev):
-            raise TypeError(f"{name} must be a contiguous int32 {shape} tensor on q's device")
+    _int32("lengths", lengths, B, dev)
+    if slot_ids is not None:
+        _int32("slot_ids", slot_ids, B, dev)
     if block_table is not None and (block_table.dtype != torch.int32 or block_table.dim() != 2
                                     or block_table.shape[0] != B or not block_table.is_contiguous()
                                     or block_table.get_device() != dev):
@@ -741,17 +767,17 @@ def attend_selected(q, k_cache, v_cache, selection, *, out=None, status=None, ke
             or Hq % Hkv or n2 % sel.block_size:
         raise ValueError("shape mismatch between q, the caches and the selection")
     _status_checks(status, q.device)
-    o = ctypes.byref(_opts(kernel, grid_ctas, sched_pad, device=q.device, k_scale=k_scale, v_scale=v_scale, Hkv=Hkv,
-                           k_group_scale=k_group_scale, v_group_scale=v_group_scale))
+    o = _opts(kernel, grid_ctas, sched_pad, device=q.device, k_scale=k_scale, v_scale=v_scale, Hkv=Hkv,
+              k_group_scale=k_group_scale, v_group_scale=v_group_scale)
     lib = _lib.load()
     _, table, slots = sel._ptrs()
     with _on(q.device):
-        need = lib.gqa_workspace_bytes(B * Hkv, Hq // Hkv, 1, D, dt, o)
+        need = _need(lib, B * Hkv, Hq // Hkv, 1, D, dt, kernel, grid_ctas, o, q.device)
         ws = _workspace(q.device, need, stream) if workspace is None else workspace
         rc = lib.gqa_attend_selected(_ptr(q), _DTYPES[q.dtype], _ptr(k_cache), _ptr(v_cache), table, slots, _ptr(out),
                                      B, Hq, Hkv, D, n0 * Hkv * (n2 // sel.block_size), sel.block_size, sel.n_select,
                                      dt, _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
-                                     _stream(stream, q.device), o)
+                                     _stream(stream, q.device), ctypes.byref(o))
     _check(rc, "gqa_attend_selected")
     return out
 
