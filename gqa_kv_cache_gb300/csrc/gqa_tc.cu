@@ -33,6 +33,8 @@ cudaError_t tc_launch(const DecodeParams &p, const TcMaps &maps, cudaStream_t st
                        : launch_q<false, false, false, true>(p, maps, st);
         return win ? launch_q<true, true, false, true>(p, maps, st) : launch_q<true, false, false, true>(p, maps, st);
     }
+    if (p.scale_heads)   // the attend over selected blocks
+        return tc_launch_fine(p, maps, st);
     if (p.q_bf16)
         return win ? launch_q<false, true, false>(p, maps, st) : launch_q<false, false, false>(p, maps, st);
     return win ? launch_q<true, true, false>(p, maps, st) : launch_q<true, false, false>(p, maps, st);

@@ -344,6 +344,14 @@ __device__ __forceinline__ void split_bf16(float2 v, uint32_t &hi, uint32_t &lo)
     lo = pack_bf16(v.x - __uint_as_float(hi << 16), v.y - __uint_as_float(hi & 0xffff0000u));
 }
 
+// A float32 pair as three bf16 parts: v = hi + mid + lo to 24 bits.
+__device__ __forceinline__ void split3_bf16(float2 v, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+{
+    hi = pack_bf16(v.x, v.y);
+    const float2 r = make_float2(v.x - __uint_as_float(hi << 16), v.y - __uint_as_float(hi & 0xffff0000u));
+    split_bf16(r, mid, lo);
+}
+
 // Byte offset, within one 64-element half, of 16-byte chunk c8 of row r
 // under the 128-byte swizzle (the half starts on a 1024-byte boundary).
 __device__ __forceinline__ uint32_t swz(int r, int c8) { return (uint32_t)(r * 128 + ((c8 ^ (r & 7)) << 4)); }
@@ -553,8 +561,12 @@ __device__ __forceinline__ void pair_sync(int pr)
 // an E4M3 cache. MR: multi-token units of 9 to 16 (MR = 16) or of 17 to 32
 // (MR = 32) query rows, which keep the rows on the M = 16 side of the
 // products; units of up to 8 rows (and every single-token unit, MR = 0) put
-// them on the N = 8 side.
-template <bool QF32, bool WIN, bool MULTI, bool KV8, int MR>
+// them on the N = 8 side. FINE (single tokens over a bfloat16 cache): the
+// weights enter as three bfloat16 parts, all 24 bits, in a third product. The
+// attend over selected blocks takes it: 64 of 2048 blocks of 64 slots against
+// 64 bits, relative error 1.5e-6 with two parts, at the same time (28.7 us:
+// the kernel waits for memory and its start, not for the products).
+template <bool QF32, bool WIN, bool MULTI, bool KV8, int MR, bool FINE>
 __global__ void __launch_bounds__((Ring<QF32, KV8, MULTI, MR>::kThreads), (Ring<QF32, KV8, MULTI, MR>::kCtas))
     tc_decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mk16,
@@ -1366,7 +1378,15 @@ __global__ void __launch_bounds__((Ring<QF32, KV8, MULTI, MR>::kThreads), (Ring<
                 // result does not depend on the split of a unit beyond float32
                 // rounding; over an E4M3 cache as f16 (11 bits).
                 uint32_t ph0, ph1, pl0 = 0u, pl1 = 0u;
-                if constexpr (KV8) {
+                [[maybe_unused]] uint32_t pt0 = 0u, pt1 = 0u;   // FINE: the third parts
+                if constexpr (FINE) {
+                    split3_bf16(make_float2(p00, p10), ph0, pl0, pt0);
+                    split3_bf16(make_float2(p01, p11), ph1, pl1, pt1);
+                    pl0 = movmatrix_t(pl0);
+                    pl1 = movmatrix_t(pl1);
+                    pt0 = movmatrix_t(pt0);
+                    pt1 = movmatrix_t(pt1);
+                } else if constexpr (KV8) {
                     ph0 = pack_f16(p00, p10);
                     ph1 = pack_f16(p01, p11);
                 } else {
@@ -1409,6 +1429,8 @@ __global__ void __launch_bounds__((Ring<QF32, KV8, MULTI, MR>::kThreads), (Ring<
                             ldsm_x4_t(vbase + (c >> 3) * kHalfBytes + swz(r, c & 7), vb);
                             mma_bf16(acc_o[mt], vb[0], vb[2], vb[1], vb[3], pb0, pb1);
                             mma_bf16(acc_o[mt], vb[0], vb[2], vb[1], vb[3], pl0, pl1);   // the remainders
+                            if constexpr (FINE)
+                                mma_bf16(acc_o[mt], vb[0], vb[2], vb[1], vb[3], pt0, pt1);
                         }
                     }
                 }
@@ -1661,7 +1683,7 @@ __global__ void __launch_bounds__((Ring<QF32, KV8, MULTI, MR>::kThreads), (Ring<
 }
 
 
-template <bool QF32, bool WIN, bool MULTI, bool KV8 = false, int MR = 0>
+template <bool QF32, bool WIN, bool MULTI, bool KV8 = false, int MR = 0, bool FINE = false>
 cudaError_t launch_q(const DecodeParams &p, const TcMaps &maps, cudaStream_t st)
 {
     constexpr int kDynSmem = Ring<QF32, KV8, MULTI, MR>::kDynSmem;
@@ -1675,7 +1697,7 @@ cudaError_t launch_q(const DecodeParams &p, const TcMaps &maps, cudaStream_t st)
         return e;
     const unsigned long long bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
     if (!bit || !(attr_set.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(tc_decode_kernel<QF32, WIN, MULTI, KV8, MR>,
+        e = cudaFuncSetAttribute(tc_decode_kernel<QF32, WIN, MULTI, KV8, MR, FINE>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmem);
         if (e != cudaSuccess)
             return e;
@@ -1691,7 +1713,7 @@ cudaError_t launch_q(const DecodeParams &p, const TcMaps &maps, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tc_decode_kernel<QF32, WIN, MULTI, KV8, MR>, p, maps.k, maps.v, maps.k16,
+    return cudaLaunchKernelEx(&cfg, tc_decode_kernel<QF32, WIN, MULTI, KV8, MR, FINE>, p, maps.k, maps.v, maps.k16,
                               maps.v16);
 }
 
@@ -1701,5 +1723,7 @@ cudaError_t launch_q(const DecodeParams &p, const TcMaps &maps, cudaStream_t st)
 // (gqa_tc.cu, compiled without the multi-token schedule code) and the
 // multi-token kernels (gqa_tc_multi.cu).
 cudaError_t tc_launch_multi(const DecodeParams &p, const TcMaps &maps, cudaStream_t st);
+// The FINE form (gqa_tc_fine.cu): no window.
+cudaError_t tc_launch_fine(const DecodeParams &p, const TcMaps &maps, cudaStream_t st);
 
 }  // namespace gqa
