@@ -217,16 +217,84 @@ def _group_scales(caches, k_group_scale, v_group_scale, D):
         raise ValueError("the group scales must be contiguous and on the caches' device")
 
 
-def _row_checks(lengths, slot_ids, block_table, B, dev):
-    """Checks of the per-row tensors of a call over an E2M1 cache."""
-    if lengths.shape != (B,):
-        raise ValueError("lengths must be of shape (B,)")
-    for name, t in (("slot_ids", slot_ids), ("block_table", block_table)):
+def _plain(dev, *tensors):
+    """Raises unless every tensor given is contiguous and on device `dev`."""
+    for t in tensors:
         if t is not None and (t.get_device() != dev or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous and on q's device")
+            raise ValueError("every tensor must be contiguous and on q's device")
 
 
-def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False, groups=None):
+def _check_e2m1(q, k, v, kg, vg, out):
+    """Checks of a query and a 4-bit cache; returns (device index, out)."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if q.dtype not in _DTYPES:
+        raise TypeError("q must be float32 or bfloat16")
+    _group_scales((("the key cache", k), ("the value cache", v)), kg, vg, q.shape[2])
+    _plain(dev, q, k, v, out)
+    if out is None:
+        out = torch.empty_like(q, dtype=torch.float32)
+    elif out.shape != q.shape or out.dtype != torch.float32:
+        raise ValueError("out must be a contiguous float32 (B, Hq, D) tensor on q's device")
+    return dev, out
+
+
+def _step_e2m1(q, k_new, v_new, k, v, lengths, slot_ids, table, k_scale, v_scale, kg, vg, out, status, kernel,
+               grid_ctas, workspace, stream, sched_pad, sink, window, kept_prefix):
+    """The decode step (k_new, v_new given) or the attend over a 4-bit cache,
+    dense or paged (table given). Written out for itself: the step is short,
+    and its time on the host counts."""
+    dev, out = _check_e2m1(q, k, v, kg, vg, out)
+    B, Hq, D = q.shape
+    n0, Hkv, n2, _ = k.shape
+    if Hq % Hkv or lengths.shape != (B,):
+        raise ValueError("shape mismatch between q, the caches and lengths")
+    if lengths.dtype != torch.int32:
+        raise TypeError("lengths must be a contiguous int32 tensor on q's device")
+    if slot_ids is not None and (slot_ids.dtype != torch.int32 or slot_ids.shape != (B,)):
+        raise TypeError("slot_ids must be int32 of shape (B,)")
+    if table is not None and (table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B):
+        raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor")
+    _plain(dev, lengths, slot_ids, table, k_new, v_new)
+    if k_new is not None:
+        if q.dtype != torch.bfloat16 or k_new.dtype != torch.bfloat16 or v_new.dtype != torch.bfloat16:
+            raise TypeError("over an E2M1 cache q, k_new and v_new are bfloat16")
+        if k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D):
+            raise ValueError("shape mismatch between q, k_new and v_new")
+    device = q.device
+    o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, device, B, Hq, k_scale, v_scale, Hkv,
+              k_group_scale=kg, v_group_scale=vg)
+    lib = _lib.load()
+    with _on(device):
+        need = _need(lib, B, Hq, Hkv, D, E2M1, kernel, grid_ctas, o, device)
+        ws = _workspace(device, need, stream) if workspace is None else workspace
+        at, size, st = ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(status)
+        if table is None:
+            if k_new is None:
+                what, code = "gqa_attend", lib.gqa_attend(
+                    q.data_ptr(), _DTYPES[q.dtype], k.data_ptr(), v.data_ptr(), lengths.data_ptr(), _ptr(slot_ids),
+                    out.data_ptr(), B, Hq, Hkv, D, n0, n2, E2M1, at, size, st, _stream(stream), ctypes.byref(o))
+            else:
+                what, code = "gqa_decode_step", lib.gqa_decode_step_ex(
+                    q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k.data_ptr(), v.data_ptr(), lengths.data_ptr(),
+                    _ptr(slot_ids), out.data_ptr(), B, Hq, Hkv, D, n0, n2, E2M1, at, size, st, _stream(stream),
+                    ctypes.byref(o))
+        elif k_new is None:
+            what, code = "gqa_attend_paged", lib.gqa_attend_paged(
+                q.data_ptr(), _DTYPES[q.dtype], k.data_ptr(), v.data_ptr(), table.data_ptr(), lengths.data_ptr(),
+                out.data_ptr(), B, Hq, Hkv, D, n0, n2, table.shape[1], E2M1, at, size, st, _stream(stream),
+                ctypes.byref(o))
+        else:
+            what, code = "gqa_decode_step_paged", lib.gqa_decode_step_paged_ex(
+                q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k.data_ptr(), v.data_ptr(), table.data_ptr(),
+                lengths.data_ptr(), out.data_ptr(), B, Hq, Hkv, D, n0, n2, table.shape[1], E2M1, at, size, st,
+                _stream(stream), ctypes.byref(o))
+    _check(code, what)
+    return out
+
+
+def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False):
     """Checks shared by the entry points; returns (cache gqa_dtype, out). The
     query and the new keys / values share the cache dtype, except over an E4M3
     cache (bfloat16 then; the attend's query is free)."""
@@ -236,14 +304,10 @@ def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False, gro
     qt = q.dtype
     if qt not in _DTYPES:
         raise TypeError("q must be float32 or bfloat16")
-    if groups is not None and (groups[0] is not None or groups[1] is not None):
-        _group_scales(caches, *groups, q.shape[-1])
-        code = E2M1
-    else:
-        code = _cache_code(caches[0][1])
-    if code >= E4M3:
+    code = _cache_code(caches[0][1])
+    if code == E4M3:
         if not q_any_dtype and qt != torch.bfloat16:
-            raise TypeError("over an E4M3 or E2M1 cache q, k_new and v_new are bfloat16")
+            raise TypeError("over an E4M3 cache q, k_new and v_new are bfloat16")
         new_dt = torch.bfloat16
     else:
         dt = caches[0][1].dtype if q_any_dtype else qt
@@ -284,19 +348,21 @@ def decode_step(q, k_new, v_new, k_cache, v_cache, lengths, slot_ids=None, *, ou
     ``workspace`` passed in must be zero-filled before its first use (the
     library leaves it zero-filled after every call). ``sink``, ``window`` and
     ``kept_prefix`` are the softmax modifiers of the C header's gqa_options."""
+    if k_group_scale is not None or v_group_scale is not None:   # a 4-bit cache
+        return _step_e2m1(q, k_new, v_new, k_cache, v_cache, lengths, slot_ids, None, k_scale, v_scale, k_group_scale,
+                          v_group_scale, out, status, kernel, grid_ctas, workspace, stream, sched_pad, sink, window,
+                          kept_prefix)
     dt, out = _common_checks(q, k_new, v_new, (("k_cache", k_cache), ("v_cache", v_cache)),
-                             lengths, out, groups=(k_group_scale, v_group_scale))
+                             lengths, out)
     B, Hq, D = q.shape
     R, Hkv, Smax, D2 = k_cache.shape
-    if (D2 * 2 if dt == E2M1 else D2) != D or v_cache.shape != k_cache.shape or k_new.shape != (B, Hkv, D) \
+    if D2 != D or v_cache.shape != k_cache.shape or k_new.shape != (B, Hkv, D) \
             or v_new.shape != (B, Hkv, D):
         raise ValueError("shape mismatch between q, k_new, v_new and the caches")
     if slot_ids is not None and (slot_ids.dtype != torch.int32 or slot_ids.shape != (B,)):
         raise TypeError("slot_ids must be int32 of shape (B,)")
-    if dt == E2M1:
-        _row_checks(lengths, slot_ids, None, B, q.get_device())
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
-              wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
+              wait_limit_cycles, test_stall)
     lib = _lib.load()
     with _on(q.device):
         need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, q.device)
@@ -316,21 +382,23 @@ def decode_step_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths,
                       v_group_scale=None):
     """One decode step on a paged cache (num_blocks, Hkv, block_size, D) with
     a (B, max_blocks) int32 block table (-1 = unused). Appends in place."""
+    if k_group_scale is not None or v_group_scale is not None:   # a 4-bit cache
+        return _step_e2m1(q, k_new, v_new, k_blocks, v_blocks, lengths, None, block_table, k_scale, v_scale, k_group_scale,
+                          v_group_scale, out, status, kernel, grid_ctas, workspace, stream, sched_pad, sink, window,
+                          kept_prefix)
     dt, out = _common_checks(q, k_new, v_new, (("k_blocks", k_blocks), ("v_blocks", v_blocks)),
-                             lengths, out, groups=(k_group_scale, v_group_scale))
+                             lengths, out)
     B, Hq, D = q.shape
     NB, Hkv, BS, D2 = k_blocks.shape
-    if (D2 * 2 if dt == E2M1 else D2) != D or v_blocks.shape != k_blocks.shape or k_new.shape != (B, Hkv, D) \
+    if D2 != D or v_blocks.shape != k_blocks.shape or k_new.shape != (B, Hkv, D) \
             or v_new.shape != (B, Hkv, D):
         raise ValueError("shape mismatch between q, k_new, v_new and the blocks")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
             or not block_table.is_contiguous():
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor")
     MB = block_table.shape[1]
-    if dt == E2M1:
-        _row_checks(lengths, None, block_table, B, q.get_device())
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
-              wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
+              wait_limit_cycles, test_stall)
     lib = _lib.load()
     with _on(q.device):
         need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, q.device)
@@ -351,19 +419,20 @@ def attend(q, k_cache, v_cache, lengths, slot_ids=None, *, out=None, status=None
     """Read-only attend on a dense (R, Hkv, Smax, D) cache: slots
     ``0..lengths[b]-1`` (1 <= lengths[b] <= Smax), nothing written but ``out``.
     ``q`` (B, Hq, D) is float32 or bfloat16 whatever the cache dtype."""
+    if k_group_scale is not None or v_group_scale is not None:   # a 4-bit cache
+        return _step_e2m1(q, None, None, k_cache, v_cache, lengths, slot_ids, None, k_scale, v_scale, k_group_scale,
+                          v_group_scale, out, status, kernel, grid_ctas, workspace, stream, sched_pad, sink, window,
+                          kept_prefix)
     dt, out = _common_checks(q, None, None, (("k_cache", k_cache), ("v_cache", v_cache)),
-                             lengths, out, q_any_dtype=True,
-                             groups=(k_group_scale, v_group_scale))
+                             lengths, out, q_any_dtype=True)
     B, Hq, D = q.shape
     R, Hkv, Smax, D2 = k_cache.shape
-    if (D2 * 2 if dt == E2M1 else D2) != D or v_cache.shape != k_cache.shape or Hq % Hkv:
+    if D2 != D or v_cache.shape != k_cache.shape or Hq % Hkv:
         raise ValueError("shape mismatch between q and the caches")
     if slot_ids is not None and (slot_ids.dtype != torch.int32 or slot_ids.shape != (B,)):
         raise TypeError("slot_ids must be int32 of shape (B,)")
-    if dt == E2M1:
-        _row_checks(lengths, slot_ids, None, B, q.get_device())
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
-              wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
+              wait_limit_cycles, test_stall)
     lib = _lib.load()
     with _on(q.device):
         need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, q.device)
@@ -382,20 +451,21 @@ def attend_paged(q, k_blocks, v_blocks, block_table, lengths, *, out=None, statu
                 wait_limit_cycles=0, test_stall=False, k_group_scale=None,
                  v_group_scale=None):
     """Read-only attend on a paged cache (num_blocks, Hkv, block_size, D)."""
+    if k_group_scale is not None or v_group_scale is not None:   # a 4-bit cache
+        return _step_e2m1(q, None, None, k_blocks, v_blocks, lengths, None, block_table, k_scale, v_scale, k_group_scale,
+                          v_group_scale, out, status, kernel, grid_ctas, workspace, stream, sched_pad, sink, window,
+                          kept_prefix)
     dt, out = _common_checks(q, None, None, (("k_blocks", k_blocks), ("v_blocks", v_blocks)),
-                             lengths, out, q_any_dtype=True,
-                             groups=(k_group_scale, v_group_scale))
+                             lengths, out, q_any_dtype=True)
     B, Hq, D = q.shape
     NB, Hkv, BS, D2 = k_blocks.shape
-    if (D2 * 2 if dt == E2M1 else D2) != D or v_blocks.shape != k_blocks.shape or Hq % Hkv:
+    if D2 != D or v_blocks.shape != k_blocks.shape or Hq % Hkv:
         raise ValueError("shape mismatch between q and the blocks")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
             or not block_table.is_contiguous():
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor")
-    if dt == E2M1:
-        _row_checks(lengths, None, block_table, B, q.get_device())
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, q.device, B, Hq, k_scale, v_scale, Hkv,
-              wait_limit_cycles, test_stall, k_group_scale, v_group_scale)
+              wait_limit_cycles, test_stall)
     lib = _lib.load()
     with _on(q.device):
         need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, q.device)
@@ -759,8 +829,13 @@ def attend_selected(q, k_cache, v_cache, selection, *, out=None, status=None, ke
         with torch.cuda.stream(stream):
             out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
     sel = selection
-    dt, out = _common_checks(q, None, None, (("k_cache", k_cache), ("v_cache", v_cache)), sel._buf, out,
-                             q_any_dtype=True, groups=(k_group_scale, v_group_scale))
+    if k_group_scale is not None or v_group_scale is not None:
+        dt = E2M1
+        _, out = _check_e2m1(q, k_cache, v_cache, k_group_scale, v_group_scale, out)
+        _plain(q.get_device(), sel._buf)
+    else:
+        dt, out = _common_checks(q, None, None, (("k_cache", k_cache), ("v_cache", v_cache)), sel._buf, out,
+                                 q_any_dtype=True)
     B, Hq, D = q.shape
     n0, Hkv, n2, D2 = k_cache.shape
     if (D2 * 2 if dt == E2M1 else D2) != D or v_cache.shape != k_cache.shape or (B, Hkv) != (sel.B, sel.Hkv) \
