@@ -225,7 +225,7 @@ def _plain(dev, *tensors):
 
 
 def _check_e2m1(q, k, v, kg, vg, out):
-    """Checks of a query and a 4-bit cache; returns (device index, out)."""
+    """Checks of a query, a 4-bit cache and an output that was given; returns the device index."""
     dev = q.get_device()
     if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
@@ -233,11 +233,9 @@ def _check_e2m1(q, k, v, kg, vg, out):
         raise TypeError("q must be float32 or bfloat16")
     _group_scales((("the key cache", k), ("the value cache", v)), kg, vg, q.shape[2])
     _plain(dev, q, k, v, out)
-    if out is None:
-        out = torch.empty_like(q, dtype=torch.float32)
-    elif out.shape != q.shape or out.dtype != torch.float32:
+    if out is not None and (out.shape != q.shape or out.dtype != torch.float32):
         raise ValueError("out must be a contiguous float32 (B, Hq, D) tensor on q's device")
-    return dev, out
+    return dev
 
 
 def _step_e2m1(q, k_new, v_new, k, v, lengths, slot_ids, table, k_scale, v_scale, kg, vg, out, status, kernel,
@@ -245,7 +243,7 @@ def _step_e2m1(q, k_new, v_new, k, v, lengths, slot_ids, table, k_scale, v_scale
     """The decode step (k_new, v_new given) or the attend over a 4-bit cache,
     dense or paged (table given). Written out for itself: the step is short,
     and its time on the host counts."""
-    dev, out = _check_e2m1(q, k, v, kg, vg, out)
+    dev = _check_e2m1(q, k, v, kg, vg, out)
     B, Hq, D = q.shape
     n0, Hkv, n2, _ = k.shape
     if Hq % Hkv or lengths.shape != (B,):
@@ -270,6 +268,8 @@ def _step_e2m1(q, k_new, v_new, k, v, lengths, slot_ids, table, k_scale, v_scale
         need = _need(lib, B, Hq, Hkv, D, E2M1, kernel, grid_ctas, o, device)
         ws = _workspace(device, need, stream) if workspace is None else workspace
         at, size, st = ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(status)
+        if out is None:   # last: right after another launch an allocation takes longer (4.6 us for 1.4)
+            out = torch.empty_like(q, dtype=torch.float32)
         if table is None:
             if k_new is None:
                 what, code = "gqa_attend", lib.gqa_attend(
@@ -831,8 +831,7 @@ def attend_selected(q, k_cache, v_cache, selection, *, out=None, status=None, ke
     sel = selection
     if k_group_scale is not None or v_group_scale is not None:
         dt = E2M1
-        _, out = _check_e2m1(q, k_cache, v_cache, k_group_scale, v_group_scale, out)
-        _plain(q.get_device(), sel._buf)
+        _plain(_check_e2m1(q, k_cache, v_cache, k_group_scale, v_group_scale, out), sel._buf)
     else:
         dt, out = _common_checks(q, None, None, (("k_cache", k_cache), ("v_cache", v_cache)), sel._buf, out,
                                  q_any_dtype=True)
@@ -849,6 +848,8 @@ def attend_selected(q, k_cache, v_cache, selection, *, out=None, status=None, ke
     with _on(q.device):
         need = _need(lib, B * Hkv, Hq // Hkv, 1, D, dt, kernel, grid_ctas, o, q.device)
         ws = _workspace(q.device, need, stream) if workspace is None else workspace
+        if out is None:
+            out = torch.empty_like(q, dtype=torch.float32)
         rc = lib.gqa_attend_selected(_ptr(q), _DTYPES[q.dtype], _ptr(k_cache), _ptr(v_cache), table, slots, _ptr(out),
                                      B, Hq, Hkv, D, n0 * Hkv * (n2 // sel.block_size), sel.block_size, sel.n_select,
                                      dt, _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
