@@ -1,38 +1,56 @@
 // Decode step and read-only attend over an E2M1 cache (D = 64 or 128, G <= 8).
 //
 // A cached vector is D / 2 bytes of codes and D / 16 bytes of E4M3 scales
-// (gqa_fp4.cuh), 0.5625 bytes an element, so the step is bound by what the
-// SMs spend on unpacking about as much as by memory; the kernel is laid out to
-// unpack with few instructions and to need no shared memory for the cache:
+// (gqa_fp4.cuh), 0.5625 bytes an element. Reading them takes the HBM less time
+// than unpacking takes the SMs (below), so the kernel is laid out to unpack
+// with few instructions:
 //  * the schedule, the split of a unit between CTAs and its merge are those of
-//    the other decode kernels (gqa_common.cuh). A CTA is four warps, a tile
-//    4 x 16 x kSub slots; each warp takes its 16 x kSub slots of every tile
-//    straight from global memory into registers, in the layout of the matrix
-//    instructions' operands, one tile ahead.
+//    the other decode kernels (gqa_common.cuh); short units get a CTA each
+//    (q4_whole_units). A CTA is four warps, a tile 4 x 32 slots. Each warp
+//    copies its 32 slots of every tile into a ring of its own in shared memory
+//    (16-byte asynchronous copies, kStages tiles deep: no barrier between the
+//    warps, no registers for data in flight), and runs on to the CTA's next
+//    segment, whose query rows and scales come the same way. Registers as the
+//    stage instead (one tile ahead, 8 warps an SM) took 146 us where the ring
+//    takes 94 (four rows of 32768 .. 131071 slots, G = 8).
 //  * S^T = K Q^T (m16n8k16, f16 in, float32 sums): the M side is 16 slots, the
-//    N side the G <= 8 query rows. Lane (g, t) of a warp holds slots g and
+//    N side the G <= 8 query rows. Lane (g, t) of a warp takes slots g and
 //    g + 8, and of each the D / 4 contiguous dims from D / 4 * t: one 16-byte
 //    load (D = 128) a slot. Which dims make up a product step does not matter
 //    to a dot product as long as the query fragments are taken in the same
 //    order.
 //  * O^T += V^T P^T: the M side is 16 dims, the N side the query rows, the
-//    contraction 16 slots. Lane (g, t) holds slots 2t, 2t + 1, 2t + 8, 2t + 9
-//    and of each the D / 8 contiguous dims from D / 8 * g, the rows of the M
-//    side being interleaved to match; a pair of slots is put together while it
-//    is multiplied by its scales.
+//    contraction 8 slots, each twice: the weight P is an f16 and an f16
+//    remainder, neighbours in the contraction, and the value stands beside
+//    both, as the doubled half of a register that its scale multiplies anyway.
+//    (Pairing two slots' values in a register took a byte permute each: 155 us
+//    for 148 on 64 rows of 512 .. 16383 slots, G = 6.) Lane (g, t) takes D / 8
+//    contiguous dims from D / 8 * g of four slots.
 //  * codes become f16 by the hardware's conversion and every E2M1 x E4M3
 //    product is an f16 exactly, so K and V enter the products unrounded. A
 //    bfloat16 query is scaled by a power of two into f16's range (exact but
 //    for elements 2^-38 below the row's largest); a float32 query is an f16
-//    and an f16 remainder (22 bits). The weights P are an f16 and a remainder
-//    too: in f16 alone the output would be off by 1e-4.
+//    and an f16 remainder (22 bits). With P in f16 alone the output would be
+//    off by 1e-4; so it is within 4e-7 of the 64-bit result on the sizes above.
 //  * the softmax keeps a reference below the running maximum: weights are
 //    2^(s - m) with m set to max - 7 and raised only when a score passes
 //    m + 15, so they stay within f16's range and a tile costs a vote instead
 //    of a reduction.
+//  * the matrix unit truncates its sums: the products of a tile are summed
+//    from zero and added to the output in float32 (truncated on, a long cache's
+//    output drifted by 3.5e-6).
 //  * the new token (decode step): the warp whose tile holds slot L quantises
-//    k_new and v_new, writes them to the cache, and then loads the tile; no
+//    k_new and v_new, writes them to the cache, and then copies the tile; no
 //    other warp touches slot L.
+// What bounds it. Per 16 slots a warp issues about 343 instructions (D = 128):
+// 64 conversions and 47 others on the ALU, 100 f16 and 57 float32 on the FMA
+// pipes, 24 matrix products. Each of these pipes takes a warp's instruction in
+// two cycles, a product in 8.3, and conversions and f16 products overlap only
+// in part (alone 7.9 cycles for four, together 12.2): 0.6 instructions a cycle
+// is what the mix reaches (0.71 for the bare conversions and products), 490
+// cycles per 16 slots and SM quarter, 5.4 TB/s of cache, 0.8 of the measured
+// HBM copy rate. More warps (four CTAs of 128 registers) or scores of one tile
+// beside the values of the one before changed nothing: it is the instructions.
 #define GQA_MULTI_TOKEN 0   // single-token steps only
 #include <cuda_fp16.h>
 
@@ -50,14 +68,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kSub = 2;                       // 16-slot parts of a warp's share of a tile (the code has two)
 constexpr int kShare = 16 * kSub;              // a warp's slots of a tile
 constexpr int kTile4 = kWarps * kShare;       // slots a tile
-#ifndef Q4_STAGES
-#define Q4_STAGES 3
-#endif
-#ifndef Q4_CTAS
-#define Q4_CTAS 3
-#endif
-constexpr int kStages = Q4_STAGES;            // tiles of a warp's ring
-constexpr int kCtas = Q4_CTAS;                // resident CTAs per SM
+constexpr int kStages = 3;                    // tiles of a warp's ring (2: paged 160 us for 154)
+constexpr int kCtas = 3;                      // resident CTAs per SM: 168 registers a thread (4 of 128: 167 us)
 constexpr int kSegs = 4;                      // segments a warp's copies and products are in at once (< kStages + 1)
 constexpr int kRows = 8;                      // query rows (G <= 8)
 constexpr float kLift = 7.f;                  // a reference is set this far below the maximum ...
@@ -491,8 +503,7 @@ __device__ __forceinline__ void weigh_pair(uint32_t x, uint32_t y, __half2 sc, u
 
 // O^T += V^T P^T over the warp's share; w[u][0..3] are the weights in the
 // positions of the scores. The products of a share are summed from zero and
-// then added to o: the matrix unit truncates its sums, which over a long
-// cache would add up to a relative 1e-5.
+// then added to o (the matrix unit truncates its sums).
 template <int D>
 __device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float (&w)[kSub][4], float (&o)[D / 16][4])
 {
