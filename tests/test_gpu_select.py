@@ -126,6 +126,66 @@ def test_long_rows(bs, n_blocks):
             assert torch.equal(_select(p, x, n).ids.cpu(), _want(p, x, n))
 
 
+@pytest.mark.parametrize("D,G,q", [(256, 3, torch.float32), (64, 16, torch.bfloat16), (256, 12, torch.bfloat16)])
+def test_widths_and_wide_groups(D, G, q):
+    """Selection alone, for head widths and group sizes that only some attends take."""
+    p = Problem("f32", "slots", [700, 33, 1000], 2 * G, 2, D, 1008, seed=G, q_dtype=q)
+    box = _bounds(p)
+    for n, first, last in ((5, 0, 1), (20, 2, 2)):
+        assert torch.equal(_select(p, box, n, first, last).ids.cpu(), _want(p, box, n, first, last))
+
+
+@pytest.mark.parametrize("kind", ["e2m1", "bf16"])
+def test_steps_without_waiting(kind):
+    """Steps of append, select, attend and decode queued back to back give the
+    bits of the same steps with a wait after every call."""
+    import gqa_kv_cache_gb300 as gqa
+    B, Hq, Hkv, D, bs, Smax, steps = 5, 8, 2, 128, 16, 2048, 60
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(steps, 3, B, Hkv, D, generator=gen, device="cuda").bfloat16()
+    q = torch.randn(steps, B, Hq, D, generator=gen, device="cuda").bfloat16()
+    pre = torch.randn(2, B * 700, Hkv, D, generator=gen, device="cuda").bfloat16()
+    g = torch.full((Hkv,), 0.002, device="cuda")
+    at = torch.tensor([[700 + 2 * i] * B for i in range(steps + 1)], dtype=torch.int32, device="cuda")
+    zero, cu0 = torch.zeros(B, dtype=torch.int32, device="cuda"), (torch.arange(B + 1, device="cuda") * 700).int()
+    cu = torch.arange(B + 1, device="cuda").int()
+    one = torch.ones(B, dtype=torch.int32, device="cuda")
+    now = [at[i] + one for i in range(steps)]
+    torch.cuda.synchronize()
+
+    def run(wait):
+        row = D // 2 if kind == "e2m1" else D
+        kv = [torch.zeros(B, Hkv, Smax, row, dtype=torch.uint8 if kind == "e2m1" else torch.bfloat16, device="cuda")
+              for _ in range(2)]
+        kw = {}
+        if kind == "e2m1":
+            gs = [torch.zeros(B, Hkv, Smax, D // 16, dtype=torch.uint8, device="cuda") for _ in range(2)]
+            kw = dict(k_scale=g, v_scale=g, k_group_scale=gs[0], v_group_scale=gs[1])
+        box = torch.zeros(B, Hkv, Smax // bs, 2, D, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        outs = []
+
+        def done(y):
+            if wait:
+                torch.cuda.synchronize()
+            return y
+        done(gqa.append(pre[0], pre[1], *kv, zero, cu0, k_bounds=box, **kw))
+        for i in range(steps):
+            done(gqa.append(x[i, 0], x[i, 1], *kv, at[i], cu, k_bounds=box, **kw))
+            sel = done(gqa.select_blocks(q[i], box, now[i], 9, block_size=bs))
+            outs.append(done(gqa.attend_selected(q[i], *kv, sel, **kw)))
+            # the next slot's token by the decode step, its bounds by an append of the same
+            outs.append(done(gqa.decode_step(q[i], x[i, 2], x[i, 1], *kv, now[i], **kw)))
+            done(gqa.append(x[i, 2], x[i, 1], *kv, now[i], cu, k_bounds=box, **kw))
+            outs.extend(done(gqa.read(*kv, at[i], cu, B, **kw)))
+        torch.cuda.synchronize()
+        return outs, kv
+    a, ka = run(True)
+    for _ in range(3):
+        b, kb = run(False)
+        assert all(torch.equal(u, v) for u, v in zip(a, b)) and all(torch.equal(u, v) for u, v in zip(ka, kb))
+
+
 def test_ties_and_borders():
     """Equal scores go to the lowest index; scores that float32 cannot tell apart are told apart."""
     B, n_blocks, bs, D = 1, 200, 16, 128
