@@ -204,11 +204,12 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
         uint32_t *out = cl.map_shared_rank(key, 0);
         const int j0 = (int)((long long)n * rank / ranks), j1 = (int)((long long)n * (rank + 1) / ranks);
         bool bad = false;
+        // (past the share's end its last block again, whose score is not used)
         auto place = [&](int base) {
-            return lane < 16 && base + lane < j1 ? pool_block(p, b, h, r, base + lane) : 0;
+            return lane < 16 ? pool_block(p, b, h, r, max(0, min(base + lane, j1 - 1))) : 0;
         };
         uint4 xa[H], xb[H];
-        // a block behind the last (or a bad one) reads the first of the pool: its score is not used
+        // a bad block reads the first of the pool: its score is not used
         auto load = [&](int at, int i0) {
             const int a = max(0, __shfl_sync(0xffffffffu, at, g)), c = max(0, __shfl_sync(0xffffffffu, at, g + 8));
             const uint4 *x0 = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.bounds) + (long long)a * E);
@@ -454,7 +455,10 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
             float wsum = 0.f;
             for (int i = 0; i < NW; ++i)
                 wsum += warp_w[i];
-            const float e = 1.1f * (float)(E / 16 + 8 + G) * 5.9604645e-8f * wsum * amax + 2e-37f * amax;
+            // where a part of a sum may have left float32's range (or a NaN is
+            // met), the 64-bit sums of all of them decide
+            const float most = wsum * amax;
+            const float e = most < 1e38f ? 1.1f * (float)(E / 16 + 8 + G) * 5.9604645e-8f * most + 2e-37f * amax : INFINITY;
             lo = T - 2.f * e;
             hi = T + 2.f * e;
             // one rounding of each border outwards

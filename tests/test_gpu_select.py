@@ -229,6 +229,19 @@ def test_nan_and_infinite_bounds():
     assert _select(p, x, 6).ids.cpu()[0, 0].tolist() == [0, 1, 2, 3, 4, n_blocks - 1]
 
 
+@pytest.mark.parametrize("n", [3, 4, 6])
+def test_scores_past_float32(n):
+    """Finite bounds whose score, or only a part of its sum, leaves float32's range."""
+    p = Problem("bf16", "dense", [40 * 16], 1, 1, 64, 40 * 16, seed=8)
+    p.q = torch.ones(1, 1, 64, dtype=torch.bfloat16)
+    x = torch.randn(1, 1, 40, 2, 64, generator=torch.Generator().manual_seed(4)).sort(3).values.bfloat16()
+    x[0, 0, 9, 1, :2] = 3e38
+    x[0, 0, 30, 1, 5:9] = 3e38
+    x[0, 0, 17, 1, :2] = 2e38                            # 4e38 and then back to the lowest of all
+    x[0, 0, 17, :, 4:33:28] = -3e38
+    assert torch.equal(_select(p, x, n).ids.cpu(), _want(p, x, n))
+
+
 def test_blocks_behind_the_row_never_matter():
     p = Problem("bf16", "paged", [100, 333], 4, 2, 128, 512, seed=6)
     box = _bounds(p)
