@@ -723,6 +723,7 @@ class Selection:
     def __init__(self, B, Hkv, n_select, block_size, device):
         self.B, self.Hkv, self.n_select, self.block_size = B, Hkv, n_select, block_size
         self._n = B * Hkv * n_select
+        self._pool = 0      # (block, head) pairs of the cache it was made over; 0: not made yet
         self._buf = torch.empty(2 * self._n + B * Hkv, dtype=torch.int32, device=device)
 
     @property
@@ -779,6 +780,7 @@ def _select(q, k_bounds, block_table, lengths, n_select, slot_ids, block_size, n
             or selection._buf.device != q.device:
         raise ValueError("selection was made for other sizes")
     ids, table, slots = selection._ptrs()
+    selection._pool = k_bounds.shape[0] * Hkv * (k_bounds.shape[2] if block_table is None else 1)
     lib = _lib.load()
     with _on(q.device):
         if block_table is None:
@@ -838,7 +840,7 @@ def attend_selected(q, k_cache, v_cache, selection, *, out=None, status=None, ke
     B, Hq, D = q.shape
     n0, Hkv, n2, D2 = k_cache.shape
     if (D2 * 2 if dt == E2M1 else D2) != D or v_cache.shape != k_cache.shape or (B, Hkv) != (sel.B, sel.Hkv) \
-            or Hq % Hkv or n2 % sel.block_size:
+            or Hq % Hkv or n2 % sel.block_size or n0 * Hkv * (n2 // sel.block_size) != sel._pool:
         raise ValueError("shape mismatch between q, the caches and the selection")
     _status_checks(status, q.device)
     o = _opts(kernel, grid_ctas, sched_pad, device=q.device, k_scale=k_scale, v_scale=v_scale, Hkv=Hkv,

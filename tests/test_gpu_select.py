@@ -362,6 +362,26 @@ def test_a_run_of_steps(kind):
         _check_attend(p, sel, ids, out)
 
 
+@pytest.mark.parametrize("layout", ["dense", "paged"])
+def test_a_selection_of_another_cache_is_refused(layout):
+    """A selection names blocks of one pool: another block size or number of rows
+    would be other slots."""
+    import gqa_kv_cache_gb300 as gqa
+    p = Problem("bf16", layout, [200, 100], 4, 2, 128, 256, bs=32)
+    box, kv = _bounds(p), [x.cuda() for x in p.kv]
+    sel = _select(p, box, 4)
+    gqa.attend_selected(p.q.cuda(), *kv, sel)
+    p.bs, p.lengths = 16, torch.tensor([100, 50], dtype=torch.int32)
+    half = _select(p, box, 4)                            # pages (or bounds) of 32 taken for 16
+    with pytest.raises(ValueError):
+        gqa.attend_selected(p.q.cuda(), *kv, half)
+    with pytest.raises(ValueError):
+        gqa.attend_selected(p.q.cuda(), *[torch.cat([x, x]) for x in kv], sel)
+    empty = gqa.Selection(2, 2, 4, 32, torch.device("cuda", 0))
+    with pytest.raises(ValueError):
+        gqa.attend_selected(p.q.cuda(), *kv, empty)
+
+
 def test_all_blocks_kept_is_the_plain_attend():
     import gqa_kv_cache_gb300 as gqa
     p = Problem("e2m1", "dense", [256, 100, 33], 8, 2, 128, 256, seed=12)
