@@ -314,6 +314,17 @@ struct Share {
     }
 };
 
+// Rows whose offsets decrease (or begin outside the tokens) have no token that
+// could tell: the CTAs look at the rows' offsets too.
+__device__ __forceinline__ void check_rows(const RowsParams &p)
+{
+    for (long long b = (long long)blockIdx.x * kThreads + threadIdx.x; b < p.B; b += (long long)gridDim.x * kThreads) {
+        const int t0 = __ldg(p.cu_q + b), t1 = __ldg(p.cu_q + b + 1);
+        if (t0 < 0 || t1 < t0 || t1 > p.T)
+            rows_report(p, kBadQLen);
+    }
+}
+
 // One CTA: `chunk` tokens and, with bounds, the rest of the last run that
 // begins among them. Shared memory: the tokens' slots, then (bounds) one
 // Bounds a thread.
@@ -346,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_kerne
                 atomicMin(i < p.chunk ? &first : &last, i);
         }
     }
+    check_rows(p);
     __syncthreads();
     const int a = first, e = max(a, last);
     const Share s(p);
@@ -438,6 +450,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowsParams p)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int i = tid; i < n; i += kThreads)
         tok[i] = find_token(p, t0 + i);
+    check_rows(p);
     __syncthreads();
     const Share s(p);
     const long long head = (long long)(p.paged ? p.block_size : p.Smax) * p.D;

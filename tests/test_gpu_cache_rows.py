@@ -337,6 +337,19 @@ def test_bad_content():
     assert int(st) == 32 and float(c.kv[0][1].abs().sum()) == 0 and float(c.kv[0][0].abs().sum()) > 0
 
 
+@pytest.mark.parametrize("cu", [[0, 5, 3, 8], [0, 8, 8, 7], [0, 4, -1, 8]])
+def test_decreasing_offsets_are_reported(cu):
+    """A row whose offsets decrease has no token that could tell."""
+    import gqa_kv_cache_gb300 as gqa
+    x = torch.zeros(8, 2, 64, dtype=torch.bfloat16, device="cuda")
+    kv = [torch.zeros(3, 2, 32, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    at = [torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 0, 0], cu)]
+    for call in (lambda st: gqa.append(x, x, *kv, *at, status=st), lambda st: gqa.read(*kv, *at, 8, status=st)):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        call(st)
+        assert int(st) == 32
+
+
 def test_graph_and_stream():
     c = Case("e2m1", "dense", [0, 7], [30, 9], 2, 128, 64, seed=6, bounds=False)
     c.append()
