@@ -486,7 +486,7 @@ template <typename K>
 cudaError_t launch(K kernel, const RowsParams &p, size_t smem, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((p.T + p.chunk - 1) / p.chunk);
+    cfg.gridDim = dim3((unsigned)(((long long)p.T + p.chunk - 1) / p.chunk));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -524,8 +524,8 @@ cudaError_t rows_launch(RowsParams p, int kv_dtype, bool write, int sms, cudaStr
     // (131071 tokens of 8 x 128 with bounds of 64 slots: 16 tokens 156 us, 32
     // 147, 64 139), 32 to read (113 us; 64: 115)
     const int ctas = sms * 8, most = write ? 64 : 32;
-    p.chunk = (p.T + ctas - 1) / ctas;
-    p.chunk = p.chunk < 1 ? 1 : p.chunk > most ? most : p.chunk;
+    const long long share = ((long long)p.T + ctas - 1) / ctas;
+    p.chunk = share < 1 ? 1 : share > most ? most : (int)share;
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.k_new) | reinterpret_cast<uintptr_t>(p.v_new) |
                          reinterpret_cast<uintptr_t>(p.k_out) | reinterpret_cast<uintptr_t>(p.v_out) |
                          reinterpret_cast<uintptr_t>(p.k_cache) | reinterpret_cast<uintptr_t>(p.v_cache);

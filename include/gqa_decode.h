@@ -446,7 +446,9 @@ gqa_status gqa_decode_step_noalloc(const void *q, const void *k_new, const void 
  * rounded to the cache's type. Tokens of the packed batch that belong to no
  * row (t >= cu_q[B]) are ignored. Of a row with a bad length, slot id or
  * offsets nothing is written, of a token whose block is bad neither; the
- * status bits are those of gqa_decode_multi.
+ * status bits are those of gqa_decode_multi. Two tokens of one slot (a cache
+ * row or block written through two rows, offsets that decrease), or with
+ * k_bounds two rows that write one block, are undefined.
  *
  *  k_new, v_new (device) (T, Hkv, D) of new_dtype; D a multiple of 16
  *  k_bounds     (device) bfloat16 key bounds, or NULL. Dense: (R, Hkv,
@@ -456,7 +458,9 @@ gqa_status gqa_decode_step_noalloc(const void *q, const void *k_new, const void 
  *               given (a float32 key rounded outwards; NaN if any is). A
  *               token at a block's first slot starts the block's bounds
  *               afresh, others widen them: bounds stay valid, if wider than
- *               need be, when a row is cut back and written again.
+ *               need be, when a row is cut back and written again. The
+ *               decode calls append to the cache alone: a step that selects
+ *               blocks appends its token with this call.
  *  bounds_block (dense, with k_bounds) slots a block: divides Smax, <= 1024
  *               (paged: block_size, <= 1024 with k_bounds)
  */
