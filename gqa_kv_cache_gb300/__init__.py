@@ -254,16 +254,20 @@ def _step_e2m1(q, k_new, v_new, k, v, lengths, slot_ids, table, k_scale, v_scale
         raise TypeError("slot_ids must be int32 of shape (B,)")
     if table is not None and (table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B):
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor")
-    _plain(dev, lengths, slot_ids, table, k_new, v_new)
+    _plain(dev, lengths, slot_ids, table, k_new, v_new, workspace)
     if k_new is not None:
         if q.dtype != torch.bfloat16 or k_new.dtype != torch.bfloat16 or v_new.dtype != torch.bfloat16:
             raise TypeError("over an E2M1 cache q, k_new and v_new are bfloat16")
         if k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D):
             raise ValueError("shape mismatch between q, k_new and v_new")
     device = q.device
+    _status_checks(status, device)
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, device, B, Hq, k_scale, v_scale, Hkv,
               k_group_scale=kg, v_group_scale=vg)
     lib = _lib.load()
+    if stream is not None and out is None:   # the memory of the stream that writes it
+        with torch.cuda.stream(stream):
+            out = torch.empty(q.shape, dtype=torch.float32, device=device)
     with _on(device):
         need = _need(lib, B, Hq, Hkv, D, E2M1, kernel, grid_ctas, o, device)
         ws = _workspace(device, need, stream) if workspace is None else workspace
@@ -843,6 +847,7 @@ def attend_selected(q, k_cache, v_cache, selection, *, out=None, status=None, ke
             or Hq % Hkv or n2 % sel.block_size or n0 * Hkv * (n2 // sel.block_size) != sel._pool:
         raise ValueError("shape mismatch between q, the caches and the selection")
     _status_checks(status, q.device)
+    _plain(q.get_device(), workspace)
     o = _opts(kernel, grid_ctas, sched_pad, device=q.device, k_scale=k_scale, v_scale=v_scale, Hkv=Hkv,
               k_group_scale=k_group_scale, v_group_scale=v_group_scale)
     lib = _lib.load()

@@ -243,6 +243,21 @@ def test_graphs_and_streams():
             assert torch.equal(o, w)
 
 
+def test_output_of_a_stream_is_its_own_memory():
+    """What the current stream just freed may still be read there: the output of a
+    call on another stream comes from that stream's memory."""
+    p = Problem("e2m1", "dense", [100, 20], 8, 2, 128, 112, seed=22)
+    t, side = _gpu(p), torch.cuda.Stream()
+    freed = [torch.empty(2, 8, 128, device="cuda") for _ in range(4)]
+    at = {x.data_ptr() for x in freed}
+    torch.cuda.synchronize()
+    del freed
+    out = _attend(p, t, stream=side)
+    side.synchronize()
+    assert out.data_ptr() not in at
+    _check(p, out)
+
+
 def test_same_bits_twice_and_empty_batch():
     import gqa_kv_cache_gb300 as gqa
     p = Problem("e2m1", "paged", [900, 64, 333], 8, 1, 128, 912, seed=30)
@@ -297,6 +312,12 @@ def test_refusals():
         _decode(p, {**t, "q": t["q"].float()}, bf, bf)
     with pytest.raises(ValueError):                      # more rows than lengths
         _attend(p, {**t, "q": t["q"].repeat(2, 1, 1)})
+    with pytest.raises(TypeError):                       # a status word of the host, or of another type
+        _attend(p, t, status=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        _attend(p, t, status=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):                      # a workspace of the host
+        _attend(p, t, workspace=torch.zeros(1 << 20, dtype=torch.uint8))
     w = Problem("e2m1", "dense", [5], 9, 1, 128, 16, seed=32)
     with pytest.raises(gqa.GqaError):                    # G = 9
         _attend(w, _gpu(w))

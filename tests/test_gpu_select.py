@@ -418,6 +418,8 @@ def test_refusals():
     g = torch.ones(2, device="cuda")
     with pytest.raises(gqa.GqaError):                    # an E4M3 cache
         gqa.attend_selected(p.q.cuda(), f8, f8.clone(), sel, k_scale=g, v_scale=g)
+    with pytest.raises(ValueError):                      # a workspace of the host
+        gqa.attend_selected(p.q.cuda(), k, v, sel, workspace=torch.zeros(1 << 20, dtype=torch.uint8))
     wide = torch.zeros(1, 2, 17000, 2, 128, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(gqa.GqaError):                    # too many blocks a row
         gqa.select_blocks(p.q.cuda(), wide, p.lengths.cuda(), 4, block_size=16)
