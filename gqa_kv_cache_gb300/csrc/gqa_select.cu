@@ -130,12 +130,16 @@ __device__ __forceinline__ void raise(uint32_t &top, uint32_t x)
     asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(x));
 }
 
-// Element d of query head g of the unit.
-__device__ __forceinline__ float query(const SelectParams &p, long long head0, int g, int D, int d)
+// Element d of query head g of the unit, as loaded, and its value.
+__device__ __forceinline__ uint32_t query_raw(const SelectParams &p, long long head0, int g, int D, int d)
 {
     const long long at = (head0 + g) * D + d;
-    return p.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.q)[at])
-                    : static_cast<const float *>(p.q)[at];
+    return p.q_bf16 ? (uint32_t)__ldg(static_cast<const unsigned short *>(p.q) + at)
+                    : __ldg(static_cast<const uint32_t *>(p.q) + at);
+}
+__device__ __forceinline__ float query(const SelectParams &p, uint32_t raw)
+{
+    return __uint_as_float(p.q_bf16 ? raw << 16 : raw);
 }
 
 // NT threads a CTA: 256 where a unit has few CTAs, 128 where the units fill
@@ -176,6 +180,15 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len = __ldg(p.lengths + b);
+    // the first query heads' elements, asked for before the bounds (behind
+    // every CTA's first bounds they came 4 us later)
+    constexpr int DS = (D + NT - 1) / NT, GS = 8;
+    uint32_t raw[DS][GS];
+#pragma unroll
+    for (int i = 0; i < DS; ++i)
+#pragma unroll
+        for (int q = 0; q < GS; ++q)
+            raw[i][q] = q < G && tid + i * NT < D ? query_raw(p, head0, q, D, tid + i * NT) : 0u;
     const int r = p.paged ? 0 : (p.slot_ids ? __ldg(p.slot_ids + b) : b);
     int bits = 0;
     if (len < 1 || (long long)len > (long long)p.NB * p.block_size)
@@ -222,18 +235,23 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
         };
         constexpr int STEP = 16 * NW;
         int at = place(j0 + 16 * warp), at_next = place(j0 + 16 * warp + STEP);
-        bad |= at < 0;
-        load(at, 0);
 
         float mag = 0.f;
-        for (int d = tid; d < D; d += NT) {
+#pragma unroll
+        for (int k = 0; k < DS; ++k) {
+            const int d = tid + k * NT;
+            if (d >= D)
+                break;
             float dn = 0.f, up = 0.f;      // N_d, P_d
-#pragma unroll 8
-            for (int q = 0; q < G; ++q) {
-                const float v = query(p, head0, q, D, d);
+            auto add = [&](float v) {
                 dn += v != v ? v : fminf(v, 0.f);
                 up += v != v ? v : fmaxf(v, 0.f);
-            }
+            };
+#pragma unroll
+            for (int q = 0; q < GS; ++q)
+                add(query(p, raw[k][q]));  // (0 past the last head)
+            for (int q = GS; q < G; ++q)
+                add(query(p, query_raw(p, head0, q, D, d)));
             mag += fabsf(dn) + fabsf(up);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
@@ -244,6 +262,8 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
                 up -= __bfloat162float(y);
             }
         }
+        bad |= at < 0;
+        load(at, 0);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             mag += __shfl_xor_sync(0xffffffffu, mag, o);
@@ -415,6 +435,8 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
                             few[atomicAdd(&n_few, 1)] = j;
                     }
                     __syncthreads();
+                    if (tid == 0)
+                        n_few = 0;         // for the next list (behind the barrier below)
                     for (int i = tid; i < members; i += NT) {
                         const uint32_t k = key[few[i]];
                         int above = 0, same = 0;
@@ -429,8 +451,6 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
                     __syncthreads();
                     T = unkey32(warp_key[0][0]);
                     have = true;
-                    if (tid == 0)
-                        n_few = 0;
                 }
             }
             if (!have) {
@@ -468,9 +488,14 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
             for (int j = tid; j < n; j += NT) {
                 const uint32_t k = key[j];
                 const float s = unkey32(k);
-                const bool f = k == kForced;
-                above += f || s > hi;
-                between += !f && !(s > hi) && !(s < lo);
+                if (k == kForced || s > hi) {
+                    ++above;
+                } else if (!(s < lo)) {
+                    ++between;
+                    const int i = atomicAdd(&n_few, 1);
+                    if (i < kFew)
+                        few[i] = j;
+                }
             }
             const int both = sum(above | (between << 16));
             above = both & 0xffff;
@@ -484,37 +509,65 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
                     double dn = 0.0, up = 0.0;
 #pragma unroll 8
                     for (int q = 0; q < G; ++q) {
-                        const float v = query(p, head0, q, D, d);
+                        const float v = query(p, query_raw(p, head0, q, D, d));
                         dn += v != v ? (double)v : (double)fminf(v, 0.f);
                         up += v != v ? (double)v : (double)fmaxf(v, 0.f);
                     }
                     wt64[d] = dn;
                     wt64[D + d] = up;
                 }
-                __syncthreads();
-                for (int base = warp * 32; base < n; base += NT) {
-                    const int j = base + lane;
-                    const float s = j < n ? unkey32(key[j]) : 0.f;
-                    const bool is = j < n && key[j] != kForced && !(s > hi) && !(s < lo);
-                    if (j < n)
-                        key64[j] = 0;      // not in between (no score has this key)
-                    __syncwarp();
-                    for (unsigned left = __ballot_sync(0xffffffffu, is); left; left &= left - 1) {
-                        const int jj = base + __ffs(left) - 1;
-                        const int at = max(0, pool_block(p, b, h, r, jj));
-                        const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.bounds) + (long long)at * E;
-                        double acc = 0.0;
+                // the elements of a block that this lane sums, and the sum of all
+                using Part = __nv_bfloat16[E / 32];
+                auto fetch = [&](int a, Part &x) {
+                    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.bounds) + (long long)max(0, a) * E;
 #pragma unroll
-                        for (int d = 0; d < E; d += 32)
-                            acc += wt64[d + lane] * (double)__bfloat162float(x[d + lane]);
+                    for (int d = 0; d < E / 32; ++d)
+                        x[d] = v[32 * d + lane];
+                };
+                auto total = [&](const Part &x) {
+                    double acc = 0.0;
 #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1)
-                            acc += __shfl_xor_sync(0xffffffffu, acc, o);
-                        if (lane == 0) {
-                            key64[jj] = key64_of(acc + 0.0);
-                            const int i = atomicAdd(&n_few, 1);
-                            if (i < kFew)
-                                few[i] = jj;
+                    for (int d = 0; d < E / 32; ++d)
+                        acc += wt64[32 * d + lane] * (double)__bfloat162float(x[d]);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1)
+                        acc += __shfl_xor_sync(0xffffffffu, acc, o);
+                    return key64_of(acc + 0.0);
+                };
+                Part x;
+                if (between <= kFew) {
+                    // dealt out to the warps, their places looked up at once
+                    // and the next one's elements loaded beside a sum
+                    const int c = warp + NW * lane;
+                    const int a = c < between ? pool_block(p, b, h, r, few[c]) : 0;
+                    fetch(__shfl_sync(0xffffffffu, a, 0), x);
+                    __syncthreads();
+                    for (int i = warp, l = 1; i < between; i += NW, ++l) {
+                        Part y;
+                        fetch(__shfl_sync(0xffffffffu, a, l & 31), y);
+                        const unsigned long long k = total(x);
+                        if (lane == 0)
+                            key64[few[i]] = k;
+#pragma unroll
+                        for (int d = 0; d < E / 32; ++d)
+                            x[d] = y[d];
+                    }
+                } else {
+                    __syncthreads();
+                    for (int base = warp * 32; base < n; base += NT) {
+                        const int j = base + lane;
+                        const float s = j < n ? unkey32(key[j]) : 0.f;
+                        const bool is = j < n && key[j] != kForced && !(s > hi) && !(s < lo);
+                        const int a = is ? pool_block(p, b, h, r, j) : 0;
+                        if (j < n)
+                            key64[j] = 0;  // not in between (no score has this key)
+                        __syncwarp();
+                        for (unsigned left = __ballot_sync(0xffffffffu, is); left; left &= left - 1) {
+                            const int l = __ffs(left) - 1;
+                            fetch(__shfl_sync(0xffffffffu, a, l), x);
+                            const unsigned long long k = total(x);
+                            if (lane == 0)
+                                key64[base + l] = k;
                         }
                     }
                 }
@@ -561,52 +614,58 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
             p.ids[row + i] = p.table[row + i] = -1;
         return;
     }
-    // the kept blocks in ascending order: each thread a stretch of the blocks
-    const int per = (n + NT - 1) / NT;
-    const int c0 = min(n, tid * per), c1 = min(n, c0 + per);
-    // 2: kept, 1: kept if among the first `take` of its equals, 0: not
-    auto state = [&](int j) {
-        if (mode == 0 || key[j] == kForced)
-            return 2;
-        const float s = unkey32(key[j]);
-        if (mode == 1)
-            return !(s < lo) && lo < INFINITY ? 2 : 0;
-        return s > hi || key64[j] > thr64 ? 2 : key64[j] == thr64 ? 1 : 0;
-    };
-    int mine = 0;                          // kept | ties << 16
-    for (int j = c0; j < c1; ++j) {
-        const int k = state(j);
-        mine += k == 2 ? 1 : k << 16;
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o)
-            incl += x;
-    }
-    __syncthreads();
-    if (lane == 31)
-        scan[warp] = incl;
-    __syncthreads();
-    int before = incl - mine;
-    for (int i = 0; i < warp; ++i)
-        before += scan[i];
-    int ties = (int)((unsigned)before >> 16), at = (before & 0xffff) + min(ties, take);
-    for (int j = c0; j < c1; ++j) {
-        const int k = state(j);
-        if (k == 2 || (k == 1 && ties < take)) {
-            if (at < p.n_select) {
-                p.ids[row + at] = j;
-                p.table[row + at] = pool_block(p, b, h, r, j);
-            }
-            ++at;
-        }
-        ties += k == 1;
-    }
     const int total = min(n, p.n_select);
-    for (int i = total + tid; i < p.n_select; i += NT)
-        p.ids[row + i] = p.table[row + i] = -1;
+    int *list = reinterpret_cast<int *>(key64);
+    if (!all) {
+        // the kept blocks in ascending order: each thread a stretch of the
+        // blocks (an odd number: its words lie in different banks)
+        const int per = (n + NT - 1) / NT | 1;
+        const int c0 = min(n, tid * per), c1 = min(n, c0 + per);
+        // 2: kept, 1: kept if among the first `take` of its equals, 0: not
+        auto state = [&](int j) {
+            if (key[j] == kForced)
+                return 2;
+            const float s = unkey32(key[j]);
+            if (mode == 1)
+                return !(s < lo) && lo < INFINITY ? 2 : 0;
+            if (s > hi || s < lo)
+                return s > hi ? 2 : 0;
+            return key64[j] > thr64 ? 2 : key64[j] == thr64 ? 1 : 0;
+        };
+        int mine = 0;                      // kept | ties << 16
+        for (int j = c0; j < c1; ++j) {
+            const int k = state(j);
+            key[j] = k;
+            mine += k == 2 ? 1 : k << 16;
+        }
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += x;
+        }
+        __syncthreads();                   // (the bins' use of scan, and key64, are over)
+        if (lane == 31)
+            scan[warp] = incl;
+        __syncthreads();
+        int before = incl - mine;
+        for (int i = 0; i < warp; ++i)
+            before += scan[i];
+        int ties = (int)((unsigned)before >> 16), at = (before & 0xffff) + min(ties, take);
+        for (int j = c0; j < c1; ++j) {
+            const int k = (int)key[j];
+            if ((k == 2 || (k == 1 && ties < take)) && at < total)
+                list[at++] = j;
+            ties += k == 1;
+        }
+        __syncthreads();
+    }
+    for (int i = tid; i < p.n_select; i += NT) {
+        const int j = i >= total ? -1 : all ? i : list[i];
+        p.ids[row + i] = j;
+        p.table[row + i] = j < 0 ? -1 : pool_block(p, b, h, r, j);
+    }
     if (tid == 0)
         p.sel_lengths[unit] = (total - 1) * p.block_size + (len - (n - 1) * p.block_size);
 }
