@@ -503,19 +503,6 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
             if (above + between != need) {
                 mode = 2;
                 take = need - above;
-                // the weights in 64 bits, then the sums of the blocks in
-                // between, a warp each
-                for (int d = tid; d < D; d += NT) {
-                    double dn = 0.0, up = 0.0;
-#pragma unroll 8
-                    for (int q = 0; q < G; ++q) {
-                        const float v = query(p, query_raw(p, head0, q, D, d));
-                        dn += v != v ? (double)v : (double)fminf(v, 0.f);
-                        up += v != v ? (double)v : (double)fmaxf(v, 0.f);
-                    }
-                    wt64[d] = dn;
-                    wt64[D + d] = up;
-                }
                 // the elements of a block that this lane sums, and the sum of all
                 using Part = __nv_bfloat16[E / 32];
                 auto fetch = [&](int a, Part &x) {
@@ -534,14 +521,26 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
                         acc += __shfl_xor_sync(0xffffffffu, acc, o);
                     return key64_of(acc + 0.0);
                 };
+                // dealt out to the warps, their places looked up at once and
+                // the next one's elements loaded beside a sum
                 Part x;
+                const int c = warp + NW * lane;
+                const int a = c < min(between, kFew) ? pool_block(p, b, h, r, few[c]) : 0;
+                fetch(__shfl_sync(0xffffffffu, a, 0), x);
+                // the weights in 64 bits
+                for (int d = tid; d < D; d += NT) {
+                    double dn = 0.0, up = 0.0;
+#pragma unroll 8
+                    for (int q = 0; q < G; ++q) {
+                        const float v = query(p, query_raw(p, head0, q, D, d));
+                        dn += v != v ? (double)v : (double)fminf(v, 0.f);
+                        up += v != v ? (double)v : (double)fmaxf(v, 0.f);
+                    }
+                    wt64[d] = dn;
+                    wt64[D + d] = up;
+                }
+                __syncthreads();
                 if (between <= kFew) {
-                    // dealt out to the warps, their places looked up at once
-                    // and the next one's elements loaded beside a sum
-                    const int c = warp + NW * lane;
-                    const int a = c < between ? pool_block(p, b, h, r, few[c]) : 0;
-                    fetch(__shfl_sync(0xffffffffu, a, 0), x);
-                    __syncthreads();
                     for (int i = warp, l = 1; i < between; i += NW, ++l) {
                         Part y;
                         fetch(__shfl_sync(0xffffffffu, a, l & 31), y);
@@ -553,7 +552,6 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
                             x[d] = y[d];
                     }
                 } else {
-                    __syncthreads();
                     for (int base = warp * 32; base < n; base += NT) {
                         const int j = base + lane;
                         const float s = j < n ? unkey32(key[j]) : 0.f;
