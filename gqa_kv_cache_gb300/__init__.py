@@ -254,14 +254,17 @@ def _step_e2m1(q, k_new, v_new, k, v, lengths, slot_ids, table, k_scale, v_scale
         raise TypeError("slot_ids must be int32 of shape (B,)")
     if table is not None and (table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B):
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor")
-    _plain(dev, lengths, slot_ids, table, k_new, v_new, workspace)
+    _plain(dev, lengths, slot_ids, table, k_new, v_new)
     if k_new is not None:
         if q.dtype != torch.bfloat16 or k_new.dtype != torch.bfloat16 or v_new.dtype != torch.bfloat16:
             raise TypeError("over an E2M1 cache q, k_new and v_new are bfloat16")
         if k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D):
             raise ValueError("shape mismatch between q, k_new and v_new")
     device = q.device
-    _status_checks(status, device)
+    if status is not None:
+        _status_checks(status, device)
+    if workspace is not None:
+        _plain(dev, workspace)
     o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, device, B, Hq, k_scale, v_scale, Hkv,
               k_group_scale=kg, v_group_scale=vg)
     lib = _lib.load()
@@ -567,7 +570,8 @@ def _rows_checks(caches, lengths, cu_q, slot_ids, block_table, groups, D):
     dev = k.get_device()
     if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if v.shape != k.shape or v.dtype != k.dtype or v.get_device() != dev or k.dim() != 4:
+    shape = k.shape
+    if v.shape != shape or v.dtype != k.dtype or v.get_device() != dev or len(shape) != 4:
         raise ValueError("the two caches must be 4-dimensional and alike")
     if not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("the caches must be contiguous")
@@ -576,7 +580,7 @@ def _rows_checks(caches, lengths, cu_q, slot_ids, block_table, groups, D):
         code = E2M1
     else:
         code = _cache_code(k)
-        if k.shape[-1] != D:
+        if shape[3] != D:
             raise ValueError("shape mismatch between the vectors and the caches")
     B = lengths.shape[0]
     _int32("lengths", lengths, B, dev)
@@ -615,10 +619,12 @@ def _append(k_new, v_new, k, v, block_table, lengths, cu_q, slot_ids, scales, gr
     for t in (k_new, v_new):
         if t.get_device() != dev or not t.is_contiguous():
             raise ValueError("k_new and v_new must be contiguous and on the caches' device")
-    if k.shape[1] != Hkv:
+    n0, heads, n2, _ = k.shape
+    if heads != Hkv:
         raise ValueError("shape mismatch between k_new and the caches")
-    _status_checks(status, k.device)
-    n0, _, n2, _ = k.shape
+    device = k.device
+    if status is not None:
+        _status_checks(status, device)
     block = 0
     if k_bounds is not None:
         if block_table is not None:
@@ -631,20 +637,20 @@ def _append(k_new, v_new, k, v, block_table, lengths, cu_q, slot_ids, scales, gr
         if k_bounds.dtype != torch.bfloat16 or k_bounds.shape != shape or not k_bounds.is_contiguous() \
                 or k_bounds.get_device() != dev:
             raise TypeError(f"k_bounds must be a contiguous bfloat16 {shape} tensor on the caches' device")
-    o = _rows_opts(code, Hkv, k.device, *scales, groups)
+    o = _rows_opts(code, Hkv, device, *scales, groups)
     lib = _lib.load()
     B = lengths.shape[0]
-    with _on(k.device):
+    with _on(device):
         if block_table is not None:
             what = "gqa_append_paged"
             rc = lib.gqa_append_paged(_ptr(k_new), _ptr(v_new), _DTYPES[k_new.dtype], _ptr(k), _ptr(v),
                                       _ptr(block_table), _ptr(lengths), _ptr(cu_q), _ptr(k_bounds), B, T, Hkv, D, n0,
-                                      n2, block_table.shape[1], code, _ptr(status), _stream(stream, k.device), o)
+                                      n2, block_table.shape[1], code, _ptr(status), _stream(stream, device), o)
         else:
             what = "gqa_append"
             rc = lib.gqa_append(_ptr(k_new), _ptr(v_new), _DTYPES[k_new.dtype], _ptr(k), _ptr(v), _ptr(lengths),
                                 _ptr(cu_q), _ptr(slot_ids), _ptr(k_bounds), block, B, T, Hkv, D, n0, n2, code,
-                                _ptr(status), _stream(stream, k.device), o)
+                                _ptr(status), _stream(stream, device), o)
     _check(rc, what)
 
 
@@ -673,8 +679,9 @@ def _read(k, v, block_table, lengths, cu_q, T, slot_ids, dtype, k_out, v_out, sc
         raise TypeError("dtype must be torch.float32 or torch.bfloat16")
     D = k.shape[-1] * (2 if groups[0] is not None or groups[1] is not None else 1)
     code = _rows_checks(((names[0], k), (names[1], v)), lengths, cu_q, slot_ids, block_table, groups, D)
-    _status_checks(status, k.device)
-    dev = k.get_device()
+    device, dev = k.device, k.get_device()
+    if status is not None:
+        _status_checks(status, device)
     n0, Hkv, n2, _ = k.shape
     T, shape = int(T), (int(T), Hkv, D)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
@@ -682,21 +689,21 @@ def _read(k, v, block_table, lengths, cu_q, T, slot_ids, dtype, k_out, v_out, sc
             raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor on the caches' device")
     if k_out is None or v_out is None:
         with torch.cuda.stream(stream) if stream is not None else _HERE:
-            k_out = torch.empty(shape, dtype=dtype, device=k.device) if k_out is None else k_out
-            v_out = torch.empty(shape, dtype=dtype, device=k.device) if v_out is None else v_out
-    o = _rows_opts(code, Hkv, k.device, *scales, groups)
+            k_out = torch.empty(shape, dtype=dtype, device=device) if k_out is None else k_out
+            v_out = torch.empty(shape, dtype=dtype, device=device) if v_out is None else v_out
+    o = _rows_opts(code, Hkv, device, *scales, groups)
     lib = _lib.load()
     B = lengths.shape[0]
-    with _on(k.device):
+    with _on(device):
         if block_table is not None:
             what = "gqa_read_paged"
             rc = lib.gqa_read_paged(_ptr(k), _ptr(v), _ptr(block_table), _ptr(lengths), _ptr(cu_q), _ptr(k_out),
                                     _ptr(v_out), _DTYPES[dtype], B, T, Hkv, D, n0, n2, block_table.shape[1], code,
-                                    _ptr(status), _stream(stream, k.device), o)
+                                    _ptr(status), _stream(stream, device), o)
         else:
             what = "gqa_read"
             rc = lib.gqa_read(_ptr(k), _ptr(v), _ptr(lengths), _ptr(cu_q), _ptr(slot_ids), _ptr(k_out), _ptr(v_out),
-                              _DTYPES[dtype], B, T, Hkv, D, n0, n2, code, _ptr(status), _stream(stream, k.device), o)
+                              _DTYPES[dtype], B, T, Hkv, D, n0, n2, code, _ptr(status), _stream(stream, device), o)
     _check(rc, what)
     return k_out, v_out
 
@@ -755,17 +762,14 @@ def _select(q, k_bounds, block_table, lengths, n_select, slot_ids, block_size, n
     if q.dtype not in _DTYPES or q.dim() != 3:
         raise TypeError("q must be a float32 or bfloat16 (B, Hq, D) tensor")
     B, Hq, D = q.shape
-    want = 5 if block_table is None else 4
-    if k_bounds.dtype != torch.bfloat16 or k_bounds.dim() != want or k_bounds.shape[-2] != 2 \
-            or k_bounds.shape[-1] != D:
+    kb = k_bounds.shape
+    if k_bounds.dtype != torch.bfloat16 or len(kb) != (5 if block_table is None else 4) or kb[-2] != 2 or kb[-1] != D:
         raise TypeError("k_bounds must be bfloat16, (R, Hkv, NB, 2, D) for a dense cache and (num_blocks, Hkv, 2, D) "
                         "for a paged one")
-    Hkv = k_bounds.shape[1]
+    Hkv = kb[1]
     if Hq % Hkv:
         raise ValueError("Hq must be a multiple of Hkv")
-    for name, t in (("q", q), ("k_bounds", k_bounds)):
-        if t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous and on q's device")
+    _plain(dev, q, k_bounds)
     _int32("lengths", lengths, B, dev)
     if slot_ids is not None:
         _int32("slot_ids", slot_ids, B, dev)
@@ -773,32 +777,34 @@ def _select(q, k_bounds, block_table, lengths, n_select, slot_ids, block_size, n
                                     or block_table.shape[0] != B or not block_table.is_contiguous()
                                     or block_table.get_device() != dev):
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor on q's device")
-    _status_checks(status, q.device)
+    device = q.device
+    if status is not None:
+        _status_checks(status, device)
     n_select = int(n_select)
     if selection is None:
         if n_select < 1 or block_size < 1:
             raise ValueError("n_select and block_size must be positive")
         with torch.cuda.stream(stream) if stream is not None else _HERE:
-            selection = Selection(B, Hkv, n_select, int(block_size), q.device)
+            selection = Selection(B, Hkv, n_select, int(block_size), device)
     elif (selection.B, selection.Hkv, selection.n_select, selection.block_size) != (B, Hkv, n_select, int(block_size)) \
-            or selection._buf.device != q.device:
+            or selection._buf.device != device:
         raise ValueError("selection was made for other sizes")
     ids, table, slots = selection._ptrs()
-    selection._pool = k_bounds.shape[0] * Hkv * (k_bounds.shape[2] if block_table is None else 1)
+    selection._pool = kb[0] * Hkv * (kb[2] if block_table is None else 1)
     lib = _lib.load()
-    with _on(q.device):
+    with _on(device):
         if block_table is None:
             what = "gqa_select_blocks"
             rc = lib.gqa_select_blocks(_ptr(q), _DTYPES[q.dtype], _ptr(k_bounds), _ptr(lengths), _ptr(slot_ids), ids,
-                                       table, slots, B, Hq, Hkv, D, k_bounds.shape[0], k_bounds.shape[2],
+                                       table, slots, B, Hq, Hkv, D, kb[0], kb[2],
                                        selection.block_size, n_select, int(n_first), int(n_last), _ptr(status),
-                                       _stream(stream, q.device))
+                                       _stream(stream, device))
         else:
             what = "gqa_select_blocks_paged"
             rc = lib.gqa_select_blocks_paged(_ptr(q), _DTYPES[q.dtype], _ptr(k_bounds), _ptr(block_table),
-                                             _ptr(lengths), ids, table, slots, B, Hq, Hkv, D, k_bounds.shape[0],
+                                             _ptr(lengths), ids, table, slots, B, Hq, Hkv, D, kb[0],
                                              selection.block_size, block_table.shape[1], n_select, int(n_first),
-                                             int(n_last), _ptr(status), _stream(stream, q.device))
+                                             int(n_last), _ptr(status), _stream(stream, device))
     _check(rc, what)
     return selection
 
@@ -846,21 +852,24 @@ def attend_selected(q, k_cache, v_cache, selection, *, out=None, status=None, ke
     if (D2 * 2 if dt == E2M1 else D2) != D or v_cache.shape != k_cache.shape or (B, Hkv) != (sel.B, sel.Hkv) \
             or Hq % Hkv or n2 % sel.block_size or n0 * Hkv * (n2 // sel.block_size) != sel._pool:
         raise ValueError("shape mismatch between q, the caches and the selection")
-    _status_checks(status, q.device)
-    _plain(q.get_device(), workspace)
-    o = _opts(kernel, grid_ctas, sched_pad, device=q.device, k_scale=k_scale, v_scale=v_scale, Hkv=Hkv,
+    device = q.device
+    if status is not None:
+        _status_checks(status, device)
+    if workspace is not None:
+        _plain(device.index, workspace)
+    o = _opts(kernel, grid_ctas, sched_pad, device=device, k_scale=k_scale, v_scale=v_scale, Hkv=Hkv,
               k_group_scale=k_group_scale, v_group_scale=v_group_scale)
     lib = _lib.load()
     _, table, slots = sel._ptrs()
-    with _on(q.device):
-        need = _need(lib, B * Hkv, Hq // Hkv, 1, D, dt, kernel, grid_ctas, o, q.device)
-        ws = _workspace(q.device, need, stream) if workspace is None else workspace
+    with _on(device):
+        need = _need(lib, B * Hkv, Hq // Hkv, 1, D, dt, kernel, grid_ctas, o, device)
+        ws = _workspace(device, need, stream) if workspace is None else workspace
         if out is None:
             out = torch.empty_like(q, dtype=torch.float32)
         rc = lib.gqa_attend_selected(_ptr(q), _DTYPES[q.dtype], _ptr(k_cache), _ptr(v_cache), table, slots, _ptr(out),
                                      B, Hq, Hkv, D, n0 * Hkv * (n2 // sel.block_size), sel.block_size, sel.n_select,
                                      dt, _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
-                                     _stream(stream, q.device), ctypes.byref(o))
+                                     _stream(stream, device), ctypes.byref(o))
     _check(rc, "gqa_attend_selected")
     return out
 
