@@ -26,6 +26,12 @@
 //    (Pairing two slots' values in a register took a byte permute each: 155 us
 //    for 148 on 64 rows of 512 .. 16383 slots, G = 6.) Lane (g, t) takes D / 8
 //    contiguous dims from D / 8 * g of four slots.
+//  * up to four query rows (FEW) leave half the N side free: every row has two
+//    columns there. In S^T they are the same; in O^T one takes the first
+//    element of a code pair, the other the second (the weight stands beside a
+//    zero), so the pairs enter the product as the conversion gives them: half
+//    the f16 products, sums and softmax steps (32 rows of 1024 .. 4095 slots:
+//    G = 4 37.7 -> 34.8 us, G = 1 38.5 -> 34.8).
 //  * codes become f16 by the hardware's conversion and every E2M1 x E4M3
 //    product is an f16 exactly, so K and V enter the products unrounded. A
 //    bfloat16 query is scaled by a power of two into f16's range (exact but
@@ -42,7 +48,8 @@
 //  * the new token (decode step): the warp whose tile holds slot L quantises
 //    k_new and v_new, writes them to the cache, and then copies the tile; no
 //    other warp touches slot L.
-// What bounds it. Per 16 slots a warp issues about 343 instructions (D = 128):
+// What bounds it. Per 16 slots a warp issues about 343 instructions (D = 128,
+// G > 4):
 // 64 conversions and 47 others on the ALU, 100 f16 and 57 float32 on the FMA
 // pipes, 24 matrix products. Each of these pipes takes a warp's instruction in
 // two cycles, a product in 8.3, and conversions and f16 products overlap only
@@ -72,6 +79,7 @@ constexpr int kStages = 3;                    // tiles of a warp's ring (2: page
 constexpr int kCtas = 3;                      // resident CTAs per SM: 168 registers a thread (4 of 128: 167 us)
 constexpr int kSegs = 4;                      // segments a warp's copies and products are in at once (< kStages + 1)
 constexpr int kRows = 8;                      // query rows (G <= 8)
+constexpr int kFew = 4;                       // and of the form for few
 constexpr float kLift = 7.f;                  // a reference is set this far below the maximum ...
 constexpr float kRoom = 15.f;                 // ... and holds until a score is this far above it
 
@@ -224,12 +232,12 @@ __device__ __noinline__ void append_token(const DecodeParams &p, int b, int kvh,
 // The unit's query fragments: lane (g, t) holds row g's D / 4 dims from
 // D / 4 * t, scaled by a power of two into f16's range; `mul` is the factor
 // that takes a product to a base-2 score for row g. q: the rows in shared memory.
-template <int D, bool QF32>
+template <int D, bool QF32, bool FEW>
 __device__ __forceinline__ void load_query(const DecodeParams &p, const void *q, int lane,
                                            uint32_t (&qh)[D / 16][2], uint32_t (&ql)[QF32 ? D / 16 : 1][2], float &mul)
 {
     constexpr int N = D / 4;
-    const int g = lane >> 2, t = lane & 3;
+    const int g = FEW ? lane >> 3 : lane >> 2, t = lane & 3;   // query row of column lane / 4
     float x[N];
     if constexpr (QF32) {
         const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(q) + g * D + N * t);
@@ -282,10 +290,10 @@ struct Segment {
     float ks, vs;      // its head's scales
 };
 
-template <int D, bool QF32>
+template <int D, bool QF32, bool FEW>
 constexpr int query_bytes()
 {
-    return kRows * D * (QF32 ? 4 : 2);
+    return (FEW ? kFew : kRows) * D * (QF32 ? 4 : 2);
 }
 
 // What a warp's copies are taken from.
@@ -314,17 +322,18 @@ __device__ __forceinline__ int load_page(const DecodeParams &p, const Fetch<D, P
 // The copies' segment becomes that of cursor c. The segment's query rows (rows
 // behind the G are zeros) and scales are copied too, a part by each warp, in
 // the group of the copies that comes next.
-template <int D, bool QF32, bool PAGED>
+template <int D, bool QF32, bool PAGED, bool FEW>
 __device__ __forceinline__ void enter(const DecodeParams &p, const TileCursor &c, Fetch<D, PAGED> &f, Segment *seg, int *bad,
                                       void *q, int shift, bool pages, int warp, int lane)
 {
     constexpr int B = QF32 ? 4 : 2;                // bytes an element
     constexpr int C = D * B / 16;                  // 16-byte pieces a row
+    constexpr int R = FEW ? kFew : kRows;
     const char *src = static_cast<const char *>(p.q) + ((long long)c.b * p.Hq + (long long)c.kvh * p.G) * D * B;
 #pragma unroll
-    for (int i = 0; i < (kRows * C + kThreads - 1) / kThreads; ++i) {
+    for (int i = 0; i < (R * C + kThreads - 1) / kThreads; ++i) {
         const int x = i * kThreads + warp * 32 + lane;
-        if (kRows * C % kThreads == 0 || x < kRows * C)
+        if (R * C % kThreads == 0 || x < R * C)
             copy16(smem_at(q) + x * 16, x / C < p.G ? src + x * 16 : src, x / C < p.G ? 16 : 0);
     }
     if (lane < 2) {
@@ -504,11 +513,31 @@ __device__ __forceinline__ void weigh_pair(uint32_t x, uint32_t y, __half2 sc, u
 // O^T += V^T P^T over the warp's share; w[u][0..3] are the weights in the
 // positions of the scores. The products of a share are summed from zero and
 // then added to o (the matrix unit truncates its sums).
-template <int D>
-__device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float (&w)[kSub][4], float (&o)[D / 16][4])
+// Two code pairs of slots x and y (scales sc) for few query rows: rows g and
+// g + 8 are the pairs of bytes 2 Q and 2 Q + 1, a column one element of the
+// pairs for one query; the weights' f16 (bh), then their remainders (bl).
+template <int Q>
+__device__ __forceinline__ void weigh_few(uint32_t x, uint32_t y, __half2 sc, const uint32_t (&bh)[2], const uint32_t (&bl)[2],
+                                          float (&d)[4])
+{
+    const __half2 sx = __low2half2(sc), sy = __high2half2(sc);
+    const uint32_t a0 = u32(__hmul2(h2(e2m1x2_f16<2 * Q>(x)), sx)), a1 = u32(__hmul2(h2(e2m1x2_f16<2 * Q + 1>(x)), sx));
+    const uint32_t a2 = u32(__hmul2(h2(e2m1x2_f16<2 * Q>(y)), sy)), a3 = u32(__hmul2(h2(e2m1x2_f16<2 * Q + 1>(y)), sy));
+    mma_f16(d, a0, a1, a2, a3, bh[0], bh[1]);
+    mma_f16(d, a0, a1, a2, a3, bl[0], bl[1]);
+}
+
+// O^T += V^T P^T over a warp's slots of a tile. FEW: o[i] are dims 4 i .. + 3
+// (from D / 8 * g) of query t; else dims 2 i, 2 i + 1 of queries 2t, 2t + 1.
+template <int D, bool FEW>
+__device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float (&w)[kSub][FEW ? 2 : 4],
+                                      float (&o)[D / (FEW ? 32 : 16)][4])
 {
     const int g = lane >> 2, t = lane & 3;
-    uint32_t b[kSub][4];                   // rows 2t, 2t + 1, 2t + 8, 2t + 9 of the slot side: (f16, remainder)
+    // rows 2t, 2t + 1, 2t + 8, 2t + 9 of the slot side: (f16, remainder) of a
+    // slot; FEW: (f16, 0) of a slot where the column is the pair's first
+    // element, (0, f16) where its second, and the remainders likewise
+    uint32_t b[kSub][4], br[FEW ? kSub : 1][4];
     __half2 sc[kSub][2];                   // their scales
     uint32_t v[kSub][4][D / 64];
 #pragma unroll
@@ -516,11 +545,22 @@ __device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float 
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             uint32_t h, l;
-            split2(w[u][2 * i], w[u][2 * i + 1], h, l);
+            if constexpr (FEW)
+                split2(w[u][i], w[u][i], h, l);
+            else
+                split2(w[u][2 * i], w[u][2 * i + 1], h, l);
             h = movmatrix_t(h);
             l = movmatrix_t(l);
-            b[u][2 * i] = __byte_perm(h, l, 0x5410);
-            b[u][2 * i + 1] = __byte_perm(h, l, 0x7632);
+            if constexpr (FEW) {
+                const uint32_t first = g & 1 ? 0x1044u : 0x4410u, second = g & 1 ? 0x3244u : 0x4432u;
+                b[u][2 * i] = __byte_perm(h, 0u, first);
+                b[u][2 * i + 1] = __byte_perm(h, 0u, second);
+                br[u][2 * i] = __byte_perm(l, 0u, first);
+                br[u][2 * i + 1] = __byte_perm(l, 0u, second);
+            } else {
+                b[u][2 * i] = __byte_perm(h, l, 0x5410);
+                b[u][2 * i + 1] = __byte_perm(h, l, 0x7632);
+            }
         }
         uint32_t e[4];
 #pragma unroll
@@ -541,22 +581,29 @@ __device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float 
     }
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-        float d[4][4] = {};
+        constexpr int N = FEW ? 2 : 4;
+        float d[N][4] = {};
 #pragma unroll
         for (int u = 0; u < kSub; ++u)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint32_t x = v[u][2 * j][i], y = v[u][2 * j + 1][i];
-                weigh_pair<0>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[0]);
-                weigh_pair<1>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[1]);
-                weigh_pair<2>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[2]);
-                weigh_pair<3>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[3]);
+                if constexpr (FEW) {
+                    const uint32_t bh[2] = {b[u][2 * j], b[u][2 * j + 1]}, bl[2] = {br[u][2 * j], br[u][2 * j + 1]};
+                    weigh_few<0>(x, y, sc[u][j], bh, bl, d[0]);
+                    weigh_few<1>(x, y, sc[u][j], bh, bl, d[1]);
+                } else {
+                    weigh_pair<0>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[0]);
+                    weigh_pair<1>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[1]);
+                    weigh_pair<2>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[2 % N]);
+                    weigh_pair<3>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[3 % N]);
+                }
             }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < N; ++q)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                o[4 * i + q][j] += d[q][j];
+                o[N * i + q][j] += d[q][j];
     }
 }
 
@@ -565,12 +612,13 @@ __device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float 
 template <int D>
 using Merge = MergeBufT<kRows, D == 128 ? 28 : 12>;
 
-template <int D, bool QF32, bool PAGED>
+template <int D, bool QF32, bool PAGED, bool FEW>
 __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const DecodeParams p)
 {
+    constexpr int C = FEW ? 1 : 2;             // query rows of a lane: t4, or 2t4 and 2t4 + 1
     extern __shared__ __align__(128) unsigned char dyn[];
     Stage<D>(*ring)[kWarps] = reinterpret_cast<Stage<D>(*)[kWarps]>(dyn);      // [kStages]
-    auto sm_q = reinterpret_cast<uint8_t(*)[query_bytes<D, QF32>()]>(dyn + kStages * kWarps * sizeof(Stage<D>));   // [kSegs]
+    auto sm_q = reinterpret_cast<uint8_t(*)[query_bytes<D, QF32, FEW>()]>(dyn + kStages * kWarps * sizeof(Stage<D>));   // [kSegs]
     __shared__ long long sched[kThreads / 32 + 8];
     __shared__ TileWalk walk;
     __shared__ Segment segs[kSegs];            // every warp writes the same
@@ -608,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
             if (!left)
                 return;
         }
-        enter<D, QF32>(p, c, f, &segs[0], &sm_bad[warp][0], sm_q[0], shift, pages, warp, lane);
+        enter<D, QF32, PAGED, FEW>(p, c, f, &segs[0], &sm_bad[warp][0], sm_q[0], shift, pages, warp, lane);
         __syncwarp();
     }
     auto fetch = [&](int slot) {
@@ -629,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
                 left = !p.whole_units && walk_next(p, c, walk, in_b);
                 if (left) {
                     sf = (sf + 1) % kSegs;
-                    enter<D, QF32>(p, c, f, &segs[sf], &sm_bad[warp][sf], sm_q[sf], shift, pages, warp, lane);
+                    enter<D, QF32, PAGED, FEW>(p, c, f, &segs[sf], &sm_bad[warp][sf], sm_q[sf], shift, pages, warp, lane);
                     __syncwarp();
                 }
             }
@@ -647,24 +695,25 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
     copy_wait<kStages - 2>();
     __syncthreads();
     uint32_t qh[D / 16][2], ql[QF32 ? D / 16 : 1][2];
-    float mul0, mul1;                      // product to base-2 score, rows 2t4 and 2t4 + 1
-    float m0, m1, l0, l1;
-    float o[D / 16][4];
+    float mul[C], m[C], l[C];              // product to base-2 score, reference and sum of the lane's rows
+    float o[D / (FEW ? 32 : 16)][4];
     for (int sc = 0;; sc = (sc + 1) % kSegs) {
         // the next segment
         const Segment *seg = &segs[sc];
         const bool good = seg->good;
         if (!good && tid == 0 && seg->c.t == 0 && seg->c.kvh == 0)
             report(p, row_error_bits(p, seg->c.b, seg->c.L));
-        float mul;
-        load_query<D, QF32>(p, sm_q[sc], lane, qh, ql, mul);
+        float mine;
+        load_query<D, QF32, FEW>(p, sm_q[sc], lane, qh, ql, mine);
         const float ks = seg->ks;
-        mul0 = __shfl_sync(0xffffffffu, mul, 8 * t4) * ks;
-        mul1 = __shfl_sync(0xffffffffu, mul, 8 * t4 + 4) * ks;
-        m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
+        for (int c = 0; c < C; ++c) {
+            mul[c] = __shfl_sync(0xffffffffu, mine, 8 * t4 + 4 * c) * ks;
+            m[c] = -INFINITY;
+            l[c] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < D / (FEW ? 32 : 16); ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 o[i][j] = 0.f;
@@ -696,78 +745,76 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
                         if (!attended(L, lo, P, s0 + 16 * u + slot_of(g) + 8 * i))
                             ok &= ~(1u << (2 * u + i));
             }
-            // x = base-2 score - reference
-            float x[kSub][4], top = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < kSub; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[u][i] = fmaf(s[u][i], i & 1 ? mul1 : mul0, i & 1 ? -m1 : -m0);
-                    x[u][i] = (ok >> (2 * u + (i >> 1))) & 1u ? x[u][i] : -INFINITY;
-                    top = fmaxf(top, x[u][i]);
-                }
-            if (__any_sync(0xffffffffu, top > kRoom)) {
-                float c0 = -INFINITY, c1 = -INFINITY;
+            // x = base-2 score - reference, of slots u, i and rows c
+            float x[kSub][2 * C], top = -INFINITY;
+            auto shifted = [&] {
 #pragma unroll
                 for (int u = 0; u < kSub; ++u)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        if ((ok >> (2 * u + i)) & 1u) {
-                            c0 = fmaxf(c0, s[u][2 * i] * mul0);
-                            c1 = fmaxf(c1, s[u][2 * i + 1] * mul1);
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            float &y = x[u][C * i + c];
+                            y = fmaf(s[u][2 * i + c], mul[c], -m[c]);
+                            y = (ok >> (2 * u + i)) & 1u ? y : -INFINITY;
                         }
+            };
+            shifted();
 #pragma unroll
-                for (int q = 4; q < 32; q <<= 1) {
-                    c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, q));
-                    c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, q));
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int i = 0; i < 2 * C; ++i)
+                    top = fmaxf(top, x[u][i]);
+            if (__any_sync(0xffffffffu, top > kRoom)) {
+                float r[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    float most = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if ((ok >> (2 * u + i)) & 1u)
+                                most = fmaxf(most, s[u][2 * i + c] * mul[c]);
+#pragma unroll
+                    for (int q = 4; q < 32; q <<= 1)
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, q));
+                    const float n = most - m[c] > kRoom ? most - kLift : m[c];
+                    r[c] = m[c] == -INFINITY ? 0.f : fast_ex2(m[c] - n);
+                    m[c] = n;
+                    l[c] *= r[c];
                 }
-                const float n0 = c0 - m0 > kRoom ? c0 - kLift : m0, n1 = c1 - m1 > kRoom ? c1 - kLift : m1;
-                const float r0 = m0 == -INFINITY ? 0.f : fast_ex2(m0 - n0);
-                const float r1 = m1 == -INFINITY ? 0.f : fast_ex2(m1 - n1);
-                m0 = n0;
-                m1 = n1;
-                l0 *= r0;
-                l1 *= r1;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    o[i][0] *= r0;
-                    o[i][1] *= r1;
-                    o[i][2] *= r0;
-                    o[i][3] *= r1;
-                }
+                for (int i = 0; i < D / (FEW ? 32 : 16); ++i)
 #pragma unroll
-                for (int u = 0; u < kSub; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[u][i] = fmaf(s[u][i], i & 1 ? mul1 : mul0, i & 1 ? -m1 : -m0);
-                        x[u][i] = (ok >> (2 * u + (i >> 1))) & 1u ? x[u][i] : -INFINITY;
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        o[i][j] *= r[j % C];
+                shifted();
             }
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 2 * C; ++i)
                     x[u][i] = fast_ex2(x[u][i]);
-                l0 += x[u][0] + x[u][2];
-                l1 += x[u][1] + x[u][3];
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    l[c] += x[u][c] + x[u][C + c];
             }
-            weigh<D>(st, lane, x, o);
+            weigh<D, FEW>(st, lane, x, o);
         }
 
         // the end of the segment
 #pragma unroll
-        for (int q = 4; q < 32; q <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, q);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, q);
-        }
-        // a NaN score raises no reference: keep the NaN sum in the merge
-        m0 = (l0 != l0 && m0 == -INFINITY) ? 0.f : m0;
-        m1 = (l1 != l1 && m1 == -INFINITY) ? 0.f : m1;
-        if (g == 0) {
-            sm_m[warp][2 * t4] = m0;
-            sm_m[warp][2 * t4 + 1] = m1;
-            sm_l[warp][2 * t4] = l0;
-            sm_l[warp][2 * t4 + 1] = l1;
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int q = 4; q < 32; q <<= 1)
+                l[c] += __shfl_xor_sync(0xffffffffu, l[c], q);
+            // a NaN score raises no reference: keep the NaN sum in the merge
+            m[c] = (l[c] != l[c] && m[c] == -INFINITY) ? 0.f : m[c];
+            if (g == 0) {
+                sm_m[warp][C * t4 + c] = m[c];
+                sm_l[warp][C * t4 + c] = l[c];
+            }
         }
         // the ring's slot of the last tile is free until the next segment's
         // first fetch: the warps' outputs and the merge's scratch go there
@@ -777,13 +824,21 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
         static_assert(sizeof sm_o + sizeof(Merge<D>) <= kWarps * sizeof(Stage<D>), "the slot holds both");
         __syncthreads();                   // every warp has read its part of the slot
         const float vs = seg->vs;
+        if constexpr (FEW) {
+            // row t4: dims D / 8 * g + 4 i .. + 3
 #pragma unroll
-        for (int i = 0; i < D / 16; i += 2) {
-            // rows 2t4, 2t4 + 1: dims D / 8 * g + 2 i .. + 3
-            *reinterpret_cast<float4 *>(&sm_o[warp][2 * t4][D / 8 * g + 2 * i]) =
-                make_float4(o[i][0] * vs, o[i][2] * vs, o[i + 1][0] * vs, o[i + 1][2] * vs);
-            *reinterpret_cast<float4 *>(&sm_o[warp][2 * t4 + 1][D / 8 * g + 2 * i]) =
-                make_float4(o[i][1] * vs, o[i][3] * vs, o[i + 1][1] * vs, o[i + 1][3] * vs);
+            for (int i = 0; i < D / 32; ++i)
+                *reinterpret_cast<float4 *>(&sm_o[warp][t4][D / 8 * g + 4 * i]) =
+                    make_float4(o[i][0] * vs, o[i][1] * vs, o[i][2] * vs, o[i][3] * vs);
+        } else {
+#pragma unroll
+            for (int i = 0; i < D / 16; i += 2) {
+                // rows 2t4, 2t4 + 1: dims D / 8 * g + 2 i .. + 3
+                *reinterpret_cast<float4 *>(&sm_o[warp][2 * t4][D / 8 * g + 2 * i]) =
+                    make_float4(o[i][0] * vs, o[i][2] * vs, o[i + 1][0] * vs, o[i + 1][2] * vs);
+                *reinterpret_cast<float4 *>(&sm_o[warp][2 * t4 + 1][D / 8 * g + 2 * i]) =
+                    make_float4(o[i][1] * vs, o[i][3] * vs, o[i + 1][1] * vs, o[i + 1][3] * vs);
+            }
         }
         __syncwarp();
         TileCursor cur = seg->c;
@@ -802,13 +857,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
     }
 }
 
-template <int D, bool QF32>
+template <int D, bool QF32, bool FEW>
 constexpr int dyn_bytes()
 {
-    return kWarps * kStages * (int)sizeof(Stage<D>) + kSegs * query_bytes<D, QF32>();
+    return kWarps * kStages * (int)sizeof(Stage<D>) + kSegs * query_bytes<D, QF32, FEW>();
 }
 
-template <int D, bool QF32, bool PAGED>
+template <int D, bool QF32, bool PAGED, bool FEW>
 cudaError_t launch_one(const DecodeParams *p, cudaStream_t st, int *per_sm)
 {
     // the ring's size is set once a device
@@ -819,39 +874,41 @@ cudaError_t launch_one(const DecodeParams *p, cudaStream_t st, int *per_sm)
         return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(q4_decode_kernel<D, QF32, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 dyn_bytes<D, QF32>());
+        e = cudaFuncSetAttribute(q4_decode_kernel<D, QF32, PAGED, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 dyn_bytes<D, QF32, FEW>());
         if (e != cudaSuccess)
             return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     if (!p)
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, q4_decode_kernel<D, QF32, PAGED>, kThreads,
-                                                             dyn_bytes<D, QF32>());
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, q4_decode_kernel<D, QF32, PAGED, FEW>, kThreads,
+                                                             dyn_bytes<D, QF32, FEW>());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p->grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = dyn_bytes<D, QF32>();
+    cfg.dynamicSmemBytes = dyn_bytes<D, QF32, FEW>();
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, q4_decode_kernel<D, QF32, PAGED>, *p);
+    return cudaLaunchKernelEx(&cfg, q4_decode_kernel<D, QF32, PAGED, FEW>, *p);
 }
 
-template <int D>
+template <int D, bool FEW>
 cudaError_t launch_d(bool q_bf16, bool paged, const DecodeParams *p, cudaStream_t st, int *per_sm)
 {
     if (q_bf16)
-        return paged ? launch_one<D, false, true>(p, st, per_sm) : launch_one<D, false, false>(p, st, per_sm);
-    return paged ? launch_one<D, true, true>(p, st, per_sm) : launch_one<D, true, false>(p, st, per_sm);
+        return paged ? launch_one<D, false, true, FEW>(p, st, per_sm) : launch_one<D, false, false, FEW>(p, st, per_sm);
+    return paged ? launch_one<D, true, true, FEW>(p, st, per_sm) : launch_one<D, true, false, FEW>(p, st, per_sm);
 }
 
-cudaError_t launch(int D, bool q_bf16, bool paged, const DecodeParams *p, cudaStream_t st, int *per_sm)
+cudaError_t launch(int D, int G, bool q_bf16, bool paged, const DecodeParams *p, cudaStream_t st, int *per_sm)
 {
-    return D == 128 ? launch_d<128>(q_bf16, paged, p, st, per_sm) : launch_d<64>(q_bf16, paged, p, st, per_sm);
+    if (G <= kFew)
+        return D == 128 ? launch_d<128, true>(q_bf16, paged, p, st, per_sm) : launch_d<64, true>(q_bf16, paged, p, st, per_sm);
+    return D == 128 ? launch_d<128, false>(q_bf16, paged, p, st, per_sm) : launch_d<64, false>(q_bf16, paged, p, st, per_sm);
 }
 
 }  // namespace
@@ -874,14 +931,20 @@ bool q4_whole_units(long long capacity, long long units, int grid)
 
 int q4_ctas_per_sm(int D, bool q_bf16)
 {
-    int a = 0, b = 0;
-    if (launch(D, q_bf16, false, nullptr, nullptr, &a) != cudaSuccess ||
-        launch(D, q_bf16, true, nullptr, nullptr, &b) != cudaSuccess)
-        return 1;
-    const int n = a < b ? a : b;
-    return n > 0 ? n : 1;
+    int least = 1 << 30;
+    for (int G : {kFew, kRows})
+        for (bool paged : {false, true}) {
+            int n = 0;
+            if (launch(D, G, q_bf16, paged, nullptr, nullptr, &n) != cudaSuccess)
+                return 1;
+            least = n < least ? n : least;
+        }
+    return least > 0 ? least : 1;
 }
 
-cudaError_t q4_launch(const DecodeParams &p, cudaStream_t st) { return launch(p.D, p.q_bf16, p.paged, &p, st, nullptr); }
+cudaError_t q4_launch(const DecodeParams &p, cudaStream_t st)
+{
+    return launch(p.D, p.G, p.q_bf16, p.paged, &p, st, nullptr);
+}
 
 }  // namespace gqa
