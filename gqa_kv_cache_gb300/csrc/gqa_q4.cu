@@ -27,11 +27,12 @@
 //    for 148 on 64 rows of 512 .. 16383 slots, G = 6.) Lane (g, t) takes D / 8
 //    contiguous dims from D / 8 * g of four slots.
 //  * up to four query rows (FEW) leave half the N side free: every row has two
-//    columns there. In S^T they are the same; in O^T one takes the first
-//    element of a code pair, the other the second (the weight stands beside a
-//    zero), so the pairs enter the product as the conversion gives them: half
-//    the f16 products, sums and softmax steps (32 rows of 1024 .. 4095 slots:
-//    G = 4 37.7 -> 34.8 us, G = 1 38.5 -> 34.8).
+//    columns there. In S^T they are the same (a float32 query: its f16 and its
+//    remainder); in O^T one takes the first element of a code pair, the other
+//    the second (the weight stands beside a zero), so the pairs enter the
+//    product as the conversion gives them: half the f16 products, sums and
+//    softmax steps (32 rows of 1024 .. 4095 slots: G = 4 37.7 -> 34.8 us,
+//    G = 1 38.5 -> 34.8; float32 query, 64 rows of 512 .. 16383: 147 -> 139).
 //  * codes become f16 by the hardware's conversion and every E2M1 x E4M3
 //    product is an f16 exactly, so K and V enter the products unrounded. A
 //    bfloat16 query is scaled by a power of two into f16's range (exact but
@@ -234,7 +235,7 @@ __device__ __noinline__ void append_token(const DecodeParams &p, int b, int kvh,
 // that takes a product to a base-2 score for row g. q: the rows in shared memory.
 template <int D, bool QF32, bool FEW>
 __device__ __forceinline__ void load_query(const DecodeParams &p, const void *q, int lane,
-                                           uint32_t (&qh)[D / 16][2], uint32_t (&ql)[QF32 ? D / 16 : 1][2], float &mul)
+                                           uint32_t (&qh)[D / 16][2], uint32_t (&ql)[QF32 && !FEW ? D / 16 : 1][2], float &mul)
 {
     constexpr int N = D / 4;
     const int g = FEW ? lane >> 3 : lane >> 2, t = lane & 3;   // query row of column lane / 4
@@ -274,7 +275,12 @@ __device__ __forceinline__ void load_query(const DecodeParams &p, const void *q,
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float a = x[4 * i + 2 * j] * up, b = x[4 * i + 2 * j + 1] * up;
-            if constexpr (QF32)
+            if constexpr (QF32 && FEW) {
+                // the row's first column takes the f16, its second the remainder
+                uint32_t h, l;
+                split2(a, b, h, l);
+                qh[i][j] = lane & 4 ? l : h;
+            } else if constexpr (QF32)
                 split2(a, b, qh[i][j], ql[i][j]);
             else
                 qh[i][j] = u32(__floats2half2_rn(a, b));
@@ -451,9 +457,9 @@ __device__ __forceinline__ int slot_of(int i) { return (i >> 1) + 4 * (i & 1); }
 
 // Scores of part u before their scale: s[0], s[1] slot slot_of(g) and query
 // rows 2t, 2t + 1; s[2], s[3] eight slots on.
-template <int D, bool QF32>
+template <int D, bool QF32, bool FEW>
 __device__ __forceinline__ void scores(const Stage<D> &st, int u, int lane, const uint32_t (&qh)[D / 16][2],
-                                       const uint32_t (&ql)[QF32 ? D / 16 : 1][2], float (&s)[4])
+                                       const uint32_t (&ql)[QF32 && !FEW ? D / 16 : 1][2], float (&s)[4])
 {
     const int g = lane >> 2, t = lane & 3;
     float s2[4] = {0.f, 0.f, 0.f, 0.f};
@@ -487,7 +493,7 @@ __device__ __forceinline__ void scores(const Stage<D> &st, int u, int lane, cons
         const uint32_t a3 = u32(__hmul2(h2(e2m1x2_f16<3>(k[0][w])), ma)), b3 = u32(__hmul2(h2(e2m1x2_f16<3>(k[1][w])), mb));
         mma_f16(s, a0, b0, a1, b1, qh[2 * w][0], qh[2 * w][1]);
         mma_f16(s2, a2, b2, a3, b3, qh[2 * w + 1][0], qh[2 * w + 1][1]);
-        if constexpr (QF32) {
+        if constexpr (QF32 && !FEW) {
             mma_f16(s, a0, b0, a1, b1, ql[2 * w][0], ql[2 * w][1]);
             mma_f16(s2, a2, b2, a3, b3, ql[2 * w + 1][0], ql[2 * w + 1][1]);
         }
@@ -495,6 +501,10 @@ __device__ __forceinline__ void scores(const Stage<D> &st, int u, int lane, cons
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         s[i] += s2[i];
+    if constexpr (QF32 && FEW) {
+        s[0] += s[1];
+        s[2] += s[3];
+    }
 }
 
 // One product of the sum below: the pair of dims in byte Q of the words x, y
@@ -694,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
     // the warps meet at)
     copy_wait<kStages - 2>();
     __syncthreads();
-    uint32_t qh[D / 16][2], ql[QF32 ? D / 16 : 1][2];
+    uint32_t qh[D / 16][2], ql[QF32 && !FEW ? D / 16 : 1][2];
     float mul[C], m[C], l[C];              // product to base-2 score, reference and sum of the lane's rows
     float o[D / (FEW ? 32 : 16)][4];
     for (int sc = 0;; sc = (sc + 1) % kSegs) {
@@ -733,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_decode_kernel(const Decode
             float s[kSub][4];
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
-                scores<D, QF32>(st, u, lane, qh, ql, s[u]);
+                scores<D, QF32, FEW>(st, u, lane, qh, ql, s[u]);
             // bits 2 u + i: slot 16 u + slot_of(g) + 8 i is in the softmax
             unsigned ok = good ? ~0u : 0u;
             const int s0 = share_slot(t, seg->c.tp, seg->c.gap, warp), L = seg->c.L, lo = seg->c.lo, P = seg->c.P;
