@@ -929,11 +929,11 @@ int q4_tile() { return kTile4; }
 
 // One CTA a unit, whole, where units are short: no schedule to assemble, no
 // partial states to merge. Measured back to back (G = 4, D = 128, bfloat16
-// query; one CTA a unit / the schedule, us): capacity 256: 8 units 5.7 / 9.6,
-// 512 units 13.7 / 16.6, 2048 units 34.6 / 36.2; 512: 7.5 / 10.6, 19.3 / 20.6,
-// 52.8 / 53.4; 1024: 10.9 / 11.5, 26.9 / 28.4, 80.2 / 84.3, but 512 units with
-// cold caches 43 / 39; 2048: 17.6 / 12.9, 46.9 / 45.2. So: up to four tiles, or
-// eight where all units run at once.
+// query; one CTA a unit / the schedule, us): capacity 256: 8 units 5.4 / 8.8,
+// 512 units 12.2 / 15.1, 2048 units 30.2 / 31.6; 512: 6.8 / 9.7, 16.3 / 18.8,
+// 46.6 / 47.2; 1024: 9.9 / 10.5, 23.8 / 25.6, 70.9 / 74.3, but 512 units with
+// cold caches 32.8 / 30.7; 2048: 15.7 / 12.0, 41.5 / 40.7. So: up to four
+// tiles, or eight where all units run at once.
 bool q4_whole_units(long long capacity, long long units, int grid)
 {
     return capacity <= 4 * kTile4 || (capacity <= 8 * kTile4 && units <= grid);
