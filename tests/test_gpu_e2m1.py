@@ -292,6 +292,68 @@ def test_many_short_rows():
         _check(p, _attend(p, t, grid_ctas=300), rows=range(0, 700, 7))
 
 
+FORMS = [(1, 128, torch.bfloat16), (2, 64, torch.float32), (4, 128, torch.float32), (5, 128, torch.bfloat16),
+         (8, 64, torch.bfloat16), (8, 128, torch.float32)]
+
+
+@pytest.mark.parametrize("G,D,q", FORMS)
+def test_modifiers_in_both_forms(G, D, q):
+    """Windows, prefixes, sinks and stale NaN for up to four query rows a head and for more."""
+    p = Problem("e2m1", "paged", [5, 100, 641, 900], 2 * G, 2, D, 960, bs=24, seed=50 + G, q_dtype=q)
+    t = _gpu(p)
+    sink = torch.randn(2 * G, generator=torch.Generator().manual_seed(G))
+    for window, prefix, grid in ((1, 0, 0), (130, 37, 13), (40, 300, 7)):
+        slots = [[[j for j in range(n) if j > n - 1 - window or j < prefix]] * 2 for n in p.lens]
+        kw = dict(window=window, kept_prefix=prefix, sink=sink.cuda(), grid_ctas=grid)
+        a = _attend(p, t, **kw)
+        _check(p, a, slots, sink)
+        u = {n: x.clone() for n, x in t.items()}
+        for b, n in enumerate(p.lens):
+            for j in range(-(-n // p.bs) * p.bs):
+                if j >= n or (prefix <= j <= n - 1 - window):
+                    for name in ("kg", "vg"):
+                        u[name][int(p.table[b, j // p.bs]), :, j % p.bs] = 0x7F
+        assert torch.equal(a, _attend(p, u, **kw))
+
+
+@pytest.mark.parametrize("G,D,q", FORMS)
+def test_nan_and_range_in_both_forms(G, D, q):
+    p = Problem("e2m1", "dense", [50, 300, 513], 2 * G, 2, D, 513, seed=60 + G, q_dtype=q)
+    # rows of very different size in one product
+    p.q = (p.q.float() * torch.logspace(-6, 4, 2 * G)[None, :, None]).to(q)
+    t = _gpu(p)
+    _check(p, _attend(p, t))
+    for where in ("kg", "vg"):
+        u = {n: x.clone() for n, x in t.items()}
+        u[where][1, 1, 7, 2] = 0x7F
+        for grid in (0, 3):
+            out = _attend(p, u, grid_ctas=grid).cpu()
+            _check(p, out, rows=[0, 2])
+            want, vmax, amax = p.expect(1)
+            assert (out[1, :G].double() - want[:G]).abs().max() <= attend_tolerance(D, vmax, amax)
+            bad = torch.isnan(out[1, G:])
+            assert bad.all() if where == "kg" else bad[:, 32:48].all() and not bad[:, :32].any() and not bad[:, 48:].any()
+
+
+@pytest.mark.parametrize("grid", [0, 5])
+@pytest.mark.parametrize("G,D", [(1, 128), (3, 64), (4, 128), (6, 128), (8, 64)])
+def test_decode_step_in_both_forms(G, D, grid):
+    """The appended token is attended as stored, alone and with others, in whole and cut units."""
+    lens = [0, 15, 127, 700]
+    p = Problem("e2m1", "slots", lens, 2 * G, 2, D, 701, seed=70 + G)
+    gen = torch.Generator().manual_seed(G)
+    kn, vn = (torch.randn(p.B, 2, D, generator=gen).bfloat16() for _ in range(2))
+    t = _gpu(p)
+    got = _decode(p, t, kn.cuda(), vn.cuda(), grid_ctas=grid)
+    for i, x in enumerate((kn, vn)):
+        c, s, _, _ = quantise_e2m1(x, p.g[i].view(-1, 1))
+        for b, n in enumerate(lens):
+            p.kv[i][int(p.slots[b]), :, n], p.groups[i][int(p.slots[b]), :, n] = c[b], s[b]
+    assert torch.equal(t["k"].cpu(), p.kv[0]) and torch.equal(t["vg"].cpu(), p.groups[1])
+    p.lens = [n + 1 for n in lens]
+    _check(p, got)
+
+
 def test_refusals():
     import gqa_kv_cache_gb300 as gqa
     p = Problem("e2m1", "dense", [5], 8, 2, 128, 16, seed=31)
