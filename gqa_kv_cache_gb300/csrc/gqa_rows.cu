@@ -51,11 +51,11 @@ __device__ inline Token find_token(const RowsParams &p, int t)
     const int t0 = __ldg(p.cu_q + lo), t1 = __ldg(p.cu_q + lo + 1);
     if (t < t0 || t >= t1)
         return k;                      // padding behind (or before) the rows' tokens
+    k.b = lo;
     if (t0 < 0 || t1 > p.T) {
         rows_report(p, kBadQLen);
         return k;
     }
-    k.b = lo;
     const long long L = __ldg(p.lengths + lo);
     const long long cap = p.paged ? (long long)p.max_blocks * p.block_size : (long long)p.Smax;
     if (L < 0 || L + (t1 - t0) > cap) {

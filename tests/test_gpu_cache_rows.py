@@ -417,3 +417,31 @@ def test_refusals():
     b = Case("bf16", "dense", [0], [2], 1, 24, 8)        # D not a multiple of 16
     with pytest.raises(gqa.GqaError):
         b.append()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("cu,bad,free", [([0, 2, 99], [2, 3, 4, 5], []), ([1, 3, 7], [3, 4, 5], [0]),
+                                         ([-2, 3, 5], [0, 1, 2], [5]), ([0, 2, 6], [], [])])
+def test_read_of_a_row_with_bad_offsets_is_nan(cu, bad, free, kind, dtype):
+    """A row whose offsets leave the packed tokens: its tokens among them read as
+    NaN, those of no row are left as they were, the others are right."""
+    c = Case(kind, "dense", [0, 0], [3, 3], 2, 64, 8, dtype=dtype, seed=9)
+    c.append()
+    c.cu = torch.tensor(cu, dtype=torch.int32)
+    out = [torch.full((6, 2, 64), 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.read(dtype=dtype, k_out=out[0], v_out=out[1], status=st)
+    assert int(st) == (32 if bad else 0)
+    for i, y in enumerate(out):
+        vals = cache_values(kind, c.kv[i].cpu(), None if c.groups[i] is None else c.groups[i].cpu(), c.g[i])
+        for t in range(6):
+            if t in free:
+                assert bool((y[t] == 7).all()), t
+            elif t in bad:
+                assert bool(torch.isnan(y[t]).all()), t
+            else:
+                b = max(x for x in range(2) if cu[x] <= t)
+                want = vals[b, :, t - cu[b]]
+                tol = want.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -24) * (1 + 2.0 ** -8)
+                assert bool(((y[t].double().cpu() - want).abs() <= tol).all()), t
