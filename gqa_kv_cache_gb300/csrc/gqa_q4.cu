@@ -23,6 +23,12 @@
 //    contraction 8 slots, each twice: the weight P is an f16 and an f16
 //    remainder, neighbours in the contraction, and the value stands beside
 //    both, as the doubled half of a register that its scale multiplies anyway.
+//    The remainder enters 2^12 times as large, beside the value over 2^12 (both
+//    exact), so that small weights keep their bits: a weight's error is at most
+//    2^-23 of it and 2^-37, 2^-49 of the largest weight. (With one range for
+//    both parts it was 2^-25, and 131072 slots of 2^-32.5 of the largest weight
+//    counted as nothing; G > 4 took 105.0 us for 108.5, four rows of 32768 ..
+//    131071 slots, float32 query.)
 //    (Pairing two slots' values in a register took a byte permute each: 155 us
 //    for 148 on 64 rows of 512 .. 16383 slots, G = 6.) Lane (g, t) takes D / 8
 //    contiguous dims from D / 8 * g of four slots.
@@ -33,6 +39,7 @@
 //    product as the conversion gives them: half the f16 products, sums and
 //    softmax steps (32 rows of 1024 .. 4095 slots: G = 4 37.7 -> 34.8 us,
 //    G = 1 38.5 -> 34.8; float32 query, 64 rows of 512 .. 16383: 147 -> 139).
+//    The remainders have sums of their own there (141 us for 139).
 //  * codes become f16 by the hardware's conversion and every E2M1 x E4M3
 //    product is an f16 exactly, so K and V enter the products unrounded. A
 //    bfloat16 query is scaled by a power of two into f16's range (exact but
@@ -40,9 +47,10 @@
 //    and an f16 remainder (22 bits). With P in f16 alone the output would be
 //    off by 1e-4; so it is within 4e-7 of the 64-bit result on the sizes above.
 //  * the softmax keeps a reference below the running maximum: weights are
-//    2^(s - m) with m set to max - 7 and raised only when a score passes
+//    2^(s - m) with m set to max - 12 and raised only when a score passes
 //    m + 15, so they stay within f16's range and a tile costs a vote instead
-//    of a reduction.
+//    of a reduction. (max - 14, raised at every octave: 110.6 us for 108.5 on
+//    the rows above.)
 //  * the matrix unit truncates its sums: the products of a tile are summed
 //    from zero and added to the output in float32 (truncated on, a long cache's
 //    output drifted by 3.5e-6).
@@ -81,8 +89,9 @@ constexpr int kCtas = 3;                      // resident CTAs per SM: 168 regis
 constexpr int kSegs = 4;                      // segments a warp's copies and products are in at once (< kStages + 1)
 constexpr int kRows = 8;                      // query rows (G <= 8)
 constexpr int kFew = 4;                       // and of the form for few
-constexpr float kLift = 7.f;                  // a reference is set this far below the maximum ...
+constexpr float kLift = 12.f;                 // a reference is set this far below the maximum ...
 constexpr float kRoom = 15.f;                 // ... and holds until a score is this far above it
+constexpr float kRest = 4096.f;               // a weight's remainder enters the products this much larger
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1)
@@ -110,6 +119,16 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     const float2 f = __half22float2(h);
     hi = u32(h);
     lo = u32(__floats2half2_rn(x - f.x, y - f.y));
+}
+
+// Two weights (at most 2^15) as an f16 pair and the f16 pair of kRest times what
+// it leaves: a remainder of its own range, at most 2^15 like the weight.
+__device__ __forceinline__ void split_weights(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    hi = u32(h);
+    lo = u32(__floats2half2_rn((x - f.x) * kRest, (y - f.y) * kRest));
 }
 
 // One tile's share of a warp in shared memory: its slots' codes of K and V
@@ -508,36 +527,37 @@ __device__ __forceinline__ void scores(const Stage<D> &st, int u, int lane, cons
 }
 
 // One product of the sum below: the pair of dims in byte Q of the words x, y
-// of two slots, their scales in the halves of sc, and the weights b0, b1 of
-// the two slots as (f16, remainder) pairs. The contraction runs over (slot,
-// part of the weight), so a value enters twice in a row -- the halves of a
-// register -- and is never paired with another slot's.
+// of two slots, their scales sx, sy as (s, s / kRest) pairs, and the weights
+// b0, b1 of the two slots as (f16, remainder) pairs. The contraction runs over
+// (slot, part of the weight), so a value enters twice in a row -- the halves of
+// a register, the second over kRest -- and is never paired with another slot's.
 template <int Q>
-__device__ __forceinline__ void weigh_pair(uint32_t x, uint32_t y, __half2 sc, uint32_t b0, uint32_t b1, float (&d)[4])
+__device__ __forceinline__ void weigh_pair(uint32_t x, uint32_t y, __half2 sx, __half2 sy, uint32_t b0, uint32_t b1,
+                                           float (&d)[4])
 {
     const __half2 p = h2(e2m1x2_f16<Q>(x)), q = h2(e2m1x2_f16<Q>(y));
-    mma_f16(d, u32(__hmul2(__low2half2(p), __low2half2(sc))), u32(__hmul2(__high2half2(p), __low2half2(sc))),
-            u32(__hmul2(__low2half2(q), __high2half2(sc))), u32(__hmul2(__high2half2(q), __high2half2(sc))), b0, b1);
+    mma_f16(d, u32(__hmul2(__low2half2(p), sx)), u32(__hmul2(__high2half2(p), sx)), u32(__hmul2(__low2half2(q), sy)),
+            u32(__hmul2(__high2half2(q), sy)), b0, b1);
 }
 
-// O^T += V^T P^T over the warp's share; w[u][0..3] are the weights in the
-// positions of the scores. The products of a share are summed from zero and
-// then added to o (the matrix unit truncates its sums).
 // Two code pairs of slots x and y (scales sc) for few query rows: rows g and
 // g + 8 are the pairs of bytes 2 Q and 2 Q + 1, a column one element of the
-// pairs for one query; the weights' f16 (bh), then their remainders (bl).
+// pairs for one query; the weights' f16 (bh) are summed in d, their remainders
+// (bl, kRest times as large) in r.
 template <int Q>
 __device__ __forceinline__ void weigh_few(uint32_t x, uint32_t y, __half2 sc, const uint32_t (&bh)[2], const uint32_t (&bl)[2],
-                                          float (&d)[4])
+                                          float (&d)[4], float (&r)[4])
 {
     const __half2 sx = __low2half2(sc), sy = __high2half2(sc);
     const uint32_t a0 = u32(__hmul2(h2(e2m1x2_f16<2 * Q>(x)), sx)), a1 = u32(__hmul2(h2(e2m1x2_f16<2 * Q + 1>(x)), sx));
     const uint32_t a2 = u32(__hmul2(h2(e2m1x2_f16<2 * Q>(y)), sy)), a3 = u32(__hmul2(h2(e2m1x2_f16<2 * Q + 1>(y)), sy));
     mma_f16(d, a0, a1, a2, a3, bh[0], bh[1]);
-    mma_f16(d, a0, a1, a2, a3, bl[0], bl[1]);
+    mma_f16(r, a0, a1, a2, a3, bl[0], bl[1]);
 }
 
-// O^T += V^T P^T over a warp's slots of a tile. FEW: o[i] are dims 4 i .. + 3
+// O^T += V^T P^T over a warp's slots of a tile; w[u] are the weights in the
+// positions of the scores. The products of a tile are summed from zero and then
+// added to o (the matrix unit truncates its sums). FEW: o[i] are dims 4 i .. + 3
 // (from D / 8 * g) of query t; else dims 2 i, 2 i + 1 of queries 2t, 2t + 1.
 template <int D, bool FEW>
 __device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float (&w)[kSub][FEW ? 2 : 4],
@@ -549,6 +569,7 @@ __device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float 
     // element, (0, f16) where its second, and the remainders likewise
     uint32_t b[kSub][4], br[FEW ? kSub : 1][4];
     __half2 sc[kSub][2];                   // their scales
+    [[maybe_unused]] __half2 sp[FEW ? 1 : kSub][4];   // as (s, s / kRest) (both exact: an E4M3 and one over 2^12)
     uint32_t v[kSub][4][D / 64];
 #pragma unroll
     for (int u = 0; u < kSub; ++u) {
@@ -556,9 +577,9 @@ __device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float 
         for (int i = 0; i < 2; ++i) {
             uint32_t h, l;
             if constexpr (FEW)
-                split2(w[u][i], w[u][i], h, l);
+                split_weights(w[u][i], w[u][i], h, l);
             else
-                split2(w[u][2 * i], w[u][2 * i + 1], h, l);
+                split_weights(w[u][2 * i], w[u][2 * i + 1], h, l);
             h = movmatrix_t(h);
             l = movmatrix_t(l);
             if constexpr (FEW) {
@@ -588,11 +609,20 @@ __device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float 
         }
         sc[u][0] = h2(e4m3x2_f16(e[0] | (e[1] << 8)));
         sc[u][1] = h2(e4m3x2_f16(e[2] | (e[3] << 8)));
+        if constexpr (!FEW) {
+            const __half2 parts = __floats2half2_rn(1.f, 1.f / kRest);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                sp[u][2 * j] = __hmul2(__low2half2(sc[u][j]), parts);
+                sp[u][2 * j + 1] = __hmul2(__high2half2(sc[u][j]), parts);
+            }
+        }
     }
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
         constexpr int N = FEW ? 2 : 4;
         float d[N][4] = {};
+        [[maybe_unused]] float r[N][4] = {};   // FEW: the remainders' products
 #pragma unroll
         for (int u = 0; u < kSub; ++u)
 #pragma unroll
@@ -600,20 +630,23 @@ __device__ __forceinline__ void weigh(const Stage<D> &st, int lane, const float 
                 const uint32_t x = v[u][2 * j][i], y = v[u][2 * j + 1][i];
                 if constexpr (FEW) {
                     const uint32_t bh[2] = {b[u][2 * j], b[u][2 * j + 1]}, bl[2] = {br[u][2 * j], br[u][2 * j + 1]};
-                    weigh_few<0>(x, y, sc[u][j], bh, bl, d[0]);
-                    weigh_few<1>(x, y, sc[u][j], bh, bl, d[1]);
+                    weigh_few<0>(x, y, sc[u][j], bh, bl, d[0], r[0]);
+                    weigh_few<1>(x, y, sc[u][j], bh, bl, d[1], r[1]);
                 } else {
-                    weigh_pair<0>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[0]);
-                    weigh_pair<1>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[1]);
-                    weigh_pair<2>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[2 % N]);
-                    weigh_pair<3>(x, y, sc[u][j], b[u][2 * j], b[u][2 * j + 1], d[3 % N]);
+                    weigh_pair<0>(x, y, sp[u][2 * j], sp[u][2 * j + 1], b[u][2 * j], b[u][2 * j + 1], d[0]);
+                    weigh_pair<1>(x, y, sp[u][2 * j], sp[u][2 * j + 1], b[u][2 * j], b[u][2 * j + 1], d[1]);
+                    weigh_pair<2>(x, y, sp[u][2 * j], sp[u][2 * j + 1], b[u][2 * j], b[u][2 * j + 1], d[2 % N]);
+                    weigh_pair<3>(x, y, sp[u][2 * j], sp[u][2 * j + 1], b[u][2 * j], b[u][2 * j + 1], d[3 % N]);
                 }
             }
 #pragma unroll
         for (int q = 0; q < N; ++q)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {
                 o[N * i + q][j] += d[q][j];
+                if constexpr (FEW)
+                    o[N * i + q][j] = fmaf(r[q][j], 1.f / kRest, o[N * i + q][j]);
+            }
     }
 }
 

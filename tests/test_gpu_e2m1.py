@@ -403,3 +403,39 @@ def test_values_helper_matches_torch():
     v = values_e2m1(c, s, torch.tensor([1.0]))[0]
     assert v.tolist() == [0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6]
     assert math.copysign(1, float(v[8])) == -1
+
+
+SINKS = [(1, 128, torch.bfloat16), (1, 64, torch.float32), (4, 128, torch.bfloat16), (4, 64, torch.float32),
+         (3, 128, torch.float32), (8, 128, torch.bfloat16), (8, 64, torch.float32), (6, 128, torch.float32)]
+
+
+@pytest.mark.parametrize("grid", [1, 0])
+@pytest.mark.parametrize("G,D,q_dtype", SINKS)
+def test_many_small_weights_behind_a_large_one(G, D, q_dtype, grid):
+    """Slots whose weights are 2^-30 to 2^-33 of the largest, which carries no value:
+    the output is theirs alone. grid 1: one CTA meets all of them behind the large
+    one, slots 0, 32, 64 and 96, one for each warp."""
+    import gqa_kv_cache_gb300 as gqa
+    n = 131072
+    sinks = [0, 32, 64, 96]
+    k = torch.zeros(1, 1, n, D // 2, dtype=torch.uint8)
+    v = torch.full((1, 1, n, D // 2), 0x22, dtype=torch.uint8)   # 1, 1
+    v[..., 1::2] = 0xA3                                  # 1.5, -1
+    one = torch.full((1, 1, n, D // 16), 0x38, dtype=torch.uint8)
+    k[0, 0, sinks, 0], v[0, 0, sinks] = 2, 0             # dim 0 is 1
+    octaves = [32.5, 31.5, 30.0, 33.0, 32.0, 31.0, 30.5, 32.8][:G]
+    q = torch.zeros(1, G, D)
+    q[0, :, 0] = torch.tensor(octaves) * math.log(2) * math.sqrt(D)
+    q = q.to(q_dtype)
+    t = dict(q=q, lengths=torch.tensor([n], dtype=torch.int32), k=k, v=v, kg=one, vg=one.clone(), ks=torch.ones(1),
+             vs=torch.ones(1))
+    t = {x: y.cuda() for x, y in t.items()}
+    got = gqa.attend(t["q"], t["k"], t["v"], t["lengths"], grid_ctas=grid, **_scales(t)).double().cpu()[0]
+    w = torch.exp(-q[0, :, 0].double() / math.sqrt(D))   # of the others, against the sinks' 1
+    val = torch.tensor([1.0, 1.0, 1.5, -1.0], dtype=torch.float64).repeat(D // 4)
+    want = ((n - 4) * w / (4 + (n - 4) * w))[:, None] * val
+    rel = ((got - want) / want).abs().amax(1)
+    # scores of 33 ln 2: a float32 query's 22 bits and up to four roundings, 2^-24
+    # each, are 2^-16.5 of a weight; its own error 2^-49 of the largest one is 2^-16
+    # of it; the sums' roundings 2^-16
+    assert float(rel.max()) <= 2.0 ** -14
