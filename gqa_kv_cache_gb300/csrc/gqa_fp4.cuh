@@ -99,7 +99,9 @@ __device__ __forceinline__ float over_t(float x, float t) { return t > 0.f ? __f
 // The codes of a group x with scale byte s and t, eight a word. The quotients
 // x / t come from one correctly rounded reciprocal r: a product, its exact
 // remainder and one correction (P. Markstein, IBM J. Res. Dev. 34, 1990),
-// which rounds as the division does where nothing leaves float32's range. A t
+// which rounds as the division does where nothing leaves float32's range (a
+// quotient of -0 too: the remainder is taken as p t - x and subtracted, which
+// adds -0; as x - p t it would add +0). A t
 // near its ends is first brought towards 1 with its x, by a power of two, and
 // x that the largest scale cannot reach is clamped; both are rare. x is changed.
 __device__ __forceinline__ uint2 e2m1_codes16(float (&x)[16], uint32_t s, float t)
@@ -118,8 +120,8 @@ __device__ __forceinline__ uint2 e2m1_codes16(float (&x)[16], uint32_t s, float 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float p = __fmul_rn(x[2 * i], r), q = __fmul_rn(x[2 * i + 1], r);
-        u[i >> 2] |= to_e2m1x2(__fmaf_rn(__fmaf_rn(-p, t, x[2 * i]), r, p),
-                               __fmaf_rn(__fmaf_rn(-q, t, x[2 * i + 1]), r, q))
+        u[i >> 2] |= to_e2m1x2(__fmaf_rn(-__fmaf_rn(p, t, -x[2 * i]), r, p),
+                               __fmaf_rn(-__fmaf_rn(q, t, -x[2 * i + 1]), r, q))
                      << (8 * (i & 3));
     }
     return make_uint2(u[0], u[1]);

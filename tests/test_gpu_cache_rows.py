@@ -445,3 +445,39 @@ def test_read_of_a_row_with_bad_offsets_is_nan(cu, bad, free, kind, dtype):
                 want = vals[b, :, t - cu[b]]
                 tol = want.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -24) * (1 + 2.0 ** -8)
                 assert bool(((y[t].double().cpu() - want).abs() <= tol).all()), t
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_negative_zeros_keep_their_sign(D, kind, dtype):
+    """-0.0 is stored as -0, whatever the group's other values, and by the decode step as by append."""
+    import gqa_kv_cache_gb300 as gqa
+    B, Hkv = 6, 2
+    c = Case(kind, "dense", [0] * B, [1] * B, Hkv, D, 16, dtype=dtype, seed=D)
+    for x in c.x:
+        x[:, :, ::3] = -0.0
+        x[1, :, 16:32] = -0.0                            # a group of nothing else: scale 0
+        x[2, :, 17] = -1e9                               # past the largest scale
+        x[3] *= 1e-3                                     # scales near E4M3's smallest
+        x[4, :, :16] = 0.0
+        x[4, :, 5] = -0.0
+    c.append()
+    _check_bytes(c)
+    if kind == "e2m1" and dtype == torch.bfloat16:
+        kv, gs = [torch.zeros_like(x) for x in c.kv], [torch.zeros_like(x) for x in c.groups]
+        q = torch.zeros(B, 2 * Hkv, D, dtype=dtype, device="cuda")
+        gqa.decode_step(q, c.x[0].cuda(), c.x[1].cuda(), *kv, c.lengths.cuda(), k_scale=c.g[0].cuda(),
+                        v_scale=c.g[1].cuda(), k_group_scale=gs[0], v_group_scale=gs[1])
+        assert all(torch.equal(a, b) for a, b in zip(kv + gs, c.kv + c.groups))
+
+
+@pytest.mark.parametrize("g", [1e-34, 1e30])
+def test_negative_zeros_under_extreme_scales(g):
+    c = Case("e2m1", "dense", [0], [4], 1, 32, 8, dtype=torch.float32, seed=3)
+    c.g = [torch.tensor([g], dtype=torch.float32)] * 2
+    c.x = [x * (100 * g) for x in c.x]
+    for x in c.x:
+        x[:, :, ::3] = -0.0
+    c.append()
+    _check_bytes(c)
