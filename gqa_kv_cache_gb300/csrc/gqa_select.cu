@@ -17,7 +17,9 @@
 //
 // Scores are summed in float32, which cannot order two scores that differ by
 // less than its rounding. Every score is within E of its exact value, E =
-// (adds in a row) 2^-24 sum_d |w_d| max_j |x_jd| over the unit's blocks; with T
+// (a count of roundings, derived below) 2^-24 sum_d |w_d| max |x| over the unit's
+// blocks (paged, 512 rows of heads: 57 us; 55 with half the count, which terms
+// that a matrix step drops could pass); with T
 // the n-th largest float32 score, a score above T + 2 E is kept and one below
 // T - 2 E is not, whatever the rounding. The few in between, when they do not
 // all fit, are summed again in 64 bits and ordered by that.
@@ -467,18 +469,24 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
                     least = min(least, warp_key[1][i]);
                 T = unkey32(least);
             }
-            // sum_d |w_d| |x_d| of any block is at most the sum of |w| times the
-            // largest |x|. In units of 2^-24 of it: a matrix step truncates
-            // its sum (4), E / 64 steps in a row; joining the sums, the
-            // weights' third parts and the group's queries 8 + G. 1.1 covers
-            // higher orders; a weight near float32's smallest loses its low parts
+            // sum_d |w_d| |x_d| of any block is at most M, the sum of |w| times
+            // the largest |x|. In units of 2^-24 of M: a matrix step aligns its
+            // 16 products and the sum so far to the largest of them and cuts
+            // each below 2^-25 of its power of two (as measured: 16 products of
+            // 0.498 units beside 1 add nothing, 16 of 0.996 add 8), 17 halves,
+            // and cuts its result to 24 bits, 2 more: 10.5. A sum takes E / 64
+            // steps, and what the four sums side by side are largest by is M
+            // together. Joining the sums, the weights' third parts and the
+            // group's queries: 8 + G. 1.1 covers higher orders (the second
+            // parts' sums, 2^-8 of these); a weight near float32's smallest
+            // loses its low parts
             float wsum = 0.f;
             for (int i = 0; i < NW; ++i)
                 wsum += warp_w[i];
             // where a part of a sum may have left float32's range (or a NaN is
             // met), the 64-bit sums of all of them decide
             const float most = wsum * amax;
-            const float e = most < 1e38f ? 1.1f * (float)(E / 16 + 8 + G) * 5.9604645e-8f * most + 2e-37f * amax : INFINITY;
+            const float e = most < 1e38f ? 1.1f * (float)(21 * E / 128 + 8 + G) * 5.9604645e-8f * most + 2e-37f * amax : INFINITY;
             lo = T - 2.f * e;
             hi = T + 2.f * e;
             // one rounding of each border outwards

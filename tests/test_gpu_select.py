@@ -423,3 +423,23 @@ def test_refusals():
     wide = torch.zeros(1, 2, 17000, 2, 128, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(gqa.GqaError):                    # too many blocks a row
         gqa.select_blocks(p.q.cuda(), wide, p.lengths.cuda(), 4, block_size=16)
+
+
+def test_terms_that_a_matrix_step_drops():
+    """Blocks whose scores hold a few large terms and hundreds that a sum in
+    float32's width drops one by one; all of a block's dropped terms have one sign,
+    so that its float32 score is far from the exact one."""
+    D, nb = 256, 40
+    p = Problem("bf16", "dense", [1], 2, 1, D, 16, seed=1)
+    p.lens, p.Smax = [nb * 16], nb * 16
+    p.lengths = torch.tensor(p.lens, dtype=torch.int32)
+    q, x = torch.zeros(1, 2, D), torch.zeros(1, 1, nb, 2, D)
+    small = 1.9921875 * 2.0 ** -12
+    q[0, 0], q[0, 1] = 2.0 ** -14, -2.0 ** -14           # the weights of the upper and of the lower bounds
+    x[..., 0, :], x[..., 1, :] = -small, small           # every term 2^-26 * 1.99
+    x[:, :, 1::2] *= -1                                  # of the odd blocks: below zero
+    big = [0, 4, 32, 36]                                 # a term of 1 in each of the sums side by side
+    q[0, 1, big], x[..., 0, big] = -1.0, -1.0
+    x[:, :, 1::2, 1, 128] = 15 / 32                      # and 480 * 2^-24 more, exact in any order
+    p.q, x = q.bfloat16(), x.bfloat16()
+    assert torch.equal(_select(p, x, 10, 0, 1).ids.cpu(), _want(p, x, 10, 0, 1))
