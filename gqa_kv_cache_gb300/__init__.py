@@ -734,7 +734,7 @@ class Selection:
     def __init__(self, B, Hkv, n_select, block_size, device):
         self.B, self.Hkv, self.n_select, self.block_size = B, Hkv, n_select, block_size
         self._n = B * Hkv * n_select
-        self._pool = 0      # (block, head) pairs of the cache it was made over; 0: not made yet
+        self._pool = None   # (rows, blocks a row; paged: blocks, 0) of the cache it was made over; None: not made yet
         self._buf = torch.empty(2 * self._n + B * Hkv, dtype=torch.int32, device=device)
 
     @property
@@ -790,7 +790,7 @@ def _select(q, k_bounds, block_table, lengths, n_select, slot_ids, block_size, n
             or selection._buf.device != device:
         raise ValueError("selection was made for other sizes")
     ids, table, slots = selection._ptrs()
-    selection._pool = kb[0] * Hkv * (kb[2] if block_table is None else 1)
+    selection._pool = None
     lib = _lib.load()
     with _on(device):
         if block_table is None:
@@ -806,6 +806,7 @@ def _select(q, k_bounds, block_table, lengths, n_select, slot_ids, block_size, n
                                              selection.block_size, block_table.shape[1], n_select, int(n_first),
                                              int(n_last), _ptr(status), _stream(stream, device))
     _check(rc, what)
+    selection._pool = (kb[0], kb[2] if block_table is None else 0)
     return selection
 
 
@@ -850,7 +851,8 @@ def attend_selected(q, k_cache, v_cache, selection, *, out=None, status=None, ke
     B, Hq, D = q.shape
     n0, Hkv, n2, D2 = k_cache.shape
     if (D2 * 2 if dt == E2M1 else D2) != D or v_cache.shape != k_cache.shape or (B, Hkv) != (sel.B, sel.Hkv) \
-            or Hq % Hkv or n2 % sel.block_size or n0 * Hkv * (n2 // sel.block_size) != sel._pool:
+            or Hq % Hkv or sel._pool is None \
+            or (n0, n2) != (sel._pool[0], (sel._pool[1] or 1) * sel.block_size):
         raise ValueError("shape mismatch between q, the caches and the selection")
     device = q.device
     if status is not None:

@@ -443,3 +443,38 @@ def test_terms_that_a_matrix_step_drops():
     x[:, :, 1::2, 1, 128] = 15 / 32                      # and 480 * 2^-24 more, exact in any order
     p.q, x = q.bfloat16(), x.bfloat16()
     assert torch.equal(_select(p, x, 10, 0, 1).ids.cpu(), _want(p, x, 10, 0, 1))
+
+
+def test_a_selection_of_another_shape_is_refused():
+    """As many (block, head) pairs, but other blocks: rows and blocks a row exchanged, or dense and paged."""
+    import gqa_kv_cache_gb300 as gqa
+    B, Hkv, D, bs = 2, 2, 128, 16
+    q = torch.randn(B, 4, D).bfloat16().cuda()
+    ln = torch.tensor([128, 100], dtype=torch.int32, device="cuda")
+    pool = [torch.randn(64, Hkv, bs, D).bfloat16().cuda() for _ in range(2)]
+    table = torch.arange(2 * 8, dtype=torch.int32, device="cuda").view(2, 8)
+    kept = {}
+    for R in (4, 8):
+        box = torch.zeros(R, Hkv, 64 // R, 2, D, dtype=torch.bfloat16, device="cuda")
+        kept[R] = gqa.select_blocks(q, box, ln, 4, block_size=bs)
+    kept["paged"] = gqa.select_blocks_paged(q, box.view(64, Hkv, 2, D), table, ln, 4, block_size=bs)
+    cache = {R: [x.view(R, Hkv, -1, D) for x in pool] for R in (4, 8)}
+    cache["paged"] = pool
+    for a in kept:
+        for b in cache:
+            if a == b:
+                gqa.attend_selected(q, *cache[b], kept[a])
+            else:
+                with pytest.raises(ValueError):
+                    gqa.attend_selected(q, *cache[b], kept[a])
+
+
+def test_a_selection_that_failed_is_not_attended():
+    import gqa_kv_cache_gb300 as gqa
+    p = Problem("bf16", "dense", [200, 100], 4, 2, 128, 256)
+    box, kv = _bounds(p), [x.cuda() for x in p.kv]
+    sel = gqa.Selection(2, 2, 4, 16, torch.device("cuda", 0))
+    with pytest.raises(gqa.GqaError):
+        _select(p, box, 4, 4, 4, selection=sel)
+    with pytest.raises(ValueError):
+        gqa.attend_selected(p.q.cuda(), *kv, sel)
