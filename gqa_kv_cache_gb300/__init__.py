@@ -146,24 +146,37 @@ def _stream(stream, device=None):
 
 
 _ws_cache: dict = {}
+_ws_captured: dict = {}   # (capture, workspace) of the captures under way, by stream
 
 
 def _workspace(device, nbytes, stream=None):
     """A workspace of the device and stream, zero-filled when allocated; the
     library leaves it zero-filled after every call, whatever the sizes. Calls
     on one stream run one after the other; each stream has its own, and so has
-    every call that is captured into a graph (the graph fills it with zeros
-    and may then be replayed beside any other work)."""
-    if stream is not None:
-        with torch.cuda.stream(stream):   # zero-filled before the stream's next kernel
-            return _workspace(device, nbytes)
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(max(nbytes, 1), dtype=torch.uint8, device=device)
-    handle = _stream(None, device)
+    each stream of a capture (the graph fills it with zeros before its first
+    call, and may then be replayed beside any other work)."""
+    handle = _stream(stream, device)
+    capture = 0
+    if stream is not None or torch.cuda.is_current_stream_capturing():
+        n = ctypes.c_uint64()
+        _check(_lib.load().gqa_stream_capture_id(handle, ctypes.byref(n)), "gqa_stream_capture_id")
+        capture = n.value
     key = (device, handle) if handle else device
-    buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    if capture:
+        was, buf = _ws_captured.get(key, (0, None))
+        if was == capture and buf.numel() >= nbytes:
+            return buf
+    else:
+        if _ws_captured:   # the graphs' own memory is theirs once their captures are over
+            _ws_captured.clear()
+        buf = _ws_cache.get(key)
+        if buf is not None and buf.numel() >= nbytes:
+            return buf
+    with torch.cuda.stream(stream) if stream is not None else _HERE:   # zero-filled before the stream's next kernel
+        buf = torch.zeros(max(nbytes, 1 if capture else 1 << 20), dtype=torch.uint8, device=device)
+    if capture:
+        _ws_captured[key] = capture, buf
+    else:
         _ws_cache[key] = buf
     return buf
 

@@ -15,6 +15,7 @@ SIGNATURES = {
     "gqa_status_string": (ctypes.c_char_p, [I]),
     "gqa_workspace_bytes": (Z, [I, I, I, I, I, P]),
     "gqa_workspace_reset": (I, [P, Z, P]),
+    "gqa_stream_capture_id": (I, [P, P]),
     "gqa_decode_step": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, Z, P, P]),
     "gqa_decode_step_paged": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, Z, P, P]),
     "gqa_decode_step_ex": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, Z, P, P, P]),

@@ -739,6 +739,22 @@ gqa_status gqa_workspace_reset(void *workspace, size_t workspace_bytes, void *st
                : GQA_ERR_CUDA;
 }
 
-int gqa_version(void) { return 101; }
+gqa_status gqa_stream_capture_id(void *stream, uint64_t *id)
+{
+    if (!id)
+        return GQA_ERR_INVALID_ARGUMENT;
+    *id = 0;
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    unsigned long long n = 0;
+    if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &st, &n) != cudaSuccess) {
+        cudaGetLastError();   // reported here
+        return GQA_ERR_CUDA;
+    }
+    if (st != cudaStreamCaptureStatusNone)
+        *id = n;
+    return GQA_OK;
+}
+
+int gqa_version(void) { return 102; }
 
 }  // extern "C"

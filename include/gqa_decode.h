@@ -202,6 +202,14 @@ size_t gqa_workspace_bytes(int B, int Hq, int Hkv, int D, gqa_dtype dt, const gq
 gqa_status gqa_workspace_reset(void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * *id = the number of the graph capture that `stream` takes part in, unique in
+ * the process; 0 when it is not being captured. For callers that give every
+ * captured graph a workspace of its own (calls of one stream of a capture run
+ * one after the other and can share it).
+ */
+gqa_status gqa_stream_capture_id(void *stream, uint64_t *id);
+
+/*
  * Dense or continuous-batch decode step.
  *
  *  q        (device) (B, Hq, D)          query of the new token

@@ -154,3 +154,7 @@ def test_binding_refuses_host_tensors():
         gqa.read(c, c, n, cu, 1)
     with pytest.raises(ValueError):
         gqa.select_blocks(x, torch.zeros(1, 1, 1, 2, 64, dtype=torch.bfloat16), n, 2, block_size=4)
+
+
+def test_capture_id_checks(lib):
+    assert lib.gqa_stream_capture_id(None, None) == INVALID

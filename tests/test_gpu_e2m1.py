@@ -439,3 +439,60 @@ def test_many_small_weights_behind_a_large_one(G, D, q_dtype, grid):
     # each, are 2^-16.5 of a weight; its own error 2^-49 of the largest one is 2^-16
     # of it; the sums' roundings 2^-16
     assert float(rel.max()) <= 2.0 ** -14
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e2m1"])
+def test_a_capture_fills_its_workspace_once(kind, monkeypatch):
+    """One zero-filled workspace a capture, not one a call."""
+    import gqa_kv_cache_gb300 as gqa
+    lens = [3000, 50, 2000]
+    p = Problem(kind, "dense", lens, 8, 2, 128, 3100, seed=20)
+    q, ln, kv = p.q.cuda(), p.lengths.cuda(), [x.cuda() for x in p.kv]
+    kw = {}
+    if kind == "e2m1":
+        kw = dict(k_scale=p.g[0].cuda(), v_scale=p.g[1].cuda(), k_group_scale=p.groups[0].cuda(),
+                  v_group_scale=p.groups[1].cuda())
+    want = gqa.attend(q, *kv, ln, **kw)
+    torch.cuda.synchronize()
+    made, zeros = [], torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: made.append(a) or zeros(*a, **k))
+    for turn in (1, 2):
+        g, outs = torch.cuda.CUDAGraph(), [torch.empty_like(want) for _ in range(4)]
+        with torch.cuda.graph(g):
+            for o in outs:
+                gqa.attend(q, *kv, ln, out=o, **kw)
+        assert len(made) == turn
+        for _ in range(3):
+            for o in outs:
+                o.fill_(float("nan"))
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(o, want) for o in outs)
+
+
+def test_two_streams_of_a_capture():
+    """Steps on two streams of one capture may run at once: a workspace each. Larger
+    sizes later in the capture change nothing."""
+    ps = [Problem("e2m1", "dense", [3000 - 7 * i, 50, 2000] * (1 + i), 8, 2, 128, 3100, seed=60 + i) for i in range(3)]
+    ts = [_gpu(p) for p in ps]
+    want = [_attend(p, t) for p, t in zip(ps, ts)]
+    torch.cuda.synchronize()
+    g, side, outs = torch.cuda.CUDAGraph(), torch.cuda.Stream(), [[torch.empty_like(w) for w in want] for _ in range(3)]
+    with torch.cuda.graph(g):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        for p, t, *o in zip(ps, ts, *outs):
+            _attend(p, t, out=o[0])
+            with torch.cuda.stream(side):
+                _attend(p, t, out=o[1])
+            _attend(p, t, out=o[2], stream=side)
+        here.wait_stream(side)
+    for _ in range(20):
+        for o in outs:
+            for x in o:
+                x.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(x, w) for x, w in zip(o, want))
+    assert all(torch.equal(_attend(p, t), w) for p, t, w in zip(ps, ts, want))
