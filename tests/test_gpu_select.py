@@ -478,3 +478,85 @@ def test_a_selection_that_failed_is_not_attended():
         _select(p, box, 4, 4, 4, selection=sel)
     with pytest.raises(ValueError):
         gqa.attend_selected(p.q.cuda(), *kv, sel)
+
+
+def _drawn(B, Hkv, G, D, lens, nb, bs, layout, seed, q_dtype=torch.bfloat16):
+    gen = torch.Generator().manual_seed(seed)
+    p = Problem("bf16", "dense", [1] * B, G * Hkv, Hkv, D, bs, bs=bs, seed=seed, q_dtype=q_dtype)
+    p.lens, p.Smax = lens, nb * bs
+    p.lengths = torch.tensor(lens, dtype=torch.int32)
+    if layout == "paged":
+        perm = torch.randperm(B * nb, generator=gen).view(B, nb).int()
+        held = torch.tensor([-(-n // bs) for n in lens])
+        p.table = torch.where(torch.arange(nb) < held[:, None], perm, -1)
+        shape = (B * nb, Hkv, 2, D)
+    else:
+        shape = (B, Hkv, nb, 2, D)
+    box = torch.randn(shape, generator=gen).sort(-2).values.bfloat16()
+    return p, box
+
+
+@pytest.mark.parametrize("layout", ["dense", "paged"])
+@pytest.mark.parametrize("D,G,q_dtype", [(64, 2, torch.float32), (128, 6, torch.bfloat16), (256, 1, torch.bfloat16)])
+def test_many_units(D, G, q_dtype, layout):
+    """More (row, cache head) pairs than two a multiprocessor: uneven rows, and
+    among them equal scores, scores too close for float32 (more of them than are
+    ranked directly), NaN and infinite bounds."""
+    B, Hkv, nb, bs = 64, 8, 220, 16
+    assert B * Hkv > 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    lens = [1 + (b * 997) % (nb * bs) if b % 8 else nb * bs - b for b in range(B)]
+    p, box = _drawn(B, Hkv, G, D, lens, nb, bs, layout, D, q_dtype)
+    gen = torch.Generator().manual_seed(1)
+    for b in range(0, B, 8):
+        at = (lambda h, j: (p.table[b, j].long(), h)) if layout == "paged" else (lambda h, j: (b, h, j))
+        j = torch.arange(-(-lens[b] // bs))
+        for h in range(Hkv):
+            if h % 4 == 0:
+                box[at(h, j)] = box[at(h, j[:1])]        # equal scores
+            elif h % 4 == 1:                             # a large term that cancels
+                q = p.q.view(B, Hkv, G, D)
+                q[b, h] = 0
+                q[b, h, 0, 0], q[b, h, 0, 1], q[b, h, 0, 2] = 1024.0, -1024.0, 2.0 ** -12
+                x = torch.zeros(len(j), 2, D)
+                x[..., :2] = 256.0
+                x[..., 2] = (torch.randperm(len(j), generator=gen).float() / 256)[:, None]
+                box[at(h, j)] = x.bfloat16()
+            elif h % 4 == 2:
+                box[at(h, j[40])], box[at(h, j[7])] = math.nan, math.inf
+    for n, first, last in ((5, 0, 1), (100, 2, 3)):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        assert torch.equal(_select(p, box, n, first, last, status=st).ids.cpu(), _want(p, box, n, first, last))
+        assert int(st) == 0
+
+
+@pytest.mark.parametrize("nb", [256, 300, 511])
+def test_two_ctas_a_unit(nb):
+    """Few units of 256 to 511 blocks: a cluster of two."""
+    p, box = _drawn(2, 2, 4, 128, [nb * 16, nb * 16 - 37], nb, 16, "dense", nb)
+    for n in (3, 64, 200):
+        assert torch.equal(_select(p, box, n).ids.cpu(), _want(p, box, n))
+
+
+@pytest.mark.parametrize("q_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 6, 8])
+def test_weights_of_a_bfloat16_cache_are_whole(G, q_dtype):
+    """Every eighth slot of the largest weight and no value, the others of one smaller
+    weight and the value 1: the output follows that weight, and an error of its
+    rounding is not averaged out (16 bits of it: up to 2^-17)."""
+    import gqa_kv_cache_gb300 as gqa
+    D, n, bs = 128, 1024, 64
+    q = torch.zeros(1, G, D)
+    q[0, :, 0] = torch.tensor([3.0, 5.1, 7.7, 9.3, 11.9, 13.2, 15.7, 17.3][-G:])
+    q = q.to(q_dtype)
+    k, v = torch.zeros(1, 1, n, D).bfloat16(), torch.ones(1, 1, n, D).bfloat16()
+    k[0, 0, ::8, 0], v[0, 0, ::8] = 1.0, 0.0
+    box = torch.zeros(1, 1, n // bs, 2, D, dtype=torch.bfloat16, device="cuda")
+    ln = torch.tensor([n], dtype=torch.int32, device="cuda")
+    sel = gqa.select_blocks(q.cuda(), box, ln, n // bs, block_size=bs)
+    got = gqa.attend_selected(q.cuda(), k.cuda(), v.cuda(), sel).double().cpu()[0]
+    w = 7 * torch.exp(-q[0, :, 0].double() / math.sqrt(D))
+    rel = (got / (w / (1 + w))[:, None] - 1).abs().amax(1)
+    # scores of up to 1.53: three roundings of 2^-24 are 2^-21 of a weight; its 24 bits,
+    # the exponential and the sums' roundings 2^-21 together. A float32 query enters as
+    # two bfloat16, |q - hi| <= 2^-9 |q| and |q - hi - lo| <= 2^-9 |q - hi|: 2^-18 of a score
+    assert float(rel.max()) <= 2.0 ** -20 + (1.53 * 2.0 ** -18 if q_dtype == torch.float32 else 0)
