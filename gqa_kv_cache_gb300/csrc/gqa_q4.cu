@@ -57,16 +57,18 @@
 //  * the new token (decode step): the warp whose tile holds slot L quantises
 //    k_new and v_new, writes them to the cache, and then copies the tile; no
 //    other warp touches slot L.
-// What bounds it. Per 16 slots a warp issues about 343 instructions (D = 128,
-// G > 4):
-// 64 conversions and 47 others on the ALU, 100 f16 and 57 float32 on the FMA
-// pipes, 24 matrix products. Each of these pipes takes a warp's instruction in
-// two cycles, a product in 8.3, and conversions and f16 products overlap only
-// in part (alone 7.9 cycles for four, together 12.2): 0.6 instructions a cycle
-// is what the mix reaches (0.71 for the bare conversions and products), 490
-// cycles per 16 slots and SM quarter, 5.4 TB/s of cache, 0.8 of the measured
-// HBM copy rate. More warps (four CTAs of 128 registers) or scores of one tile
-// beside the values of the one before changed nothing: it is the instructions.
+// What bounds it. Per 16 slots a warp issues about 358 instructions (D = 128,
+// G > 4): 64 conversions and 47 others on the ALU, 104 f16 and 62 float32 on
+// the FMA pipes, 24 matrix products. Each of these pipes takes a warp's
+// instruction in two cycles, a product in 8.3, and conversions and f16 products
+// overlap only in part (alone 7.9 cycles for four, together 12.2). The kernel
+// issues 0.58 instructions a cycle (16 rows of 20000 .. 24000 slots, G = 8: 102
+// us), 620 cycles per 16 slots and SM quarter, 4.0 TB/s of cache, 0.59 of the
+// measured HBM copy rate; it hardly waits for memory (long scoreboard 0.12 of an
+// issue). The bare conversions and products run at 0.71, which would be 500
+// cycles and 5 TB/s; what keeps the kernel from that is not divided into parts.
+// More warps (four CTAs of 128 registers) or scores of one tile beside the
+// values of the one before changed nothing.
 #define GQA_MULTI_TOKEN 0   // single-token steps only
 #include <cuda_fp16.h>
 

@@ -158,12 +158,13 @@ typedef struct gqa_options {
                        may be skipped, GQA_STATUS_TIMEOUT is set), every copy it issued
                        still lands before it exits, and the workspace is left
                        zero-filled. For tests of the timeout path; < 0 is
-                       GQA_ERR_INVALID_ARGUMENT                                        */
+                       GQA_ERR_INVALID_ARGUMENT. Kernels without such waits (the
+                       CUDA-core kernel, that of E2M1 caches) make nothing of it       */
     int test_stall;   /* 0: off. 1 (tests of the timeout path): every tensor-core
                        consumer warp's first wait for a tile also waits on an on-chip
                        barrier that nothing completes, so that wait runs out after
                        wait_limit_cycles (keep it short) and every CTA aborts as
-                       described above                                                 */
+                       described above; without effect on the same kernels             */
     int reserved[1];
     const float *head_sink;          /* (device) (Hq,) float32 logits, or NULL          */
     const int32_t *kept_prefix_rows; /* (device) (B,) int32 P per batch row, or NULL;
