@@ -18,11 +18,11 @@
 // Scores are summed in float32, which cannot order two scores that differ by
 // less than its rounding. Every score is within E of its exact value, E =
 // (a count of roundings, derived below) 2^-24 sum_d |w_d| max |x| over the unit's
-// blocks (paged, 512 rows of heads: 57 us; 55 with half the count, which terms
-// that a matrix step drops could pass); with T
-// the n-th largest float32 score, a score above T + 2 E is kept and one below
-// T - 2 E is not, whatever the rounding. The few in between, when they do not
-// all fit, are summed again in 64 bits and ordered by that.
+// blocks (512 units of up to 1024 blocks: 57 us; 55 with half the count, which
+// the terms that a matrix step drops could pass); with T the n-th largest
+// float32 score, a score above T + 2 E is kept and one below T - 2 E is not,
+// whatever the rounding. The few in between, when they do not all fit, are
+// summed again in 64 bits and ordered by that.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -475,11 +475,10 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 4 : 2) select_kernel(const Sel
             // each below 2^-25 of its power of two (as measured: 16 products of
             // 0.498 units beside 1 add nothing, 16 of 0.996 add 8), 17 halves,
             // and cuts its result to 24 bits, 2 more: 10.5. A sum takes E / 64
-            // steps, and what the four sums side by side are largest by is M
-            // together. Joining the sums, the weights' third parts and the
-            // group's queries: 8 + G. 1.1 covers higher orders (the second
-            // parts' sums, 2^-8 of these); a weight near float32's smallest
-            // loses its low parts
+            // steps, and the four sums side by side share M. Joining the sums,
+            // the weights' third parts and the group's queries: 8 + G. 1.1
+            // covers higher orders (the second parts' sums, 2^-8 of these); a
+            // weight near float32's smallest loses its low parts
             float wsum = 0.f;
             for (int i = 0; i < NW; ++i)
                 wsum += warp_w[i];
