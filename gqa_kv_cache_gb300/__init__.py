@@ -26,6 +26,19 @@ A cache of 4-bit E2M1 values holds D / 2 bytes a vector (``torch.uint8`` or
 besides: E4M3 bytes of the cache's shape with D // 16 last, one scale per 16
 dims (the format is the C header's GQA_DTYPE_E2M1).
 
+An 8-bit cache holds ``torch.int8`` codes with a float32 scale per (block of
+slots, cache head): ``k_block_scale`` / ``v_block_scale``, (R, Hkv, NB) for a
+dense cache (NB blocks a row) and (num_blocks, Hkv) for a paged one. The calls
+that append keep the scales; start them (and the codes) at zero.
+
+Over a bfloat16 or 8-bit cache ``score_cap`` (c tanh(s / c)), ``head_slopes``
+(float32 (Hq,): slope_h (j - L) added to the score of slot j, L the query's
+position) and ``weights`` (float32 counts, the cache's shape without D, to which
+every slot's softmax weights, summed over its head's queries, are added) extend
+``decode_step`` and ``attend`` and their paged forms. ``evict`` and
+``evict_paged`` cut rows to the slots with the largest counts, and ``rotate``
+turns queries and keys by their positions (:class:`Rotary`).
+
 ``append`` and ``append_paged`` write packed tokens into any of these caches
 without attending (and keep the key bounds of its blocks), ``read`` and
 ``read_paged`` give slots back as vectors. ``select_blocks`` and
@@ -36,6 +49,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 
 import torch
 
@@ -43,7 +57,8 @@ from . import _lib
 
 __all__ = ["decode_step", "decode_step_paged", "attend", "attend_paged", "decode_multi",
            "decode_multi_paged", "append", "append_paged", "read", "read_paged", "select_blocks",
-           "select_blocks_paged", "attend_selected", "Selection", "workspace_bytes", "validate", "validate_attend", "validate_multi",
+           "select_blocks_paged", "attend_selected", "Selection", "Rotary", "rotate", "evict", "evict_paged",
+           "workspace_bytes", "validate", "validate_attend", "validate_multi",
            "GqaError", "trace_enable", "trace_collect", "KERNELS", "library_path"]
 
 OK, INVALID_ARGUMENT, UNSUPPORTED, CUDA_ERROR, WORKSPACE = 0, 1, 2, 3, 4
@@ -51,7 +66,7 @@ KERNELS = {"auto": 0, "simt": 1, "tc": 2, "unit": 3, "tc5": 4}
 STATUS_BITS = {1: "bad length", 2: "bad slot id", 4: "bad block", 8: "timeout", 16: "bad kept prefix",
                32: "bad token offsets"}
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
-E4M3, E2M1 = 2, 3
+E4M3, E2M1, I8 = 2, 3, 4
 _GROUP = 16   # dims that share an E4M3 scale in an E2M1 cache
 _NIBBLE_DTYPES = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
 _BYTE_DTYPES = (torch.uint8,) + ((torch.float8_e4m3fn,) if hasattr(torch, "float8_e4m3fn") else ())
@@ -92,7 +107,7 @@ def _head_scale(name, t, Hkv, device):
 
 def _opts(kernel, grid_ctas, sched_pad=None, sink=None, window=0, kept_prefix=0, device=None, B=None,
           Hq=None, k_scale=None, v_scale=None, Hkv=None, wait_limit_cycles=0, test_stall=False,
-          k_group_scale=None, v_group_scale=None):
+          k_group_scale=None, v_group_scale=None, k_block_scale=None, v_block_scale=None, scale_block=0):
     """The gqa_options struct. Softmax modifiers: ``sink`` a float32 (Hq,)
     device tensor, ``window`` an int >= 0, ``kept_prefix`` an int >= 0 or an
     int32 (B,) device tensor. ``wait_limit_cycles`` > 0 shortens the
@@ -131,6 +146,10 @@ def _opts(kernel, grid_ctas, sched_pad=None, sink=None, window=0, kept_prefix=0,
     if k_group_scale is not None:
         o.k_group_scale = k_group_scale.data_ptr()
         o.v_group_scale = v_group_scale.data_ptr()
+    if k_block_scale is not None:
+        o.k_block_scale = k_block_scale.data_ptr()
+        o.v_block_scale = v_block_scale.data_ptr()
+        o.scale_block = scale_block
     return o
 
 
@@ -184,9 +203,9 @@ def _workspace(device, nbytes, stream=None):
 _need_cache: dict = {}
 
 
-def _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, device):
+def _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, device, scored=False):
     """gqa_workspace_bytes of these sizes on this device (asked once)."""
-    key = (B, Hq, Hkv, D, dt, kernel, grid_ctas, device.index)
+    key = (B, Hq, Hkv, D, dt, kernel, grid_ctas, device.index, scored)
     n = _need_cache.get(key)
     if n is None:
         n = _need_cache[key] = lib.gqa_workspace_bytes(B, Hq, Hkv, D, dt, ctypes.byref(o))
@@ -203,11 +222,14 @@ def _on(device):
 _HERE = contextlib.nullcontext()
 
 
-def workspace_bytes(B, Hq, Hkv, D, dtype=torch.bfloat16, kernel="auto", grid_ctas=0) -> int:
+def workspace_bytes(B, Hq, Hkv, D, dtype=torch.bfloat16, kernel="auto", grid_ctas=0, scored=False) -> int:
     """Workspace bytes the library needs for one step of these sizes.
-    ``dtype`` is the cache's; "e2m1" for a 4-bit cache."""
+    ``dtype`` is the cache's; "e2m1" for a 4-bit cache. ``scored``:
+    for steps over a bfloat16 cache with capped, biased or counted scores."""
     o = _opts(kernel, grid_ctas)
-    code = E2M1 if dtype == "e2m1" else E4M3 if dtype in _BYTE_DTYPES else _DTYPES[dtype]
+    if scored:
+        o.score_cap = 1.0
+    code = E2M1 if dtype == "e2m1" else I8 if dtype == torch.int8 else E4M3 if dtype in _BYTE_DTYPES else _DTYPES[dtype]
     return int(_lib.load().gqa_workspace_bytes(B, Hq, Hkv, D, code, ctypes.byref(o)))
 
 
@@ -314,6 +336,113 @@ def _step_e2m1(q, k_new, v_new, k, v, lengths, slot_ids, table, k_scale, v_scale
     return out
 
 
+def _block_scales(k, ks, vs, paged):
+    """Checks of an 8-bit cache's scales; returns the slots a block."""
+    n0, Hkv, n2, _ = k.shape
+    if ks is None or vs is None or ks.dtype != torch.float32 or vs.dtype != torch.float32:
+        raise TypeError("an int8 cache needs k_block_scale and v_block_scale, both float32")
+    if paged:
+        shape, block = (n0, Hkv), n2
+    else:
+        if ks.dim() != 3 or ks.shape[2] < 1 or n2 % ks.shape[2]:
+            raise ValueError("the block scales must be (R, Hkv, NB) with NB a divisor of Smax")
+        shape, block = (n0, Hkv, ks.shape[2]), n2 // ks.shape[2]
+    if ks.shape != shape or vs.shape != shape:
+        raise ValueError(f"the block scales must be {shape}")
+    _plain(k.get_device(), ks, vs)
+    return block
+
+
+def _step_scored(q, k_new, v_new, k, v, lengths, slot_ids, table, out, status, kernel, grid_ctas, workspace, stream,
+                 sched_pad, sink, window, kept_prefix, k_block_scale, v_block_scale, score_cap, head_slopes, weights):
+    """The decode step (k_new, v_new given) or the attend over an 8-bit cache, or
+    with capped, biased or counted scores; dense or paged (table given)."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if q.dtype not in _DTYPES or q.dim() != 3:
+        raise TypeError("q must be a float32 or bfloat16 (B, Hq, D) tensor")
+    B, Hq, D = q.shape
+    paged = table is not None
+    dt = I8 if k.dtype == torch.int8 else _DTYPES.get(k.dtype)
+    if dt != I8 and dt != _DTYPES[torch.bfloat16]:
+        raise TypeError("score_cap, head_slopes and weights need a bfloat16 or int8 cache")
+    if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or k.shape[3] != D or Hq % k.shape[1] \
+            or lengths.shape != (B,):
+        raise ValueError("shape mismatch between q, the caches and lengths")
+    n0, Hkv, n2, _ = k.shape
+    if lengths.dtype != torch.int32:
+        raise TypeError("lengths must be a contiguous int32 tensor on q's device")
+    if slot_ids is not None and (slot_ids.dtype != torch.int32 or slot_ids.shape != (B,)):
+        raise TypeError("slot_ids must be int32 of shape (B,)")
+    if paged and (table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B):
+        raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor")
+    _plain(dev, q, k, v, lengths, slot_ids, table, k_new, v_new, out, workspace)
+    if k_new is not None:
+        if q.dtype != torch.bfloat16 or k_new.dtype != torch.bfloat16 or v_new.dtype != torch.bfloat16:
+            raise TypeError("q, k_new and v_new must be bfloat16")
+        if k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D):
+            raise ValueError("shape mismatch between q, k_new and v_new")
+    if out is not None and (out.shape != q.shape or out.dtype != torch.float32):
+        raise ValueError("out must be a contiguous float32 (B, Hq, D) tensor on q's device")
+    block = 0
+    if dt == I8:
+        block = _block_scales(k, k_block_scale, v_block_scale, paged)
+    elif k_block_scale is not None or v_block_scale is not None:
+        raise TypeError("block scales belong to an int8 cache")
+    device = q.device
+    if status is not None:
+        _status_checks(status, device)
+    o = _opts(kernel, grid_ctas, sched_pad, sink, window, kept_prefix, device, B, Hq, None, None, Hkv,
+              k_block_scale=k_block_scale, v_block_scale=v_block_scale, scale_block=block)
+    if score_cap:
+        o.score_cap = score_cap
+    if head_slopes is not None:
+        if head_slopes.dtype != torch.float32 or head_slopes.shape != (Hq,):
+            raise TypeError("head_slopes must be a contiguous float32 (Hq,) tensor on q's device")
+        _plain(dev, head_slopes)
+        o.head_slopes = head_slopes.data_ptr()
+    lib = _lib.load()
+    with _on(device):
+        scratch = None
+        if weights is not None:
+            if weights.dtype != torch.float32 or weights.shape != k.shape[:3]:
+                raise TypeError("weights must be a contiguous float32 tensor of the cache's shape without D")
+            _plain(dev, weights)
+            o.weights = weights.data_ptr()
+            need = lib.gqa_weights_scratch_bytes(B, Hq, Hkv, table.shape[1] * n2 if paged else n2)
+            with torch.cuda.stream(stream) if stream is not None else _HERE:
+                scratch = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+            o.weights_scratch = scratch.data_ptr()
+            o.weights_scratch_bytes = need
+        need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, device, True)
+        ws = _workspace(device, need, stream) if workspace is None else workspace
+        if out is None:
+            with torch.cuda.stream(stream) if stream is not None else _HERE:
+                out = torch.empty(q.shape, dtype=torch.float32, device=device)
+        at, size, st, opt = ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(status), ctypes.byref(o)
+        s = _stream(stream, device)
+        if not paged:
+            if k_new is None:
+                what, code = "gqa_attend", lib.gqa_attend(
+                    q.data_ptr(), _DTYPES[q.dtype], k.data_ptr(), v.data_ptr(), lengths.data_ptr(), _ptr(slot_ids),
+                    out.data_ptr(), B, Hq, Hkv, D, n0, n2, dt, at, size, st, s, opt)
+            else:
+                what, code = "gqa_decode_step", lib.gqa_decode_step_ex(
+                    q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k.data_ptr(), v.data_ptr(), lengths.data_ptr(),
+                    _ptr(slot_ids), out.data_ptr(), B, Hq, Hkv, D, n0, n2, dt, at, size, st, s, opt)
+        elif k_new is None:
+            what, code = "gqa_attend_paged", lib.gqa_attend_paged(
+                q.data_ptr(), _DTYPES[q.dtype], k.data_ptr(), v.data_ptr(), table.data_ptr(), lengths.data_ptr(),
+                out.data_ptr(), B, Hq, Hkv, D, n0, n2, table.shape[1], dt, at, size, st, s, opt)
+        else:
+            what, code = "gqa_decode_step_paged", lib.gqa_decode_step_paged_ex(
+                q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k.data_ptr(), v.data_ptr(), table.data_ptr(),
+                lengths.data_ptr(), out.data_ptr(), B, Hq, Hkv, D, n0, n2, table.shape[1], dt, at, size, st, s, opt)
+    _check(code, what)
+    return out
+
+
 def _common_checks(q, k_new, v_new, caches, lengths, out, q_any_dtype=False):
     """Checks shared by the entry points; returns (cache gqa_dtype, out). The
     query and the new keys / values share the cache dtype, except over an E4M3
@@ -362,12 +491,24 @@ def decode_step(q, k_new, v_new, k_cache, v_cache, lengths, slot_ids=None, *, ou
                 status=None, kernel="auto", grid_ctas=0, workspace=None, stream=None, sched_pad=None,
                 sink=None, window=0, kept_prefix=0, k_scale=None, v_scale=None,
                 wait_limit_cycles=0, test_stall=False, k_group_scale=None,
-                v_group_scale=None):
+                v_group_scale=None, k_block_scale=None, v_block_scale=None,
+                score_cap=0.0, head_slopes=None, weights=None):
     """One decode step on a dense (R, Hkv, Smax, D) cache (continuous batch
     when ``slot_ids`` is given). Appends in place; returns ``out``. A
     ``workspace`` passed in must be zero-filled before its first use (the
     library leaves it zero-filled after every call). ``sink``, ``window`` and
-    ``kept_prefix`` are the softmax modifiers of the C header's gqa_options."""
+    ``kept_prefix`` are the softmax modifiers of the C header's gqa_options. Over
+    a bfloat16 or int8 cache ``score_cap``, ``head_slopes`` and ``weights`` (see
+    above); ``k_block_scale`` / ``v_block_scale`` belong to an int8 cache, whose
+    q, k_new and v_new are bfloat16."""
+    if k_cache.dtype == torch.int8 or score_cap or head_slopes is not None or weights is not None \
+            or k_block_scale is not None or v_block_scale is not None:
+        if k_scale is not None or v_scale is not None or k_group_scale is not None or v_group_scale is not None \
+                or wait_limit_cycles or test_stall:
+            raise TypeError("k_scale, group scales and the tests of the timeout path belong to other caches and kernels")
+        return _step_scored(q, k_new, v_new, k_cache, v_cache, lengths, slot_ids, None, out, status, kernel, grid_ctas,
+                            workspace, stream, sched_pad, sink, window, kept_prefix, k_block_scale, v_block_scale,
+                            score_cap, head_slopes, weights)
     if k_group_scale is not None or v_group_scale is not None:   # a 4-bit cache
         return _step_e2m1(q, k_new, v_new, k_cache, v_cache, lengths, slot_ids, None, k_scale, v_scale, k_group_scale,
                           v_group_scale, out, status, kernel, grid_ctas, workspace, stream, sched_pad, sink, window,
@@ -399,9 +540,18 @@ def decode_step_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths,
                       status=None, kernel="auto", grid_ctas=0, workspace=None, stream=None,
                       sched_pad=None, sink=None, window=0, kept_prefix=0, k_scale=None, v_scale=None,
                       wait_limit_cycles=0, test_stall=False, k_group_scale=None,
-                      v_group_scale=None):
+                      v_group_scale=None, k_block_scale=None, v_block_scale=None,
+                      score_cap=0.0, head_slopes=None, weights=None):
     """One decode step on a paged cache (num_blocks, Hkv, block_size, D) with
     a (B, max_blocks) int32 block table (-1 = unused). Appends in place."""
+    if k_blocks.dtype == torch.int8 or score_cap or head_slopes is not None or weights is not None \
+            or k_block_scale is not None or v_block_scale is not None:
+        if k_scale is not None or v_scale is not None or k_group_scale is not None or v_group_scale is not None \
+                or wait_limit_cycles or test_stall:
+            raise TypeError("k_scale, group scales and the tests of the timeout path belong to other caches and kernels")
+        return _step_scored(q, k_new, v_new, k_blocks, v_blocks, lengths, None, block_table, out, status, kernel, grid_ctas,
+                            workspace, stream, sched_pad, sink, window, kept_prefix, k_block_scale, v_block_scale,
+                            score_cap, head_slopes, weights)
     if k_group_scale is not None or v_group_scale is not None:   # a 4-bit cache
         return _step_e2m1(q, k_new, v_new, k_blocks, v_blocks, lengths, None, block_table, k_scale, v_scale, k_group_scale,
                           v_group_scale, out, status, kernel, grid_ctas, workspace, stream, sched_pad, sink, window,
@@ -435,10 +585,19 @@ def decode_step_paged(q, k_new, v_new, k_blocks, v_blocks, block_table, lengths,
 def attend(q, k_cache, v_cache, lengths, slot_ids=None, *, out=None, status=None, kernel="auto",
            grid_ctas=0, workspace=None, stream=None, sched_pad=None, sink=None, window=0,
            kept_prefix=0, k_scale=None, v_scale=None, wait_limit_cycles=0, test_stall=False, k_group_scale=None,
-           v_group_scale=None):
+           v_group_scale=None, k_block_scale=None, v_block_scale=None,
+           score_cap=0.0, head_slopes=None, weights=None):
     """Read-only attend on a dense (R, Hkv, Smax, D) cache: slots
     ``0..lengths[b]-1`` (1 <= lengths[b] <= Smax), nothing written but ``out``.
     ``q`` (B, Hq, D) is float32 or bfloat16 whatever the cache dtype."""
+    if k_cache.dtype == torch.int8 or score_cap or head_slopes is not None or weights is not None \
+            or k_block_scale is not None or v_block_scale is not None:
+        if k_scale is not None or v_scale is not None or k_group_scale is not None or v_group_scale is not None \
+                or wait_limit_cycles or test_stall:
+            raise TypeError("k_scale, group scales and the tests of the timeout path belong to other caches and kernels")
+        return _step_scored(q, None, None, k_cache, v_cache, lengths, slot_ids, None, out, status, kernel, grid_ctas,
+                            workspace, stream, sched_pad, sink, window, kept_prefix, k_block_scale, v_block_scale,
+                            score_cap, head_slopes, weights)
     if k_group_scale is not None or v_group_scale is not None:   # a 4-bit cache
         return _step_e2m1(q, None, None, k_cache, v_cache, lengths, slot_ids, None, k_scale, v_scale, k_group_scale,
                           v_group_scale, out, status, kernel, grid_ctas, workspace, stream, sched_pad, sink, window,
@@ -469,8 +628,17 @@ def attend_paged(q, k_blocks, v_blocks, block_table, lengths, *, out=None, statu
                  kernel="auto", grid_ctas=0, workspace=None, stream=None, sched_pad=None,
                  sink=None, window=0, kept_prefix=0, k_scale=None, v_scale=None,
                 wait_limit_cycles=0, test_stall=False, k_group_scale=None,
-                 v_group_scale=None):
+                 v_group_scale=None, k_block_scale=None, v_block_scale=None,
+                 score_cap=0.0, head_slopes=None, weights=None):
     """Read-only attend on a paged cache (num_blocks, Hkv, block_size, D)."""
+    if k_blocks.dtype == torch.int8 or score_cap or head_slopes is not None or weights is not None \
+            or k_block_scale is not None or v_block_scale is not None:
+        if k_scale is not None or v_scale is not None or k_group_scale is not None or v_group_scale is not None \
+                or wait_limit_cycles or test_stall:
+            raise TypeError("k_scale, group scales and the tests of the timeout path belong to other caches and kernels")
+        return _step_scored(q, None, None, k_blocks, v_blocks, lengths, None, block_table, out, status, kernel, grid_ctas,
+                            workspace, stream, sched_pad, sink, window, kept_prefix, k_block_scale, v_block_scale,
+                            score_cap, head_slopes, weights)
     if k_group_scale is not None or v_group_scale is not None:   # a 4-bit cache
         return _step_e2m1(q, None, None, k_blocks, v_blocks, lengths, None, block_table, k_scale, v_scale, k_group_scale,
                           v_group_scale, out, status, kernel, grid_ctas, workspace, stream, sched_pad, sink, window,
@@ -577,8 +745,9 @@ def _int32(name, t, n, dev):
         raise TypeError(f"{name} must be a contiguous int32 ({n},) tensor on the other tensors' device")
 
 
-def _rows_checks(caches, lengths, cu_q, slot_ids, block_table, groups, D):
-    """Checks shared by append and read; returns the cache's gqa_dtype."""
+def _rows_checks(caches, lengths, cu_q, slot_ids, block_table, groups, D, blocks):
+    """Checks shared by append and read; returns the cache's gqa_dtype and the
+    slots a block of an 8-bit cache's scales."""
     (_, k), (_, v) = caches
     dev = k.get_device()
     if dev < 0:
@@ -588,7 +757,17 @@ def _rows_checks(caches, lengths, cu_q, slot_ids, block_table, groups, D):
         raise ValueError("the two caches must be 4-dimensional and alike")
     if not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("the caches must be contiguous")
-    if groups[0] is not None or groups[1] is not None:
+    block = 0
+    if k.dtype == torch.int8:
+        code = I8
+        block = _block_scales(k, *blocks, block_table is not None)
+        if groups[0] is not None or groups[1] is not None:
+            raise TypeError("group scales belong to an E2M1 cache")
+        if shape[3] != D:
+            raise ValueError("shape mismatch between the vectors and the caches")
+    elif blocks[0] is not None or blocks[1] is not None:
+        raise TypeError("block scales belong to an int8 cache")
+    elif groups[0] is not None or groups[1] is not None:
         _group_scales(caches, *groups, D)
         code = E2M1
     else:
@@ -604,13 +783,15 @@ def _rows_checks(caches, lengths, cu_q, slot_ids, block_table, groups, D):
                                     or block_table.shape[0] != B or not block_table.is_contiguous()
                                     or block_table.get_device() != dev):
         raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor on the caches' device")
-    return code
+    return code, block
 
 
-def _rows_opts(code, Hkv, device, k_scale, v_scale, groups):
+def _rows_opts(code, Hkv, device, k_scale, v_scale, groups, blocks, block):
     """The options that carry a quantised cache's scales (None for the others)."""
     if code < E4M3:
         return None
+    if code == I8:
+        return ctypes.byref(_opts("auto", 0, k_block_scale=blocks[0], v_block_scale=blocks[1], scale_block=block))
     return ctypes.byref(_opts("auto", 0, device=device, k_scale=k_scale, v_scale=v_scale, Hkv=Hkv,
                               k_group_scale=groups[0], v_group_scale=groups[1]))
 
@@ -620,12 +801,13 @@ def _status_checks(status, device):
         raise TypeError("status must be an int32 tensor on the caches' device")
 
 
-def _append(k_new, v_new, k, v, block_table, lengths, cu_q, slot_ids, scales, groups, k_bounds, status, stream,
-            names):
+def _append(k_new, v_new, k, v, block_table, lengths, cu_q, slot_ids, scales, groups, blocks, k_bounds, status,
+            stream, names):
     if k_new.dim() != 3 or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must both be (T, Hkv, D)")
     T, Hkv, D = k_new.shape
-    code = _rows_checks(((names[0], k), (names[1], v)), lengths, cu_q, slot_ids, block_table, groups, D)
+    code, scale_block = _rows_checks(((names[0], k), (names[1], v)), lengths, cu_q, slot_ids, block_table, groups, D,
+                                     blocks)
     dev = k.get_device()
     if k_new.dtype not in _DTYPES or v_new.dtype != k_new.dtype:
         raise TypeError("k_new and v_new must both be float32 or bfloat16")
@@ -650,7 +832,7 @@ def _append(k_new, v_new, k, v, block_table, lengths, cu_q, slot_ids, scales, gr
         if k_bounds.dtype != torch.bfloat16 or k_bounds.shape != shape or not k_bounds.is_contiguous() \
                 or k_bounds.get_device() != dev:
             raise TypeError(f"k_bounds must be a contiguous bfloat16 {shape} tensor on the caches' device")
-    o = _rows_opts(code, Hkv, device, *scales, groups)
+    o = _rows_opts(code, Hkv, device, *scales, groups, blocks, scale_block)
     lib = _lib.load()
     B = lengths.shape[0]
     with _on(device):
@@ -668,30 +850,34 @@ def _append(k_new, v_new, k, v, block_table, lengths, cu_q, slot_ids, scales, gr
 
 
 def append(k_new, v_new, k_cache, v_cache, lengths, cu_q, slot_ids=None, *, k_bounds=None, k_scale=None,
-           v_scale=None, k_group_scale=None, v_group_scale=None, status=None, stream=None):
+           v_scale=None, k_group_scale=None, v_group_scale=None, k_block_scale=None, v_block_scale=None, status=None,
+           stream=None):
     """Writes the packed tokens cu_q[b] .. cu_q[b+1]-1 (``k_new``, ``v_new``
     (T, Hkv, D), float32 or bfloat16) into slots lengths[b] .. of row b of a
     dense (R, Hkv, Smax, D) cache, in place, rounded to its type. Tokens behind
     the last row are ignored. ``k_bounds``, a bfloat16 (R, Hkv, NB, 2, D)
     tensor, follows the smallest and largest key of every block of Smax // NB
-    slots for :func:`select_blocks`."""
+    slots for :func:`select_blocks` (not over an int8 cache)."""
     _append(k_new, v_new, k_cache, v_cache, None, lengths, cu_q, slot_ids, (k_scale, v_scale),
-            (k_group_scale, v_group_scale), k_bounds, status, stream, ("k_cache", "v_cache"))
+            (k_group_scale, v_group_scale), (k_block_scale, v_block_scale), k_bounds, status, stream, ("k_cache", "v_cache"))
 
 
 def append_paged(k_new, v_new, k_blocks, v_blocks, block_table, lengths, cu_q, *, k_bounds=None, k_scale=None,
-                 v_scale=None, k_group_scale=None, v_group_scale=None, status=None, stream=None):
+                 v_scale=None, k_group_scale=None, v_group_scale=None, k_block_scale=None, v_block_scale=None,
+                 status=None, stream=None):
     """:func:`append` into a paged cache (num_blocks, Hkv, block_size, D);
     ``k_bounds`` is (num_blocks, Hkv, 2, D)."""
     _append(k_new, v_new, k_blocks, v_blocks, block_table, lengths, cu_q, None, (k_scale, v_scale),
-            (k_group_scale, v_group_scale), k_bounds, status, stream, ("k_blocks", "v_blocks"))
+            (k_group_scale, v_group_scale), (k_block_scale, v_block_scale), k_bounds, status, stream, ("k_blocks", "v_blocks"))
 
 
-def _read(k, v, block_table, lengths, cu_q, T, slot_ids, dtype, k_out, v_out, scales, groups, status, stream, names):
+def _read(k, v, block_table, lengths, cu_q, T, slot_ids, dtype, k_out, v_out, scales, groups, blocks, status, stream,
+          names):
     if dtype not in _DTYPES:
         raise TypeError("dtype must be torch.float32 or torch.bfloat16")
     D = k.shape[-1] * (2 if groups[0] is not None or groups[1] is not None else 1)
-    code = _rows_checks(((names[0], k), (names[1], v)), lengths, cu_q, slot_ids, block_table, groups, D)
+    code, scale_block = _rows_checks(((names[0], k), (names[1], v)), lengths, cu_q, slot_ids, block_table, groups, D,
+                                     blocks)
     device, dev = k.device, k.get_device()
     if status is not None:
         _status_checks(status, device)
@@ -704,7 +890,7 @@ def _read(k, v, block_table, lengths, cu_q, T, slot_ids, dtype, k_out, v_out, sc
         with torch.cuda.stream(stream) if stream is not None else _HERE:
             k_out = torch.empty(shape, dtype=dtype, device=device) if k_out is None else k_out
             v_out = torch.empty(shape, dtype=dtype, device=device) if v_out is None else v_out
-    o = _rows_opts(code, Hkv, device, *scales, groups)
+    o = _rows_opts(code, Hkv, device, *scales, groups, blocks, scale_block)
     lib = _lib.load()
     B = lengths.shape[0]
     with _on(device):
@@ -722,20 +908,22 @@ def _read(k, v, block_table, lengths, cu_q, T, slot_ids, dtype, k_out, v_out, sc
 
 
 def read(k_cache, v_cache, lengths, cu_q, T, slot_ids=None, *, dtype=torch.bfloat16, k_out=None, v_out=None,
-         k_scale=None, v_scale=None, k_group_scale=None, v_group_scale=None, status=None, stream=None):
+         k_scale=None, v_scale=None, k_group_scale=None, v_group_scale=None, k_block_scale=None, v_block_scale=None,
+         status=None, stream=None):
     """Slots lengths[b] .. lengths[b] + cu_q[b+1] - cu_q[b] - 1 of row b of a
     dense cache as vectors: two (T, Hkv, D) tensors of ``dtype``, packed by
     ``cu_q`` (what :func:`append` with the same arguments wrote, rounded to the
     cache's type). Packed rows of no batch row are left as they were."""
     return _read(k_cache, v_cache, None, lengths, cu_q, T, slot_ids, dtype, k_out, v_out, (k_scale, v_scale),
-                 (k_group_scale, v_group_scale), status, stream, ("k_cache", "v_cache"))
+                 (k_group_scale, v_group_scale), (k_block_scale, v_block_scale), status, stream, ("k_cache", "v_cache"))
 
 
 def read_paged(k_blocks, v_blocks, block_table, lengths, cu_q, T, *, dtype=torch.bfloat16, k_out=None, v_out=None,
-               k_scale=None, v_scale=None, k_group_scale=None, v_group_scale=None, status=None, stream=None):
+               k_scale=None, v_scale=None, k_group_scale=None, v_group_scale=None, k_block_scale=None,
+               v_block_scale=None, status=None, stream=None):
     """:func:`read` from a paged cache (num_blocks, Hkv, block_size, D)."""
     return _read(k_blocks, v_blocks, block_table, lengths, cu_q, T, None, dtype, k_out, v_out, (k_scale, v_scale),
-                 (k_group_scale, v_group_scale), status, stream, ("k_blocks", "v_blocks"))
+                 (k_group_scale, v_group_scale), (k_block_scale, v_block_scale), status, stream, ("k_blocks", "v_blocks"))
 
 
 class Selection:
@@ -887,6 +1075,199 @@ def attend_selected(q, k_cache, v_cache, selection, *, out=None, status=None, ke
                                      _stream(stream, device), ctypes.byref(o))
     _check(rc, "gqa_attend_selected")
     return out
+
+
+# ---- rotary positions and eviction ----
+
+class Rotary:
+    """Angles of rotary positions over the first ``dim`` elements of a head:
+    pair i turns by position * f_i, f_i = base ** (-2 i / dim). ``layout``:
+    "half" (pair i is elements i and i + dim / 2) or "interleaved" (2 i and
+    2 i + 1). ``scaling`` for long contexts, a dict with ``kind``
+
+    - "linear": ``factor`` s, f / s;
+    - "ntk": ``factor`` s, base * s ** (dim / (dim - 2)) in the base's place;
+    - "bands": ``factor`` s, ``original`` length n, ``low`` and ``high``: with
+      r = n f / (2 pi) turns within the original length and u = (r - low) /
+      (high - low) clamped to 0 .. 1, f (u + (1 - u) / s); ``attention`` (1)
+      multiplies the turned elements (as do its square the scores).
+    """
+
+    def __init__(self, dim, *, base=10000.0, layout="half", scaling=None, device="cuda"):
+        dim = int(dim)
+        if dim < 2 or dim % 2:
+            raise ValueError("dim must be even and positive")
+        if layout not in ("half", "interleaved"):
+            raise ValueError("layout must be 'half' or 'interleaved'")
+        if not (base > 0 and math.isfinite(base)):
+            raise ValueError("base must be positive")
+        k = dict(scaling or {})
+        kind = k.pop("kind", None)
+        names = {None: (), "linear": ("factor",), "ntk": ("factor",),
+                 "bands": ("factor", "original", "low", "high", "attention")}
+        if kind not in names or not set(k) <= set(names[kind]) or not set(names[kind]) - {"attention"} <= set(k):
+            raise ValueError("scaling must be None or a dict with kind 'linear', 'ntk' or 'bands' and its values")
+        if any(not (v > 0 and math.isfinite(v)) for v in k.values()) or (kind == "bands" and k["high"] <= k["low"]) \
+                or (kind == "ntk" and dim == 2):
+            raise ValueError("scaling values must be positive, high above low (and dim above 2 for 'ntk')")
+        self.dim, self.layout, self.factor = dim, layout, float(k.get("attention", 1.0))
+        s = k.get("factor", 1.0)
+        freqs = []
+        for i in range(dim // 2):
+            f = (base * s ** (dim / (dim - 2)) if kind == "ntk" else base) ** (-2 * i / dim)
+            if kind == "linear":
+                f /= s
+            elif kind == "bands":
+                u = min(1.0, max(0.0, (k["original"] * f / (2 * math.pi) - k["low"]) / (k["high"] - k["low"])))
+                f *= u + (1 - u) / s
+            t = round(math.fmod(f / (2 * math.pi), 1.0) * 2 ** 64) % 2 ** 64   # of a turn
+            freqs.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+        self.freqs = torch.tensor(freqs, dtype=torch.int64, device=device)
+
+
+def rotate(q, k, rotary, positions=None, *, lengths=None, cu_q=None, q_out=None, k_out=None, status=None, stream=None):
+    """Turns queries (T, Hq, D) and keys (T, Hkv, D), float32 or bfloat16, by
+    their positions; either may be None. ``positions`` is int32 (T,); or, with
+    ``lengths`` and ``cu_q`` as in :func:`append`, token t of row b is at
+    lengths[b] + t - cu_q[b] (tokens of no row are not turned). The tensors may be
+    views whose last axis is contiguous (parts of one projection); ``q_out`` and
+    ``k_out`` may be ``q`` and ``k`` (in place). Returns (q_out, k_out)."""
+    given = [t for t in (q, k) if t is not None]
+    if not given:
+        raise ValueError("q or k must be given")
+    dt, T, D, device = given[0].dtype, given[0].shape[0], given[0].shape[-1], given[0].device
+    dev = given[0].get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if dt not in _DTYPES:
+        raise TypeError("q and k must be float32 or bfloat16")
+    if rotary.dim > D:
+        raise ValueError("the rotary dim is larger than the heads")
+    if rotary.freqs.get_device() != dev:
+        raise ValueError("rotary was made for another device")
+    strides = (ctypes.c_int64 * 8)()
+    heads, outs = [], []
+    for i, (name, t, out) in enumerate((("q", q, q_out), ("k", k, k_out))):
+        if t is None:
+            if out is not None:
+                raise ValueError(f"{name}_out without {name}")
+            heads.append(0)
+            outs.append(None)
+            continue
+        if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or t.dtype != dt or t.get_device() != dev:
+            raise ValueError("q and k must be (T, H, D) of one type on one device")
+        if out is None:
+            with torch.cuda.stream(stream) if stream is not None else _HERE:
+                out = torch.empty(t.shape, dtype=dt, device=device)
+        elif out.shape != t.shape or out.dtype != dt or out.get_device() != dev:
+            raise ValueError(f"{name}_out must be like {name}")
+        if (t.stride(2) != 1 or out.stride(2) != 1) and D > 1 and t.numel():
+            raise ValueError(f"the last axis of {name} and {name}_out must be contiguous")
+        strides[2 * i], strides[2 * i + 1] = t.stride(0), t.stride(1)
+        strides[4 + 2 * i], strides[5 + 2 * i] = out.stride(0), out.stride(1)
+        heads.append(t.shape[1])
+        outs.append(out)
+    B = 0
+    if positions is not None:
+        if lengths is not None or cu_q is not None:
+            raise ValueError("give positions, or lengths and cu_q")
+        _int32("positions", positions, T, dev)
+    else:
+        if lengths is None or cu_q is None:
+            raise ValueError("give positions, or lengths and cu_q")
+        B = lengths.shape[0]
+        _int32("lengths", lengths, B, dev)
+        _int32("cu_q", cu_q, B + 1, dev)
+    if status is not None:
+        _status_checks(status, device)
+    lib = _lib.load()
+    with _on(device):
+        rc = lib.gqa_rotate(_ptr(q), _ptr(k), _ptr(outs[0]), _ptr(outs[1]), _DTYPES[dt], strides, _ptr(positions),
+                            _ptr(lengths), _ptr(cu_q), rotary.freqs.data_ptr(), rotary.factor,
+                            int(rotary.layout == "interleaved"), B, T, heads[0], heads[1], D, rotary.dim, _ptr(status),
+                            _stream(stream, device))
+    _check(rc, "gqa_rotate")
+    return outs[0], outs[1]
+
+
+def _evict(k, v, block_table, weights, lengths, n_keep, slot_ids, n_first, n_last, k_out, v_out, weights_out, status,
+           stream):
+    dev = k.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("the two caches must be 4-dimensional and alike")
+    if k.dtype == torch.int8:
+        raise TypeError("an int8 cache cannot be evicted from: its slots share their scales")
+    code = _cache_code(k)
+    n0, Hkv, n2, D = k.shape
+    B = lengths.shape[0]
+    _int32("lengths", lengths, B, dev)
+    if slot_ids is not None:
+        _int32("slot_ids", slot_ids, B, dev)
+    if block_table is not None and (block_table.dtype != torch.int32 or block_table.dim() != 2
+                                    or block_table.shape[0] != B or not block_table.is_contiguous()
+                                    or block_table.get_device() != dev):
+        raise TypeError("block_table must be a contiguous int32 (B, max_blocks) tensor on the caches' device")
+    if weights.dtype != torch.float32 or weights.shape != k.shape[:3]:
+        raise TypeError("weights must be a contiguous float32 tensor of the cache's shape without D")
+    _plain(dev, k, v, weights, k_out, v_out, weights_out)
+    n_keep, n_first, n_last = int(n_keep), int(n_first), int(n_last)
+    if n_keep < 1 or n_first < 0 or n_last < 0 or n_first + n_last > n_keep:
+        raise ValueError("n_keep must be positive and hold n_first and n_last")
+    slots = 0
+    if k_out is not None or v_out is not None:
+        if k_out is None or v_out is None:
+            raise ValueError("give both k_out and v_out, or neither")
+        slots = k_out.shape[2] if k_out.dim() == 4 else 0
+        if slots < n_keep or k_out.shape != (B, Hkv, slots, D) or v_out.shape != k_out.shape or k_out.dtype != k.dtype \
+                or v_out.dtype != k.dtype:
+            raise ValueError("k_out and v_out must be (B, Hkv, at least n_keep, D) of the caches' type")
+    if weights_out is not None and (slots == 0 or weights_out.shape != (B, Hkv, slots)
+                                    or weights_out.dtype != torch.float32):
+        raise ValueError("weights_out must be float32 (B, Hkv, slots) beside k_out and v_out")
+    device = k.device
+    if status is not None:
+        _status_checks(status, device)
+    with torch.cuda.stream(stream) if stream is not None else _HERE:
+        ids = torch.empty((B, Hkv, n_keep), dtype=torch.int32, device=device)
+        new = torch.empty((B,), dtype=torch.int32, device=device)
+    lib = _lib.load()
+    with _on(device):
+        if block_table is None:
+            what, rc = "gqa_evict", lib.gqa_evict(
+                _ptr(k), _ptr(v), _ptr(weights), _ptr(lengths), _ptr(slot_ids), _ptr(ids), _ptr(new), _ptr(k_out),
+                _ptr(v_out), _ptr(weights_out), slots, B, Hkv, D, n0, n2, code, n_keep, n_first, n_last, _ptr(status),
+                _stream(stream, device))
+        else:
+            what, rc = "gqa_evict_paged", lib.gqa_evict_paged(
+                _ptr(k), _ptr(v), _ptr(weights), _ptr(block_table), _ptr(lengths), _ptr(ids), _ptr(new), _ptr(k_out),
+                _ptr(v_out), _ptr(weights_out), slots, B, Hkv, D, n0, n2, block_table.shape[1], code, n_keep, n_first,
+                n_last, _ptr(status), _stream(stream, device))
+    _check(rc, what)
+    return ids, new
+
+
+def evict(k_cache, v_cache, weights, lengths, n_keep, slot_ids=None, *, n_first=0, n_last=1, k_out=None, v_out=None,
+          weights_out=None, status=None, stream=None):
+    """Cuts the rows of a dense (R, Hkv, Smax, D) float32, bfloat16 or E4M3 cache
+    that hold more than ``n_keep`` slots: for every cache head the first
+    ``n_first``, the last ``n_last`` and, of the others, the slots with the
+    largest counts (``weights``, as :func:`attend` adds them up; equal ones: the
+    lowest slot) move together in ascending order, in place, or into ``k_out``,
+    ``v_out`` (B, Hkv, slots, D) and ``weights_out``, the cache then only being
+    read. Keys keep the positions that were turned into them. Returns the kept
+    slots (B, Hkv, n_keep) int32 (then -1) and the new lengths (B,)."""
+    return _evict(k_cache, v_cache, None, weights, lengths, n_keep, slot_ids, n_first, n_last, k_out, v_out,
+                  weights_out, status, stream)
+
+
+def evict_paged(k_blocks, v_blocks, block_table, weights, lengths, n_keep, *, n_first=0, n_last=1, k_out=None,
+                v_out=None, weights_out=None, status=None, stream=None):
+    """:func:`evict` from a paged cache (num_blocks, Hkv, block_size, D), in
+    place into the first blocks of every row, or into dense outputs."""
+    return _evict(k_blocks, v_blocks, block_table, weights, lengths, n_keep, None, n_first, n_last, k_out, v_out,
+                  weights_out, status, stream)
 
 
 def validate_multi(lengths, cu_q, T, *, slot_ids=None, R=None, Smax=None, block_table=None,

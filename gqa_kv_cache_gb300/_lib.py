@@ -36,6 +36,10 @@ SIGNATURES = {
     "gqa_select_blocks": (I, [P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P]),
     "gqa_select_blocks_paged": (I, [P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P]),
     "gqa_attend_selected": (I, [P, I, P, P, P, P, P, I, I, I, I, I, I, I, I, P, Z, P, P, P]),
+    "gqa_weights_scratch_bytes": (Z, [I, I, I, ctypes.c_longlong]),
+    "gqa_rotate": (I, [P, P, P, P, I, P, P, P, P, P, ctypes.c_float, I, I, I, I, I, I, I, P, P]),
+    "gqa_evict": (I, [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P]),
+    "gqa_evict_paged": (I, [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, P, P]),
     "gqa_trace_enable": (I, [I]),
     "gqa_trace_collect": (I, [I, P, P]),
     "gqa_kernel_name": (ctypes.c_char_p, [I]),
@@ -52,7 +56,11 @@ class GqaOptions(ctypes.Structure):
                 ("test_stall", ctypes.c_int), ("reserved", ctypes.c_int * 1),
                 ("head_sink", ctypes.c_void_p), ("kept_prefix_rows", ctypes.c_void_p),
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
-                ("k_group_scale", ctypes.c_void_p), ("v_group_scale", ctypes.c_void_p)]
+                ("k_group_scale", ctypes.c_void_p), ("v_group_scale", ctypes.c_void_p),
+                ("k_block_scale", ctypes.c_void_p), ("v_block_scale", ctypes.c_void_p),
+                ("scale_block", ctypes.c_int), ("score_cap", ctypes.c_float),
+                ("head_slopes", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("weights_scratch", ctypes.c_void_p), ("weights_scratch_bytes", ctypes.c_size_t)]
 
 
 _lock = threading.Lock()

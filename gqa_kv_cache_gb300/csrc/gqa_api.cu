@@ -41,6 +41,13 @@ bool unit_ok(gqa_dtype dt, int D, int G, long long cap_rows, bool multi)
            unit_supports(dt == GQA_DTYPE_BF16, D, G, cap_rows);
 }
 
+// Whether the scored attend runs the step: an 8-bit cache, or scores that are
+// capped, biased or counted.
+bool is_scored(gqa_dtype dt, const gqa_options *opt)
+{
+    return dt == GQA_DTYPE_I8 || (opt && (opt->score_cap > 0.f || opt->head_slopes || opt->weights));
+}
+
 // Kernel the call will use (GQA_KERNEL_SIMT / _TC / _UNIT) or -1. AUTO takes
 // the small-cache kernel when it applies and the units (B * Hkv, known > 0)
 // fit in one wave of it; else the tensor-core kernel where it applies, else
@@ -48,6 +55,10 @@ bool unit_ok(gqa_dtype dt, int D, int G, long long cap_rows, bool multi)
 int pick_kernel(const gqa_options *opt, gqa_dtype dt, int D, int G, bool paged, int block_size,
                 long long cap_rows = -1, bool multi = false, long long units = 0)
 {
+    if (is_scored(dt, opt))     // one kernel, on the tensor cores
+        return (!opt || opt->kernel == GQA_KERNEL_AUTO || opt->kernel == GQA_KERNEL_TC) && !multi && scored_supports(dt, D, G)
+                   ? GQA_KERNEL_TC
+                   : -1;
     if (dt == GQA_DTYPE_E2M1)   // one kernel, on the tensor cores
         return (!opt || opt->kernel == GQA_KERNEL_AUTO || opt->kernel == GQA_KERNEL_TC) && !multi && q4_supports(D, G)
                    ? GQA_KERNEL_TC
@@ -91,6 +102,14 @@ int grid_for(int kernel, const gqa_options *opt, gqa_dtype dt, int D, int G, gqa
     if (cudaGetDevice(&dev) != cudaSuccess)
         return 0;
     const int sms = sm_count(dev);
+    if (is_scored(dt, opt)) {
+        static std::atomic<int> per_sm[2][2][2][2];   // by kind, D, rows, query type
+        std::atomic<int> &c = per_sm[dt == GQA_DTYPE_I8][D == 128][G <= 4][q_dt == GQA_DTYPE_BF16];
+        int n = c.load(std::memory_order_relaxed);
+        if (!n)
+            c.store(n = scored_ctas_per_sm(dt, D, G, q_dt == GQA_DTYPE_BF16), std::memory_order_relaxed);
+        return sms * n;
+    }
     if (dt == GQA_DTYPE_E2M1) {
         // (a bfloat16 query's grid is the larger one: it sizes the workspace)
         static std::atomic<int> per_sm[2][2];   // by D, query type
@@ -251,7 +270,8 @@ gqa_status check_shape(const Shape &s)
 {
     if (s.B < 0 || s.Hq < 1 || s.Hkv < 1 || s.D < 1 || s.Hq % s.Hkv != 0)
         return GQA_ERR_INVALID_ARGUMENT;
-    if ((!valid_dtype(s.dt) && s.dt != GQA_DTYPE_E4M3 && s.dt != GQA_DTYPE_E2M1) || !valid_dtype(s.q_dt))
+    if ((!valid_dtype(s.dt) && s.dt != GQA_DTYPE_E4M3 && s.dt != GQA_DTYPE_E2M1 && s.dt != GQA_DTYPE_I8) ||
+        !valid_dtype(s.q_dt))
         return GQA_ERR_INVALID_ARGUMENT;
     if (s.paged) {
         if (s.num_blocks < 1 || s.block_size < 1 || s.max_blocks < 1)
@@ -266,6 +286,76 @@ gqa_status check_shape(const Shape &s)
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The scored attend (after the new tokens' write, in the decode step).
+cudaError_t run_scored(const Shape &s, const DecodeParams &d, const gqa_options *opt, long long cap_rows, cudaStream_t st)
+{
+    if (!s.attend) {
+        RowsParams r = {};
+        r.k_new = d.k_new;
+        r.v_new = d.v_new;
+        r.k_cache = d.k_cache;
+        r.v_cache = d.v_cache;
+        r.lengths = d.lengths;
+        r.slot_ids = d.slot_ids;
+        r.block_table = d.block_table;
+        r.status = d.status;
+        r.vec_bf16 = 1;
+        r.B = r.T = s.B;
+        r.Hkv = s.Hkv;
+        r.D = s.D;
+        r.R = s.R;
+        r.Smax = s.Smax;
+        r.paged = s.paged;
+        r.num_blocks = s.num_blocks;
+        r.block_size = s.block_size;
+        r.max_blocks = s.max_blocks;
+        cudaError_t e;
+        if (s.dt == GQA_DTYPE_I8) {
+            r.k_block_scale = opt->k_block_scale;
+            r.v_block_scale = opt->v_block_scale;
+            r.scale_block = s.paged ? s.block_size : opt->scale_block;
+            int dev = 0;
+            e = cudaGetDevice(&dev);
+            if (e == cudaSuccess)
+                e = rows_launch(r, GQA_DTYPE_I8, true, sm_count(dev), st);
+        } else {
+            e = tokens_launch(r, st);
+        }
+        if (e != cudaSuccess)
+            return e;
+    }
+    ScoredParams p = {};
+    static_cast<DecodeParams &>(p) = d;
+    p.kind = s.dt;
+    p.scale_shift = -1;
+    p.scale_block = 1;
+    if (s.dt == GQA_DTYPE_I8) {
+        p.k_block_scale = opt->k_block_scale;
+        p.v_block_scale = opt->v_block_scale;
+        p.scale_block = s.paged ? s.block_size : opt->scale_block;
+        for (int i = 0; i < 31; ++i)
+            if (1 << i == p.scale_block)
+                p.scale_shift = i;
+    }
+    if (opt) {
+        if (opt->score_cap > 0.f) {
+            p.cap = (float)(1.4426950408889634 * opt->score_cap);
+            p.scale_cap = (float)(1.0 / (std::sqrt((double)s.D) * opt->score_cap));
+        }
+        p.slopes = opt->head_slopes;
+        p.weights = opt->weights;
+    }
+    p.gp = d.G <= 4 ? 4 : 8;
+    p.xs_cap = cap_rows;
+    if (p.weights) {
+        p.xs = static_cast<float *>(opt->weights_scratch);
+        p.row_end = reinterpret_cast<float2 *>(static_cast<char *>(opt->weights_scratch) +
+                                               align_up((size_t)s.B * s.Hkv * (size_t)cap_rows * p.gp * sizeof(float), 256));
+    }
+    return scored_launch(p, st);
+}
 
 gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void *v_new, void *kc,
                     void *vc, const int32_t *lengths, const int32_t *slot_ids,
@@ -301,17 +391,33 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
         return GQA_ERR_INVALID_ARGUMENT;
     if (!s.attend && (!aligned16(k_new) || !aligned16(v_new)))
         return GQA_ERR_INVALID_ARGUMENT;
+    const bool kvi = s.dt == GQA_DTYPE_I8;
+    if (opt && (!(opt->score_cap >= 0.f && opt->score_cap <= 3.402823466e38f) || !aligned4(opt->head_slopes) ||
+                !aligned4(opt->weights)))
+        return GQA_ERR_INVALID_ARGUMENT;
+    if (kvi && (!opt || !opt->k_block_scale || !opt->v_block_scale || !aligned4(opt->k_block_scale) ||
+                !aligned4(opt->v_block_scale) ||
+                (!s.paged && (opt->scale_block < 1 || s.Smax % opt->scale_block))))
+        return GQA_ERR_INVALID_ARGUMENT;
     const int Gh = s.Hq / s.Hkv;
     if (s.multi && Gh > 8)
         return GQA_ERR_UNSUPPORTED;
     const long long cap_rows = s.paged ? (long long)s.max_blocks * s.block_size : (long long)s.Smax;
-    // the E2M1 kernel numbers the cache's vectors in 32 bits
-    if (kv4 && (s.paged ? (double)s.num_blocks * s.Hkv * s.block_size : (double)s.R * s.Hkv * s.Smax) >= 4294967296.0)
+    // the E2M1 and the scored kernel number the cache's vectors in 32 bits
+    const bool scored = is_scored(s.dt, opt);
+    if ((kv4 || scored) && (s.paged ? (double)s.num_blocks * s.Hkv * s.block_size : (double)s.R * s.Hkv * s.Smax) >= 4294967296.0)
         return GQA_ERR_UNSUPPORTED;
     const int kernel = pick_kernel(opt, s.dt, s.D, Gh, s.paged, s.block_size, cap_rows, s.multi,
                                    (long long)s.B * s.Hkv);
     if (kernel < 0)
         return GQA_ERR_UNSUPPORTED;
+    if (opt && opt->weights) {
+        if (scored_count_ctas(s.B, s.Hkv, cap_rows) > INT_MAX)
+            return GQA_ERR_UNSUPPORTED;
+        if (!opt->weights_scratch || !aligned16(opt->weights_scratch) ||
+            opt->weights_scratch_bytes < scored_scratch_bytes(s.B, s.Hq, s.Hkv, cap_rows))
+            return GQA_ERR_WORKSPACE;
+    }
     const MultiCut cut = s.multi ? multi_cut(Gh, s.max_q, kernel == GQA_KERNEL_TC ? 32 : 8) : MultiCut{1, 1};
     const int G = Gh * cut.tpc;             // query rows of a unit
     const int Bv = s.B * cut.chunks;        // (virtual) rows of the schedule
@@ -370,12 +476,13 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
         p.kept_prefix = opt->kept_prefix;
         p.kept_prefix_rows = opt->kept_prefix_rows;
     }
-    p.tile = kv4 ? q4_tile() : kernel == GQA_KERNEL_TC ? tc_tile() : simt_tile();
+    p.tile = scored ? scored_tile(s.dt, s.D) : kv4 ? q4_tile() : kernel == GQA_KERNEL_TC ? tc_tile() : simt_tile();
     // about the time a CTA spends finishing a sequence, in tiles of streaming
     p.pad_tiles = (opt && opt->sched_pad > 0) ? opt->sched_pad - 1 : kDefaultSchedPad;
     p.grid = grid;
-    if (kv4 && opt->grid_ctas <= 0 && (long long)p.B * p.Hkv < INT_MAX &&
-        q4_whole_units(cap_rows, (long long)p.B * p.Hkv, grid)) {
+    if ((kv4 || scored) && (!opt || opt->grid_ctas <= 0) && (long long)p.B * p.Hkv < INT_MAX &&
+        (scored ? scored_whole_units(s.dt, s.D, cap_rows, (long long)p.B * p.Hkv, grid)
+                : q4_whole_units(cap_rows, (long long)p.B * p.Hkv, grid))) {
         p.whole_units = 1;
         p.grid = p.B * p.Hkv;
     }
@@ -391,7 +498,10 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
 
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (kv4) {
+    if (scored) {
+        TraceScope ts(1, cs);
+        e = run_scored(s, p, opt, cap_rows, cs);
+    } else if (kv4) {
         TraceScope ts(1, cs);
         e = q4_launch(p, cs);
     } else if (kernel == GQA_KERNEL_TC) {
@@ -462,7 +572,10 @@ size_t gqa_workspace_bytes(int B, int Hq, int Hkv, int D, gqa_dtype dt, const gq
         return 0;
     int grid = grid_for(kernel, opt, dt, D, G);
     // AUTO may pick either kernel depending on the block size: size for the larger grid
-    if (dt != GQA_DTYPE_E2M1 && (!opt || opt->kernel == GQA_KERNEL_AUTO) && simt_supports(D, G)) {
+    if (is_scored(dt, opt)) {   // for either query type
+        const int g2 = grid_for(kernel, opt, dt, D, G, GQA_DTYPE_F32);
+        grid = grid > g2 ? grid : g2;
+    } else if (dt != GQA_DTYPE_E2M1 && (!opt || opt->kernel == GQA_KERNEL_AUTO) && simt_supports(D, G)) {
         const int g2 = grid_for(GQA_KERNEL_SIMT, opt, dt, D, G);
         grid = grid > g2 ? grid : g2;
     }
@@ -471,14 +584,21 @@ size_t gqa_workspace_bytes(int B, int Hq, int Hkv, int D, gqa_dtype dt, const gq
     return workspace_layout(B, Hkv, G, D, grid).bytes;
 }
 
+size_t gqa_weights_scratch_bytes(int B, int Hq, int Hkv, long long capacity)
+{
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || capacity < 1 || capacity > INT_MAX)
+        return 0;
+    return scored_scratch_bytes(B, Hq, Hkv, capacity);
+}
+
 gqa_status gqa_decode_step_ex(const void *q, const void *k_new, const void *v_new, void *k_cache,
                               void *v_cache, const int32_t *lengths, const int32_t *slot_ids,
                               float *out, int B, int Hq, int Hkv, int D, int R, int Smax,
                               gqa_dtype dt, void *workspace, size_t workspace_bytes,
                               int32_t *d_status, void *stream, const gqa_options *opt)
 {
-    // over an E4M3 or E2M1 cache the query and the new key / value are bfloat16
-    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 || dt == GQA_DTYPE_E2M1 ? GQA_DTYPE_BF16 : dt;
+    // over an E4M3, E2M1 or 8-bit cache the query and the new key / value are bfloat16
+    const gqa_dtype qdt = dt >= GQA_DTYPE_E4M3 ? GQA_DTYPE_BF16 : dt;
     Shape s = {B, Hq, Hkv, D, dt, false, R, Smax, 0, 0, 0, false, qdt};
     return run_step(s, q, k_new, v_new, k_cache, v_cache, lengths, slot_ids, nullptr, out,
                     workspace, workspace_bytes, d_status, stream, opt);
@@ -502,7 +622,7 @@ gqa_status gqa_decode_step_paged_ex(const void *q, const void *k_new, const void
                                     gqa_dtype dt, void *workspace, size_t workspace_bytes,
                                     int32_t *d_status, void *stream, const gqa_options *opt)
 {
-    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 || dt == GQA_DTYPE_E2M1 ? GQA_DTYPE_BF16 : dt;
+    const gqa_dtype qdt = dt >= GQA_DTYPE_E4M3 ? GQA_DTYPE_BF16 : dt;
     Shape s = {B, Hq, Hkv, D, dt, true, 0, 0, num_blocks, block_size, max_blocks, false, qdt};
     return run_step(s, q, k_new, v_new, k_blocks, v_blocks, lengths, nullptr, block_table, out,
                     workspace, workspace_bytes, d_status, stream, opt);
@@ -587,7 +707,8 @@ gqa_status gqa_validate_multi(const int32_t *lengths, const int32_t *cu_q, const
 size_t gqa_workspace_bytes_multi(int B, int Hq, int Hkv, int D, gqa_dtype dt, int max_q_len,
                                  const gqa_options *opt)
 {
-    if (B < 0 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv || max_q_len < 0 || Hq / Hkv > 8 || dt == GQA_DTYPE_E2M1)
+    if (B < 0 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv || max_q_len < 0 || Hq / Hkv > 8 || dt == GQA_DTYPE_E2M1 ||
+        is_scored(dt, opt))
         return 0;
     const int Gh = Hq / Hkv;
     // enough for whichever kernel the call will pick (AUTO may depend on the
@@ -619,7 +740,7 @@ gqa_status gqa_decode_multi(const void *q, const void *k_new, const void *v_new,
                             size_t workspace_bytes, int32_t *d_status, void *stream,
                             const gqa_options *opt)
 {
-    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 || dt == GQA_DTYPE_E2M1 ? GQA_DTYPE_BF16 : dt;   // query and new tokens
+    const gqa_dtype qdt = dt >= GQA_DTYPE_E4M3 ? GQA_DTYPE_BF16 : dt;   // query and new tokens
     Shape s = {B, Hq, Hkv, D, dt, false, R, Smax, 0, 0, 0, false, qdt, true, T, max_q_len};
     return run_step(s, q, k_new, v_new, k_cache, v_cache, lengths, slot_ids, nullptr, out, workspace,
                     workspace_bytes, d_status, stream, opt, cu_q);
@@ -633,7 +754,7 @@ gqa_status gqa_decode_multi_paged(const void *q, const void *k_new, const void *
                                   size_t workspace_bytes, int32_t *d_status, void *stream,
                                   const gqa_options *opt)
 {
-    const gqa_dtype qdt = dt == GQA_DTYPE_E4M3 || dt == GQA_DTYPE_E2M1 ? GQA_DTYPE_BF16 : dt;
+    const gqa_dtype qdt = dt >= GQA_DTYPE_E4M3 ? GQA_DTYPE_BF16 : dt;
     Shape s = {B, Hq, Hkv, D, dt, true, 0, 0, num_blocks, block_size, max_blocks, false, qdt, true, T,
                max_q_len};
     return run_step(s, q, k_new, v_new, k_blocks, v_blocks, lengths, nullptr, block_table, out,
@@ -673,9 +794,10 @@ gqa_status gqa_attend_selected(const void *q, gqa_dtype q_dtype, const void *k_c
 {
     if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (long long)B * Hkv > INT_MAX)
         return GQA_ERR_INVALID_ARGUMENT;
-    if (opt && (opt->window || opt->kept_prefix || opt->kept_prefix_rows || opt->head_sink))
+    if (opt && (opt->window || opt->kept_prefix || opt->kept_prefix_rows || opt->head_sink || opt->score_cap != 0.f ||
+                opt->head_slopes || opt->weights))
         return GQA_ERR_INVALID_ARGUMENT;
-    if (kv_dtype == GQA_DTYPE_E4M3)
+    if (kv_dtype == GQA_DTYPE_E4M3 || kv_dtype == GQA_DTYPE_I8)
         return GQA_ERR_UNSUPPORTED;      // its kernels take one scale per head of a row's cache
     // every (row, cache head) is a row of its own over the pool of one-head blocks
     Shape s = {B * Hkv, Hq / Hkv, 1, D, kv_dtype, true, 0, 0, pool_blocks, block_size, n_select, true, q_dtype};
@@ -755,6 +877,6 @@ gqa_status gqa_stream_capture_id(void *stream, uint64_t *id)
     return GQA_OK;
 }
 
-int gqa_version(void) { return 102; }
+int gqa_version(void) { return 103; }
 
 }  // extern "C"

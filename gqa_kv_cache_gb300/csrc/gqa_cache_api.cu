@@ -34,7 +34,7 @@ int current_sms()
 
 gqa_status run_rows(RowsParams p, gqa_dtype vec, gqa_dtype kv, bool write, void *stream, const gqa_options *opt)
 {
-    if (p.B < 0 || p.T < 0 || p.Hkv < 1 || p.D < 1 || !vec_dtype(vec) || kv < GQA_DTYPE_F32 || kv > GQA_DTYPE_E2M1)
+    if (p.B < 0 || p.T < 0 || p.Hkv < 1 || p.D < 1 || !vec_dtype(vec) || kv < GQA_DTYPE_F32 || kv > GQA_DTYPE_I8)
         return GQA_ERR_INVALID_ARGUMENT;
     if (p.paged) {
         if (p.num_blocks < 1 || p.block_size < 1 || p.max_blocks < 1 ||
@@ -51,7 +51,18 @@ gqa_status run_rows(RowsParams p, gqa_dtype vec, gqa_dtype kv, bool write, void 
         if (p.bounds_block > 1024)
             return GQA_ERR_UNSUPPORTED;
     }
-    if (kv >= GQA_DTYPE_E4M3) {
+    if (kv == GQA_DTYPE_I8) {
+        if (p.bounds)
+            return GQA_ERR_UNSUPPORTED;
+        if (!opt || !opt->k_block_scale || !opt->v_block_scale || !aligned(opt->k_block_scale, 4) ||
+            !aligned(opt->v_block_scale, 4))
+            return GQA_ERR_INVALID_ARGUMENT;
+        p.scale_block = p.paged ? p.block_size : opt->scale_block;
+        if (p.scale_block < 1 || (!p.paged && p.Smax % p.scale_block))
+            return GQA_ERR_INVALID_ARGUMENT;
+        p.k_block_scale = opt->k_block_scale;
+        p.v_block_scale = opt->v_block_scale;
+    } else if (kv >= GQA_DTYPE_E4M3) {
         if (!opt || !opt->k_scale || !opt->v_scale || !aligned(opt->k_scale, 4) || !aligned(opt->v_scale, 4))
             return GQA_ERR_INVALID_ARGUMENT;
         p.k_scale = opt->k_scale;

@@ -689,15 +689,21 @@ __device__ __forceinline__ float *out_row(const DecodeParams &p, const TileCurso
     }
 }
 
+// What a kernel keeps of a finished unit's softmax: nothing, or (a kernel that
+// passes its own) query row g's base-2 maximum M and denominator den.
+struct NoRowEnd {
+    __device__ __forceinline__ void operator()(int, float, float) const {}
+};
+
 // First part of the end of a unit segment: the weights of the warp states,
 // then the normalised output (the segment is the whole unit) or this CTA's
 // partial state (a cut unit). Returns whether the unit was whole. Every
 // calling thread takes part; ends with a sync().
-template <int NW, int GP, int DD, int DP, bool MULTI, class Sync, int GR, int KM>
+template <int NW, int GP, int DD, int DP, bool MULTI, class Sync, int GR, int KM, class RowEnd = NoRowEnd>
 __device__ inline bool segment_out(const DecodeParams &p, const TileCursor &cur, int seg_first_t, bool bad,
                                    const float (&sm_m)[NW][GP], const float (&sm_l)[NW][GP],
                                    const float (&sm_o)[NW][GP][DP], MergeBufT<GR, KM> &mb, int tid, int nthr,
-                                   Sync sync)
+                                   Sync sync, RowEnd row_end = RowEnd())
 {
     static_assert(NW <= kMergeW && GP <= GR && DP >= DD, "merge buffer too small");
     const int G = p.G, b = cur.b, kvh = cur.kvh;
@@ -723,6 +729,8 @@ __device__ inline bool segment_out(const DecodeParams &p, const TileCursor &cur,
         }
         mb.M[tid] = M;
         mb.den[tid] = den;
+        if (whole)
+            row_end(tid, M, bad ? qnan : den);
         if (!whole) {
             p.ws_ml[(P * G + tid) * 2 + 0] = bad ? qnan : M;
             p.ws_ml[(P * G + tid) * 2 + 1] = bad ? qnan : den;
@@ -787,10 +795,10 @@ __device__ inline bool segment_out(const DecodeParams &p, const TileCursor &cur,
 // at GPU scope then publishes them (release is cumulative), and the last
 // arriver's acquire plus the barrier order its reads after the stores of
 // every other CTA of the unit.
-template <int DD, bool MULTI, bool PRE2, class Sync, int GR, int KM>
+template <int DD, bool MULTI, bool PRE2, class Sync, int GR, int KM, class RowEnd = NoRowEnd>
 __device__ inline void unit_ticket_merge(const DecodeParams &p, const TileCursor &cur, int first, int last,
                                          int *sm_flag, MergeBufT<GR, KM> &mb, int tid, int nthr, Sync sync,
-                                         int pre_cnt)
+                                         int pre_cnt, RowEnd row_end = RowEnd())
 {
     const int G = p.G, kvh = cur.kvh;
     const int u = cur.b * p.Hkv + kvh;
@@ -837,6 +845,7 @@ __device__ inline void unit_ticket_merge(const DecodeParams &p, const TileCursor
                     den = fmaf(a, mb.l[i * G + tid], den);
                 }
                 mb.inv_den[tid] = 1.f / den;
+                row_end(tid, M, den);
             }
             sync();
             for (int idx = tid * V; idx < G * DD; idx += nthr * V) {
@@ -972,6 +981,8 @@ __device__ inline void unit_ticket_merge(const DecodeParams &p, const TileCursor
                 }
                 if (g < nrow)
                     out_row<MULTI>(p, cur, g, DD)[d] = num / den;
+                if (d == 0)
+                    row_end(g, M, den);
             }
         }
         sync();
@@ -990,19 +1001,20 @@ __device__ inline void unit_ticket_merge(const DecodeParams &p, const TileCursor
 // semantics shortly before the segment's end, or -1. When it already shows
 // every other piece of the unit arrived, this CTA is the last arriver: it
 // skips the ticket's round trip and merges at once.
-template <int NW, int GP, int DD, int DP, bool MULTI, bool PRE2 = false, class Sync, int GR, int KM>
+template <int NW, int GP, int DD, int DP, bool MULTI, bool PRE2 = false, class Sync, int GR, int KM,
+          class RowEnd = NoRowEnd>
 __device__ inline void finish_segment(const DecodeParams &p, const TileCursor &cur, const TileWalk &walk,
                                       int seg_first_t,
                                       bool bad, const float (&sm_m)[NW][GP], const float (&sm_l)[NW][GP],
                                       const float (&sm_o)[NW][GP][DP], int *sm_flag, MergeBufT<GR, KM> &mb,
-                                      int tid, int nthr, Sync sync, int pre_cnt = -1)
+                                      int tid, int nthr, Sync sync, int pre_cnt = -1, RowEnd row_end = RowEnd())
 {
-    if (segment_out<NW, GP, DD, DP, MULTI>(p, cur, seg_first_t, bad, sm_m, sm_l, sm_o, mb, tid, nthr, sync))
+    if (segment_out<NW, GP, DD, DP, MULTI>(p, cur, seg_first_t, bad, sm_m, sm_l, sm_o, mb, tid, nthr, sync, row_end))
         return;
     const long long first_tile = cur.g - cur.t;
     const int first = cta_of_tile(first_tile, walk.N, walk.C);
     const int last = cta_of_tile(first_tile + cur.nr - 1, walk.N, walk.C);
-    unit_ticket_merge<DD, MULTI, PRE2>(p, cur, first, last, sm_flag, mb, tid, nthr, sync, pre_cnt);
+    unit_ticket_merge<DD, MULTI, PRE2>(p, cur, first, last, sm_flag, mb, tid, nthr, sync, pre_cnt, row_end);
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }

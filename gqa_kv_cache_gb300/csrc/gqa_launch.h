@@ -48,6 +48,29 @@ bool q4_whole_units(long long capacity, long long units, int grid);   // one CTA
 int q4_ctas_per_sm(int D, bool q_bf16);   // resident CTAs per SM
 cudaError_t q4_launch(const DecodeParams &p, cudaStream_t st);
 
+// Attend over an 8-bit cache with block scales, and with capped, biased or
+// counted scores over it or a bfloat16 cache (gqa_scored*.cu): D = 64 or 128.
+constexpr int kBf16 = 1, kI8 = 4;   // kinds of cache (gqa_dtype's values)
+struct ScoredParams : DecodeParams {
+    int kind;                        // kBf16 or kI8
+    const float *k_block_scale, *v_block_scale;   // 8 bits: (block, head) of the cache
+    int scale_block, scale_shift;    // slots a block (paged: block_size), its logarithm or -1
+    float cap, scale_cap;            // cap log2(e) (0: none), 1 / (sqrt(D) cap)
+    const float *slopes;             // (Hq) or null
+    float *weights;                  // counts: (R, Hkv, Smax) or (num_blocks, Hkv, block_size), or null
+    float *xs;                       // with weights: base-2 scores (B, Hkv, xs_cap, gp) ...
+    float2 *row_end;                 // ... and (B, Hq) maxima and 1 / denominators
+    long long xs_cap;
+    int gp;                          // query rows a slot of xs: 4 or 8
+};
+bool scored_supports(int kind, int D, int G);
+int scored_tile(int kind, int D);
+bool scored_whole_units(int kind, int D, long long capacity, long long units, int grid);   // one CTA a unit
+int scored_ctas_per_sm(int kind, int D, int G, bool q_bf16);   // resident CTAs per SM
+long long scored_count_ctas(int B, int Hkv, long long capacity);   // of the kernel that counts
+size_t scored_scratch_bytes(int B, int Hq, int Hkv, long long capacity);   // of xs and row_end
+cudaError_t scored_launch(const ScoredParams &p, cudaStream_t st);   // the attend, and the counts where asked for
+
 // Packed tokens into a cache and slots back out (gqa_rows.cu).
 struct RowsParams {
     const void *k_new, *v_new;       // append: (T, Hkv, D)
@@ -56,7 +79,9 @@ struct RowsParams {
     void *k_group, *v_group;         // E2M1 caches: E4M3 scales, one per 16 dims
     const float *k_scale, *v_scale;  // E4M3 and E2M1 caches: (Hkv)
     void *bounds;                    // append: key bounds (block, head, 2, D) bfloat16, or null
-    const int32_t *lengths, *cu_q, *slot_ids, *block_table;
+    float *k_block_scale, *v_block_scale;   // 8-bit caches: a scale a (block, head)
+    int scale_block;                 // slots a block of theirs (paged: block_size)
+    const int32_t *lengths, *cu_q, *slot_ids, *block_table;   // cu_q null: one token a row (append to 8-bit and bfloat16 caches)
     int32_t *status;
     int vec_bf16;                    // the vectors' type: 1 bfloat16, 0 float32
     int B, T, Hkv, D, R, Smax, paged, num_blocks, block_size, max_blocks;
@@ -70,6 +95,7 @@ __device__ __forceinline__ void rows_report(const RowsParams &p, int bits)
         atomicOr(p.status, bits);
 }
 cudaError_t rows_launch(RowsParams p, int kv_dtype, bool write, int sms, cudaStream_t st);
+cudaError_t tokens_launch(RowsParams p, cudaStream_t st);   // one token a row into a bfloat16 cache
 
 // Block selection from key bounds (gqa_select.cu).
 struct SelectParams {
@@ -85,6 +111,36 @@ struct SelectParams {
 };
 bool select_supports(int D, int NB);
 cudaError_t select_launch(const SelectParams &p, int sms, cudaStream_t st);
+
+// Rotary positions (gqa_rotate.cu). Strides in elements.
+struct RotateParams {
+    const void *q, *k;               // (T, Hq, D), (T, Hkv, D)
+    void *q_out, *k_out;             // may be q, k
+    long long q_token, q_head, k_token, k_head, qo_token, qo_head, ko_token, ko_head;
+    const int32_t *positions;        // (T), or null: lengths[b] + t - cu_q[b]
+    const int32_t *lengths, *cu_q;
+    const uint64_t *freqs;           // (dim / 2) fractions of a turn a position, times 2^64
+    int32_t *status;
+    float factor;
+    int bf16, half, B, T, Hq, Hkv, D, dim;
+    int rest, units, tokens;         // set by rotate_launch
+};
+cudaError_t rotate_launch(RotateParams p, int sms, cudaStream_t st);
+
+// Eviction (gqa_evict.cu).
+struct EvictParams {
+    void *k_cache, *v_cache;         // dense (R, Hkv, Smax, row) or blocks (num_blocks, Hkv, block_size, row)
+    float *weights;                  // counts: the cache's shape without its last
+    void *k_out, *v_out;             // (B, Hkv, out_slots, row), or null: in place
+    float *weights_out;              // (B, Hkv, out_slots), or null
+    const int32_t *lengths, *slot_ids, *block_table;
+    int32_t *ids, *new_lengths;      // (B, Hkv, n_keep), (B)
+    int32_t *status;
+    int B, Hkv, R, Smax, paged, num_blocks, block_size, max_blocks;
+    int row_bytes, out_slots, n_keep, n_first, n_last;
+    int cached, shares;              // set by evict_launch
+};
+cudaError_t evict_launch(EvictParams p, cudaStream_t st);
 
 // Content validation (gqa_validate.cu). *d_result must be zero on entry; the
 // kernel sets it to 1 on any violation. attend = 1 checks the read-only

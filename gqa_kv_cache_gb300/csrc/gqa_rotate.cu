@@ -1,0 +1,256 @@
+// Rotary positions: over the first `dim` elements of a head, pair i of a token
+// at position pos becomes m (x cos a - y sin a, x sin a + y cos a), a = pos f_i;
+// the elements behind `dim` stay as they are. Pair i is (i, i + dim / 2) or
+// (2 i, 2 i + 1).
+//
+// Angles. f_i is given as a fraction of a turn in 64-bit fixed point
+// (f_i / 2 pi 2^64), so pos f_i mod a turn is the wrapped integer product: exact
+// for every int32 position, without 64-bit floating point (which this GPU has
+// little of). The nearest quarter turn is taken off in integers, and cos and
+// sin of the rest (|a| <= pi / 4, a 30-bit integer rounded to float32) come from
+// sincospif: both are off by less than 2^-23.
+//
+// A CTA takes a few tokens (or a part of one's heads): the angles of a token,
+// shared by all heads of q and k, go through shared memory while the first
+// vectors are on their way. Bound by memory: every vector is read and written
+// once, 16 bytes a thread at a time; odd sizes and strides go element by
+// element.
+#include "gqa_common.cuh"
+#include "gqa_launch.h"
+
+namespace gqa {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float2 turn(uint64_t x, float m)
+{
+    const uint32_t h = (uint32_t)(x >> 32);
+    const uint32_t q = (h + 0x20000000u) >> 30;         // nearest quarter
+    const float f = (float)(int)(h - (q << 30)) * 0x1p-31f;   // the rest in half turns
+    float s, c;
+    sincospif(f, &s, &c);
+    const float a = q & 1 ? -s : c, b = q & 1 ? c : s;
+    return q & 2 ? make_float2(-a * m, -b * m) : make_float2(a * m, b * m);
+}
+
+// N elements of type T, 16 bytes of them or one.
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Vec {
+    T x[N];
+};
+
+__device__ __forceinline__ float wide(float v) { return v; }
+__device__ __forceinline__ float wide(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Position of token t; false: a token of no row.
+__device__ __forceinline__ bool position(const RotateParams &p, int t, int &pos)
+{
+    if (p.positions) {
+        pos = __ldg(p.positions + t);
+        return true;
+    }
+    int lo = 0, hi = p.B;              // the last b with cu_q[b] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.cu_q + mid) <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int t0 = __ldg(p.cu_q + lo), t1 = __ldg(p.cu_q + lo + 1);
+    if (t < t0 || t >= t1)
+        return false;
+    if (t0 < 0 || t1 > p.T) {
+        if (p.status)
+            atomicOr(p.status, kBadQLen);
+        return false;
+    }
+    pos = (int)((unsigned)__ldg(p.lengths + lo) + (unsigned)(t - t0));
+    return true;
+}
+
+// A unit of work: N elements (HALF: of each half of the turned elements) of one
+// head of a token.
+template <typename T, int N, bool HALF>
+struct Unit {
+    const T *src;
+    T *dst;
+    int i;             // first pair, or -1: elements behind `dim`
+    Vec<T, N> a, b;
+};
+
+template <typename T, int N, bool HALF>
+__device__ __forceinline__ void find(const RotateParams &p, int t, int x, Unit<T, N, HALF> &w)
+{
+    const int head = x / p.units, c = x - head * p.units;
+    const bool key = head >= p.Hq;
+    const int h = key ? head - p.Hq : head;
+    w.src = static_cast<const T *>(key ? p.k : p.q) + t * (key ? p.k_token : p.q_token) + h * (key ? p.k_head : p.q_head);
+    w.dst = static_cast<T *>(key ? p.k_out : p.q_out) + t * (key ? p.ko_token : p.qo_token) +
+            h * (key ? p.ko_head : p.qo_head);
+    // units of turned elements: dim / (2 N) pairs of pieces; N = 1 (2 elements) else N / 2 pairs
+    const int turned = HALF || N == 1 ? p.dim / 2 / N : p.dim / N;
+    if (c < turned) {
+        w.i = HALF ? c * N : N == 1 ? c : c * (N / 2);
+        const int d = HALF ? c * N : N == 1 ? 2 * c : c * N;
+        w.src += d;
+        w.dst += d;
+    } else {
+        w.i = -1;
+        const int d = p.dim + (c - turned) * N;
+        w.src += d;
+        w.dst += d;
+    }
+}
+
+template <typename T, int N, bool HALF>
+__device__ __forceinline__ void load(const RotateParams &p, Unit<T, N, HALF> &w)
+{
+    w.a = *reinterpret_cast<const Vec<T, N> *>(w.src);
+    if (w.i >= 0 && (HALF || N == 1))
+        w.b = *reinterpret_cast<const Vec<T, N> *>(w.src + (HALF ? p.dim / 2 : 1));
+}
+
+template <typename T, int N, bool HALF>
+__device__ __forceinline__ void store(const RotateParams &p, Unit<T, N, HALF> &w, const float2 *cs, bool known)
+{
+    if (w.i < 0 || !known) {
+        *reinterpret_cast<Vec<T, N> *>(w.dst) = w.a;
+        if (w.i >= 0 && (HALF || N == 1))
+            *reinterpret_cast<Vec<T, N> *>(w.dst + (HALF ? p.dim / 2 : 1)) = w.b;
+        return;
+    }
+    if constexpr (HALF || N == 1) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float2 e = cs[w.i + j];
+            const float x = wide(w.a.x[j]), y = wide(w.b.x[j]);
+            w.a.x[j] = narrow<T>(x * e.x - y * e.y);
+            w.b.x[j] = narrow<T>(x * e.y + y * e.x);
+        }
+        *reinterpret_cast<Vec<T, N> *>(w.dst) = w.a;
+        *reinterpret_cast<Vec<T, N> *>(w.dst + (HALF ? p.dim / 2 : 1)) = w.b;
+    } else {
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+            const float2 e = cs[w.i + j];
+            const float x = wide(w.a.x[2 * j]), y = wide(w.a.x[2 * j + 1]);
+            w.a.x[2 * j] = narrow<T>(x * e.x - y * e.y);
+            w.a.x[2 * j + 1] = narrow<T>(x * e.y + y * e.x);
+        }
+        *reinterpret_cast<Vec<T, N> *>(w.dst) = w.a;
+    }
+}
+
+// blockIdx.x: `tokens` tokens; blockIdx.y: a part of their units.
+template <typename T, int N, bool HALF>
+__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p)
+{
+    extern __shared__ float2 cs[];             // [tokens][dim / 2]
+    __shared__ int known[32];                  // whether the token has a position
+    const int tid = threadIdx.x, pairs = p.dim / 2;
+    const int t0 = blockIdx.x * p.tokens, n = min(p.tokens, p.T - t0);
+    const int all = (p.Hq + p.Hkv) * p.units;  // units a token
+    const int u0 = (int)((long long)all * blockIdx.y / gridDim.y), u1 = (int)((long long)all * (blockIdx.y + 1) / gridDim.y);
+    const int per = u1 - u0, total = per * n;
+    // the next kernel may be set up meanwhile (it waits for this one's end)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Unit<T, N, HALF> w;
+    int x = tid, tok = 0;
+    if (x < total) {
+        tok = x / per;
+        find(p, t0 + tok, u0 + x - tok * per, w);
+        load(p, w);
+    }
+    for (int i = tid; i < n * pairs; i += kThreads) {
+        const int t = i / pairs, j = i - t * pairs;
+        int pos = 0;
+        const bool ok = position(p, t0 + t, pos);
+        if (j == 0)
+            known[t] = ok;
+        cs[i] = turn((uint64_t)(int64_t)pos * __ldg(p.freqs + j), p.factor);
+    }
+    if (p.cu_q && blockIdx.y == 0)
+        for (long long b = (long long)blockIdx.x * kThreads + tid; b < p.B; b += (long long)gridDim.x * kThreads) {
+            const int a = __ldg(p.cu_q + b), e = __ldg(p.cu_q + b + 1);
+            if ((a < 0 || e < a || e > p.T) && p.status)
+                atomicOr(p.status, kBadQLen);
+        }
+    __syncthreads();
+    while (x < total) {
+        const int y = x + kThreads;
+        Unit<T, N, HALF> next;
+        int ntok = 0;
+        if (y < total) {                       // the next unit is on its way while this one is turned
+            ntok = y / per;
+            find(p, t0 + ntok, u0 + y - ntok * per, next);
+            load(p, next);
+        }
+        store(p, w, cs + tok * pairs, known[tok]);
+        x = y;
+        tok = ntok;
+        w = next;
+    }
+}
+
+template <typename T, int N, bool HALF>
+cudaError_t launch(RotateParams &p, int sms, cudaStream_t st)
+{
+    const int turned = HALF || N == 1 ? p.dim / 2 / N : p.dim / N;
+    p.units = turned + (p.rest ? (p.D - p.dim) / N : 0);
+    const long long all = (long long)(p.Hq + p.Hkv) * p.units;
+    // tokens a CTA: as many as leave every SM eight CTAs, at most 8 (65521
+    // tokens); parts of a token's heads where there are few tokens
+    const long long share = p.T / ((long long)sms * 8);
+    p.tokens = share < 1 ? 1 : share > 8 ? 8 : (int)share;
+    const long long ctas = ((long long)p.T + p.tokens - 1) / p.tokens;
+    long long parts = (all * p.tokens + kThreads - 1) / kThreads, room = (long long)sms * 4 / ctas;
+    parts = parts > room ? room : parts;
+    parts = parts < 1 ? 1 : parts > 64 ? 64 : parts;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)parts);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)p.tokens * (p.dim / 2) * sizeof(float2);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rotate_kernel<T, N, HALF>, p);
+}
+
+template <typename T>
+cudaError_t launch_type(RotateParams &p, int sms, cudaStream_t st)
+{
+    constexpr int N = 16 / sizeof(T);
+    // 16-byte pieces: addresses, strides and the parts of a head fit them
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) |
+                         reinterpret_cast<uintptr_t>(p.q_out) | reinterpret_cast<uintptr_t>(p.k_out);
+    const long long strides = p.q_token | p.q_head | p.k_token | p.k_head | p.qo_token | p.qo_head | p.ko_token | p.ko_head;
+    const bool pieces = (at & 15u) == 0 && strides % N == 0 && (p.D - p.dim) % N == 0 &&
+                        (p.half ? p.dim / 2 : p.dim) % N == 0;
+    if (p.half)
+        return pieces ? launch<T, N, true>(p, sms, st) : launch<T, 1, true>(p, sms, st);
+    return pieces ? launch<T, N, false>(p, sms, st) : launch<T, 1, false>(p, sms, st);
+}
+
+}  // namespace
+
+cudaError_t rotate_launch(RotateParams p, int sms, cudaStream_t st)
+{
+    // in place the elements behind `dim` need no copy
+    p.rest = p.q_out != p.q || p.k_out != p.k || p.qo_token != p.q_token || p.qo_head != p.q_head ||
+             p.ko_token != p.k_token || p.ko_head != p.k_head;
+    return p.bf16 ? launch_type<__nv_bfloat16>(p, sms, st) : launch_type<float>(p, sms, st);
+}
+
+}  // namespace gqa

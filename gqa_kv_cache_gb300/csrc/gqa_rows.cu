@@ -1,5 +1,6 @@
 // Writing packed tokens into a cache (append) and reading slots back (read):
-// float32, bfloat16, E4M3 and E2M1 caches; dense, slot-id and paged addressing.
+// float32, bfloat16, E4M3, E2M1 and 8-bit caches; dense, slot-id and paged
+// addressing.
 //
 // Token t of the packed batch belongs to the row b with cu_q[b] <= t <
 // cu_q[b + 1] and to slot lengths[b] + t - cu_q[b] of that row. A CTA takes a
@@ -33,22 +34,26 @@ struct Token {
     int b, slot;     // its row (-1: of no row) and slot
 };
 
-// The row of packed token t and its slot's offset. Reports what is wrong with
-// the token's row (the row's first token only, a bad block each time).
+// The row of packed token t and its slot's offset (ONE: row t has token t and
+// no other). Reports what is wrong with the token's row (the row's first token
+// only, a bad block each time).
+template <bool ONE = false>
 __device__ inline Token find_token(const RowsParams &p, int t)
 {
     Token k;
     k.off = kSkip;
     k.b = k.slot = -1;
     int lo = 0, hi = p.B;              // the last b with cu_q[b] <= t
-    while (hi - lo > 1) {
+    if (ONE)
+        lo = t;
+    while (!ONE && hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (__ldg(p.cu_q + mid) <= t)
             lo = mid;
         else
             hi = mid;
     }
-    const int t0 = __ldg(p.cu_q + lo), t1 = __ldg(p.cu_q + lo + 1);
+    const int t0 = ONE ? t : __ldg(p.cu_q + lo), t1 = ONE ? t + 1 : __ldg(p.cu_q + lo + 1);
     if (t < t0 || t >= t1)
         return k;                      // padding behind (or before) the rows' tokens
     k.b = lo;
@@ -482,6 +487,296 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowsParams p)
     }
 }
 
+// ---- 8-bit caches: a scale for each (block of slots, cache head) ----
+//
+// A block's values are c t, c an int8 code and t the block's scale. A run (the
+// call's tokens of one block) that begins the block sets t = max|x| / 127; one
+// behind earlier slots keeps the block's scale t0 where it holds the run, else
+// t = t0 2^k, the smallest k with max|x| / 127 <= t, and the earlier codes become
+// rint(c / 2^k). Codes are rint(x / t), 0 where t is 0. A scale that grows by
+// powers of two keeps the codes' error under one step of the final scale
+// however often it grows (1/2 + 1/4 + ... of the roundings before the last,
+// which is 1/2), where max|x| / 127 at every growth would add half a step each
+// time. A run with a value that is not finite makes the scale NaN.
+//
+// A warp takes a (run, head) of K or of V: 16 elements a lane at a time, kept
+// in registers up to kKeep of them (a 16-slot block of D = 128) and read again
+// (from L1) behind that. Bound by memory: es D + D bytes a vector.
+
+constexpr int kKeep = 4;   // groups of 16 elements a lane keeps between the two passes
+
+struct Run {
+    int tok, n;        // first token (of the CTA's) and tokens
+    int slot;          // its slot
+    long long off;     // element offset of that slot's vector of head 0
+    long long scale;   // index of the block's scale of head 0
+};
+
+// Index of the scale of head 0 of the block that holds the token's slot.
+__device__ __forceinline__ long long scale_index(const RowsParams &p, const Token &k)
+{
+    if (p.paged)
+        return k.off / ((long long)p.D * p.block_size);   // off is in head 0 of its block: block * Hkv
+    const long long r = p.slot_ids ? __ldg(p.slot_ids + k.b) : k.b;
+    return r * p.Hkv * (p.Smax / p.scale_block) + k.slot / p.scale_block;
+}
+
+// Largest magnitude of a group as loaded; NaN if it holds one.
+template <typename T>
+__device__ __forceinline__ float group_max(const Raw<T> &w)
+{
+    if constexpr (sizeof(T) == 2) {
+        uint32_t m = w.u[0];               // two at a time (the signs get mixed up)
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w.u[i]));
+        return max_nan(fabsf(bf16_lo(m)), fabsf(bf16_hi(m)));
+    } else {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            a = max_nan(a, fabsf(__uint_as_float(w.u[i])));
+        return a;
+    }
+}
+
+// Four codes as a word. A float32 of magnitude up to 127 plus 1.5 2^23 is
+// rounded to a whole number (ties to even) whose low byte is the code.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d)
+{
+    const float k = 12582912.f;
+    const uint32_t x = __float_as_uint(a + k), y = __float_as_uint(b + k), z = __float_as_uint(c + k), w = __float_as_uint(d + k);
+    return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+}
+
+// The codes of a group under scale t; r = 1 / t correctly rounded, quick: t is
+// far enough from float32's ends for the quotient to come from r (a product,
+// its exact remainder and one correction: P. Markstein, IBM J. Res. Dev. 34,
+// 1990, which rounds as the division does).
+template <typename T>
+__device__ __forceinline__ uint4 codes16(const Raw<T> &w, float t, float r, bool quick)
+{
+    float x[16];
+    widen16(w, x);
+    if (quick) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float q = __fmul_rn(x[i], r);
+            x[i] = __fmaf_rn(-__fmaf_rn(q, t, -x[i]), r, q);
+        }
+    } else {
+        // a zero or NaN scale: codes 0; a subnormal one may be coarse
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            x[i] = t > 0.f ? fminf(fmaxf(__fdiv_rn(x[i], t), -127.f), 127.f) : 0.f;
+    }
+    return make_uint4(codes4(x[0], x[1], x[2], x[3]), codes4(x[4], x[5], x[6], x[7]),
+                      codes4(x[8], x[9], x[10], x[11]), codes4(x[12], x[13], x[14], x[15]));
+}
+
+// Four codes divided by a power of two (times f).
+__device__ __forceinline__ uint32_t fewer4(uint32_t u, float f)
+{
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = (float)((int)(u << (24 - 8 * i)) >> 24) * f;
+    return codes4(x[0], x[1], x[2], x[3]);
+}
+
+// One CTA: the runs that begin among its `chunk` tokens, to their ends. Shared
+// memory: the tokens' slots, then the runs.
+template <typename T, bool ONE>
+__global__ void __launch_bounds__(kThreads) append8_kernel(const RowsParams p)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    Token *tok = reinterpret_cast<Token *>(smem);                         // [chunk]
+    Run *runs = reinterpret_cast<Run *>(smem + sizeof(Token) * p.chunk);   // [chunk]
+    __shared__ int n_runs;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int t0 = blockIdx.x * p.chunk;
+    const int n = min(p.chunk, p.T - t0);
+    // the next kernel may be set up meanwhile (it waits for this one's end)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid == 0)
+        n_runs = 0;
+    __syncthreads();
+    const int sb = p.scale_block;
+    for (int i = tid; i < n; i += kThreads) {
+        const Token k = find_token<ONE>(p, t0 + i);
+        tok[i] = k;
+        // the first token of its block or of its row (the row's others are in
+        // order with it: a bad block's are all skipped)
+        if (k.off != kSkip) {
+            const int end = ONE ? t0 + i + 1 : __ldg(p.cu_q + k.b + 1);
+            if (k.slot % sb == 0 || ONE || t0 + i == __ldg(p.cu_q + k.b)) {
+                const int at = atomicAdd(&n_runs, 1);   // the order of the runs does not matter
+                runs[at] = Run{i, min(sb - k.slot % sb, end - (t0 + i)), k.slot, k.off, scale_index(p, k)};
+            }
+        }
+    }
+    if constexpr (!ONE)
+        check_rows(p);
+    __syncthreads();
+    const int per = p.D / kGroup;                       // groups a vector
+    const int shift = (per & (per - 1)) == 0 ? __ffs(per) - 1 : -1;
+    const long long head = (long long)(p.paged ? p.block_size : p.Smax) * p.D;   // elements between heads
+    const long long scale_head = p.paged ? 1 : p.Smax / sb;
+    const long long row = (long long)p.Hkv * p.D;
+    const int items = n_runs * p.Hkv * 2;               // neighbours: K and V of a head
+    for (int it = tid >> 5; it < items; it += kThreads / 32) {
+        const Run run = runs[it / (2 * p.Hkv)];
+        const int h = (it >> 1) % p.Hkv;
+        const bool val = it & 1;
+        const T *src = static_cast<const T *>(val ? p.v_new : p.k_new) + (long long)(t0 + run.tok) * row + (long long)h * p.D;
+        int8_t *dst = static_cast<int8_t *>(val ? p.v_cache : p.k_cache) + run.off + h * head;
+        float *scale = (val ? p.v_block_scale : p.k_block_scale) + run.scale + h * scale_head;
+        const int before = run.slot % sb;               // earlier slots of the block
+        const float was = before ? *scale : 0.f;
+        const int groups = run.n * per;
+        auto place = [&](int i, int &m, int &d) {       // token and element of group i
+            m = shift >= 0 ? i >> shift : i / per;
+            d = (i - m * per) * kGroup;
+        };
+        Raw<T> kept[kKeep];
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int at = lane + 32 * i;
+            if (at < groups) {
+                int m, d;
+                place(at, m, d);
+                kept[i] = load_raw(src + m * row + d, p.wide);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i)
+            if (lane + 32 * i < groups)
+                top = max_nan(top, group_max(kept[i]));
+        for (int at = lane + 32 * kKeep; at < groups; at += 32) {
+            int m, d;
+            place(at, m, d);
+            top = max_nan(top, group_max(load_raw(src + m * row + d, p.wide)));
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float t = __fdiv_rn(top, 127.f), f = 1.f;
+        if (!(top <= 3.402823466e38f)) {
+            t = __int_as_float(0x7fc00000);             // an infinity or a NaN among them
+        } else if (!(was <= 0.f)) {                     // (a block without a scale yet: its codes are zeros)
+            const float need = t;
+            t = was;
+            while (t < need) {                          // at most 276 doublings
+                t *= 2.f;
+                f *= 0.5f;
+            }
+        }
+        if (f != 1.f) {                                 // the block's earlier codes, as the whole vectors they are
+            int8_t *old = dst - (long long)before * p.D;
+            for (int at = lane; at < before * per; at += 32) {
+                uint4 *w = reinterpret_cast<uint4 *>(old + (long long)at * kGroup);
+                const uint4 u = *w;
+                *w = make_uint4(fewer4(u.x, f), fewer4(u.y, f), fewer4(u.z, f), fewer4(u.w, f));
+            }
+        }
+        const bool quick = t > 0x1p-90f && t < 0x1p90f;
+        const float r = quick ? __frcp_rn(t) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int at = lane + 32 * i;
+            if (at < groups)                            // the run's vectors follow each other in the cache
+                *reinterpret_cast<uint4 *>(dst + (long long)at * kGroup) = codes16(kept[i], t, r, quick);
+        }
+        for (int at = lane + 32 * kKeep; at < groups; at += 32) {
+            int m, d;
+            place(at, m, d);
+            *reinterpret_cast<uint4 *>(dst + (long long)at * kGroup) = codes16(load_raw(src + m * row + d, p.wide), t, r, quick);
+        }
+        if (lane == 0)
+            *scale = t;
+    }
+}
+
+// One CTA reads `chunk` tokens' slots of an 8-bit cache back.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) read8_kernel(const RowsParams p)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    Token *tok = reinterpret_cast<Token *>(smem);                                      // [chunk]
+    long long *scale = reinterpret_cast<long long *>(smem + sizeof(Token) * p.chunk);   // [chunk]
+    const int tid = threadIdx.x;
+    const int t0 = blockIdx.x * p.chunk;
+    const int n = min(p.chunk, p.T - t0);
+    // the next kernel may be set up meanwhile (it waits for this one's end)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = tid; i < n; i += kThreads) {
+        const Token k = find_token(p, t0 + i);
+        tok[i] = k;
+        scale[i] = k.off == kSkip ? 0 : scale_index(p, k);
+    }
+    check_rows(p);
+    __syncthreads();
+    const Share s(p);
+    const long long head = (long long)(p.paged ? p.block_size : p.Smax) * p.D;
+    const long long scale_head = p.paged ? 1 : p.Smax / p.scale_block;
+    for (int c0 = 0; c0 < s.per; c0 += kThreads) {
+        const int c = c0 + s.c;
+        if (c >= s.per || s.lane >= s.lanes)
+            break;
+        const int h = c / (p.D / kGroup), d = (c % (p.D / kGroup)) * kGroup;
+        const long long row = (long long)p.Hkv * p.D, to = (long long)t0 * row + (long long)c * kGroup;
+        for (int m = s.lane; m < n; m += s.lanes) {
+            const Token k = tok[m];
+            if (k.b < 0)
+                continue;                  // of no row: left as it was
+            float x[16], y[16];
+            if (k.off == kSkip) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    x[q] = y[q] = __int_as_float(0x7fc00000);
+            } else {
+                const long long src = k.off + h * head + d, at = scale[m] + h * scale_head;
+                const uint4 kw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const int8_t *>(p.k_cache) + src));
+                const uint4 vw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const int8_t *>(p.v_cache) + src));
+                const float ks = __ldg(p.k_block_scale + at), vs = __ldg(p.v_block_scale + at);
+                const uint32_t a[4] = {kw.x, kw.y, kw.z, kw.w}, b[4] = {vw.x, vw.y, vw.z, vw.w};
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    x[q] = __fmul_rn((float)((int)(a[q / 4] << (24 - 8 * (q % 4))) >> 24), ks);
+                    y[q] = __fmul_rn((float)((int)(b[q / 4] << (24 - 8 * (q % 4))) >> 24), vs);
+                }
+            }
+            store_raw(static_cast<T *>(p.k_out) + to + m * row, round16<T>(x), p.wide);
+            store_raw(static_cast<T *>(p.v_out) + to + m * row, round16<T>(y), p.wide);
+        }
+    }
+}
+
+// One token a row into a bfloat16 cache: a CTA a row.
+__global__ void __launch_bounds__(kThreads) tokens_kernel(const RowsParams p)
+{
+    __shared__ Token tok;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x == 0)
+        tok = find_token<true>(p, blockIdx.x);
+    __syncthreads();
+    if (tok.off == kSkip)
+        return;
+    const long long head = (long long)(p.paged ? p.block_size : p.Smax) * p.D;
+    const int per = p.D / 8;                            // 16-byte pieces a vector
+    const uint4 *k = static_cast<const uint4 *>(p.k_new) + (long long)blockIdx.x * p.Hkv * per;
+    const uint4 *v = static_cast<const uint4 *>(p.v_new) + (long long)blockIdx.x * p.Hkv * per;
+    for (int i = threadIdx.x; i < p.Hkv * per; i += kThreads) {
+        const long long to = tok.off + i / per * head + i % per * 8;
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.k_cache) + to) = __ldg(k + i);
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.v_cache) + to) = __ldg(v + i);
+    }
+}
+
 template <typename K>
 cudaError_t launch(K kernel, const RowsParams &p, size_t smem, cudaStream_t st)
 {
@@ -516,7 +811,22 @@ cudaError_t launch_kind(const RowsParams &p, bool write, cudaStream_t st)
     return p.vec_bf16 ? launch(read_kernel<__nv_bfloat16, KIND>, p, smem, st) : launch(read_kernel<float, KIND>, p, smem, st);
 }
 
+template <typename T>
+cudaError_t launch8(const RowsParams &p, bool write, cudaStream_t st)
+{
+    if (!write)
+        return launch(read8_kernel<T>, p, (sizeof(Token) + sizeof(long long)) * (size_t)p.chunk, st);
+    const size_t smem = (sizeof(Token) + sizeof(Run)) * (size_t)p.chunk;
+    return p.cu_q ? launch(append8_kernel<T, false>, p, smem, st) : launch(append8_kernel<T, true>, p, smem, st);
+}
+
 }  // namespace
+
+cudaError_t tokens_launch(RowsParams p, cudaStream_t st)
+{
+    p.chunk = 1;
+    return launch(tokens_kernel, p, 0, st);
+}
 
 cudaError_t rows_launch(RowsParams p, int kv_dtype, bool write, int sms, cudaStream_t st)
 {
@@ -534,6 +844,7 @@ cudaError_t rows_launch(RowsParams p, int kv_dtype, bool write, int sms, cudaStr
     case GQA_DTYPE_F32: return launch_kind<GQA_DTYPE_F32>(p, write, st);
     case GQA_DTYPE_BF16: return launch_kind<GQA_DTYPE_BF16>(p, write, st);
     case GQA_DTYPE_E4M3: return launch_kind<GQA_DTYPE_E4M3>(p, write, st);
+    case GQA_DTYPE_I8: return p.vec_bf16 ? launch8<__nv_bfloat16>(p, write, st) : launch8<float>(p, write, st);
     default: return launch_kind<GQA_DTYPE_E2M1>(p, write, st);
     }
 }

@@ -1,0 +1,12 @@
+// Instantiations of the scored attend (gqa_scored_kernel.cuh): 8-bit caches, D = 128.
+#include "gqa_scored_kernel.cuh"
+
+namespace gqa {
+
+cudaError_t scored_i8_128(bool few, bool q_bf16, bool paged, const ScoredParams *p, cudaStream_t st, int *per_sm)
+{
+    return few ? scored::launch_d<kI8, 128, true>(q_bf16, paged, p, st, per_sm)
+               : scored::launch_d<kI8, 128, false>(q_bf16, paged, p, st, per_sm);
+}
+
+}  // namespace gqa

@@ -1,0 +1,994 @@
+// Attend over an 8-bit cache with a scale for each (block of slots, cache
+// head), and attend with capped or distance-biased scores or with the slots'
+// weights counted, over that cache or a bfloat16 one (D = 64 or 128, G <= 8).
+//
+// A base-2 score of slot j and query head h (query position L) is
+//   y = log2(e) (cap tanh(s / cap) + slope_h (j - L)),  s = t_j q.c_j / sqrt(D)
+// (t_j: the key scale of the slot's block, 1 over a bfloat16 cache; without a
+// cap s itself), the output sum_j 2^(y_j - m) u_j v_j / sum_j 2^(y_j - m) with
+// the value scales u_j. The schedule, the split of a unit between CTAs and its
+// merge are those of the other decode kernels (gqa_common.cuh). A CTA is four
+// warps; a tile is 16 kSub slots a warp, copied into a ring of the warp's own in
+// shared memory by 16-byte asynchronous copies, with no barrier between warps.
+//
+//  * S^T = K Q^T (m16n8k16, float32 sums): 16 slots by the query rows. Over an
+//    8-bit cache lane (g, t) takes slots g, g + 8 and of each the D / 4
+//    contiguous dims from D / 4 * t (the order of the contraction is free);
+//    codes become f16 by a byte permute under 0x64 (1024 + 128 + c) and one
+//    subtraction, exactly; a bfloat16 query is scaled by a power of two into
+//    f16's range (exact but for elements 2^-38 below the row's largest), a
+//    float32 one is an f16 and an f16 remainder (22 bits). Over a bfloat16 cache
+//    the fragments come by ldmatrix, a float32 query as three bfloat16 (24 bits).
+//  * O^T += V^T P^T: 16 dims by the query rows, 16 slots a step, V unrounded.
+//    8 bits: lane (g, t) takes D / 8 contiguous dims of slots 2t, 2t + 1, 2t + 8,
+//    2t + 9, neighbours paired by a byte permute. P is an f16 and an f16
+//    remainder 2^12 times as large with sums of its own (a weight's error: 2^-23
+//    of it and 2^-37 - 12 bits of the largest weight). bfloat16: P in three parts.
+//  * up to four query rows over an 8-bit cache (FEW): every row has two of the
+//    eight columns: in S^T the same query (float32: f16 and remainder), in O^T
+//    the weight's two parts: half the matrix products and half the softmax.
+//  * value scales: a weight is multiplied by u / ref with ref a power of two of
+//    the warp, raised when a scale passes 8 ref, so that products stay within
+//    f16's range; the running sum takes the weight before.
+//  * the softmax keeps a reference below the running maximum, raised only when
+//    a score passes it by kRoom; sums of a tile start from zero and are added to
+//    the output in float32 (the matrix unit truncates its sums).
+//  * counted weights: the scores go to a scratch array as they come (float32,
+//    G padded to 4 or 8 a slot), each row's maximum and denominator at the end of
+//    its unit, and a second kernel adds sum_g 2^(y_g - M_g) / den_g to the slot's
+//    count. (A second pass over the keys would read 2 D bytes a slot instead of
+//    8 G.)
+#pragma once
+
+#define GQA_MULTI_TOKEN 0   // single-token steps only
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "gqa_common.cuh"
+#include "gqa_launch.h"
+
+namespace gqa {
+namespace scored {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 8;                      // query rows (G <= 8)
+constexpr int kFew = 4;                       // and of the form for few
+constexpr int kSegs = 4;                      // segments a warp's copies and products are in at once
+constexpr float kLift = 10.f;                 // a reference is set this far below the maximum ...
+constexpr float kRoom = 12.f;                 // ... and holds until a score is this far above it
+constexpr float kOver = 8.f;                  // value scales reach this times their reference
+constexpr float kRest = 4096.f;               // a weight's remainder enters the products this much larger
+
+template <int KIND, int D>
+struct Form {
+    static constexpr bool I8 = KIND == kI8;
+    static constexpr int VB = I8 ? D : 2 * D;             // bytes a vector
+    static constexpr int SUB = VB == 256 ? 1 : 2;         // 16-slot parts of a warp's share of a tile
+    static constexpr int SHARE = 16 * SUB;                // a warp's slots of a tile
+    static constexpr int TILE = kWarps * SHARE;           // slots a tile
+    static constexpr int LV = VB / 16;                    // lanes (16-byte pieces) a vector
+    static constexpr int VI = 32 / LV;                    // vectors a copy instruction
+    static constexpr int NI = 16 / VI;                    // copy instructions a part
+    static constexpr int CTAS = VB == 64 ? 3 : 2;         // resident CTAs per SM
+};
+
+// Tiles of a warp's ring: as many as let CTAS CTAs share an SM (the rows of a
+// float32 query take 16 KB where there are more than four).
+template <int KIND, int D, bool QF32, bool FEW>
+constexpr int stages()
+{
+    return KIND == kI8 && D == 128 && QF32 && !FEW ? 2 : 3;
+}
+
+// One tile's share of a warp in shared memory: vectors in slot order, their
+// 16-byte pieces permuted so that the operand loads below have no bank
+// conflicts, and (8 bits) the slots' scales.
+template <int KIND, int D>
+struct Stage {
+    uint8_t k[Form<KIND, D>::SHARE * Form<KIND, D>::VB], v[Form<KIND, D>::SHARE * Form<KIND, D>::VB];
+    float ks[KIND == kI8 ? Form<KIND, D>::SHARE : 4], vs[KIND == kI8 ? Form<KIND, D>::SHARE : 4];
+};
+
+// Offset of 16-byte piece c of the share's vector r.
+template <int VB>
+__device__ __forceinline__ int piece(int r, int c)
+{
+    if constexpr (VB == 64)
+        return (r >> 1) * 128 + (((((r & 1) << 2) + c) ^ (2 * ((r >> 1) & 3))) << 4);
+    else
+        return r * VB + ((c ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ uint32_t smem_at(const void *p)
+{
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Asynchronous copies to shared memory; `n` of the bytes come from src (all or
+// none of them) and the others are zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int n)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1)
+{
+    if constexpr (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t a)
+{
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at)
+{
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(at)
+                     : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(at)
+                     : "memory");
+}
+
+__device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<__half2 *>(&v); }
+__device__ __forceinline__ uint32_t u32(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
+__device__ __forceinline__ uint32_t u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t *>(&v); }
+
+// Bytes SEL of w (codes with the sign bit flipped: c + 128) as an f16 pair: the
+// byte under 0x64 is the f16 1024 + 128 + c; exact.
+template <int SEL>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w)
+{
+    return u32(__hsub2(h2(__byte_perm(w, 0x64646464u, SEL)), h2(0x64806480u)));
+}
+
+// Two float32 as an f16 pair and the f16 pair of MUL times what it leaves.
+__device__ __forceinline__ void split2(float x, float y, float times, uint32_t &hi, uint32_t &lo)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    hi = u32(h);
+    lo = u32(__floats2half2_rn((x - f.x) * times, (y - f.y) * times));
+}
+
+// Two float32 as three bfloat16 pairs.
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&p)[3])
+{
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        p[i] = u32(__floats2bfloat162_rn(x, y));
+        x -= bf16_lo(p[i]);
+        y -= bf16_hi(p[i]);
+    }
+}
+
+// Vector index of slot s of a unit of a paged cache, or -1.
+static __device__ __noinline__ long long paged_row(const int32_t *table, int block_size, int num_blocks, int Hkv, int kvh,
+                                                   int s)
+{
+    const int blk = __ldg(table + s / block_size);
+    if (blk < 0 || blk >= num_blocks)
+        return -1;
+    return ((long long)blk * Hkv + kvh) * block_size + s % block_size;
+}
+
+// The unit's query fragments. 8 bits: lane (g, t) holds row g's D / 4 dims from
+// D / 4 * t, scaled by a power of two into f16's range, and `mul` is the factor
+// that takes a product to a score over `scale`. bfloat16: the fragments of the
+// product as they are, PARTS of them. q: the rows in shared memory.
+template <int KIND, int D, bool QF32, bool FEW, int PARTS>
+__device__ __forceinline__ void load_query(float scale, const void *q, int lane, uint32_t (&qf)[PARTS][D / 16][2], float &mul)
+{
+    if constexpr (KIND == kI8) {
+        constexpr int N = D / 4;
+        const int g = FEW ? lane >> 3 : lane >> 2, t = lane & 3;   // query row of column lane / 4
+        float x[N];
+        if constexpr (QF32) {
+            const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(q) + g * D + N * t);
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i) {
+                const float4 v = s[i];
+                x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+            }
+        } else {
+            const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(q) + g * D + N * t);
+#pragma unroll
+            for (int i = 0; i < N / 8; ++i) {
+                const uint4 v = s[i];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[8 * i + 2 * j] = bf16_lo(w[j]);
+                    x[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+                }
+            }
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            amax = fmaxf(amax, fabsf(x[i]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 2^(14 - exponent of amax), within float32's normal range both ways
+        const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -110), 127);
+        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        mul = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * scale;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float a = x[4 * i + 2 * j] * up, b = x[4 * i + 2 * j + 1] * up;
+                if constexpr (QF32 && FEW) {
+                    // the row's first column takes the f16, its second the remainder
+                    uint32_t h, l;
+                    split2(a, b, 1.f, h, l);
+                    qf[0][i][j] = lane & 4 ? l : h;
+                } else if constexpr (QF32) {
+                    split2(a, b, 1.f, qf[0][i][j], qf[PARTS - 1][i][j]);
+                } else {
+                    qf[0][i][j] = u32(__floats2half2_rn(a, b));
+                }
+            }
+    } else {
+        const int g = lane >> 2, t = lane & 3;
+        mul = scale;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int d = g * D + 16 * i + 8 * j + 2 * t;
+                if constexpr (QF32) {
+                    const float2 v = *reinterpret_cast<const float2 *>(static_cast<const float *>(q) + d);
+                    uint32_t part[3];
+                    split3(v.x, v.y, part);
+#pragma unroll
+                    for (int k = 0; k < PARTS; ++k)
+                        qf[k][i][j] = part[k];
+                } else {
+                    qf[0][i][j] = *reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(q) + d);
+                }
+            }
+    }
+}
+
+// A segment of a unit: consecutive tiles that this CTA computes. Kept in a
+// small ring in shared memory: the copies run ahead of the products.
+struct Segment {
+    TileCursor c;      // at its first tile
+    int t_last;        // its last tile
+    int good;          // the row's content is in order
+};
+
+template <int D, bool QF32, bool FEW>
+constexpr int query_bytes()
+{
+    return (FEW ? kFew : kRows) * D * (QF32 ? 4 : 2);
+}
+
+// What a warp's copies are taken from.
+struct Fetch {
+    int t, t_last;     // (the rest of its segment is read from shared memory)
+    bool good;
+    uint32_t line;     // dense: vector of slot 0
+    uint32_t block0;   // dense, 8 bits: block of slot 0
+    int page, page_next;   // paged: the block of part lane % SUB of a tile, 32 / SUB tiles; of the tiles behind them
+};
+
+template <class F>
+__device__ __forceinline__ int share_slot(int t, int tp, int gap, int warp)
+{
+    return (t < tp ? t : t + gap) * F::TILE + warp * F::SHARE;
+}
+
+// lane's page of the 32 / SUB tiles from `tile`
+template <class F>
+__device__ __forceinline__ int load_page(const ScoredParams &p, const Fetch &f, const TileCursor &c, int shift, int tile,
+                                         int warp, int lane)
+{
+    const int x = tile + lane / F::SUB;
+    const int s = share_slot<F>(x, c.tp, c.gap, warp) + 16 * (lane % F::SUB);
+    return x <= f.t_last && s <= c.L ? __ldg(p.block_table + (long long)c.b * p.max_blocks + (s >> shift)) : 0;
+}
+
+// The copies' segment becomes that of cursor c. The segment's query rows (rows
+// behind the G are zeros) are copied too, a part by each warp, in the group of
+// the copies that comes next.
+template <class F, int D, bool QF32, bool PAGED, bool FEW>
+__device__ __forceinline__ void enter(const ScoredParams &p, const TileCursor &c, Fetch &f, Segment *seg, int *bad, void *q,
+                                      int shift, bool pages, int warp, int lane)
+{
+    constexpr int B = QF32 ? 4 : 2;                // bytes an element
+    constexpr int C = D * B / 16;                  // 16-byte pieces a row
+    constexpr int R = FEW ? kFew : kRows;
+    constexpr int PER = 32 / F::SUB;
+    const char *src = static_cast<const char *>(p.q) + ((long long)c.b * p.Hq + (long long)c.kvh * p.G) * D * B;
+#pragma unroll
+    for (int i = 0; i < (R * C + kThreads - 1) / kThreads; ++i) {
+        const int x = i * kThreads + warp * 32 + lane;
+        if (R * C % kThreads == 0 || x < R * C)
+            copy16(smem_at(q) + x * 16, x / C < p.G ? src + x * 16 : src, x / C < p.G ? 16 : 0);
+    }
+    f.t = c.t;
+    f.t_last = (int)min((long long)c.nr - 1, c.t + (c.end - c.g) - 1);
+    f.good = row_ok(p, c.b, c.L);
+    if constexpr (PAGED) {
+        if (f.good && pages) {
+            f.page = load_page<F>(p, f, c, shift, f.t & ~(PER - 1), warp, lane);
+            f.page_next = load_page<F>(p, f, c, shift, (f.t & ~(PER - 1)) + PER, warp, lane);
+        }
+    } else if (f.good) {
+        const int r = p.slot_ids ? __ldg(p.slot_ids + c.b) : c.b;
+        f.line = ((uint32_t)r * p.Hkv + c.kvh) * (uint32_t)p.Smax;
+        if constexpr (F::I8)
+            f.block0 = ((uint32_t)r * p.Hkv + c.kvh) * (uint32_t)(p.Smax / p.scale_block);
+    }
+    if (lane == 0) {
+        seg->c = c;
+        seg->t_last = f.t_last;
+        seg->good = f.good;
+        *bad = 0;
+    }
+}
+
+// Starts the copies of the warp's share of tile f.t.
+template <int KIND, int D, bool PAGED>
+__device__ __forceinline__ void fetch_tile(const ScoredParams &p, const Fetch &f, const TileCursor &c, Stage<KIND, D> &st,
+                                           int *bad, int shift, bool pages, int warp, int lane)
+{
+    using F = Form<KIND, D>;
+    if (!f.good)
+        return;                            // its output is NaN, whatever is in the stage
+    const int s = share_slot<F>(f.t, c.tp, c.gap, warp);
+    const uint32_t dk = smem_at(st.k), dv = smem_at(st.v);
+    [[maybe_unused]] const uint32_t dks = smem_at(st.ks), dvs = smem_at(st.vs);
+    const uint8_t *kc = static_cast<const uint8_t *>(p.k_cache), *vc = static_cast<const uint8_t *>(p.v_cache);
+    const int e = s + F::SHARE - 1;
+    const int r0 = lane / F::LV, c0 = lane % F::LV;
+    // block (of the dense cache) that holds slot x
+    [[maybe_unused]] auto block_of = [&](int x) {
+        return f.block0 + (p.scale_shift >= 0 ? (uint32_t)x >> p.scale_shift : (uint32_t)x / (uint32_t)p.scale_block);
+    };
+    if (pages && e <= c.L && (s >= c.lo || e < c.P)) {
+        // every slot is in the softmax, 16 vectors in a row at least
+#pragma unroll
+        for (int u = 0; u < F::SUB; ++u) {
+            uint32_t row;
+            [[maybe_unused]] uint32_t block = 0;
+            if constexpr (PAGED) {
+                int blk = __shfl_sync(0xffffffffu, f.page, F::SUB * (f.t & (32 / F::SUB - 1)) + u);
+                if (blk < 0 || blk >= p.num_blocks) {
+                    *bad = 1;
+                    blk = 0;               // read something: the unit's output is NaN
+                }
+                block = (uint32_t)blk * p.Hkv + c.kvh;
+                row = (block << shift) + ((uint32_t)(s + 16 * u) & ((1u << shift) - 1u));
+            } else {
+                row = f.line + (uint32_t)(s + 16 * u);
+            }
+            const uint64_t in = (uint64_t)(row + r0) * F::VB + c0 * 16;
+            const uint8_t *k0 = kc + in, *v0 = vc + in;
+#pragma unroll
+            for (int j = 0; j < F::NI; ++j) {
+                const uint32_t to = (uint32_t)piece<F::VB>(16 * u + F::VI * j + r0, c0);
+                copy16(dk + to, k0 + j * F::VI * F::VB);
+                copy16(dv + to, v0 + j * F::VI * F::VB);
+            }
+            if constexpr (F::I8) {
+                // lanes 0 .. 15 the key scales of the part's slots, 16 .. 31 the value scales
+                const int i = 16 * u + (lane & 15);
+                if constexpr (!PAGED)
+                    block = block_of(s + i);
+                copy4((lane < 16 ? dks : dvs) + 4 * i, (lane < 16 ? p.k_block_scale : p.v_block_scale) + block, 4);
+            }
+        }
+        return;
+    }
+    // slot by slot: any block size; a slot outside the softmax becomes zeros
+    auto vector = [&](int j) -> long long {
+        if (!attended(c.L, c.lo, c.P, s + j))
+            return -1;
+        if constexpr (PAGED) {
+            const long long r = paged_row(p.block_table + (long long)c.b * p.max_blocks, p.block_size, p.num_blocks,
+                                          p.Hkv, c.kvh, s + j);
+            if (r < 0)
+                *bad = 1;
+            return r;
+        } else {
+            return (long long)f.line + s + j;
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < F::SHARE / F::VI; ++j) {
+        const int r = F::VI * j + r0;
+        const long long x = vector(r);
+        const uint64_t at = x < 0 ? 0 : (uint64_t)x * F::VB + c0 * 16;
+        copy16(dk + piece<F::VB>(r, c0), kc + at, x < 0 ? 0 : 16);
+        copy16(dv + piece<F::VB>(r, c0), vc + at, x < 0 ? 0 : 16);
+    }
+    if constexpr (F::I8) {
+        const int j = lane;                // SHARE = 32 slots
+        const long long x = vector(j);
+        uint64_t at = 0;
+        if (x >= 0) {
+            if constexpr (PAGED)
+                at = (uint64_t)x / (uint32_t)p.block_size;
+            else
+                at = block_of(s + j);
+        }
+        copy4(dks + 4 * j, p.k_block_scale + at, x < 0 ? 0 : 4);
+        copy4(dvs + 4 * j, p.v_block_scale + at, x < 0 ? 0 : 4);
+    }
+}
+
+// Products of part u: s[0], s[1] slot g and query rows 2t, 2t + 1 (FEW: both
+// row t); s[2], s[3] slot g + 8. 8 bits: times the slot's key scale.
+template <int KIND, int D, bool QF32, bool FEW, int PARTS>
+__device__ __forceinline__ void scores(const Stage<KIND, D> &st, int u, int lane, const uint32_t (&qf)[PARTS][D / 16][2],
+                                       float (&s)[4])
+{
+    using F = Form<KIND, D>;
+    const int g = lane >> 2, t = lane & 3;
+    float s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        s[i] = 0.f;
+    if constexpr (KIND == kI8) {
+        uint32_t k[2][D / 16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(st.k + piece<F::VB>(16 * u + g + 8 * i, D / 64 * t + j));
+                k[i][4 * j] = w.x; k[i][4 * j + 1] = w.y; k[i][4 * j + 2] = w.z; k[i][4 * j + 3] = w.w;
+            }
+#pragma unroll
+        for (int w = 0; w < D / 16; ++w) {
+            const uint32_t x = k[0][w] ^ 0x80808080u, y = k[1][w] ^ 0x80808080u;
+            const uint32_t a0 = code_pair<0x4140>(x), a1 = code_pair<0x4140>(y), a2 = code_pair<0x4342>(x), a3 = code_pair<0x4342>(y);
+            float(&d)[4] = w & 1 ? s2 : s;
+            mma<true>(d, a0, a1, a2, a3, qf[0][w][0], qf[0][w][1]);
+            if constexpr (PARTS == 2)
+                mma<true>(d, a0, a1, a2, a3, qf[1][w][0], qf[1][w][1]);
+        }
+    } else {
+#pragma unroll
+        for (int w = 0; w < D / 16; ++w) {
+            uint32_t a[4];
+            ldmatrix4<false>(a, smem_at(st.k) + piece<F::VB>(16 * u + (lane & 15), 2 * w + (lane >> 4)));
+            float(&d)[4] = w & 1 ? s2 : s;
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k)
+                mma<false>(d, a[0], a[1], a[2], a[3], qf[k][w][0], qf[k][w][1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        s[i] += s2[i];
+    if constexpr (KIND == kI8) {
+        if constexpr (QF32 && FEW) {
+            s[0] += s[1];
+            s[2] += s[3];
+        }
+        const float a = st.ks[16 * u + g], b = st.ks[16 * u + g + 8];
+        s[0] *= a;
+        s[2] *= b;
+        if constexpr (!FEW) {
+            s[1] *= a;
+            s[3] *= b;
+        }
+    }
+}
+
+// O^T += V^T P^T over a warp's slots of a tile; w[u] are the weights in the
+// positions of the scores. The products of a tile are summed from zero and then
+// added to o (the matrix unit truncates its sums). Where o's elements lie:
+// out_dim.
+template <int KIND, int D, bool FEW>
+__device__ __forceinline__ void weigh(const Stage<KIND, D> &st, int lane, const float (&w)[Form<KIND, D>::SUB][FEW ? 2 : 4],
+                                      float (&o)[D / 16][FEW ? 2 : 4])
+{
+    using F = Form<KIND, D>;
+    constexpr int SUB = F::SUB;
+    const int g = lane >> 2, t = lane & 3;
+    if constexpr (KIND == kI8) {
+        // FEW: a row's two columns take the weight's f16 and its remainder
+        uint32_t bh[SUB][2], bl[FEW ? 1 : SUB][2];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (FEW) {
+                    const __half h = __float2half_rn(w[u][i]);
+                    bh[u][i] = movmatrix_t(u32(__halves2half2(h, __float2half_rn((w[u][i] - __half2float(h)) * kRest))));
+                } else {
+                    uint32_t h, l;
+                    split2(w[u][2 * i], w[u][2 * i + 1], kRest, h, l);
+                    bh[u][i] = movmatrix_t(h);
+                    bl[u][i] = movmatrix_t(l);
+                }
+            }
+        constexpr int W = D / 32;          // words of a slot's share: dims D / 8 * g + 4 i
+        uint32_t v[SUB][4][W];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 16 * u + 2 * t + (j & 1) + 8 * (j >> 1);
+                if constexpr (D == 128) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(st.v + piece<F::VB>(r, g));
+                    v[u][j][0] = x.x; v[u][j][1] = x.y; v[u][j][2] = x.z; v[u][j][3] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(st.v + piece<F::VB>(r, g >> 1) + 8 * (g & 1));
+                    v[u][j][0] = x.x; v[u][j][1] = x.y;
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            float d[2][4] = {};
+            [[maybe_unused]] float r[FEW ? 1 : 2][4] = {};
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                // bytes: dims 4 i, 4 i + 1 (then + 2, + 3) of two neighbouring slots
+                const uint32_t x0 = v[u][0][i] ^ 0x80808080u, x1 = v[u][1][i] ^ 0x80808080u;
+                const uint32_t x2 = v[u][2][i] ^ 0x80808080u, x3 = v[u][3][i] ^ 0x80808080u;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t a = __byte_perm(x0, x1, q ? 0x7362 : 0x5140), b = __byte_perm(x2, x3, q ? 0x7362 : 0x5140);
+                    const uint32_t a0 = code_pair<0x4140>(a), a1 = code_pair<0x4342>(a);
+                    const uint32_t a2 = code_pair<0x4140>(b), a3 = code_pair<0x4342>(b);
+                    mma<true>(d[q], a0, a1, a2, a3, bh[u][0], bh[u][1]);
+                    if constexpr (!FEW)
+                        mma<true>(r[q], a0, a1, a2, a3, bl[u][0], bl[u][1]);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float(&y)[FEW ? 2 : 4] = o[2 * i + q];
+                if constexpr (FEW) {
+                    y[0] += fmaf(d[q][1], 1.f / kRest, d[q][0]);
+                    y[1] += fmaf(d[q][3], 1.f / kRest, d[q][2]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        y[j] += fmaf(r[q][j], 1.f / kRest, d[q][j]);
+                }
+            }
+        }
+    } else {
+        uint32_t b[SUB][3][2];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t part[3];
+                split3(w[u][2 * i], w[u][2 * i + 1], part);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    b[u][k][i] = movmatrix_t(part[k]);
+            }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                uint32_t a[4];
+                ldmatrix4<true>(a, smem_at(st.v) + piece<F::VB>(16 * u + (lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    mma<false>(d, a[0], a[1], a[2], a[3], b[u][k][0], b[u][k][1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[i][j] += d[j];
+        }
+    }
+}
+
+// Scratch of the merge (segment_out, unit_ticket_merge): as many partials at a
+// time as the spare slot has room for.
+template <int KIND, int D>
+using Merge = MergeBufT<kRows, D == 128 ? 28 : 12>;
+
+template <int KIND, int D, bool QF32, bool PAGED, bool FEW>
+__global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(const ScoredParams p)
+{
+    using F = Form<KIND, D>;
+    using St = Stage<KIND, D>;
+    constexpr bool I8 = F::I8;
+    constexpr int SUB = F::SUB, STAGES = stages<KIND, D, QF32, FEW>(), SHARE = F::SHARE;
+    constexpr int C = FEW ? 1 : 2;             // query rows of a lane: t4, or 2t4 and 2t4 + 1
+    constexpr int PARTS = !QF32 ? 1 : !I8 ? 3 : FEW ? 1 : 2;
+    extern __shared__ __align__(128) unsigned char dyn[];
+    St(*ring)[kWarps] = reinterpret_cast<St(*)[kWarps]>(dyn);      // [STAGES]
+    auto sm_q = reinterpret_cast<uint8_t(*)[query_bytes<D, QF32, FEW>()]>(dyn + STAGES * kWarps * sizeof(St));   // [kSegs]
+    __shared__ long long sched[kThreads / 32 + 8];
+    __shared__ TileWalk walk;
+    __shared__ Segment segs[kSegs];            // every warp writes the same
+    __shared__ int sm_bad[kWarps][kSegs];      // a block that the segment needs is not usable
+    __shared__ int sm_flag;
+    __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int g = lane >> 2, t4 = lane & 3;
+
+    // the next kernel may be set up meanwhile (it waits for this one's end);
+    // programmatic dependent of the previous kernel: read no input before it is done
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!p.whole_units)
+        schedule_walk(p, sched, &walk);
+    // whole pages of 16 slots: one vector index a part; else slot by slot
+    const int shift = PAGED ? __ffs(p.block_size) - 1 : 0;
+    const bool pages = !PAGED || (p.block_size >= 16 && (p.block_size & (p.block_size - 1)) == 0);
+
+    // the copies: tile f.t of segment sf is the next to fetch
+    Fetch f = {};
+    int sf = 0;
+    bool in_b = false, left;
+    {
+        TileCursor c;
+        if (p.whole_units) {
+            // this CTA's tiles are those of its unit, one segment
+            c = cursor_at(p, blockIdx.x / p.Hkv, 0, 0, 0);
+            c.kvh = blockIdx.x % p.Hkv;
+            c.end = c.nr;
+            left = true;
+        } else {
+            left = walk_first(p, c, walk, in_b);
+            if (!left)
+                return;
+        }
+        enter<F, D, QF32, PAGED, FEW>(p, c, f, &segs[0], &sm_bad[warp][0], sm_q[0], shift, pages, warp, lane);
+        __syncwarp();
+    }
+    auto fetch = [&](int slot) {
+        if (left) {
+            fetch_tile<KIND, D, PAGED>(p, f, segs[sf].c, ring[slot][warp], &sm_bad[warp][sf], shift, pages, warp, lane);
+            if (f.t < f.t_last) {
+                ++f.t;
+                if constexpr (PAGED) {
+                    constexpr int PER = 32 / SUB;
+                    if ((f.t & (PER - 1)) == 0 && f.good && pages) {
+                        f.page = f.page_next;
+                        f.page_next = load_page<F>(p, f, segs[sf].c, shift, f.t + PER, warp, lane);
+                    }
+                }
+            } else {
+                TileCursor c = segs[sf].c;
+                c.g += f.t - c.t;
+                c.t = f.t;
+                left = !p.whole_units && walk_next(p, c, walk, in_b);
+                if (left) {
+                    sf = (sf + 1) % kSegs;
+                    enter<F, D, QF32, PAGED, FEW>(p, c, f, &segs[sf], &sm_bad[warp][sf], sm_q[sf], shift, pages, warp, lane);
+                    __syncwarp();
+                }
+            }
+        }
+        copy_commit();                     // an empty group behind the last tile
+    };
+    int slot = 0;                          // ring slot of the tile to compute
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+        fetch(i);
+
+    // the first segment's query rows, every warp's part (those of a later one
+    // came with the last tile of the segment before it, whose end the warps
+    // meet at)
+    copy_wait<STAGES - 2>();
+    __syncthreads();
+    // scores that are more than a product: capped, biased or counted ones are
+    // formed in place, and then need no factor
+    const bool formed = p.cap > 0.f || p.slopes || p.xs;
+    uint32_t qf[PARTS][D / 16][2];
+    float mul[C], fin[C], slope[C];        // product to score; score to base-2 score; base-2 bias a slot
+    float m[C], l[C];                      // reference and sum of the lane's rows
+    float o[D / 16][FEW ? 2 : 4];
+    for (int sc = 0;; sc = (sc + 1) % kSegs) {
+        // the next segment
+        const Segment *seg = &segs[sc];
+        const bool good = seg->good;
+        if (!good && tid == 0 && seg->c.t == 0 && seg->c.kvh == 0)
+            report(p, row_error_bits(p, seg->c.b, seg->c.L));
+        float mine;
+        load_query<KIND, D, QF32, FEW, PARTS>(p.cap > 0.f ? p.scale_cap : p.scale_log2, sm_q[sc], lane, qf, mine);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int row = C * t4 + c;
+            mul[c] = I8 ? __shfl_sync(0xffffffffu, mine, 8 * t4 + 4 * c) : mine;
+            fin[c] = formed ? 1.f : mul[c];
+            slope[c] = p.slopes && row < p.G ? __ldg(p.slopes + seg->c.kvh * p.G + row) * 1.4426950408889634f : 0.f;
+            m[c] = -INFINITY;
+            l[c] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < (FEW ? 2 : 4); ++j)
+                o[i][j] = 0.f;
+        [[maybe_unused]] float vref = 0.f;     // 8 bits: 1 / the reference of the value scales (0: none yet)
+
+        int arrived = -1;                  // thread 0: the unit's arrival count before the last tile
+        for (int t = seg->c.t; t <= seg->t_last; ++t) {
+            if (t == seg->t_last && tid == 0 && (seg->c.t != 0 || t != seg->c.nr - 1))
+                asm volatile("ld.acquire.gpu.global.s32 %0, [%1];"
+                             : "=r"(arrived)
+                             : "l"(p.ws_cnt + seg->c.b * p.Hkv + seg->c.kvh)
+                             : "memory");
+            copy_wait<STAGES - 2>();       // this lane's copies of the tile, then the other lanes'
+            __syncwarp();
+            fetch(slot == 0 ? STAGES - 1 : slot - 1);
+            const St &st = ring[slot][warp];
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+            float s[SUB][4];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+                scores<KIND, D, QF32, FEW, PARTS>(st, u, lane, qf, s[u]);
+            // bits 2 u + i: slot 16 u + g + 8 i is in the softmax
+            unsigned ok = good ? ~0u : 0u;
+            const int s0 = share_slot<F>(t, seg->c.tp, seg->c.gap, warp), L = seg->c.L, lo = seg->c.lo, P = seg->c.P;
+            if (s0 + SHARE - 1 > L || (s0 < lo && s0 + SHARE - 1 >= P)) {
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (!attended(L, lo, P, s0 + 16 * u + g + 8 * i))
+                            ok &= ~(1u << (2 * u + i));
+            }
+            if (formed) {
+                // base-2 scores in place
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int j = s0 + 16 * u + g + 8 * i;
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            float &y = s[u][2 * i + c];
+                            y *= mul[c];
+                            if (p.cap > 0.f)
+                                y = tanhf(y) * p.cap;
+                            if (p.slopes)
+                                y = fmaf(slope[c], (float)(j - L), y);
+                        }
+                        if (p.xs && ((ok >> (2 * u + i)) & 1u) && C * t4 < p.gp) {
+                            float *to = p.xs + (((unsigned long long)seg->c.b * p.Hkv + seg->c.kvh) * p.xs_cap + j) * p.gp + C * t4;
+                            if constexpr (FEW)
+                                *to = s[u][2 * i];
+                            else
+                                *reinterpret_cast<float2 *>(to) = make_float2(s[u][2 * i], s[u][2 * i + 1]);
+                        }
+                    }
+            }
+            // x = base-2 score - reference, of slots u, i and rows c
+            float x[SUB][2 * C], top = -INFINITY;
+            auto shifted = [&] {
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            float &y = x[u][C * i + c];
+                            y = fmaf(s[u][2 * i + c], fin[c], -m[c]);
+                            y = (ok >> (2 * u + i)) & 1u ? y : -INFINITY;
+                        }
+            };
+            shifted();
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int i = 0; i < 2 * C; ++i)
+                    top = fmaxf(top, x[u][i]);
+            bool raise = top > kRoom;
+            [[maybe_unused]] float vs[SUB][2];
+            if constexpr (I8) {
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        vs[u][i] = st.vs[16 * u + g + 8 * i];
+                        raise |= vs[u][i] * vref > kOver;
+                    }
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+                float r[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    float most = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if ((ok >> (2 * u + i)) & 1u)
+                                most = fmaxf(most, s[u][2 * i + c] * fin[c]);
+#pragma unroll
+                    for (int q = 4; q < 32; q <<= 1)
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, q));
+                    const float n = most - m[c] > kRoom ? most - kLift : m[c];
+                    r[c] = m[c] == -INFINITY ? 0.f : fast_ex2(m[c] - n);
+                    m[c] = n;
+                    l[c] *= r[c];
+                }
+                if constexpr (I8) {
+                    float most = 0.f;
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+                        most = fmaxf(most, fmaxf(vs[u][0], vs[u][1]));
+#pragma unroll
+                    for (int q = 4; q < 32; q <<= 1)
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, q));
+                    if (vref == 0.f || most * vref > kOver) {
+                        // the power of two above the largest scale, within 2^-100 .. 2^100
+                        const int e = min(max((int)(__float_as_uint(most) >> 23) - 126, -100), 100);
+                        const float next = __uint_as_float((uint32_t)(127 - e) << 23);
+                        const float less = vref == 0.f ? 0.f : next / vref;
+#pragma unroll
+                        for (int c = 0; c < C; ++c)
+                            r[c] *= less;
+                        vref = next;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int j = 0; j < (FEW ? 2 : 4); ++j)
+                        o[i][j] *= r[j % C];
+                shifted();
+            }
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+                for (int i = 0; i < 2 * C; ++i)
+                    x[u][i] = fast_ex2(x[u][i]);
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    l[c] += x[u][c] + x[u][C + c];
+                if constexpr (I8)
+#pragma unroll
+                    for (int i = 0; i < 2 * C; ++i)
+                        x[u][i] *= vs[u][i / C] * vref;
+            }
+            weigh<KIND, D, FEW>(st, lane, x, o);
+        }
+
+        // the end of the segment
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int q = 4; q < 32; q <<= 1)
+                l[c] += __shfl_xor_sync(0xffffffffu, l[c], q);
+            // a NaN score raises no reference: keep the NaN sum in the merge
+            m[c] = (l[c] != l[c] && m[c] == -INFINITY) ? 0.f : m[c];
+            if (g == 0) {
+                sm_m[warp][C * t4 + c] = m[c];
+                sm_l[warp][C * t4 + c] = l[c];
+            }
+        }
+        // the ring's slot of the last tile is free until the next segment's
+        // first fetch: the warps' outputs and the merge's scratch go there
+        St *spare = ring[slot == 0 ? STAGES - 1 : slot - 1];
+        auto &sm_o = *reinterpret_cast<float(*)[kWarps][kRows][D]>(spare);
+        auto &sm_merge = *reinterpret_cast<Merge<KIND, D> *>(reinterpret_cast<unsigned char *>(spare) + sizeof sm_o);
+        static_assert(sizeof sm_o + sizeof(Merge<KIND, D>) <= kWarps * sizeof(St), "the slot holds both");
+        __syncthreads();                   // every warp has read its part of the slot
+        if constexpr (I8) {
+            const float f = vref == 0.f ? 0.f : 1.f / vref;
+            // dims D / 8 * g + 2 i, + 1 in o[i][0 ..] and o[i][C ..]
+#pragma unroll
+            for (int i = 0; i < D / 16; i += 2)
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    *reinterpret_cast<float4 *>(&sm_o[warp][C * t4 + c][D / 8 * g + 2 * i]) =
+                        make_float4(o[i][c] * f, o[i][C + c] * f, o[i + 1][c] * f, o[i + 1][C + c] * f);
+        } else {
+            // dims 16 i + g and 16 i + g + 8
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sm_o[warp][2 * t4 + (j & 1)][16 * i + g + 8 * (j >> 1)] = o[i][j % (FEW ? 2 : 4)];
+        }
+        __syncwarp();
+        TileCursor cur = seg->c;
+        const int first_t = cur.t;
+        cur.g += seg->t_last - cur.t;
+        cur.t = seg->t_last;
+        const bool any_bad = __syncthreads_or(sm_bad[warp][sc]) != 0;
+        if (any_bad && good && tid == 0)
+            report(p, kBadBlock);
+        const bool end = !left && sc == sf;
+        finish_segment<kWarps, kRows, D, D, false, true>(
+            p, cur, walk, first_t, !good || any_bad, sm_m, sm_l, sm_o, &sm_flag, sm_merge, tid, kThreads,
+            [] { __syncthreads(); }, arrived, [&](int row, float M, float den) {
+                if (p.row_end)             // a NaN denominator: a bad row
+                    p.row_end[(long long)cur.b * p.Hq + cur.kvh * p.G + row] = make_float2(M, 1.f / den);
+            });
+        if (end)
+            break;
+    }
+}
+
+template <int KIND, int D, bool QF32, bool FEW>
+constexpr int dyn_bytes()
+{
+    return kWarps * stages<KIND, D, QF32, FEW>() * (int)sizeof(Stage<KIND, D>) + kSegs * query_bytes<D, QF32, FEW>();
+}
+
+template <int KIND, int D, bool QF32, bool PAGED, bool FEW>
+cudaError_t launch_one(const ScoredParams *p, cudaStream_t st, int *per_sm)
+{
+    // the ring's size is set once a device
+    static std::atomic<uint64_t> ready;
+    constexpr int bytes = dyn_bytes<KIND, D, QF32, FEW>();
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(scored_kernel<KIND, D, QF32, PAGED, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess)
+            return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    if (!p)
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, scored_kernel<KIND, D, QF32, PAGED, FEW>, kThreads, bytes);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p->grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, scored_kernel<KIND, D, QF32, PAGED, FEW>, *p);
+}
+
+template <int KIND, int D, bool FEW>
+cudaError_t launch_d(bool q_bf16, bool paged, const ScoredParams *p, cudaStream_t st, int *per_sm)
+{
+    if (q_bf16)
+        return paged ? launch_one<KIND, D, false, true, FEW>(p, st, per_sm) : launch_one<KIND, D, false, false, FEW>(p, st, per_sm);
+    return paged ? launch_one<KIND, D, true, true, FEW>(p, st, per_sm) : launch_one<KIND, D, true, false, FEW>(p, st, per_sm);
+}
+
+}  // namespace scored
+}  // namespace gqa

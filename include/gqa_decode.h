@@ -94,7 +94,24 @@ typedef enum gqa_dtype {
                            read-only attend a float32 or bfloat16 query; D = 64 or
                            128, G <= 8, any paged block size; GQA_KERNEL_AUTO or
                            GQA_KERNEL_TC. No multi-token step (write prompts with
-                           gqa_append).                                            */
+                           gqa_append).                                            */,
+    GQA_DTYPE_I8 = 4    /* a cache of int8 codes with a float32 scale per (block of slots,
+                           cache head) (gqa_options.k_block_scale / v_block_scale): dense
+                           (R, Hkv, Smax / scale_block), paged (num_blocks, Hkv), a block
+                           each. A slot's vector is c t, t the scale of its block (finite,
+                           not negative, within 2^-100 .. 2^100 or 0; NaN where a value
+                           that is not finite was written). The calls that write keep the
+                           scales: a block that begins with a new token takes t = max|x| /
+                           127 over the call's tokens of the block; one that gets tokens
+                           behind earlier slots keeps its t where max|x| / 127 <= t, else
+                           t doubles until it does and the earlier codes become rint(c /
+                           2^k) (0: a block without a scale, whose codes are zeros, takes
+                           max|x| / 127). Codes are rint(x / t), 0 where t is 0; float32
+                           arithmetic, rounded to nearest even. The decode step takes
+                           bfloat16 q, k_new and v_new, the read-only attend a float32 or
+                           bfloat16 query; D = 64 or 128, G <= 8, any paged block size;
+                           GQA_KERNEL_AUTO or GQA_KERNEL_TC. No multi-token step (write
+                           prompts with gqa_append), no key bounds.                 */
 } gqa_dtype;
 
 /* Bits OR-ed into *d_status by the kernels. */
@@ -178,6 +195,33 @@ typedef struct gqa_options {
                                         (then also k_scale / v_scale; 16-byte aligned),
                                         written by the calls that append, else ignored  */
     void *v_group_scale;             /* (device) the value cache's, likewise            */
+    float *k_block_scale;            /* (device) float32, required with an 8-bit cache
+                                        (GQA_DTYPE_I8), written by the calls that append,
+                                        else ignored                                    */
+    float *v_block_scale;            /* (device) the value cache's, likewise            */
+    int scale_block;                 /* dense 8-bit cache: slots a block, a divisor of Smax
+                                        (paged: ignored, block_size)                    */
+    /* The three below change the scores of a single-token step or attend or
+     * count its weights: a bfloat16 or 8-bit cache, D = 64 or 128, G <= 8,
+     * GQA_KERNEL_AUTO or GQA_KERNEL_TC; GQA_ERR_UNSUPPORTED elsewhere.          */
+    float score_cap;                 /* c > 0: the score s becomes c tanh(s / c); 0: off;
+                                        < 0, infinite or NaN is GQA_ERR_INVALID_ARGUMENT */
+    const float *head_slopes;        /* (device) (Hq,) float32 or NULL: slope_h (j - L) is
+                                        added to the (capped) score of slot j, L the
+                                        query's position: a positive slope takes from
+                                        distant slots                                   */
+    float *weights;                  /* (device) float32 counts, 4-byte aligned, or NULL: the
+                                        cache's shape without D ((R, Hkv, Smax) or
+                                        (num_blocks, Hkv, block_size)). Every attended slot's
+                                        softmax weights, summed over the G queries of its
+                                        head, are ADDED to its count; other counts are left.
+                                        A row with a bad block gets NaN counts in its usable
+                                        blocks, any other bad row none. Two rows of the batch
+                                        that share a cache row or block are undefined here  */
+    void *weights_scratch;           /* (device) with weights: gqa_weights_scratch_bytes(...)
+                                        bytes, 16-byte aligned, contents free before and
+                                        after the call; one call at a time              */
+    size_t weights_scratch_bytes;
 } gqa_options;
 
 /* Human-readable name of a status code (static storage). */
@@ -198,6 +242,12 @@ const char *gqa_status_string(gqa_status s);
  * overlap on the GPU need different workspaces).
  */
 size_t gqa_workspace_bytes(int B, int Hq, int Hkv, int D, gqa_dtype dt, const gqa_options *opt);
+
+/*
+ * Scratch bytes of a call with gqa_options.weights; capacity = Smax, or
+ * max_blocks * block_size. 0 for invalid sizes.
+ */
+size_t gqa_weights_scratch_bytes(int B, int Hq, int Hkv, long long capacity);
 
 /* Zero-fills a workspace asynchronously on `stream` (a cudaMemsetAsync). */
 gqa_status gqa_workspace_reset(void *workspace, size_t workspace_bytes, void *stream);
@@ -557,6 +607,67 @@ gqa_status gqa_attend_selected(const void *q, gqa_dtype q_dtype, const void *k_c
                                int D, int pool_blocks, int block_size, int n_select, gqa_dtype kv_dtype,
                                void *workspace, size_t workspace_bytes, int32_t *d_status, void *stream,
                                const gqa_options *opt);
+
+/*
+ * Rotary positions. Over the first `dim` elements of every head of q and k,
+ * pair i of a token at position pos becomes factor (x cos a - y sin a, x sin a
+ * + y cos a) with a = pos f_i; pair i is elements (i, i + dim / 2), with
+ * `interleaved` (2 i, 2 i + 1). Elements behind `dim` are copied. Rounded once
+ * to the vectors' type.
+ *
+ *  q, k      (device) (T, Hq, D) and (T, Hkv, D) of dt (float32 or bfloat16);
+ *            Hq or Hkv may be 0 (then its pointers are not used). D <= 1024
+ *  q_out, k_out (device) likewise; the same tensor (pointer and strides) is
+ *            turned in place, tensors that overlap otherwise are undefined
+ *  strides   (host) 8 values in elements: token and head of q, of k, of q_out,
+ *            of k_out; a head's elements lie next to each other. The fast form
+ *            wants 16-byte aligned pointers and strides
+ *  positions (device) (T,) int32, any value, or NULL: token t of row b (cu_q[b]
+ *            <= t < cu_q[b + 1]) is at lengths[b] + t - cu_q[b] then, and tokens
+ *            of no row are copied as they are (and those of a row with offsets
+ *            outside 0 .. T: GQA_STATUS_BAD_QLEN)
+ *  freqs     (device) (dim / 2) unsigned 64-bit: f_i / (2 pi) in fixed point, 64
+ *            bits behind the point, modulo one turn
+ */
+gqa_status gqa_rotate(const void *q, const void *k, void *q_out, void *k_out, gqa_dtype dt, const int64_t *strides,
+                      const int32_t *positions, const int32_t *lengths, const int32_t *cu_q, const uint64_t *freqs,
+                      float factor, int interleaved, int B, int T, int Hq, int Hkv, int D, int dim, int32_t *d_status,
+                      void *stream);
+
+/*
+ * Eviction: for every (row, cache head) of a row with more than n_keep valid
+ * slots, its first n_first slots, its last n_last and, of the others, those
+ * with the largest counts (gqa_options.weights; equal ones: the lowest slot, NaN
+ * counts as largest) are kept, n_keep in all, and moved together in ascending
+ * order: to slots 0 .. n_keep - 1 of the row (in place; counts move along, those
+ * behind become 0, the vectors behind stay as they are), or, with k_out and
+ * v_out, to slots 0 .. of row b of other buffers, the cache then only being
+ * read. Shorter rows keep every slot (and are copied too when there are outputs).
+ * Keys are moved as they are: positions that were turned into them stay.
+ *
+ *  k_cache, v_cache (device) float32, bfloat16 or E4M3 (GQA_ERR_UNSUPPORTED for
+ *           the others); D times the element size a multiple of 16
+ *  weights  (device) float32 counts, the cache's shape without D
+ *  lengths  (device) (B,) int32 valid slots, 0 <= lengths[b] <= capacity
+ *  n_keep   >= 1, >= n_first + n_last (both >= 0)
+ *  ids      (device) (B, Hkv, n_keep) int32: the kept slots, then -1
+ *  new_lengths (device) (B,) int32: min(lengths[b], n_keep); not `lengths` itself
+ *  k_out, v_out (device) (B, Hkv, out_slots, D), out_slots >= n_keep, both or
+ *           neither; must not overlap the cache. Slots behind the kept ones are left
+ *  weights_out (device) (B, Hkv, out_slots) or NULL: the kept counts, then zeros
+ * A row with a bad length, slot id or block sets its status bit: ids -1, length
+ * 0, nothing moved. Rows that share a block or cache row are undefined in place.
+ */
+gqa_status gqa_evict(void *k_cache, void *v_cache, float *weights, const int32_t *lengths, const int32_t *slot_ids,
+                     int32_t *ids, int32_t *new_lengths, void *k_out, void *v_out, float *weights_out, int out_slots,
+                     int B, int Hkv, int D, int R, int Smax, gqa_dtype kv_dtype, int n_keep, int n_first, int n_last,
+                     int32_t *d_status, void *stream);
+
+gqa_status gqa_evict_paged(void *k_blocks, void *v_blocks, float *weights, const int32_t *block_table,
+                           const int32_t *lengths, int32_t *ids, int32_t *new_lengths, void *k_out, void *v_out,
+                           float *weights_out, int out_slots, int B, int Hkv, int D, int num_blocks, int block_size,
+                           int max_blocks, gqa_dtype kv_dtype, int n_keep, int n_first, int n_last, int32_t *d_status,
+                           void *stream);
 
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH. */
 int gqa_version(void);
