@@ -56,6 +56,8 @@ __device__ __forceinline__ bool position(const RotateParams &p, int t, int &pos)
         pos = __ldg(p.positions + t);
         return true;
     }
+    if (p.B == 0)
+        return false;
     int lo = 0, hi = p.B;              // the last b with cu_q[b] <= t
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;

@@ -58,12 +58,12 @@ gqa_status gqa_rotate(const void *q, const void *k, void *q_out, void *k_out, gq
     if ((dt != GQA_DTYPE_F32 && dt != GQA_DTYPE_BF16) || T < 0 || Hq < 0 || Hkv < 0 || (long long)Hq + Hkv < 1 ||
         D < 1 || dim < 2 || dim % 2 || dim > D)
         return GQA_ERR_INVALID_ARGUMENT;
-    if (!positions && (B < 0 || !cu_q != !lengths || (!cu_q && T > 0 && B > 0)))
+    if (T == 0)
+        return GQA_OK;
+    if (!positions && (B < 0 || !cu_q || !lengths))
         return GQA_ERR_INVALID_ARGUMENT;
     if (D > 1024 || ((long long)Hq + Hkv) * D > (1 << 24))
         return GQA_ERR_UNSUPPORTED;
-    if (T == 0 || (!positions && B == 0))
-        return GQA_OK;
     if (!freqs || !strides || (Hq && (!q || !q_out)) || (Hkv && (!k || !k_out)))
         return GQA_ERR_INVALID_ARGUMENT;
     const unsigned es = dt == GQA_DTYPE_F32 ? 4 : 2;

@@ -1,0 +1,225 @@
+"""Capped, distance-biased and counted scores over bfloat16 and 8-bit caches."""
+import math
+
+import pytest
+import torch
+
+import gqa_kv_cache_gb300 as gqa
+import serve_reference as R
+
+pytestmark = pytest.mark.gpu
+
+
+class Case:
+    """A random cache; ``row`` gives its values in 64 bits."""
+
+    def __init__(self, kind, layout, lens, Hkv, G, D, Smax, bs=16, qt=torch.bfloat16, seed=0, room=0):
+        self.gen = g = torch.Generator().manual_seed(seed)
+        self.kind, self.lens, self.Hkv, self.G, self.D, self.bs, self.Smax = kind, lens, Hkv, G, D, bs, Smax
+        B = len(lens)
+        self.shape, self.table, self.slots = R.layout_of(layout, B, Hkv, Smax, bs, g, [n + room for n in lens])
+        self.q = torch.randn(B, Hkv * G, D, generator=g).to(qt)
+        self.kv, self.scales, self.kw = [], [None, None], {}
+        for i in range(2):
+            x = torch.randn(*self.shape, D, generator=g)
+            if kind == "int8":
+                self.kv.append((x * 34).round().clamp(-127, 127).to(torch.int8))
+                s = self.shape[:2] if self.table is not None else (*self.shape[:2], Smax // bs)
+                self.scales[i] = 0.02 + 0.02 * torch.rand(s, generator=g)
+            else:
+                self.kv.append(x.bfloat16())
+        if kind == "int8":
+            self.kw = dict(k_block_scale=self.scales[0].cuda(), v_block_scale=self.scales[1].cuda())
+        self.g = [x.cuda() for x in self.kv]
+
+    def row(self, i, b, n):
+        x = R.row_slots(self.kv[i], b, n, self.table, self.slots, self.bs).double()
+        if self.kind != "int8":
+            return x
+        s = self.scales[i]
+        if self.table is not None:
+            t = s[self.table[b, :-(-n // self.bs)].long()].T
+        else:
+            t = s[int(self.slots[b]) if self.slots is not None else b]
+        return x * torch.repeat_interleave(t.double(), self.bs, 1)[:, :n, None]
+
+    def attend(self, lens=None, **kw):
+        n = torch.tensor(self.lens if lens is None else lens, dtype=torch.int32).cuda()
+        if self.table is not None:
+            return gqa.attend_paged(self.q.cuda(), *self.g, self.table.cuda(), n, **self.kw, **kw)
+        return gqa.attend(self.q.cuda(), *self.g, n, None if self.slots is None else self.slots.cuda(), **self.kw, **kw)
+
+    def expect(self, cap=0.0, slopes=None, window=0, prefix=0, sink=None, lens=None):
+        """Per row: out, its tolerance, counts (Hkv, n), their tolerance."""
+        got = []
+        for b, n in enumerate(self.lens if lens is None else lens):
+            k, v, ok = self.row(0, b, n), self.row(1, b, n), R.attended(n, window, prefix)
+            shape = (self.Hkv, self.G)
+            o, w, e = R.attention(self.q[b].double().view(*shape, self.D), k, v, cap,
+                                  None if slopes is None else slopes.view(shape), ok,
+                                  None if sink is None else sink.view(shape))
+            got.append((o.reshape(-1, self.D), R.out_tolerance(w, e, float(v[:, ok].abs().max())), w.sum(1),
+                        R.count_tolerance(w, e)))
+        return got
+
+    def check(self, out, want, weights=None, base=None):
+        for b, (o, tol, w, wtol) in enumerate(want):
+            err = (out[b].cpu().double() - o).abs().max()
+            assert err <= tol, (b, float(err / tol))
+            if weights is not None:
+                n = w.shape[1]
+                got = R.row_slots(weights.cpu(), b, n, self.table, self.slots, self.bs).double()
+                was = R.row_slots(base, b, n, self.table, self.slots, self.bs).double()
+                bound = wtol + 2.0 ** -24 * (was + w)
+                assert ((got - was - w).abs() <= bound).all(), (b, float(((got - was - w).abs() / bound).max()))
+
+
+KINDS = ["bf16", "int8"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("layout,bs", [("dense", 32), ("slots", 16), ("paged", 16), ("paged", 24), ("paged", 64)])
+@pytest.mark.parametrize("D,G,qt", [(128, 4, torch.bfloat16), (64, 8, torch.float32), (128, 6, torch.float32),
+                                    (64, 1, torch.bfloat16), (128, 3, torch.float32)])
+def test_all_at_once(kind, layout, bs, D, G, qt):
+    lens = [1, 15, 16, 33, 130, 517]
+    c = Case(kind, layout, lens, 2, G, D, -(-576 // bs) * bs, bs, qt, seed=D + G)
+    slopes = torch.exp2(-torch.arange(1, 2 * G + 1).float() / 2)
+    sink = torch.randn(2 * G, generator=c.gen)
+    for kw in (dict(), dict(cap=5.0), dict(slopes=slopes), dict(cap=2.0, slopes=slopes, window=100, prefix=20, sink=sink)):
+        want = c.expect(**kw)
+        args = dict(window=kw.get("window", 0), kept_prefix=kw.get("prefix", 0), score_cap=kw.get("cap", 0.0),
+                    head_slopes=slopes.cuda() if "slopes" in kw else None, sink=sink.cuda() if "sink" in kw else None)
+        for grid in (0, 1, 5, 33):
+            base = torch.rand(c.shape, generator=c.gen)
+            weights = base.cuda()
+            out = c.attend(grid_ctas=grid, weights=weights, **args)
+            c.check(out, want, weights, base)
+            touched = torch.zeros(c.shape, dtype=torch.bool)
+            for b, n in enumerate(lens):
+                ok = R.attended(n, args["window"], args["kept_prefix"]).expand(2, -1)
+                R.put_row(touched, b, n, ok, c.table, c.slots, bs)
+            assert torch.equal(weights.cpu()[~touched], base[~touched])      # other counts are left
+            if kw or kind == "int8":
+                c.check(c.attend(grid_ctas=grid, **args), want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_cap_far_above_the_scores_changes_little(kind):
+    """cap = 2^20: c tanh(s / c) is s to s^3 / (3 c^2); tanhf to its steps."""
+    c = Case(kind, "dense", [100, 400], 2, 4, 128, 512, seed=3)
+    c.check(c.attend(score_cap=2.0 ** 20), c.expect(cap=2.0 ** 20))
+    small = c.attend(score_cap=1e-6)                              # every score the same: the mean of the values
+    for b, n in enumerate(c.lens):
+        v = c.row(1, b, n)
+        mean = v.mean(1)[:, None].expand(-1, 4, -1).reshape(-1, 128)
+        assert (small[b].cpu().double() - mean).abs().max() <= (2e-6 + 2.0 ** -17) * v.abs().max()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_masked_places_may_hold_anything(kind):
+    lens = [35, 70]                                               # windows from slots 16 and 51 on
+    c = Case(kind, "dense", lens, 1, 5, 64, 96, seed=4)
+    want = c.expect(cap=10.0, window=19)
+    for i in range(2):
+        if kind == "bf16":
+            c.g[i][:, :, 75:] = math.nan
+            c.g[i][:, :, :10] = math.inf
+        else:
+            c.kw["kv"[i] + "_block_scale"][:, :, 5:] = math.nan
+            c.kw["kv"[i] + "_block_scale"][:, :, 0] = math.nan
+    base = torch.zeros(c.shape)
+    weights = base.cuda()
+    c.check(c.attend(score_cap=10.0, window=19, weights=weights), want, weights, base)
+
+
+def test_scores_that_are_not_finite():
+    """A NaN key gives its row NaN and no other; -inf scores count as nothing."""
+    c = Case("bf16", "dense", [40, 40], 1, 2, 64, 48, seed=5)
+    c.g[0][0, 0, 7, 3] = math.nan
+    weights = torch.zeros(c.shape, device="cuda")
+    out = c.attend(weights=weights)
+    assert out[0].isnan().all() and weights[0, 0, :40].isnan().all() and not weights[0, 0, 40:].any()
+    want = c.expect()
+    assert (out[1].cpu().double() - want[1][0]).abs().max() <= want[1][1]
+    d = Case("bf16", "dense", [40], 1, 2, 64, 48, seed=6)
+    d.q = d.q.abs()
+    d.kv[0][0, 0, 7] = -math.inf
+    d.g[0] = d.kv[0].cuda()
+    weights = torch.zeros(d.shape, device="cuda")
+    out = d.attend(weights=weights)
+    assert out.isfinite().all() and float(weights[0, 0, 7]) == 0.0
+    assert abs(float(weights.sum()) - 2.0) <= 2 * 2.0 ** -15
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("layout", ["dense", "paged"])
+def test_decode_step(kind, layout):
+    lens = [0, 5, 31, 64, 300]
+    c = Case(kind, layout, lens, 2, 4, 128, 320, seed=8, room=1)
+    k, v = (torch.randn(5, 2, 128, generator=c.gen).bfloat16() for _ in range(2))
+    slopes = torch.rand(8, generator=c.gen)
+    weights = torch.zeros(c.shape, device="cuda")
+    at = torch.tensor(lens, dtype=torch.int32).cuda()
+    kw = dict(score_cap=3.0, head_slopes=slopes.cuda(), weights=weights, **c.kw)
+    if c.table is not None:
+        out = gqa.decode_step_paged(c.q.cuda(), k.cuda(), v.cuda(), *c.g, c.table.cuda(), at, **kw)
+    else:
+        out = gqa.decode_step(c.q.cuda(), k.cuda(), v.cuda(), *c.g, at, **kw)
+    after = [n + 1 for n in lens]
+    if kind == "bf16":
+        for i, x in enumerate((k, v)):
+            for b, n in enumerate(lens):
+                row = R.row_slots(c.kv[i], b, n + 1, c.table, None, 16).clone()
+                row[:, n] = x[b]
+                R.put_row(c.kv[i], b, n + 1, row, c.table, None, 16)
+            assert torch.equal(c.g[i].cpu(), c.kv[i])
+    else:                                                          # the codes' own test is test_gpu_block8
+        c.kv = [x.cpu() for x in c.g]
+        c.scales = [c.kw["k_block_scale"].cpu(), c.kw["v_block_scale"].cpu()]
+    c.check(out, c.expect(cap=3.0, slopes=slopes, lens=after), weights, torch.zeros(c.shape))
+
+
+def test_long_rows_and_many_pieces():
+    """One row of 60000 slots cut among every CTA, its counts summing to the heads."""
+    c = Case("int8", "paged", [60000], 1, 8, 64, 60032, bs=64, seed=9)
+    base = torch.zeros(c.shape)
+    weights = base.cuda()
+    c.check(c.attend(weights=weights), c.expect(), weights, base)
+    weights.zero_()
+    c.check(c.attend(weights=weights, grid_ctas=700), c.expect(), weights, base)
+
+
+def test_bad_rows():
+    c = Case("bf16", "paged", [40, 40, 40], 2, 2, 64, 64, seed=10)
+    c.table[1, 1] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    weights = torch.zeros(c.shape, device="cuda")
+    out = c.attend(lens=[40, 40, 65], weights=weights, status=status)
+    assert int(status) == 5 and out[1:].isnan().all() and out[0].isfinite().all()
+    assert weights[c.table[1, 0].long()].isnan().all()
+    assert not weights[c.table[2, :3].long()].any()
+    assert abs(float(weights[c.table[0, :3].long()].sum()) - 4.0) < 1e-3
+
+
+def test_refusals():
+    c = Case("bf16", "dense", [20, 20], 2, 2, 64, 32)
+    w = torch.zeros(c.shape, device="cuda")
+    for bad in (dict(head_slopes=torch.zeros(3, device="cuda")), dict(head_slopes=torch.zeros(4, device="cuda").double()),
+                dict(weights=w[:, :1].contiguous()), dict(weights=w.double()), dict(k_scale=w[0, :, 0], score_cap=1.0),
+                dict(wait_limit_cycles=5, score_cap=1.0)):
+        with pytest.raises(TypeError):
+            c.attend(**bad)
+    for bad in (dict(weights=w.cpu()), dict(head_slopes=torch.zeros(4)),
+                dict(weights=torch.zeros(2, 32, 2, device="cuda").transpose(1, 2))):
+        with pytest.raises(ValueError):
+            c.attend(**bad)
+    for bad in (dict(score_cap=-1.0), dict(score_cap=math.inf), dict(score_cap=math.nan), dict(score_cap=1.0, kernel="simt")):
+        with pytest.raises(gqa.GqaError):
+            c.attend(**bad)
+    q, n = c.q.cuda(), torch.tensor([20, 20], dtype=torch.int32).cuda()
+    with pytest.raises(TypeError):
+        gqa.attend(q, c.g[0].float(), c.g[1].float(), n, score_cap=2.0)
+    d = Case("bf16", "dense", [20], 1, 9, 64, 32)
+    with pytest.raises(gqa.GqaError):
+        d.attend(score_cap=2.0)
