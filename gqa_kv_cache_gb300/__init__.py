@@ -203,7 +203,7 @@ def _workspace(device, nbytes, stream=None):
 _need_cache: dict = {}
 
 
-def _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, device, scored=False):
+def _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, device, scored=0):
     """gqa_workspace_bytes of these sizes on this device (asked once)."""
     key = (B, Hq, Hkv, D, dt, kernel, grid_ctas, device.index, scored)
     n = _need_cache.get(key)
@@ -415,7 +415,8 @@ def _step_scored(q, k_new, v_new, k, v, lengths, slot_ids, table, out, status, k
                 scratch = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
             o.weights_scratch = scratch.data_ptr()
             o.weights_scratch_bytes = need
-        need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, device, True)
+        need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, device,
+                     1 + bool(score_cap or head_slopes is not None or weights is not None))
         ws = _workspace(device, need, stream) if workspace is None else workspace
         if out is None:
             with torch.cuda.stream(stream) if stream is not None else _HERE:

@@ -21,7 +21,8 @@ SOURCES = ["gqa_api.cu", "gqa_simt.cu", "gqa_simt_f32_small.cu", "gqa_simt_f32_l
            "gqa_simt_bf16_small.cu", "gqa_simt_bf16_large.cu", "gqa_simt_f32_small_plain.cu",
            "gqa_simt_f32_large_plain.cu", "gqa_simt_bf16_small_plain.cu", "gqa_simt_bf16_large_plain.cu",
            "gqa_tc.cu", "gqa_tc_fine.cu", "gqa_tc_multi.cu", "gqa_unit.cu",
-           "gqa_q4.cu", "gqa_scored.cu", "gqa_scored_i8_128.cu", "gqa_scored_i8_64.cu", "gqa_scored_bf16.cu",
+           "gqa_q4.cu", "gqa_scored.cu", *(f"gqa_scored_i8_{d}_{rows}{more}.cu" for d in (128, 64) for rows in ("few", "rows")
+                                            for more in ("", "_more")), "gqa_scored_bf16_128.cu", "gqa_scored_bf16_64.cu",
            "gqa_rows.cu", "gqa_select.cu", "gqa_cache_api.cu",
            "gqa_rotate.cu", "gqa_evict.cu", "gqa_serve_api.cu",
            "gqa_validate.cu",

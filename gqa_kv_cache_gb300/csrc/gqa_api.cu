@@ -43,10 +43,8 @@ bool unit_ok(gqa_dtype dt, int D, int G, long long cap_rows, bool multi)
 
 // Whether the scored attend runs the step: an 8-bit cache, or scores that are
 // capped, biased or counted.
-bool is_scored(gqa_dtype dt, const gqa_options *opt)
-{
-    return dt == GQA_DTYPE_I8 || (opt && (opt->score_cap > 0.f || opt->head_slopes || opt->weights));
-}
+bool more_scores(const gqa_options *opt) { return opt && (opt->score_cap > 0.f || opt->head_slopes || opt->weights); }
+bool is_scored(gqa_dtype dt, const gqa_options *opt) { return dt == GQA_DTYPE_I8 || more_scores(opt); }
 
 // Kernel the call will use (GQA_KERNEL_SIMT / _TC / _UNIT) or -1. AUTO takes
 // the small-cache kernel when it applies and the units (B * Hkv, known > 0)
@@ -103,11 +101,12 @@ int grid_for(int kernel, const gqa_options *opt, gqa_dtype dt, int D, int G, gqa
         return 0;
     const int sms = sm_count(dev);
     if (is_scored(dt, opt)) {
-        static std::atomic<int> per_sm[2][2][2][2];   // by kind, D, rows, query type
-        std::atomic<int> &c = per_sm[dt == GQA_DTYPE_I8][D == 128][G <= 4][q_dt == GQA_DTYPE_BF16];
+        static std::atomic<int> per_sm[2][2][2][2][2];   // by kind, D, rows, scores, query type
+        const bool more = more_scores(opt), q_bf16 = q_dt == GQA_DTYPE_BF16;
+        std::atomic<int> &c = per_sm[dt == GQA_DTYPE_I8][D == 128][G <= 4][more][q_bf16];
         int n = c.load(std::memory_order_relaxed);
         if (!n)
-            c.store(n = scored_ctas_per_sm(dt, D, G, q_dt == GQA_DTYPE_BF16), std::memory_order_relaxed);
+            c.store(n = scored_ctas_per_sm(dt, D, G, more, q_bf16), std::memory_order_relaxed);
         return sms * n;
     }
     if (dt == GQA_DTYPE_E2M1) {

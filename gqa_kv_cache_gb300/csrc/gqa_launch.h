@@ -66,7 +66,7 @@ struct ScoredParams : DecodeParams {
 bool scored_supports(int kind, int D, int G);
 int scored_tile(int kind, int D);
 bool scored_whole_units(int kind, int D, long long capacity, long long units, int grid);   // one CTA a unit
-int scored_ctas_per_sm(int kind, int D, int G, bool q_bf16);   // resident CTAs per SM
+int scored_ctas_per_sm(int kind, int D, int G, bool more, bool q_bf16);   // resident CTAs per SM (more: see gqa_scored.cu)
 long long scored_count_ctas(int B, int Hkv, long long capacity);   // of the kernel that counts
 size_t scored_scratch_bytes(int B, int Hq, int Hkv, long long capacity);   // of xs and row_end
 cudaError_t scored_launch(const ScoredParams &p, cudaStream_t st);   // the attend, and the counts where asked for

@@ -4,21 +4,23 @@
 
 namespace gqa {
 
-cudaError_t scored_i8_128(bool few, bool q_bf16, bool paged, const ScoredParams *p, cudaStream_t st, int *per_sm);
-cudaError_t scored_i8_64(bool few, bool q_bf16, bool paged, const ScoredParams *p, cudaStream_t st, int *per_sm);
-cudaError_t scored_bf16(int D, bool q_bf16, bool paged, const ScoredParams *p, cudaStream_t st, int *per_sm);
+using Launch = cudaError_t(bool q_bf16, bool paged, const ScoredParams *p, cudaStream_t st, int *per_sm);
+Launch scored_i8_128_few_more, scored_i8_128_few, scored_i8_128_rows_more, scored_i8_128_rows,
+    scored_i8_64_few_more, scored_i8_64_few, scored_i8_64_rows_more, scored_i8_64_rows,
+    scored_bf16_128, scored_bf16_64;
 
 namespace {
 
 using scored::kFew;
 using scored::kRows;
 
-cudaError_t launch(int kind, int D, int G, bool q_bf16, bool paged, const ScoredParams *p, cudaStream_t st, int *per_sm)
+// more: capped, biased or counted scores (over a bfloat16 cache always)
+cudaError_t launch(int kind, int D, int G, bool more, bool q_bf16, bool paged, const ScoredParams *p, cudaStream_t st, int *per_sm)
 {
-    if (kind == kBf16)
-        return scored_bf16(D, q_bf16, paged, p, st, per_sm);
-    return D == 128 ? scored_i8_128(G <= kFew, q_bf16, paged, p, st, per_sm)
-                    : scored_i8_64(G <= kFew, q_bf16, paged, p, st, per_sm);
+    Launch *const of[2][2][2] = {{{scored_i8_64_rows, scored_i8_64_rows_more}, {scored_i8_64_few, scored_i8_64_few_more}},
+                                 {{scored_i8_128_rows, scored_i8_128_rows_more}, {scored_i8_128_few, scored_i8_128_few_more}}};
+    Launch *f = kind == kI8 ? of[D == 128][G <= kFew][more] : D == 128 ? scored_bf16_128 : scored_bf16_64;
+    return f(q_bf16, paged, p, st, per_sm);
 }
 
 constexpr int kCountThreads = 256, kCountSlots = 4;   // slots a thread
@@ -112,12 +114,12 @@ bool scored_whole_units(int kind, int D, long long capacity, long long units, in
     return capacity <= 4 * tile || (capacity <= 8 * tile && units <= grid);
 }
 
-int scored_ctas_per_sm(int kind, int D, int G, bool q_bf16)
+int scored_ctas_per_sm(int kind, int D, int G, bool more, bool q_bf16)
 {
     int least = 1 << 30;
     for (bool paged : {false, true}) {
         int n = 0;
-        if (launch(kind, D, G, q_bf16, paged, nullptr, nullptr, &n) != cudaSuccess)
+        if (launch(kind, D, G, more, q_bf16, paged, nullptr, nullptr, &n) != cudaSuccess)
             return 1;
         least = n < least ? n : least;
     }
@@ -138,7 +140,7 @@ size_t scored_scratch_bytes(int B, int Hq, int Hkv, long long capacity)
 
 cudaError_t scored_launch(const ScoredParams &p, cudaStream_t st)
 {
-    const cudaError_t e = launch(p.kind, p.D, p.G, p.q_bf16, p.paged, &p, st, nullptr);
+    const cudaError_t e = launch(p.kind, p.D, p.G, p.cap > 0.f || p.slopes || p.weights, p.q_bf16, p.paged, &p, st, nullptr);
     if (e != cudaSuccess || !p.weights)
         return e;
     return p.gp == 4 ? launch_count<4>(p, st) : launch_count<8>(p, st);

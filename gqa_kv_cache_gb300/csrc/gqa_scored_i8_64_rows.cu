@@ -1,0 +1,11 @@
+// Instantiations of the scored attend (gqa_scored_kernel.cuh): 8-bit caches, D = 64, more query rows.
+#include "gqa_scored_kernel.cuh"
+
+namespace gqa {
+
+cudaError_t scored_i8_64_rows(bool q_bf16, bool paged, const ScoredParams *p, cudaStream_t st, int *per_sm)
+{
+    return scored::launch_d<kI8, 64, false, false>(q_bf16, paged, p, st, per_sm);
+}
+
+}  // namespace gqa

@@ -65,17 +65,24 @@ template <int KIND, int D>
 struct Form {
     static constexpr bool I8 = KIND == kI8;
     static constexpr int VB = I8 ? D : 2 * D;             // bytes a vector
-    static constexpr int SUB = VB == 256 ? 1 : 2;         // 16-slot parts of a warp's share of a tile
+        static constexpr int SUB = VB == 256 ? 1 : 2;         // 16-slot parts of a warp's share of a tile
     static constexpr int SHARE = 16 * SUB;                // a warp's slots of a tile
     static constexpr int TILE = kWarps * SHARE;           // slots a tile
     static constexpr int LV = VB / 16;                    // lanes (16-byte pieces) a vector
     static constexpr int VI = 32 / LV;                    // vectors a copy instruction
     static constexpr int NI = 16 / VI;                    // copy instructions a part
-    static constexpr int CTAS = VB == 64 ? 3 : 2;         // resident CTAs per SM
 };
 
-// Tiles of a warp's ring: as many as let CTAS CTAs share an SM (the rows of a
-// float32 query take 16 KB where there are more than four).
+// Resident CTAs per SM, and tiles of a warp's ring. Measured on four rows of
+// 32768 .. 131071 slots: 8 bits, D = 128, G = 8 two CTAs of three tiles 109.9
+// us, three of two 114.5 (168 registers are too few); D = 64 three of three 80.0,
+// four of three 82.3, two of five 85.2. The rows of a float32 query of more than
+// four take 16 KB, which leaves room for two tiles.
+template <int KIND, int D>
+constexpr int ctas()
+{
+    return KIND == kI8 && D == 64 ? 3 : 2;
+}
 template <int KIND, int D, bool QF32, bool FEW>
 constexpr int stages()
 {
@@ -86,9 +93,9 @@ constexpr int stages()
 // 16-byte pieces permuted so that the operand loads below have no bank
 // conflicts, and (8 bits) the slots' scales.
 template <int KIND, int D>
-struct Stage {
+struct alignas(128) Stage {
     uint8_t k[Form<KIND, D>::SHARE * Form<KIND, D>::VB], v[Form<KIND, D>::SHARE * Form<KIND, D>::VB];
-    float ks[KIND == kI8 ? Form<KIND, D>::SHARE : 4], vs[KIND == kI8 ? Form<KIND, D>::SHARE : 4];
+    float ks[KIND == kI8 ? Form<KIND, D>::SHARE : 1], vs[KIND == kI8 ? Form<KIND, D>::SHARE : 1];
 };
 
 // Offset of 16-byte piece c of the share's vector r.
@@ -106,11 +113,18 @@ __device__ __forceinline__ uint32_t smem_at(const void *p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// Asynchronous copies to shared memory; `n` of the bytes come from src (all or
-// none of them) and the others are zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+// Asynchronous copies to shared memory (DO, SO: byte offsets; HINT: with a
+// cache policy), and those of which `n` bytes come from src (all or none of
+// them) and the others are zeros.
+template <int DO, int SO, bool HINT>
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint64_t policy)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    if constexpr (HINT)
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0 + %2], [%1 + %3], 16, %4;" ::"r"(dst), "l"(src), "n"(DO),
+                     "n"(SO), "l"(policy)
+                     : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DO), "n"(SO) : "memory");
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n)
 {
@@ -127,20 +141,22 @@ __device__ __forceinline__ void copy_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// d += a b, or (first) d = a b: the sum's zeros then take no registers.
 template <bool F16>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+__device__ __forceinline__ void mma(bool first, float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1)
 {
+    const float c0 = first ? 0.f : d[0], c1 = first ? 0.f : d[1], c2 = first ? 0.f : d[2], c3 = first ? 0.f : d[3];
     if constexpr (F16)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+            "{%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     else
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+            "{%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t a)
@@ -171,11 +187,16 @@ __device__ __forceinline__ uint32_t u32(__nv_bfloat162 v) { return *reinterpret_
 
 // Bytes SEL of w (codes with the sign bit flipped: c + 128) as an f16 pair: the
 // byte under 0x64 is the f16 1024 + 128 + c; exact.
+// over: 0x64646464 in a register of its own (magic_bytes).
 template <int SEL>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w)
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t over)
 {
-    return u32(__hsub2(h2(__byte_perm(w, 0x64646464u, SEL)), h2(0x64806480u)));
+    return u32(__hsub2(h2(__byte_perm(w, over, SEL)), h2(0x64806480u)));
 }
+
+// 0x64646464 that the compiler cannot see through: as a constant it was moved
+// to a register again before most of its 128 uses a tile.
+__device__ __forceinline__ uint32_t magic_bytes() { return __shfl_sync(0xffffffffu, 0x64646464u, 0); }
 
 // Two float32 as an f16 pair and the f16 pair of MUL times what it leaves.
 __device__ __forceinline__ void split2(float x, float y, float times, uint32_t &hi, uint32_t &lo)
@@ -306,6 +327,7 @@ struct Fetch {
     bool good;
     uint32_t line;     // dense: vector of slot 0
     uint32_t block0;   // dense, 8 bits: block of slot 0
+    uint64_t policy;   // cache policy of the vectors
     int page, page_next;   // paged: the block of part lane % SUB of a tile, 32 / SUB tiles; of the tiles behind them
 };
 
@@ -365,8 +387,23 @@ __device__ __forceinline__ void enter(const ScoredParams &p, const TileCursor &c
     }
 }
 
+// The copies of part U's vectors, which follow each other: instruction j takes
+// vectors VI j + lane / LV, whose pieces are permuted as those of vector lane /
+// LV but for bits of the piece's number that VI j brings (constants here; the
+// stage lies on 128 bytes).
+template <class F, int U, bool MORE, int J = 0>
+__device__ __forceinline__ void copy_part(uint32_t dk, uint32_t dv, const uint8_t *k, const uint8_t *v, uint64_t policy)
+{
+    constexpr int FLIP = F::VB == 64 ? 0 : ((F::VI * J) & 7) << 4;
+    constexpr int DO = (16 * U + F::VI * J) * F::VB, SO = F::VI * J * F::VB;
+    copy16<DO, SO, MORE>(dk ^ FLIP, k, policy);
+    copy16<DO, SO, MORE>(dv ^ FLIP, v, policy);
+    if constexpr (J + 1 < F::NI)
+        copy_part<F, U, MORE, J + 1>(dk, dv, k, v, policy);
+}
+
 // Starts the copies of the warp's share of tile f.t.
-template <int KIND, int D, bool PAGED>
+template <int KIND, int D, bool PAGED, bool MORE>
 __device__ __forceinline__ void fetch_tile(const ScoredParams &p, const Fetch &f, const TileCursor &c, Stage<KIND, D> &st,
                                            int *bad, int shift, bool pages, int warp, int lane)
 {
@@ -379,12 +416,9 @@ __device__ __forceinline__ void fetch_tile(const ScoredParams &p, const Fetch &f
     const uint8_t *kc = static_cast<const uint8_t *>(p.k_cache), *vc = static_cast<const uint8_t *>(p.v_cache);
     const int e = s + F::SHARE - 1;
     const int r0 = lane / F::LV, c0 = lane % F::LV;
-    // block (of the dense cache) that holds slot x
-    [[maybe_unused]] auto block_of = [&](int x) {
-        return f.block0 + (p.scale_shift >= 0 ? (uint32_t)x >> p.scale_shift : (uint32_t)x / (uint32_t)p.scale_block);
-    };
     if (pages && e <= c.L && (s >= c.lo || e < c.P)) {
         // every slot is in the softmax, 16 vectors in a row at least
+        const uint32_t to = (uint32_t)piece<F::VB>(r0, c0);
 #pragma unroll
         for (int u = 0; u < F::SUB; ++u) {
             uint32_t row;
@@ -400,19 +434,16 @@ __device__ __forceinline__ void fetch_tile(const ScoredParams &p, const Fetch &f
             } else {
                 row = f.line + (uint32_t)(s + 16 * u);
             }
-            const uint64_t in = (uint64_t)(row + r0) * F::VB + c0 * 16;
-            const uint8_t *k0 = kc + in, *v0 = vc + in;
-#pragma unroll
-            for (int j = 0; j < F::NI; ++j) {
-                const uint32_t to = (uint32_t)piece<F::VB>(16 * u + F::VI * j + r0, c0);
-                copy16(dk + to, k0 + j * F::VI * F::VB);
-                copy16(dv + to, v0 + j * F::VI * F::VB);
-            }
+            const uint64_t in = (uint64_t)row * F::VB + lane * 16;
+            if (u == 0)
+                copy_part<F, 0, MORE>(dk + to, dv + to, kc + in, vc + in, f.policy);
+            else
+                copy_part<F, F::SUB - 1, MORE>(dk + to, dv + to, kc + in, vc + in, f.policy);
             if constexpr (F::I8) {
                 // lanes 0 .. 15 the key scales of the part's slots, 16 .. 31 the value scales
                 const int i = 16 * u + (lane & 15);
                 if constexpr (!PAGED)
-                    block = block_of(s + i);
+                    block = f.block0 + ((uint32_t)(s + i) >> p.scale_shift);
                 copy4((lane < 16 ? dks : dvs) + 4 * i, (lane < 16 ? p.k_block_scale : p.v_block_scale) + block, 4);
             }
         }
@@ -448,7 +479,7 @@ __device__ __forceinline__ void fetch_tile(const ScoredParams &p, const Fetch &f
             if constexpr (PAGED)
                 at = (uint64_t)x / (uint32_t)p.block_size;
             else
-                at = block_of(s + j);
+                at = f.block0 + (uint32_t)(s + j) / (uint32_t)p.scale_block;
         }
         copy4(dks + 4 * j, p.k_block_scale + at, x < 0 ? 0 : 4);
         copy4(dvs + 4 * j, p.v_block_scale + at, x < 0 ? 0 : 4);
@@ -459,14 +490,11 @@ __device__ __forceinline__ void fetch_tile(const ScoredParams &p, const Fetch &f
 // row t); s[2], s[3] slot g + 8. 8 bits: times the slot's key scale.
 template <int KIND, int D, bool QF32, bool FEW, int PARTS>
 __device__ __forceinline__ void scores(const Stage<KIND, D> &st, int u, int lane, const uint32_t (&qf)[PARTS][D / 16][2],
-                                       float (&s)[4])
+                                       float (&s)[4], [[maybe_unused]] uint32_t over)
 {
     using F = Form<KIND, D>;
     const int g = lane >> 2, t = lane & 3;
-    float s2[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        s[i] = 0.f;
+    float s2[4];
     if constexpr (KIND == kI8) {
         uint32_t k[2][D / 16];
 #pragma unroll
@@ -479,11 +507,12 @@ __device__ __forceinline__ void scores(const Stage<KIND, D> &st, int u, int lane
 #pragma unroll
         for (int w = 0; w < D / 16; ++w) {
             const uint32_t x = k[0][w] ^ 0x80808080u, y = k[1][w] ^ 0x80808080u;
-            const uint32_t a0 = code_pair<0x4140>(x), a1 = code_pair<0x4140>(y), a2 = code_pair<0x4342>(x), a3 = code_pair<0x4342>(y);
+            const uint32_t a0 = code_pair<0x4140>(x, over), a1 = code_pair<0x4140>(y, over);
+            const uint32_t a2 = code_pair<0x4342>(x, over), a3 = code_pair<0x4342>(y, over);
             float(&d)[4] = w & 1 ? s2 : s;
-            mma<true>(d, a0, a1, a2, a3, qf[0][w][0], qf[0][w][1]);
+            mma<true>(w < 2, d, a0, a1, a2, a3, qf[0][w][0], qf[0][w][1]);
             if constexpr (PARTS == 2)
-                mma<true>(d, a0, a1, a2, a3, qf[1][w][0], qf[1][w][1]);
+                mma<true>(false, d, a0, a1, a2, a3, qf[1][w][0], qf[1][w][1]);
         }
     } else {
 #pragma unroll
@@ -493,7 +522,7 @@ __device__ __forceinline__ void scores(const Stage<KIND, D> &st, int u, int lane
             float(&d)[4] = w & 1 ? s2 : s;
 #pragma unroll
             for (int k = 0; k < PARTS; ++k)
-                mma<false>(d, a[0], a[1], a[2], a[3], qf[k][w][0], qf[k][w][1]);
+                mma<false>(w < 2 && k == 0, d, a[0], a[1], a[2], a[3], qf[k][w][0], qf[k][w][1]);
         }
     }
 #pragma unroll
@@ -520,7 +549,7 @@ __device__ __forceinline__ void scores(const Stage<KIND, D> &st, int u, int lane
 // out_dim.
 template <int KIND, int D, bool FEW>
 __device__ __forceinline__ void weigh(const Stage<KIND, D> &st, int lane, const float (&w)[Form<KIND, D>::SUB][FEW ? 2 : 4],
-                                      float (&o)[D / 16][FEW ? 2 : 4])
+                                      float (&o)[D / 16][FEW ? 2 : 4], [[maybe_unused]] uint32_t over)
 {
     using F = Form<KIND, D>;
     constexpr int SUB = F::SUB;
@@ -559,8 +588,8 @@ __device__ __forceinline__ void weigh(const Stage<KIND, D> &st, int lane, const 
             }
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            float d[2][4] = {};
-            [[maybe_unused]] float r[FEW ? 1 : 2][4] = {};
+            float d[2][4];
+            [[maybe_unused]] float r[FEW ? 1 : 2][4];
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
                 // bytes: dims 4 i, 4 i + 1 (then + 2, + 3) of two neighbouring slots
@@ -569,11 +598,11 @@ __device__ __forceinline__ void weigh(const Stage<KIND, D> &st, int lane, const 
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const uint32_t a = __byte_perm(x0, x1, q ? 0x7362 : 0x5140), b = __byte_perm(x2, x3, q ? 0x7362 : 0x5140);
-                    const uint32_t a0 = code_pair<0x4140>(a), a1 = code_pair<0x4342>(a);
-                    const uint32_t a2 = code_pair<0x4140>(b), a3 = code_pair<0x4342>(b);
-                    mma<true>(d[q], a0, a1, a2, a3, bh[u][0], bh[u][1]);
+                    const uint32_t a0 = code_pair<0x4140>(a, over), a1 = code_pair<0x4342>(a, over);
+                    const uint32_t a2 = code_pair<0x4140>(b, over), a3 = code_pair<0x4342>(b, over);
+                    mma<true>(u == 0, d[q], a0, a1, a2, a3, bh[u][0], bh[u][1]);
                     if constexpr (!FEW)
-                        mma<true>(r[q], a0, a1, a2, a3, bl[u][0], bl[u][1]);
+                        mma<true>(u == 0, r[q], a0, a1, a2, a3, bl[u][0], bl[u][1]);
                 }
             }
 #pragma unroll
@@ -603,14 +632,14 @@ __device__ __forceinline__ void weigh(const Stage<KIND, D> &st, int lane, const 
             }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            float d[4];
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
                 uint32_t a[4];
                 ldmatrix4<true>(a, smem_at(st.v) + piece<F::VB>(16 * u + (lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)));
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
-                    mma<false>(d, a[0], a[1], a[2], a[3], b[u][k][0], b[u][k][1]);
+                    mma<false>(u == 0 && k == 0, d, a[0], a[1], a[2], a[3], b[u][k][0], b[u][k][1]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -619,13 +648,61 @@ __device__ __forceinline__ void weigh(const Stage<KIND, D> &st, int lane, const 
     }
 }
 
+// s -> cap tanh(s) of the lane's scores (s over the cap, cap in base-2 units).
+// While every score of the warp is within the cap tanh is Lambert's continued
+// fraction cut at the 7th partial quotient (off by 2.2e-12 of it at 1, less
+// below), in all four steps of 2^-24, in tanhf's place, which takes
+// about three times as long.
+template <int SUB, int C>
+__device__ __forceinline__ void cap_scores(float (&s)[SUB][4], float cap)
+{
+    float top = 0.f;
+#pragma unroll
+    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 2 * C; ++i)
+            top = fmaxf(top, fabsf(s[u][i / C * 2 + i % C]));
+    if (__any_sync(0xffffffffu, top > 1.f)) {
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 2 * C; ++i) {
+                float &y = s[u][i / C * 2 + i % C];
+                y = tanhf(y) * cap;
+            }
+        return;
+    }
+#pragma unroll
+    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 2 * C; ++i) {
+            float &y = s[u][i / C * 2 + i % C];
+            const float z = y * y;
+            // z (378 + z) .. over 135135: both sides of the fraction divided by it
+            const float num = fmaf(fmaf(fmaf(z, 1.f / 135135.f, 378.f / 135135.f), z, 17325.f / 135135.f), z, 1.f);
+            const float den = fmaf(fmaf(fmaf(z, 28.f / 135135.f, 3150.f / 135135.f), z, 62370.f / 135135.f), z, 1.f);
+            y = __fdividef(y * cap * num, den);
+        }
+}
+
+// A lane's scores of a slot into the array of counted scores (C = 1: the first),
+// to stay in L2 until they are read.
+template <int C>
+__device__ __forceinline__ void store_scores(float *to, float x, float y, uint64_t keep)
+{
+    if constexpr (C == 1)
+        asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(to), "f"(x), "l"(keep) : "memory");
+    else
+        asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(to), "f"(x), "f"(y), "l"(keep) : "memory");
+}
+
 // Scratch of the merge (segment_out, unit_ticket_merge): as many partials at a
 // time as the spare slot has room for.
 template <int KIND, int D>
 using Merge = MergeBufT<kRows, D == 128 ? 28 : 12>;
 
-template <int KIND, int D, bool QF32, bool PAGED, bool FEW>
-__global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(const ScoredParams p)
+template <int KIND, int D, bool QF32, bool PAGED, bool FEW, bool MORE>
+__global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const ScoredParams p)
 {
     using F = Form<KIND, D>;
     using St = Stage<KIND, D>;
@@ -652,12 +729,19 @@ __global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!p.whole_units)
         schedule_walk(p, sched, &walk);
-    // whole pages of 16 slots: one vector index a part; else slot by slot
+    // whole pages of 16 slots: one vector index a part; else slot by slot (a
+    // dense 8-bit cache: where a block of scales is not a power of two)
     const int shift = PAGED ? __ffs(p.block_size) - 1 : 0;
-    const bool pages = !PAGED || (p.block_size >= 16 && (p.block_size & (p.block_size - 1)) == 0);
+    const bool pages = PAGED ? p.block_size >= 16 && (p.block_size & (p.block_size - 1)) == 0 : !I8 || p.scale_shift >= 0;
 
     // the copies: tile f.t of segment sf is the next to fetch
     Fetch f = {};
+    if constexpr (MORE) {
+        if (p.xs)                          // the vectors leave the L2 to the scores
+            asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(f.policy));
+        else
+            asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(f.policy));
+    }
     int sf = 0;
     bool in_b = false, left;
     {
@@ -678,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(c
     }
     auto fetch = [&](int slot) {
         if (left) {
-            fetch_tile<KIND, D, PAGED>(p, f, segs[sf].c, ring[slot][warp], &sm_bad[warp][sf], shift, pages, warp, lane);
+            fetch_tile<KIND, D, PAGED, MORE>(p, f, segs[sf].c, ring[slot][warp], &sm_bad[warp][sf], shift, pages, warp, lane);
             if (f.t < f.t_last) {
                 ++f.t;
                 if constexpr (PAGED) {
@@ -707,16 +791,20 @@ __global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(c
     for (int i = 0; i < STAGES - 1; ++i)
         fetch(i);
 
+    const uint32_t over = I8 ? magic_bytes() : 0u;
     // the first segment's query rows, every warp's part (those of a later one
     // came with the last tile of the segment before it, whose end the warps
     // meet at)
     copy_wait<STAGES - 2>();
     __syncthreads();
-    // scores that are more than a product: capped, biased or counted ones are
-    // formed in place, and then need no factor
-    const bool formed = p.cap > 0.f || p.slopes || p.xs;
+    [[maybe_unused]] uint64_t keep;        // cache policy of the counted scores
+    if constexpr (MORE)
+        asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
     uint32_t qf[PARTS][D / 16][2];
-    float mul[C], fin[C], slope[C];        // product to score; score to base-2 score; base-2 bias a slot
+    // product to (base-2) score, base-2 bias a slot. MORE: scores that are capped,
+    // biased or counted are formed in place
+    float mul[C];
+    [[maybe_unused]] float slope[C];
     float m[C], l[C];                      // reference and sum of the lane's rows
     float o[D / 16][FEW ? 2 : 4];
     for (int sc = 0;; sc = (sc + 1) % kSegs) {
@@ -726,13 +814,13 @@ __global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(c
         if (!good && tid == 0 && seg->c.t == 0 && seg->c.kvh == 0)
             report(p, row_error_bits(p, seg->c.b, seg->c.L));
         float mine;
-        load_query<KIND, D, QF32, FEW, PARTS>(p.cap > 0.f ? p.scale_cap : p.scale_log2, sm_q[sc], lane, qf, mine);
+        load_query<KIND, D, QF32, FEW, PARTS>(MORE && p.cap > 0.f ? p.scale_cap : p.scale_log2, sm_q[sc], lane, qf, mine);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int row = C * t4 + c;
+            [[maybe_unused]] const int row = C * t4 + c;
             mul[c] = I8 ? __shfl_sync(0xffffffffu, mine, 8 * t4 + 4 * c) : mine;
-            fin[c] = formed ? 1.f : mul[c];
-            slope[c] = p.slopes && row < p.G ? __ldg(p.slopes + seg->c.kvh * p.G + row) * 1.4426950408889634f : 0.f;
+            if constexpr (MORE)
+                slope[c] = p.slopes && row < p.G ? __ldg(p.slopes + seg->c.kvh * p.G + row) * 1.4426950408889634f : 0.f;
             m[c] = -INFINITY;
             l[c] = 0.f;
         }
@@ -758,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(c
             float s[SUB][4];
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
-                scores<KIND, D, QF32, FEW, PARTS>(st, u, lane, qf, s[u]);
+                scores<KIND, D, QF32, FEW, PARTS>(st, u, lane, qf, s[u], over);
             // bits 2 u + i: slot 16 u + g + 8 i is in the softmax
             unsigned ok = good ? ~0u : 0u;
             const int s0 = share_slot<F>(t, seg->c.tp, seg->c.gap, warp), L = seg->c.L, lo = seg->c.lo, P = seg->c.P;
@@ -770,30 +858,35 @@ __global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(c
                         if (!attended(L, lo, P, s0 + 16 * u + g + 8 * i))
                             ok &= ~(1u << (2 * u + i));
             }
-            if (formed) {
+            if constexpr (MORE) {
                 // base-2 scores in place
 #pragma unroll
                 for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int j = s0 + 16 * u + g + 8 * i;
+                    for (int i = 0; i < 2 * C; ++i)
+                        s[u][i / C * 2 + i % C] *= mul[i % C];
+                if (p.cap > 0.f)
+                    cap_scores<SUB, C>(s, p.cap);
+                if (p.slopes) {
 #pragma unroll
-                        for (int c = 0; c < C; ++c) {
-                            float &y = s[u][2 * i + c];
-                            y *= mul[c];
-                            if (p.cap > 0.f)
-                                y = tanhf(y) * p.cap;
-                            if (p.slopes)
-                                y = fmaf(slope[c], (float)(j - L), y);
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float far = (float)(s0 + 16 * u + g + 8 * i - L);
+#pragma unroll
+                            for (int c = 0; c < C; ++c)
+                                s[u][2 * i + c] = fmaf(slope[c], far, s[u][2 * i + c]);
                         }
-                        if (p.xs && ((ok >> (2 * u + i)) & 1u) && C * t4 < p.gp) {
-                            float *to = p.xs + (((unsigned long long)seg->c.b * p.Hkv + seg->c.kvh) * p.xs_cap + j) * p.gp + C * t4;
-                            if constexpr (FEW)
-                                *to = s[u][2 * i];
-                            else
-                                *reinterpret_cast<float2 *>(to) = make_float2(s[u][2 * i], s[u][2 * i + 1]);
-                        }
-                    }
+                }
+                if (p.xs && C * t4 < p.gp) {
+                    float *to = p.xs + (((unsigned long long)seg->c.b * p.Hkv + seg->c.kvh) * p.xs_cap + s0 + g) * p.gp + C * t4;
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if ((ok >> (2 * u + i)) & 1u)
+                                store_scores<C>(to + (16 * u + 8 * i) * p.gp, s[u][2 * i], s[u][2 * i + 1], keep);
+                }
             }
             // x = base-2 score - reference, of slots u, i and rows c
             float x[SUB][2 * C], top = -INFINITY;
@@ -805,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(c
 #pragma unroll
                         for (int c = 0; c < C; ++c) {
                             float &y = x[u][C * i + c];
-                            y = fmaf(s[u][2 * i + c], fin[c], -m[c]);
+                            y = MORE ? s[u][2 * i + c] - m[c] : fmaf(s[u][2 * i + c], mul[c], -m[c]);
                             y = (ok >> (2 * u + i)) & 1u ? y : -INFINITY;
                         }
             };
@@ -836,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(c
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             if ((ok >> (2 * u + i)) & 1u)
-                                most = fmaxf(most, s[u][2 * i + c] * fin[c]);
+                                most = fmaxf(most, MORE ? s[u][2 * i + c] : s[u][2 * i + c] * mul[c]);
 #pragma unroll
                     for (int q = 4; q < 32; q <<= 1)
                         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, q));
@@ -884,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(c
                     for (int i = 0; i < 2 * C; ++i)
                         x[u][i] *= vs[u][i / C] * vref;
             }
-            weigh<KIND, D, FEW>(st, lane, x, o);
+            weigh<KIND, D, FEW>(st, lane, x, o, over);
         }
 
         // the end of the segment
@@ -936,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, Form<KIND, D>::CTAS) scored_kernel(c
         finish_segment<kWarps, kRows, D, D, false, true>(
             p, cur, walk, first_t, !good || any_bad, sm_m, sm_l, sm_o, &sm_flag, sm_merge, tid, kThreads,
             [] { __syncthreads(); }, arrived, [&](int row, float M, float den) {
-                if (p.row_end)             // a NaN denominator: a bad row
+                if (MORE && p.row_end)     // a NaN denominator: a bad row
                     p.row_end[(long long)cur.b * p.Hq + cur.kvh * p.G + row] = make_float2(M, 1.f / den);
             });
         if (end)
@@ -950,7 +1043,7 @@ constexpr int dyn_bytes()
     return kWarps * stages<KIND, D, QF32, FEW>() * (int)sizeof(Stage<KIND, D>) + kSegs * query_bytes<D, QF32, FEW>();
 }
 
-template <int KIND, int D, bool QF32, bool PAGED, bool FEW>
+template <int KIND, int D, bool QF32, bool PAGED, bool FEW, bool MORE>
 cudaError_t launch_one(const ScoredParams *p, cudaStream_t st, int *per_sm)
 {
     // the ring's size is set once a device
@@ -962,13 +1055,13 @@ cudaError_t launch_one(const ScoredParams *p, cudaStream_t st, int *per_sm)
         return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(scored_kernel<KIND, D, QF32, PAGED, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(scored_kernel<KIND, D, QF32, PAGED, FEW, MORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess)
             return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     if (!p)
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, scored_kernel<KIND, D, QF32, PAGED, FEW>, kThreads, bytes);
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, scored_kernel<KIND, D, QF32, PAGED, FEW, MORE>, kThreads, bytes);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p->grid);
     cfg.blockDim = dim3(kThreads);
@@ -979,15 +1072,17 @@ cudaError_t launch_one(const ScoredParams *p, cudaStream_t st, int *per_sm)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, scored_kernel<KIND, D, QF32, PAGED, FEW>, *p);
+    return cudaLaunchKernelEx(&cfg, scored_kernel<KIND, D, QF32, PAGED, FEW, MORE>, *p);
 }
 
-template <int KIND, int D, bool FEW>
+template <int KIND, int D, bool FEW, bool MORE>
 cudaError_t launch_d(bool q_bf16, bool paged, const ScoredParams *p, cudaStream_t st, int *per_sm)
 {
     if (q_bf16)
-        return paged ? launch_one<KIND, D, false, true, FEW>(p, st, per_sm) : launch_one<KIND, D, false, false, FEW>(p, st, per_sm);
-    return paged ? launch_one<KIND, D, true, true, FEW>(p, st, per_sm) : launch_one<KIND, D, true, false, FEW>(p, st, per_sm);
+        return paged ? launch_one<KIND, D, false, true, FEW, MORE>(p, st, per_sm)
+                     : launch_one<KIND, D, false, false, FEW, MORE>(p, st, per_sm);
+    return paged ? launch_one<KIND, D, true, true, FEW, MORE>(p, st, per_sm)
+                 : launch_one<KIND, D, true, false, FEW, MORE>(p, st, per_sm);
 }
 
 }  // namespace scored
