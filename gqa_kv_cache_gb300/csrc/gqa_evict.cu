@@ -4,11 +4,11 @@
 //
 // evict_select_kernel, a CTA a (row, head): the counts as integers in order
 // (sign folded, -0 as 0), the first kCached of them kept in shared memory; the
-// smallest kept count by three histograms of 11, 11 and 10 bits, each over the
-// slots that agree in the bits before; then one pass in slot order that gives
-// every kept slot its place (ballots, a scan of the warps' totals). Bound by
-// the latency of these passes; a count is read from memory once where the row
-// fits. The counts move in the same kernel.
+// smallest kept count by histograms of its first 11 bits, then of the next 11
+// and 10 over the few that share the first (a list; all slots again where many
+// do); then every warp counts and places the kept slots of its run. Bound by
+// the instructions of these sweeps; a count is read from memory once where the
+// row fits. The counts move in the same kernel.
 //
 // Kept vectors are copied elsewhere by evict_gather_kernel, every 16 bytes on
 // their own, or within the cache by evict_compact_kernel. In place, kept slot i
@@ -26,10 +26,11 @@
 namespace gqa {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kCached = 16384;     // counts kept in shared memory (64 KB: two CTAs an SM)
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kCached = 15360;     // counts kept in shared memory (60 KB: three CTAs an SM)
 constexpr int kBins = 2048;
-constexpr int kEach = 4;           // slots a thread per step of the last pass
+constexpr int kList = 1024;        // counts that share their first digit with the smallest kept one
+constexpr int kEach = 4;           // counts a thread loads at once
 
 __device__ __forceinline__ uint32_t order_of(float w)
 {
@@ -40,24 +41,58 @@ __device__ __forceinline__ uint32_t order_of(float w)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Index of slot j's vector of the unit (a paged block is known to be usable).
-__device__ __forceinline__ long long vector_at(const EvictParams &p, int b, int h, int j)
-{
-    if (p.paged) {
-        const int blk = __ldg(p.block_table + (long long)b * p.max_blocks + j / p.block_size);
-        return ((long long)blk * p.Hkv + h) * p.block_size + j % p.block_size;
+// Where the vectors of a (row, head) lie (its blocks are known to be usable).
+struct Line {
+    const int32_t *table;
+    long long first;   // dense: vector of slot 0
+    int Hkv, h, block_size, shift;
+    __device__ __forceinline__ Line(const EvictParams &p, int b, int head)
+    {
+        table = p.paged ? p.block_table + (long long)b * p.max_blocks : nullptr;
+        Hkv = p.Hkv;
+        h = head;
+        block_size = p.block_size;
+        shift = p.block_shift;
+        first = 0;
+        if (!p.paged)
+            first = ((long long)(p.slot_ids ? __ldg(p.slot_ids + b) : b) * Hkv + h) * p.Smax;
     }
-    const long long r = p.slot_ids ? __ldg(p.slot_ids + b) : b;
-    return (r * p.Hkv + h) * p.Smax + j;
-}
+    __device__ __forceinline__ long long at(int j) const
+    {
+        if (!table)
+            return first + j;
+        if (shift >= 0)
+            return (((long long)__ldg(table + (j >> shift)) * Hkv + h) << shift) + (j & ((1 << shift) - 1));
+        return ((long long)__ldg(table + j / block_size) * Hkv + h) * block_size + j % block_size;
+    }
+    // N of them: the blocks are looked up side by side, ahead of their use
+    template <int N>
+    __device__ __forceinline__ void look_up(const int (&j)[N], int (&blk)[N]) const
+    {
+        if (!table)
+            return;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            blk[e] = __ldg(table + (shift >= 0 ? j[e] >> shift : j[e] / block_size));
+    }
+    template <int N>
+    __device__ __forceinline__ void place(const int (&j)[N], const int (&blk)[N], long long (&to)[N]) const
+    {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            to[e] = !table       ? first + j[e]
+                    : shift >= 0 ? (((long long)blk[e] * Hkv + h) << shift) + (j[e] & ((1 << shift) - 1))
+                                 : ((long long)blk[e] * Hkv + h) * block_size + j[e] % block_size;
+    }
+};
 
 // The digit of the k-th largest among the counted ones: hist[] is summed from
-// the top. Every thread of the CTA calls it; returns the digit, and k less the
-// number above it.
-__device__ __forceinline__ int find_digit(const int *hist, int bins, int &k, int *scan, int *found)
+// the top. Every thread of the CTA calls it; returns the digit, k less the
+// number above it, and the number that share it.
+__device__ __forceinline__ int find_digit(const int *hist, int bins, int &k, int &equal, int *scan, int *found)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = bins / kThreads;   // 1 or 2 bins a thread, from the top
+    const int per = bins / kThreads;   // bins a thread, from the top
     int mine = 0;
     for (int i = 0; i < per; ++i)
         mine += hist[bins - 1 - (tid * per + i)];
@@ -72,14 +107,15 @@ __device__ __forceinline__ int find_digit(const int *hist, int bins, int &k, int
         scan[warp] = incl;
     __syncthreads();
     if (warp == 0) {
-        int v = scan[lane];
+        int v = lane < kWarps ? scan[lane] : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
+        for (int o = 1; o < kWarps; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, v, o);
             if (lane >= o)
                 v += y;
         }
-        scan[lane] = v;
+        if (lane < kWarps)
+            scan[lane] = v;
     }
     __syncthreads();
     int above = incl - mine + (warp ? scan[warp - 1] : 0);
@@ -89,6 +125,7 @@ __device__ __forceinline__ int find_digit(const int *hist, int bins, int &k, int
             if (above + c >= k) {
                 found[0] = bin;
                 found[1] = k - above;
+                found[2] = c;
                 break;
             }
             above += c;
@@ -96,15 +133,73 @@ __device__ __forceinline__ int find_digit(const int *hist, int bins, int &k, int
     }
     __syncthreads();
     k = found[1];
-    return found[0];
+    equal = found[2];
+    const int digit = found[0];
+    __syncthreads();                           // before the next call's
+    return digit;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParams p)
+constexpr int kMove = 256;         // threads of the moving kernels
+constexpr int kPieces = 4;         // 16-byte pieces of K, and as many of V, a thread and step
+constexpr int kSteps = 4;          // steps a CTA of the gathering kernel
+
+// Pieces x0 .. end - 1 of a unit's kept vectors into the outputs, by THREADS
+// threads. The places of the next step's vectors (ids, then blocks) are looked up
+// while the vectors of this one are on their way.
+template <int THREADS>
+__device__ __forceinline__ void gather(const EvictParams &p, const Line &line, int unit, long long x0, long long end)
+{
+    const unsigned per = p.row_bytes / 16;     // pieces a vector
+    const int shift = (per & (per - 1)) == 0 ? __ffs(per) - 1 : -1;
+    const uint4 *ks = static_cast<const uint4 *>(p.k_cache), *vs = static_cast<const uint4 *>(p.v_cache);
+    uint4 *kd = static_cast<uint4 *>(p.k_out) + (long long)unit * p.out_slots * per;
+    uint4 *vd = static_cast<uint4 *>(p.v_out) + (long long)unit * p.out_slots * per;
+    const int32_t *ids = p.ids + (long long)unit * p.n_keep;
+    long long from[kPieces];
+    auto find = [&](long long x) {
+        int id[kPieces], blk[kPieces] = {};
+        unsigned c[kPieces];
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e) {
+            const unsigned y = (unsigned)(x + e * THREADS), i = shift >= 0 ? y >> shift : y / per;
+            c[e] = y - i * per;
+            id[e] = x + e * THREADS < end ? ids[i] : 0;
+        }
+        line.look_up(id, blk);
+        line.place(id, blk, from);
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e)
+            from[e] = from[e] * per + c[e];
+    };
+    x0 += threadIdx.x;
+    if (x0 >= end)
+        return;
+    find(x0);
+    for (long long x = x0; x < end; x += THREADS * kPieces) {
+        uint4 k[kPieces], v[kPieces];
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e)
+            if (x + e * THREADS < end) {
+                k[e] = __ldg(ks + from[e]);
+                v[e] = __ldg(vs + from[e]);
+            }
+        find(x + THREADS * kPieces);
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e)
+            if (x + e * THREADS < end) {
+                kd[x + e * THREADS] = k[e];
+                vd[x + e * THREADS] = v[e];
+            }
+    }
+}
+
+// MOVE: the CTA also moves its unit's vectors into the outputs.
+template <bool MOVE>
+__global__ void __launch_bounds__(kThreads, MOVE ? 2 : 3) evict_select_kernel(const EvictParams p)
 {
     extern __shared__ uint32_t keys[];         // [min(capacity, kCached)]
-    __shared__ int hist[kBins], scan[kWarps], found[2], bad;
-    __shared__ int totals[kEach * kWarps];     // kept slots, then their places
-    __shared__ int ties[kEach * kWarps];
+    __shared__ int hist[kBins], scan[kWarps], tied[kWarps], found[3], bad, listed;
+    __shared__ uint32_t list[kList];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
     // the next kernel may be set up meanwhile (it waits for this one's end)
@@ -128,6 +223,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
         }
     __syncthreads();
     bits = bad;
+    const Line line(p, bits ? 0 : b, h);
     int32_t *ids = p.ids + (long long)blockIdx.x * p.n_keep;
     const int n = bits ? 0 : min(L, p.n_keep);
     if (tid == 0 && h == 0) {
@@ -143,106 +239,147 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
             ids[i] = i < n ? i : -1;
         if (to && !bits)
             for (int i = tid; i < p.out_slots; i += kThreads)
-                to[i] = i < n ? p.weights[vector_at(p, b, h, i)] : 0.f;
+                to[i] = i < n ? p.weights[line.at(i)] : 0.f;
+        if constexpr (MOVE) {
+            __syncthreads();                   // the ids are there
+            gather<kThreads>(p, line, blockIdx.x, 0, (long long)n * (p.row_bytes / 16));
+        }
         return;
     }
     const int lo = p.n_first, hi = L - p.n_last;       // the slots that compete
     const int held = min(L, p.cached);
-    for (int j = tid; j < held; j += kThreads)
-        keys[j] = order_of(p.weights[vector_at(p, b, h, j)]);
-    auto key = [&](int j) { return j < held ? keys[j] : order_of(p.weights[vector_at(p, b, h, j)]); };
-
-    // the smallest kept count `least`, and how many that equal it are kept
-    int k = p.n_keep - p.n_first - p.n_last;
-    uint32_t least = 0xffffffffu, mask = 0;
-    if (k > 0) {
-        least = 0;
+    int k = p.n_keep - p.n_first - p.n_last;           // how many of them are kept
+    for (int i = tid; i < kBins; i += kThreads)
+        hist[i] = 0;
+    if (tid == 0)
+        listed = 0;
+    __syncthreads();
+    // the counts, and a histogram of their first 11 bits
+    {
+        int j[kEach], blk[kEach] = {};
+        auto look = [&](int j0) {
 #pragma unroll
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-            for (int i = tid; i < bins; i += kThreads)
-                hist[i] = 0;
-            __syncthreads();                   // (also: the keys are there)
-            // a thread adds up the slots in a row of one digit (many slots may never have been attended)
-            int bin = -1, count = 0;
-            for (int j = lo + tid; j < hi; j += kThreads) {
-                const uint32_t u = key(j);
-                if ((u & mask) == least) {
-                    const int d = (u >> shift) & (bins - 1);
-                    if (d != bin && count) {
-                        atomicAdd(&hist[bin], count);
-                        count = 0;
-                    }
-                    bin = d;
-                    ++count;
-                }
-            }
-            if (count)
-                atomicAdd(&hist[bin], count);
-            __syncthreads();
-            const int digit = find_digit(hist, bins, k, scan, found);
-            least |= (uint32_t)digit << shift;
-            mask |= (uint32_t)(bins - 1) << shift;
-            __syncthreads();
-        }
-    } else {
-        __syncthreads();
-    }
-    // k: kept slots among those that equal `least` (0: none competes)
-    int before = 0, same = 0;                  // kept slots (but ties), ties so far
-    for (int j0 = 0; j0 < L; j0 += kThreads * kEach) {
-        unsigned more[kEach], tie[kEach];
+            for (int e = 0; e < kEach; ++e)
+                j[e] = min(j0 + e * kThreads, L - 1);
+            line.look_up(j, blk);
+        };
+        look(tid);
+        for (int j0 = tid; j0 < L; j0 += kThreads * kEach) {
+            long long at[kEach];
+            float w[kEach];
+            line.place(j, blk, at);
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const int j = j0 + e * kThreads + tid;
-            const bool in = j >= lo && j < hi;
-            const uint32_t u = in ? key(j) : 0u;
-            more[e] = __ballot_sync(0xffffffffu, j < L && (!in || (k > 0 && u > least)));
-            tie[e] = __ballot_sync(0xffffffffu, in && k > 0 && u == least);
-            if (lane == 0) {
-                totals[e * kWarps + warp] = __popc(more[e]);
-                ties[e * kWarps + warp] = __popc(tie[e]);
-            }
-        }
-        __syncthreads();
-        if (warp < 2) {                        // warp 0 scans the totals, warp 1 the ties
-            int *a = warp ? ties : totals;
-            int carry = 0;
+            for (int e = 0; e < kEach; ++e)
+                w[e] = p.weights[at[e]];
+            look(j0 + kThreads * kEach);
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
-                const int x = a[e * kWarps + lane];
-                int v = x;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, v, o);
-                    if (lane >= o)
-                        v += y;
-                }
-                a[e * kWarps + lane] = carry + v - x;
-                carry += __shfl_sync(0xffffffffu, v, 31);
+                const int x = j0 + e * kThreads;
+                const uint32_t u = order_of(w[e]);
+                if (x < held)
+                    keys[x] = u;
+                if (x >= lo && x < hi)
+                    atomicAdd(&hist[u >> 21], 1);
             }
-            if (lane == 0)
-                found[warp] = carry;
         }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const unsigned below = (1u << lane) - 1u;
-            const int m = before + totals[e * kWarps + warp] + __popc(more[e] & below);
-            const int s = same + ties[e * kWarps + warp] + __popc(tie[e] & below);
-            const bool is_tie = tie[e] >> lane & 1u;
-            if ((more[e] >> lane & 1u) || (is_tie && s < k))
-                ids[m + min(s, k)] = j0 + e * kThreads + tid;
-        }
-        before += found[0];
-        same += found[1];
-        __syncthreads();
     }
+    __syncthreads();
+    auto key = [&](int j) { return j < held ? keys[j] : order_of(p.weights[line.at(j)]); };
+
+    // the smallest kept count `least`, how many equal it (`equal`), and how many of those are kept (k)
+    uint32_t least = 0xffffffffu;
+    int equal = 0;
+    if (k > 0) {
+        least = (uint32_t)find_digit(hist, kBins, k, equal, scan, found) << 21;
+        // the others' digits are found among the counts that share the first: a list of them where it holds them
+        const bool few = equal <= kList;
+        if (few) {
+            for (int j = lo + tid; j < hi; j += kThreads) {
+                const uint32_t u = key(j);
+                if (u >> 21 == least >> 21)
+                    list[atomicAdd(&listed, 1)] = u;
+            }
+        }
+        uint32_t mask = 0xffe00000u;
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+            const int shift = pass == 0 ? 10 : 0, bins = pass == 0 ? 2048 : 1024;
+            for (int i = tid; i < bins; i += kThreads)
+                hist[i] = 0;
+            __syncthreads();                   // (also: the list is there)
+            const int n0 = few ? 0 : lo, n1 = few ? listed : hi;
+            for (int j = n0 + tid; j < n1; j += kThreads) {
+                const uint32_t u = few ? list[j] : key(j);
+                if ((u & mask) == least)
+                    atomicAdd(&hist[(u >> shift) & (bins - 1)], 1);
+            }
+            __syncthreads();
+            least |= (uint32_t)find_digit(hist, bins, k, equal, scan, found) << shift;
+            mask |= (uint32_t)(bins - 1) << shift;
+        }
+    }
+    // A warp takes a run of slots: it counts its kept ones, the warps' counts are
+    // added up, then every kept slot has its place. Of those that equal `least`
+    // the first k are kept, all of them where there are no more.
+    const bool all = equal == k;
+    const int share = (L + 32 * kWarps - 1) / (32 * kWarps) * 32, j0 = warp * share, j1 = min(L, j0 + share);
+    auto look = [&](int j, unsigned &more, unsigned &tie) {
+        const bool in = j >= lo && j < hi;
+        const uint32_t u = in ? key(j) : 0u;
+        more = __ballot_sync(0xffffffffu, j < j1 && (!in || (k > 0 && (u > least || (all && u == least)))));
+        tie = all ? 0u : __ballot_sync(0xffffffffu, j < j1 && in && u == least);
+    };
+    int mine = 0, ties = 0;
+    for (int j = j0 + lane; j - lane < j1; j += 32) {
+        unsigned more, tie;
+        look(j, more, tie);
+        mine += __popc(more);
+        ties += __popc(tie);
+    }
+    if (lane == 0) {
+        scan[warp] = mine;
+        tied[warp] = ties;
+    }
+    __syncthreads();
+    int before = 0, same = 0;                  // kept slots (but ties), ties of the warps before
+    for (int w = 0; w < warp; ++w) {
+        before += scan[w];
+        same += tied[w];
+    }
+    for (int j = j0 + lane; j - lane < j1; j += 32) {
+        unsigned more, tie;
+        look(j, more, tie);
+        const unsigned below = (1u << lane) - 1u;
+        const int m = before + __popc(more & below), s = same + __popc(tie & below);
+        if ((more >> lane & 1u) || ((tie >> lane & 1u) && s < k))
+            ids[m + min(s, k)] = j;
+        before += __popc(more);
+        same += __popc(tie);
+    }
+    __syncthreads();
     // the counts: kept ones in order, zeros behind them
     if (p.k_out) {
-        if (to)
-            for (int i = tid; i < p.out_slots; i += kThreads)
-                to[i] = i < n ? p.weights[vector_at(p, b, h, ids[i])] : 0.f;
+        for (int i0 = tid; to && i0 < p.out_slots; i0 += kThreads * kEach) {
+            int j[kEach], blk[kEach] = {};
+            long long at[kEach];
+            float w[kEach];
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                j[e] = ids[min(i0 + e * kThreads, n - 1)];
+            line.look_up(j, blk);
+            line.place(j, blk, at);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                w[e] = p.weights[at[e]];
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int i = i0 + e * kThreads;
+                if (i < p.out_slots)
+                    to[i] = i < n ? w[e] : 0.f;
+            }
+        }
+        if constexpr (MOVE)
+            gather<kThreads>(p, line, blockIdx.x, 0, (long long)n * (p.row_bytes / 16));
         return;
     }
     for (int i0 = 0; i0 < n; i0 += kThreads * kEach) {
@@ -250,53 +387,31 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int i = i0 + e * kThreads + tid;
-            w[e] = i < n ? p.weights[vector_at(p, b, h, ids[i])] : 0.f;
+            w[e] = i < n ? p.weights[line.at(ids[i])] : 0.f;
         }
         __syncthreads();                       // later counts come from behind these places
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int i = i0 + e * kThreads + tid;
             if (i < n)
-                p.weights[vector_at(p, b, h, i)] = w[e];
+                p.weights[line.at(i)] = w[e];
         }
         __syncthreads();
     }
     for (int j = n + tid; j < L; j += kThreads)
-        p.weights[vector_at(p, b, h, j)] = 0.f;
+        p.weights[line.at(j)] = 0.f;
 }
 
-constexpr int kMove = 256;         // threads of the moving kernels
-constexpr int kPieces = 8;         // 16-byte pieces a thread
-
-// Kept vectors into other buffers (B, Hkv, out_slots, row): blockIdx.x a share
-// of a unit's pieces of K (blockIdx.y = 0) or V.
-__global__ void __launch_bounds__(kMove) evict_gather_kernel(const EvictParams p)
+// Kept vectors into other buffers (B, Hkv, out_slots, row): a CTA takes a share
+// of a unit's pieces.
+__global__ void __launch_bounds__(kMove, 4) evict_gather_kernel(const EvictParams p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr long long share = kMove * kPieces * kSteps;
     const int unit = blockIdx.x / p.shares, b = unit / p.Hkv, h = unit % p.Hkv;
-    const int per = p.row_bytes / 16;          // pieces a vector
-    const long long x0 = (long long)(blockIdx.x % p.shares) * kMove * kPieces, n = (long long)p.new_lengths[b] * per;
-    if (x0 >= n)
-        return;
-    const uint4 *src = static_cast<const uint4 *>(blockIdx.y ? p.v_cache : p.k_cache);
-    uint4 *dst = static_cast<uint4 *>(blockIdx.y ? p.v_out : p.k_out) + (long long)unit * p.out_slots * per;
-    const int32_t *ids = p.ids + (long long)unit * p.n_keep;
-    uint4 w[kPieces];
-#pragma unroll
-    for (int e = 0; e < kPieces; ++e) {
-        const long long x = x0 + e * kMove + threadIdx.x;
-        if (x < n) {
-            const int i = (int)(x / per);
-            w[e] = __ldg(src + vector_at(p, b, h, __ldg(ids + i)) * per + (x - (long long)i * per));
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < kPieces; ++e) {
-        const long long x = x0 + e * kMove + threadIdx.x;
-        if (x < n)
-            dst[x] = w[e];
-    }
+    const long long x0 = blockIdx.x % p.shares * share;
+    gather<kMove>(p, Line(p, b, h), unit, x0, min((long long)p.new_lengths[b] * (p.row_bytes / 16), x0 + share));
 }
 
 constexpr int kDeep = 4;           // chunks on their way
@@ -314,6 +429,7 @@ __global__ void __launch_bounds__(kMove) evict_compact_kernel(const EvictParams 
     const int columns = p.row_bytes / SLICE;
     const int unit = blockIdx.x / columns, b = unit / p.Hkv, h = unit % p.Hkv;
     const int n = p.new_lengths[b], tid = threadIdx.x;
+    const Line line(p, b, h);
     const int32_t *ids = p.ids + (long long)unit * p.n_keep;
     char *cache = static_cast<char *>(blockIdx.y ? p.v_cache : p.k_cache) + (blockIdx.x % columns) * SLICE;
     // the kept slots that stay where they are come first: chunks of them alone need no copy
@@ -336,7 +452,7 @@ __global__ void __launch_bounds__(kMove) evict_compact_kernel(const EvictParams 
             for (int e = 0; e < N; ++e) {
                 const int x = e * kMove + tid, i = c * kChunk + x / PER;
                 if (i < n) {
-                    const char *src = cache + vector_at(p, b, h, __ldg(ids + i)) * p.row_bytes + x % PER * 16;
+                    const char *src = cache + line.at(__ldg(ids + i)) * p.row_bytes + x % PER * 16;
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                                      static_cast<uint32_t>(__cvta_generic_to_shared(&ring[c % kDeep][x]))),
                                  "l"(src)
@@ -356,7 +472,7 @@ __global__ void __launch_bounds__(kMove) evict_compact_kernel(const EvictParams 
         for (int e = 0; e < N; ++e) {
             const int x = e * kMove + tid, i = c * kChunk + x / PER;
             if (i < n)
-                *reinterpret_cast<uint4 *>(cache + vector_at(p, b, h, i) * p.row_bytes + x % PER * 16) = ring[c % kDeep][x];
+                *reinterpret_cast<uint4 *>(cache + line.at(i) * p.row_bytes + x % PER * 16) = ring[c % kDeep][x];
         }
         // a thread reads back what it copied itself, so the slot is free for its next copies
     }
@@ -378,11 +494,15 @@ cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t st, 
 
 }  // namespace
 
-cudaError_t evict_launch(EvictParams p, cudaStream_t st)
+cudaError_t evict_launch(EvictParams p, int sms, cudaStream_t st)
 {
     cudaLaunchAttribute attr[1];
     const long long cap = p.paged ? (long long)p.max_blocks * p.block_size : (long long)p.Smax;
     p.cached = (int)(cap < kCached ? cap : kCached);
+    p.block_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (p.paged && 1 << i == p.block_size)
+            p.block_shift = i;
     const int smem = p.cached * (int)sizeof(uint32_t);
     static std::atomic<uint64_t> ready;        // the size is set once a device
     int dev = 0;
@@ -391,21 +511,27 @@ cudaError_t evict_launch(EvictParams p, cudaStream_t st)
         return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kCached * (int)sizeof(uint32_t));
+        constexpr int most = kCached * (int)sizeof(uint32_t);
+        e = cudaFuncSetAttribute(evict_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess)
             return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     const unsigned units = (unsigned)(p.B * p.Hkv);
+    // enough units to fill the GPU: each moves its own vectors once its slots are
+    // chosen, beside others' choosing (XXX)
+    const bool move = p.k_out && (int)units >= sms;
     cudaLaunchConfig_t cfg = config(dim3(units), kThreads, smem, st, attr);
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
-    if (e != cudaSuccess)
+    e = move ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p) : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p);
+    if (e != cudaSuccess || move)
         return e;
     if (p.k_out) {
         const long long pieces = (long long)(p.n_keep < cap ? p.n_keep : cap) * (p.row_bytes / 16);
-        p.shares = (int)((pieces + kMove * kPieces - 1) / (kMove * kPieces));
-        cfg = config(dim3(units * (unsigned)p.shares, 2), kMove, 0, st, attr);
+        constexpr int share = kMove * kPieces * kSteps;
+        p.shares = (int)((pieces + share - 1) / share);
+        cfg = config(dim3(units * (unsigned)p.shares), kMove, 0, st, attr);
         return cudaLaunchKernelEx(&cfg, evict_gather_kernel, p);
     }
     // columns of 64 bytes, or of the largest power of two that divides the rows

@@ -138,9 +138,9 @@ struct EvictParams {
     int32_t *status;
     int B, Hkv, R, Smax, paged, num_blocks, block_size, max_blocks;
     int row_bytes, out_slots, n_keep, n_first, n_last;
-    int cached, shares;              // set by evict_launch
+    int cached, shares, block_shift; // set by evict_launch
 };
-cudaError_t evict_launch(EvictParams p, cudaStream_t st);
+cudaError_t evict_launch(EvictParams p, int sms, cudaStream_t st);
 
 // Content validation (gqa_validate.cu). *d_result must be zero on entry; the
 // kernel sets it to 1 on any violation. attend = 1 checks the read-only

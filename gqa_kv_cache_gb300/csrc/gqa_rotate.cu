@@ -12,9 +12,9 @@
 //
 // A CTA takes a few tokens (or a part of one's heads): the angles of a token,
 // shared by all heads of q and k, go through shared memory while the first
-// vectors are on their way. Bound by memory: every vector is read and written
-// once, 16 bytes a thread at a time; odd sizes and strides go element by
-// element.
+// vectors are on their way. A thread keeps its place in the heads from token to
+// token. Bound by memory: every vector is read and written once, 16 bytes a
+// thread at a time; odd sizes and strides go element by element.
 #include "gqa_common.cuh"
 #include "gqa_launch.h"
 
@@ -78,82 +78,84 @@ __device__ __forceinline__ bool position(const RotateParams &p, int t, int &pos)
     return true;
 }
 
-// A unit of work: N elements (HALF: of each half of the turned elements) of one
-// head of a token.
+// What a thread turns in every token it takes: N elements (HALF: of each half of
+// the turned elements) of one head.
+template <typename T>
+struct Place {
+    const T *src;      // in token 0
+    T *dst;
+    long long from, to;   // elements between tokens
+    int i;             // first pair, or -1: elements behind `dim`
+};
+
+template <typename T, int N, bool HALF>
+__device__ __forceinline__ Place<T> find(const RotateParams &p, int x)
+{
+    Place<T> w;
+    const int head = x / p.units, c = x - head * p.units;
+    const bool key = head >= p.Hq;
+    const int h = key ? head - p.Hq : head;
+    w.from = key ? p.k_token : p.q_token;
+    w.to = key ? p.ko_token : p.qo_token;
+    w.src = static_cast<const T *>(key ? p.k : p.q) + h * (key ? p.k_head : p.q_head);
+    w.dst = static_cast<T *>(key ? p.k_out : p.q_out) + h * (key ? p.ko_head : p.qo_head);
+    // units of turned elements: dim / (2 N) pairs of pieces; N = 1 (2 elements) else N / 2 pairs
+    const int turned = HALF || N == 1 ? p.dim / 2 / N : p.dim / N;
+    const int d = c >= turned ? p.dim + (c - turned) * N : HALF ? c * N : N == 1 ? 2 * c : c * N;
+    w.i = c >= turned ? -1 : HALF ? c * N : N == 1 ? c : c * (N / 2);
+    w.src += d;
+    w.dst += d;
+    return w;
+}
+
 template <typename T, int N, bool HALF>
 struct Unit {
-    const T *src;
-    T *dst;
-    int i;             // first pair, or -1: elements behind `dim`
     Vec<T, N> a, b;
 };
 
 template <typename T, int N, bool HALF>
-__device__ __forceinline__ void find(const RotateParams &p, int t, int x, Unit<T, N, HALF> &w)
+__device__ __forceinline__ void load(const RotateParams &p, const Place<T> &at, int t, Unit<T, N, HALF> &w)
 {
-    const int head = x / p.units, c = x - head * p.units;
-    const bool key = head >= p.Hq;
-    const int h = key ? head - p.Hq : head;
-    w.src = static_cast<const T *>(key ? p.k : p.q) + t * (key ? p.k_token : p.q_token) + h * (key ? p.k_head : p.q_head);
-    w.dst = static_cast<T *>(key ? p.k_out : p.q_out) + t * (key ? p.ko_token : p.qo_token) +
-            h * (key ? p.ko_head : p.qo_head);
-    // units of turned elements: dim / (2 N) pairs of pieces; N = 1 (2 elements) else N / 2 pairs
-    const int turned = HALF || N == 1 ? p.dim / 2 / N : p.dim / N;
-    if (c < turned) {
-        w.i = HALF ? c * N : N == 1 ? c : c * (N / 2);
-        const int d = HALF ? c * N : N == 1 ? 2 * c : c * N;
-        w.src += d;
-        w.dst += d;
-    } else {
-        w.i = -1;
-        const int d = p.dim + (c - turned) * N;
-        w.src += d;
-        w.dst += d;
-    }
+    const T *src = at.src + t * at.from;
+    w.a = *reinterpret_cast<const Vec<T, N> *>(src);
+    if ((HALF || N == 1) && at.i >= 0)
+        w.b = *reinterpret_cast<const Vec<T, N> *>(src + (HALF ? p.dim / 2 : 1));
 }
 
 template <typename T, int N, bool HALF>
-__device__ __forceinline__ void load(const RotateParams &p, Unit<T, N, HALF> &w)
+__device__ __forceinline__ void store(const RotateParams &p, const Place<T> &at, int t, Unit<T, N, HALF> &w, const float2 *cs,
+                                      bool known)
 {
-    w.a = *reinterpret_cast<const Vec<T, N> *>(w.src);
-    if (w.i >= 0 && (HALF || N == 1))
-        w.b = *reinterpret_cast<const Vec<T, N> *>(w.src + (HALF ? p.dim / 2 : 1));
-}
-
-template <typename T, int N, bool HALF>
-__device__ __forceinline__ void store(const RotateParams &p, Unit<T, N, HALF> &w, const float2 *cs, bool known)
-{
-    if (w.i < 0 || !known) {
-        *reinterpret_cast<Vec<T, N> *>(w.dst) = w.a;
-        if (w.i >= 0 && (HALF || N == 1))
-            *reinterpret_cast<Vec<T, N> *>(w.dst + (HALF ? p.dim / 2 : 1)) = w.b;
-        return;
-    }
-    if constexpr (HALF || N == 1) {
+    T *dst = at.dst + t * at.to;
+    if (at.i >= 0 && known) {
+        if constexpr (HALF || N == 1) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float2 e = cs[w.i + j];
-            const float x = wide(w.a.x[j]), y = wide(w.b.x[j]);
-            w.a.x[j] = narrow<T>(x * e.x - y * e.y);
-            w.b.x[j] = narrow<T>(x * e.y + y * e.x);
-        }
-        *reinterpret_cast<Vec<T, N> *>(w.dst) = w.a;
-        *reinterpret_cast<Vec<T, N> *>(w.dst + (HALF ? p.dim / 2 : 1)) = w.b;
-    } else {
+            for (int j = 0; j < N; ++j) {
+                const float2 e = cs[at.i + j];
+                const float x = wide(w.a.x[j]), y = wide(w.b.x[j]);
+                w.a.x[j] = narrow<T>(x * e.x - y * e.y);
+                w.b.x[j] = narrow<T>(x * e.y + y * e.x);
+            }
+        } else {
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-            const float2 e = cs[w.i + j];
-            const float x = wide(w.a.x[2 * j]), y = wide(w.a.x[2 * j + 1]);
-            w.a.x[2 * j] = narrow<T>(x * e.x - y * e.y);
-            w.a.x[2 * j + 1] = narrow<T>(x * e.y + y * e.x);
+            for (int j = 0; j < N / 2; ++j) {
+                const float2 e = cs[at.i + j];
+                const float x = wide(w.a.x[2 * j]), y = wide(w.a.x[2 * j + 1]);
+                w.a.x[2 * j] = narrow<T>(x * e.x - y * e.y);
+                w.a.x[2 * j + 1] = narrow<T>(x * e.y + y * e.x);
+            }
         }
-        *reinterpret_cast<Vec<T, N> *>(w.dst) = w.a;
     }
+    *reinterpret_cast<Vec<T, N> *>(dst) = w.a;
+    if ((HALF || N == 1) && at.i >= 0)
+        *reinterpret_cast<Vec<T, N> *>(dst + (HALF ? p.dim / 2 : 1)) = w.b;
 }
 
-// blockIdx.x: `tokens` tokens; blockIdx.y: a part of their units.
+
+// blockIdx.x: `tokens` tokens; blockIdx.y: a part of their units. A thread keeps
+// its place in the heads from token to token.
 template <typename T, int N, bool HALF>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p)
+__global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotateParams p)
 {
     extern __shared__ float2 cs[];             // [tokens][dim / 2]
     __shared__ int known[32];                  // whether the token has a position
@@ -161,16 +163,25 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p)
     const int t0 = blockIdx.x * p.tokens, n = min(p.tokens, p.T - t0);
     const int all = (p.Hq + p.Hkv) * p.units;  // units a token
     const int u0 = (int)((long long)all * blockIdx.y / gridDim.y), u1 = (int)((long long)all * (blockIdx.y + 1) / gridDim.y);
-    const int per = u1 - u0, total = per * n;
+    const int per = u1 - u0;
+    const int lanes = per >= kThreads ? 1 : kThreads / per;         // tokens at once
+    const int lane = per >= kThreads ? 0 : tid / per, c = per >= kThreads ? tid : tid % per;
     // the next kernel may be set up meanwhile (it waits for this one's end)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    Unit<T, N, HALF> w;
-    int x = tid, tok = 0;
-    if (x < total) {
-        tok = x / per;
-        find(p, t0 + tok, u0 + x - tok * per, w);
-        load(p, w);
+    constexpr int A = HALF ? 2 : 4;            // tokens of a thread on their way at once
+    Place<T> at, next;
+    Unit<T, N, HALF> w[A], v[A];
+    const bool mine = c < per && lane < lanes;
+    auto fetch = [&](const Place<T> &from, int t, Unit<T, N, HALF> (&to)[A]) {
+#pragma unroll
+        for (int a = 0; a < A; ++a)
+            if (t + a * lanes < n)
+                load(p, from, t0 + t + a * lanes, to[a]);
+    };
+    if (mine) {
+        next = at = find<T, N, HALF>(p, u0 + c);
+        fetch(at, lane, w);                    // before the angles
     }
     for (int i = tid; i < n * pairs; i += kThreads) {
         const int t = i / pairs, j = i - t * pairs;
@@ -187,19 +198,33 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p)
                 atomicOr(p.status, kBadQLen);
         }
     __syncthreads();
-    while (x < total) {
-        const int y = x + kThreads;
-        Unit<T, N, HALF> next;
-        int ntok = 0;
-        if (y < total) {                       // the next unit is on its way while this one is turned
-            ntok = y / per;
-            find(p, t0 + ntok, u0 + y - ntok * per, next);
-            load(p, next);
+    if (!mine)
+        return;
+    int x = c, t = lane;
+    while (true) {
+        // the next tokens (or the next place's first) are on their way while these are turned
+        int s = t + A * lanes;
+        if (s >= n) {
+            s = lane;
+            x += kThreads;                     // (per < kThreads: there is none)
+            if (x < per)
+                next = find<T, N, HALF>(p, u0 + x);
         }
-        store(p, w, cs + tok * pairs, known[tok]);
-        x = y;
-        tok = ntok;
-        w = next;
+        if (x < per)
+            fetch(next, s, v);
+#pragma unroll
+        for (int a = 0; a < A; ++a) {
+            const int k = t + a * lanes;
+            if (k < n)
+                store(p, at, t0 + k, w[a], cs + k * pairs, known[k]);
+        }
+        if (x >= per)
+            break;
+        at = next;
+        t = s;
+#pragma unroll
+        for (int a = 0; a < A; ++a)
+            w[a] = v[a];
     }
 }
 
@@ -209,10 +234,11 @@ cudaError_t launch(RotateParams &p, int sms, cudaStream_t st)
     const int turned = HALF || N == 1 ? p.dim / 2 / N : p.dim / N;
     p.units = turned + (p.rest ? (p.D - p.dim) / N : 0);
     const long long all = (long long)(p.Hq + p.Hkv) * p.units;
-    // tokens a CTA: as many as leave every SM eight CTAs, at most 8 (65521
-    // tokens); parts of a token's heads where there are few tokens
-    const long long share = p.T / ((long long)sms * 8);
-    p.tokens = share < 1 ? 1 : share > 8 ? 8 : (int)share;
+    // tokens a CTA: as many as leave every SM eight CTAs, at most 16 (65521 tokens
+    // of 56 heads: 8 304 us, 16 289, 32 302) and 32 KB of angles; parts of a
+    // token's heads where there are few tokens
+    const long long share = p.T / ((long long)sms * 8), most = p.dim <= 512 ? 16 : 8192 / p.dim;
+    p.tokens = share < 1 ? 1 : share > most ? (int)most : (int)share;
     const long long ctas = ((long long)p.T + p.tokens - 1) / p.tokens;
     long long parts = (all * p.tokens + kThreads - 1) / kThreads, room = (long long)sms * 4 / ctas;
     parts = parts > room ? room : parts;

@@ -1,5 +1,6 @@
 // C ABI of rotary positions and eviction (include/gqa_decode.h): host-side
 // argument checks and launches.
+#include <atomic>
 #include <climits>
 
 #include "gqa_decode.h"
@@ -8,6 +9,25 @@
 using namespace gqa;
 
 namespace {
+
+// Streaming multiprocessors of the current device (0: a CUDA error).
+int current_sms()
+{
+    constexpr int kDevices = 64;
+    static std::atomic<int> cache[kDevices];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0)
+        return 0;
+    if (dev < kDevices)
+        n = cache[dev].load(std::memory_order_relaxed);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return 0;
+        if (dev < kDevices)
+            cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) == 0; }
 
@@ -32,7 +52,8 @@ gqa_status run_evict(EvictParams p, int D, gqa_dtype kv, void *stream)
     const long long cap = p.paged ? (long long)p.max_blocks * p.block_size : (long long)p.Smax;
     const long long moved = p.n_keep < cap ? p.n_keep : cap;
     if (row % 16 || row > (1 << 20) || (long long)p.B * p.Hkv > (1 << 24) ||
-        (double)p.B * p.Hkv * ((double)moved * row / (1 << 15) + row / 16.0 + 1.0) > INT_MAX)
+        (double)p.B * p.Hkv * ((double)moved * row / (1 << 15) + row / 16.0 + 1.0) > INT_MAX ||
+        (double)moved * row / 16 > INT_MAX)
         return GQA_ERR_UNSUPPORTED;
     if (p.B == 0)
         return GQA_OK;
@@ -43,7 +64,10 @@ gqa_status run_evict(EvictParams p, int D, gqa_dtype kv, void *stream)
         !aligned(p.weights, 4) || !aligned(p.weights_out, 4))
         return GQA_ERR_INVALID_ARGUMENT;
     p.row_bytes = (int)row;
-    return evict_launch(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+    const int sms = current_sms();
+    if (!sms)
+        return GQA_ERR_CUDA;
+    return evict_launch(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 }  // namespace
@@ -69,9 +93,8 @@ gqa_status gqa_rotate(const void *q, const void *k, void *q_out, void *k_out, gq
     const unsigned es = dt == GQA_DTYPE_F32 ? 4 : 2;
     if (!aligned(q, es) || !aligned(k, es) || !aligned(q_out, es) || !aligned(k_out, es) || !aligned(freqs, 8))
         return GQA_ERR_INVALID_ARGUMENT;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    const int sms = current_sms();
+    if (!sms)
         return GQA_ERR_CUDA;
     RotateParams p = {};
     p.q = q;
