@@ -200,6 +200,23 @@ def _workspace(device, nbytes, stream=None):
     return buf
 
 
+_scratch_cache: dict = {}
+
+
+def _scratch(device, nbytes, stream=None):
+    """Scratch whose contents are free before and after a call: kept for the
+    device and stream up to 16 MB, else (and in a capture) the call's own."""
+    if nbytes <= 1 << 24 and stream is None and not torch.cuda.is_current_stream_capturing():
+        handle = _stream(None, device)
+        key = (device, handle) if handle else device
+        buf = _scratch_cache.get(key)
+        if buf is None or buf.numel() < nbytes:
+            buf = _scratch_cache[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        return buf
+    with torch.cuda.stream(stream) if stream is not None else _HERE:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+
+
 _need_cache: dict = {}
 
 
@@ -404,25 +421,23 @@ def _step_scored(q, k_new, v_new, k, v, lengths, slot_ids, table, out, status, k
         o.head_slopes = head_slopes.data_ptr()
     lib = _lib.load()
     with _on(device):
-        scratch = None
         if weights is not None:
             if weights.dtype != torch.float32 or weights.shape != k.shape[:3]:
                 raise TypeError("weights must be a contiguous float32 tensor of the cache's shape without D")
             _plain(dev, weights)
             o.weights = weights.data_ptr()
             need = lib.gqa_weights_scratch_bytes(B, Hq, Hkv, table.shape[1] * n2 if paged else n2)
-            with torch.cuda.stream(stream) if stream is not None else _HERE:
-                scratch = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+            scratch = _scratch(device, need, stream)
             o.weights_scratch = scratch.data_ptr()
             o.weights_scratch_bytes = need
         need = _need(lib, B, Hq, Hkv, D, dt, kernel, grid_ctas, o, device,
                      1 + bool(score_cap or head_slopes is not None or weights is not None))
         ws = _workspace(device, need, stream) if workspace is None else workspace
-        if out is None:
-            with torch.cuda.stream(stream) if stream is not None else _HERE:
-                out = torch.empty(q.shape, dtype=torch.float32, device=device)
         at, size, st, opt = ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(status), ctypes.byref(o)
         s = _stream(stream, device)
+        if out is None:   # last: see _step_e2m1
+            with torch.cuda.stream(stream) if stream is not None else _HERE:
+                out = torch.empty_like(q, dtype=torch.float32)
         if not paged:
             if k_new is None:
                 what, code = "gqa_attend", lib.gqa_attend(
@@ -1133,41 +1148,21 @@ def rotate(q, k, rotary, positions=None, *, lengths=None, cu_q=None, q_out=None,
     lengths[b] + t - cu_q[b] (tokens of no row are not turned). The tensors may be
     views whose last axis is contiguous (parts of one projection); ``q_out`` and
     ``k_out`` may be ``q`` and ``k`` (in place). Returns (q_out, k_out)."""
-    given = [t for t in (q, k) if t is not None]
-    if not given:
+    one = q if q is not None else k
+    if one is None:
         raise ValueError("q or k must be given")
-    dt, T, D, device = given[0].dtype, given[0].shape[0], given[0].shape[-1], given[0].device
-    dev = given[0].get_device()
+    dt, dev = one.dtype, one.get_device()
     if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
     if dt not in _DTYPES:
         raise TypeError("q and k must be float32 or bfloat16")
+    if one.dim() != 3:
+        raise ValueError("q and k must be (T, H, D) of one type on one device")
+    T, _, D = one.shape
     if rotary.dim > D:
         raise ValueError("the rotary dim is larger than the heads")
     if rotary.freqs.get_device() != dev:
         raise ValueError("rotary was made for another device")
-    strides = (ctypes.c_int64 * 8)()
-    heads, outs = [], []
-    for i, (name, t, out) in enumerate((("q", q, q_out), ("k", k, k_out))):
-        if t is None:
-            if out is not None:
-                raise ValueError(f"{name}_out without {name}")
-            heads.append(0)
-            outs.append(None)
-            continue
-        if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or t.dtype != dt or t.get_device() != dev:
-            raise ValueError("q and k must be (T, H, D) of one type on one device")
-        if out is None:
-            with torch.cuda.stream(stream) if stream is not None else _HERE:
-                out = torch.empty(t.shape, dtype=dt, device=device)
-        elif out.shape != t.shape or out.dtype != dt or out.get_device() != dev:
-            raise ValueError(f"{name}_out must be like {name}")
-        if (t.stride(2) != 1 or out.stride(2) != 1) and D > 1 and t.numel():
-            raise ValueError(f"the last axis of {name} and {name}_out must be contiguous")
-        strides[2 * i], strides[2 * i + 1] = t.stride(0), t.stride(1)
-        strides[4 + 2 * i], strides[5 + 2 * i] = out.stride(0), out.stride(1)
-        heads.append(t.shape[1])
-        outs.append(out)
     B = 0
     if positions is not None:
         if lengths is not None or cu_q is not None:
@@ -1179,16 +1174,49 @@ def rotate(q, k, rotary, positions=None, *, lengths=None, cu_q=None, q_out=None,
         B = lengths.shape[0]
         _int32("lengths", lengths, B, dev)
         _int32("cu_q", cu_q, B + 1, dev)
+    device = one.device
     if status is not None:
         _status_checks(status, device)
+    Hq, q_at, q_by = _turned("q", q, q_out, T, D, dt, dev)
+    Hkv, k_at, k_by = _turned("k", k, k_out, T, D, dt, dev)
     lib = _lib.load()
     with _on(device):
-        rc = lib.gqa_rotate(_ptr(q), _ptr(k), _ptr(outs[0]), _ptr(outs[1]), _DTYPES[dt], strides, _ptr(positions),
-                            _ptr(lengths), _ptr(cu_q), rotary.freqs.data_ptr(), rotary.factor,
-                            int(rotary.layout == "interleaved"), B, T, heads[0], heads[1], D, rotary.dim, _ptr(status),
+        with torch.cuda.stream(stream) if stream is not None else _HERE:
+            if q_out is None and q is not None:
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            if k_out is None and k is not None:
+                k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        qo_by, ko_by = _NONE if q is None else q_out.stride(), _NONE if k is None else k_out.stride()
+        strides = (ctypes.c_int64 * 8)(q_by[0], q_by[1], k_by[0], k_by[1], qo_by[0], qo_by[1], ko_by[0], ko_by[1])
+        rc = lib.gqa_rotate(q_at, k_at, None if q is None else q_out.data_ptr(), None if k is None else k_out.data_ptr(),
+                            _DTYPES[dt], strides, _ptr(positions), _ptr(lengths), _ptr(cu_q), rotary.freqs.data_ptr(),
+                            rotary.factor, rotary.layout == "interleaved", B, T, Hq, Hkv, D, rotary.dim, _ptr(status),
                             _stream(stream, device))
     _check(rc, "gqa_rotate")
-    return outs[0], outs[1]
+    return q_out, k_out
+
+
+_NONE = (0, 0, 1)
+
+
+def _turned(name, t, out, T, D, dt, dev):
+    """Checks of the queries or keys of :func:`rotate` and of an output that was
+    given; returns (heads, address, strides)."""
+    if t is None:
+        if out is not None:
+            raise ValueError(f"{name}_out without {name}")
+        return 0, None, _NONE
+    shape, by = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or t.dtype != dt or t.get_device() != dev:
+        raise ValueError("q and k must be (T, H, D) of one type on one device")
+    if by[2] != 1 and t.numel():
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    if out is not None:
+        if out.shape != shape or out.dtype != dt or out.get_device() != dev:
+            raise ValueError(f"{name}_out must be like {name}")
+        if out.stride(2) != 1 and t.numel():
+            raise ValueError(f"the last axis of {name}_out must be contiguous")
+    return shape[1], t.data_ptr(), by
 
 
 def _evict(k, v, block_table, weights, lengths, n_keep, slot_ids, n_first, n_last, k_out, v_out, weights_out, status,
@@ -1230,10 +1258,10 @@ def _evict(k, v, block_table, weights, lengths, n_keep, slot_ids, n_first, n_las
     device = k.device
     if status is not None:
         _status_checks(status, device)
+    lib = _lib.load()
     with torch.cuda.stream(stream) if stream is not None else _HERE:
         ids = torch.empty((B, Hkv, n_keep), dtype=torch.int32, device=device)
-        new = torch.empty((B,), dtype=torch.int32, device=device)
-    lib = _lib.load()
+        new = torch.empty_like(lengths)
     with _on(device):
         if block_table is None:
             what, rc = "gqa_evict", lib.gqa_evict(

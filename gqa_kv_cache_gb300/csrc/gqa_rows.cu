@@ -499,16 +499,29 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowsParams p)
 // which is 1/2), where max|x| / 127 at every growth would add half a step each
 // time. A run with a value that is not finite makes the scale NaN.
 //
-// A warp takes a (run, head) of K or of V: 16 elements a lane at a time, kept
-// in registers up to kKeep of them (a 16-slot block of D = 128) and read again
-// (from L1) behind that. Bound by memory: es D + D bytes a vector.
+// A team of 1, 2, 4 or 8 warps takes a (run, head) of K or of V: 16 elements a
+// lane at a time, up to kKeep of them kept in registers (a 16-slot block of D =
+// 128 a warp), those behind read again. It moves es D + D bytes a vector; what
+// bounds it is issue, about 180 instructions a group of 16 (65536 tokens of 8 x
+// 128, bfloat16, in prompts of 1 .. 2047: 16-slot blocks 78 us, 0.75 of the
+// measured copy rate, 64-slot blocks 96, with one warp an item 108; float32 112,
+// 0.88).
 
-constexpr int kKeep = 4;   // groups of 16 elements a lane keeps between the two passes
+// Groups of 16 elements that a lane keeps between the two passes (64 registers
+// of float32, 32 of bfloat16), and the CTAs an SM that leave it the registers
+// (65536 tokens, 16-slot blocks: bfloat16 2 CTAs 95 us, 3 78, 4 90; float32 2 112,
+// 3 157).
+constexpr int kKeep = 4;
+template <typename T>
+constexpr int append_ctas()
+{
+    return sizeof(T) == 2 ? 3 : 2;
+}
 
 struct Run {
     int tok, n;        // first token (of the CTA's) and tokens
     int slot;          // its slot
-    long long off;     // element offset of that slot's vector of head 0
+    long long off;     // element offset of that slot's vector of head 0 (its row, until that is known), or kSkip
     long long scale;   // index of the block's scale of head 0
 };
 
@@ -584,16 +597,17 @@ __device__ __forceinline__ uint32_t fewer4(uint32_t u, float f)
     return codes4(x[0], x[1], x[2], x[3]);
 }
 
-// One CTA: the runs that begin among its `chunk` tokens, to their ends. Shared
-// memory: the tokens' slots, then the runs.
+// One CTA: the runs that begin among its `chunk` tokens, to their ends. The
+// threads look at the rows (ONE: at the tokens), a row's thread notes the runs
+// that it begins here, then a thread a run finds its block.
 template <typename T, bool ONE>
-__global__ void __launch_bounds__(kThreads) append8_kernel(const RowsParams p)
+__global__ void __launch_bounds__(kThreads, append_ctas<T>()) append8_kernel(const RowsParams p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    Token *tok = reinterpret_cast<Token *>(smem);                         // [chunk]
-    Run *runs = reinterpret_cast<Run *>(smem + sizeof(Token) * p.chunk);   // [chunk]
+    Run *runs = reinterpret_cast<Run *>(smem);          // [chunk]
     __shared__ int n_runs;
-    const int tid = threadIdx.x, lane = tid & 31;
+    __shared__ float tops[2][kThreads / 32];
+    const int tid = threadIdx.x;
     const int t0 = blockIdx.x * p.chunk;
     const int n = min(p.chunk, p.T - t0);
     // the next kernel may be set up meanwhile (it waits for this one's end)
@@ -603,65 +617,122 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const RowsParams p)
         n_runs = 0;
     __syncthreads();
     const int sb = p.scale_block;
-    for (int i = tid; i < n; i += kThreads) {
-        const Token k = find_token<ONE>(p, t0 + i);
-        tok[i] = k;
-        // the first token of its block or of its row (the row's others are in
-        // order with it: a bad block's are all skipped)
-        if (k.off != kSkip) {
-            const int end = ONE ? t0 + i + 1 : __ldg(p.cu_q + k.b + 1);
-            if (k.slot % sb == 0 || ONE || t0 + i == __ldg(p.cu_q + k.b)) {
-                const int at = atomicAdd(&n_runs, 1);   // the order of the runs does not matter
-                runs[at] = Run{i, min(sb - k.slot % sb, end - (t0 + i)), k.slot, k.off, scale_index(p, k)};
-            }
+    const long long cap = p.paged ? (long long)p.max_blocks * p.block_size : (long long)p.Smax;
+    for (int b = ONE ? t0 + tid : tid; b < (ONE ? t0 + n : p.B); b += kThreads) {
+        const int a = ONE ? b : __ldg(p.cu_q + b), e = ONE ? b + 1 : __ldg(p.cu_q + b + 1);
+        if (a < 0 || e < a || e > p.T) {
+            rows_report(p, kBadQLen);
+            continue;
+        }
+        if (e <= t0 || a >= t0 + n || e == a)
+            continue;                                   // none of its tokens is here
+        const long long L = __ldg(p.lengths + b);
+        if (L < 0 || L + (e - a) > cap) {
+            rows_report(p, kBadLength);
+            continue;
+        }
+        int t = max(a, t0);
+        int slot = (int)L + (t - a);
+        if (t > a && slot % sb) {                       // that run began earlier
+            t += sb - slot % sb;
+            slot += sb - slot % sb;
+        }
+        while (t < min(e, t0 + n)) {
+            const int m = min(sb - slot % sb, e - t);
+            runs[atomicAdd(&n_runs, 1)] = Run{t - t0, m, slot, b, 0};   // the order does not matter
+            t += m;
+            slot += m;
         }
     }
-    if constexpr (!ONE)
-        check_rows(p);
+    __syncthreads();
+    for (int i = tid; i < n_runs; i += kThreads) {
+        const int b = (int)runs[i].off, slot = runs[i].slot;
+        long long off = kSkip, scale = 0;
+        if (p.paged) {
+            const int blk = __ldg(p.block_table + (long long)b * p.max_blocks + slot / sb);
+            if (blk < 0 || blk >= p.num_blocks) {
+                rows_report(p, kBadBlock);
+            } else {
+                scale = (long long)blk * p.Hkv;
+                off = (scale * sb + slot % sb) * p.D;
+            }
+        } else {
+            const int r = p.slot_ids ? __ldg(p.slot_ids + b) : b;
+            if (r < 0 || r >= p.R) {
+                rows_report(p, kBadSlotId);
+            } else {
+                off = ((long long)r * p.Hkv * p.Smax + slot) * p.D;
+                scale = (long long)r * p.Hkv * (p.Smax / sb) + slot / sb;
+            }
+        }
+        runs[i].off = off;
+        runs[i].scale = scale;
+    }
     __syncthreads();
     const int per = p.D / kGroup;                       // groups a vector
     const int shift = (per & (per - 1)) == 0 ? __ffs(per) - 1 : -1;
     const long long head = (long long)(p.paged ? p.block_size : p.Smax) * p.D;   // elements between heads
     const long long scale_head = p.paged ? 1 : p.Smax / sb;
-    const long long row = (long long)p.Hkv * p.D;
-    const int items = n_runs * p.Hkv * 2;               // neighbours: K and V of a head
-    for (int it = tid >> 5; it < items; it += kThreads / 32) {
-        const Run run = runs[it / (2 * p.Hkv)];
-        const int h = (it >> 1) % p.Hkv;
-        const bool val = it & 1;
-        const T *src = static_cast<const T *>(val ? p.v_new : p.k_new) + (long long)(t0 + run.tok) * row + (long long)h * p.D;
+    const int row = p.Hkv * p.D;                        // (at most 2^24)
+    const int step = 32 * p.team, team = tid / step, lane = tid % step, teams = kThreads / step;
+    const int heads = 2 * p.Hkv;                        // neighbours: K and V of a head
+    // a lane's groups lie `far` elements apart where a step is whole vectors
+    const bool even = shift >= 0 && step >= per;
+    const int first = even ? (lane >> shift) * row + (lane & (per - 1)) * kGroup : 0, far = even ? (step >> shift) * row : 0;
+    auto from = [&](const T *src, int i) {
+        if (even)
+            return src + first + (long long)i * far;
+        const int at = lane + step * i, m = at / per;
+        return src + (long long)m * row + (at - m * per) * kGroup;
+    };
+    int turn = 0, r = 0, hv = team;
+    while (hv >= heads && r < n_runs) {
+        hv -= heads;
+        ++r;
+    }
+    while (r < n_runs) {
+        const Run run = runs[r];
+        const int h = hv >> 1;
+        const bool val = hv & 1;
+        hv += teams;
+        while (hv >= heads) {
+            hv -= heads;
+            ++r;
+        }
+        if (run.off == kSkip)
+            continue;
+        const T *src = static_cast<const T *>(val ? p.v_new : p.k_new) + (long long)(t0 + run.tok) * row + h * p.D;
         int8_t *dst = static_cast<int8_t *>(val ? p.v_cache : p.k_cache) + run.off + h * head;
         float *scale = (val ? p.v_block_scale : p.k_block_scale) + run.scale + h * scale_head;
         const int before = run.slot % sb;               // earlier slots of the block
         const float was = before ? *scale : 0.f;
         const int groups = run.n * per;
-        auto place = [&](int i, int &m, int &d) {       // token and element of group i
-            m = shift >= 0 ? i >> shift : i / per;
-            d = (i - m * per) * kGroup;
-        };
+        const int mine = groups > lane ? (groups - lane + step - 1) / step : 0;   // this lane's
         Raw<T> kept[kKeep];
         float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            const int at = lane + 32 * i;
-            if (at < groups) {
-                int m, d;
-                place(at, m, d);
-                kept[i] = load_raw(src + m * row + d, p.wide);
-            }
-        }
+        for (int i = 0; i < kKeep; ++i)
+            if (i < mine)
+                kept[i] = load_raw(from(src, i), p.wide);
 #pragma unroll
         for (int i = 0; i < kKeep; ++i)
-            if (lane + 32 * i < groups)
+            if (i < mine)
                 top = max_nan(top, group_max(kept[i]));
-        for (int at = lane + 32 * kKeep; at < groups; at += 32) {
-            int m, d;
-            place(at, m, d);
-            top = max_nan(top, group_max(load_raw(src + m * row + d, p.wide)));
-        }
+        for (int i = kKeep; i < mine; ++i)
+            top = max_nan(top, group_max(load_raw(from(src, i), p.wide)));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1)
             top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (p.team > 1) {
+            // the team's warps meet once an item (it also keeps the scale's
+            // reads before its write); two sets of their maxima take turns
+            if ((tid & 31) == 0)
+                tops[turn][tid >> 5] = top;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(step) : "memory");
+            for (int w = 0; w < p.team; ++w)
+                top = max_nan(top, tops[turn][team * p.team + w]);
+            turn ^= 1;
+        }
         float t = __fdiv_rn(top, 127.f), f = 1.f;
         if (!(top <= 3.402823466e38f)) {
             t = __int_as_float(0x7fc00000);             // an infinity or a NaN among them
@@ -675,25 +746,21 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const RowsParams p)
         }
         if (f != 1.f) {                                 // the block's earlier codes, as the whole vectors they are
             int8_t *old = dst - (long long)before * p.D;
-            for (int at = lane; at < before * per; at += 32) {
+            for (int at = lane; at < before * per; at += step) {
                 uint4 *w = reinterpret_cast<uint4 *>(old + (long long)at * kGroup);
                 const uint4 u = *w;
                 *w = make_uint4(fewer4(u.x, f), fewer4(u.y, f), fewer4(u.z, f), fewer4(u.w, f));
             }
         }
         const bool quick = t > 0x1p-90f && t < 0x1p90f;
-        const float r = quick ? __frcp_rn(t) : 0.f;
+        const float inv = quick ? __frcp_rn(t) : 0.f;
+        uint4 *to = reinterpret_cast<uint4 *>(dst) + lane;   // the run's vectors follow each other in the cache
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            const int at = lane + 32 * i;
-            if (at < groups)                            // the run's vectors follow each other in the cache
-                *reinterpret_cast<uint4 *>(dst + (long long)at * kGroup) = codes16(kept[i], t, r, quick);
-        }
-        for (int at = lane + 32 * kKeep; at < groups; at += 32) {
-            int m, d;
-            place(at, m, d);
-            *reinterpret_cast<uint4 *>(dst + (long long)at * kGroup) = codes16(load_raw(src + m * row + d, p.wide), t, r, quick);
-        }
+        for (int i = 0; i < kKeep; ++i)
+            if (i < mine)
+                to[i * step] = codes16(kept[i], t, inv, quick);
+        for (int i = kKeep; i < mine; ++i)
+            to[i * step] = codes16(load_raw(from(src, i), p.wide), t, inv, quick);
         if (lane == 0)
             *scale = t;
     }
@@ -812,11 +879,16 @@ cudaError_t launch_kind(const RowsParams &p, bool write, cudaStream_t st)
 }
 
 template <typename T>
-cudaError_t launch8(const RowsParams &p, bool write, cudaStream_t st)
+cudaError_t launch8(RowsParams p, bool write, cudaStream_t st)
 {
     if (!write)
         return launch(read8_kernel<T>, p, (sizeof(Token) + sizeof(long long)) * (size_t)p.chunk, st);
-    const size_t smem = (sizeof(Token) + sizeof(Run)) * (size_t)p.chunk;
+    const size_t smem = sizeof(Run) * (size_t)p.chunk;
+    const long long groups = (long long)(p.cu_q ? p.scale_block : 1) * (p.D / kGroup);
+    for (p.team = 1; p.team < kThreads / 32 && groups > 32 * kKeep * p.team; p.team *= 2) {}
+    // runs come whole to the CTA of their first token: of large blocks a CTA
+    // looks for less than one (64-slot blocks, four CTAs an SM: 118 us with 53 tokens, 103 with 16)
+    p.chunk = p.team > 1 && p.chunk > 16 ? 16 : p.chunk;
     return p.cu_q ? launch(append8_kernel<T, false>, p, smem, st) : launch(append8_kernel<T, true>, p, smem, st);
 }
 
