@@ -426,7 +426,10 @@ def _step_scored(q, k_new, v_new, k, v, lengths, slot_ids, table, out, status, k
                 raise TypeError("weights must be a contiguous float32 tensor of the cache's shape without D")
             _plain(dev, weights)
             o.weights = weights.data_ptr()
-            need = lib.gqa_weights_scratch_bytes(B, Hq, Hkv, table.shape[1] * n2 if paged else n2)
+            key = (B, Hq, Hkv, table.shape[1] * n2 if paged else n2)
+            need = _need_cache.get(key)
+            if need is None:
+                need = _need_cache[key] = lib.gqa_weights_scratch_bytes(*key)
             scratch = _scratch(device, need, stream)
             o.weights_scratch = scratch.data_ptr()
             o.weights_scratch_bytes = need

@@ -391,7 +391,7 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
     if (!s.attend && (!aligned16(k_new) || !aligned16(v_new)))
         return GQA_ERR_INVALID_ARGUMENT;
     const bool kvi = s.dt == GQA_DTYPE_I8;
-    if (opt && (!(opt->score_cap >= 0.f && opt->score_cap <= 3.402823466e38f) || !aligned4(opt->head_slopes) ||
+    if (opt && (!(opt->score_cap == 0.f || (opt->score_cap >= 0x1p-60f && opt->score_cap <= 0x1p60f)) || !aligned4(opt->head_slopes) ||
                 !aligned4(opt->weights)))
         return GQA_ERR_INVALID_ARGUMENT;
     if (kvi && (!opt || !opt->k_block_scale || !opt->v_block_scale || !aligned4(opt->k_block_scale) ||

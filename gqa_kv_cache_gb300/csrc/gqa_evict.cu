@@ -520,9 +520,11 @@ cudaError_t evict_launch(EvictParams p, int sms, cudaStream_t st)
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     const unsigned units = (unsigned)(p.B * p.Hkv);
-    // enough units to fill the GPU: each moves its own vectors once its slots are
-    // chosen, beside others' choosing (XXX)
-    const bool move = p.k_out && (int)units >= sms;
+    // where units fill half the GPU each moves its own vectors once its slots are
+    // chosen, beside others' choosing: of up to 16384 slots to 2048 (moved by the
+    // same / another kernel) 40 units 60.6 / 43.7 us, 80 71.3 / 81.6, 160 98.0 /
+    // 105.4, 240 118 / 143, 320 183 / 179
+    const bool move = p.k_out && 2LL * units >= sms;
     cudaLaunchConfig_t cfg = config(dim3(units), kThreads, smem, st, attr);
     e = move ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p) : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p);
     if (e != cudaSuccess || move)

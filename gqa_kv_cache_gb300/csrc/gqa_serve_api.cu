@@ -31,6 +31,12 @@ int current_sms()
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) == 0; }
 
+bool apart(const void *a, double na, const void *b, double nb)
+{
+    const double x = (double)reinterpret_cast<uintptr_t>(a), y = (double)reinterpret_cast<uintptr_t>(b);
+    return x + na <= y || y + nb <= x;
+}
+
 gqa_status run_evict(EvictParams p, int D, gqa_dtype kv, void *stream)
 {
     if (p.B < 0 || p.Hkv < 1 || D < 1 || kv < GQA_DTYPE_F32 || kv > GQA_DTYPE_I8)
@@ -63,6 +69,15 @@ gqa_status run_evict(EvictParams p, int D, gqa_dtype kv, void *stream)
     if (!aligned(p.k_cache, 16) || !aligned(p.v_cache, 16) || !aligned(p.k_out, 16) || !aligned(p.v_out, 16) ||
         !aligned(p.weights, 4) || !aligned(p.weights_out, 4))
         return GQA_ERR_INVALID_ARGUMENT;
+    if (p.k_out) {
+        const double vectors = p.paged ? (double)p.num_blocks * p.Hkv * p.block_size : (double)p.R * p.Hkv * p.Smax;
+        const double out = (double)p.B * p.Hkv * p.out_slots, in = vectors * row;
+        if (!apart(p.k_out, out * row, p.v_out, out * row) || (p.weights_out && !apart(p.weights, vectors * 4, p.weights_out, out * 4)))
+            return GQA_ERR_INVALID_ARGUMENT;
+        for (const void *o : {p.k_out, p.v_out})
+            if (!apart(p.k_cache, in, o, out * row) || !apart(p.v_cache, in, o, out * row))
+                return GQA_ERR_INVALID_ARGUMENT;
+    }
     p.row_bytes = (int)row;
     const int sms = current_sms();
     if (!sms)
@@ -84,7 +99,7 @@ gqa_status gqa_rotate(const void *q, const void *k, void *q_out, void *k_out, gq
         return GQA_ERR_INVALID_ARGUMENT;
     if (T == 0)
         return GQA_OK;
-    if (!positions && (B < 0 || !cu_q || !lengths))
+    if (!positions && (B < 0 || !cu_q || (B && !lengths)))
         return GQA_ERR_INVALID_ARGUMENT;
     if (D > 1024 || ((long long)Hq + Hkv) * D > (1 << 24))
         return GQA_ERR_UNSUPPORTED;

@@ -98,10 +98,10 @@ typedef enum gqa_dtype {
     GQA_DTYPE_I8 = 4    /* a cache of int8 codes with a float32 scale per (block of slots,
                            cache head) (gqa_options.k_block_scale / v_block_scale): dense
                            (R, Hkv, Smax / scale_block), paged (num_blocks, Hkv), a block
-                           each. A slot's vector is c t, t the scale of its block (finite,
-                           not negative, within 2^-100 .. 2^100 or 0; NaN where a value
-                           that is not finite was written). The calls that write keep the
-                           scales: a block that begins with a new token takes t = max|x| /
+                           each. A slot's vector is c t, t the scale of its block (0, or
+                           positive and, where it is attended, within 2^-64 .. 2^64; NaN
+                           where a value that is not finite was written). The calls that
+                           write keep the scales: a block that begins with a new token takes t = max|x| /
                            127 over the call's tokens of the block; one that gets tokens
                            behind earlier slots keeps its t where max|x| / 127 <= t, else
                            t doubles until it does and the earlier codes become rint(c /
@@ -111,7 +111,8 @@ typedef enum gqa_dtype {
                            bfloat16 q, k_new and v_new, the read-only attend a float32 or
                            bfloat16 query; D = 64 or 128, G <= 8, any paged block size;
                            GQA_KERNEL_AUTO or GQA_KERNEL_TC. No multi-token step (write
-                           prompts with gqa_append), no key bounds.                 */
+                           prompts with gqa_append), no key bounds; two rows that write
+                           one block are undefined.                                 */
 } gqa_dtype;
 
 /* Bits OR-ed into *d_status by the kernels. */
@@ -205,7 +206,8 @@ typedef struct gqa_options {
      * count its weights: a bfloat16 or 8-bit cache, D = 64 or 128, G <= 8,
      * GQA_KERNEL_AUTO or GQA_KERNEL_TC; GQA_ERR_UNSUPPORTED elsewhere.          */
     float score_cap;                 /* c > 0: the score s becomes c tanh(s / c); 0: off;
-                                        < 0, infinite or NaN is GQA_ERR_INVALID_ARGUMENT */
+                                        other values outside 2^-60 .. 2^60 are
+                                        GQA_ERR_INVALID_ARGUMENT                        */
     const float *head_slopes;        /* (device) (Hq,) float32 or NULL: slope_h (j - L) is
                                         added to the (capped) score of slot j, L the
                                         query's position: a positive slope takes from
@@ -461,10 +463,11 @@ gqa_status gqa_validate_multi(const int32_t *lengths, const int32_t *cu_q, const
  * around the kernel it launches; gqa_trace_collect waits for them and
  * returns, per kernel kind, the launches and total milliseconds since the
  * previous collect. Kinds: 0 = SIMT decode, 1 = tensor-core decode (over an
- * E2M1 cache q4_decode_kernel), 2 = the small-cache decode, 3 = the tcgen05 form of 17- to 32-row multi-token
+ * E2M1 cache q4_decode_kernel; over an 8-bit one, or with capped, biased or
+ * counted scores, scored_kernel with the writes and counts around it), 2 = the small-cache decode, 3 = the tcgen05 form of 17- to 32-row multi-token
  * units (each decode step is exactly one kernel launch); gqa_kernel_name
- * gives each kind's kernel name. append, read and block selection are not
- * traced. Meant for benchmarks.
+ * gives each kind's kernel name. append, read, block selection, rotation and
+ * eviction are not traced. Meant for benchmarks.
  */
 int gqa_trace_enable(int on);
 gqa_status gqa_trace_collect(int n_kinds, int64_t *launches, double *ms);
@@ -653,7 +656,8 @@ gqa_status gqa_rotate(const void *q, const void *k, void *q_out, void *k_out, gq
  *  ids      (device) (B, Hkv, n_keep) int32: the kept slots, then -1
  *  new_lengths (device) (B,) int32: min(lengths[b], n_keep); not `lengths` itself
  *  k_out, v_out (device) (B, Hkv, out_slots, D), out_slots >= n_keep, both or
- *           neither; must not overlap the cache. Slots behind the kept ones are left
+ *           neither, apart from each other and from the cache. Slots behind the kept
+ *           ones are left
  *  weights_out (device) (B, Hkv, out_slots) or NULL: the kept counts, then zeros
  * A row with a bad length, slot id or block sets its status bit: ids -1, length
  * 0, nothing moved. Rows that share a block or cache row are undefined in place.

@@ -151,3 +151,47 @@ def test_runs_give_the_same_bits():
     for n, x in start.items():
         state[n].copy_(x)
     assert all(torch.equal(a, b) for a, b in zip(run(state), first))
+
+
+def test_empty_batches():
+    """No rows, or rows without tokens: nothing is launched or written."""
+    k8 = torch.zeros(2, Hkv, S, D, dtype=torch.int8, device="cuda")
+    kw = dict(k_block_scale=torch.zeros(2, Hkv, 4, device="cuda"), v_block_scale=torch.zeros(2, Hkv, 4, device="cuda"))
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    q = torch.zeros(0, Hq, D, dtype=torch.bfloat16, device="cuda")
+    new = torch.zeros(0, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    assert gqa.attend(q, k8, k8, none, **kw).shape == (0, Hq, D)
+    assert gqa.decode_step(q, new, new, k8, k8, none, **kw).shape == (0, Hq, D)
+    kb = torch.zeros(2, Hkv, S, D, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(2, Hkv, S, device="cuda")
+    assert gqa.attend(q, kb, kb, none, score_cap=3.0, weights=w).shape == (0, Hq, D)
+    ids, lengths = gqa.evict(kb, kb, w, none, 8)
+    assert ids.shape == (0, Hkv, 8) and lengths.shape == (0,)
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gqa.append(new, new, k8, k8, none, one, **kw)
+    gqa.append(torch.ones(3, Hkv, D, device="cuda"), torch.ones(3, Hkv, D, device="cuda"), k8, k8.clone(),
+               torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda"), **kw)
+    assert not k8.any() and not kw["k_block_scale"].any()
+    a, _ = gqa.rotate(torch.ones(3, 1, D, device="cuda"), None, gqa.Rotary(D), lengths=none, cu_q=one)
+    assert (a == 1).all()                                         # tokens of no row
+
+
+def test_decode_steps_with_bad_rows():
+    """A row that cannot take its token is left as it is and gives NaN; the others are served."""
+    g = torch.Generator().manual_seed(3)
+    for kind in (torch.int8, torch.bfloat16):
+        cache = [torch.ones(3, Hkv, S, D, dtype=kind, device="cuda") for _ in range(2)]
+        kw = dict(k_block_scale=torch.ones(3, Hkv, 16, device="cuda"), v_block_scale=torch.ones(3, Hkv, 16, device="cuda")) \
+            if kind == torch.int8 else dict(score_cap=4.0)
+        weights = torch.zeros(3, Hkv, S, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q, k, v = _inputs(1, g)
+        at = torch.tensor([S, 7, -1], dtype=torch.int32).cuda()
+        out = gqa.decode_step(q, k, v, *cache, at, status=status, weights=weights, **kw)
+        assert int(status) == 1 and out[0].isnan().all() and out[2].isnan().all() and out[1].isfinite().all()
+        assert (cache[0][0] == 1).all() and (cache[0][2] == 1).all() and not weights[0].any() and not weights[2].any()
+        assert abs(float(weights[1].sum()) - Hq) < 1e-4
+        ids = torch.tensor([0, 9, 1], dtype=torch.int32).cuda()
+        status.zero_()
+        out = gqa.decode_step(q, k, v, *cache, at.clamp(0, 9), ids, status=status, **kw)
+        assert int(status) == 2 and out[1].isnan().all() and out[0].isfinite().all()

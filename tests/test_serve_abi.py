@@ -60,7 +60,9 @@ def test_evict_checks(lib):
     for bad in (dict(k=None), dict(w=None), dict(ln=None), dict(ids=None), dict(nl=None), dict(nl=P), dict(B=-1),
                 dict(Hkv=0), dict(D=0), dict(R=1), dict(S=0), dict(kv=9), dict(kv=-1), dict(n=0), dict(first=-1),
                 dict(last=-1), dict(first=5, last=4), dict(k=264), dict(w=258), dict(ko=P), dict(wo=P),
-                dict(ko=P, vo=P, os=7), dict(ko=264, vo=P, os=8)):
+                dict(ko=P, vo=P, os=7), dict(ko=264, vo=P, os=8), dict(ko=P, vo=1 << 20, os=8),
+                dict(ko=1 << 20, vo=P + 2 * 2 * 64 * 128 - 16, os=8), dict(ko=1 << 20, vo=1 << 20, os=8),
+                dict(ko=1 << 20, vo=1 << 22, wo=P, os=8)):
         assert _evict(lib, **bad) == INVALID, bad
     for bad in (dict(kv=I8), dict(kv=E2M1), dict(D=12), dict(B=1 << 20, Hkv=64, sl=P), dict(kv=E4M3, D=24)):
         assert _evict(lib, **bad) == UNSUPPORTED, bad
@@ -98,7 +100,8 @@ def test_attend_checks(lib):
     for bad in (dict(), dict(k_block_scale=P), {**good, "scale_block": 0}, {**good, "scale_block": 48},
                 {**good, "score_cap": -1.0}):
         assert _attend(lib, I8, **bad) == INVALID, bad
-    for bad in (dict(score_cap=-1.0), dict(score_cap=float("nan")), dict(score_cap=float("inf")), dict(head_slopes=258),
+    for bad in (dict(score_cap=-1.0), dict(score_cap=float("nan")), dict(score_cap=float("inf")), dict(score_cap=2.0 ** 61),
+                dict(score_cap=2.0 ** -61), dict(head_slopes=258),
                 dict(weights=258)):
         assert _attend(lib, **bad) == INVALID, bad
     for bad in (dict(kv=F32), dict(D=32), dict(Hq=18), dict(kernel=1), dict(kernel=3), dict(kernel=4)):
