@@ -411,7 +411,7 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
     if (kernel < 0)
         return GQA_ERR_UNSUPPORTED;
     if (opt && opt->weights) {
-        if (scored_count_ctas(s.B, s.Hkv, cap_rows) > INT_MAX)
+        if (cap_rows > (1 << 30) || scored_count_ctas(s.B, s.Hkv, cap_rows) > INT_MAX)
             return GQA_ERR_UNSUPPORTED;
         if (!opt->weights_scratch || !aligned16(opt->weights_scratch) ||
             opt->weights_scratch_bytes < scored_scratch_bytes(s.B, s.Hq, s.Hkv, cap_rows))

@@ -18,6 +18,8 @@
 // memory may run kDeep chunks ahead of the stores as long as a chunk is stored
 // after it and those before it have come. Both are bound by memory: 2 rows of
 // bytes a kept vector.
+#include <cooperative_groups.h>
+
 #include <atomic>
 
 #include "gqa_common.cuh"
@@ -26,8 +28,11 @@
 namespace gqa {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCached = 15360;     // counts kept in shared memory (60 KB: three CTAs an SM)
+constexpr int kCachedWide = 49152; // and by each CTA of a cluster (192 KB)
 constexpr int kBins = 2048;
 constexpr int kList = 1024;        // counts that share their first digit with the smallest kept one
 constexpr int kEach = 4;           // counts a thread loads at once
@@ -193,15 +198,20 @@ __device__ __forceinline__ void gather(const EvictParams &p, const Line &line, i
     }
 }
 
-// MOVE: the CTA also moves its unit's vectors into the outputs.
-template <bool MOVE>
-__global__ void __launch_bounds__(kThreads, MOVE ? 2 : 3) evict_select_kernel(const EvictParams p)
+// MOVE: the CTA also moves its unit's vectors into the outputs. WIDE: a unit is a
+// cluster of p.cluster CTAs, each with a part of the row's slots; histograms and
+// counts are summed over the cluster's shared memory.
+template <bool MOVE, bool WIDE>
+__global__ void __launch_bounds__(kThreads, MOVE ? 2 : WIDE ? 1 : 3) evict_select_kernel(const EvictParams p)
 {
-    extern __shared__ uint32_t keys[];         // [min(capacity, kCached)]
-    __shared__ int hist[kBins], scan[kWarps], tied[kWarps], found[3], bad, listed;
+    extern __shared__ uint32_t keys[];         // [p.cached]
+    __shared__ int hist[kBins], scan[kWarps], tied[kWarps], found[3], part[2], bad, listed;
+    __shared__ int sum[WIDE ? kBins : 1];
     __shared__ uint32_t list[kList];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int CL = WIDE ? p.cluster : 1, rank = WIDE ? (int)cluster.block_rank() : 0;
+    const int unit = blockIdx.x / CL, b = unit / p.Hkv, h = unit % p.Hkv;
     // the next kernel may be set up meanwhile (it waits for this one's end)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -216,38 +226,41 @@ __global__ void __launch_bounds__(kThreads, MOVE ? 2 : 3) evict_select_kernel(co
         bad = bits;
     __syncthreads();
     if (!bits && p.paged)
-        for (int i = tid; i < (L + p.block_size - 1) / p.block_size; i += kThreads) {
+        for (int i = tid; i < (int)(((long long)L + p.block_size - 1) / p.block_size); i += kThreads) {
             const int blk = __ldg(p.block_table + (long long)b * p.max_blocks + i);
             if (blk < 0 || blk >= p.num_blocks)
                 bad = kBadBlock;
         }
     __syncthreads();
-    bits = bad;
+    bits = bad;                                // the same in every CTA of the cluster
     const Line line(p, bits ? 0 : b, h);
-    int32_t *ids = p.ids + (long long)blockIdx.x * p.n_keep;
+    int32_t *ids = p.ids + (long long)unit * p.n_keep;
     const int n = bits ? 0 : min(L, p.n_keep);
-    if (tid == 0 && h == 0) {
+    if (tid == 0 && h == 0 && rank == 0) {
         p.new_lengths[b] = n;
         if (bits && p.status)
             atomicOr(p.status, bits);
     }
     float *to = nullptr;                       // where the counts go
     if (p.k_out)
-        to = p.weights_out ? p.weights_out + (long long)blockIdx.x * p.out_slots : nullptr;
+        to = p.weights_out ? p.weights_out + (long long)unit * p.out_slots : nullptr;
     if (bits || L <= p.n_keep) {
-        for (int i = tid; i < p.n_keep; i += kThreads)
+        for (int i = rank * kThreads + tid; i < p.n_keep; i += kThreads * CL)
             ids[i] = i < n ? i : -1;
         if (to && !bits)
-            for (int i = tid; i < p.out_slots; i += kThreads)
+            for (int i = rank * kThreads + tid; i < p.out_slots; i += kThreads * CL)
                 to[i] = i < n ? p.weights[line.at(i)] : 0.f;
         if constexpr (MOVE) {
             __syncthreads();                   // the ids are there
-            gather<kThreads>(p, line, blockIdx.x, 0, (long long)n * (p.row_bytes / 16));
+            gather<kThreads>(p, line, unit, 0, (long long)n * (p.row_bytes / 16));
         }
         return;
     }
     const int lo = p.n_first, hi = L - p.n_last;       // the slots that compete
-    const int held = min(L, p.cached);
+    // this CTA's slots, the counts of the first `held` of them in shared memory
+    const int mine = WIDE ? (L / CL / 32 + 1) * 32 : L;
+    const int a0 = min((long long)L, (long long)rank * mine), a1 = min((long long)L, (long long)a0 + mine);
+    const int held = min(a1 - a0, p.cached);
     int k = p.n_keep - p.n_first - p.n_last;           // how many of them are kept
     for (int i = tid; i < kBins; i += kThreads)
         hist[i] = 0;
@@ -255,16 +268,16 @@ __global__ void __launch_bounds__(kThreads, MOVE ? 2 : 3) evict_select_kernel(co
         listed = 0;
     __syncthreads();
     // the counts, and a histogram of their first 11 bits
-    {
+    if (a0 < a1) {
         int j[kEach], blk[kEach] = {};
         auto look = [&](int j0) {
 #pragma unroll
             for (int e = 0; e < kEach; ++e)
-                j[e] = min(j0 + e * kThreads, L - 1);
+                j[e] = min(j0 + e * kThreads, a1 - 1);
             line.look_up(j, blk);
         };
-        look(tid);
-        for (int j0 = tid; j0 < L; j0 += kThreads * kEach) {
+        look(a0 + tid);
+        for (int j0 = a0 + tid; j0 < a1; j0 += kThreads * kEach) {
             long long at[kEach];
             float w[kEach];
             line.place(j, blk, at);
@@ -276,25 +289,41 @@ __global__ void __launch_bounds__(kThreads, MOVE ? 2 : 3) evict_select_kernel(co
             for (int e = 0; e < kEach; ++e) {
                 const int x = j0 + e * kThreads;
                 const uint32_t u = order_of(w[e]);
-                if (x < held)
-                    keys[x] = u;
-                if (x >= lo && x < hi)
+                if (x < a0 + held)
+                    keys[x - a0] = u;
+                if (x >= lo && x < min(hi, a1))
                     atomicAdd(&hist[u >> 21], 1);
             }
         }
     }
     __syncthreads();
-    auto key = [&](int j) { return j < held ? keys[j] : order_of(p.weights[line.at(j)]); };
+    auto key = [&](int j) { return j < a0 + held ? keys[j - a0] : order_of(p.weights[line.at(j)]); };
+    // the unit's histogram
+    auto whole = [&](int bins) -> const int * {
+        if constexpr (WIDE) {
+            cluster.sync();
+            for (int i = tid; i < bins; i += kThreads) {
+                int v = 0;
+                for (int r = 0; r < CL; ++r)
+                    v += cluster.map_shared_rank(hist, r)[i];
+                sum[i] = v;
+            }
+            cluster.sync();
+            return sum;
+        } else {
+            return hist;
+        }
+    };
 
     // the smallest kept count `least`, how many equal it (`equal`), and how many of those are kept (k)
     uint32_t least = 0xffffffffu;
     int equal = 0;
     if (k > 0) {
-        least = (uint32_t)find_digit(hist, kBins, k, equal, scan, found) << 21;
+        least = (uint32_t)find_digit(whole(kBins), kBins, k, equal, scan, found) << 21;
         // the others' digits are found among the counts that share the first: a list of them where it holds them
         const bool few = equal <= kList;
         if (few) {
-            for (int j = lo + tid; j < hi; j += kThreads) {
+            for (int j = max(lo, a0) + tid; j < min(hi, a1); j += kThreads) {
                 const uint32_t u = key(j);
                 if (u >> 21 == least >> 21)
                     list[atomicAdd(&listed, 1)] = u;
@@ -307,14 +336,14 @@ __global__ void __launch_bounds__(kThreads, MOVE ? 2 : 3) evict_select_kernel(co
             for (int i = tid; i < bins; i += kThreads)
                 hist[i] = 0;
             __syncthreads();                   // (also: the list is there)
-            const int n0 = few ? 0 : lo, n1 = few ? listed : hi;
+            const int n0 = few ? 0 : max(lo, a0), n1 = few ? listed : min(hi, a1);
             for (int j = n0 + tid; j < n1; j += kThreads) {
                 const uint32_t u = few ? list[j] : key(j);
                 if ((u & mask) == least)
                     atomicAdd(&hist[(u >> shift) & (bins - 1)], 1);
             }
             __syncthreads();
-            least |= (uint32_t)find_digit(hist, bins, k, equal, scan, found) << shift;
+            least |= (uint32_t)find_digit(whole(bins), bins, k, equal, scan, found) << shift;
             mask |= (uint32_t)(bins - 1) << shift;
         }
     }
@@ -322,22 +351,23 @@ __global__ void __launch_bounds__(kThreads, MOVE ? 2 : 3) evict_select_kernel(co
     // added up, then every kept slot has its place. Of those that equal `least`
     // the first k are kept, all of them where there are no more.
     const bool all = equal == k;
-    const int share = (L + 32 * kWarps - 1) / (32 * kWarps) * 32, j0 = warp * share, j1 = min(L, j0 + share);
+    const int share = ((a1 - a0) / (32 * kWarps) + 1) * 32, j0 = min((long long)a1, (long long)a0 + (long long)warp * share);
+    const int j1 = min((long long)a1, (long long)j0 + share);
     auto look = [&](int j, unsigned &more, unsigned &tie) {
-        const bool in = j >= lo && j < hi;
+        const bool in = j < j1 && j >= lo && j < hi;
         const uint32_t u = in ? key(j) : 0u;
         more = __ballot_sync(0xffffffffu, j < j1 && (!in || (k > 0 && (u > least || (all && u == least)))));
-        tie = all ? 0u : __ballot_sync(0xffffffffu, j < j1 && in && u == least);
+        tie = all ? 0u : __ballot_sync(0xffffffffu, in && u == least);
     };
-    int mine = 0, ties = 0;
+    int kept = 0, ties = 0;
     for (int j = j0 + lane; j - lane < j1; j += 32) {
         unsigned more, tie;
         look(j, more, tie);
-        mine += __popc(more);
+        kept += __popc(more);
         ties += __popc(tie);
     }
     if (lane == 0) {
-        scan[warp] = mine;
+        scan[warp] = kept;
         tied[warp] = ties;
     }
     __syncthreads();
@@ -345,6 +375,18 @@ __global__ void __launch_bounds__(kThreads, MOVE ? 2 : 3) evict_select_kernel(co
     for (int w = 0; w < warp; ++w) {
         before += scan[w];
         same += tied[w];
+    }
+    if constexpr (WIDE) {
+        if (warp == kWarps - 1 && lane == 0) {
+            part[0] = before + kept;
+            part[1] = same + ties;
+        }
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {       // and of the CTAs before
+            const int *q = cluster.map_shared_rank(part, r);
+            before += q[0];
+            same += q[1];
+        }
     }
     for (int j = j0 + lane; j - lane < j1; j += 32) {
         unsigned more, tie;
@@ -356,10 +398,13 @@ __global__ void __launch_bounds__(kThreads, MOVE ? 2 : 3) evict_select_kernel(co
         before += __popc(more);
         same += __popc(tie);
     }
-    __syncthreads();
+    if constexpr (WIDE)
+        cluster.sync();                        // every CTA's ids are there (and nobody's shared memory is read any more)
+    else
+        __syncthreads();
     // the counts: kept ones in order, zeros behind them
     if (p.k_out) {
-        for (int i0 = tid; to && i0 < p.out_slots; i0 += kThreads * kEach) {
+        for (int i0 = rank * kEach * kThreads + tid; to && i0 < p.out_slots; i0 += kThreads * kEach * CL) {
             int j[kEach], blk[kEach] = {};
             long long at[kEach];
             float w[kEach];
@@ -379,10 +424,10 @@ __global__ void __launch_bounds__(kThreads, MOVE ? 2 : 3) evict_select_kernel(co
             }
         }
         if constexpr (MOVE)
-            gather<kThreads>(p, line, blockIdx.x, 0, (long long)n * (p.row_bytes / 16));
+            gather<kThreads>(p, line, unit, 0, (long long)n * (p.row_bytes / 16));
         return;
     }
-    for (int i0 = 0; i0 < n; i0 += kThreads * kEach) {
+    for (int i0 = 0; rank == 0 && i0 < n; i0 += kThreads * kEach) {
         float w[kEach];
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
@@ -398,8 +443,20 @@ __global__ void __launch_bounds__(kThreads, MOVE ? 2 : 3) evict_select_kernel(co
         }
         __syncthreads();
     }
-    for (int j = n + tid; j < L; j += kThreads)
-        p.weights[line.at(j)] = 0.f;
+    if constexpr (WIDE)
+        cluster.sync();                        // the kept counts have been read
+    for (int j0 = n + rank * kEach * kThreads + tid; j0 < L; j0 += kThreads * kEach * CL) {
+        int j[kEach], blk[kEach] = {};
+        long long at[kEach];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            j[e] = min(j0 + e * kThreads, L - 1);
+        line.look_up(j, blk);
+        line.place(j, blk, at);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            p.weights[at[e]] = 0.f;            // (the last slot more than once)
+    }
 }
 
 // Kept vectors into other buffers (B, Hkv, out_slots, row): a CTA takes a share
@@ -496,25 +553,25 @@ cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t st, 
 
 cudaError_t evict_launch(EvictParams p, int sms, cudaStream_t st)
 {
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     const long long cap = p.paged ? (long long)p.max_blocks * p.block_size : (long long)p.Smax;
-    p.cached = (int)(cap < kCached ? cap : kCached);
     p.block_shift = -1;
     for (int i = 0; i < 31; ++i)
         if (p.paged && 1 << i == p.block_size)
             p.block_shift = i;
-    const int smem = p.cached * (int)sizeof(uint32_t);
-    static std::atomic<uint64_t> ready;        // the size is set once a device
+    static std::atomic<uint64_t> ready;        // the sizes are set once a device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        constexpr int most = kCached * (int)sizeof(uint32_t);
-        e = cudaFuncSetAttribute(evict_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        constexpr int one = kCached * (int)sizeof(uint32_t), wide = kCachedWide * (int)sizeof(uint32_t);
+        e = cudaFuncSetAttribute(evict_select_kernel<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, one);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+            e = cudaFuncSetAttribute(evict_select_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, one);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(evict_select_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, wide);
         if (e != cudaSuccess)
             return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
@@ -525,8 +582,25 @@ cudaError_t evict_launch(EvictParams p, int sms, cudaStream_t st)
     // same / another kernel) 40 units 60.6 / 43.7 us, 80 71.3 / 81.6, 160 98.0 /
     // 105.4, 240 118 / 143, 320 183 / 179
     const bool move = p.k_out && 2LL * units >= sms;
-    cudaLaunchConfig_t cfg = config(dim3(units), kThreads, smem, st, attr);
-    e = move ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p) : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p);
+    // few units of long rows: clusters of CTAs, as many as the GPU has SMs for and
+    // 4096 slots each are left to (8 units, one CTA / a cluster: 8192 slots to 512
+    // 23.1 / 24.2 us, 16384 to 1024 40.9 / 25.7, 131072 to 4096 470 / 48.2)
+    p.cluster = 1;
+    while (!move && cap > 8192 && p.cluster < 8 && (long long)units * p.cluster * 2 <= sms && cap / (p.cluster * 2) >= 4096)
+        p.cluster *= 2;
+    const long long most = p.cluster > 1 ? kCachedWide : kCached, held = (cap / p.cluster / 32 + 1) * 32;
+    p.cached = (int)(held < most ? held : most);
+    cudaLaunchConfig_t cfg = config(dim3(units * p.cluster), kThreads, (size_t)p.cached * sizeof(uint32_t), st, attr);
+    if (p.cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = p.cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    e = p.cluster > 1 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<false, true>, p)
+        : move        ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true, false>, p)
+                      : cudaLaunchKernelEx(&cfg, evict_select_kernel<false, false>, p);
     if (e != cudaSuccess || move)
         return e;
     if (p.k_out) {

@@ -139,7 +139,7 @@ struct EvictParams {
     int32_t *status;
     int B, Hkv, R, Smax, paged, num_blocks, block_size, max_blocks;
     int row_bytes, out_slots, n_keep, n_first, n_last;
-    int cached, shares, block_shift; // set by evict_launch
+    int cached, cluster, shares, block_shift;   // set by evict_launch
 };
 cudaError_t evict_launch(EvictParams p, int sms, cudaStream_t st);
 

@@ -219,7 +219,8 @@ typedef struct gqa_options {
                                         head, are ADDED to its count; other counts are left.
                                         A row with a bad block gets NaN counts in its usable
                                         blocks, any other bad row none. Two rows of the batch
-                                        that share a cache row or block are undefined here  */
+                                        that share a cache row or block are undefined here;
+                                        rows of at most 2^30 slots                      */
     void *weights_scratch;           /* (device) with weights: gqa_weights_scratch_bytes(...)
                                         bytes, 16-byte aligned, contents free before and
                                         after the call; one call at a time              */
@@ -649,7 +650,8 @@ gqa_status gqa_rotate(const void *q, const void *k, void *q_out, void *k_out, gq
  * Keys are moved as they are: positions that were turned into them stay.
  *
  *  k_cache, v_cache (device) float32, bfloat16 or E4M3 (GQA_ERR_UNSUPPORTED for
- *           the others); D times the element size a multiple of 16
+ *           the others, and for rows of more than 2^30 slots); D times the element
+ *           size a multiple of 16
  *  weights  (device) float32 counts, the cache's shape without D
  *  lengths  (device) (B,) int32 valid slots, 0 <= lengths[b] <= capacity
  *  n_keep   >= 1, >= n_first + n_last (both >= 0)

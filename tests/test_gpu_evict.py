@@ -89,7 +89,7 @@ def test_in_place_and_elsewhere(layout, bs, kind, D, n_keep, n_first, n_last):
 
 @pytest.mark.parametrize("counts", ["same", "zero", "few", "signs"])
 def test_equal_counts_go_to_the_lowest_slot(counts):
-    c = Case("bf16", "dense", [700, 5000], 1, 64, 5008, counts=counts)
+    c = Case("bf16", "dense", [700, 5000], 1, 64, 9008, counts=counts)
     for n_keep, n_first, n_last in ((64, 0, 0), (1000, 10, 20), (4999, 0, 1)):
         _same(c.run(n_keep, n_first=n_first, n_last=n_last), c.expect(n_keep, n_first, n_last))
 
@@ -106,6 +106,34 @@ def test_a_row_longer_than_the_cached_counts():
     c = Case("e4m3", "paged", [40000, 16384, 16385], 1, 16, 40000, bs=32, seed=4)
     for n_keep in (100, 20000):
         _same(c.run(n_keep, n_first=1, n_last=5), c.expect(n_keep, 1, 5))
+
+
+@pytest.mark.parametrize("counts", ["spread", "same", "few"])
+def test_long_rows_elsewhere(counts):
+    """Long rows of few heads (several CTAs each), into other buffers; many equal counts among them."""
+    c = Case("e4m3", "paged", [40000, 7, 33333], 1, 16, 40000, bs=32, seed=6, counts=counts)
+    for n_keep, n_first, n_last in ((9000, 2, 3), (500, 0, 0)):
+        want = c.expect(n_keep, n_first, n_last)
+        k2, v2 = (torch.zeros(3, 1, n_keep, 16, dtype=torch.uint8, device="cuda") for _ in range(2))
+        w2 = torch.zeros(3, 1, n_keep, device="cuda")
+        ids, new, *_ = c.run(n_keep, n_first=n_first, n_last=n_last, k_out=k2, v_out=v2, weights_out=w2)
+        _same((ids, new), want[:2])
+        for b, n in enumerate(want[1].tolist()):
+            for out, x in ((k2, want[2]), (v2, want[3]), (w2, want[4])):
+                assert torch.equal(out[b, :, :n].cpu(), R.row_slots(x, b, n, c.table, c.slots, 32))
+
+
+def test_many_rows():
+    """More (row, head) pairs than SMs, rows longer than the counts that one CTA holds: in place and elsewhere."""
+    lens = [(i * 7919) % 17000 for i in range(80)]
+    c = Case("e4m3", "dense", lens, 2, 16, 17000, seed=7)
+    want = c.expect(64, 1, 2)
+    _same(c.run(64, n_first=1, n_last=2), want)
+    k2, v2 = (torch.zeros(80, 2, 64, 16, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ids, new, *_ = c.run(64, n_first=1, n_last=2, k_out=k2, v_out=v2)
+    _same((ids, new), want[:2])
+    for b, n in enumerate(want[1].tolist()):
+        assert torch.equal(k2[b, :, :n].cpu(), want[2][b, :, :n]) and torch.equal(v2[b, :, :n].cpu(), want[3][b, :, :n])
 
 
 def test_bad_rows_stay():
