@@ -218,16 +218,6 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t (&p)[3])
     }
 }
 
-// Vector index of slot s of a unit of a paged cache, or -1.
-static __device__ __noinline__ long long paged_row(const int32_t *table, int block_size, int num_blocks, int Hkv, int kvh,
-                                                   int s)
-{
-    const int blk = __ldg(table + s / block_size);
-    if (blk < 0 || blk >= num_blocks)
-        return -1;
-    return ((long long)blk * Hkv + kvh) * block_size + s % block_size;
-}
-
 // The unit's query fragments. 8 bits: lane (g, t) holds row g's D / 4 dims from
 // D / 4 * t, scaled by a power of two into f16's range, and `mul` is the factor
 // that takes a product to a score over `scale`. bfloat16: the fragments of the
@@ -328,7 +318,9 @@ struct Fetch {
     uint32_t line;     // dense: vector of slot 0
     uint32_t block0;   // dense, 8 bits: block of slot 0
     uint64_t policy;   // cache policy of the vectors
-    int page, page_next;   // paged: the block of part lane % SUB of a tile, 32 / SUB tiles; of the tiles behind them
+    // paged, whole pages of 16 slots: the block of part lane % SUB of a tile, 32 /
+    // SUB tiles, and of the tiles behind them; else the block of slot lane of tile t
+    int page, page_next;
 };
 
 template <class F>
@@ -345,6 +337,14 @@ __device__ __forceinline__ int load_page(const ScoredParams &p, const Fetch &f, 
     const int x = tile + lane / F::SUB;
     const int s = share_slot<F>(x, c.tp, c.gap, warp) + 16 * (lane % F::SUB);
     return x <= f.t_last && s <= c.L ? __ldg(p.block_table + (long long)c.b * p.max_blocks + (s >> shift)) : 0;
+}
+
+// the block of the lane's slot of tile f.t
+template <class F>
+__device__ __forceinline__ int load_slot_page(const ScoredParams &p, const Fetch &f, const TileCursor &c, int warp, int lane)
+{
+    const int s = share_slot<F>(f.t, c.tp, c.gap, warp) + lane % F::SHARE;
+    return s <= c.L ? __ldg(p.block_table + (long long)c.b * p.max_blocks + s / p.block_size) : 0;
 }
 
 // The copies' segment becomes that of cursor c. The segment's query rows (rows
@@ -372,6 +372,8 @@ __device__ __forceinline__ void enter(const ScoredParams &p, const TileCursor &c
         if (f.good && pages) {
             f.page = load_page<F>(p, f, c, shift, f.t & ~(PER - 1), warp, lane);
             f.page_next = load_page<F>(p, f, c, shift, (f.t & ~(PER - 1)) + PER, warp, lane);
+        } else if (f.good) {
+            f.page = load_slot_page<F>(p, f, c, warp, lane);
         }
     } else if (f.good) {
         const int r = p.slot_ids ? __ldg(p.slot_ids + c.b) : c.b;
@@ -449,40 +451,38 @@ __device__ __forceinline__ void fetch_tile(const ScoredParams &p, const Fetch &f
         }
         return;
     }
-    // slot by slot: any block size; a slot outside the softmax becomes zeros
-    auto vector = [&](int j) -> long long {
-        if (!attended(c.L, c.lo, c.P, s + j))
-            return -1;
+    // any block size, and slots outside the softmax, which become zeros: a lane
+    // finds the vector of one slot, the copies take it from there
+    const int x = s + lane % F::SHARE;
+    uint32_t row = ~0u;
+    [[maybe_unused]] uint32_t block = 0;
+    if (attended(c.L, c.lo, c.P, x)) {
         if constexpr (PAGED) {
-            const long long r = paged_row(p.block_table + (long long)c.b * p.max_blocks, p.block_size, p.num_blocks,
-                                          p.Hkv, c.kvh, s + j);
-            if (r < 0)
+            const int blk = pages ? __ldg(p.block_table + (long long)c.b * p.max_blocks + (x >> shift)) : f.page;
+            if (blk < 0 || blk >= p.num_blocks) {
                 *bad = 1;
-            return r;
+            } else {
+                block = (uint32_t)blk * p.Hkv + c.kvh;
+                row = block * (uint32_t)p.block_size + (uint32_t)x % (uint32_t)p.block_size;
+            }
         } else {
-            return (long long)f.line + s + j;
+            row = f.line + (uint32_t)x;
+            if constexpr (F::I8)
+                block = f.block0 + (uint32_t)x / (uint32_t)p.scale_block;
         }
-    };
+    }
 #pragma unroll
     for (int j = 0; j < F::SHARE / F::VI; ++j) {
         const int r = F::VI * j + r0;
-        const long long x = vector(r);
-        const uint64_t at = x < 0 ? 0 : (uint64_t)x * F::VB + c0 * 16;
-        copy16(dk + piece<F::VB>(r, c0), kc + at, x < 0 ? 0 : 16);
-        copy16(dv + piece<F::VB>(r, c0), vc + at, x < 0 ? 0 : 16);
+        const uint32_t v = __shfl_sync(0xffffffffu, row, r);
+        const uint64_t at = v == ~0u ? 0 : (uint64_t)v * F::VB + c0 * 16;
+        copy16(dk + piece<F::VB>(r, c0), kc + at, v == ~0u ? 0 : 16);
+        copy16(dv + piece<F::VB>(r, c0), vc + at, v == ~0u ? 0 : 16);
     }
-    if constexpr (F::I8) {
-        const int j = lane;                // SHARE = 32 slots
-        const long long x = vector(j);
-        uint64_t at = 0;
-        if (x >= 0) {
-            if constexpr (PAGED)
-                at = (uint64_t)x / (uint32_t)p.block_size;
-            else
-                at = f.block0 + (uint32_t)(s + j) / (uint32_t)p.scale_block;
-        }
-        copy4(dks + 4 * j, p.k_block_scale + at, x < 0 ? 0 : 4);
-        copy4(dvs + 4 * j, p.v_block_scale + at, x < 0 ? 0 : 4);
+    if constexpr (F::I8) {                 // SHARE = 32 slots
+        const int n = row == ~0u ? 0 : 4;
+        copy4(dks + 4 * lane, p.k_block_scale + block, n);
+        copy4(dvs + 4 * lane, p.v_block_scale + block, n);
     }
 }
 
@@ -767,7 +767,9 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
                 ++f.t;
                 if constexpr (PAGED) {
                     constexpr int PER = 32 / SUB;
-                    if ((f.t & (PER - 1)) == 0 && f.good && pages) {
+                    if (f.good && !pages) {
+                        f.page = load_slot_page<F>(p, f, segs[sf].c, warp, lane);
+                    } else if ((f.t & (PER - 1)) == 0 && f.good) {
                         f.page = f.page_next;
                         f.page_next = load_page<F>(p, f, segs[sf].c, shift, f.t + PER, warp, lane);
                     }
