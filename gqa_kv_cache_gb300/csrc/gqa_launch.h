@@ -124,7 +124,7 @@ struct RotateParams {
     int32_t *status;
     float factor;
     int bf16, half, B, T, Hq, Hkv, D, dim;
-    int rest, units, tokens;         // set by rotate_launch
+    int rest, rest_gap, units, tokens;   // set by rotate_launch
 };
 cudaError_t rotate_launch(RotateParams p, int sms, cudaStream_t st);
 
