@@ -12,8 +12,8 @@
 //
 // Kept vectors are copied elsewhere by evict_gather_kernel, every 16 bytes on
 // their own, or within the cache by evict_compact_kernel. In place, kept slot i
-// comes from a slot >= i; a CTA takes a column of kSlice bytes of the vectors of
-// a (row, head), chunk by chunk of kChunk kept slots: the sources of a later
+// comes from a slot >= i; a CTA takes a column of 64 bytes of the vectors of
+// a (row, head), chunk by chunk of kBytes: the sources of a later
 // chunk lie behind the destinations of an earlier one, so copies into shared
 // memory may run kDeep chunks ahead of the stores as long as a chunk is stored
 // after it and those before it have come. Both are bound by memory: 2 rows of
@@ -472,15 +472,16 @@ __global__ void __launch_bounds__(kMove, 4) evict_gather_kernel(const EvictParam
 }
 
 constexpr int kDeep = 4;           // chunks on their way
-constexpr int kChunk = 256;        // kept slots a chunk
+constexpr int kBytes = 16384;      // of a chunk
 
 // Kept vectors within the cache: blockIdx.x a (unit, column of SLICE bytes), blockIdx.y K or V.
 template <int SLICE>
 __global__ void __launch_bounds__(kMove) evict_compact_kernel(const EvictParams p)
 {
     constexpr int PER = SLICE / 16;            // pieces a slot
-    constexpr int N = kChunk * PER / kMove;    // pieces a thread and chunk
-    __shared__ uint4 ring[kDeep][kChunk * PER];
+    constexpr int CHUNK = kBytes / SLICE;      // kept slots a chunk
+    constexpr int N = kBytes / 16 / kMove;     // pieces a thread and chunk
+    extern __shared__ uint4 ring[];            // [kDeep][kBytes / 16]
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int columns = p.row_bytes / SLICE;
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kMove) evict_compact_kernel(const EvictParams 
     const int n = p.new_lengths[b], tid = threadIdx.x;
     const Line line(p, b, h);
     const int32_t *ids = p.ids + (long long)unit * p.n_keep;
-    char *cache = static_cast<char *>(blockIdx.y ? p.v_cache : p.k_cache) + (blockIdx.x % columns) * SLICE;
+    char *cache = static_cast<char *>(blockIdx.y ? p.v_cache : p.k_cache) + (blockIdx.x % columns) * SLICE + tid % PER * 16;
     // the kept slots that stay where they are come first: chunks of them alone need no copy
     int c0 = 0;
     {
@@ -500,25 +501,45 @@ __global__ void __launch_bounds__(kMove) evict_compact_kernel(const EvictParams 
             else
                 hi = mid;
         }
-        c0 = lo / kChunk;
+        c0 = lo / CHUNK;
     }
-    const int chunks = (n + kChunk - 1) / kChunk;
+    const int chunks = (n + CHUNK - 1) / CHUNK;
+    if (c0 >= chunks)
+        return;
+    // where this thread's pieces of a chunk come from and go to, looked up a chunk ahead
+    const int first = tid / PER;               // its slot of a chunk; the others are kMove / PER apart
+    long long from[N], to[N];
+    auto sources = [&](int c) {
+        int j[N], blk[N] = {};
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            j[e] = __ldg(ids + min(c * CHUNK + first + e * (kMove / PER), n - 1));
+        line.look_up(j, blk);
+        line.place(j, blk, from);
+    };
+    auto places = [&](int c) {
+        int j[N], blk[N] = {};
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            j[e] = min(c * CHUNK + first + e * (kMove / PER), n - 1);
+        line.look_up(j, blk);
+        line.place(j, blk, to);
+    };
     auto fetch = [&](int c) {
         if (c < chunks) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const int x = e * kMove + tid, i = c * kChunk + x / PER;
-                if (i < n) {
-                    const char *src = cache + line.at(__ldg(ids + i)) * p.row_bytes + x % PER * 16;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                     static_cast<uint32_t>(__cvta_generic_to_shared(&ring[c % kDeep][x]))),
-                                 "l"(src)
+            for (int e = 0; e < N; ++e)
+                if (c * CHUNK + first + e * (kMove / PER) < n)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(
+                                     __cvta_generic_to_shared(ring + (c % kDeep) * (kBytes / 16) + e * kMove + tid))),
+                                 "l"(cache + from[e] * p.row_bytes)
                                  : "memory");
-                }
-            }
+            sources(min(c + 1, chunks - 1));
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    sources(c0);
+    places(c0);
     for (int c = c0; c < c0 + kDeep - 1; ++c)
         fetch(c);
     for (int c = c0; c < chunks; ++c) {
@@ -526,11 +547,10 @@ __global__ void __launch_bounds__(kMove) evict_compact_kernel(const EvictParams 
         asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
         __syncthreads();                       // every thread's copies of the chunk (and of those before) have come
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int x = e * kMove + tid, i = c * kChunk + x / PER;
-            if (i < n)
-                *reinterpret_cast<uint4 *>(cache + line.at(i) * p.row_bytes + x % PER * 16) = ring[c % kDeep][x];
-        }
+        for (int e = 0; e < N; ++e)
+            if (c * CHUNK + first + e * (kMove / PER) < n)
+                *reinterpret_cast<uint4 *>(cache + to[e] * p.row_bytes) = ring[(c % kDeep) * (kBytes / 16) + e * kMove + tid];
+        places(min(c + 1, chunks - 1));
         // a thread reads back what it copied itself, so the slot is free for its next copies
     }
 }
@@ -572,6 +592,9 @@ cudaError_t evict_launch(EvictParams p, int sms, cudaStream_t st)
             e = cudaFuncSetAttribute(evict_select_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, one);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(evict_select_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, wide);
+        for (auto *f : {evict_compact_kernel<16>, evict_compact_kernel<32>, evict_compact_kernel<64>})
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kDeep * kBytes);
         if (e != cudaSuccess)
             return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
@@ -610,9 +633,11 @@ cudaError_t evict_launch(EvictParams p, int sms, cudaStream_t st)
         cfg = config(dim3(units * (unsigned)p.shares), kMove, 0, st, attr);
         return cudaLaunchKernelEx(&cfg, evict_gather_kernel, p);
     }
-    // columns of 64 bytes, or of the largest power of two that divides the rows
+    // columns of 64 bytes (in place, 64 rows of up to 16384 slots of 8 x 256 bytes
+    // to 2048: 32 bytes 336 us, 64 288, 128 283; 4 rows of up to 131072 to 16384:
+    // 227, 178, 236), or of what divides the rows
     const int slice = p.row_bytes % 64 == 0 ? 64 : p.row_bytes % 32 == 0 ? 32 : 16;
-    cfg = config(dim3(units * (unsigned)(p.row_bytes / slice), 2), kMove, 0, st, attr);
+    cfg = config(dim3(units * (unsigned)(p.row_bytes / slice), 2), kMove, kDeep * kBytes, st, attr);
     return slice == 64   ? cudaLaunchKernelEx(&cfg, evict_compact_kernel<64>, p)
            : slice == 32 ? cudaLaunchKernelEx(&cfg, evict_compact_kernel<32>, p)
                          : cudaLaunchKernelEx(&cfg, evict_compact_kernel<16>, p);
