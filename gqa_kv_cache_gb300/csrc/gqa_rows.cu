@@ -631,15 +631,14 @@ __global__ void __launch_bounds__(kThreads, append_ctas<T>()) append8_kernel(con
             rows_report(p, kBadLength);
             continue;
         }
-        int t = max(a, t0);
-        int slot = (int)L + (t - a);
+        long long t = max(a, t0), slot = L + (t - a);   // (a block's end may lie behind 2^31)
         if (t > a && slot % sb) {                       // that run began earlier
             t += sb - slot % sb;
             slot += sb - slot % sb;
         }
         while (t < min(e, t0 + n)) {
-            const int m = min(sb - slot % sb, e - t);
-            runs[atomicAdd(&n_runs, 1)] = Run{t - t0, m, slot, b, 0};   // the order does not matter
+            const int m = (int)min((long long)sb - slot % sb, e - t);
+            runs[atomicAdd(&n_runs, 1)] = Run{(int)(t - t0), m, (int)slot, b, 0};   // the order does not matter
             t += m;
             slot += m;
         }
@@ -678,10 +677,11 @@ __global__ void __launch_bounds__(kThreads, append_ctas<T>()) append8_kernel(con
     const int heads = 2 * p.Hkv;                        // neighbours: K and V of a head
     // a lane's groups lie `far` elements apart where a step is whole vectors
     const bool even = shift >= 0 && step >= per;
-    const int first = even ? (lane >> shift) * row + (lane & (per - 1)) * kGroup : 0, far = even ? (step >> shift) * row : 0;
+    const long long first = even ? (long long)(lane >> shift) * row + (lane & (per - 1)) * kGroup : 0;
+    const long long far = even ? (long long)(step >> shift) * row : 0;
     auto from = [&](const T *src, int i) {
         if (even)
-            return src + first + (long long)i * far;
+            return src + first + i * far;
         const int at = lane + step * i, m = at / per;
         return src + (long long)m * row + (at - m * per) * kGroup;
     };
