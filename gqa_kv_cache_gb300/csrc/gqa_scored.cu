@@ -26,7 +26,8 @@ cudaError_t launch(int kind, int D, int G, bool more, bool q_bf16, bool paged, c
 constexpr int kCountThreads = 256, kCountSlots = 4;   // slots a thread
 
 // weights[slot] += sum over the rows of 2^(y - M) / den: the scores of a slot
-// are neighbours, 16 or 32 bytes. Bound by memory: 4 G + 8 bytes a slot.
+// are neighbours, 16 or 32 bytes. Bound by memory: 4 G + 8 bytes a slot (327k
+// slots of 8 heads, G = 8: 22 us for 105 MB, part of it from L2).
 template <int GP>
 __global__ void __launch_bounds__(kCountThreads) count_kernel(const ScoredParams p)
 {

@@ -36,8 +36,20 @@
 //  * counted weights: the scores go to a scratch array as they come (float32,
 //    G padded to 4 or 8 a slot), each row's maximum and denominator at the end of
 //    its unit, and a second kernel adds sum_g 2^(y_g - M_g) / den_g to the slot's
-//    count. (A second pass over the keys would read 2 D bytes a slot instead of
-//    8 G.)
+//    count. (A second pass over the keys would read D or 2 D bytes a slot
+//    instead of 8 G.) The scores ask to stay in L2, the vectors to leave it: four
+//    bfloat16 rows of 32768 .. 131071 slots, G = 8, 259 -> 247 us.
+// What bounds it. Over a bfloat16 cache the memory (64 rows of 512 .. 16383 slots
+// in 16-slot blocks, G = 6, capped: 329 us, 0.99 of the measured copy rate). Over
+// an 8-bit cache of D = 128 nearly so: four rows of 32768 .. 131071 slots, G = 4
+// 107 us (0.92), G = 8 110 (0.90; with a cap 124). There a warp issues 785
+// instructions for 32 slots (160 byte permutes, 136 f16 sums, 64 sign flips, 48
+// products), 0.52 a cycle with two warps a scheduler: dependent instructions
+// ("wait" 0.90 of an issue) and little else. D = 64 has the same instructions
+// around half the bytes (80 us for half the cache, 0.62). Short units are bound by
+// starts and ends: a segment's end costs a CTA about 2.5 us (256 rows of 16 ..
+// 8191 slots, 4 heads, G = 8: 78 us, of which the slots would take 56; a float32
+// query 83, with slopes 91).
 #pragma once
 
 #define GQA_MULTI_TOKEN 0   // single-token steps only
