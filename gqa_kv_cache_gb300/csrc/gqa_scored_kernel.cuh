@@ -33,6 +33,9 @@
 //  * the softmax keeps a reference below the running maximum, raised only when
 //    a score passes it by kRoom; sums of a tile start from zero and are added to
 //    the output in float32 (the matrix unit truncates its sums).
+//  * with slopes a segment's tiles go backwards: the largest biased scores stand
+//    at the row's end, and forwards steep heads raised their reference at every
+//    tile (256 rows of 16 .. 8191 slots, float32 query: 93 -> 86 us).
 //  * counted weights: the scores go to a scratch array as they come (float32,
 //    G padded to 4 or 8 a slot), each row's maximum and denominator at the end of
 //    its unit, and a second kernel adds sum_g 2^(y_g - M_g) / den_g to the slot's
@@ -88,18 +91,17 @@ struct Form {
 // Resident CTAs per SM, and tiles of a warp's ring. Measured on four rows of
 // 32768 .. 131071 slots: 8 bits, D = 128, G = 8 two CTAs of three tiles 109.9
 // us, three of two 114.5 (168 registers are too few); D = 64 three of three 80.0,
-// four of three 82.3, two of five 85.2. The rows of a float32 query of more than
-// four take 16 KB, which leaves room for two tiles.
+// four of three 82.3, two of five 85.2. Three places for query rows are enough
+// for the four segments, as a segment's rows are in registers before the copies
+// take their place: a fourth left a float32 query of a bfloat16 cache one CTA an
+// SM (64 paged rows, capped: 406 us for 331) and one of an 8-bit cache two tiles.
 template <int KIND, int D>
 constexpr int ctas()
 {
     return KIND == kI8 && D == 64 ? 3 : 2;
 }
-template <int KIND, int D, bool QF32, bool FEW>
-constexpr int stages()
-{
-    return KIND == kI8 && D == 128 && QF32 && !FEW ? 2 : 3;
-}
+constexpr int kStages = 3;
+constexpr int kQueries = kSegs - 1;
 
 // One tile's share of a warp in shared memory: vectors in slot order, their
 // 16-byte pieces permuted so that the operand loads below have no bank
@@ -326,6 +328,7 @@ constexpr int query_bytes()
 // What a warp's copies are taken from.
 struct Fetch {
     int t, t_last;     // (the rest of its segment is read from shared memory)
+    int turn;          // tiles backwards (see kernel): the sum of a tile's place and its number, else -1
     bool good;
     uint32_t line;     // dense: vector of slot 0
     uint32_t block0;   // dense, 8 bits: block of slot 0
@@ -341,6 +344,9 @@ __device__ __forceinline__ int share_slot(int t, int tp, int gap, int warp)
     return (t < tp ? t : t + gap) * F::TILE + warp * F::SHARE;
 }
 
+// The number of the segment's tile at place t.
+__device__ __forceinline__ int tile_at(int turn, int t) { return turn < 0 ? t : turn - t; }
+
 // lane's page of the 32 / SUB tiles from `tile`
 template <class F>
 __device__ __forceinline__ int load_page(const ScoredParams &p, const Fetch &f, const TileCursor &c, int shift, int tile,
@@ -348,21 +354,21 @@ __device__ __forceinline__ int load_page(const ScoredParams &p, const Fetch &f, 
 {
     const int x = tile + lane / F::SUB;
     const int s = share_slot<F>(x, c.tp, c.gap, warp) + 16 * (lane % F::SUB);
-    return x <= f.t_last && s <= c.L ? __ldg(p.block_table + (long long)c.b * p.max_blocks + (s >> shift)) : 0;
+    return x >= 0 && x <= f.t_last && s <= c.L ? __ldg(p.block_table + (long long)c.b * p.max_blocks + (s >> shift)) : 0;
 }
 
 // the block of the lane's slot of tile f.t
 template <class F>
 __device__ __forceinline__ int load_slot_page(const ScoredParams &p, const Fetch &f, const TileCursor &c, int warp, int lane)
 {
-    const int s = share_slot<F>(f.t, c.tp, c.gap, warp) + lane % F::SHARE;
+    const int s = share_slot<F>(tile_at(f.turn, f.t), c.tp, c.gap, warp) + lane % F::SHARE;
     return s <= c.L ? __ldg(p.block_table + (long long)c.b * p.max_blocks + s / p.block_size) : 0;
 }
 
 // The copies' segment becomes that of cursor c. The segment's query rows (rows
 // behind the G are zeros) are copied too, a part by each warp, in the group of
 // the copies that comes next.
-template <class F, int D, bool QF32, bool PAGED, bool FEW>
+template <class F, int D, bool QF32, bool PAGED, bool FEW, bool BACK>
 __device__ __forceinline__ void enter(const ScoredParams &p, const TileCursor &c, Fetch &f, Segment *seg, int *bad, void *q,
                                       int shift, bool pages, int warp, int lane)
 {
@@ -379,11 +385,13 @@ __device__ __forceinline__ void enter(const ScoredParams &p, const TileCursor &c
     }
     f.t = c.t;
     f.t_last = (int)min((long long)c.nr - 1, c.t + (c.end - c.g) - 1);
+    f.turn = BACK && p.slopes ? f.t + f.t_last : -1;
     f.good = row_ok(p, c.b, c.L);
     if constexpr (PAGED) {
         if (f.good && pages) {
-            f.page = load_page<F>(p, f, c, shift, f.t & ~(PER - 1), warp, lane);
-            f.page_next = load_page<F>(p, f, c, shift, (f.t & ~(PER - 1)) + PER, warp, lane);
+            const int group = tile_at(f.turn, f.t) & ~(PER - 1);
+            f.page = load_page<F>(p, f, c, shift, group, warp, lane);
+            f.page_next = load_page<F>(p, f, c, shift, f.turn < 0 ? group + PER : group - PER, warp, lane);
         } else if (f.good) {
             f.page = load_slot_page<F>(p, f, c, warp, lane);
         }
@@ -424,7 +432,7 @@ __device__ __forceinline__ void fetch_tile(const ScoredParams &p, const Fetch &f
     using F = Form<KIND, D>;
     if (!f.good)
         return;                            // its output is NaN, whatever is in the stage
-    const int s = share_slot<F>(f.t, c.tp, c.gap, warp);
+    const int tile = tile_at(f.turn, f.t), s = share_slot<F>(tile, c.tp, c.gap, warp);
     const uint32_t dk = smem_at(st.k), dv = smem_at(st.v);
     [[maybe_unused]] const uint32_t dks = smem_at(st.ks), dvs = smem_at(st.vs);
     const uint8_t *kc = static_cast<const uint8_t *>(p.k_cache), *vc = static_cast<const uint8_t *>(p.v_cache);
@@ -438,7 +446,7 @@ __device__ __forceinline__ void fetch_tile(const ScoredParams &p, const Fetch &f
             uint32_t row;
             [[maybe_unused]] uint32_t block = 0;
             if constexpr (PAGED) {
-                int blk = __shfl_sync(0xffffffffu, f.page, F::SUB * (f.t & (32 / F::SUB - 1)) + u);
+                int blk = __shfl_sync(0xffffffffu, f.page, F::SUB * (tile & (32 / F::SUB - 1)) + u);
                 if (blk < 0 || blk >= p.num_blocks) {
                     *bad = 1;
                     blk = 0;               // read something: the unit's output is NaN
@@ -719,12 +727,12 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
     using F = Form<KIND, D>;
     using St = Stage<KIND, D>;
     constexpr bool I8 = F::I8;
-    constexpr int SUB = F::SUB, STAGES = stages<KIND, D, QF32, FEW>(), SHARE = F::SHARE;
+    constexpr int SUB = F::SUB, STAGES = kStages, SHARE = F::SHARE;
     constexpr int C = FEW ? 1 : 2;             // query rows of a lane: t4, or 2t4 and 2t4 + 1
     constexpr int PARTS = !QF32 ? 1 : !I8 ? 3 : FEW ? 1 : 2;
     extern __shared__ __align__(128) unsigned char dyn[];
     St(*ring)[kWarps] = reinterpret_cast<St(*)[kWarps]>(dyn);      // [STAGES]
-    auto sm_q = reinterpret_cast<uint8_t(*)[query_bytes<D, QF32, FEW>()]>(dyn + STAGES * kWarps * sizeof(St));   // [kSegs]
+    auto sm_q = reinterpret_cast<uint8_t(*)[query_bytes<D, QF32, FEW>()]>(dyn + STAGES * kWarps * sizeof(St));   // [kQueries]
     __shared__ long long sched[kThreads / 32 + 8];
     __shared__ TileWalk walk;
     __shared__ Segment segs[kSegs];            // every warp writes the same
@@ -754,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
         else
             asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(f.policy));
     }
-    int sf = 0;
+    int sf = 0, qf_at = 0;                 // and its query rows' place
     bool in_b = false, left;
     {
         TileCursor c;
@@ -769,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
             if (!left)
                 return;
         }
-        enter<F, D, QF32, PAGED, FEW>(p, c, f, &segs[0], &sm_bad[warp][0], sm_q[0], shift, pages, warp, lane);
+        enter<F, D, QF32, PAGED, FEW, MORE>(p, c, f, &segs[0], &sm_bad[warp][0], sm_q[0], shift, pages, warp, lane);
         __syncwarp();
     }
     auto fetch = [&](int slot) {
@@ -779,11 +787,12 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
                 ++f.t;
                 if constexpr (PAGED) {
                     constexpr int PER = 32 / SUB;
+                    const int tile = tile_at(f.turn, f.t);
                     if (f.good && !pages) {
                         f.page = load_slot_page<F>(p, f, segs[sf].c, warp, lane);
-                    } else if ((f.t & (PER - 1)) == 0 && f.good) {
+                    } else if ((tile & (PER - 1)) == (f.turn < 0 ? 0 : PER - 1) && f.good) {
                         f.page = f.page_next;
-                        f.page_next = load_page<F>(p, f, segs[sf].c, shift, f.t + PER, warp, lane);
+                        f.page_next = load_page<F>(p, f, segs[sf].c, shift, f.turn < 0 ? tile + PER : tile - 2 * PER + 1, warp, lane);
                     }
                 }
             } else {
@@ -793,7 +802,8 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
                 left = !p.whole_units && walk_next(p, c, walk, in_b);
                 if (left) {
                     sf = (sf + 1) % kSegs;
-                    enter<F, D, QF32, PAGED, FEW>(p, c, f, &segs[sf], &sm_bad[warp][sf], sm_q[sf], shift, pages, warp, lane);
+                    qf_at = qf_at == kQueries - 1 ? 0 : qf_at + 1;
+                    enter<F, D, QF32, PAGED, FEW, MORE>(p, c, f, &segs[sf], &sm_bad[warp][sf], sm_q[qf_at], shift, pages, warp, lane);
                     __syncwarp();
                 }
             }
@@ -821,14 +831,15 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
     [[maybe_unused]] float slope[C];
     float m[C], l[C];                      // reference and sum of the lane's rows
     float o[D / 16][FEW ? 2 : 4];
-    for (int sc = 0;; sc = (sc + 1) % kSegs) {
+    for (int sc = 0, q_at = 0;; sc = (sc + 1) % kSegs, q_at = q_at == kQueries - 1 ? 0 : q_at + 1) {
         // the next segment
         const Segment *seg = &segs[sc];
         const bool good = seg->good;
         if (!good && tid == 0 && seg->c.t == 0 && seg->c.kvh == 0)
             report(p, row_error_bits(p, seg->c.b, seg->c.L));
         float mine;
-        load_query<KIND, D, QF32, FEW, PARTS>(MORE && p.cap > 0.f ? p.scale_cap : p.scale_log2, sm_q[sc], lane, qf, mine);
+        load_query<KIND, D, QF32, FEW, PARTS>(MORE && p.cap > 0.f ? p.scale_cap : p.scale_log2, sm_q[q_at], lane, qf, mine);
+        __syncthreads();                   // the copies that run ahead may take the rows' place
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             [[maybe_unused]] const int row = C * t4 + c;
@@ -863,7 +874,8 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
                 scores<KIND, D, QF32, FEW, PARTS>(st, u, lane, qf, s[u], over);
             // bits 2 u + i: slot 16 u + g + 8 i is in the softmax
             unsigned ok = good ? ~0u : 0u;
-            const int s0 = share_slot<F>(t, seg->c.tp, seg->c.gap, warp), L = seg->c.L, lo = seg->c.lo, P = seg->c.P;
+            const int tile = tile_at(MORE && p.slopes ? seg->c.t + seg->t_last : -1, t);
+            const int s0 = share_slot<F>(tile, seg->c.tp, seg->c.gap, warp), L = seg->c.L, lo = seg->c.lo, P = seg->c.P;
             if (s0 + SHARE - 1 > L || (s0 < lo && s0 + SHARE - 1 >= P)) {
 #pragma unroll
                 for (int u = 0; u < SUB; ++u)
@@ -1054,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
 template <int KIND, int D, bool QF32, bool FEW>
 constexpr int dyn_bytes()
 {
-    return kWarps * stages<KIND, D, QF32, FEW>() * (int)sizeof(Stage<KIND, D>) + kSegs * query_bytes<D, QF32, FEW>();
+    return kWarps * kStages * (int)sizeof(Stage<KIND, D>) + kQueries * query_bytes<D, QF32, FEW>();
 }
 
 template <int KIND, int D, bool QF32, bool PAGED, bool FEW, bool MORE>

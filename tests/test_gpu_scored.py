@@ -190,6 +190,24 @@ def test_long_rows_and_many_pieces():
     c.check(c.attend(weights=weights, grid_ctas=700), c.expect(), weights, base)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("layout,bs", [("paged", 16), ("paged", 24), ("paged", 64), ("slots", 16)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_slopes_over_long_rows(kind, layout, bs, sign):
+    """Rows of many tiles and pages with steep and flat slopes of either sign, whole and in pieces."""
+    lens = [9000, 4097, 300, 6001]
+    c = Case(kind, layout, lens, 1, 6, 128, -(-9024 // bs) * bs, bs, torch.float32, seed=11)
+    slopes = sign * torch.exp2(-torch.tensor([0.5, 2.0, 4.0, 7.0, 10.0, 14.0]))
+    base = torch.zeros(c.shape)
+    for kw in (dict(), dict(window=3000, prefix=70)):
+        want = c.expect(slopes=slopes, **kw)
+        for grid in (0, 3, 61):
+            weights = base.cuda()
+            out = c.attend(head_slopes=slopes.cuda(), weights=weights, grid_ctas=grid, window=kw.get("window", 0),
+                           kept_prefix=kw.get("prefix", 0))
+            c.check(out, want, weights, base)
+
+
 def test_bad_rows():
     c = Case("bf16", "paged", [40, 40, 40], 2, 2, 64, 64, seed=10)
     c.table[1, 1] = -1
