@@ -52,7 +52,7 @@
 // around half the bytes (80 us for half the cache, 0.62). Short units are bound by
 // starts and ends: a segment's end costs a CTA about 2.5 us (256 rows of 16 ..
 // 8191 slots, 4 heads, G = 8: 78 us, of which the slots would take 56; a float32
-// query 83, with slopes 91).
+// query 82, with slopes 86).
 #pragma once
 
 #define GQA_MULTI_TOKEN 0   // single-token steps only
@@ -80,7 +80,7 @@ template <int KIND, int D>
 struct Form {
     static constexpr bool I8 = KIND == kI8;
     static constexpr int VB = I8 ? D : 2 * D;             // bytes a vector
-        static constexpr int SUB = VB == 256 ? 1 : 2;         // 16-slot parts of a warp's share of a tile
+    static constexpr int SUB = VB == 256 ? 1 : 2;         // 16-slot parts of a warp's share of a tile
     static constexpr int SHARE = 16 * SUB;                // a warp's slots of a tile
     static constexpr int TILE = kWarps * SHARE;           // slots a tile
     static constexpr int LV = VB / 16;                    // lanes (16-byte pieces) a vector
