@@ -59,6 +59,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <cfloat>
 
 #include "gqa_common.cuh"
 #include "gqa_launch.h"
@@ -73,6 +74,7 @@ constexpr int kFew = 4;                       // and of the form for few
 constexpr int kSegs = 4;                      // segments a warp's copies and products are in at once
 constexpr float kLift = 10.f;                 // a reference is set this far below the maximum ...
 constexpr float kRoom = 12.f;                 // ... and holds until a score is this far above it
+constexpr float kNone = -FLT_MAX;             // the first one: a score equals it or is 2^100 above, or is -inf, whose weight is 0
 constexpr float kOver = 8.f;                  // value scales reach this times their reference
 constexpr float kRest = 4096.f;               // a weight's remainder enters the products this much larger
 
@@ -846,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
             mul[c] = I8 ? __shfl_sync(0xffffffffu, mine, 8 * t4 + 4 * c) : mine;
             if constexpr (MORE)
                 slope[c] = p.slopes && row < p.G ? __ldg(p.slopes + seg->c.kvh * p.G + row) * 1.4426950408889634f : 0.f;
-            m[c] = -INFINITY;
+            m[c] = kNone;
             l[c] = 0.f;
         }
 #pragma unroll
@@ -960,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
                     for (int q = 4; q < 32; q <<= 1)
                         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, q));
                     const float n = most - m[c] > kRoom ? most - kLift : m[c];
-                    r[c] = m[c] == -INFINITY ? 0.f : fast_ex2(m[c] - n);
+                    r[c] = fast_ex2(m[c] - n);
                     m[c] = n;
                     l[c] *= r[c];
                 }
@@ -1013,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
             for (int q = 4; q < 32; q <<= 1)
                 l[c] += __shfl_xor_sync(0xffffffffu, l[c], q);
             // a NaN score raises no reference: keep the NaN sum in the merge
-            m[c] = (l[c] != l[c] && m[c] == -INFINITY) ? 0.f : m[c];
+            m[c] = l[c] == 0.f ? -INFINITY : l[c] != l[c] && m[c] == kNone ? 0.f : m[c];
             if (g == 0) {
                 sm_m[warp][C * t4 + c] = m[c];
                 sm_l[warp][C * t4 + c] = l[c];

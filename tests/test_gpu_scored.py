@@ -133,6 +133,31 @@ def test_masked_places_may_hold_anything(kind):
     c.check(c.attend(score_cap=10.0, window=19, weights=weights), want, weights, base)
 
 
+@pytest.mark.parametrize("layout,bs", [("dense", 16), ("paged", 24)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("where", [slice(0, 300), slice(170, 600), slice(500, 699)])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_slots_masked_by_keys_of_minus_infinity(layout, bs, D, where, slopes):
+    # scores of minus infinity: those slots weigh nothing, tiles full of them too
+    n, G = 700, 4
+    c = Case("bf16", layout, [n], 2, G, D, 720, bs=bs, seed=31)
+    c.q[..., 0] = c.q[..., 0].abs() + 0.25
+    ok = torch.ones(n, dtype=torch.bool)
+    ok[where] = False
+    k = R.row_slots(c.kv[0], 0, n, c.table, None, bs).clone()
+    k[:, ~ok, 0] = -math.inf
+    R.put_row(c.kv[0], 0, n, k, c.table, None, bs)
+    c.g[0].copy_(c.kv[0])
+    sl = 0.05 * torch.randn(2 * G, generator=c.gen) if slopes else None
+    o, w, e = R.attention(c.q[0].double().view(2, G, D), k.double(), c.row(1, 0, n), 0.0,
+                          None if sl is None else sl.view(2, G), ok)
+    weights = torch.zeros(*c.shape, device="cuda")
+    out = c.attend(weights=weights, **({} if sl is None else dict(head_slopes=sl.cuda())))
+    vmax = float(c.row(1, 0, n).abs().max())
+    c.check(out, [(o.reshape(-1, D), R.out_tolerance(w, e, vmax), w.sum(1), R.count_tolerance(w, e))], weights,
+            torch.zeros(*c.shape))
+
+
 def test_scores_that_are_not_finite():
     """A NaN key gives its row NaN and no other; -inf scores count as nothing."""
     c = Case("bf16", "dense", [40, 40], 1, 2, 64, 48, seed=5)
