@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const ScoredParams
                 if (4 * k + g < p.G)
                     sum += fast_ex2(y[g] - M[4 * k + g]) * inv[4 * k + g];
         }
-        p.weights[at] += sum;
+        atomicAdd(p.weights + at, sum);        // rows may share a block; a slot of one row has one writer
     }
 }
 

@@ -218,9 +218,10 @@ typedef struct gqa_options {
                                         softmax weights, summed over the G queries of its
                                         head, are ADDED to its count; other counts are left.
                                         A row with a bad block gets NaN counts in its usable
-                                        blocks, any other bad row none. Two rows of the batch
-                                        that share a cache row or block are undefined here;
-                                        rows of at most 2^30 slots                      */
+                                        blocks, any other bad row none. Rows of the batch that
+                                        share a cache row or block all add to its counts (the
+                                        order, so the last bit, may then differ from call to
+                                        call); rows of at most 2^30 slots               */
     void *weights_scratch;           /* (device) with weights: gqa_weights_scratch_bytes(...)
                                         bytes, 16-byte aligned, contents free before and
                                         after the call; one call at a time              */

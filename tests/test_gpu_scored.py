@@ -233,6 +233,25 @@ def test_slopes_over_long_rows(kind, layout, bs, sign):
             c.check(out, want, weights, base)
 
 
+def test_rows_that_share_blocks_all_count():
+    # three rows with the first 8 blocks in common, as after a common prompt
+    lens = [150, 163, 200]
+    c = Case("bf16", "paged", lens, 2, 4, 64, 208, seed=41)
+    c.table[:, :8] = c.table[0, :8]
+    want = c.expect()
+    weights = torch.zeros(c.shape, device="cuda")
+    out = c.attend(weights=weights)
+    c.check(out, want)
+    got = weights.cpu().double()
+    total, bound = torch.zeros(c.shape, dtype=torch.float64), torch.zeros(c.shape, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        for j in range(-(-n // 16)):
+            m = min(16, n - 16 * j)
+            total[int(c.table[b, j]), :, :m] += want[b][2][:, 16 * j:16 * j + m]
+            bound[int(c.table[b, j]), :, :m] += want[b][3][:, 16 * j:16 * j + m]
+    assert ((got - total).abs() <= bound + 3 * 2.0 ** -24 * total).all()
+
+
 def test_bad_rows():
     c = Case("bf16", "paged", [40, 40, 40], 2, 2, 64, 64, seed=10)
     c.table[1, 1] = -1
