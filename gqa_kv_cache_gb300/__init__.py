@@ -1150,7 +1150,8 @@ def rotate(q, k, rotary, positions=None, *, lengths=None, cu_q=None, q_out=None,
     ``lengths`` and ``cu_q`` as in :func:`append`, token t of row b is at
     lengths[b] + t - cu_q[b] (tokens of no row are not turned). The tensors may be
     views whose last axis is contiguous (parts of one projection); ``q_out`` and
-    ``k_out`` may be ``q`` and ``k`` (in place). Returns (q_out, k_out)."""
+    ``k_out`` may be ``q`` and ``k`` (in place; tensors that overlap otherwise are
+    undefined). Returns (q_out, k_out)."""
     one = q if q is not None else k
     if one is None:
         raise ValueError("q or k must be given")
@@ -1219,6 +1220,8 @@ def _turned(name, t, out, T, D, dt, dev):
             raise ValueError(f"{name}_out must be like {name}")
         if out.stride(2) != 1 and t.numel():
             raise ValueError(f"the last axis of {name}_out must be contiguous")
+        if (T > 1 and out.stride(0) == 0) or (shape[1] > 1 and out.stride(1) == 0):
+            raise ValueError(f"the tokens and heads of {name}_out must not share memory")
     return shape[1], t.data_ptr(), by
 
 
@@ -1288,8 +1291,9 @@ def evict(k_cache, v_cache, weights, lengths, n_keep, slot_ids=None, *, n_first=
     largest counts (``weights``, as :func:`attend` adds them up; equal ones: the
     lowest slot) move together in ascending order, in place, or into ``k_out``,
     ``v_out`` (B, Hkv, slots, D) and ``weights_out``, the cache then only being
-    read. Keys keep the positions that were turned into them. Returns the kept
-    slots (B, Hkv, n_keep) int32 (then -1) and the new lengths (B,)."""
+    read; rows that share a cache row or blocks need such outputs. Keys keep the
+    positions that were turned into them. Returns the kept slots (B, Hkv, n_keep)
+    int32 (then -1) and the new lengths (B,)."""
     return _evict(k_cache, v_cache, None, weights, lengths, n_keep, slot_ids, n_first, n_last, k_out, v_out,
                   weights_out, status, stream)
 

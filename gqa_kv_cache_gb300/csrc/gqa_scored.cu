@@ -27,7 +27,8 @@ constexpr int kCountThreads = 256, kCountSlots = 4;   // slots a thread
 
 // weights[slot] += sum over the rows of 2^(y - M) / den: the scores of a slot
 // are neighbours, 16 or 32 bytes. Bound by memory: 4 G + 8 bytes a slot (327k
-// slots of 8 heads, G = 8: 22 us for 105 MB, part of it from L2).
+// slots of 8 heads, G = 8: 105 MB, part of it from L2). Added in L2, which lets
+// rows share blocks and spares a load (attend and counts 244 -> 239 us).
 template <int GP>
 __global__ void __launch_bounds__(kCountThreads) count_kernel(const ScoredParams p)
 {

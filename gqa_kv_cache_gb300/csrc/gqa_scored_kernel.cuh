@@ -41,7 +41,7 @@
 //    its unit, and a second kernel adds sum_g 2^(y_g - M_g) / den_g to the slot's
 //    count. (A second pass over the keys would read D or 2 D bytes a slot
 //    instead of 8 G.) The scores ask to stay in L2, the vectors to leave it: four
-//    bfloat16 rows of 32768 .. 131071 slots, G = 8, 259 -> 247 us.
+//    bfloat16 rows of 32768 .. 131071 slots, G = 8, 259 -> 247 us (now 239).
 // What bounds it. Over a bfloat16 cache the memory (64 rows of 512 .. 16383 slots
 // in 16-slot blocks, G = 6, capped: 329 us, 0.99 of the measured copy rate). Over
 // an 8-bit cache of D = 128 nearly so: four rows of 32768 .. 131071 slots, G = 4

@@ -115,6 +115,16 @@ def test_empty():
     assert a.shape == (0, 2, 64)
 
 
+def test_an_output_whose_tokens_or_heads_share_memory_is_refused():
+    q = torch.zeros(4, 2, 64, device="cuda")
+    pos, rot = torch.zeros(4, dtype=torch.int32, device="cuda"), gqa.Rotary(64)
+    for out in (q[:1].expand(4, 2, 64), q[:, :1].expand(4, 2, 64)):
+        with pytest.raises(ValueError):
+            gqa.rotate(q, None, rot, pos, q_out=out)
+    got = gqa.rotate(q[:1, :1].expand(4, 2, 64), None, rot, pos)[0]     # inputs may
+    assert got.shape == q.shape and not got.any()
+
+
 def test_refusals():
     q, k = torch.zeros(4, 2, 64, device="cuda"), torch.zeros(4, 1, 64, device="cuda")
     pos = torch.zeros(4, dtype=torch.int32, device="cuda")
