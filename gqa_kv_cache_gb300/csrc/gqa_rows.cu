@@ -599,13 +599,15 @@ __device__ __forceinline__ uint32_t fewer4(uint32_t u, float f)
 
 // One CTA: the runs that begin among its `chunk` tokens, to their ends. The
 // threads look at the rows (ONE: at the tokens), a row's thread notes the runs
-// that it begins here, then a thread a run finds its block.
+// that it begins here, then a thread a run finds its block. Rows whose offsets
+// are in order begin at most a run a token; those that fall and rise again may
+// name a token many times: runs that find no place are left out and reported.
 template <typename T, bool ONE>
 __global__ void __launch_bounds__(kThreads, append_ctas<T>()) append8_kernel(const RowsParams p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     Run *runs = reinterpret_cast<Run *>(smem);          // [chunk]
-    __shared__ int n_runs;
+    __shared__ unsigned n_runs;                         // (at most chunk + B)
     __shared__ float tops[2][kThreads / 32];
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * p.chunk;
@@ -638,13 +640,19 @@ __global__ void __launch_bounds__(kThreads, append_ctas<T>()) append8_kernel(con
         }
         while (t < min(e, t0 + n)) {
             const int m = (int)min((long long)sb - slot % sb, e - t);
-            runs[atomicAdd(&n_runs, 1)] = Run{(int)(t - t0), m, (int)slot, b, 0};   // the order does not matter
+            const unsigned place = atomicAdd(&n_runs, 1u);   // the order does not matter
+            if (place >= (unsigned)p.chunk) {
+                rows_report(p, kBadQLen);
+                break;
+            }
+            runs[place] = Run{(int)(t - t0), m, (int)slot, b, 0};
             t += m;
             slot += m;
         }
     }
     __syncthreads();
-    for (int i = tid; i < n_runs; i += kThreads) {
+    const int count = (int)min(n_runs, (unsigned)p.chunk);
+    for (int i = tid; i < count; i += kThreads) {
         const int b = (int)runs[i].off, slot = runs[i].slot;
         long long off = kSkip, scale = 0;
         if (p.paged) {
@@ -686,11 +694,11 @@ __global__ void __launch_bounds__(kThreads, append_ctas<T>()) append8_kernel(con
         return src + (long long)m * row + (at - m * per) * kGroup;
     };
     int turn = 0, r = 0, hv = team;
-    while (hv >= heads && r < n_runs) {
+    while (hv >= heads && r < count) {
         hv -= heads;
         ++r;
     }
-    while (r < n_runs) {
+    while (r < count) {
         const Run run = runs[r];
         const int h = hv >> 1;
         const bool val = hv & 1;

@@ -162,6 +162,39 @@ def test_bad_rows_write_nothing():
     c.same()
 
 
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cu,T", [([0, 5, 3, 8], 8), ([0, 8, 8, 7], 8), ([0, 4, -1, 8], 8), ([0, 10] * 24 + [0], 10),
+                                  ([0, 5000] * 160, 5000), ([0, 700, 0, 700, 20, 5000] * 40, 5000),
+                                  ([0] + [5000, 4990] * 300, 5000)])
+def test_decreasing_offsets_are_reported(cu, T, paged, dtype):
+    """Rows whose offsets fall and rise again name more runs than there are tokens: reported, and nothing but
+    the rows' own slots is written."""
+    B, bs, S = len(cu) - 1, 16, 5008
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, 2, 16, generator=g).to(dtype).cuda()
+    spare = 2 * (S // bs) if paged else 2
+    # all rows in the same cache row (what they write there is undefined), the others must stay as they are
+    codes = [torch.full((spare, 2, bs, 16) if paged else (spare, 2, S, 16), 77, dtype=torch.int8, device="cuda")
+             for _ in range(2)]
+    scales = [torch.full((spare, 2) if paged else (spare, 2, S // bs), 3.0, device="cuda") for _ in range(2)]
+    kw = dict(k_block_scale=scales[0], v_block_scale=scales[1])
+    at = [torch.zeros(B, dtype=torch.int32, device="cuda"), torch.tensor(cu, dtype=torch.int32, device="cuda")]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if paged:
+        table = torch.arange(S // bs, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+        gqa.append_paged(x, x, *codes, table, *at, status=status, **kw)
+    else:
+        gqa.append(x, x, *codes, *at, torch.zeros(B, dtype=torch.int32, device="cuda"), status=status, **kw)
+    assert int(status) == 32
+    half = spare // 2
+    blocks = -(-T // bs)
+    for c, s in zip(codes, scales):
+        assert (c[half:] == 77).all() and (s[half:] == 3).all()
+        assert ((c[blocks:half] == 77).all() and (s[blocks:half] == 3).all()) if paged else \
+            ((c[0, :, blocks * bs:] == 77).all() and (s[0, :, blocks:] == 3).all())
+
+
 # ---- attention ----
 
 def _expect(c, q, n, window=0, prefix=0, sink=None):
