@@ -50,6 +50,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import threading
 
 import torch
 
@@ -200,18 +201,25 @@ def _workspace(device, nbytes, stream=None):
     return buf
 
 
-_scratch_cache: dict = {}
+class _Scratch(threading.local):
+    def __init__(self):
+        self.of: dict = {}
+
+
+_scratch_cache = _Scratch()
 
 
 def _scratch(device, nbytes, stream=None):
     """Scratch whose contents are free before and after a call: kept for the
-    device and stream up to 16 MB, else (and in a capture) the call's own."""
+    thread, device and stream up to 16 MB, else (and in a capture) the call's
+    own. A call may launch several kernels that hand it on: two threads that
+    shared it could put theirs between each other's on one stream."""
     if nbytes <= 1 << 24 and stream is None and not torch.cuda.is_current_stream_capturing():
         handle = _stream(None, device)
         key = (device, handle) if handle else device
-        buf = _scratch_cache.get(key)
+        buf = _scratch_cache.of.get(key)
         if buf is None or buf.numel() < nbytes:
-            buf = _scratch_cache[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+            buf = _scratch_cache.of[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
         return buf
     with torch.cuda.stream(stream) if stream is not None else _HERE:
         return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)

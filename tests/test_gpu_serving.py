@@ -144,6 +144,38 @@ def test_two_graphs_side_by_side():
             assert torch.equal(out, want) and torch.equal(w, once)
 
 
+def test_two_threads_count_on_one_stream():
+    """Counted attends of two threads, on the default stream of both: each has the counts it has alone."""
+    import threading
+    jobs = []
+    for seed in range(2):
+        g = torch.Generator().manual_seed(seed)
+        q = torch.randn(B, Hq, D, generator=g).cuda()
+        k, v = (torch.randn(B, Hkv, 1024, D, generator=g).bfloat16().cuda() for _ in range(2))
+        n = torch.tensor([1024, 17, 300], dtype=torch.int32).cuda()
+        once = torch.zeros(B, Hkv, 1024, device="cuda")
+        out = gqa.attend(q, k, v, n, weights=once)
+        jobs.append((q, k, v, n, once, out))
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def run(i):
+        q, k, v, n, once, _ = jobs[i]
+        for _ in range(300):
+            w = torch.zeros_like(once)
+            got[i].append((gqa.attend(q, k, v, n, weights=w), w))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for (*_, once, out), runs in zip(jobs, got):
+        assert len(runs) == 300
+        assert all(torch.equal(w, once) and torch.equal(o, out) for o, w in runs)
+
+
 def test_runs_give_the_same_bits():
     state, run = _steps()
     start = {n: state[n].clone() for n in ("k8", "v8", "ks", "vs", "w", "kb", "vb")}

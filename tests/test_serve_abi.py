@@ -149,3 +149,27 @@ def test_rotary_tables_on_the_host():
                 dict(dim=64, scaling=dict(kind="bands", factor=2.0, original=64, low=4.0, high=4.0))):
         with pytest.raises(ValueError):
             gqa.Rotary(bad.pop("dim"), device="cpu", **bad)
+
+
+def test_threads_have_scratch_of_their_own(monkeypatch):
+    """A counted call's kernels hand scores on through the scratch: two threads on one stream must not share it."""
+    import threading
+
+    import gqa_kv_cache_gb300 as gqa
+    monkeypatch.setattr(gqa, "_stream", lambda stream, device=None: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    device, got, meet = torch.device("cpu"), [], threading.Barrier(2)
+
+    def call():
+        got.append((gqa._scratch(device, 1000), gqa._scratch(device, 2000)))
+        meet.wait(30)                    # this call is still under way when the other thread's begins
+
+    first, second = (threading.Thread(target=call) for _ in range(2))
+    first.start()
+    while not got and first.is_alive():
+        pass
+    second.start()
+    first.join()
+    second.join()
+    (a, b), (c, d) = got
+    assert a is b and c is d and a.data_ptr() != c.data_ptr()
