@@ -49,6 +49,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import decimal
 import math
 import threading
 
@@ -1106,6 +1107,36 @@ def attend_selected(q, k_cache, v_cache, selection, *, out=None, status=None, ke
 
 # ---- rotary positions and eviction ----
 
+_PI = "3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803"
+
+
+def _turns(dim, base, kind, k):
+    """The frequencies of :class:`Rotary` as fractions of a turn a position, in
+    units of 2 ** -64, rounded once: a position of 31 bits multiplies their
+    error, which 64-bit floats would leave at 2 ** -56 of a turn."""
+    with decimal.localcontext() as c:
+        c.prec, c.Emax, c.Emin = 80, decimal.MAX_EMAX, decimal.MIN_EMIN
+        base, two_pi, turn = decimal.Decimal(base), 2 * decimal.Decimal(_PI), decimal.Decimal(2 ** 64)
+        k = {n: decimal.Decimal(v) for n, v in k.items()}
+        s = k.get("factor", decimal.Decimal(1))
+        if kind == "ntk":
+            base *= s ** (decimal.Decimal(dim) / (dim - 2))
+        out, power, ratio = [], decimal.Decimal(1), base ** (decimal.Decimal(-2) / dim)
+        for _ in range(dim // 2):
+            f, power = power, power * ratio
+            if kind == "linear":
+                f /= s
+            elif kind == "bands":
+                u = (k["original"] * f / two_pi - k["low"]) / (k["high"] - k["low"])
+                u = min(max(u, decimal.Decimal(0)), decimal.Decimal(1))
+                f *= u + (1 - u) / s
+            f /= two_pi
+            if f.adjusted() > 40:
+                raise ValueError("a frequency is too high")
+            out.append(int((f % 1 * turn).to_integral_value()) % 2 ** 64)
+        return out
+
+
 class Rotary:
     """Angles of rotary positions over the first ``dim`` elements of a head:
     pair i turns by position * f_i, f_i = base ** (-2 i / dim). ``layout``:
@@ -1129,26 +1160,17 @@ class Rotary:
         if not (base > 0 and math.isfinite(base)):
             raise ValueError("base must be positive")
         k = dict(scaling or {})
-        kind = k.pop("kind", None)
+        kind, base = k.pop("kind", None), float(base)
         names = {None: (), "linear": ("factor",), "ntk": ("factor",),
                  "bands": ("factor", "original", "low", "high", "attention")}
         if kind not in names or not set(k) <= set(names[kind]) or not set(names[kind]) - {"attention"} <= set(k):
             raise ValueError("scaling must be None or a dict with kind 'linear', 'ntk' or 'bands' and its values")
+        k = {n: float(v) for n, v in k.items()}
         if any(not (v > 0 and math.isfinite(v)) for v in k.values()) or (kind == "bands" and k["high"] <= k["low"]) \
                 or (kind == "ntk" and dim == 2):
             raise ValueError("scaling values must be positive, high above low (and dim above 2 for 'ntk')")
         self.dim, self.layout, self.factor = dim, layout, float(k.get("attention", 1.0))
-        s = k.get("factor", 1.0)
-        freqs = []
-        for i in range(dim // 2):
-            f = (base * s ** (dim / (dim - 2)) if kind == "ntk" else base) ** (-2 * i / dim)
-            if kind == "linear":
-                f /= s
-            elif kind == "bands":
-                u = min(1.0, max(0.0, (k["original"] * f / (2 * math.pi) - k["low"]) / (k["high"] - k["low"])))
-                f *= u + (1 - u) / s
-            t = round(math.fmod(f / (2 * math.pi), 1.0) * 2 ** 64) % 2 ** 64   # of a turn
-            freqs.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+        freqs = [t - 2 ** 64 if t >= 2 ** 63 else t for t in _turns(dim, base, kind, k)]
         self.freqs = torch.tensor(freqs, dtype=torch.int64, device=device)
 
 

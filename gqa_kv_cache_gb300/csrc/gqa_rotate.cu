@@ -4,11 +4,13 @@
 // (2 i, 2 i + 1).
 //
 // Angles. f_i is given as a fraction of a turn in 64-bit fixed point
-// (f_i / 2 pi 2^64), so pos f_i mod a turn is the wrapped integer product: exact
-// for every int32 position, without 64-bit floating point (which this GPU has
-// little of). The nearest quarter turn is taken off in integers, and cos and
-// sin of the rest (|a| <= pi / 4, a 30-bit integer rounded to float32) come from
-// sincospif: both are off by less than 2^-23.
+// (f_i / 2 pi 2^64, rounded once), so pos f_i mod a turn is the wrapped integer
+// product: within 2^-34 of a turn for every int32 position, without 64-bit
+// floating point (which this GPU has little of). Its first 32 bits are used
+// (another 2^-32 of a turn, 1.5e-9 radians): the nearest quarter turn is taken
+// off in integers, and cos and sin of the rest (|a| <= pi / 4, a 30-bit integer
+// rounded to float32: 2.4e-8) come from sincospif (one step, 6e-8): both are off
+// by less than 2^-23 (1.19e-7).
 //
 // A CTA takes a few tokens (or a part of one's heads): the angles of a token,
 // shared by all heads of q and k, go through shared memory while the first

@@ -632,7 +632,9 @@ gqa_status gqa_attend_selected(const void *q, gqa_dtype q_dtype, const void *k_c
  *            of no row are copied as they are (and those of a row with offsets
  *            outside 0 .. T: GQA_STATUS_BAD_QLEN)
  *  freqs     (device) (dim / 2) unsigned 64-bit: f_i / (2 pi) in fixed point, 64
- *            bits behind the point, modulo one turn
+ *            bits behind the point, modulo one turn. A position multiplies their
+ *            error: rounded from the exact value (not from a 64-bit float, whose
+ *            53 bits leave 2^-56 of a turn) angles are within 2^-34 of a turn
  */
 gqa_status gqa_rotate(const void *q, const void *k, void *q_out, void *k_out, gqa_dtype dt, const int64_t *strides,
                       const int32_t *positions, const int32_t *lengths, const int32_t *cu_q, const uint64_t *freqs,

@@ -108,6 +108,30 @@ def test_scores_depend_on_the_distance():
     assert (s - s[0]).abs().max() <= 16 * 2.0 ** -24 * float(x.norm() * y.norm()) * math.sqrt(D)
 
 
+@pytest.mark.parametrize("base", [10000.0, 500000.0])
+def test_angles_of_far_positions(base):
+    """cos and sin themselves (the pairs are (1, 0)) at positions of 31 bits, angles reduced in decimal.
+
+    Tolerance: 2^-34 of a turn from the table and 2^-32 from its cut (2e-9 radians), 2.4e-8 from the rest of the
+    angle in float32 (at most pi / 4), one step of sincospif (6e-8): 8.6e-8, under 2^-23."""
+    import decimal
+    dim = 128
+    at = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 12345, 2 ** 30 + 1, -(2 ** 30) - 77, 10 ** 9, 123456789, 0, 1]
+    x = torch.zeros(len(at), 1, dim, device="cuda")
+    x[..., :dim // 2] = 1
+    got, _ = gqa.rotate(x, None, gqa.Rotary(dim, base=base), torch.tensor(at, dtype=torch.int32, device="cuda"))
+    want = torch.empty(len(at), dim, dtype=torch.float64)
+    with decimal.localcontext() as c:
+        c.prec = 60
+        two_pi = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+        for i in range(dim // 2):
+            turns = (-2 * i * decimal.Decimal(base).ln() / dim).exp() / two_pi
+            for t, pos in enumerate(at):
+                a = float((pos * turns) % 1 * two_pi)
+                want[t, i], want[t, i + dim // 2] = math.cos(a), math.sin(a)
+    assert (got[:, 0].cpu().double() - want).abs().max() <= 2.0 ** -23
+
+
 def test_empty():
     rot = gqa.Rotary(64)
     q = torch.zeros(0, 2, 64, device="cuda")

@@ -173,3 +173,58 @@ def test_threads_have_scratch_of_their_own(monkeypatch):
     second.join()
     (a, b), (c, d) = got
     assert a is b and c is d and a.data_ptr() != c.data_ptr()
+
+
+def _exact_turns(dim, base, scaling):
+    """Frequencies over 2 pi, times 2^64, in decimal: powers by exp and ln, pi by Machin's formula."""
+    from decimal import Decimal as Dec
+
+    def atan_of(n):                      # atan(1 / n)
+        x, k, total = Dec(1) / n, 0, Dec(0)
+        while abs(x) > Dec(10) ** -118:
+            total += (-1) ** k * x / (2 * k + 1)
+            x, k = x / (n * n), k + 1
+        return total
+
+    two_pi = 2 * (16 * atan_of(5) - 4 * atan_of(239))
+    k = {n: Dec(v) for n, v in (scaling or {}).items() if n != "kind"}
+    kind = (scaling or {}).get("kind")
+    ln = Dec(base).ln() + (k["factor"].ln() * dim / (dim - 2) if kind == "ntk" else 0)
+    out = []
+    for i in range(dim // 2):
+        f = (-2 * i * ln / dim).exp()
+        if kind == "linear":
+            f /= k["factor"]
+        if kind == "bands":
+            u = (k["original"] * f / two_pi - k["low"]) / (k["high"] - k["low"])
+            u = min(max(u, Dec(0)), Dec(1))
+            f = f * u + f * (1 - u) / k["factor"]
+        out.append(f / two_pi % 1 * 2 ** 64)
+    return out
+
+
+@pytest.mark.parametrize("base", [10000.0, 500000.0, 1e6, 0.5])
+@pytest.mark.parametrize("scaling", [None, dict(kind="linear", factor=0.05), dict(kind="linear", factor=3.0),
+                                     dict(kind="ntk", factor=8.0),
+                                     dict(kind="bands", factor=8.0, original=4096, low=1.0, high=32.0)])
+def test_rotary_tables_are_rounded_once(base, scaling):
+    """An angle is a position times the table's entry: an entry from a 64-bit float would be 2^-56 of a turn off,
+    2^-25 at far positions."""
+    import decimal
+
+    import gqa_kv_cache_gb300 as gqa
+    for dim in (4, 64, 104, 128):
+        rot = gqa.Rotary(dim, base=base, scaling=scaling, device="cpu")
+        with decimal.localcontext() as c:
+            c.prec = 120
+            for got, want in zip(rot.freqs.tolist(), _exact_turns(dim, base, scaling)):
+                off = (got - want) % 2 ** 64
+                assert min(off, 2 ** 64 - off) <= decimal.Decimal("0.5000001")
+
+
+def test_rotary_takes_any_size_of_scaling():
+    import gqa_kv_cache_gb300 as gqa
+    rot = gqa.Rotary(4, scaling=dict(kind="ntk", factor=1e300), device="cpu")   # a base of 10^604
+    assert rot.freqs.tolist()[1] == 0
+    with pytest.raises(ValueError):
+        gqa.Rotary(4, scaling=dict(kind="linear", factor=1e-300), device="cpu")
