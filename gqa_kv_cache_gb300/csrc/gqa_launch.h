@@ -58,7 +58,7 @@ struct ScoredParams : DecodeParams {
     float cap, scale_cap;            // cap log2(e) (0: none), 1 / (sqrt(D) cap)
     const float *slopes;             // (Hq) or null
     float *weights;                  // counts: (R, Hkv, Smax) or (num_blocks, Hkv, block_size), or null
-    float *xs;                       // with weights: base-2 scores (B, Hkv, xs_cap, gp) ...
+    float *xs;                       // with weights: base-2 scores without bias (B, Hkv, xs_cap, gp) ...
     float2 *row_end;                 // ... and (B, Hq) maxima and 1 / denominators
     long long xs_cap;
     int gp;                          // query rows a slot of xs: 4 or 8

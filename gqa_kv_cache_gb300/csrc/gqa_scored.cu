@@ -25,11 +25,12 @@ cudaError_t launch(int kind, int D, int G, bool more, bool q_bf16, bool paged, c
 
 constexpr int kCountThreads = 256, kCountSlots = 4;   // slots a thread
 
-// weights[slot] += sum over the rows of 2^(y - M) / den: the scores of a slot
-// are neighbours, 16 or 32 bytes. Bound by memory: 4 G + 8 bytes a slot (327k
+// weights[slot] += sum over the rows of 2^(y - M) / den (the bias, which may be
+// as large as M, meets M in one rounding): the scores of a slot are neighbours, 16
+// or 32 bytes. Bound by memory: 4 G + 8 bytes a slot (327k
 // slots of 8 heads, G = 8: 105 MB, part of it from L2). Added in L2, which lets
 // rows share blocks and spares a load (attend and counts 244 -> 239 us).
-template <int GP>
+template <int GP, bool SLOPES>
 __global__ void __launch_bounds__(kCountThreads) count_kernel(const ScoredParams p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -42,11 +43,14 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const ScoredParams
     if (j0 > r.L || !row_ok(p, b, r.L))
         return;
     float M[GP], inv[GP];
+    [[maybe_unused]] float slope[SLOPES ? GP : 1];
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
         const float2 e = g < p.G ? p.row_end[(long long)b * p.Hq + kvh * p.G + g] : make_float2(0.f, 0.f);
         M[g] = e.x;
         inv[g] = e.y;
+        if constexpr (SLOPES)
+            slope[g] = g < p.G ? __ldg(p.slopes + kvh * p.G + g) * 1.4426950408889634f : 0.f;
     }
     long long line = 0;
     if (!p.paged)
@@ -64,6 +68,7 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const ScoredParams
                 continue;
             at = ((long long)blk * p.Hkv + kvh) * p.block_size + j % p.block_size;
         }
+        [[maybe_unused]] const float far = (float)(j - r.L);
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < GP / 4; ++k) {
@@ -71,8 +76,12 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const ScoredParams
             const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int g = 0; g < 4; ++g)
-                if (4 * k + g < p.G)
-                    sum += fast_ex2(y[g] - M[4 * k + g]) * inv[4 * k + g];
+                if (4 * k + g < p.G) {
+                    if constexpr (SLOPES)
+                        sum += fast_ex2(y[g] + fmaf(slope[4 * k + g], far, -M[4 * k + g])) * inv[4 * k + g];
+                    else
+                        sum += fast_ex2(y[g] - M[4 * k + g]) * inv[4 * k + g];
+                }
         }
         atomicAdd(p.weights + at, sum);        // rows may share a block; a slot of one row has one writer
     }
@@ -91,7 +100,7 @@ cudaError_t launch_count(const ScoredParams &p, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, count_kernel<GP>, p);
+    return p.slopes ? cudaLaunchKernelEx(&cfg, count_kernel<GP, true>, p) : cudaLaunchKernelEx(&cfg, count_kernel<GP, false>, p);
 }
 
 }  // namespace

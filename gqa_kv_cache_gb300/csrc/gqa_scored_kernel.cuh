@@ -37,9 +37,9 @@
 //    at the row's end, and forwards steep heads raised their reference at every
 //    tile (256 rows of 16 .. 8191 slots, float32 query: 93 -> 86 us).
 //  * counted weights: the scores go to a scratch array as they come (float32,
-//    G padded to 4 or 8 a slot), each row's maximum and denominator at the end of
-//    its unit, and a second kernel adds sum_g 2^(y_g - M_g) / den_g to the slot's
-//    count. (A second pass over the keys would read D or 2 D bytes a slot
+//    without the bias, G padded to 4 or 8 a slot), each row's maximum and
+//    denominator at the end of its unit, and a second kernel adds sum_g 2^(y_g -
+//    M_g) / den_g to the slot's count. (A second pass over the keys would read D or 2 D bytes a slot
 //    instead of 8 G.) The scores ask to stay in L2, the vectors to leave it: four
 //    bfloat16 rows of 32768 .. 131071 slots, G = 8, 259 -> 247 us (now 239).
 // What bounds it. Over a bfloat16 cache the memory (64 rows of 512 .. 16383 slots
@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
                             ok &= ~(1u << (2 * u + i));
             }
             if constexpr (MORE) {
-                // base-2 scores in place
+                // base-2 scores (but for the bias) in place
 #pragma unroll
                 for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -895,17 +895,6 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
                         s[u][i / C * 2 + i % C] *= mul[i % C];
                 if (p.cap > 0.f)
                     cap_scores<SUB, C>(s, p.cap);
-                if (p.slopes) {
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float far = (float)(s0 + 16 * u + g + 8 * i - L);
-#pragma unroll
-                            for (int c = 0; c < C; ++c)
-                                s[u][2 * i + c] = fmaf(slope[c], far, s[u][2 * i + c]);
-                        }
-                }
                 if (p.xs && C * t4 < p.gp) {
                     float *to = p.xs + (((unsigned long long)seg->c.b * p.Hkv + seg->c.kvh) * p.xs_cap + s0 + g) * p.gp + C * t4;
 #pragma unroll
@@ -916,19 +905,30 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
                                 store_scores<C>(to + (16 * u + 8 * i) * p.gp, s[u][2 * i], s[u][2 * i + 1], keep);
                 }
             }
-            // x = base-2 score - reference, of slots u, i and rows c
+            // distance of slots u, i from the query
+            [[maybe_unused]] const float far0 = (float)(s0 + g - L);
+            [[maybe_unused]] auto far = [&](int u, int i) { return far0 + (float)(16 * u + 8 * i); };
+            // x = base-2 score - reference, of slots u, i and rows c. A bias and the
+            // reference may be large and near each other (a negative slope's, in a long
+            // row): they meet in one rounding, before the score
             float x[SUB][2 * C], top = -INFINITY;
             auto shifted = [&] {
 #pragma unroll
                 for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < 2 * C; ++i)
+                        x[u][i] = MORE ? s[u][i / C * 2 + i % C] - m[i % C] : fmaf(s[u][i / C * 2 + i % C], mul[i % C], -m[i % C]);
+                if (MORE && p.slopes)
 #pragma unroll
-                        for (int c = 0; c < C; ++c) {
-                            float &y = x[u][C * i + c];
-                            y = MORE ? s[u][2 * i + c] - m[c] : fmaf(s[u][2 * i + c], mul[c], -m[c]);
-                            y = (ok >> (2 * u + i)) & 1u ? y : -INFINITY;
-                        }
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int i = 0; i < 2 * C; ++i)
+                            x[u][i] = s[u][i / C * 2 + i % C] + fmaf(slope[i % C], far(u, i / C), -m[i % C]);
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2 * C; ++i)
+                        x[u][i] = (ok >> (2 * u + i / C)) & 1u ? x[u][i] : -INFINITY;
             };
             shifted();
 #pragma unroll
@@ -957,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, ctas<KIND, D>()) scored_kernel(const
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             if ((ok >> (2 * u + i)) & 1u)
-                                most = fmaxf(most, MORE ? s[u][2 * i + c] : s[u][2 * i + c] * mul[c]);
+                                most = fmaxf(most, MORE ? fmaf(slope[c], far(u, i), s[u][2 * i + c]) : s[u][2 * i + c] * mul[c]);
 #pragma unroll
                     for (int q = 4; q < 32; q <<= 1)
                         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, q));

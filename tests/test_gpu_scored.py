@@ -233,6 +233,38 @@ def test_slopes_over_long_rows(kind, layout, bs, sign):
             c.check(out, want, weights, base)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("layout,bs", [("dense", 64), ("paged", 16), ("paged", 24)])
+@pytest.mark.parametrize("D,G,qt", [(64, 4, torch.float32), (128, 6, torch.bfloat16)])
+def test_large_biases_of_the_slots_that_win(kind, layout, bs, D, G, qt):
+    """Negative slopes in long rows: the slots that weigh have the largest biases, of which their scores must not
+    take the rounding. What is rounded is the bias less the winning slot's (and what a reference lies below the
+    largest score: 12 and 10 in base 2): the common part of all biases leaves the softmax as it is."""
+    lens = [100001, 48013]
+    c = Case(kind, layout, lens, 1, G, D, -(-100032 // bs) * bs, bs, qt, seed=21)
+    slopes = -torch.tensor([0.70710678, 0.25, 3.0, 0.01, 11.0, 0.1])[:G]
+    for window, prefix in ((0, 0), (30011, 7)):
+        want = []
+        for b, n in enumerate(lens):
+            ok = R.attended(n, window, prefix)
+            k, v = c.row(0, b, n)[0, ok], c.row(1, b, n)[0, ok]
+            q = c.q[b].double()
+            s = q @ k.T / math.sqrt(D)
+            bias = slopes.double()[:, None] * (torch.arange(n)[ok] - (n - 1)).double()
+            w = torch.softmax(s + bias, -1)
+            near = (bias - bias.gather(1, (s + bias).argmax(-1, keepdim=True))).abs()
+            big = (q.abs() @ k.abs().T).amax(-1, keepdim=True) / math.sqrt(D)
+            err = R.score_error(D, big, s.abs() + near + 24)
+            full, d = torch.zeros(1, G, n, dtype=torch.float64), torch.zeros(1, G, n, dtype=torch.float64)
+            full[0][:, ok], d[0][:, ok] = w, err
+            want.append((w @ v, R.out_tolerance(full, d, float(v.abs().max())), full.sum(1), R.count_tolerance(full, d)))
+        base = torch.zeros(c.shape)
+        for grid in (0, 3):
+            weights = base.cuda()
+            out = c.attend(head_slopes=slopes.cuda(), weights=weights, window=window, kept_prefix=prefix, grid_ctas=grid)
+            c.check(out, want, weights, base)
+
+
 def test_rows_that_share_blocks_all_count():
     # three rows with the first 8 blocks in common, as after a common prompt
     lens = [150, 163, 200]
