@@ -18,7 +18,10 @@
 //    subtraction, exactly; a bfloat16 query is scaled by a power of two into
 //    f16's range (exact but for elements 2^-38 below the row's largest), a
 //    float32 one is an f16 and an f16 remainder (22 bits). Over a bfloat16 cache
-//    the fragments come by ldmatrix, a float32 query as three bfloat16 (24 bits).
+//    the fragments come by ldmatrix, a float32 query as three bfloat16 (24 bits),
+//    the second and third with sums of their own: infinite keys meet the first
+//    alone (so it is with values and the weights' parts: with_rest; four long
+//    counted rows 241 -> 243 us).
 //  * O^T += V^T P^T: 16 dims by the query rows, 16 slots a step, V unrounded.
 //    8 bits: lane (g, t) takes D / 8 contiguous dims of slots 2t, 2t + 1, 2t + 8,
 //    2t + 9, neighbours paired by a byte permute. P is an f16 and an f16
@@ -508,6 +511,14 @@ __device__ __forceinline__ void fetch_tile(const ScoredParams &p, const Fetch &f
     }
 }
 
+// The product of a number's first part and that of its remainders, together.
+// Where an operand is infinite the first is the whole product: a remainder's
+// would be the other infinity, or 0 times infinity.
+__device__ __forceinline__ float with_rest(float first, float rest)
+{
+    return fabsf(first) <= FLT_MAX ? first + rest : first;
+}
+
 // Products of part u: s[0], s[1] slot g and query rows 2t, 2t + 1 (FEW: both
 // row t); s[2], s[3] slot g + 8. 8 bits: times the slot's key scale.
 template <int KIND, int D, bool QF32, bool FEW, int PARTS>
@@ -541,15 +552,21 @@ __device__ __forceinline__ void scores(const Stage<KIND, D> &st, int u, int lane
         for (int w = 0; w < D / 16; ++w) {
             uint32_t a[4];
             ldmatrix4<false>(a, smem_at(st.k) + piece<F::VB>(16 * u + (lane & 15), 2 * w + (lane >> 4)));
-            float(&d)[4] = w & 1 ? s2 : s;
+            if constexpr (PARTS == 1) {
+                float(&d)[4] = w & 1 ? s2 : s;
+                mma<false>(w < 2, d, a[0], a[1], a[2], a[3], qf[0][w][0], qf[0][w][1]);
+            } else {
+                // the remainders' products on their own
+                mma<false>(w == 0, s, a[0], a[1], a[2], a[3], qf[0][w][0], qf[0][w][1]);
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k)
-                mma<false>(w < 2 && k == 0, d, a[0], a[1], a[2], a[3], qf[k][w][0], qf[k][w][1]);
+                for (int k = 1; k < PARTS; ++k)
+                    mma<false>(w == 0 && k == 1, s2, a[0], a[1], a[2], a[3], qf[k][w][0], qf[k][w][1]);
+            }
         }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        s[i] += s2[i];
+        s[i] = KIND != kI8 && PARTS > 1 ? with_rest(s[i], s2[i]) : s[i] + s2[i];
     if constexpr (KIND == kI8) {
         if constexpr (QF32 && FEW) {
             s[0] += s[1];
@@ -654,18 +671,18 @@ __device__ __forceinline__ void weigh(const Stage<KIND, D> &st, int lane, const 
             }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-            float d[4];
+            float d[4], r[4];
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
                 uint32_t a[4];
                 ldmatrix4<true>(a, smem_at(st.v) + piece<F::VB>(16 * u + (lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)));
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    mma<false>(u == 0 && k == 0, d, a[0], a[1], a[2], a[3], b[u][k][0], b[u][k][1]);
+                mma<false>(u == 0, d, a[0], a[1], a[2], a[3], b[u][0][0], b[u][0][1]);
+                mma<false>(u == 0, r, a[0], a[1], a[2], a[3], b[u][1][0], b[u][1][1]);
+                mma<false>(false, r, a[0], a[1], a[2], a[3], b[u][2][0], b[u][2][1]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                o[i][j] += d[j];
+                o[i][j] += with_rest(d[j], r[j]);
         }
     }
 }

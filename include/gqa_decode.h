@@ -44,6 +44,10 @@
  *    and a bit is OR-ed into *d_status (if d_status is not NULL).
  *    *d_status is sticky: the library never clears it. gqa_validate checks
  *    content completely (including duplicates) and synchronously.
+ *  - Attended keys and values are taken to be finite. Infinite ones follow the
+ *    formulas (a score of minus infinity weighs nothing) where scores are
+ *    capped, biased or counted over a bfloat16 cache; elsewhere a row that
+ *    meets one may be NaN.
  *  - B = 0 is valid: nothing is launched and GQA_OK is returned (empty
  *    tensors, "aclnnMlaPrologV3WeightNz", shape restrictions).
  *  - Results are deterministic: the same inputs and launch configuration give

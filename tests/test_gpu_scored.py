@@ -158,6 +158,59 @@ def test_slots_masked_by_keys_of_minus_infinity(layout, bs, D, where, slopes):
             torch.zeros(*c.shape))
 
 
+@pytest.mark.parametrize("layout,bs", [("dense", 16), ("paged", 24)])
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 5)])
+@pytest.mark.parametrize("where", [slice(0, 300), slice(500, 699)])
+def test_float32_queries_over_keys_of_minus_infinity(layout, bs, D, G, where):
+    # a query's elements with remainders of either sign, and without any, meet infinite keys
+    n = 700
+    c = Case("bf16", layout, [n], 2, G, D, 720, bs, torch.float32, seed=33)
+    c.q[..., 0] = c.q[..., 0].abs() + 0.25
+    c.q[0, ::3, 0] = c.q[0, ::3, 0].bfloat16().float()
+    ok = torch.ones(n, dtype=torch.bool)
+    ok[where] = False
+    k = R.row_slots(c.kv[0], 0, n, c.table, None, bs).clone()
+    k[:, ~ok, 0] = -math.inf
+    R.put_row(c.kv[0], 0, n, k, c.table, None, bs)
+    c.g[0].copy_(c.kv[0])
+    for cap in (0.0, 8.0):
+        if cap:                               # capped, they are the smallest score there is
+            s = torch.einsum("hgd,hnd->hgn", c.q[0].double().view(2, G, D), k.double()) / math.sqrt(D)
+            w = torch.softmax(cap * torch.tanh(s / cap), -1)
+            v, e = c.row(1, 0, n), torch.full_like(w, 2.0 ** -16)   # (D / 16 + 6) 2^-23 of sums up to 100 / sqrt(D)
+            o = torch.einsum("hgn,hnd->hgd", w, v)
+        else:
+            o, w, e = R.attention(c.q[0].double().view(2, G, D), k.double(), c.row(1, 0, n), 0.0, None, ok)
+        want = [(o.reshape(-1, D), R.out_tolerance(w, e, float(c.row(1, 0, n).abs().max())), w.sum(1), R.count_tolerance(w, e))]
+        for grid in (0, 3):
+            weights = torch.zeros(c.shape, device="cuda")
+            c.check(c.attend(weights=weights, score_cap=cap, grid_ctas=grid), want, weights, torch.zeros(c.shape))
+
+
+@pytest.mark.parametrize("layout,bs", [("dense", 16), ("paged", 24)])
+@pytest.mark.parametrize("D,G,qt", [(64, 4, torch.bfloat16), (128, 5, torch.float32)])
+def test_values_of_infinity(layout, bs, D, G, qt):
+    """An infinite value gives its element infinity of its sign, infinities of both signs NaN, other elements nothing."""
+    n = 700
+    c = Case("bf16", layout, [n], 2, G, D, 720, bs, qt, seed=34)
+    v = R.row_slots(c.kv[1], 0, n, c.table, None, bs).clone()
+    good = v.clone()
+    for j, d, x in ((3, 1, math.inf), (699, 7, -math.inf), (350, 8, math.inf), (351, 8, math.inf), (10, 20, math.inf),
+                    (600, 20, -math.inf)):
+        v[:, j, d], good[:, j, d] = x, 0
+    R.put_row(c.kv[1], 0, n, v, c.table, None, bs)
+    c.g[1].copy_(c.kv[1])
+    o, w, e = R.attention(c.q[0].double().view(2, G, D), c.row(0, 0, n), good.double())
+    tol = R.out_tolerance(w, e, float(good.abs().max()))
+    for grid in (0, 3, 33):
+        out = c.attend(score_cap=2.0 ** 40, grid_ctas=grid)[0].cpu().double()
+        assert (out[:, 1] == math.inf).all() and (out[:, 7] == -math.inf).all() and (out[:, 8] == math.inf).all()
+        assert out[:, 20].isnan().all()
+        rest = torch.ones(D, dtype=torch.bool)
+        rest[[1, 7, 8, 20]] = False
+        assert ((out - o.reshape(-1, D))[:, rest].abs() <= tol).all()
+
+
 def test_scores_that_are_not_finite():
     """A NaN key gives its row NaN and no other; -inf scores count as nothing."""
     c = Case("bf16", "dense", [40, 40], 1, 2, 64, 48, seed=5)
