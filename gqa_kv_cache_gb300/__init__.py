@@ -33,7 +33,7 @@ that append keep the scales; start them (and the codes) at zero.
 
 Over a bfloat16 or 8-bit cache ``score_cap`` (c tanh(s / c)), ``head_slopes``
 (float32 (Hq,): slope_h (j - L) added to the score of slot j, L the query's
-position) and ``weights`` (float32 counts, the cache's shape without D, to which
+slot) and ``weights`` (float32 counts, the cache's shape without D, to which
 every slot's softmax weights, summed over its head's queries, are added) extend
 ``decode_step`` and ``attend`` and their paged forms. ``evict`` and
 ``evict_paged`` cut rows to the slots with the largest counts, and ``rotate``
@@ -1322,8 +1322,11 @@ def evict(k_cache, v_cache, weights, lengths, n_keep, slot_ids=None, *, n_first=
     lowest slot) move together in ascending order, in place, or into ``k_out``,
     ``v_out`` (B, Hkv, slots, D) and ``weights_out``, the cache then only being
     read; rows that share a cache row or blocks need such outputs. Keys keep the
-    positions that were turned into them. Returns the kept slots (B, Hkv, n_keep)
-    int32 (then -1) and the new lengths (B,)."""
+    positions that were turned into them; ``head_slopes``, ``window`` and
+    ``kept_prefix`` count slots, which are closer than their tokens were from
+    then on, and key bounds of a row cut in place are void. (The bytes of an E2M1
+    cache look like E4M3 ones: it must not be given.) Returns the kept slots
+    (B, Hkv, n_keep) int32 (then -1) and the new lengths (B,)."""
     return _evict(k_cache, v_cache, None, weights, lengths, n_keep, slot_ids, n_first, n_last, k_out, v_out,
                   weights_out, status, stream)
 

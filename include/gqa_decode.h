@@ -214,8 +214,9 @@ typedef struct gqa_options {
                                         GQA_ERR_INVALID_ARGUMENT                        */
     const float *head_slopes;        /* (device) (Hq,) float32 or NULL: slope_h (j - L) is
                                         added to the (capped) score of slot j, L the
-                                        query's position: a positive slope takes from
-                                        distant slots                                   */
+                                        query's slot: a positive slope takes from
+                                        distant slots. In a row that gqa_evict has cut
+                                        slots are nearer than their tokens were         */
     float *weights;                  /* (device) float32 counts, 4-byte aligned, or NULL: the
                                         cache's shape without D ((R, Hkv, Smax) or
                                         (num_blocks, Hkv, block_size)). Every attended slot's
@@ -654,7 +655,12 @@ gqa_status gqa_rotate(const void *q, const void *k, void *q_out, void *k_out, gq
  * behind become 0, the vectors behind stay as they are), or, with k_out and
  * v_out, to slots 0 .. of row b of other buffers, the cache then only being
  * read. Shorter rows keep every slot (and are copied too when there are outputs).
- * Keys are moved as they are: positions that were turned into them stay.
+ * Keys are moved as they are: positions that were turned into them stay (turn new
+ * tokens by their positions, not by the shorter lengths). What counts slots counts
+ * the kept ones from then on: the distances of gqa_options.head_slopes and its
+ * window and kept prefix are no longer those between tokens. Key bounds of
+ * gqa_append are not moved: those of a row cut in place are void until its blocks
+ * are written again from their first slots.
  *
  *  k_cache, v_cache (device) float32, bfloat16 or E4M3 (GQA_ERR_UNSUPPORTED for
  *           the others, and for rows of more than 2^30 slots); D times the element

@@ -58,6 +58,20 @@ def test_a_loop_with_eviction():
     assert torch.equal(read, k)
 
 
+def test_biases_and_windows_of_a_row_that_was_cut_count_slots():
+    """What evict says of head_slopes and window: distances are those of the kept slots."""
+    gen = torch.Generator().manual_seed(5)
+    k, v = (torch.randn(1, Hkv, S, D, generator=gen).bfloat16().cuda() for _ in range(2))
+    w, n = torch.rand(1, Hkv, S, generator=gen).cuda(), torch.tensor([200], dtype=torch.int32).cuda()
+    _, n = gqa.evict(k, v, w, n, 40, n_first=2, n_last=8)
+    q, slopes = torch.randn(1, Hq, D, generator=gen), torch.rand(Hq, generator=gen)
+    for window in (0, 12):
+        out = gqa.attend(q.cuda(), k, v, n, head_slopes=slopes.cuda(), window=window)
+        o, weight, e = R.attention(q[0].double().view(Hkv, -1, D), k[0, :, :40].cpu().double(), v[0, :, :40].cpu().double(),
+                                   slopes=slopes.view(Hkv, -1), ok=R.attended(40, window))
+        assert (out[0].cpu().double() - o.reshape(Hq, D)).abs().max() <= R.out_tolerance(weight, e, float(v.abs().max()))
+
+
 def _steps(stream=None, workspace=None):
     """A fixed run of all the calls; returns every output."""
     gen = torch.Generator().manual_seed(1)
