@@ -1392,7 +1392,8 @@ def trace_enable(on: bool = True) -> bool:
 
 
 def trace_collect() -> dict:
-    """{kernel name: (launches, total ms)} since the previous collect."""
+    """{kernel name: (calls, total ms)} since the previous collect (a scored
+    step is one call of one to three kernels)."""
     lib = _lib.load()
     n = 4
     launches = (ctypes.c_int64 * n)()

@@ -51,7 +51,8 @@
  *  - B = 0 is valid: nothing is launched and GQA_OK is returned (empty
  *    tensors, "aclnnMlaPrologV3WeightNz", shape restrictions).
  *  - Results are deterministic: the same inputs and launch configuration give
- *    the same bits (no floating-point atomics).
+ *    the same bits (no floating-point atomics), but for counts of weights
+ *    (gqa_options.weights) that several rows of a call add to.
  */
 #ifndef GQA_DECODE_H
 #define GQA_DECODE_H
@@ -467,14 +468,16 @@ gqa_status gqa_validate_multi(const int32_t *lengths, const int32_t *cu_q, const
 
 /*
  * Kernel timing trace. When enabled, every decode call records CUDA events
- * around the kernel it launches; gqa_trace_collect waits for them and
- * returns, per kernel kind, the launches and total milliseconds since the
- * previous collect. Kinds: 0 = SIMT decode, 1 = tensor-core decode (over an
- * E2M1 cache q4_decode_kernel; over an 8-bit one, or with capped, biased or
- * counted scores, scored_kernel with the writes and counts around it), 2 = the small-cache decode, 3 = the tcgen05 form of 17- to 32-row multi-token
- * units (each decode step is exactly one kernel launch); gqa_kernel_name
- * gives each kind's kernel name. append, read, block selection, rotation and
- * eviction are not traced. Meant for benchmarks.
+ * around what it launches; gqa_trace_collect waits for them and returns, per
+ * kernel kind, the calls and their total milliseconds since the previous
+ * collect. Kinds: 0 = SIMT decode, 1 = tensor-core decode (over an E2M1 cache
+ * q4_decode_kernel; over an 8-bit one, or with capped, biased or counted
+ * scores, scored_kernel and, in the same span, the kernels that write a step's
+ * tokens before it and count weights after it: one to three launches), 2 = the
+ * small-cache decode, 3 = the tcgen05 form of 17- to 32-row multi-token units
+ * (but for those spans each decode step is exactly one kernel launch);
+ * gqa_kernel_name gives each kind's kernel name. append, read, block selection,
+ * rotation and eviction are not traced. Meant for benchmarks.
  */
 int gqa_trace_enable(int on);
 gqa_status gqa_trace_collect(int n_kinds, int64_t *launches, double *ms);
