@@ -60,6 +60,8 @@ gqa_status run_rows(RowsParams p, gqa_dtype vec, gqa_dtype kv, bool write, void 
         p.scale_block = p.paged ? p.block_size : opt->scale_block;
         if (p.scale_block < 1 || (!p.paged && p.Smax % p.scale_block))
             return GQA_ERR_INVALID_ARGUMENT;
+        if (write && !append8_supports(p.scale_block, p.Hkv, p.D))
+            return GQA_ERR_UNSUPPORTED;
         p.k_block_scale = opt->k_block_scale;
         p.v_block_scale = opt->v_block_scale;
     } else if (kv >= GQA_DTYPE_E4M3) {

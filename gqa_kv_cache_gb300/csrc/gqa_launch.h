@@ -95,6 +95,11 @@ __device__ __forceinline__ void rows_report(const RowsParams &p, int bits)
     if (p.status)
         atomicOr(p.status, bits);
 }
+// The appends number the 16-element groups of a block, and of a token, in 32 bits.
+inline bool append8_supports(int scale_block, int Hkv, int D)
+{
+    return (long long)scale_block * (D / 16) <= 1 << 30 && (long long)Hkv * D <= 1 << 24;
+}
 cudaError_t rows_launch(RowsParams p, int kv_dtype, bool write, int sms, cudaStream_t st);
 cudaError_t tokens_launch(RowsParams p, cudaStream_t st);   // one token a row into a bfloat16 cache
 

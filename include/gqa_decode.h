@@ -117,7 +117,8 @@ typedef enum gqa_dtype {
                            bfloat16 query; D = 64 or 128, G <= 8, any paged block size;
                            GQA_KERNEL_AUTO or GQA_KERNEL_TC. No multi-token step (write
                            prompts with gqa_append), no key bounds; two rows that write
-                           one block are undefined.                                 */
+                           one block are undefined. Blocks written: at most 2^30 groups
+                           of 16 elements a head.                                   */
 } gqa_dtype;
 
 /* Bits OR-ed into *d_status by the kernels. */

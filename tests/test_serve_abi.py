@@ -88,6 +88,21 @@ def test_append_and_read_of_8_bits(lib):
         == INVALID
 
 
+def test_blocks_past_32_bits_are_refused(lib):
+    """The appends number a block's groups of 16 elements in 32 bits: larger blocks were written in part."""
+    for S, D, want in ((1 << 30, 64, UNSUPPORTED), (1 << 29, 64, UNSUPPORTED), (1 << 28, 128, UNSUPPORTED)):
+        big = _opt(k_block_scale=P, v_block_scale=P, scale_block=S, grid_ctas=8)
+        assert lib.gqa_append(P, P, BF16, P, P, P, P, None, None, 0, 1, 3, 1, D, 1, S, I8, None, None, big) == want
+        assert lib.gqa_append_paged(P, P, BF16, P, P, P, P, P, None, 1, 3, 1, D, 1, S, 1, I8, None, None, big) == want
+        assert lib.gqa_decode_step_ex(P, P, P, P, P, P, None, P, 1, 1, 1, D, 1, S, I8, None, 0, None, None, big) == want
+        assert lib.gqa_attend(P, BF16, P, P, P, None, P, 1, 1, 1, D, 1, S, I8, None, 0, None, None, big) == WORKSPACE
+    heads = 1 << 18                                       # and a token's elements
+    wide = _opt(k_block_scale=P, v_block_scale=P, scale_block=1, grid_ctas=8, score_cap=2.0)
+    for kv in (I8, BF16):
+        assert lib.gqa_decode_step_ex(P, P, P, P, P, P, None, P, 1, heads, heads, 128, 1, 1, kv, None, 0, None, None,
+                                      wide) == UNSUPPORTED
+
+
 def _attend(lib, kv=BF16, D=128, Hq=8, Hkv=2, S=64, dt=BF16, **opt):
     opt.setdefault("grid_ctas", 8)
     return lib.gqa_attend(P, dt, P, P, P, None, P, 1, Hq, Hkv, D, 1, S, kv, None, 0, None, None, _opt(**opt))
