@@ -406,6 +406,9 @@ gqa_status run_step(const Shape &s, const void *q, const void *k_new, const void
     const bool scored = is_scored(s.dt, opt);
     if ((kv4 || scored) && (s.paged ? (double)s.num_blocks * s.Hkv * s.block_size : (double)s.R * s.Hkv * s.Smax) >= 4294967296.0)
         return GQA_ERR_UNSUPPORTED;
+    // its slot numbers run a tile behind the row's last slot
+    if (scored && cap_rows > INT_MAX - 1024)
+        return GQA_ERR_UNSUPPORTED;
     if (scored && !s.attend && !append8_supports(!kvi ? 1 : s.paged ? s.block_size : opt->scale_block, s.Hkv, s.D))
         return GQA_ERR_UNSUPPORTED;
     const int kernel = pick_kernel(opt, s.dt, s.D, Gh, s.paged, s.block_size, cap_rows, s.multi,

@@ -620,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, append_ctas<T>()) append8_kernel(con
     __syncthreads();
     const int sb = p.scale_block;
     const long long cap = p.paged ? (long long)p.max_blocks * p.block_size : (long long)p.Smax;
-    for (int b = ONE ? t0 + tid : tid; b < (ONE ? t0 + n : p.B); b += kThreads) {
-        const int a = ONE ? b : __ldg(p.cu_q + b), e = ONE ? b + 1 : __ldg(p.cu_q + b + 1);
+    for (unsigned b = ONE ? t0 + tid : tid; b < (unsigned)(ONE ? t0 + n : p.B); b += kThreads) {
+        const int a = ONE ? (int)b : __ldg(p.cu_q + b), e = ONE ? a + 1 : __ldg(p.cu_q + b + 1);
         if (a < 0 || e < a || e > p.T) {
             rows_report(p, kBadQLen);
             continue;

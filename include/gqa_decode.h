@@ -114,9 +114,10 @@ typedef enum gqa_dtype {
                            max|x| / 127). Codes are rint(x / t), 0 where t is 0; float32
                            arithmetic, rounded to nearest even. The decode step takes
                            bfloat16 q, k_new and v_new, the read-only attend a float32 or
-                           bfloat16 query; D = 64 or 128, G <= 8, any paged block size;
-                           GQA_KERNEL_AUTO or GQA_KERNEL_TC. No multi-token step (write
-                           prompts with gqa_append), no key bounds; two rows that write
+                           bfloat16 query; D = 64 or 128, G <= 8, any paged block size,
+                           rows of at most 2^31 - 1025 slots; GQA_KERNEL_AUTO or
+                           GQA_KERNEL_TC. No multi-token step (write prompts with
+                           gqa_append), no key bounds; two rows that write
                            one block are undefined. Blocks written: at most 2^30 groups
                            of 16 elements a head.                                   */
 } gqa_dtype;
@@ -209,8 +210,9 @@ typedef struct gqa_options {
     int scale_block;                 /* dense 8-bit cache: slots a block, a divisor of Smax
                                         (paged: ignored, block_size)                    */
     /* The three below change the scores of a single-token step or attend or
-     * count its weights: a bfloat16 or 8-bit cache, D = 64 or 128, G <= 8,
-     * GQA_KERNEL_AUTO or GQA_KERNEL_TC; GQA_ERR_UNSUPPORTED elsewhere.          */
+     * count its weights: a bfloat16 or 8-bit cache, D = 64 or 128, G <= 8, rows
+     * of at most 2^31 - 1025 slots, GQA_KERNEL_AUTO or GQA_KERNEL_TC;
+     * GQA_ERR_UNSUPPORTED elsewhere.                                            */
     float score_cap;                 /* c > 0: the score s becomes c tanh(s / c); 0: off;
                                         other values outside 2^-60 .. 2^60 are
                                         GQA_ERR_INVALID_ARGUMENT                        */
@@ -667,8 +669,8 @@ gqa_status gqa_rotate(const void *q, const void *k, void *q_out, void *k_out, gq
  * are written again from their first slots.
  *
  *  k_cache, v_cache (device) float32, bfloat16 or E4M3 (GQA_ERR_UNSUPPORTED for
- *           the others, and for rows of more than 2^30 slots); D times the element
- *           size a multiple of 16
+ *           the others, and for rows, n_keep or out_slots of more than 2^30 slots);
+ *           D times the element size a multiple of 16
  *  weights  (device) float32 counts, the cache's shape without D
  *  lengths  (device) (B,) int32 valid slots, 0 <= lengths[b] <= capacity
  *  n_keep   >= 1, >= n_first + n_last (both >= 0)

@@ -103,6 +103,22 @@ def test_blocks_past_32_bits_are_refused(lib):
                                       wide) == UNSUPPORTED
 
 
+def test_sizes_near_the_end_of_32_bits_are_refused(lib):
+    """Loops step a few thousand places, and tiles a few hundred slots, behind the last one."""
+    for bad in (dict(n=(1 << 30) + 1, last=0), dict(n=2 ** 31 - 1), dict(ko=1 << 20, vo=1 << 60, os=2 ** 31 - 1),
+                dict(ko=1 << 20, vo=1 << 60, os=(1 << 30) + 1)):
+        assert _evict(lib, **bad) == UNSUPPORTED, bad
+        assert lib.gqa_evict_paged(P, P, P, P, P, P, 512, bad.get("ko"), bad.get("vo"), None, bad.get("os", 0), 1, 1, 64, 4, 16,
+                                   2, BF16, bad.get("n", 8), 0, 0, None, None) == UNSUPPORTED
+    block = dict(k_block_scale=P, v_block_scale=P)
+    for blocks in (2 ** 31 // 16 - 1, 2 ** 31 // 16 - 64):
+        for kv, opt in ((I8, _opt(grid_ctas=8, **block)), (BF16, _opt(grid_ctas=8, score_cap=2.0))):
+            assert lib.gqa_attend_paged(P, BF16, P, P, P, P, P, 1, 8, 2, 128, 64, 16, blocks, kv, None, 0, None, None,
+                                        opt) == UNSUPPORTED
+            assert lib.gqa_attend_paged(P, BF16, P, P, P, P, P, 1, 8, 2, 128, 64, 16, blocks // 2, kv, None, 0, None, None,
+                                        opt) == WORKSPACE
+
+
 def _attend(lib, kv=BF16, D=128, Hq=8, Hkv=2, S=64, dt=BF16, **opt):
     opt.setdefault("grid_ctas", 8)
     return lib.gqa_attend(P, dt, P, P, P, None, P, 1, Hq, Hkv, D, 1, S, kv, None, 0, None, None, _opt(**opt))
