@@ -251,7 +251,7 @@ _HERE = contextlib.nullcontext()
 def workspace_bytes(B, Hq, Hkv, D, dtype=torch.bfloat16, kernel="auto", grid_ctas=0, scored=False) -> int:
     """Workspace bytes the library needs for one step of these sizes.
     ``dtype`` is the cache's; "e2m1" for a 4-bit cache. ``scored``:
-    for steps over a bfloat16 cache with capped, biased or counted scores."""
+    for steps with capped, biased or counted scores."""
     o = _opts(kernel, grid_ctas)
     if scored:
         o.score_cap = 1.0

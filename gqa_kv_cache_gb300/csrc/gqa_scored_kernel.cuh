@@ -16,7 +16,7 @@
 //    contiguous dims from D / 4 * t (the order of the contraction is free);
 //    codes become f16 by a byte permute under 0x64 (1024 + 128 + c) and one
 //    subtraction, exactly; a bfloat16 query is scaled by a power of two into
-//    f16's range (exact but for elements 2^-38 below the row's largest), a
+//    f16's range (exact but for elements 2^-31 below the row's largest), a
 //    float32 one is an f16 and an f16 remainder (22 bits). Over a bfloat16 cache
 //    the fragments come by ldmatrix, a float32 query as three bfloat16 (24 bits),
 //    the second and third with sums of their own: infinite keys meet the first
@@ -44,7 +44,7 @@
 //    denominator at the end of its unit, and a second kernel adds sum_g 2^(y_g -
 //    M_g) / den_g to the slot's count. (A second pass over the keys would read D or 2 D bytes a slot
 //    instead of 8 G.) The scores ask to stay in L2, the vectors to leave it: four
-//    bfloat16 rows of 32768 .. 131071 slots, G = 8, 259 -> 247 us (now 239).
+//    bfloat16 rows of 32768 .. 131071 slots, G = 8, 259 -> 247 us (now 243).
 // What bounds it. Over a bfloat16 cache the memory (64 rows of 512 .. 16383 slots
 // in 16-slot blocks, G = 6, capped: 329 us, 0.99 of the measured copy rate). Over
 // an 8-bit cache of D = 128 nearly so: four rows of 32768 .. 131071 slots, G = 4
