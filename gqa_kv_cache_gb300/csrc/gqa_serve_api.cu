@@ -58,7 +58,8 @@ gqa_status run_evict(EvictParams p, int D, gqa_dtype kv, void *stream)
     const long long cap = p.paged ? (long long)p.max_blocks * p.block_size : (long long)p.Smax;
     const long long moved = p.n_keep < cap ? p.n_keep : cap;
     // (the kernels step over slots, kept slots and places of the outputs in 32 bits)
-    if (row % 16 || row > (1 << 20) || cap > (1 << 30) || p.n_keep > (1 << 30) || p.out_slots > (1 << 30) || (long long)p.B * p.Hkv > (1 << 24) ||
+    if (row % 16 || row > (1 << 20) || cap > (1 << 30) || p.n_keep > (1 << 30) || p.out_slots > (1 << 30) ||
+        (long long)p.B * p.Hkv > (1 << 24) ||
         (double)p.B * p.Hkv * ((double)moved * row / (1 << 15) + row / 16.0 + 1.0) > INT_MAX ||
         (double)moved * row / 16 > INT_MAX)
         return GQA_ERR_UNSUPPORTED;
